@@ -55,7 +55,8 @@ extern "C" {
 
 typedef enum mamba2_dtype {
   MAMBA2_F32 = 0,
-  MAMBA2_BF16 = 1
+  MAMBA2_BF16 = 1,
+  MAMBA2_E4M3 = 2 /* 8-bit operands and outputs of block.h only */
 } mamba2_dtype;
 
 typedef enum mamba2_status {

@@ -11,7 +11,10 @@ Entry points (same names as the C ABI without the ``mamba2_`` prefix):
 ``gated_rmsnorm``, ``decode_step``, ``decode_step_device``, ``prefill_host`` (+
 ``prefill_host_workspace_bytes``), ``padded_spans``, ``pack_rows``, ``unpack_rows``,
 ``in_proj``, ``out_proj``, ``state_bytes_per_layer``; and the Mamba-3 SISO forward
-``mamba3_siso_varlen_forward`` (C name unchanged). ``selective_scan_gb300.padded`` holds the padded-batch
+``mamba3_siso_varlen_forward`` (C name unchanged). The operators of the recurrent block
+(``include/block.h``): ``add_rmsnorm``, ``linear`` and ``gated_recurrence``, each with its
+``_backward``, and ``gated_recurrence_step`` / ``gated_recurrence_step_device``;
+``selective_scan_gb300.recurrent_block`` runs them together. ``selective_scan_gb300.padded`` holds the padded-batch
 layer view built on them (attention mask in, HF-style cache out).
 """
 from __future__ import annotations
@@ -23,7 +26,9 @@ from typing import Optional, Sequence
 _PKG = Path(__file__).resolve().parent
 LIB_PATH = _PKG / "libmamba2.so"
 
-F32, BF16 = 0, 1
+F32, BF16, E4M3 = 0, 1, 2
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
+RECURRENCE_CHUNK = 128  # tokens between two checkpoints of the gated recurrence
 (OK, ERR_INVALID_ARGUMENT, ERR_SLOT_OUT_OF_RANGE, ERR_SLOT_SHARED, ERR_RUNS_DONT_COVER_ROWS,
  ERR_NOT_IMPLEMENTED, ERR_CUDA, ERR_WORKSPACE_TOO_SMALL) = range(8)
 MAX_SEQS = 1024
@@ -90,6 +95,28 @@ def _lib():
         lib.mamba2_prefill_host.argtypes = [p, p, p, p, p, p, p, p, p, p, i32, f32, p, p, i32, dims, ctypes.c_int,
                                             rb, i32, p, sz, p]
         lib.mamba3_siso_varlen_forward.argtypes = [p] * 16 + [p, i32, i32, i32, i32, i32, i32, p]
+        i64, act = ctypes.c_int64, ctypes.c_int
+        lib.mamba2_gated_recurrence_checkpoints.argtypes = [p, i32]
+        lib.mamba2_gated_recurrence_checkpoints.restype = i64
+        lib.mamba2_gated_recurrence_workspace_bytes.argtypes = [p, i32, i32, i32]
+        lib.mamba2_gated_recurrence_workspace_bytes.restype = sz
+        lib.mamba2_gated_recurrence.argtypes = [p] * 6 + [i32, i32, i32, i64, i64, i64, act, rb, p, sz, p]
+        lib.mamba2_gated_recurrence_step.argtypes = [p] * 5 + [i32, i32, i64, i64, i64, act, rb, p]
+        lib.mamba2_gated_recurrence_step_device.argtypes = [p] * 5 + [i32, i32, i64, i64, i64, act, p, p, p, i32, p, p]
+        lib.mamba2_gated_recurrence_backward.argtypes = [p] * 10 + [i32, i32, i64, i64, i64, i64, i64, act, p, i32, p,
+                                                                    sz, p]
+        lib.mamba2_add_rmsnorm.argtypes = [p] * 6 + [i32, i32, f32, act, act, act, p]
+        lib.mamba2_add_rmsnorm_backward_workspace_bytes.argtypes = [i32, i32]
+        lib.mamba2_add_rmsnorm_backward_workspace_bytes.restype = sz
+        lib.mamba2_add_rmsnorm_backward.argtypes = [p] * 7 + [i32, i32, f32, act, act, p, sz, p]
+        lib.mamba2_linear.argtypes = [p] * 8 + [i32, i32, i32, i64, i64, i64, act, act, act, p]
+        lib.mamba2_linear_backward_workspace_bytes.argtypes = [i32, i32, i32]
+        lib.mamba2_linear_backward_workspace_bytes.restype = sz
+        lib.mamba2_linear_backward.argtypes = [p] * 7 + [i32, i32, i32, i64, act, p, sz, p]
+        for name in ("mamba2_gated_recurrence", "mamba2_gated_recurrence_step", "mamba2_gated_recurrence_step_device",
+                     "mamba2_gated_recurrence_backward", "mamba2_add_rmsnorm", "mamba2_add_rmsnorm_backward",
+                     "mamba2_linear", "mamba2_linear_backward"):
+            getattr(lib, name).restype = ctypes.c_int
         for name in ("mamba2_causal_conv1d", "mamba2_ssd_scan", "mamba2_gated_rmsnorm", "mamba2_decode_step",
                      "mamba2_decode_step_device", "mamba2_prefill_host", "mamba2_padded_spans", "mamba2_pack_rows",
                      "mamba2_unpack_rows", "mamba2_in_proj", "mamba2_out_proj", "mamba3_siso_varlen_forward"):
@@ -124,6 +151,40 @@ def _ptr(t) -> Optional[int]:
     if not t.is_contiguous():
         raise ValueError("tensors must be contiguous")
     return t.data_ptr()
+
+
+def _rows(t):
+    """(pointer, row stride) of a matrix whose columns are adjacent: a contiguous one or a column range of one."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("expected a matrix with adjacent columns")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError("rows overlap")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _type(t) -> int:
+    import torch
+    return E4M3 if t.dtype == torch.float8_e4m3fn else _dt(t)
+
+
+def _same(name, t, shape, dtype=None):
+    """Raises ValueError unless the tensor (None passes) has this shape, and this type where one is given."""
+    if t is not None and (tuple(t.shape) != tuple(shape) or (dtype is not None and t.dtype != dtype)):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}" + (f" of {dtype}" if dtype is not None else "") +
+                         f", got {tuple(t.shape)} of {t.dtype}")
+
+
+def _workspace(need: int, workspace, device, stream):
+    """(pointer, bytes, tensor) of the caller's workspace, or of one made here, whose memory is not given to other
+    work before `stream` has passed the call; keep the tensor until the call returns."""
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        import torch
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        if stream is not None:
+            workspace.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+    return _ptr(workspace), workspace.numel() * workspace.element_size(), workspace
 
 
 def _stream(stream) -> Optional[int]:
@@ -376,6 +437,206 @@ def mamba3_siso_varlen_forward(out, final_angle, final_ssm, final_k, final_v, q,
         int(rows), int(heads), int(headdim), int(q.shape[1]), int(angles.shape[1]), _stream(stream))
     if check:
         _check(st, "mamba3_siso_varlen_forward")
+    return st
+
+
+def _cu(cu_seqlens):
+    return cu_seqlens if isinstance(cu_seqlens, ctypes.Array) else (ctypes.c_int32 * max(1, len(cu_seqlens)))(*cu_seqlens)
+
+
+def gated_recurrence_checkpoints(cu_seqlens) -> int:
+    """``mamba2_gated_recurrence_checkpoints``: rows of the ``checkpoints`` of a batch with these runs."""
+    cu = _cu(cu_seqlens)
+    n = int(_lib().mamba2_gated_recurrence_checkpoints(cu, len(cu) - 1))
+    if n < 0:
+        raise Mamba2Error(ERR_RUNS_DONT_COVER_ROWS, "mamba2_gated_recurrence_checkpoints")
+    return n
+
+
+def gated_recurrence_workspace_bytes(cu_seqlens, dim, backward=False) -> int:
+    """``mamba2_gated_recurrence_workspace_bytes`` of the forward or backward call."""
+    cu = _cu(cu_seqlens)
+    return int(_lib().mamba2_gated_recurrence_workspace_bytes(cu, len(cu) - 1, int(dim), 1 if backward else 0))
+
+
+def gated_recurrence(y, x, gate, lower, state, cu_seqlens=None, slots=None, fresh=None, checkpoints=None,
+                     workspace=None, stream=None, check=True, batch=None) -> int:
+    """``mamba2_gated_recurrence``: h_t = f_t h_{t-1} + (1 - f_t) x_t over packed runs, f from ``gate`` and the
+    lower bounds; ``state`` updated at the slots. x, gate and y may be column ranges of wider matrices.
+    ``checkpoints`` [gated_recurrence_checkpoints(cu_seqlens), dim] f32 is for the backward pass."""
+    import torch
+    rows, dim = x.shape
+    b = _batch(cu_seqlens, slots, fresh, batch)
+    _same("gate", gate, x.shape, x.dtype)
+    _same("y", y, x.shape, x.dtype)
+    _same("lower", lower, (dim,), torch.float32)
+    _same("state", state, (state.shape[0], dim), torch.float32)
+    if checkpoints is not None and b.cu is not None:
+        _same("checkpoints", checkpoints, (gated_recurrence_checkpoints(b.cu), dim), torch.float32)
+    need = gated_recurrence_workspace_bytes(b.cu, dim) if workspace is None and b.cu is not None else 0
+    ws, ws_bytes, _keep = _workspace(need, workspace, x.device, stream)
+    (yp, ly), (xp, lx), (gp, lg) = _rows(y), _rows(x), _rows(gate)
+    st = _lib().mamba2_gated_recurrence(yp, _ptr(checkpoints), xp, gp, _ptr(lower), _ptr(state), state.shape[0], rows,
+                                        dim, ly, lx, lg, _dt(x), b.ref(), ws, ws_bytes, _stream(stream))
+    if check:
+        _check(st, "mamba2_gated_recurrence")
+    return st
+
+
+def gated_recurrence_step(y, x, gate, lower, state, slots=None, fresh=None, cu_seqlens=None, stream=None, check=True,
+                          batch=None) -> int:
+    """``mamba2_gated_recurrence_step``: one token per sequence."""
+    import torch
+    b = _batch(cu_seqlens, slots, fresh, batch)
+    dim = x.shape[1]
+    _same("x", x, (b.rb.num_seqs, dim))
+    _same("gate", gate, x.shape, x.dtype)
+    _same("y", y, x.shape, x.dtype)
+    _same("lower", lower, (dim,), torch.float32)
+    _same("state", state, (state.shape[0], dim), torch.float32)
+    (yp, ly), (xp, lx), (gp, lg) = _rows(y), _rows(x), _rows(gate)
+    st = _lib().mamba2_gated_recurrence_step(yp, xp, gp, _ptr(lower), _ptr(state), state.shape[0], dim, ly, lx, lg,
+                                             _dt(x), b.ref(), _stream(stream))
+    if check:
+        _check(st, "mamba2_gated_recurrence_step")
+    return st
+
+
+def gated_recurrence_step_device(y, x, gate, lower, state, slots_dev, fresh_dev, num_seqs_dev, status_dev, stream=None,
+                                 check=True) -> int:
+    """``mamba2_gated_recurrence_step_device``: the step with its batch in device memory, as ``decode_step_device``
+    takes it (``fresh_dev`` may be None: no sequence is fresh)."""
+    import torch
+    cap, dim = int(slots_dev.shape[0]), x.shape[1]
+    _same("x", x, (cap, dim))
+    _same("gate", gate, x.shape, x.dtype)
+    _same("y", y, x.shape, x.dtype)
+    _same("lower", lower, (dim,), torch.float32)
+    _same("state", state, (state.shape[0], dim), torch.float32)
+    _same("slots_dev", slots_dev, (cap,), torch.int32)
+    _same("fresh_dev", fresh_dev, (cap,), torch.uint8)
+    _same("num_seqs_dev", num_seqs_dev, (1,), torch.int32)
+    _same("status_dev", status_dev, (1,), torch.int32)
+    (yp, ly), (xp, lx), (gp, lg) = _rows(y), _rows(x), _rows(gate)
+    st = _lib().mamba2_gated_recurrence_step_device(yp, xp, gp, _ptr(lower), _ptr(state), state.shape[0], dim, ly, lx,
+                                                    lg, _dt(x), _ptr(slots_dev), _ptr(fresh_dev), _ptr(num_seqs_dev),
+                                                    cap, _ptr(status_dev), _stream(stream))
+    if check:
+        _check(st, "mamba2_gated_recurrence_step_device")
+    return st
+
+
+def gated_recurrence_backward(dx, dgate, dlower, dstate, dy, dstate_end, x, gate, lower, checkpoints, cu_seqlens,
+                              workspace=None, stream=None, check=True) -> int:
+    """``mamba2_gated_recurrence_backward``: gradients of x, gate, lower and the initial states (``dlower``, ``dstate``
+    and ``dstate_end`` may be None) from the forward call's checkpoints."""
+    import torch
+    rows, dim = x.shape
+    cu = _cu(cu_seqlens)
+    n = len(cu) - 1
+    for name, t in (("gate", gate), ("dy", dy), ("dx", dx), ("dgate", dgate)):
+        _same(name, t, x.shape, x.dtype)
+    for name, t in (("lower", lower), ("dlower", dlower)):
+        _same(name, t, (dim,), torch.float32)
+    for name, t in (("dstate", dstate), ("dstate_end", dstate_end)):
+        _same(name, t, (n, dim), torch.float32)
+    _same("checkpoints", checkpoints, (gated_recurrence_checkpoints(cu), dim), torch.float32)
+    need = gated_recurrence_workspace_bytes(cu, dim, True) if workspace is None else 0
+    ws, ws_bytes, _keep = _workspace(need, workspace, x.device, stream)
+    (dxp, ldx), (dgp, ldg), (dyp, ldy), (xp, lx), (gp, lg) = _rows(dx), _rows(dgate), _rows(dy), _rows(x), _rows(gate)
+    st = _lib().mamba2_gated_recurrence_backward(dxp, dgp, _ptr(dlower), _ptr(dstate), dyp, _ptr(dstate_end), xp, gp,
+                                                 _ptr(lower), _ptr(checkpoints), rows, dim, ldx, ldg, ldy, lx, lg,
+                                                 _dt(x), cu, n, ws, ws_bytes, _stream(stream))
+    if check:
+        _check(st, "mamba2_gated_recurrence_backward")
+    return st
+
+
+def add_rmsnorm(out, x, weight, eps, residual=None, sum=None, scale=None, stream=None, check=True) -> int:
+    """``mamba2_add_rmsnorm``: s = x + residual, out = s / rms(s) * weight; ``sum`` gets s (it may be ``residual``).
+    An e4m3 ``out`` takes a ``scale`` per row: out * scale is the normed row."""
+    import torch
+    rows, dim = x.shape
+    wide = residual if residual is not None else sum
+    stype = _dt(wide) if wide is not None else _dt(x)
+    _same("out", out, x.shape)
+    _same("weight", weight, (dim,), torch.float32)
+    _same("residual", residual, x.shape)
+    _same("sum", sum, x.shape, wide.dtype if wide is not None else None)
+    _same("scale", scale, (rows,), torch.float32)
+    st = _lib().mamba2_add_rmsnorm(_ptr(out), _ptr(scale), _ptr(sum), _ptr(x), _ptr(residual), _ptr(weight), rows, dim,
+                                   float(eps), _dt(x), stype, _type(out), _stream(stream))
+    if check:
+        _check(st, "mamba2_add_rmsnorm")
+    return st
+
+
+def add_rmsnorm_backward(dx, dresidual, dweight, dy, dsum, sum, weight, eps, workspace=None, stream=None,
+                         check=True) -> int:
+    """``mamba2_add_rmsnorm_backward``: from ``sum`` and the gradients of both outputs (``dsum`` may be None) to those
+    of x, the residual and the weight (each may be None). ``dresidual`` may be ``dsum`` itself."""
+    import torch
+    rows, dim = sum.shape
+    _same("dy", dy, sum.shape)
+    _same("dx", dx, sum.shape, dy.dtype)
+    _same("dresidual", dresidual, sum.shape, sum.dtype)
+    _same("dsum", dsum, sum.shape, sum.dtype)
+    _same("weight", weight, (dim,), torch.float32)
+    _same("dweight", dweight, (dim,), torch.float32)
+    need = 0
+    if workspace is None and dweight is not None:
+        need = int(_lib().mamba2_add_rmsnorm_backward_workspace_bytes(rows, dim))
+    ws, ws_bytes, _keep = _workspace(need, workspace, sum.device, stream)
+    st = _lib().mamba2_add_rmsnorm_backward(_ptr(dx), _ptr(dresidual), _ptr(dweight), _ptr(dy), _ptr(dsum), _ptr(sum),
+                                            _ptr(weight), rows, dim, float(eps), _dt(dy), _dt(sum), ws, ws_bytes,
+                                            _stream(stream))
+    if check:
+        _check(st, "mamba2_add_rmsnorm_backward")
+    return st
+
+
+def linear(out, x, w, x_scale=None, w_scale=None, bias=None, residual=None, activation="none", pre=None, stream=None,
+           check=True) -> int:
+    """``mamba2_linear``: out = activation(x . w^T * scales + bias) + residual from bf16 or e4m3 operands. x, out and
+    residual may be column ranges of wider matrices; ``pre`` gets the pre-activation for the backward pass."""
+    import torch
+    (rows, k), n = x.shape, w.shape[0]
+    _same("w", w, (n, k), x.dtype)
+    _same("out", out, (rows, n))
+    _same("x_scale", x_scale, (rows,), torch.float32)
+    _same("w_scale", w_scale, (n,), torch.float32)
+    _same("bias", bias, (n,), torch.float32)
+    _same("residual", residual, (rows, n), out.dtype)
+    _same("pre", pre, (rows, n), torch.bfloat16)
+    (op, lo), (xp, lx) = _rows(out), _rows(x)
+    rp, lr = _rows(residual) if residual is not None else (None, 0)
+    st = _lib().mamba2_linear(op, _ptr(pre), xp, _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(bias), rp, rows, k, n, lo,
+                              lx, lr, _type(x), _dt(out), ACTIVATIONS[activation], _stream(stream))
+    if check:
+        _check(st, "mamba2_linear")
+    return st
+
+
+def linear_backward(dx, dw, dbias, dy, x, w, activation="none", pre=None, workspace=None, stream=None,
+                    check=True) -> int:
+    """``mamba2_linear_backward``: gradients of x, w and bias (each may be None) from dy and the forward's ``pre``."""
+    import torch
+    (rows, k), n = x.shape, w.shape[0]
+    bf16 = torch.bfloat16
+    _same("x", x, (rows, k), bf16)
+    _same("w", w, (n, k), bf16)
+    _same("dy", dy, (rows, n), bf16)
+    _same("pre", pre, (rows, n), bf16)
+    _same("dx", dx, (rows, k), bf16)
+    _same("dw", dw, (n, k), bf16)
+    _same("dbias", dbias, (n,), torch.float32)
+    need = int(_lib().mamba2_linear_backward_workspace_bytes(rows, k, n)) if workspace is None else 0
+    ws, ws_bytes, _keep = _workspace(need, workspace, x.device, stream)
+    xp, lx = _rows(x)
+    st = _lib().mamba2_linear_backward(_ptr(dx), _ptr(dw), _ptr(dbias), _ptr(dy), _ptr(pre), xp, _ptr(w), rows, k, n,
+                                       lx, ACTIVATIONS[activation], ws, ws_bytes, _stream(stream))
+    if check:
+        _check(st, "mamba2_linear_backward")
     return st
 
 

@@ -13,19 +13,21 @@
 #include <vector>
 
 #include "../../include/mamba3.h"
+#include "host.h"
 #include "kernels.h"
 
 namespace mamba2 {
 namespace {
-
 thread_local char g_cuda_error[256] = "";
+}
 
 mamba2_status cuda_fail(cudaError_t e) {
   std::snprintf(g_cuda_error, sizeof g_cuda_error, "%s: %s", cudaGetErrorName(e), cudaGetErrorString(e));
   return MAMBA2_ERR_CUDA;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+namespace {
+
 // the streamed prefill's internal copy streams and events, kept per host thread and
 // CUDA context (see mamba2_prefill_host)
 struct CopyLanes {
@@ -37,10 +39,8 @@ struct CopyLanes {
 // never reused); false when there is none or the driver cannot say
 bool current_context_id(unsigned long long* id);
 
-size_t act_size(mamba2_dtype a) { return a == MAMBA2_F32 ? 4 : 2; }
-bool act_ok(mamba2_dtype a) { return a == MAMBA2_F32 || a == MAMBA2_BF16; }
+}  // namespace
 
-// Slot range, then shared slots, then coverage of [0, rows).
 mamba2_status validate_batch(const mamba2_recurrent_batch* rb, int32_t num_slots, int32_t rows,
                              bool need_cu) {
   if (!rb || rb->num_seqs < 0 || rb->num_seqs > MAMBA2_MAX_SEQS || num_slots < 0 || rows < 0)
@@ -50,8 +50,9 @@ mamba2_status validate_batch(const mamba2_recurrent_batch* rb, int32_t num_slots
   if (!rb->slots || !rb->fresh || (need_cu && !rb->cu_seqlens)) return MAMBA2_ERR_INVALID_ARGUMENT;
   for (int i = 0; i < n; ++i)
     if (rb->slots[i] < 0 || rb->slots[i] >= num_slots) return MAMBA2_ERR_SLOT_OUT_OF_RANGE;
-  std::vector<int32_t> sorted(rb->slots, rb->slots + n);
-  std::sort(sorted.begin(), sorted.end());
+  int32_t sorted[MAMBA2_MAX_SEQS];
+  std::copy(rb->slots, rb->slots + n, sorted);
+  std::sort(sorted, sorted + n);
   for (int i = 1; i < n; ++i)
     if (sorted[i] == sorted[i - 1]) return MAMBA2_ERR_SLOT_SHARED;
   if (rb->cu_seqlens) {
@@ -64,7 +65,6 @@ mamba2_status validate_batch(const mamba2_recurrent_batch* rb, int32_t num_slots
   return MAMBA2_OK;
 }
 
-// Fill cu and slot/fresh; tiles are set by the caller.
 void fill_table(SeqTable& t, const mamba2_recurrent_batch* rb) {
   t.n = rb->num_seqs;
   t.cu[0] = 0;
@@ -84,6 +84,8 @@ int device_sm_count() {
   if (dev >= 0 && dev < 64) cache[dev] = n;
   return n;
 }
+
+namespace {
 
 bool dims_ok(const mamba2_dims* d) {
   return d && d->heads > 0 && d->headdim > 0 && d->d_state > 0 && d->ngroups > 0 &&

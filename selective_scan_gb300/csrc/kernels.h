@@ -136,6 +136,119 @@ struct GemmArgs {
 cudaError_t launch_gemm_tc(const GemmArgs& g, const void* A, const void* B, cudaStream_t st);
 unsigned int read_gemm_timeouts();
 
+// ------------------------------------------------------ recurrent block ----
+// Gated recurrence, forward. tab.tile[i] = the sequence's first chunk (chunks of
+// MAMBA2_RECURRENCE_CHUNK tokens, ceil(length / chunk) a sequence).
+struct RecArgs {
+  void* y;
+  float* ckpt;  // [chunks, dim] or null
+  const void* x;
+  const void* gate;
+  const float* lower;  // [dim] or null
+  float* state;
+  int32_t dim;
+  int64_t ld_y, ld_x, ld_gate;
+  SeqTable tab;
+};
+cudaError_t launch_recurrence(const RecArgs& a, mamba2_dtype act, void* ws, cudaStream_t st);
+size_t recurrence_workspace(int64_t chunks, bool chained, int32_t dim, bool backward);
+
+struct RecStepArgs {
+  void* y;
+  const void* x;
+  const void* gate;
+  const float* lower;
+  float* state;
+  int32_t dim, n;  // n: sequences, or the capacity of a device batch
+  int64_t ld_y, ld_x, ld_gate;
+  const int32_t* dev_slots;  // device batch (null for a host batch), as in DecodeArgs
+  const uint8_t* dev_fresh;
+  const int32_t* dev_n;
+  const int32_t* dev_status;
+  uint32_t slot_fresh[MAMBA2_MAX_SEQS];
+};
+cudaError_t launch_recurrence_step(const RecStepArgs& a, mamba2_dtype act, cudaStream_t st);
+
+// Gated recurrence, backward (tab.tile as in RecArgs; slots unused).
+struct RecBwdArgs {
+  void* dx;
+  void* dgate;
+  float* dlower;
+  float* dstate;
+  const void* dy;
+  const float* dstate_end;
+  const void* x;
+  const void* gate;
+  const float* lower;
+  const float* ckpt;
+  int32_t dim;
+  int64_t ld_dx, ld_dgate, ld_dy, ld_x, ld_gate;
+  SeqTable tab;
+};
+cudaError_t launch_recurrence_backward(const RecBwdArgs& a, mamba2_dtype act, void* ws, cudaStream_t st);
+
+struct AddNormArgs {
+  void* out;
+  float* scale;
+  void* sum;
+  const void* x;
+  const void* residual;
+  const float* weight;
+  int32_t rows, dim;
+  float eps;
+};
+cudaError_t launch_add_rmsnorm(const AddNormArgs& a, mamba2_dtype act, mamba2_dtype sum_type, mamba2_dtype out_type,
+                               cudaStream_t st);
+
+struct AddNormBwdArgs {
+  void* dx;
+  void* dresidual;
+  float* dweight;
+  const void* dy;
+  const void* dsum;
+  const void* sum;
+  const float* weight;
+  float* partial;  // [add_rmsnorm_backward_parts, dim]
+  int32_t rows, dim;
+  float eps;
+};
+int add_rmsnorm_backward_parts(int32_t rows, int32_t dim);
+cudaError_t launch_add_rmsnorm_backward(const AddNormBwdArgs& a, mamba2_dtype act, mamba2_dtype sum_type,
+                                        cudaStream_t st);
+
+struct LinearArgs {
+  void* out;
+  void* pre;
+  const void* x;
+  const float* x_scale;
+  const void* w;
+  const float* w_scale;
+  const float* bias;
+  const void* residual;
+  int32_t rows, in_f, out_f;
+  int64_t ld_out, ld_x, ld_res;
+};
+cudaError_t launch_linear(const LinearArgs& a, mamba2_dtype in, mamba2_dtype out, int act, cudaStream_t st);
+
+struct LinearBwdArgs {
+  void* dx;
+  void* dw;
+  float* dbias;
+  const void* dy;
+  const void* pre;
+  const void* x;
+  const void* w;
+  int32_t rows, in_f, out_f;
+  int64_t ld_x;
+  void* dp;        // [rows, ld_dp] bf16, or null where dy serves
+  int64_t ld_dp;
+  float* partial;  // [linear_bias_parts(rows), out_f] column sums
+};
+int linear_bias_parts(int32_t rows);
+cudaError_t launch_linear_backward(const LinearBwdArgs& a, int act, cudaStream_t st);
+unsigned int read_linear_timeouts();
+unsigned int read_recurrence_timeouts();
+
 // ------------------------------------------------------------ mamba3 ----
 // Mamba-3 SISO varlen forward (head width 64, Q/K width 128). Sequence i owns
 // rows [cu[i], cu[i+1]); order[] lists the sequences longest first (the CTAs
