@@ -321,8 +321,14 @@ mamba2_status mamba2_selftest_bounded_wait(int32_t* status_dev, void* stream) {
 }
 
 unsigned int mamba2_device_timeouts(void) {
-  const unsigned int a = read_device_timeouts(), b = read_gemm_timeouts(), c = read_m3_timeouts();
-  return (a == 0xffffffffu || b == 0xffffffffu || c == 0xffffffffu) ? 0xffffffffu : a + b + c;
+  const unsigned int counts[] = {read_device_timeouts(), read_gemm_timeouts(), read_m3_timeouts(),
+                                 read_linear_timeouts()};
+  unsigned int sum = 0;
+  for (const unsigned int c : counts) {
+    if (c == 0xffffffffu) return c;
+    sum += c;
+  }
+  return sum;
 }
 
 mamba2_status mamba3_siso_varlen_forward(void* out, void* final_angle, float* final_ssm, float* final_k,

@@ -1,21 +1,39 @@
 // Matrix product with bias, activation and residual in its epilogue (block.h), from bf16
-// or e4m3 operands, and its backward pass.
+// or e4m3 operands, and its backward pass: tcgen05 products, fp32 accumulators in tensor
+// memory, operands by TMA.
 //
-// 64 x 64 output tiles, 16 deep, staged in shared memory, 16 products a thread on the
-// CUDA cores.
+// Many rows: pairs of CTAs (cta_group::2), persistent, 256 x 256 output tiles, N fastest.
+// Each CTA of a pair loads its half of A (128 rows) and of B (128 columns) per k-block of
+// 128 bytes, so a pair moves 64 KB from L2 per 256 x 256 x 64 (bf16) products, two thirds
+// of what two CTAs with 128 x 256 tiles of their own would. Roles in each CTA:
+//   warp 0      TMA loads, completing on the leader's barrier of the stage
+//   warp 1      (leader) tcgen05.mma into one of two 256-column accumulators; commits
+//               free the stage and publish the accumulator in both CTAs
+//   warps 2-9   epilogue of this CTA's 128 rows while the next tile's products run:
+//               tensor memory -> registers -> shared memory (32 x 32 blocks, so that a
+//               warp's loads and stores of global memory follow the rows) -> scales,
+//               bias, activation, residual -> global
+// Few rows: the weight takes the instruction's 128 rows and the tokens its N, and a
+// cluster splits the K axis, see few_rows_kernel.
+//
+// Every mbarrier wait is bounded; a timeout stops the CTA's roles, drains what was
+// issued, frees tensor memory and counts the CTA in g_linear_timeouts.
+#include <cuda.h>
 #include <cuda_fp8.h>
+
+#include <algorithm>
+#include <cstring>
 
 #include "../../include/block.h"
 #include "common.cuh"
 
 namespace mamba2 {
+
+__device__ unsigned int g_linear_timeouts = 0;
+
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kTile = 64, kDeep = 16;
-
-__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_float(__nv_fp8_e4m3 v) { return float(v); }
+#include "tc.cuh"
 
 __device__ __forceinline__ float activate(float v, int act) {
   switch (act) {
@@ -38,54 +56,429 @@ __device__ __forceinline__ float slope(float v, int act) {
   return 1.0f;
 }
 
-// acc[i][j] of rows m0 + ty + 16 i, columns n0 + tx + 16 j of the product of A(m, k) and B(n, k)
-template <typename FA, typename FB>
-__device__ __forceinline__ void tile_product(int M, int N, int K, FA A, FB B, float (&acc)[4][4]) {
-  __shared__ float sa[kDeep][kTile + 1], sb[kDeep][kTile + 1];
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  const int m0 = blockIdx.y * kTile, n0 = blockIdx.x * kTile;
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
-  for (int k0 = 0; k0 < K; k0 += kDeep) {
-    for (int e = threadIdx.x; e < kTile * kDeep; e += kThreads) {
-      const int r = e / kDeep, k = e % kDeep;
-      sa[k][r] = m0 + r < M && k0 + k < K ? A(m0 + r, k0 + k) : 0.0f;
-      sb[k][r] = n0 + r < N && k0 + k < K ? B(n0 + r, k0 + k) : 0.0f;
+// One product D[M][N] = sum_k A(m, k) B(n, k) and what its epilogue does:
+// D * scale_m[m] * scale_n[n] + bias[n] -> pre; activation; + residual -> out.
+struct Product {
+  int M, N, K;
+  void* out;
+  int64_t ld_out;
+  const void* residual;
+  int64_t ld_res;
+  __nv_bfloat16* pre;  // row stride N
+  const float* scale_m;
+  const float* scale_n;
+  const float* bias;
+  int act;
+  int vec;  // four columns at once: every matrix of the epilogue has rows aligned for them
+};
+
+// Four columns of one output row.
+template <typename TO> struct Quad;
+template <> struct Quad<__nv_bfloat16> {
+  using Raw = uint2;
+  __device__ __forceinline__ static void unpack(Raw r, float (&v)[4]) {
+    v[0] = __uint_as_float(r.x << 16);
+    v[1] = __uint_as_float(r.x & 0xffff0000u);
+    v[2] = __uint_as_float(r.y << 16);
+    v[3] = __uint_as_float(r.y & 0xffff0000u);
+  }
+  __device__ __forceinline__ static Raw pack(const float (&v)[4]) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+    return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  }
+};
+template <> struct Quad<float> {
+  using Raw = float4;
+  __device__ __forceinline__ static void unpack(Raw r, float (&v)[4]) {
+    v[0] = r.x;
+    v[1] = r.y;
+    v[2] = r.z;
+    v[3] = r.w;
+  }
+  __device__ __forceinline__ static Raw pack(const float (&v)[4]) { return make_float4(v[0], v[1], v[2], v[3]); }
+};
+
+// Per-column constants of four columns from col on (those past N are not used).
+struct Columns {
+  float scale[4], bias[4];
+};
+__device__ __forceinline__ Columns load_columns(const Product& g, int col) {
+  Columns c;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const bool in = col + j < g.N;
+    c.scale[j] = g.scale_n && in ? g.scale_n[col + j] : 1.0f;
+    c.bias[j] = g.bias && in ? g.bias[col + j] : 0.0f;
+  }
+  return c;
+}
+
+template <typename TO>
+__device__ __forceinline__ typename Quad<TO>::Raw load_residual(const Product& g, int64_t row, int col) {
+  typename Quad<TO>::Raw r = {};
+  if (!g.residual || row >= g.M || col >= g.N) return r;
+  const TO* p = static_cast<const TO*>(g.residual) + row * g.ld_res + col;
+  if (g.vec && col + 4 <= g.N) return *reinterpret_cast<const typename Quad<TO>::Raw*>(p);
+  float v[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = col + j < g.N ? Act<TO>::to_f(p[j]) : 0.0f;
+  return Quad<TO>::pack(v);
+}
+
+template <typename TO>
+__device__ __forceinline__ void finish(const Product& g, int64_t row, int col, float (&v)[4], const Columns& c,
+                                       typename Quad<TO>::Raw res) {
+  if (row >= g.M || col >= g.N) return;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = fmaf(v[j], c.scale[j], c.bias[j]);
+  const bool whole = g.vec && col + 4 <= g.N;
+  if (g.pre) {
+    __nv_bfloat16* p = g.pre + row * g.N + col;
+    if (whole) {
+      *reinterpret_cast<uint2*>(p) = Quad<__nv_bfloat16>::pack(v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (col + j < g.N) p[j] = __float2bfloat16_rn(v[j]);
     }
-    __syncthreads();
-    for (int k = 0; k < kDeep; ++k)
-      for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[k][ty + 16 * i], sb[k][tx + 16 * j], acc[i][j]);
-    __syncthreads();
+  }
+  if (g.act != MAMBA2_ACT_NONE) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = activate(v[j], g.act);
+  }
+  if (g.residual) {
+    float r[4];
+    Quad<TO>::unpack(res, r);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] += r[j];
+  }
+  TO* o = static_cast<TO*>(g.out) + row * g.ld_out + col;
+  if (whole) {
+    *reinterpret_cast<typename Quad<TO>::Raw*>(o) = Quad<TO>::pack(v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (col + j < g.N) o[j] = Act<TO>::from_f(v[j]);
   }
 }
 
-template <typename TI, typename TO>
-__global__ void __launch_bounds__(kThreads) linear_kernel(const LinearArgs a, int act) {
-  const TI* x = static_cast<const TI*>(a.x);
-  const TI* w = static_cast<const TI*>(a.w);
-  float acc[4][4];
-  tile_product(a.rows, a.out_f, a.in_f, [&](int m, int k) { return to_float(x[m * a.ld_x + k]); },
-               [&](int n, int k) { return to_float(w[(int64_t)n * a.in_f + k]); }, acc);
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int m = blockIdx.y * kTile + threadIdx.x / 16 + 16 * i, n = blockIdx.x * kTile + threadIdx.x % 16 + 16 * j;
-      if (m >= a.rows || n >= a.out_f) continue;
-      float v = acc[i][j];
-      if (a.w_scale) v = v * a.x_scale[m] * a.w_scale[n];
-      if (a.bias) v += a.bias[n];
-      if (a.pre) static_cast<__nv_bfloat16*>(a.pre)[(int64_t)m * a.out_f + n] = __float2bfloat16_rn(v);
-      v = activate(v, act);
-      if (a.residual) v += Act<TO>::to_f(static_cast<const TO*>(a.residual)[m * a.ld_res + n]);
-      static_cast<TO*>(a.out)[m * a.ld_out + n] = Act<TO>::from_f(v);
-    }
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+// ---- cluster helpers
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// Descriptor of a staged operand: rows of 128 bytes, 128-byte swizzle. K along the row, or
+// (mn) M or N along the row, the k-block's kRows rows deep, 64 columns to a block of kRows rows.
+template <bool mn, int kRows>
+__device__ __forceinline__ uint64_t operand(uint32_t addr) {
+  return mn ? sdesc(addr, kRows * 128, 1024) : sdesc(addr, 16, 1024);
+}
+// One tcgen05.mma takes 32 bytes of K: a step along the row, or 16 rows of 128 bytes.
+template <bool mn>
+__device__ __forceinline__ uint64_t k_step(int k) {
+  return mn ? (uint64_t)((k * 2048) >> 4) : (uint64_t)(2 * k);
+}
+__host__ __device__ constexpr uint32_t idesc(bool f8, int M, int N, bool a_mn, bool b_mn) {
+  const uint32_t type = f8 ? 0u : 1u;  // kind::f8f6f4: e4m3 = 0; kind::f16: bf16 = 1
+  return (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
+         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+constexpr uint32_t kRowBytes = 128;  // a k-block: 64 bf16 or 128 e4m3
+
+// ------------------------------------------------------------------ many rows
+
+constexpr int kBM = 256, kBN = 256, kStages = 5;
+constexpr int kEpiWarps = 8, kThreads = 32 * (2 + kEpiWarps);
+constexpr uint32_t kHalf = 128 * kRowBytes;  // one CTA's half of A or B: 16 KB
+constexpr uint32_t kStage = 2 * kHalf;
+constexpr uint32_t kOffEpi = kStages * kStage;
+constexpr int kEpiLd = 36;  // floats between the rows of a warp's 32 x 32 block: 16-byte accesses without conflicts
+constexpr uint32_t kEpiBytes = 32 * kEpiLd * 4;
+constexpr uint32_t kOffBar = kOffEpi + kEpiWarps * kEpiBytes;
+enum Bar : int { kFull = 0, kEmpty = kStages, kAccFull = 2 * kStages, kAccEmpty = 2 * kStages + 2,
+                 kDone = 2 * kStages + 4, kNumBars = 2 * kStages + 5 };
+constexpr uint32_t kOffMisc = kOffBar + 8 * kNumBars;
+constexpr uint32_t kSmem = kOffMisc + 16 + 1024;
+static_assert(kSmem <= 232448, "shared memory plan exceeds 227 KB");
+
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* tm, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+      :: "r"(dst), "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+template <bool F8>
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  if constexpr (F8)
+    asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\ntcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
+                 :: "r"(d), "l"(a), "l"(b), "r"(id), "r"(acc));
+  else
+    asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\ntcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n"
+                 :: "r"(d), "l"(a), "l"(b), "r"(id), "r"(acc));
+}
+__device__ __forceinline__ void commit_pair(uint32_t bar) {  // arrives at this offset in both CTAs
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+               :: "r"(bar), "h"((uint16_t)3) : "memory");
+}
+
+// The operand's k-block kb, 128 of its rows (or columns) from r0 on, into dst.
+template <bool F8, bool mn>
+__device__ __forceinline__ void load_half(uint32_t dst, const CUtensorMap* tm, int kb, int r0, uint32_t bar) {
+  constexpr int depth = F8 ? 128 : 64;
+  if constexpr (mn) {
+    tma_load_pair(dst, tm, r0, kb * depth, bar);
+    tma_load_pair(dst + kHalf / 2, tm, r0 + 64, kb * depth, bar);
+  } else {
+    tma_load_pair(dst, tm, kb * depth, r0, bar);
+  }
+}
+
+template <bool F8, bool A_MN, bool B_MN, typename TO>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+pair_kernel(const __grid_constant__ Product g, const __grid_constant__ CUtensorMap tma,
+            const __grid_constant__ CUtensorMap tmb) {
+  static_assert(!F8 || (!A_MN && !B_MN), "8-bit operands have K along the row");
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw_base = su32(smem_raw);
+  unsigned char* smem = smem_raw + (((raw_base + 1023u) & ~1023u) - raw_base);
+  const uint32_t sbase = su32(smem);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kOffMisc);
+  volatile uint32_t* s_abort = reinterpret_cast<volatile uint32_t*>(smem + kOffMisc + 4);
+  auto bar = [&](int id) { return sbase + kOffBar + 8u * (uint32_t)id; };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+
+  constexpr int depth = F8 ? 128 : 64;
+  const int tiles_n = (g.N + kBN - 1) / kBN;
+  const int tiles = (g.M + kBM - 1) / kBM * tiles_n;
+  const int kblocks = (g.K + depth - 1) / depth;
+  const int pair = (int)blockIdx.x >> 1, npairs = (int)gridDim.x >> 1;
+  const int my_tiles = pair < tiles ? (tiles - 1 - pair) / npairs + 1 : 0;
+  auto tile_m0 = [&](int t) { return ((pair + t * npairs) / tiles_n) * kBM; };
+  auto tile_n0 = [&](int t) { return ((pair + t * npairs) % tiles_n) * kBN; };
+
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" :: "r"(su32(s_tmem)));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  if (threadIdx.x == 32) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(bar(kFull + s), 1);   // (leader) its own expect_tx; both CTAs' bytes
+      mbar_init(bar(kEmpty + s), 1);  // the products' commit
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(bar(kAccFull + b), 1);
+      mbar_init(bar(kAccEmpty + b), 2 * kEpiWarps);  // (leader) both CTAs' epilogue warps
+    }
+    mbar_init(bar(kDone), 1);
+    *s_abort = 0u;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers are ready before either signals the other's
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+
+  if (warp == 0) {
+    // =================== TMA producer
+    int it = 0, issued = 0;
+    bool ok = true;
+    for (int t = 0; t < my_tiles && ok; ++t) {
+      const int m0 = tile_m0(t) + (int)rank * 128, n0 = tile_n0(t) + (int)rank * 128;
+      for (int kb = 0; kb < kblocks; ++kb, ++it) {
+        const int s = it % kStages;
+        if (it >= kStages && !warp_wait(bar(kEmpty + s), (uint32_t)(((it / kStages) - 1) & 1), s_abort)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          const uint32_t dst = sbase + (uint32_t)s * kStage;
+          const uint32_t full = at_rank(bar(kFull + s), 0);
+          if (leader) mbar_expect_tx(bar(kFull + s), 2 * kStage);
+          load_half<F8, A_MN>(dst, &tma, kb, m0, full);
+          load_half<F8, B_MN>(dst + kHalf, &tmb, kb, n0, full);
+        }
+        __syncwarp();
+        issued = it + 1;
+      }
+    }
+    // on an abort, let the loads in flight land before the pair exits
+    if (lane == 0 && leader && *s_abort)
+      for (int i = max(0, issued - kStages); i < issued; ++i)
+        drain_bar(bar(kFull + i % kStages), (uint32_t)((i / kStages) & 1));
+  } else if (warp == 1) {
+    // =================== MMA issuer
+    if (leader && lane == 0) {
+      constexpr uint32_t id = idesc(F8, kBM, kBN, A_MN, B_MN);
+      int it = 0;
+      bool ok = true;
+      for (int t = 0; t < my_tiles && ok; ++t) {
+        const int buf = t & 1;
+        if (t >= 2 && !wait_bar(bar(kAccEmpty + buf), (uint32_t)(((t >> 1) - 1) & 1), s_abort)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(buf * kBN);
+        for (int kb = 0; kb < kblocks; ++kb, ++it) {
+          const int s = it % kStages;
+          if (!wait_bar(bar(kFull + s), (uint32_t)((it / kStages) & 1), s_abort)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a0 = sbase + (uint32_t)s * kStage;
+          const uint64_t ad = operand<A_MN, depth>(a0), bd = operand<B_MN, depth>(a0 + kHalf);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_pair<F8>(d, ad + k_step<A_MN>(k), bd + k_step<B_MN>(k), id, (kb > 0 || k > 0) ? 1u : 0u);
+          commit_pair(bar(kEmpty + s));
+        }
+        if (!ok) break;
+        commit_pair(bar(kAccFull + buf));
+      }
+      // everything issued completes before the pair frees tensor memory
+      commit_pair(bar(kDone));
+      drain_bar(bar(kDone), 0u);
+    }
+    __syncwarp();
+  } else {
+    // =================== epilogue: lanes 32 (warp % 4) .. + 31, one half of the columns
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t lane_off = (uint32_t)(q * 32) << 16;
+    float* blk = reinterpret_cast<float*>(smem + kOffEpi + (uint32_t)(warp - 2) * kEpiBytes);
+    for (int t = 0; t < my_tiles; ++t) {
+      const int buf = t & 1;
+      const int64_t row0 = (int64_t)tile_m0(t) + (int)rank * 128 + q * 32;
+      const int n0 = tile_n0(t) + half * 128;
+      const float sm = g.scale_m && row0 + lane < g.M ? g.scale_m[row0 + lane] : 1.0f;
+      if (!warp_wait(bar(kAccFull + buf), (uint32_t)((t >> 1) & 1), s_abort)) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < 128; c += 32) {
+        const int col = n0 + c + 4 * (lane & 7);
+        if (n0 + c >= g.N || row0 >= g.M) break;  // the same for the whole warp
+        typename Quad<TO>::Raw res[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) res[i] = load_residual<TO>(g, row0 + 4 * i + (lane >> 3), col);
+        const Columns cc = load_columns(g, col);
+        uint32_t r[32];
+        tmem_ld32(tmem + lane_off + (uint32_t)(buf * kBN + half * 128 + c), r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<float4*>(blk + lane * kEpiLd + 4 * j) =
+              make_float4(__uint_as_float(r[4 * j]) * sm, __uint_as_float(r[4 * j + 1]) * sm,
+                          __uint_as_float(r[4 * j + 2]) * sm, __uint_as_float(r[4 * j + 3]) * sm);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 f = *reinterpret_cast<const float4*>(blk + (4 * i + (lane >> 3)) * kEpiLd + 4 * (lane & 7));
+          float v[4] = {f.x, f.y, f.z, f.w};
+          finish<TO>(g, row0 + 4 * i + (lane >> 3), col, v, cc, res[i]);
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0)
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
+                     :: "r"(at_rank(bar(kAccEmpty + buf), 0)) : "memory");
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && *s_abort) atomicAdd(&g_linear_timeouts, 1u);
+  cluster_sync();  // neither CTA's shared memory goes before the other is done with it
+  if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" :: "r"(tmem));
+}
+
+// ------------------------------------------------------------------ tensor maps
+
+using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                            const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                            CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+Encode encode_fn() {
+  static Encode fn = []() -> Encode {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<Encode>(p);
+  }();
+  return fn;
+}
+
+// [rows][cols] with a row stride of ld elements: boxes of 128 bytes x box_rows, 128-byte swizzle, zeros past the edges
+bool make_map(CUtensorMap* tm, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows, bool f8) {
+  std::memset(tm, 0, sizeof *tm);
+  const Encode enc = encode_fn();
+  if (!enc) return false;
+  const int e = f8 ? 1 : 2;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld * e};
+  const cuuint32_t box[2] = {(cuuint32_t)(kRowBytes / e), (cuuint32_t)box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(tm, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base),
+             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return sms;
+}
+
+template <bool F8, bool A_MN, bool B_MN, typename TO>
+cudaError_t launch_pairs(const Product& g, const void* A, int64_t lda, const void* B, int64_t ldb, cudaStream_t st) {
+  CUtensorMap tma, tmb;
+  constexpr int depth = F8 ? 128 : 64;
+  if (!(A_MN ? make_map(&tma, A, g.K, g.M, lda, depth, F8) : make_map(&tma, A, g.M, g.K, lda, 128, F8)) ||
+      !(B_MN ? make_map(&tmb, B, g.K, g.N, ldb, depth, F8) : make_map(&tmb, B, g.N, g.K, ldb, 128, F8)))
+    return cudaErrorInvalidValue;
+  auto kernel = pair_kernel<F8, A_MN, B_MN, TO>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (int64_t)((g.M + kBM - 1) / kBM) * ((g.N + kBN - 1) / kBN);
+  if (tiles > 0x3fffffff) return cudaErrorInvalidValue;
+  const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, sm_count() / 2));
+  kernel<<<2 * pairs, kThreads, kSmem, st>>>(g, tma, tmb);
+  return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------ backward: dp and the bias
+
+constexpr int kEltThreads = 256;
 constexpr int kRowsPerPart = 64;
 
 // dp = dy * activation'(pre) in bf16, and the column sums of each kRowsPerPart rows
-__global__ void __launch_bounds__(kThreads) dp_kernel(const LinearBwdArgs a, int act) {
-  const int n = blockIdx.x * kThreads + threadIdx.x;
+__global__ void __launch_bounds__(kEltThreads) dp_kernel(const LinearBwdArgs a, int act) {
+  const int n = blockIdx.x * kEltThreads + threadIdx.x;
   if (n >= a.ld_dp) return;
   const int m1 = min(a.rows, (int)(blockIdx.y + 1) * kRowsPerPart);
   float s = 0.0f;
@@ -101,58 +494,71 @@ __global__ void __launch_bounds__(kThreads) dp_kernel(const LinearBwdArgs a, int
   if (n < a.out_f) a.partial[(int64_t)blockIdx.y * a.out_f + n] = s;
 }
 
-__global__ void __launch_bounds__(kThreads) bias_sum_kernel(float* dst, const float* part, int parts, int n) {
-  const int i = blockIdx.x * kThreads + threadIdx.x;
+__global__ void __launch_bounds__(kEltThreads) bias_sum_kernel(float* dst, const float* part, int parts, int n) {
+  const int i = blockIdx.x * kEltThreads + threadIdx.x;
   if (i >= n) return;
   float s = 0.0f;
   for (int p = 0; p < parts; ++p) s += part[(int64_t)p * n + i];
   dst[i] = s;
 }
 
-// which = 0: dx[m][k] = sum_n dp[m][n] w[n][k]; 1: dw[n][k] = sum_m dp[m][n] x[m][k]
-template <int which>
-__global__ void __launch_bounds__(kThreads) grad_kernel(const LinearBwdArgs a) {
-  const __nv_bfloat16* dp = static_cast<const __nv_bfloat16*>(a.dp);
-  const __nv_bfloat16* b = static_cast<const __nv_bfloat16*>(which ? a.x : a.w);
-  const int64_t ldb = which ? a.ld_x : a.in_f;
-  const int M = which ? a.out_f : a.rows, K = which ? a.rows : a.out_f;
-  float acc[4][4];
-  tile_product(M, a.in_f, K, [&](int m, int k) { return to_float(which ? dp[k * a.ld_dp + m] : dp[m * a.ld_dp + k]); },
-               [&](int n, int k) { return to_float(b[k * ldb + n]); }, acc);
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int m = blockIdx.y * kTile + threadIdx.x / 16 + 16 * i, n = blockIdx.x * kTile + threadIdx.x % 16 + 16 * j;
-      if (m < M && n < a.in_f)
-        static_cast<__nv_bfloat16*>(which ? a.dw : a.dx)[(int64_t)m * a.in_f + n] = __float2bfloat16_rn(acc[i][j]);
-    }
+bool quad_ok(const void* p, int64_t ld, size_t elem) {
+  return !p || ((reinterpret_cast<uintptr_t>(p) & (4 * elem - 1)) == 0 && ld % 4 == 0);
 }
-
-dim3 tiles(int m, int n) { return dim3((n + kTile - 1) / kTile, (m + kTile - 1) / kTile); }
 
 }  // namespace
 
+unsigned int read_linear_timeouts() {
+  unsigned int v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_linear_timeouts, sizeof v) != cudaSuccess) return 0xffffffffu;
+  return v;
+}
+
 cudaError_t launch_linear(const LinearArgs& a, mamba2_dtype in, mamba2_dtype out, int act, cudaStream_t st) {
-  const dim3 g = tiles(a.rows, a.out_f);
+  const size_t oe = out == MAMBA2_F32 ? 4 : 2;
+  Product g = {a.rows, a.out_f, a.in_f, a.out, a.ld_out, a.residual, a.ld_res, static_cast<__nv_bfloat16*>(a.pre),
+               a.x_scale, a.w_scale, a.bias, act, 0};
+  g.vec = quad_ok(a.out, a.ld_out, oe) && quad_ok(a.residual, a.ld_res, oe) && quad_ok(a.pre, a.out_f, 2);
   if (in == MAMBA2_BF16) {
-    if (out == MAMBA2_BF16) linear_kernel<__nv_bfloat16, __nv_bfloat16><<<g, kThreads, 0, st>>>(a, act);
-    else linear_kernel<__nv_bfloat16, float><<<g, kThreads, 0, st>>>(a, act);
-  } else {
-    if (out == MAMBA2_BF16) linear_kernel<__nv_fp8_e4m3, __nv_bfloat16><<<g, kThreads, 0, st>>>(a, act);
-    else linear_kernel<__nv_fp8_e4m3, float><<<g, kThreads, 0, st>>>(a, act);
+    if (out == MAMBA2_BF16) return launch_pairs<false, false, false, __nv_bfloat16>(g, a.x, a.ld_x, a.w, a.in_f, st);
+    return launch_pairs<false, false, false, float>(g, a.x, a.ld_x, a.w, a.in_f, st);
   }
-  return cudaGetLastError();
+  if (out == MAMBA2_BF16) return launch_pairs<true, false, false, __nv_bfloat16>(g, a.x, a.ld_x, a.w, a.in_f, st);
+  return launch_pairs<true, false, false, float>(g, a.x, a.ld_x, a.w, a.in_f, st);
 }
 
 int linear_bias_parts(int32_t rows) { return (rows + kRowsPerPart - 1) / kRowsPerPart; }
 
 cudaError_t launch_linear_backward(const LinearBwdArgs& a, int act, cudaStream_t st) {
+  if (a.rows == 0) {
+    cudaError_t e = a.dw ? cudaMemsetAsync(a.dw, 0, (size_t)a.out_f * a.in_f * 2, st) : cudaSuccess;
+    if (e == cudaSuccess && a.dbias) e = cudaMemsetAsync(a.dbias, 0, (size_t)a.out_f * 4, st);
+    return e;
+  }
   const int parts = linear_bias_parts(a.rows);
-  if (parts > 0) dp_kernel<<<dim3((unsigned)((a.ld_dp + kThreads - 1) / kThreads), parts), kThreads, 0, st>>>(a, act);
-  if (a.dbias)
-    bias_sum_kernel<<<(a.out_f + kThreads - 1) / kThreads, kThreads, 0, st>>>(a.dbias, a.partial, parts, a.out_f);
-  if (a.dx && a.rows > 0) grad_kernel<0><<<tiles(a.rows, a.in_f), kThreads, 0, st>>>(a);
-  if (a.dw) grad_kernel<1><<<tiles(a.out_f, a.in_f), kThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  dp_kernel<<<dim3((unsigned)((a.ld_dp + kEltThreads - 1) / kEltThreads), parts), kEltThreads, 0, st>>>(a, act);
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess && a.dbias) {
+    bias_sum_kernel<<<(a.out_f + kEltThreads - 1) / kEltThreads, kEltThreads, 0, st>>>(a.dbias, a.partial, parts, a.out_f);
+    e = cudaGetLastError();
+  }
+  Product g = {};
+  g.N = a.in_f;
+  g.ld_out = a.in_f;
+  g.vec = a.in_f % 4 == 0;
+  if (e == cudaSuccess && a.dx) {  // dx[m][k] = sum_n dp[m][n] w[n][k]
+    g.M = a.rows;
+    g.K = a.out_f;
+    g.out = a.dx;
+    e = launch_pairs<false, false, true, __nv_bfloat16>(g, a.dp, a.ld_dp, a.w, a.in_f, st);
+  }
+  if (e == cudaSuccess && a.dw) {  // dw[n][k] = sum_m dp[m][n] x[m][k]
+    g.M = a.out_f;
+    g.K = a.rows;
+    g.out = a.dw;
+    e = launch_pairs<false, true, true, __nv_bfloat16>(g, a.dp, a.ld_dp, a.x, a.ld_x, st);
+  }
+  return e;
 }
 
 }  // namespace mamba2
