@@ -247,6 +247,7 @@ struct LinearBwdArgs {
 int linear_bias_parts(int32_t rows);
 cudaError_t launch_linear_backward(const LinearBwdArgs& a, int act, cudaStream_t st);
 unsigned int read_linear_timeouts();
+unsigned int read_recurrence_timeouts();
 
 // ------------------------------------------------------------ mamba3 ----
 // Mamba-3 SISO varlen forward (head width 64, Q/K width 128). Sequence i owns
