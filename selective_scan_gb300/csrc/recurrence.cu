@@ -9,8 +9,8 @@
 // 16 tokens each, a lane 4 bytes of channels. Per tile:
 //   1. each warp scans its tokens from zero, keeping h_t and the product of the f's in
 //      registers, and posts its map; the eight maps compose to the tile's
-//   2. the tile publishes its map in the workspace; a ninth warp meanwhile fetches what
-//      precedes the tile and folds it into the state that enters it
+//   2. the tile publishes its map in the workspace, and each warp fetches two of the (at
+//      most 16) records that precede the tile; folded, they are the state that enters it
 //   3. each warp adds (product of f's) x (its own entering state) to its tokens and stores
 // Inputs stream through a ring in shared memory by cp.async: a warp copies only the rows
 // that it will read, so the copies need no barrier, and those of the next tiles are in
@@ -38,6 +38,7 @@
 #include "common.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace mamba2 {
 
@@ -46,12 +47,12 @@ __device__ unsigned int g_recurrence_timeouts = 0;
 namespace {
 
 constexpr int kChunkR = MAMBA2_RECURRENCE_CHUNK;
-constexpr int kWarps = 8;                      // that scan; one more looks back
-constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
 constexpr int kTok = kChunkR / kWarps;         // tokens of a warp
-constexpr int kGroup = 16;                     // chunks between two published states
+constexpr int kGroup = 2 * kWarps;             // chunks between two published states
 constexpr int kInfos = 4;
-constexpr uint32_t kPollLimit = 1u << 21;      // polls before giving up (seconds)
+constexpr uint32_t kPollLimit = 1u << 21;      // polls before giving up (about a second)
 
 // A lane's channels: 4 bytes of them.
 template <typename T> constexpr int kCh = 4 / (int)sizeof(T);
@@ -61,16 +62,61 @@ template <typename T> constexpr int kTileCh = 32 * kCh<T>;
 template <bool kVec> constexpr int kPitch = kVec ? 128 : 132;
 
 // sigmoid(g) and sigmoid(-g), each with its own digits: with e = exp(-|g|) they are
-// 1 / (1 + e) and e / (1 + e), in the order that g's sign gives. small: the second.
-__device__ __forceinline__ float small_sigmoid(float g) {
-  const float e = __expf(-fabsf(g));
-  return __fdividef(e, 1.0f + e);
+// 1 / (1 + e) and e / (1 + e), in the order that g's sign gives; the first is also one minus the
+// second, to the last digit.
+__device__ __forceinline__ float recip(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
 }
 __device__ __forceinline__ void sigmoids(float g, float& up, float& down) {
-  const float s = small_sigmoid(g), r = 1.0f - s;
+  const float e = __expf(-fabsf(g)), s = e * recip(1.0f + e), r = 1.0f - s;
   up = g >= 0.0f ? r : s;
   down = g >= 0.0f ? s : r;
 }
+
+// A lane's channels as one value: a float, or a pair that the packed fp32 instructions take whole (half
+// the issue slots, the same roundings).
+template <int C> struct Pack;
+template <> struct Pack<1> {
+  using V = float;
+  __device__ __forceinline__ static V make(const float (&v)[1]) { return v[0]; }
+  __device__ __forceinline__ static V all(float v) { return v; }
+  __device__ __forceinline__ static void split(V v, float (&o)[1]) { o[0] = v; }
+  __device__ __forceinline__ static V fma(V a, V b, V c) { return fmaf(a, b, c); }
+  __device__ __forceinline__ static V mul(V a, V b) { return a * b; }
+  __device__ __forceinline__ static V add(V a, V b) { return a + b; }
+};
+template <> struct Pack<2> {
+  using V = uint64_t;
+  __device__ __forceinline__ static V make(const float (&v)[2]) {
+    V r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v[0]), "f"(v[1]));
+    return r;
+  }
+  __device__ __forceinline__ static V all(float v) {
+    const float t[2] = {v, v};
+    return make(t);
+  }
+  __device__ __forceinline__ static void split(V v, float (&o)[2]) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(o[0]), "=f"(o[1]) : "l"(v));
+  }
+  __device__ __forceinline__ static V fma(V a, V b, V c) {
+    V r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+  }
+  __device__ __forceinline__ static V mul(V a, V b) {
+    V r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+  }
+  __device__ __forceinline__ static V add(V a, V b) {
+    V r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+  }
+};
 
 template <typename T>
 __device__ __forceinline__ void unpack_word(uint32_t w, float (&v)[kCh<T>]) {
@@ -80,6 +126,37 @@ __device__ __forceinline__ void unpack_word(uint32_t w, float (&v)[kCh<T>]) {
     v[0] = __uint_as_float(w << 16);
     v[1] = __uint_as_float(w & 0xffff0000u);
   }
+}
+
+// The smaller of sigmoid(g) and sigmoid(-g) of each channel.
+template <int C>
+__device__ __forceinline__ typename Pack<C>::V small_sigmoid(const float (&g)[C]) {
+  using P = Pack<C>;
+  float e[C], d[C], r[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) e[c] = __expf(-fabsf(g[c]));
+  const typename P::V e2 = P::make(e);
+  P::split(P::add(e2, P::all(1.0f)), d);
+#pragma unroll
+  for (int c = 0; c < C; ++c) r[c] = recip(d[c]);
+  return P::mul(e2, P::make(r));
+}
+// sigmoid(g) and sigmoid(-g) from the smaller one and g's sign.
+template <int C>
+__device__ __forceinline__ void pick(typename Pack<C>::V small, const float (&g)[C], typename Pack<C>::V& up,
+                                     typename Pack<C>::V& down) {
+  using P = Pack<C>;
+  float s[C], b[C], u[C], d[C];
+  P::split(small, s);
+  P::split(P::fma(small, P::all(-1.0f), P::all(1.0f)), b);
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const bool neg = __float_as_int(g[c]) < 0;
+    u[c] = neg ? s[c] : b[c];
+    d[c] = neg ? b[c] : s[c];
+  }
+  up = P::make(u);
+  down = P::make(d);
 }
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -150,57 +227,52 @@ __device__ __forceinline__ void store_row(T* p, const float (&v)[kCh<T>], int le
   }
 }
 
-// ---- workspace: a header, a flag per (chunk, channel group), a record of one (A, B) per channel beside it
+// ---- workspace: a header, then a record of one (A, B) per channel for each (chunk, channel group).
+// All of it is set to 0xff bytes first. A record's words are their own flags: every word that a tile
+// publishes is the result of an fp32 operation, which no NaN makes 0xffffffff, so a reader polls the
+// record until that pattern is gone from it, and needs no fence and no second round trip.
 struct Chain {
-  uint32_t* head;   // ticket, abort
-  uint32_t* flags;  // [chunks, groups]
-  float* records;   // [chunks, groups, tile channels, 2]
+  uint32_t* head;  // tickets taken, less one; abort when it is no longer 0xffffffff
+  float* records;  // [chunks, groups, tile channels, 2]
 };
 constexpr size_t kHead = 256;
-size_t chain_bytes(int64_t chunks, int32_t dim) {  // for the narrower groups of f32
-  const size_t g = (size_t)chunks * ((dim + 31) / 32);
-  return (kHead + g * 4 + 255) / 256 * 256 + (g * 32 * 8 + 255) / 256 * 256;
-}
-size_t flag_bytes(int64_t chunks, int groups) { return kHead + (size_t)chunks * groups * 4; }
-Chain chain_at(void* ws, int64_t chunks, int groups) {
-  char* p = static_cast<char*>(ws);
-  return {reinterpret_cast<uint32_t*>(p), reinterpret_cast<uint32_t*>(p + kHead),
-          reinterpret_cast<float*>(p + (kHead + (size_t)chunks * groups * 4 + 255) / 256 * 256)};
+constexpr uint32_t kUnset = 0xffffffffu;
+size_t chain_bytes(int64_t chunks, int groups, int width) { return kHead + (size_t)chunks * groups * width * 8; }
+Chain chain_at(void* ws) {
+  return {static_cast<uint32_t*>(ws), reinterpret_cast<float*>(static_cast<char*>(ws) + kHead)};
 }
 
-__device__ __forceinline__ uint32_t load_acquire(const uint32_t* p) {
-  uint32_t v;
-  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  return v;
+// A lane's share of a record: (A, B) of each of its channels.
+template <int C>
+__device__ __forceinline__ void load_record(const float* p, float (&v)[2 * C]) {
+  if constexpr (C == 2)
+    asm volatile("ld.relaxed.gpu.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "l"(p) : "memory");
+  else
+    asm volatile("ld.relaxed.gpu.global.v2.f32 {%0, %1}, [%2];" : "=f"(v[0]), "=f"(v[1]) : "l"(p) : "memory");
 }
-__device__ __forceinline__ void store_release(uint32_t* p, uint32_t v) {
-  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+template <int C>
+__device__ __forceinline__ void store_record(float* p, const float (&v)[2 * C]) {
+  if constexpr (C == 2)
+    asm volatile("st.relaxed.gpu.global.v4.f32 [%0], {%1, %2, %3, %4};"
+                 ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
+  else
+    asm volatile("st.relaxed.gpu.global.v2.f32 [%0], {%1, %2};" ::"l"(p), "f"(v[0]), "f"(v[1]) : "memory");
 }
-// A whole warp's record, then its flag.
+template <typename T>
+__device__ __forceinline__ float* record_at(const Chain& ch, int64_t at, int lane) {
+  return ch.records + (at * kTileCh<T> + lane * kCh<T>) * 2;
+}
 template <typename T>
 __device__ __forceinline__ void publish(const Chain& ch, int64_t at, const float (&A)[kCh<T>], const float (&B)[kCh<T>],
                                         int lane) {
-  float* r = ch.records + (at * kTileCh<T> + lane * kCh<T>) * 2;
-  if constexpr (kCh<T> == 2) __stcg(reinterpret_cast<float4*>(r), make_float4(A[0], B[0], A[1], B[1]));
-  else __stcg(reinterpret_cast<float2*>(r), make_float2(A[0], B[0]));
-  __threadfence();
-  __syncwarp();
-  if (lane == 0) store_release(ch.flags + at, 1u);
-}
-template <typename T>
-__device__ __forceinline__ void fetch(const Chain& ch, int64_t at, float (&A)[kCh<T>], float (&B)[kCh<T>], int lane) {
-  const float* r = ch.records + (at * kTileCh<T> + lane * kCh<T>) * 2;
-  if constexpr (kCh<T> == 2) {
-    const float4 v = __ldcg(reinterpret_cast<const float4*>(r));
-    A[0] = v.x;
-    B[0] = v.y;
-    A[1] = v.z;
-    B[1] = v.w;
-  } else {
-    const float2 v = __ldcg(reinterpret_cast<const float2*>(r));
-    A[0] = v.x;
-    B[0] = v.y;
+  float v[2 * kCh<T>];
+#pragma unroll
+  for (int c = 0; c < kCh<T>; ++c) {
+    v[2 * c] = A[c];
+    v[2 * c + 1] = B[c];
   }
+  store_record<kCh<T>>(record_at<T>(ch, at, lane), v);
 }
 
 // What a CTA knows of a tile. Chunks count from the end that the pass starts at.
@@ -233,72 +305,76 @@ __device__ __forceinline__ void tile_info(Info& f, const SeqTable& t, int item, 
   f.last = f.l == of - 1;
 }
 
-// Folds what precedes chunk l of this tile's run into the value that enters it (a whole warp; all lanes
-// get theirs). base: the index of a record that lies d chunks before this one.
+// What precedes chunk l of a run, as up to kGroup records: d = 1 .. k are the maps of the chunks d before it,
+// d = k + 1 the published state, with k = (l - 1) mod kGroup. Warp w takes d = 2 w + 1 and 2 w + 2.
 template <typename T, bool kReverse>
-__device__ __forceinline__ void look_back(const Chain& ch, const Info& f, int groups, float (&h)[kCh<T>], int lane) {
-  auto at = [&](int d) {  // record of the chunk d before this one in the pass's order
-    return (int64_t)(kReverse ? f.chunk + d : f.chunk - d) * groups + f.group;
-  };
-  const int k = (f.l - 1) % kGroup;  // maps between the last published state and this chunk
-  // lane i < k watches the i-th map after the state, lane k the state
-  bool ready = lane > k;
-  const uint32_t* flag = ch.flags + at(lane == k ? k + 1 : k - lane > 0 ? k - lane : 1);
-  float A[kCh<T>], B[kCh<T>];
-  for (uint32_t it = 0; !__all_sync(0xffffffffu, ready); ++it) {
-    if (!ready) ready = load_acquire(flag) != 0u;
-    if ((it & 63u) == 63u) {
-      __nanosleep(40);
-      uint32_t stop = 0;
-      if (lane == 0) {
-        stop = load_acquire(ch.head + 1);
-        if (!stop && it >= kPollLimit) {
-          store_release(ch.head + 1, 1u);
-          atomicAdd(&g_recurrence_timeouts, 1u);
-          stop = 1;
-        }
-      }
-      if (__shfl_sync(0xffffffffu, stop, 0)) break;
+struct LookBack {
+  static constexpr int C = kCh<T>;
+  const float* at[2];
+  float r[2][2 * C];
+  bool want[2], state[2];
+
+  // Starts both loads, to be looked at by finish().
+  __device__ __forceinline__ void start(const Chain& ch, const Info& f, int groups, int warp, int lane) {
+    const int k = f.l > 0 ? (f.l - 1) % kGroup : -1;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int d = 2 * warp + 1 + j;
+      want[j] = d <= k + 1;
+      state[j] = d == k + 1;
+      at[j] = record_at<T>(ch, (int64_t)(kReverse ? f.chunk + d : f.chunk - d) * groups + f.group, lane);
+      if (want[j]) load_record<C>(at[j], r[j]);
     }
   }
-  __syncwarp();
-  fetch<T>(ch, at(k + 1), A, B, lane);
+  // Waits for both and composes them, the older first, into (A, B); a state is the map (0, state).
+  __device__ __forceinline__ void finish(const Chain& ch, float (&A)[C], float (&B)[C], int lane) {
+#pragma unroll 1
+    for (uint32_t it = 0;; ++it) {
+      bool set = true;
 #pragma unroll
-  for (int c = 0; c < kCh<T>; ++c) h[c] = B[c];
-  for (int d = k; d > 0; d -= 5) {  // five records on the way at a time
-    float ra[5][kCh<T>], rb[5][kCh<T>];
+      for (int j = 0; j < 2; ++j)
+        if (want[j])
 #pragma unroll
-    for (int j = 0; j < 5; ++j)
-      if (d - j > 0) fetch<T>(ch, at(d - j), ra[j], rb[j], lane);
+          for (int c = 0; c < 2 * C; ++c) set = set && __float_as_uint(r[j][c]) != kUnset;
+      if (__all_sync(0xffffffffu, set)) break;
+      if ((it & 63u) == 63u) {
+        uint32_t stop = 0;
+        if (lane == 0) {
+          stop = *(volatile uint32_t*)(ch.head + 1) != kUnset;
+          if (!stop && it >= kPollLimit) {
+            atomicExch(ch.head + 1, 0u);
+            atomicAdd(&g_recurrence_timeouts, 1u);
+            stop = 1;
+          }
+        }
+        if (__shfl_sync(0xffffffffu, stop, 0)) break;
+      }
 #pragma unroll
-    for (int j = 0; j < 5; ++j)
-      if (d - j > 0)
+      for (int j = 0; j < 2; ++j)
+        if (want[j]) load_record<C>(at[j], r[j]);
+    }
 #pragma unroll
-        for (int c = 0; c < kCh<T>; ++c) h[c] = fmaf(ra[j][c], h[c], rb[j][c]);
+    for (int c = 0; c < C; ++c) {
+      A[c] = 1.0f;
+      B[c] = 0.0f;
+#pragma unroll
+      for (int j = 1; j >= 0; --j)
+        if (want[j]) {
+          B[c] = state[j] ? r[j][2 * c + 1] : fmaf(r[j][2 * c], B[c], r[j][2 * c + 1]);
+          A[c] = state[j] ? 0.0f : A[c] * r[j][2 * c];
+        }
+    }
   }
-}
+};
 
-__device__ __forceinline__ void bar_sync(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-__device__ __forceinline__ void bar_arrive(int id, int threads) {
-  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-constexpr int kBarMaps = 1, kBarEnter = 2;
-
-// Takes the next tile: by ticket where tiles wait for one another, else by turns. A CTA takes tickets
-// `stages` tiles ahead; where that would be more than an even share, it takes the share and no more, so that
-// a CTA that starts late still finds its own.
-template <bool kReverse, int stages>
-__device__ __forceinline__ void take(Info& f, const Chain& ch, const SeqTable& t, int turn, int items, int groups) {
-  int item = items;
-  if (!ch.head) {
-    item = (int)min((int64_t)blockIdx.x + (int64_t)turn * gridDim.x, (int64_t)items);
-  } else {
-    const int share = (items + (int)gridDim.x - 1) / (int)gridDim.x;
-    if (share > stages || turn < share) item = (int)min(atomicAdd(ch.head, 1u), (uint32_t)items);
-  }
-  tile_info<kReverse>(f, t, item, items, groups);
+// The next tile: by ticket where tiles wait for one another, else by turns. A CTA takes tickets `stages`
+// tiles ahead; where that would be more than an even share, it takes the share and no more, so that a CTA
+// that starts late still finds its own.
+template <int stages>
+__device__ __forceinline__ int take(const Chain& ch, int turn, int items) {
+  if (!ch.head) return (int)min((int64_t)blockIdx.x + (int64_t)turn * gridDim.x, (int64_t)items);
+  const int share = (items + (int)gridDim.x - 1) / (int)gridDim.x;
+  return share > stages || turn < share ? (int)min(atomicAdd(ch.head, 1u) + 1u, (uint32_t)items) : items;
 }
 
 // ------------------------------------------------------------------ forward
@@ -309,8 +385,8 @@ template <bool kVec> constexpr int kFwdStage = 2 * kChunkR * kPitch<kVec>;
 template <typename T>
 struct FwdShared {
   Info info[kInfos];
-  float A[kWarps][kTileCh<T>], B[kWarps][kTileCh<T>];
-  float enter[2][kTileCh<T>];
+  float A[kWarps][kTileCh<T>], B[kWarps][kTileCh<T>];      // the warps' maps
+  float pa[kWarps][kTileCh<T>], pb[kWarps][kTileCh<T>];    // what each found before the tile
 };
 
 template <typename T, bool kVec>
@@ -319,6 +395,9 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ Chain 
   extern __shared__ __align__(128) unsigned char stages[];
   __shared__ FwdShared<T> s;
   constexpr int C = kCh<T>;
+  using P = Pack<C>;
+  using V = typename P::V;
+  constexpr uint32_t kMat = kChunkR * kPitch<kVec>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   // runs of no token: a fresh one zeroes its slot
@@ -333,43 +412,26 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ Chain 
       const int nt = min(kTok, f.n - warp * kTok);
       const uint32_t st = smem_addr(stages) + (uint32_t)(i % kFwdStages) * kFwdStage<kVec>;
       load_rows<T, kVec>(st, static_cast<const T*>(a.x) + f.row * a.ld_x + ch0, a.ld_x, warp * kTok, nt, m, lane);
-      load_rows<T, kVec>(st + kChunkR * kPitch<kVec>, static_cast<const T*>(a.gate) + f.row * a.ld_gate + ch0,
-                         a.ld_gate, warp * kTok, nt, m, lane);
+      load_rows<T, kVec>(st + kMat, static_cast<const T*>(a.gate) + f.row * a.ld_gate + ch0, a.ld_gate, warp * kTok, nt,
+                         m, lane);
     }
     cp_commit();
   };
-  if (warp == kWarps && lane == 0)
-    for (int i = 0; i < kFwdStages; ++i) take<false, kFwdStages>(s.info[i], ch, a.tab, i, items, groups);
+  if (threadIdx.x == 0)
+    for (int i = 0; i < kFwdStages; ++i)
+      tile_info<false>(s.info[i], a.tab, take<kFwdStages>(ch, i, items), items, groups);
   __syncthreads();
-  if (warp < kWarps)
-    for (int i = 0; i < kFwdStages; ++i) load(i);
+  for (int i = 0; i < kFwdStages; ++i) load(i);
 
   for (int i = 0;; ++i) {
     const Info f = s.info[i % kInfos];
     if (f.item < 0) break;
     const int ch0 = f.group * kTileCh<T> + lane * C;
     const int left = a.dim - ch0;  // channels of this lane and those after it
-    if (warp == kWarps) {
-      // ---- the next ticket, then what enters this tile
-      if (lane == 0) take<false, kFwdStages>(s.info[(i + kFwdStages) % kInfos], ch, a.tab, i + kFwdStages, items, groups);
-      __syncwarp();
-      bar_arrive(kBarMaps, kThreads);
-      float h[C];
-      if (f.l == 0) {
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-          h[c] = c < left && !seq_fresh(a.tab, f.seq) ? a.state[(int64_t)seq_slot(a.tab, f.seq) * a.dim + ch0 + c] : 0.0f;
-      } else {
-        look_back<T, false>(ch, f, groups, h, lane);
-      }
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        s.enter[i & 1][lane * C + c] = h[c];
-        if (a.ckpt && c < left) a.ckpt[(int64_t)f.chunk * a.dim + ch0 + c] = h[c];
-      }
-      bar_sync(kBarEnter, kThreads);
-      continue;
-    }
+    int next = 0;
+    if (threadIdx.x == 0) next = take<kFwdStages>(ch, i + kFwdStages, items);
+    LookBack<T, false> back;
+    back.start(ch, f, groups, warp, lane);
     // ---- scan from zero
     const unsigned char* st = stages + (i % kFwdStages) * kFwdStage<kVec>;
     const T* tx = static_cast<const T*>(a.x) + f.row * a.ld_x + f.group * kTileCh<T>;
@@ -380,78 +442,98 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ Chain 
       lo[c] = a.lower && c < left ? a.lower[ch0 + c] : 0.0f;
       un[c] = 1.0f - lo[c];
     }
+    const V lo2 = P::make(lo), un2 = P::make(un);
     const int nt = min(kTok, f.n - warp * kTok);
     cp_wait<kFwdStages - 1>();
     __syncwarp();
-    float hs[kTok][C], ps[kTok][C], h[C], p[C];
+    V hs[kTok], ps[kTok], h2 = P::all(0.0f), p2 = P::all(1.0f);
+    auto scan = [&](auto whole) {  // rows past the run's end count as the identity
+#pragma unroll
+      for (int j = 0; j < kTok; ++j) {
+        if (decltype(whole)::value || j < nt) {
+          const int r = warp * kTok + j;
+          float x[C], g[C];
+          unpack_word<T>(staged<T, kVec>(st, r, lane, tx, a.ld_x), x);
+          unpack_word<T>(staged<T, kVec>(st + kMat, r, lane, tg, a.ld_gate), g);
+          V up, down;
+          pick<C>(small_sigmoid<C>(g), g, up, down);
+          const V f2 = P::fma(un2, up, lo2);
+          h2 = P::fma(f2, h2, P::mul(P::mul(un2, down), P::make(x)));
+          p2 = P::mul(p2, f2);
+        }
+        hs[j] = h2;
+        ps[j] = p2;
+      }
+    };
+    if (nt == kTok) scan(std::true_type{});
+    else scan(std::false_type{});
+    float A[C], B[C], ea[C], eb[C];
+    P::split(p2, A);
+    P::split(h2, B);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      h[c] = 0.0f;
-      p[c] = 1.0f;
+      s.A[warp][lane * C + c] = A[c];
+      s.B[warp][lane * C + c] = B[c];
     }
+    __syncthreads();
+    // the map before this warp (ea, eb), and the tile's (A, B: warp 0 publishes it)
 #pragma unroll
-    for (int j = 0; j < kTok; ++j) {
-      if (j < nt) {
-        const int r = warp * kTok + j;
-        float x[C], g[C];
-        unpack_word<T>(staged<T, kVec>(st, r, lane, tx, a.ld_x), x);
-        unpack_word<T>(staged<T, kVec>(st + kChunkR * kPitch<kVec>, r, lane, tg, a.ld_gate), g);
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          float up, down;
-          sigmoids(g[c], up, down);
-          const float ft = fmaf(un[c], up, lo[c]);
-          h[c] = fmaf(ft, h[c], un[c] * down * x[c]);
-          p[c] *= ft;
-        }
-      }
+    for (int c = 0; c < C; ++c) {
+      ea[c] = 1.0f;
+      eb[c] = 0.0f;
+    }
+    for (int w = 0; w < warp; ++w)
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        hs[j][c] = h[c];
-        ps[j][c] = p[c];
+        const float wa = s.A[w][lane * C + c];
+        eb[c] = fmaf(wa, eb[c], s.B[w][lane * C + c]);
+        ea[c] *= wa;
       }
-    }
+    const int64_t at = (int64_t)f.chunk * groups + f.group;
+    if (warp == 0) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      s.A[warp][lane * C + c] = p[c];
-      s.B[warp][lane * C + c] = h[c];
-    }
-    bar_sync(kBarMaps, kThreads);
-    __syncwarp();  // every lane has read this stage
-    load(i + kFwdStages);
-    // the map before this warp (ex), and the tile's (warp 0 publishes it)
-    float ea[C], eb[C], A[C], B[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      ea[c] = A[c] = 1.0f;
-      eb[c] = B[c] = 0.0f;
-    }
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w == warp)
+      for (int w = 1; w < kWarps; ++w)
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-          ea[c] = A[c];
-          eb[c] = B[c];
-        }
-      if (w < warp || warp == 0)
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          const float wa = s.A[w][lane * C + c], wb = s.B[w][lane * C + c];
-          B[c] = fmaf(wa, B[c], wb);
+          const float wa = s.A[w][lane * C + c];
+          B[c] = fmaf(wa, B[c], s.B[w][lane * C + c]);
           A[c] *= wa;
         }
+      if (!f.last && f.l % kGroup != 0) publish<T>(ch, at, A, B, lane);
     }
-    const int64_t at = (int64_t)f.chunk * groups + f.group;
-    if (warp == 0 && !f.last && f.l % kGroup != 0) publish<T>(ch, at, A, B, lane);
-    bar_sync(kBarEnter, kThreads);
+    {
+      float pa[C], pb[C];
+      back.finish(ch, pa, pb, lane);
+      if (f.l == 0 && warp == 0)
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          pa[c] = 0.0f;
+          pb[c] = c < left && !seq_fresh(a.tab, f.seq) ? a.state[(int64_t)seq_slot(a.tab, f.seq) * a.dim + ch0 + c] : 0.0f;
+        }
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        s.pa[warp][lane * C + c] = pa[c];
+        s.pb[warp][lane * C + c] = pb[c];
+      }
+    }
+    if (threadIdx.x == 0) tile_info<false>(s.info[(i + kFwdStages) % kInfos], a.tab, next, items, groups);
+    __syncthreads();
+    load(i + kFwdStages);  // (every lane has read this stage)
+    // what enters the tile, the oldest first
     float in[C];
 #pragma unroll
-    for (int c = 0; c < C; ++c) in[c] = s.enter[i & 1][lane * C + c];
+    for (int c = 0; c < C; ++c) in[c] = 0.0f;
+#pragma unroll
+    for (int w = kWarps - 1; w >= 0; --w)
+#pragma unroll
+      for (int c = 0; c < C; ++c) in[c] = fmaf(s.pa[w][lane * C + c], in[c], s.pb[w][lane * C + c]);
     if (warp == 0) {
       float end[C];
 #pragma unroll
-      for (int c = 0; c < C; ++c) end[c] = fmaf(A[c], in[c], B[c]);
+      for (int c = 0; c < C; ++c) {
+        end[c] = fmaf(A[c], in[c], B[c]);
+        if (a.ckpt && c < left) a.ckpt[(int64_t)f.chunk * a.dim + ch0 + c] = in[c];
+      }
       if (f.last) {
 #pragma unroll
         for (int c = 0; c < C; ++c)
@@ -460,17 +542,19 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ Chain 
         publish<T>(ch, at, end, end, lane);
       }
     }
-    T* ty = static_cast<T*>(a.y) + f.row * a.ld_y + ch0;
+    T* ty = static_cast<T*>(a.y) + (f.row + warp * kTok) * a.ld_y + ch0;
+    const V in2 = P::fma(P::make(ea), P::make(in), P::make(eb));
+    auto emit = [&](auto whole) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) in[c] = fmaf(ea[c], in[c], eb[c]);
-#pragma unroll
-    for (int j = 0; j < kTok; ++j)
-      if (j < nt) {
-        float y[C];
-#pragma unroll
-        for (int c = 0; c < C; ++c) y[c] = fmaf(ps[j][c], in[c], hs[j][c]);
-        store_row<T, kVec>(ty + (int64_t)(warp * kTok + j) * a.ld_y, y, left);
-      }
+      for (int j = 0; j < kTok; ++j)
+        if (decltype(whole)::value || j < nt) {
+          float y[C];
+          P::split(P::fma(ps[j], in2, hs[j]), y);
+          store_row<T, kVec>(ty + j * a.ld_y, y, left);
+        }
+    };
+    if (nt == kTok) emit(std::true_type{});
+    else emit(std::false_type{});
   }
   cp_wait<0>();
 }
@@ -484,8 +568,8 @@ template <typename T>
 struct BwdShared {
   Info info[kInfos];
   float A[kWarps][kTileCh<T>], F[kWarps][kTileCh<T>], R[kWarps][kTileCh<T>];
-  float enter[2][kTileCh<T>];
-  float dlo[2][kWarps][kTileCh<T>];
+  float pa[kWarps][kTileCh<T>], pb[kWarps][kTileCh<T>];
+  float dlo[kWarps][kTileCh<T>];
 };
 
 template <typename T, bool kVec>
@@ -495,6 +579,8 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ Cha
   extern __shared__ __align__(128) unsigned char stages[];
   __shared__ BwdShared<T> s;
   constexpr int C = kCh<T>;
+  using P = Pack<C>;
+  using V = typename P::V;
   constexpr uint32_t kMat = kChunkR * kPitch<kVec>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -526,15 +612,15 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ Cha
     for (int c = 0; c < C; ++c) {
       float v = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) v += s.dlo[i & 1][w][lane * C + c];
+      for (int w = 0; w < kWarps; ++w) v += s.dlo[w][lane * C + c];
       if (ch0 + c < a.dim) part[(int64_t)f.chunk * a.dim + ch0 + c] = v;
     }
   };
-  if (warp == kWarps && lane == 0)
-    for (int i = 0; i < kBwdStages; ++i) take<true, kBwdStages>(s.info[i], ch, a.tab, i, items, groups);
+  if (threadIdx.x == 0)
+    for (int i = 0; i < kBwdStages; ++i)
+      tile_info<true>(s.info[i], a.tab, take<kBwdStages>(ch, i, items), items, groups);
   __syncthreads();
-  if (warp < kWarps)
-    for (int i = 0; i < kBwdStages; ++i) load(i);
+  for (int i = 0; i < kBwdStages; ++i) load(i);
 
   int i = 0;
   for (;; ++i) {
@@ -542,24 +628,10 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ Cha
     if (f.item < 0) break;
     const int ch0 = f.group * kTileCh<T> + lane * C;
     const int left = a.dim - ch0;
-    if (warp == kWarps) {
-      // info[i + 2] takes the place of the tile before the last, whose part is summed by now
-      if (lane == 0) take<true, kBwdStages>(s.info[(i + kBwdStages) % kInfos], ch, a.tab, i + kBwdStages, items, groups);
-      __syncwarp();
-      bar_arrive(kBarMaps, kThreads);
-      float h[C];
-      if (f.l == 0) {
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-          h[c] = c < left && a.dstate_end ? a.dstate_end[(int64_t)f.seq * a.dim + ch0 + c] : 0.0f;
-      } else {
-        look_back<T, true>(ch, f, groups, h, lane);
-      }
-#pragma unroll
-      for (int c = 0; c < C; ++c) s.enter[i & 1][lane * C + c] = h[c];
-      bar_sync(kBarEnter, kThreads);
-      continue;
-    }
+    int next = 0;
+    if (threadIdx.x == 0) next = take<kBwdStages>(ch, i + kBwdStages, items);
+    LookBack<T, true> back;
+    back.start(ch, f, groups, warp, lane);
     const unsigned char* st = stages + (i % kBwdStages) * kBwdStage<kVec>;
     const T* tx = static_cast<const T*>(a.x) + f.row * a.ld_x + f.group * kTileCh<T>;
     const T* tg = static_cast<const T*>(a.gate) + f.row * a.ld_gate + f.group * kTileCh<T>;
@@ -571,99 +643,123 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ Cha
       un[c] = 1.0f - lo[c];
       hp[c] = c < left ? a.ckpt[(int64_t)f.chunk * a.dim + ch0 + c] : 0.0f;
     }
+    const V lo2 = P::make(lo), un2 = P::make(un);
     const int nt = min(kTok, f.n - warp * kTok);
     cp_wait<kBwdStages - 1>();
     __syncwarp();
     // ---- both scans from zero: h's map (A, F) and R's map (A, R)
-    float sg[kTok][C];  // the smaller sigmoid, signed as the gate
-    float A[C], F[C], R[C];
+    V sg[kTok];  // the smaller sigmoid, signed as the gate
+    V A2 = P::all(1.0f), F2 = P::all(0.0f), R2 = P::all(0.0f);
+    auto gates = [&](V v, V& up, V& down, V& ft) {
+      float g[C], m[C];
+      P::split(v, g);
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      A[c] = 1.0f;
-      F[c] = R[c] = 0.0f;
-    }
-    auto gates = [&](float v, int c, float& up, float& down, float& ft) {
-      const float sm = fabsf(v), big = 1.0f - sm;
-      const bool neg = __float_as_int(v) < 0;
-      up = neg ? sm : big;
-      down = neg ? big : sm;
-      ft = fmaf(un[c], up, lo[c]);
+      for (int c = 0; c < C; ++c) m[c] = fabsf(g[c]);
+      pick<C>(P::make(m), g, up, down);
+      ft = P::fma(un2, up, lo2);
     };
+    auto scan = [&](auto whole) {
 #pragma unroll
-    for (int j = 0; j < kTok; ++j)
-      if (j < nt) {
-        const int r = warp * kTok + j;
-        float x[C], g[C], d[C];
-        unpack_word<T>(staged<T, kVec>(st, r, lane, tx, a.ld_x), x);
-        unpack_word<T>(staged<T, kVec>(st + kMat, r, lane, tg, a.ld_gate), g);
-        unpack_word<T>(staged<T, kVec>(st + 2 * kMat, r, lane, td, a.ld_dy), d);
+      for (int j = 0; j < kTok; ++j)
+        if (decltype(whole)::value || j < nt) {
+          const int r = warp * kTok + j;
+          float x[C], g[C], d[C], m[C];
+          unpack_word<T>(staged<T, kVec>(st, r, lane, tx, a.ld_x), x);
+          unpack_word<T>(staged<T, kVec>(st + kMat, r, lane, tg, a.ld_gate), g);
+          unpack_word<T>(staged<T, kVec>(st + 2 * kMat, r, lane, td, a.ld_dy), d);
+          const V small = small_sigmoid<C>(g);
+          V up, down;
+          pick<C>(small, g, up, down);
+          P::split(small, m);
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-          sg[j][c] = copysignf(small_sigmoid(g[c]), g[c]);
-          float up, down, ft;
-          gates(sg[j][c], c, up, down, ft);
-          F[c] = fmaf(ft, F[c], un[c] * down * x[c]);
-          A[c] *= ft;
-          R[c] = fmaf(A[c], d[c], R[c]);
+          for (int c = 0; c < C; ++c) m[c] = copysignf(m[c], g[c]);
+          sg[j] = P::make(m);
+          const V ft = P::fma(un2, up, lo2);
+          F2 = P::fma(ft, F2, P::mul(P::mul(un2, down), P::make(x)));
+          A2 = P::mul(A2, ft);
+          R2 = P::fma(A2, P::make(d), R2);
         }
-      }
+    };
+    if (nt == kTok) scan(std::true_type{});
+    else scan(std::false_type{});
+    float A[C], F[C], R[C], ea[C], eb[C];
+    P::split(A2, A);
+    P::split(F2, F);
+    P::split(R2, R);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       s.A[warp][lane * C + c] = A[c];
       s.F[warp][lane * C + c] = F[c];
       s.R[warp][lane * C + c] = R[c];
     }
-    bar_sync(kBarMaps, kThreads);
+    __syncthreads();
     if (warp == 1 && i > 0 && part) sum_part(i - 1);
-    // the state that enters this warp; the map of R after it; the tile's map of R
-    float ea[C], eb[C];
+    // the state that enters this warp; the map of R after it; the tile's map of R (warp 0)
+    for (int w = 0; w < warp; ++w)
+#pragma unroll
+      for (int c = 0; c < C; ++c) hp[c] = fmaf(s.A[w][lane * C + c], hp[c], s.F[w][lane * C + c]);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      ea[c] = A[c] = 1.0f;
-      eb[c] = R[c] = 0.0f;
+      ea[c] = 1.0f;
+      eb[c] = 0.0f;
     }
+    for (int w = kWarps - 1; w > warp; --w)
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-      if (w < warp)
-#pragma unroll
-        for (int c = 0; c < C; ++c) hp[c] = fmaf(s.A[w][lane * C + c], hp[c], s.F[w][lane * C + c]);
-#pragma unroll
-    for (int w = kWarps - 1; w >= 0; --w) {
-      if (w == warp)
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          ea[c] = A[c];
-          eb[c] = R[c];
-        }
-      if (w > warp || warp == 0)
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          const float wa = s.A[w][lane * C + c];
-          R[c] = fmaf(wa, R[c], s.R[w][lane * C + c]);
-          A[c] *= wa;
-        }
-    }
-    const int64_t at = (int64_t)f.chunk * groups + f.group;
-    if (warp == 0 && !f.last && f.l % kGroup != 0) publish<T>(ch, at, A, R, lane);
-    // ---- the state before each token
-    float hs[kTok][C];
-#pragma unroll
-    for (int j = 0; j < kTok; ++j)
-      if (j < nt) {
-        float x[C];
-        unpack_word<T>(staged<T, kVec>(st, warp * kTok + j, lane, tx, a.ld_x), x);
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          float up, down, ft;
-          gates(sg[j][c], c, up, down, ft);
-          hs[j][c] = hp[c];
-          hp[c] = fmaf(ft, hp[c], un[c] * down * x[c]);
-        }
+      for (int c = 0; c < C; ++c) {
+        const float wa = s.A[w][lane * C + c];
+        eb[c] = fmaf(wa, eb[c], s.R[w][lane * C + c]);
+        ea[c] *= wa;
       }
-    bar_sync(kBarEnter, kThreads);
+    const int64_t at = (int64_t)f.chunk * groups + f.group;
+    if (warp == 0) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) {  // its own tokens are the last of the pass
+        R[c] = fmaf(A[c], eb[c], R[c]);
+        A[c] *= ea[c];
+      }
+      if (!f.last && f.l % kGroup != 0) publish<T>(ch, at, A, R, lane);
+    }
+    // ---- the state before each token
+    V hs[kTok], hp2 = P::make(hp);
+    auto states = [&](auto whole) {
+#pragma unroll
+      for (int j = 0; j < kTok; ++j)
+        if (decltype(whole)::value || j < nt) {
+          float x[C];
+          unpack_word<T>(staged<T, kVec>(st, warp * kTok + j, lane, tx, a.ld_x), x);
+          V up, down, ft;
+          gates(sg[j], up, down, ft);
+          hs[j] = hp2;
+          hp2 = P::fma(ft, hp2, P::mul(P::mul(un2, down), P::make(x)));
+        }
+    };
+    if (nt == kTok) states(std::true_type{});
+    else states(std::false_type{});
+    {
+      float pa[C], pb[C];
+      back.finish(ch, pa, pb, lane);
+      if (f.l == 0 && warp == 0)
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          pa[c] = 0.0f;
+          pb[c] = c < left && a.dstate_end ? a.dstate_end[(int64_t)f.seq * a.dim + ch0 + c] : 0.0f;
+        }
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        s.pa[warp][lane * C + c] = pa[c];
+        s.pb[warp][lane * C + c] = pb[c];
+      }
+    }
+    // info[i + 2] takes the place of tile i - 2, whose part of dlower has been summed
+    if (threadIdx.x == 0) tile_info<true>(s.info[(i + kBwdStages) % kInfos], a.tab, next, items, groups);
+    __syncthreads();
     float in[C];
 #pragma unroll
-    for (int c = 0; c < C; ++c) in[c] = s.enter[i & 1][lane * C + c];
+    for (int c = 0; c < C; ++c) in[c] = 0.0f;
+#pragma unroll
+    for (int w = kWarps - 1; w >= 0; --w)
+#pragma unroll
+      for (int c = 0; c < C; ++c) in[c] = fmaf(s.pa[w][lane * C + c], in[c], s.pb[w][lane * C + c]);
     if (warp == 0) {
       float end[C];
 #pragma unroll
@@ -677,37 +773,36 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ Cha
       }
     }
     // ---- backwards over the tokens
-    T* ox = static_cast<T*>(a.dx) + f.row * a.ld_dx + ch0;
-    T* og = static_cast<T*>(a.dgate) + f.row * a.ld_dgate + ch0;
-    float dlo[C];
+    T* ox = static_cast<T*>(a.dx) + (f.row + warp * kTok) * a.ld_dx + ch0;
+    T* og = static_cast<T*>(a.dgate) + (f.row + warp * kTok) * a.ld_dgate + ch0;
+    V in2 = P::fma(P::make(ea), P::make(in), P::make(eb)), dlo2 = P::all(0.0f);
+    auto emit = [&](auto whole) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      in[c] = fmaf(ea[c], in[c], eb[c]);
-      dlo[c] = 0.0f;
-    }
-#pragma unroll
-    for (int j = kTok - 1; j >= 0; --j)
-      if (j < nt) {
-        const int r = warp * kTok + j;
-        float x[C], d[C], vx[C], vg[C];
-        unpack_word<T>(staged<T, kVec>(st, r, lane, tx, a.ld_x), x);
-        unpack_word<T>(staged<T, kVec>(st + 2 * kMat, r, lane, td, a.ld_dy), d);
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          float up, down, ft;
-          gates(sg[j][c], c, up, down, ft);
-          const float G = in[c] + d[c], k = un[c] * down;
-          const float dd = G * (hs[j][c] - x[c]) * down;  // df sigmoid(-g)
-          vx[c] = k * G;
-          vg[c] = dd * un[c] * up;
-          dlo[c] += dd;
-          in[c] = ft * G;
+      for (int j = kTok - 1; j >= 0; --j)
+        if (decltype(whole)::value || j < nt) {
+          const int r = warp * kTok + j;
+          float x[C], d[C], vx[C], vg[C];
+          unpack_word<T>(staged<T, kVec>(st, r, lane, tx, a.ld_x), x);
+          unpack_word<T>(staged<T, kVec>(st + 2 * kMat, r, lane, td, a.ld_dy), d);
+          V up, down, ft;
+          gates(sg[j], up, down, ft);
+          const V G = P::add(in2, P::make(d));
+          // df sigmoid(-g), with df = G (h - x)
+          const V dd = P::mul(P::mul(G, P::fma(P::make(x), P::all(-1.0f), hs[j])), down);
+          P::split(P::mul(P::mul(un2, down), G), vx);
+          P::split(P::mul(P::mul(dd, un2), up), vg);
+          dlo2 = P::add(dlo2, dd);
+          in2 = P::mul(ft, G);
+          store_row<T, kVec>(ox + j * a.ld_dx, vx, left);
+          store_row<T, kVec>(og + j * a.ld_dgate, vg, left);
         }
-        store_row<T, kVec>(ox + (int64_t)r * a.ld_dx, vx, left);
-        store_row<T, kVec>(og + (int64_t)r * a.ld_dgate, vg, left);
-      }
+    };
+    if (nt == kTok) emit(std::true_type{});
+    else emit(std::false_type{});
+    float dlo[C];
+    P::split(dlo2, dlo);
 #pragma unroll
-    for (int c = 0; c < C; ++c) s.dlo[i & 1][warp][lane * C + c] = dlo[c];
+    for (int c = 0; c < C; ++c) s.dlo[warp][lane * C + c] = dlo[c];
     __syncwarp();  // every lane is done with this stage
     load(i + kBwdStages);
   }
@@ -812,8 +907,8 @@ Tiles plan(const SeqTable& t, mamba2_dtype act, int32_t dim, void* ws, cudaStrea
   bool chained = false;
   for (int i = 0; i < t.n; ++i) chained |= t.tile[i + 1] - t.tile[i] > 1;
   if (chained) {
-    p.chain = chain_at(ws, chunks, p.groups);
-    p.status = cudaMemsetAsync(ws, 0, flag_bytes(chunks, p.groups), st);
+    p.chain = chain_at(ws);
+    p.status = cudaMemsetAsync(ws, 0xff, chain_bytes(chunks, p.groups, width), st);
   }
   return p;
 }
@@ -822,7 +917,8 @@ Tiles plan(const SeqTable& t, mamba2_dtype act, int32_t dim, void* ws, cudaStrea
 
 size_t recurrence_workspace(int64_t chunks, bool chained, int32_t dim, bool backward) {
   const size_t part = backward ? ((size_t)chunks * dim * 4 + 255) / 256 * 256 : 0;
-  return part + (chained ? chain_bytes(chunks, dim) : 0);
+  // (the groups of either type together are at most 63 channels wider than dim)
+  return part + (chained ? (chain_bytes(chunks, 1, dim + 63) + 255) / 256 * 256 : 0);
 }
 
 unsigned int read_recurrence_timeouts() {
