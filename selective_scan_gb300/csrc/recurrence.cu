@@ -69,8 +69,16 @@ __device__ __forceinline__ float recip(float v) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
+// 2^v. (The instruction's flushing form: what it flushes is below 2^-126; the other form scales around that
+// at four more instructions.)
+__device__ __forceinline__ float exp2_ftz(float v) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v));
+  return e;
+}
+__device__ __forceinline__ float exp_neg_abs(float g) { return exp2_ftz(fabsf(g) * -1.4426950408889634f); }
 __device__ __forceinline__ void sigmoids(float g, float& up, float& down) {
-  const float e = __expf(-fabsf(g)), s = e * recip(1.0f + e), r = 1.0f - s;
+  const float e = exp_neg_abs(g), s = e * recip(1.0f + e), r = 1.0f - s;
   up = g >= 0.0f ? r : s;
   down = g >= 0.0f ? s : r;
 }
@@ -128,13 +136,35 @@ __device__ __forceinline__ void unpack_word(uint32_t w, float (&v)[kCh<T>]) {
   }
 }
 
+// sigmoid(g) and sigmoid(-g) of each channel, each from an exponential of its own: two more of the special
+// function unit's instructions (which has slots to spare here) than from one, but no sign to select by.
+template <int C>
+__device__ __forceinline__ void both_sigmoids(const float (&g)[C], typename Pack<C>::V& up, typename Pack<C>::V& down) {
+  using P = Pack<C>;
+  float t[C], a[C], b[C];
+  P::split(P::mul(P::make(g), P::all(1.4426950408889634f)), t);
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    a[c] = exp2_ftz(-t[c]);
+    b[c] = exp2_ftz(t[c]);
+  }
+  P::split(P::add(P::make(a), P::all(1.0f)), a);
+  P::split(P::add(P::make(b), P::all(1.0f)), b);
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    a[c] = recip(a[c]);
+    b[c] = recip(b[c]);
+  }
+  up = P::make(a);
+  down = P::make(b);
+}
 // The smaller of sigmoid(g) and sigmoid(-g) of each channel.
 template <int C>
 __device__ __forceinline__ typename Pack<C>::V small_sigmoid(const float (&g)[C]) {
   using P = Pack<C>;
   float e[C], d[C], r[C];
 #pragma unroll
-  for (int c = 0; c < C; ++c) e[c] = __expf(-fabsf(g[c]));
+  for (int c = 0; c < C; ++c) e[c] = exp_neg_abs(g[c]);
   const typename P::V e2 = P::make(e);
   P::split(P::add(e2, P::all(1.0f)), d);
 #pragma unroll
@@ -181,13 +211,14 @@ __device__ __forceinline__ int odd_start(const T* row) {
 template <typename T, bool kVec>
 __device__ __forceinline__ void load_rows(uint32_t dst, const T* tile, int64_t ld, int r0, int nt, int m, int lane) {
   if constexpr (kVec) {
+    const int r = lane >> 3, c = lane & 7;
+    const int bytes = min(16, m * (int)sizeof(T) - 16 * c);
+    if (bytes <= 0) return;
+    const T* src = tile + (r0 + r) * ld + c * (16 / (int)sizeof(T));
+    dst += (uint32_t)((r0 + r) * 128 + 16 * c);
 #pragma unroll
-    for (int i = 0; i < kTok / 4; ++i) {
-      const int r = 4 * i + (lane >> 3), c = lane & 7;
-      const int bytes = min(16, m * (int)sizeof(T) - 16 * c);
-      if (r < nt && bytes > 0)
-        cp_async(dst + (uint32_t)((r0 + r) * 128 + 16 * c), tile + (int64_t)(r0 + r) * ld + c * (16 / (int)sizeof(T)), bytes);
-    }
+    for (int i = 0; i < kTok / 4; ++i, src += 4 * ld)
+      if (4 * i + r < nt) cp_async(dst + 512 * i, src, bytes);
   } else {
     for (int r = 0; r < nt; ++r) {
       const T* row = tile + (int64_t)(r0 + r) * ld;
@@ -379,7 +410,7 @@ __device__ __forceinline__ int take(const Chain& ch, int turn, int items) {
 
 // ------------------------------------------------------------------ forward
 
-constexpr int kFwdStages = 3;
+constexpr int kFwdStages = 2;
 template <bool kVec> constexpr int kFwdStage = 2 * kChunkR * kPitch<kVec>;
 
 template <typename T>
@@ -389,8 +420,13 @@ struct FwdShared {
   float pa[kWarps][kTileCh<T>], pb[kWarps][kTileCh<T>];    // what each found before the tile
 };
 
+// The products of the f's go into shared memory, over the inputs that the lane has consumed (the same 8 bytes
+// a pair of channels), so that three CTAs fit an SM's registers; where a lane's inputs lie across two words
+// they stay in registers, with two CTAs.
+template <typename T, bool kVec> constexpr int kFwdCtas = kVec ? 3 : 2;
+
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, kFwdCtas<T, kVec>)
 rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ Chain ch, const int items, const int groups) {
   extern __shared__ __align__(128) unsigned char stages[];
   __shared__ FwdShared<T> s;
@@ -433,7 +469,7 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ Chain 
     LookBack<T, false> back;
     back.start(ch, f, groups, warp, lane);
     // ---- scan from zero
-    const unsigned char* st = stages + (i % kFwdStages) * kFwdStage<kVec>;
+    unsigned char* st = stages + (i % kFwdStages) * kFwdStage<kVec>;
     const T* tx = static_cast<const T*>(a.x) + f.row * a.ld_x + f.group * kTileCh<T>;
     const T* tg = static_cast<const T*>(a.gate) + f.row * a.ld_gate + f.group * kTileCh<T>;
     float lo[C], un[C];
@@ -444,9 +480,13 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ Chain 
     }
     const V lo2 = P::make(lo), un2 = P::make(un);
     const int nt = min(kTok, f.n - warp * kTok);
+    // the lane's word of row r of x (and, kMat further, of gate)
+    auto word = [&](int j) {
+      return reinterpret_cast<float*>(st + (warp * kTok + j) * kPitch<kVec>) + lane;
+    };
     cp_wait<kFwdStages - 1>();
     __syncwarp();
-    V hs[kTok], ps[kTok], h2 = P::all(0.0f), p2 = P::all(1.0f);
+    V hs[kTok], ps[kVec ? 1 : kTok], h2 = P::all(0.0f), p2 = P::all(1.0f);
     auto scan = [&](auto whole) {  // rows past the run's end count as the identity
 #pragma unroll
       for (int j = 0; j < kTok; ++j) {
@@ -456,13 +496,20 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ Chain 
           unpack_word<T>(staged<T, kVec>(st, r, lane, tx, a.ld_x), x);
           unpack_word<T>(staged<T, kVec>(st + kMat, r, lane, tg, a.ld_gate), g);
           V up, down;
-          pick<C>(small_sigmoid<C>(g), g, up, down);
+          both_sigmoids<C>(g, up, down);
           const V f2 = P::fma(un2, up, lo2);
           h2 = P::fma(f2, h2, P::mul(P::mul(un2, down), P::make(x)));
           p2 = P::mul(p2, f2);
         }
         hs[j] = h2;
-        ps[j] = p2;
+        if constexpr (kVec) {
+          float v[C];
+          P::split(p2, v);
+#pragma unroll
+          for (int c = 0; c < C; ++c) word(j)[c * (kMat / 4)] = v[c];
+        } else {
+          ps[j] = p2;
+        }
       }
     };
     if (nt == kTok) scan(std::true_type{});
@@ -476,7 +523,7 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ Chain 
       s.B[warp][lane * C + c] = B[c];
     }
     __syncthreads();
-    // the map before this warp (ea, eb), and the tile's (A, B: warp 0 publishes it)
+    // the map before this warp (ea, eb); the last warp's and its own make the tile's
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       ea[c] = 1.0f;
@@ -490,15 +537,12 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ Chain 
         ea[c] *= wa;
       }
     const int64_t at = (int64_t)f.chunk * groups + f.group;
-    if (warp == 0) {
+    if (warp == kWarps - 1) {
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w)
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          const float wa = s.A[w][lane * C + c];
-          B[c] = fmaf(wa, B[c], s.B[w][lane * C + c]);
-          A[c] *= wa;
-        }
+      for (int c = 0; c < C; ++c) {
+        B[c] = fmaf(A[c], eb[c], B[c]);
+        A[c] *= ea[c];
+      }
       if (!f.last && f.l % kGroup != 0) publish<T>(ch, at, A, B, lane);
     }
     {
@@ -518,7 +562,6 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ Chain 
     }
     if (threadIdx.x == 0) tile_info<false>(s.info[(i + kFwdStages) % kInfos], a.tab, next, items, groups);
     __syncthreads();
-    load(i + kFwdStages);  // (every lane has read this stage)
     // what enters the tile, the oldest first
     float in[C];
 #pragma unroll
@@ -527,7 +570,7 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ Chain 
     for (int w = kWarps - 1; w >= 0; --w)
 #pragma unroll
       for (int c = 0; c < C; ++c) in[c] = fmaf(s.pa[w][lane * C + c], in[c], s.pb[w][lane * C + c]);
-    if (warp == 0) {
+    if (warp == kWarps - 1) {
       float end[C];
 #pragma unroll
       for (int c = 0; c < C; ++c) {
@@ -548,13 +591,21 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ Chain 
 #pragma unroll
       for (int j = 0; j < kTok; ++j)
         if (decltype(whole)::value || j < nt) {
-          float y[C];
-          P::split(P::fma(ps[j], in2, hs[j]), y);
+          float y[C], v[C];
+          if constexpr (kVec) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) v[c] = word(j)[c * (kMat / 4)];
+            P::split(P::fma(P::make(v), in2, hs[j]), y);
+          } else {
+            P::split(P::fma(ps[j], in2, hs[j]), y);
+          }
           store_row<T, kVec>(ty + j * a.ld_y, y, left);
         }
     };
     if (nt == kTok) emit(std::true_type{});
     else emit(std::false_type{});
+    __syncwarp();  // every lane is done with this stage
+    load(i + kFwdStages);
   }
   cp_wait<0>();
 }
@@ -868,15 +919,17 @@ bool rows16(const void* p, int64_t ld, size_t e) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (size_t)ld * e % 16 == 0;
 }
 
-// CTAs of a launch: two to an SM, no more than tiles; empty runs need one.
-int ctas(int64_t items) { return (int)std::max<int64_t>(1, std::min<int64_t>(items, 2 * (int64_t)sm_count())); }
+// CTAs of a launch: so many to an SM, no more than tiles; empty runs need one.
+int ctas(int64_t items, int per_sm) {
+  return (int)std::max<int64_t>(1, std::min<int64_t>(items, per_sm * (int64_t)sm_count()));
+}
 
 template <typename T, bool kVec>
 cudaError_t run_fwd(const RecArgs& a, const Chain& ch, int items, int groups, cudaStream_t st) {
   constexpr int smem = kFwdStages * kFwdStage<kVec>;
   const cudaError_t e = cudaFuncSetAttribute(rec_fwd_kernel<T, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  rec_fwd_kernel<T, kVec><<<ctas(items), kThreads, smem, st>>>(a, ch, items, groups);
+  rec_fwd_kernel<T, kVec><<<ctas(items, kFwdCtas<T, kVec>), kThreads, smem, st>>>(a, ch, items, groups);
   return cudaGetLastError();
 }
 template <typename T, bool kVec>
@@ -884,7 +937,7 @@ cudaError_t run_bwd(const RecBwdArgs& a, const Chain& ch, float* part, int items
   constexpr int smem = kBwdStages * kBwdStage<kVec>;
   const cudaError_t e = cudaFuncSetAttribute(rec_bwd_kernel<T, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  rec_bwd_kernel<T, kVec><<<ctas(items), kThreads, smem, st>>>(a, ch, part, items, groups);
+  rec_bwd_kernel<T, kVec><<<ctas(items, 2), kThreads, smem, st>>>(a, ch, part, items, groups);
   return cudaGetLastError();
 }
 
