@@ -66,7 +66,7 @@ size_t mamba2_gated_recurrence_workspace_bytes(const int32_t* cu_seqlens, int32_
   if (dim <= 0 || !cu_ok(cu_seqlens, num_seqs)) return 0;
   bool chained;
   const int64_t chunks = count_chunks(cu_seqlens, num_seqs, &chained);
-  return recurrence_workspace(chunks, chained, dim, backward != 0);
+  return recurrence_workspace(chunks, chained, num_seqs, dim, backward != 0);
 }
 
 mamba2_status mamba2_gated_recurrence(void* y, float* checkpoints, const void* x, const void* gate,
@@ -86,7 +86,7 @@ mamba2_status mamba2_gated_recurrence(void* y, float* checkpoints, const void* x
   if (rb->num_seqs == 0) return MAMBA2_OK;
   bool chained;
   const int64_t chunks = count_chunks(rb->cu_seqlens, rb->num_seqs, &chained);
-  const size_t need = recurrence_workspace(chunks, chained, dim, false);
+  const size_t need = recurrence_workspace(chunks, chained, rb->num_seqs, dim, false);
   if (need > 0 && (!workspace || workspace_bytes < need)) return MAMBA2_ERR_WORKSPACE_TOO_SMALL;
   if (need > 0 && !aligned_to(workspace, 256)) return MAMBA2_ERR_INVALID_ARGUMENT;
   RecArgs a;
@@ -186,7 +186,7 @@ mamba2_status mamba2_gated_recurrence_backward(void* dx, void* dgate, float* dlo
   }
   bool chained;
   const int64_t chunks = count_chunks(cu_seqlens, num_seqs, &chained);
-  const size_t need = recurrence_workspace(chunks, chained, dim, true);
+  const size_t need = recurrence_workspace(chunks, chained, num_seqs, dim, true);
   if (need > 0 && (!workspace || workspace_bytes < need)) return MAMBA2_ERR_WORKSPACE_TOO_SMALL;
   if (need > 0 && !aligned_to(workspace, 256)) return MAMBA2_ERR_INVALID_ARGUMENT;
   RecBwdArgs a;

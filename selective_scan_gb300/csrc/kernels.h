@@ -151,7 +151,7 @@ struct RecArgs {
   SeqTable tab;
 };
 cudaError_t launch_recurrence(const RecArgs& a, mamba2_dtype act, void* ws, cudaStream_t st);
-size_t recurrence_workspace(int64_t chunks, bool chained, int32_t dim, bool backward);
+size_t recurrence_workspace(int64_t chunks, bool chained, int32_t runs, int32_t dim, bool backward);
 
 struct RecStepArgs {
   void* y;

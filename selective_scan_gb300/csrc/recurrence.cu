@@ -9,19 +9,23 @@
 // 16 tokens each, a lane 4 bytes of channels. Per tile:
 //   1. each warp scans its tokens from zero, keeping h_t and the product of the f's in
 //      registers, and posts its map; the eight maps compose to the tile's
-//   2. the tile publishes its map in the workspace, and each warp fetches two of the (at
-//      most 16) records that precede the tile; folded, they are the state that enters it
+//   2. the tile publishes its map in the workspace, and each warp fetches four of the (at
+//      most 32) maps that precede the tile; folded, they give the state that enters it
 //   3. each warp adds (product of f's) x (its own entering state) to its tokens and stores
-// Inputs stream through a ring in shared memory by cp.async: a warp copies only the rows
-// that it will read, so the copies need no barrier, and those of the next tiles are in
-// flight while a tile waits for its predecessors.
+// Inputs stream through a ring in shared memory by TMA (by cp.async where rows are not 16-byte
+// aligned): a warp fetches only the rows that it will read, so a stage is handed over without
+// the other warps, and the next tile's copies are in flight while a tile waits for its
+// predecessors.
 //
 // What precedes chunk l of a run, the same for any timing (so results repeat bit for bit):
-// every 16th chunk (0, 16, 32, ...) publishes the state after it, the others their maps.
-// Chunk l takes the state after chunk 16 floor((l - 1) / 16) and folds the maps of the
-// chunks between in order: maps are published without waiting for anything, so the
-// serial part is one hop every 2 048 tokens. Chunk 0 alone reads the pool, so the run's last
-// chunk may overwrite the slot.
+// every chunk publishes its map, and every 16th (0, 16, 32, ...) the state after it too. Chunk l
+// takes the state that lies one such step further back than the nearest, and folds the maps of
+// the 16 to 31 chunks between in order. Maps are published without waiting for anything, and a
+// state is used 16 chunks later at the earliest: later than the tiles that the GPU holds at one
+// time for wide matrices, so a tile waits for maps alone. (With the nearest state it waited for
+// the maps and then for the state made from them: 232 us against 213 for one run of 65 536
+// tokens by 2 048 channels.) Chunk 0 alone reads the pool, so the run's last chunk may
+// overwrite the slot.
 //
 // Tiles are taken by ticket in an order in which a tile's predecessors come first, so a
 // waiting tile's predecessors are always held by CTAs that run. Waits are bounded; one that
@@ -34,11 +38,14 @@
 // unrounded), keeps each token's gate as the smaller of sigmoid(g) and sigmoid(-g) with
 // the sign of g (the other is one minus it, to the last digit), and makes dx and dgate in
 // one more sweep. dlower is summed per tile and then over the tiles, in order.
-#include "../../include/block.h"
-#include "common.cuh"
+#include <cuda.h>
 
 #include <algorithm>
+#include <cstring>
 #include <type_traits>
+
+#include "../../include/block.h"
+#include "common.cuh"
 
 namespace mamba2 {
 
@@ -46,11 +53,14 @@ __device__ unsigned int g_recurrence_timeouts = 0;
 
 namespace {
 
+#include "tc.cuh"
+
 constexpr int kChunkR = MAMBA2_RECURRENCE_CHUNK;
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTok = kChunkR / kWarps;         // tokens of a warp
 constexpr int kGroup = 2 * kWarps;             // chunks between two published states
+constexpr int kBack = 2 * kGroup / kWarps;     // maps that a warp looks back at, at most
 constexpr int kInfos = 4;
 constexpr uint32_t kPollLimit = 1u << 21;      // polls before giving up (about a second)
 
@@ -189,122 +199,12 @@ __device__ __forceinline__ void pick(typename Pack<C>::V small, const float (&g)
   down = P::make(d);
 }
 
-__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, int bytes16) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(bytes16) : "memory");
-}
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
 template <int n>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(n) : "memory"); }
-
-// Is the first of this row's channels in the upper half of its word? (The word is inside the
-// allocation all the same: allocations begin and end on words.)
-template <typename T>
-__device__ __forceinline__ int odd_start(const T* row) {
-  return sizeof(T) == 2 ? (int)((reinterpret_cast<uintptr_t>(row) >> 1) & 1) : 0;
-}
-
-// This warp's rows [r0, r0 + nt) of the tile at `tile` (row stride ld, m channels from there) into dst.
-template <typename T, bool kVec>
-__device__ __forceinline__ void load_rows(uint32_t dst, const T* tile, int64_t ld, int r0, int nt, int m, int lane) {
-  if constexpr (kVec) {
-    const int r = lane >> 3, c = lane & 7;
-    const int bytes = min(16, m * (int)sizeof(T) - 16 * c);
-    if (bytes <= 0) return;
-    const T* src = tile + (r0 + r) * ld + c * (16 / (int)sizeof(T));
-    dst += (uint32_t)((r0 + r) * 128 + 16 * c);
-#pragma unroll
-    for (int i = 0; i < kTok / 4; ++i, src += 4 * ld)
-      if (4 * i + r < nt) cp_async(dst + 512 * i, src, bytes);
-  } else {
-    for (int r = 0; r < nt; ++r) {
-      const T* row = tile + (int64_t)(r0 + r) * ld;
-      const int odd = odd_start(row);
-      const int words = (m * (int)sizeof(T) + 2 * odd + 3) / 4;
-      const uint32_t* src = reinterpret_cast<const uint32_t*>(row - odd);
-      const uint32_t d = dst + (uint32_t)((r0 + r) * 132);
-      if (lane < words) cp_async4(d + 4 * lane, src + lane);
-      if (lane == 0 && words > 32) cp_async4(d + 128, src + 32);
-    }
-  }
-}
-
-// The lane's word of a staged row.
-template <typename T, bool kVec>
-__device__ __forceinline__ uint32_t staged(const unsigned char* stage, int r, int lane, const T* tile, int64_t ld) {
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(stage + r * kPitch<kVec>) + lane;
-  if constexpr (kVec || sizeof(T) == 4) {
-    return *w;
-  } else {
-    return odd_start(tile + (int64_t)r * ld) ? __funnelshift_r(w[0], w[1], 16) : w[0];
-  }
-}
-
-template <typename T, bool kVec>
-__device__ __forceinline__ void store_row(T* p, const float (&v)[kCh<T>], int left) {  // left: channels from p on
-  if constexpr (sizeof(T) == 4) {
-    if (left > 0) *p = v[0];
-  } else {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(v[0], v[1]);
-    if (left >= 2 && (kVec || !odd_start(p))) {
-      *reinterpret_cast<__nv_bfloat162*>(p) = h;
-    } else {
-      if (left > 0) p[0] = h.x;
-      if (left > 1) p[1] = h.y;
-    }
-  }
-}
-
-// ---- workspace: a header, then a record of one (A, B) per channel for each (chunk, channel group).
-// All of it is set to 0xff bytes first. A record's words are their own flags: every word that a tile
-// publishes is the result of an fp32 operation, which no NaN makes 0xffffffff, so a reader polls the
-// record until that pattern is gone from it, and needs no fence and no second round trip.
-struct Chain {
-  uint32_t* head;  // tickets taken, less one; abort when it is no longer 0xffffffff
-  float* records;  // [chunks, groups, tile channels, 2]
-};
-constexpr size_t kHead = 256;
-constexpr uint32_t kUnset = 0xffffffffu;
-size_t chain_bytes(int64_t chunks, int groups, int width) { return kHead + (size_t)chunks * groups * width * 8; }
-Chain chain_at(void* ws) {
-  return {static_cast<uint32_t*>(ws), reinterpret_cast<float*>(static_cast<char*>(ws) + kHead)};
-}
-
-// A lane's share of a record: (A, B) of each of its channels.
-template <int C>
-__device__ __forceinline__ void load_record(const float* p, float (&v)[2 * C]) {
-  if constexpr (C == 2)
-    asm volatile("ld.relaxed.gpu.global.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "l"(p) : "memory");
-  else
-    asm volatile("ld.relaxed.gpu.global.v2.f32 {%0, %1}, [%2];" : "=f"(v[0]), "=f"(v[1]) : "l"(p) : "memory");
-}
-template <int C>
-__device__ __forceinline__ void store_record(float* p, const float (&v)[2 * C]) {
-  if constexpr (C == 2)
-    asm volatile("st.relaxed.gpu.global.v4.f32 [%0], {%1, %2, %3, %4};"
-                 ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
-  else
-    asm volatile("st.relaxed.gpu.global.v2.f32 [%0], {%1, %2};" ::"l"(p), "f"(v[0]), "f"(v[1]) : "memory");
-}
-template <typename T>
-__device__ __forceinline__ float* record_at(const Chain& ch, int64_t at, int lane) {
-  return ch.records + (at * kTileCh<T> + lane * kCh<T>) * 2;
-}
-template <typename T>
-__device__ __forceinline__ void publish(const Chain& ch, int64_t at, const float (&A)[kCh<T>], const float (&B)[kCh<T>],
-                                        int lane) {
-  float v[2 * kCh<T>];
-#pragma unroll
-  for (int c = 0; c < kCh<T>; ++c) {
-    v[2 * c] = A[c];
-    v[2 * c + 1] = B[c];
-  }
-  store_record<kCh<T>>(record_at<T>(ch, at, lane), v);
-}
 
 // What a CTA knows of a tile. Chunks count from the end that the pass starts at.
 struct Info {
@@ -336,67 +236,253 @@ __device__ __forceinline__ void tile_info(Info& f, const SeqTable& t, int item, 
   f.last = f.l == of - 1;
 }
 
-// What precedes chunk l of a run, as up to kGroup records: d = 1 .. k are the maps of the chunks d before it,
-// d = k + 1 the published state, with k = (l - 1) mod kGroup. Warp w takes d = 2 w + 1 and 2 w + 2.
-template <typename T, bool kReverse>
-struct LookBack {
-  static constexpr int C = kCh<T>;
-  const float* at[2];
-  float r[2][2 * C];
-  bool want[2], state[2];
+// Is the first of this row's channels in the upper half of its word? (The word is inside the
+// allocation all the same: allocations begin and end on words.)
+template <typename T>
+__device__ __forceinline__ int odd_start(const T* row) {
+  return sizeof(T) == 2 ? (int)((reinterpret_cast<uintptr_t>(row) >> 1) & 1) : 0;
+}
 
-  // Starts both loads, to be looked at by finish().
-  __device__ __forceinline__ void start(const Chain& ch, const Info& f, int groups, int warp, int lane) {
-    const int k = f.l > 0 ? (f.l - 1) % kGroup : -1;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int d = 2 * warp + 1 + j;
-      want[j] = d <= k + 1;
-      state[j] = d == k + 1;
-      at[j] = record_at<T>(ch, (int64_t)(kReverse ? f.chunk + d : f.chunk - d) * groups + f.group, lane);
-      if (want[j]) load_record<C>(at[j], r[j]);
-    }
+// This warp's rows [r0, r0 + nt) of the tile at `tile` (row stride ld, m channels from there) into dst, word
+// by word: for rows that TMA does not take (it wants them 16-byte aligned).
+template <typename T>
+__device__ __forceinline__ void load_words(uint32_t dst, const T* tile, int64_t ld, int r0, int nt, int m, int lane) {
+  for (int r = 0; r < nt; ++r) {
+    const T* row = tile + (int64_t)(r0 + r) * ld;
+    const int odd = odd_start(row);
+    const int words = (m * (int)sizeof(T) + 2 * odd + 3) / 4;
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(row - odd);
+    const uint32_t d = dst + (uint32_t)((r0 + r) * 132);
+    if (lane < words) cp_async4(d + 4 * lane, src + lane);
+    if (lane == 0 && words > 32) cp_async4(d + 128, src + 32);
   }
-  // Waits for both and composes them, the older first, into (A, B); a state is the map (0, state).
-  __device__ __forceinline__ void finish(const Chain& ch, float (&A)[C], float (&B)[C], int lane) {
-#pragma unroll 1
-    for (uint32_t it = 0;; ++it) {
-      bool set = true;
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        if (want[j])
-#pragma unroll
-          for (int c = 0; c < 2 * C; ++c) set = set && __float_as_uint(r[j][c]) != kUnset;
-      if (__all_sync(0xffffffffu, set)) break;
-      if ((it & 63u) == 63u) {
-        uint32_t stop = 0;
-        if (lane == 0) {
-          stop = *(volatile uint32_t*)(ch.head + 1) != kUnset;
-          if (!stop && it >= kPollLimit) {
-            atomicExch(ch.head + 1, 0u);
-            atomicAdd(&g_recurrence_timeouts, 1u);
-            stop = 1;
-          }
-        }
-        if (__shfl_sync(0xffffffffu, stop, 0)) break;
-      }
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        if (want[j]) load_record<C>(at[j], r[j]);
-    }
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      A[c] = 1.0f;
-      B[c] = 0.0f;
-#pragma unroll
-      for (int j = 1; j >= 0; --j)
-        if (want[j]) {
-          B[c] = state[j] ? r[j][2 * c + 1] : fmaf(r[j][2 * c], B[c], r[j][2 * c + 1]);
-          A[c] = state[j] ? 0.0f : A[c] * r[j][2 * c];
-        }
-    }
-  }
+}
+
+// A matrix that is streamed through the ring.
+template <typename T>
+struct Stream {
+  const T* p;
+  int64_t ld;
+  const CUtensorMap* map;  // boxes of 128 bytes x kTok rows
 };
+// This warp's rows of tile f of k matrices, kMat bytes apart, into the stage at st. By TMA the stage's
+// barrier of this warp tells when they are there (rows past the run's end are other runs', or zeros: nothing
+// uses them); word by word, the group of copies that this call commits.
+template <typename T, bool kVec, int k>
+__device__ __forceinline__ void load_tile(const Info& f, const Stream<T> (&m)[k], uint32_t st, uint32_t bar, int dim,
+                                          int warp, int lane) {
+  constexpr uint32_t kMat = kChunkR * kPitch<kVec>;
+  const int ch0 = f.group * kTileCh<T>, nt = f.item >= 0 ? min(kTok, f.n - warp * kTok) : 0;
+  if constexpr (kVec) {
+    if (nt > 0 && lane == 0) {
+      fence_async_smem();  // what this warp read and wrote there before comes first
+      mbar_expect_tx(bar, k * kTok * 128);
+#pragma unroll
+      for (int i = 0; i < k; ++i) tma_load_2d(st + i * kMat + warp * kTok * 128, m[i].map, ch0, f.row + warp * kTok, bar);
+    }
+  } else {
+    if (nt > 0)
+#pragma unroll
+      for (int i = 0; i < k; ++i)
+        load_words<T>(st + i * kMat, m[i].p + f.row * m[i].ld + ch0, m[i].ld, warp * kTok, nt, min(kTileCh<T>, dim - ch0), lane);
+    cp_commit();
+  }
+}
+
+// The lane's word of a staged row.
+template <typename T, bool kVec>
+__device__ __forceinline__ uint32_t staged(const unsigned char* stage, int r, int lane, const T* tile, int64_t ld) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(stage + r * kPitch<kVec>) + lane;
+  if constexpr (kVec || sizeof(T) == 4) {
+    return *w;
+  } else {
+    return odd_start(tile + (int64_t)r * ld) ? __funnelshift_r(w[0], w[1], 16) : w[0];
+  }
+}
+
+// kIn: all of the lane's channels are inside the matrix and p is on a word; else `left` are from p on.
+template <typename T, bool kIn>
+__device__ __forceinline__ void store_row(T* p, const float (&v)[kCh<T>], int left) {
+  if constexpr (sizeof(T) == 4) {
+    if (kIn || left > 0) *p = v[0];
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[0], v[1]);
+    if (kIn || (left >= 2 && !odd_start(p))) {
+      *reinterpret_cast<__nv_bfloat162*>(p) = h;
+    } else {
+      if (left > 0) p[0] = h.x;
+      if (left > 1) p[1] = h.y;
+    }
+  }
+}
+
+// ---- workspace: a header, then a record of one (A, B) per channel for each (chunk, channel group), then a
+// record of one state per channel for every kGroup-th chunk of a run (and group).
+// All of it is set to 0xff bytes first. A record's words are their own flags: every word that a tile
+// publishes is the result of an fp32 operation, which no NaN makes 0xffffffff, so a reader polls the
+// record until that pattern is gone from it, and needs no fence and no second round trip.
+struct Chain {
+  uint32_t* head;  // tickets taken, less one; abort when it is no longer 0xffffffff
+  float* maps;     // [chunks, groups, tile channels, 2]
+  float* states;   // [state_rows, groups, tile channels]
+};
+constexpr size_t kHead = 256;
+constexpr uint32_t kUnset = 0xffffffffu;
+// Row of the state after chunk l of run i, whose first chunk is t: the runs' rows do not overlap.
+__host__ __device__ constexpr int64_t state_row(int64_t t, int i, int l) { return t / kGroup + i + l / kGroup; }
+size_t chain_bytes(int64_t chunks, int runs, int64_t channels) {
+  return kHead + (size_t)chunks * channels * 8 + (size_t)state_row(chunks, runs, 0) * channels * 4;
+}
+Chain chain_at(void* ws, int64_t chunks, int64_t channels) {
+  float* maps = reinterpret_cast<float*>(static_cast<char*>(ws) + kHead);
+  return {static_cast<uint32_t*>(ws), maps, maps + chunks * channels * 2};
+}
+
+// A lane's share of a record: (A, B) of each of its channels.
+template <int C>
+__device__ __forceinline__ void load_record(const float* p, float (&v)[2 * C]) {
+  if constexpr (C == 2)
+    asm volatile("ld.relaxed.gpu.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "l"(p) : "memory");
+  else
+    asm volatile("ld.relaxed.gpu.global.v2.f32 {%0, %1}, [%2];" : "=f"(v[0]), "=f"(v[1]) : "l"(p) : "memory");
+}
+template <int C>
+__device__ __forceinline__ void store_record(float* p, const float (&v)[2 * C]) {
+  if constexpr (C == 2)
+    asm volatile("st.relaxed.gpu.global.v4.f32 [%0], {%1, %2, %3, %4};"
+                 ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
+  else
+    asm volatile("st.relaxed.gpu.global.v2.f32 [%0], {%1, %2};" ::"l"(p), "f"(v[0]), "f"(v[1]) : "memory");
+}
+template <int C>
+__device__ __forceinline__ void load_state(const float* p, float (&v)[C]) {
+  if constexpr (C == 2)
+    asm volatile("ld.relaxed.gpu.global.v2.f32 {%0, %1}, [%2];" : "=f"(v[0]), "=f"(v[1]) : "l"(p) : "memory");
+  else
+    asm volatile("ld.relaxed.gpu.global.f32 %0, [%1];" : "=f"(v[0]) : "l"(p) : "memory");
+}
+template <int n>
+__device__ __forceinline__ bool is_set(const float (&v)[n]) {
+  bool set = true;
+#pragma unroll
+  for (int c = 0; c < n; ++c) set = set && __float_as_uint(v[c]) != kUnset;
+  return set;
+}
+template <typename T>
+__device__ __forceinline__ float* map_at(const Chain& ch, int64_t chunk, int groups, int group, int lane) {
+  return ch.maps + ((chunk * groups + group) * kTileCh<T> + lane * kCh<T>) * 2;
+}
+template <typename T>
+__device__ __forceinline__ float* state_at(const Chain& ch, const Info& f, int first, int l, int groups, int lane) {
+  return ch.states + (state_row(first, f.seq, l) * groups + f.group) * kTileCh<T> + lane * kCh<T>;
+}
+template <typename T>
+__device__ __forceinline__ void publish_map(const Chain& ch, const Info& f, int groups, const float (&A)[kCh<T>],
+                                            const float (&B)[kCh<T>], int lane) {
+  float v[2 * kCh<T>];
+#pragma unroll
+  for (int c = 0; c < kCh<T>; ++c) {
+    v[2 * c] = A[c];
+    v[2 * c + 1] = B[c];
+  }
+  store_record<kCh<T>>(map_at<T>(ch, f.chunk, groups, f.group, lane), v);
+}
+template <typename T>
+__device__ __forceinline__ void publish_state(const Chain& ch, const Info& f, int first, int groups,
+                                              const float (&h)[kCh<T>], int lane) {
+  float* p = state_at<T>(ch, f, first, f.l, groups, lane);
+  if constexpr (kCh<T> == 2)
+    asm volatile("st.relaxed.gpu.global.v2.f32 [%0], {%1, %2};" ::"l"(p), "f"(h[0]), "f"(h[1]) : "memory");
+  else
+    asm volatile("st.relaxed.gpu.global.f32 [%0], %1;" ::"l"(p), "f"(h[0]) : "memory");
+}
+
+// Chunks between chunk l > 0 and the published state that it starts from.
+__device__ __forceinline__ int maps_before(int l) {
+  const int g = (l - 1) / kGroup;
+  return l - 1 - (g > 0 ? g - 1 : 0) * kGroup;
+}
+
+// Tells a waiting warp to give up: when another one has, or after kPollLimit polls.
+__device__ __forceinline__ bool gave_up(const Chain& ch, uint32_t it, int lane) {
+  if ((it & 63u) != 63u) return false;
+  uint32_t stop = 0;
+  if (lane == 0) {
+    stop = *(volatile uint32_t*)(ch.head + 1) != kUnset;
+    if (!stop && it >= kPollLimit) {
+      atomicExch(ch.head + 1, 0u);
+      atomicAdd(&g_recurrence_timeouts, 1u);
+      stop = 1;
+    }
+  }
+  return __shfl_sync(0xffffffffu, stop, 0) != 0u;
+}
+
+// What enters a tile, in shared memory: the state it starts from, and a map from each warp, the oldest last.
+template <typename T>
+struct Before {
+  float state[kTileCh<T>];
+  float A[kWarps][kTileCh<T>], B[kWarps][kTileCh<T>];
+};
+// This warp's share: the maps of the chunks kBack warp + 1 .. kBack (warp + 1) before the tile as far as there
+// are k, composed; and the state (warp 0).
+template <typename T, bool kReverse, typename First>
+__device__ __forceinline__ void look_back(const Chain& ch, const Info& f, int first, int groups, int k,
+                                          Before<T>& out, int warp, int lane, First initial) {
+  constexpr int C = kCh<T>;
+  const int d0 = kBack * warp + 1, n = min(kBack, max(0, k - d0 + 1));
+  const int64_t step = (int64_t)(kReverse ? groups : -groups) * kTileCh<T> * 2;
+  const float* p = map_at<T>(ch, kReverse ? f.chunk + d0 : f.chunk - d0, groups, f.group, lane);
+  float r[kBack][2 * C], h[C];
+#pragma unroll
+  for (int j = 0; j < kBack; ++j)
+    if (j < n) load_record<C>(p + j * step, r[j]);
+  if (warp == 0) {
+    if (f.l == 0) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) h[c] = initial(c);
+    } else {
+      const float* q = state_at<T>(ch, f, first, f.l - 1 - k, groups, lane);
+      load_state<C>(q, h);
+#pragma unroll 1
+      for (uint32_t it = 0; !__all_sync(0xffffffffu, is_set(h)) && !gave_up(ch, it, lane); ++it) load_state<C>(q, h);
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) out.state[lane * C + c] = h[c];
+  }
+#pragma unroll 1
+  for (uint32_t it = 0;; ++it) {
+    bool set = true;
+#pragma unroll
+    for (int j = 0; j < kBack; ++j) set = set && (j >= n || is_set(r[j]));
+    if (__all_sync(0xffffffffu, set) || gave_up(ch, it, lane)) break;
+#pragma unroll
+    for (int j = 0; j < kBack; ++j)
+      if (j < n) load_record<C>(p + j * step, r[j]);
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    float A = 1.0f, B = 0.0f;
+#pragma unroll
+    for (int j = kBack - 1; j >= 0; --j)
+      if (j < n) {
+        B = fmaf(r[j][2 * c], B, r[j][2 * c + 1]);
+        A *= r[j][2 * c];
+      }
+    out.A[warp][lane * C + c] = A;
+    out.B[warp][lane * C + c] = B;
+  }
+}
+// After a barrier: what enters the tile.
+template <typename T>
+__device__ __forceinline__ void fold_before(const Before<T>& in, int k, float (&v)[kCh<T>], int lane) {
+#pragma unroll
+  for (int c = 0; c < kCh<T>; ++c) v[c] = in.state[lane * kCh<T> + c];
+  for (int w = (k + kBack - 1) / kBack - 1; w >= 0; --w)
+#pragma unroll
+    for (int c = 0; c < kCh<T>; ++c) v[c] = fmaf(in.A[w][lane * kCh<T> + c], v[c], in.B[w][lane * kCh<T> + c]);
+}
 
 // The next tile: by ticket where tiles wait for one another, else by turns. A CTA takes tickets `stages`
 // tiles ahead; where that would be more than an even share, it takes the share and no more, so that a CTA
@@ -417,7 +503,9 @@ template <typename T>
 struct FwdShared {
   Info info[kInfos];
   float A[kWarps][kTileCh<T>], B[kWarps][kTileCh<T>];      // the warps' maps
-  float pa[kWarps][kTileCh<T>], pb[kWarps][kTileCh<T>];    // what each found before the tile
+  Before<T> before;
+  alignas(8) uint64_t full[kFwdStages][kWarps];
+  uint32_t abort;
 };
 
 // The products of the f's go into shared memory, over the inputs that the lane has consumed (the same 8 bytes
@@ -427,7 +515,9 @@ template <typename T, bool kVec> constexpr int kFwdCtas = kVec ? 3 : 2;
 
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads, kFwdCtas<T, kVec>)
-rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ Chain ch, const int items, const int groups) {
+rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ CUtensorMap mx,
+               const __grid_constant__ CUtensorMap mg, const __grid_constant__ Chain ch, const int items,
+               const int groups) {
   extern __shared__ __align__(128) unsigned char stages[];
   __shared__ FwdShared<T> s;
   constexpr int C = kCh<T>;
@@ -441,24 +531,23 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ Chain 
     if (a.tab.cu[i] == a.tab.cu[i + 1] && seq_fresh(a.tab, i))
       for (int c = threadIdx.x; c < a.dim; c += kThreads) a.state[(int64_t)seq_slot(a.tab, i) * a.dim + c] = 0.0f;
 
-  auto load = [&](int i) {  // this warp's rows of tile i, if there is one; always a group
-    const Info& f = s.info[i % kInfos];
-    if (f.item >= 0) {
-      const int ch0 = f.group * kTileCh<T>, m = min(kTileCh<T>, a.dim - ch0);
-      const int nt = min(kTok, f.n - warp * kTok);
-      const uint32_t st = smem_addr(stages) + (uint32_t)(i % kFwdStages) * kFwdStage<kVec>;
-      load_rows<T, kVec>(st, static_cast<const T*>(a.x) + f.row * a.ld_x + ch0, a.ld_x, warp * kTok, nt, m, lane);
-      load_rows<T, kVec>(st + kMat, static_cast<const T*>(a.gate) + f.row * a.ld_gate + ch0, a.ld_gate, warp * kTok, nt,
-                         m, lane);
-    }
-    cp_commit();
+  const Stream<T> in_streams[2] = {{static_cast<const T*>(a.x), a.ld_x, &mx}, {static_cast<const T*>(a.gate), a.ld_gate, &mg}};
+  auto load = [&](int i) {  // this warp's rows of tile i, if there is one
+    load_tile<T, kVec, 2>(s.info[i % kInfos], in_streams, su32(stages) + (uint32_t)(i % kFwdStages) * kFwdStage<kVec>,
+                          su32(&s.full[i % kFwdStages][warp]), a.dim, warp, lane);
   };
+  if (threadIdx.x < kFwdStages * kWarps) {
+    mbar_init(su32(&s.full[0][0] + threadIdx.x), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    s.abort = 0u;
+  }
   if (threadIdx.x == 0)
     for (int i = 0; i < kFwdStages; ++i)
       tile_info<false>(s.info[i], a.tab, take<kFwdStages>(ch, i, items), items, groups);
   __syncthreads();
   for (int i = 0; i < kFwdStages; ++i) load(i);
 
+  uint32_t phases = 0;  // bit s: the parity of stage s's next load
   for (int i = 0;; ++i) {
     const Info f = s.info[i % kInfos];
     if (f.item < 0) break;
@@ -466,8 +555,8 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ Chain 
     const int left = a.dim - ch0;  // channels of this lane and those after it
     int next = 0;
     if (threadIdx.x == 0) next = take<kFwdStages>(ch, i + kFwdStages, items);
-    LookBack<T, false> back;
-    back.start(ch, f, groups, warp, lane);
+    const int first = a.tab.tile[f.seq];
+    const int before = f.l > 0 ? maps_before(f.l) : 0;
     // ---- scan from zero
     unsigned char* st = stages + (i % kFwdStages) * kFwdStage<kVec>;
     const T* tx = static_cast<const T*>(a.x) + f.row * a.ld_x + f.group * kTileCh<T>;
@@ -484,8 +573,15 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ Chain 
     auto word = [&](int j) {
       return reinterpret_cast<float*>(st + (warp * kTok + j) * kPitch<kVec>) + lane;
     };
-    cp_wait<kFwdStages - 1>();
-    __syncwarp();
+    if constexpr (kVec) {
+      if (nt > 0) {
+        warp_wait(su32(&s.full[i % kFwdStages][warp]), phases >> (i % kFwdStages) & 1u, &s.abort);
+        phases ^= 1u << (i % kFwdStages);
+      }
+    } else {
+      cp_wait<kFwdStages - 1>();
+      __syncwarp();
+    }
     V hs[kTok], ps[kVec ? 1 : kTok], h2 = P::all(0.0f), p2 = P::all(1.0f);
     auto scan = [&](auto whole) {  // rows past the run's end count as the identity
 #pragma unroll
@@ -536,40 +632,21 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ Chain 
         eb[c] = fmaf(wa, eb[c], s.B[w][lane * C + c]);
         ea[c] *= wa;
       }
-    const int64_t at = (int64_t)f.chunk * groups + f.group;
     if (warp == kWarps - 1) {
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         B[c] = fmaf(A[c], eb[c], B[c]);
         A[c] *= ea[c];
       }
-      if (!f.last && f.l % kGroup != 0) publish<T>(ch, at, A, B, lane);
+      if (!f.last) publish_map<T>(ch, f, groups, A, B, lane);
     }
-    {
-      float pa[C], pb[C];
-      back.finish(ch, pa, pb, lane);
-      if (f.l == 0 && warp == 0)
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          pa[c] = 0.0f;
-          pb[c] = c < left && !seq_fresh(a.tab, f.seq) ? a.state[(int64_t)seq_slot(a.tab, f.seq) * a.dim + ch0 + c] : 0.0f;
-        }
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        s.pa[warp][lane * C + c] = pa[c];
-        s.pb[warp][lane * C + c] = pb[c];
-      }
-    }
+    look_back<T, false>(ch, f, first, groups, before, s.before, warp, lane, [&](int c) {
+      return c < left && !seq_fresh(a.tab, f.seq) ? a.state[(int64_t)seq_slot(a.tab, f.seq) * a.dim + ch0 + c] : 0.0f;
+    });
     if (threadIdx.x == 0) tile_info<false>(s.info[(i + kFwdStages) % kInfos], a.tab, next, items, groups);
     __syncthreads();
-    // what enters the tile, the oldest first
     float in[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c) in[c] = 0.0f;
-#pragma unroll
-    for (int w = kWarps - 1; w >= 0; --w)
-#pragma unroll
-      for (int c = 0; c < C; ++c) in[c] = fmaf(s.pa[w][lane * C + c], in[c], s.pb[w][lane * C + c]);
+    fold_before(s.before, before, in, lane);
     if (warp == kWarps - 1) {
       float end[C];
 #pragma unroll
@@ -582,7 +659,7 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ Chain 
         for (int c = 0; c < C; ++c)
           if (c < left) a.state[(int64_t)seq_slot(a.tab, f.seq) * a.dim + ch0 + c] = end[c];
       } else if (f.l % kGroup == 0) {
-        publish<T>(ch, at, end, end, lane);
+        publish_state<T>(ch, f, first, groups, end, lane);
       }
     }
     T* ty = static_cast<T*>(a.y) + (f.row + warp * kTok) * a.ld_y + ch0;
@@ -591,23 +668,26 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ Chain 
 #pragma unroll
       for (int j = 0; j < kTok; ++j)
         if (decltype(whole)::value || j < nt) {
-          float y[C], v[C];
+          float y[C];
           if constexpr (kVec) {
+            float v[C];
 #pragma unroll
             for (int c = 0; c < C; ++c) v[c] = word(j)[c * (kMat / 4)];
             P::split(P::fma(P::make(v), in2, hs[j]), y);
           } else {
             P::split(P::fma(ps[j], in2, hs[j]), y);
           }
-          store_row<T, kVec>(ty + j * a.ld_y, y, left);
+          store_row<T, kVec && decltype(whole)::value>(ty + j * a.ld_y, y, left);
         }
     };
-    if (nt == kTok) emit(std::true_type{});
+    if (nt == kTok && (f.group + 1) * kTileCh<T> <= a.dim) emit(std::true_type{});
     else emit(std::false_type{});
     __syncwarp();  // every lane is done with this stage
     load(i + kFwdStages);
   }
-  cp_wait<0>();
+  if constexpr (!kVec) cp_wait<0>();
+  __syncthreads();
+  if (threadIdx.x == 0 && s.abort) atomicAdd(&g_recurrence_timeouts, 1u);
 }
 
 // ------------------------------------------------------------------ backward
@@ -619,14 +699,17 @@ template <typename T>
 struct BwdShared {
   Info info[kInfos];
   float A[kWarps][kTileCh<T>], F[kWarps][kTileCh<T>], R[kWarps][kTileCh<T>];
-  float pa[kWarps][kTileCh<T>], pb[kWarps][kTileCh<T>];
+  Before<T> before;
   float dlo[kWarps][kTileCh<T>];
+  alignas(8) uint64_t full[kBwdStages][kWarps];
+  uint32_t abort;
 };
 
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads, 2)
-rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ Chain ch, float* part, const int items,
-               const int groups) {
+rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUtensorMap mx,
+               const __grid_constant__ CUtensorMap mg, const __grid_constant__ CUtensorMap md,
+               const __grid_constant__ Chain ch, float* part, const int items, const int groups) {
   extern __shared__ __align__(128) unsigned char stages[];
   __shared__ BwdShared<T> s;
   constexpr int C = kCh<T>;
@@ -641,20 +724,18 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ Cha
         for (int c = threadIdx.x; c < a.dim; c += kThreads)
           a.dstate[(int64_t)i * a.dim + c] = a.dstate_end ? a.dstate_end[(int64_t)i * a.dim + c] : 0.0f;
 
+  const Stream<T> in_streams[3] = {{static_cast<const T*>(a.x), a.ld_x, &mx},
+                                   {static_cast<const T*>(a.gate), a.ld_gate, &mg},
+                                   {static_cast<const T*>(a.dy), a.ld_dy, &md}};
   auto load = [&](int i) {
-    const Info& f = s.info[i % kInfos];
-    if (f.item >= 0) {
-      const int ch0 = f.group * kTileCh<T>, m = min(kTileCh<T>, a.dim - ch0);
-      const int nt = min(kTok, f.n - warp * kTok);
-      const uint32_t st = smem_addr(stages) + (uint32_t)(i % kBwdStages) * kBwdStage<kVec>;
-      load_rows<T, kVec>(st, static_cast<const T*>(a.x) + f.row * a.ld_x + ch0, a.ld_x, warp * kTok, nt, m, lane);
-      load_rows<T, kVec>(st + kMat, static_cast<const T*>(a.gate) + f.row * a.ld_gate + ch0, a.ld_gate, warp * kTok, nt,
-                         m, lane);
-      load_rows<T, kVec>(st + 2 * kMat, static_cast<const T*>(a.dy) + f.row * a.ld_dy + ch0, a.ld_dy, warp * kTok, nt, m,
-                         lane);
-    }
-    cp_commit();
+    load_tile<T, kVec, 3>(s.info[i % kInfos], in_streams, su32(stages) + (uint32_t)(i % kBwdStages) * kBwdStage<kVec>,
+                          su32(&s.full[i % kBwdStages][warp]), a.dim, warp, lane);
   };
+  if (threadIdx.x < kBwdStages * kWarps) {
+    mbar_init(su32(&s.full[0][0] + threadIdx.x), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    s.abort = 0u;
+  }
   // the sum of a finished tile's eight parts of dlower (one warp, a tile later)
   auto sum_part = [&](int i) {
     const Info& f = s.info[i % kInfos];
@@ -673,6 +754,7 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ Cha
   __syncthreads();
   for (int i = 0; i < kBwdStages; ++i) load(i);
 
+  uint32_t phases = 0;
   int i = 0;
   for (;; ++i) {
     const Info f = s.info[i % kInfos];
@@ -681,8 +763,8 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ Cha
     const int left = a.dim - ch0;
     int next = 0;
     if (threadIdx.x == 0) next = take<kBwdStages>(ch, i + kBwdStages, items);
-    LookBack<T, true> back;
-    back.start(ch, f, groups, warp, lane);
+    const int first = a.tab.tile[f.seq];
+    const int before = f.l > 0 ? maps_before(f.l) : 0;
     const unsigned char* st = stages + (i % kBwdStages) * kBwdStage<kVec>;
     const T* tx = static_cast<const T*>(a.x) + f.row * a.ld_x + f.group * kTileCh<T>;
     const T* tg = static_cast<const T*>(a.gate) + f.row * a.ld_gate + f.group * kTileCh<T>;
@@ -696,8 +778,15 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ Cha
     }
     const V lo2 = P::make(lo), un2 = P::make(un);
     const int nt = min(kTok, f.n - warp * kTok);
-    cp_wait<kBwdStages - 1>();
-    __syncwarp();
+    if constexpr (kVec) {
+      if (nt > 0) {
+        warp_wait(su32(&s.full[i % kBwdStages][warp]), phases >> (i % kBwdStages) & 1u, &s.abort);
+        phases ^= 1u << (i % kBwdStages);
+      }
+    } else {
+      cp_wait<kBwdStages - 1>();
+      __syncwarp();
+    }
     // ---- both scans from zero: h's map (A, F) and R's map (A, R)
     V sg[kTok];  // the smaller sigmoid, signed as the gate
     V A2 = P::all(1.0f), F2 = P::all(0.0f), R2 = P::all(0.0f);
@@ -761,14 +850,13 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ Cha
         eb[c] = fmaf(wa, eb[c], s.R[w][lane * C + c]);
         ea[c] *= wa;
       }
-    const int64_t at = (int64_t)f.chunk * groups + f.group;
     if (warp == 0) {
 #pragma unroll
       for (int c = 0; c < C; ++c) {  // its own tokens are the last of the pass
         R[c] = fmaf(A[c], eb[c], R[c]);
         A[c] *= ea[c];
       }
-      if (!f.last && f.l % kGroup != 0) publish<T>(ch, at, A, R, lane);
+      if (!f.last) publish_map<T>(ch, f, groups, A, R, lane);
     }
     // ---- the state before each token
     V hs[kTok], hp2 = P::make(hp);
@@ -786,31 +874,14 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ Cha
     };
     if (nt == kTok) states(std::true_type{});
     else states(std::false_type{});
-    {
-      float pa[C], pb[C];
-      back.finish(ch, pa, pb, lane);
-      if (f.l == 0 && warp == 0)
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          pa[c] = 0.0f;
-          pb[c] = c < left && a.dstate_end ? a.dstate_end[(int64_t)f.seq * a.dim + ch0 + c] : 0.0f;
-        }
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        s.pa[warp][lane * C + c] = pa[c];
-        s.pb[warp][lane * C + c] = pb[c];
-      }
-    }
+    look_back<T, true>(ch, f, first, groups, before, s.before, warp, lane, [&](int c) {
+      return c < left && a.dstate_end ? a.dstate_end[(int64_t)f.seq * a.dim + ch0 + c] : 0.0f;
+    });
     // info[i + 2] takes the place of tile i - 2, whose part of dlower has been summed
     if (threadIdx.x == 0) tile_info<true>(s.info[(i + kBwdStages) % kInfos], a.tab, next, items, groups);
     __syncthreads();
     float in[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c) in[c] = 0.0f;
-#pragma unroll
-    for (int w = kWarps - 1; w >= 0; --w)
-#pragma unroll
-      for (int c = 0; c < C; ++c) in[c] = fmaf(s.pa[w][lane * C + c], in[c], s.pb[w][lane * C + c]);
+    fold_before(s.before, before, in, lane);
     if (warp == 0) {
       float end[C];
 #pragma unroll
@@ -820,7 +891,7 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ Cha
         for (int c = 0; c < C; ++c)
           if (a.dstate && c < left) a.dstate[(int64_t)f.seq * a.dim + ch0 + c] = end[c];
       } else if (f.l % kGroup == 0) {
-        publish<T>(ch, at, end, end, lane);
+        publish_state<T>(ch, f, first, groups, end, lane);
       }
     }
     // ---- backwards over the tokens
@@ -844,11 +915,11 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ Cha
           P::split(P::mul(P::mul(dd, un2), up), vg);
           dlo2 = P::add(dlo2, dd);
           in2 = P::mul(ft, G);
-          store_row<T, kVec>(ox + j * a.ld_dx, vx, left);
-          store_row<T, kVec>(og + j * a.ld_dgate, vg, left);
+          store_row<T, kVec && decltype(whole)::value>(ox + j * a.ld_dx, vx, left);
+          store_row<T, kVec && decltype(whole)::value>(og + j * a.ld_dgate, vg, left);
         }
     };
-    if (nt == kTok) emit(std::true_type{});
+    if (nt == kTok && (f.group + 1) * kTileCh<T> <= a.dim) emit(std::true_type{});
     else emit(std::false_type{});
     float dlo[C];
     P::split(dlo2, dlo);
@@ -859,7 +930,8 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ Cha
   }
   __syncthreads();
   if (warp == 1 && i > 0 && part) sum_part(i - 1);
-  cp_wait<0>();
+  if constexpr (!kVec) cp_wait<0>();
+  if (threadIdx.x == 0 && s.abort) atomicAdd(&g_recurrence_timeouts, 1u);
 }
 
 // dlower[ch] = sum of the tiles' parts: 32 channels a CTA, eight threads a channel over every
@@ -924,20 +996,62 @@ int ctas(int64_t items, int per_sm) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(items, per_sm * (int64_t)sm_count()));
 }
 
+using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                            const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                            CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+Encode encode_fn() {
+  static Encode fn = []() -> Encode {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<Encode>(p);
+  }();
+  return fn;
+}
+// [rows][dim] with a row stride of ld elements: boxes of 128 bytes x kTok rows, zeros past the edges
+template <typename T>
+bool make_map(CUtensorMap* tm, const void* base, int64_t rows, int64_t dim, int64_t ld) {
+  const Encode enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)dim, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * sizeof(T)};
+  const cuuint32_t box[2] = {(cuuint32_t)kTileCh<T>, (cuuint32_t)kTok}, estr[2] = {1, 1};
+  return enc(tm, sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename T, bool kVec>
 cudaError_t run_fwd(const RecArgs& a, const Chain& ch, int items, int groups, cudaStream_t st) {
   constexpr int smem = kFwdStages * kFwdStage<kVec>;
+  CUtensorMap mx, mg;
+  std::memset(&mx, 0, sizeof mx);
+  std::memset(&mg, 0, sizeof mg);
+  const int rows = a.tab.cu[a.tab.n];
+  if (kVec && rows > 0 && !(make_map<T>(&mx, a.x, rows, a.dim, a.ld_x) && make_map<T>(&mg, a.gate, rows, a.dim, a.ld_gate)))
+    return cudaErrorInvalidValue;
   const cudaError_t e = cudaFuncSetAttribute(rec_fwd_kernel<T, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  rec_fwd_kernel<T, kVec><<<ctas(items, kFwdCtas<T, kVec>), kThreads, smem, st>>>(a, ch, items, groups);
+  rec_fwd_kernel<T, kVec><<<ctas(items, kFwdCtas<T, kVec>), kThreads, smem, st>>>(a, mx, mg, ch, items, groups);
   return cudaGetLastError();
 }
 template <typename T, bool kVec>
 cudaError_t run_bwd(const RecBwdArgs& a, const Chain& ch, float* part, int items, int groups, cudaStream_t st) {
   constexpr int smem = kBwdStages * kBwdStage<kVec>;
+  CUtensorMap mx, mg, md;
+  std::memset(&mx, 0, sizeof mx);
+  std::memset(&mg, 0, sizeof mg);
+  std::memset(&md, 0, sizeof md);
+  const int rows = a.tab.cu[a.tab.n];
+  if (kVec && rows > 0 &&
+      !(make_map<T>(&mx, a.x, rows, a.dim, a.ld_x) && make_map<T>(&mg, a.gate, rows, a.dim, a.ld_gate) &&
+        make_map<T>(&md, a.dy, rows, a.dim, a.ld_dy)))
+    return cudaErrorInvalidValue;
   const cudaError_t e = cudaFuncSetAttribute(rec_bwd_kernel<T, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  rec_bwd_kernel<T, kVec><<<ctas(items, 2), kThreads, smem, st>>>(a, ch, part, items, groups);
+  rec_bwd_kernel<T, kVec><<<ctas(items, 2), kThreads, smem, st>>>(a, mx, mg, md, ch, part, items, groups);
   return cudaGetLastError();
 }
 
@@ -960,18 +1074,18 @@ Tiles plan(const SeqTable& t, mamba2_dtype act, int32_t dim, void* ws, cudaStrea
   bool chained = false;
   for (int i = 0; i < t.n; ++i) chained |= t.tile[i + 1] - t.tile[i] > 1;
   if (chained) {
-    p.chain = chain_at(ws);
-    p.status = cudaMemsetAsync(ws, 0xff, chain_bytes(chunks, p.groups, width), st);
+    p.chain = chain_at(ws, chunks, (int64_t)p.groups * width);
+    p.status = cudaMemsetAsync(ws, 0xff, chain_bytes(chunks, t.n, (int64_t)p.groups * width), st);
   }
   return p;
 }
 
 }  // namespace
 
-size_t recurrence_workspace(int64_t chunks, bool chained, int32_t dim, bool backward) {
+size_t recurrence_workspace(int64_t chunks, bool chained, int32_t runs, int32_t dim, bool backward) {
   const size_t part = backward ? ((size_t)chunks * dim * 4 + 255) / 256 * 256 : 0;
-  // (the groups of either type together are at most 63 channels wider than dim)
-  return part + (chained ? (chain_bytes(chunks, 1, dim + 63) + 255) / 256 * 256 : 0);
+  // (either type's groups together are at most 63 channels wider than dim)
+  return part + (chained ? (chain_bytes(chunks, runs, (int64_t)dim + 63) + 255) / 256 * 256 : 0);
 }
 
 unsigned int read_recurrence_timeouts() {
@@ -995,7 +1109,7 @@ cudaError_t launch_recurrence(const RecArgs& a, mamba2_dtype act, void* ws, cuda
 cudaError_t launch_recurrence_backward(const RecBwdArgs& a, mamba2_dtype act, void* ws, cudaStream_t st) {
   const int64_t chunks = a.tab.tile[a.tab.n];
   float* part = a.dlower ? static_cast<float*>(ws) : nullptr;
-  const Tiles p = plan(a.tab, act, a.dim, static_cast<char*>(ws) + recurrence_workspace(chunks, false, a.dim, true), st);
+  const Tiles p = plan(a.tab, act, a.dim, static_cast<char*>(ws) + recurrence_workspace(chunks, false, 0, a.dim, true), st);
   if (p.status != cudaSuccess) return p.status;
   const size_t es = act == MAMBA2_BF16 ? 2 : 4;
   const bool vec = rows16(a.x, a.ld_x, es) && rows16(a.gate, a.ld_gate, es) && rows16(a.dy, a.ld_dy, es) &&
