@@ -1,14 +1,29 @@
 // RMS norm with the residual's addition (block.h), its 8-bit output, and its backward pass.
+// Each reads its inputs from HBM once and writes its outputs once, and that bounds it.
 //
-// One CTA per row; the row is read twice (the second time from L2).
+// A row lives in the registers of `nt` threads, 32 elements each at most (16 where registers would not
+// do: single elements, and fp32 in the backward pass), read and written in units of 16 bytes of bf16 (8
+// elements) where the width allows, else of 2 elements or 1. nt is the fewest whole warps that hold the
+// row, so all of a row's loads are on the way at once; with fewer rows than SMs a row is spread further,
+// up to a thread per unit. Several rows share a CTA up to 256 threads. Sums of squares go warp by warp and
+// then over the warps in order, in fp32. Rows wider than 512 threads hold are read again from L2 instead
+// (the streamed kernels).
 #include <cuda_fp8.h>
+
+#include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 
 namespace mamba2 {
 namespace {
 
-constexpr int kThreads = 256;
+// elements of a row that a thread holds
+constexpr int held_by_thread(int unit, int sum_bytes, bool backward) {
+  return unit == 1 || (backward && sum_bytes == 4) ? 16 : 32;
+}
+constexpr int kCtaThreads = 256;
+constexpr int kMaxThreads = 512;
 constexpr float kMax8 = 448.0f;  // largest e4m3 value
 
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -17,69 +32,329 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-__device__ __forceinline__ float block_sum(float v) {
-  __shared__ float part[kThreads / 32];
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float s = 0.0f;
-  for (int i = 0; i < kThreads / 32; ++i) s += part[i];
-  return s;
+// W adjacent elements.
+template <typename T, int W>
+struct Unit {
+  static constexpr int kBytes = W * (int)sizeof(T);
+  using Word = std::conditional_t<kBytes % 16 == 0, uint4,
+                                  std::conditional_t<kBytes == 8, uint2, std::conditional_t<kBytes == 4, uint32_t, uint16_t>>>;
+  static constexpr int kWords = kBytes / (int)sizeof(Word);
+  Word w[kWords];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = __ldcs(reinterpret_cast<const Word*>(p) + i);
+  }
+  __device__ __forceinline__ void store(T* p) const {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) __stcs(reinterpret_cast<Word*>(p) + i, w[i]);
+  }
+  __device__ __forceinline__ float get(int j) const { return Act<T>::to_f(reinterpret_cast<const T*>(w)[j]); }
+  __device__ __forceinline__ void set(int j, float v) { reinterpret_cast<T*>(w)[j] = Act<T>::from_f(v); }
+};
+// W e4m3 values from fp32, to nearest even
+template <int W>
+__device__ __forceinline__ void store8(__nv_fp8_storage_t* p, const float (&v)[W]) {
+  if constexpr (W == 1) {
+    *p = __nv_cvt_float_to_fp8(v[0], __NV_SATFINITE, __NV_E4M3);
+  } else {
+    uint16_t h[W / 2];
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i)
+      h[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+    if constexpr (W == 8) *reinterpret_cast<uint2*>(p) = make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
+    else *reinterpret_cast<uint16_t*>(p) = h[0];
+  }
 }
-__device__ __forceinline__ float block_max(float v) {
-  __shared__ float part[kThreads / 32];
-  for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+
+// The fp32 weights of W columns.
+template <int W>
+__device__ __forceinline__ void load_weight(const float* p, float (&w)[W]) {
+  if constexpr (W == 8) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    w[0] = a.x;
+    w[1] = a.y;
+    w[2] = a.z;
+    w[3] = a.w;
+    w[4] = b.x;
+    w[5] = b.y;
+    w[6] = b.z;
+    w[7] = b.w;
+  } else if constexpr (W == 2) {
+    const float2 a = __ldg(reinterpret_cast<const float2*>(p));
+    w[0] = a.x;
+    w[1] = a.y;
+  } else {
+    w[0] = __ldg(p);
+  }
+}
+
+// The sums (or NaN-keeping maxima) of n values over the row's nt threads, in a fixed order. part: a place per
+// warp of the CTA that no reduction before the last barrier of the row's threads used; they alone meet here.
+template <bool kMax, int n>
+__device__ __forceinline__ void row_reduce(float (&v)[n], int nt, float (*part)[n]) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < n; ++k) {
+      const float u = __shfl_xor_sync(0xffffffffu, v[k], o);
+      v[k] = kMax ? max_nan(v[k], u) : v[k] + u;
+    }
+  if (nt == 32) return;
+  const int warps = nt >> 5, row0 = (int)threadIdx.y * warps;
+  if ((threadIdx.x & 31) == 0)
+#pragma unroll
+    for (int k = 0; k < n; ++k) part[row0 + (threadIdx.x >> 5)][k] = v[k];
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + (int)threadIdx.y), "r"(nt) : "memory");
+#pragma unroll
+  for (int k = 0; k < n; ++k) v[k] = part[row0][k];
+  for (int i = 1; i < warps; ++i)
+#pragma unroll
+    for (int k = 0; k < n; ++k) v[k] = kMax ? max_nan(v[k], part[row0 + i][k]) : v[k] + part[row0 + i][k];
+}
+
+// Launched as a programmatic dependent: the weights, a parameter, may be read before the kernel in front has
+// finished; nothing else is.
+__device__ __forceinline__ void wait_for_inputs() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename T, typename S, bool F8, int W>
+__global__ void __launch_bounds__(kMaxThreads)
+add_norm_kernel(const AddNormArgs a, const int nt) {
+  constexpr int U = held_by_thread(W, sizeof(S), false) / W;
+  __shared__ float part[2][kMaxThreads / 32][1];
+  const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  const bool live = row < a.rows;
+  const T* x = static_cast<const T*>(a.x) + row * a.dim;
+  const S* r = static_cast<const S*>(a.residual) + row * a.dim;
+  wait_for_inputs();
+  Unit<T, W> xv[U];
+  Unit<S, W> rv[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int c = ((int)threadIdx.x + nt * u) * W;
+    if (live && c < a.dim) {
+      xv[u].load(x + c);
+      if (a.residual) rv[u].load(r + c);
+    }
+  }
+  float s[U][W], ss[1] = {0.0f};
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int c = ((int)threadIdx.x + nt * u) * W;
+    if (live && c < a.dim) {
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        s[u][j] = xv[u].get(j) + (a.residual ? rv[u].get(j) : 0.0f);
+        ss[0] = fmaf(s[u][j], s[u][j], ss[0]);
+      }
+      if (a.sum) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) rv[u].set(j, s[u][j]);
+        rv[u].store(static_cast<S*>(a.sum) + row * a.dim + c);
+      }
+    }
+  }
+  row_reduce<false, 1>(ss, nt, part[0]);
+  const float inv = rsqrtf(ss[0] / (float)a.dim + a.eps);
+  float top[1] = {0.0f};
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int c = ((int)threadIdx.x + nt * u) * W;
+    if (live && c < a.dim) {
+      float w[W];
+      load_weight<W>(a.weight + c, w);
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        s[u][j] = s[u][j] * inv * w[j];
+        if (F8) top[0] = max_nan(top[0], fabsf(s[u][j]));
+      }
+      if (!F8) {
+        Unit<T, W> o;
+#pragma unroll
+        for (int j = 0; j < W; ++j) o.set(j, s[u][j]);
+        o.store(static_cast<T*>(a.out) + row * a.dim + c);
+      }
+    }
+  }
+  if (F8) {
+    row_reduce<true, 1>(top, nt, part[1]);
+    const float scale = top[0] == 0.0f ? 1.0f : top[0] / kMax8, rs = 1.0f / scale;
+    if (!live) return;
+    if (threadIdx.x == 0) a.scale[row] = scale;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = ((int)threadIdx.x + nt * u) * W;
+      if (c < a.dim) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) s[u][j] *= rs;
+        store8<W>(static_cast<__nv_fp8_storage_t*>(a.out) + row * a.dim + c, s[u]);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ backward
+
+// CTAs walk the rows; a thread's columns are the same in every row, so it adds up its share of dweight in registers.
+// The CTA's row groups add theirs in order through shared memory, and the CTA writes one row of partial sums.
+template <typename T, typename S, int W>
+__global__ void __launch_bounds__(kMaxThreads)
+add_norm_bwd_kernel(const AddNormBwdArgs a, const int nt) {
+  constexpr int U = held_by_thread(W, sizeof(S), true) / W;
+  __shared__ float part[2][kMaxThreads / 32][2];
+  extern __shared__ float columns[];  // [dim], with more than one row to a CTA
+  wait_for_inputs();
+  float acc[U][W];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int j = 0; j < W; ++j) acc[u][j] = 0.0f;
+  const int64_t step = (int64_t)gridDim.x * blockDim.y;
+  int turn = 0;
+  for (int64_t row0 = (int64_t)blockIdx.x * blockDim.y; row0 < a.rows; row0 += step) {
+    const int64_t row = row0 + threadIdx.y, base = row * a.dim;
+    const bool live = row < a.rows;
+    Unit<S, W> sv[U], dv[U];
+    Unit<T, W> gv[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = ((int)threadIdx.x + nt * u) * W;
+      if (live && c < a.dim) {
+        sv[u].load(static_cast<const S*>(a.sum) + base + c);
+        gv[u].load(static_cast<const T*>(a.dy) + base + c);
+        if (a.dsum) dv[u].load(static_cast<const S*>(a.dsum) + base + c);
+      }
+    }
+    float sums[2] = {0.0f, 0.0f};  // of s^2, and of s weight dy
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = ((int)threadIdx.x + nt * u) * W;
+      if (live && c < a.dim) {
+        float w[W];
+        load_weight<W>(a.weight + c, w);
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          const float v = sv[u].get(j);
+          sums[0] = fmaf(v, v, sums[0]);
+          sums[1] = fmaf(v, w[j] * gv[u].get(j), sums[1]);
+        }
+      }
+    }
+    row_reduce<false, 2>(sums, nt, part[turn ^= 1]);
+    const float inv = rsqrtf(sums[0] / (float)a.dim + a.eps);
+    const float k = inv * inv * (sums[1] / (float)a.dim);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = ((int)threadIdx.x + nt * u) * W;
+      if (live && c < a.dim) {
+        float w[W], d[W];
+        load_weight<W>(a.weight + c, w);
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          const float v = sv[u].get(j), g = gv[u].get(j);
+          d[j] = inv * (w[j] * g - v * k);
+          if (a.dsum) d[j] += dv[u].get(j);
+          acc[u][j] = fmaf(g * v, inv, acc[u][j]);
+        }
+        if (a.dx) {
+#pragma unroll
+          for (int j = 0; j < W; ++j) gv[u].set(j, d[j]);
+          gv[u].store(static_cast<T*>(a.dx) + base + c);
+        }
+        if (a.dresidual) {
+#pragma unroll
+          for (int j = 0; j < W; ++j) sv[u].set(j, d[j]);
+          sv[u].store(static_cast<S*>(a.dresidual) + base + c);
+        }
+      }
+    }
+  }
+  if (!a.dweight) return;
+  for (int y = 0; y < (int)blockDim.y; ++y) {
+    if ((int)threadIdx.y == y) {
+      const bool last = y == (int)blockDim.y - 1;
+      float* out = last ? a.partial + (int64_t)blockIdx.x * a.dim : columns;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int c = ((int)threadIdx.x + nt * u) * W;
+        if (c < a.dim)
+#pragma unroll
+          for (int j = 0; j < W; ++j) out[c + j] = (y > 0 ? columns[c + j] : 0.0f) + acc[u][j];
+      }
+    }
+    if (blockDim.y > 1) __syncthreads();
+  }
+}
+
+// dst[i] = sum of part[.][i]: 32 columns a CTA, a warp for every 32nd row, then the warps' sums in order.
+__global__ void __launch_bounds__(1024) column_sum_kernel(float* dst, const float* part, int parts, int dim) {
+  __shared__ float sum[32][33];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, i = blockIdx.x * 32 + lane;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float s = 0.0f;
+  if (i < dim)
+    for (int p = w; p < parts; p += 32) s += part[(int64_t)p * dim + i];
+  sum[w][lane] = s;
+  __syncthreads();
+  s = sum[lane][w];  // column w of this CTA, the warps' sums in the lanes
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane == 0 && blockIdx.x * 32 + w < dim) dst[blockIdx.x * 32 + w] = s;
+}
+
+// ------------------------------------------------------------------ rows wider than a CTA holds
+
+__device__ __forceinline__ float block_reduce(float v, bool max) {
+  __shared__ float part[kCtaThreads / 32];
+  for (int o = 16; o > 0; o >>= 1) {
+    const float u = __shfl_xor_sync(0xffffffffu, v, o);
+    v = max ? max_nan(v, u) : v + u;
+  }
   __syncthreads();
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
   __syncthreads();
-  float s = 0.0f;
-  for (int i = 0; i < kThreads / 32; ++i) s = max_nan(s, part[i]);
-  return s;
+  v = part[0];
+  for (int i = 1; i < kCtaThreads / 32; ++i) v = max ? max_nan(v, part[i]) : v + part[i];
+  return v;
 }
 
 template <typename T, typename S, bool F8>
-__global__ void __launch_bounds__(kThreads) add_norm_kernel(const AddNormArgs a) {
+__global__ void __launch_bounds__(kCtaThreads) add_norm_streamed_kernel(const AddNormArgs a) {
   const int64_t base = (int64_t)blockIdx.x * a.dim;
   const T* x = static_cast<const T*>(a.x) + base;
   const S* r = a.residual ? static_cast<const S*>(a.residual) + base : nullptr;
-  extern __shared__ float srow[];  // the row's s when it fits
-  float ss = 0.0f;
   auto value = [&](int i) { return Act<T>::to_f(x[i]) + (r ? Act<S>::to_f(r[i]) : 0.0f); };
-  for (int i = threadIdx.x; i < a.dim; i += kThreads) ss = fmaf(value(i), value(i), ss);
-  const float inv = rsqrtf(block_sum(ss) / (float)a.dim + a.eps);
-  float top = 0.0f;
-  if (F8)
-    for (int i = threadIdx.x; i < a.dim; i += kThreads) top = max_nan(top, fabsf(value(i) * inv * a.weight[i]));
-  float scale = 1.0f;
+  float ss = 0.0f, top = 0.0f, scale = 1.0f;
+  for (int i = threadIdx.x; i < a.dim; i += kCtaThreads) ss = fmaf(value(i), value(i), ss);
+  const float inv = rsqrtf(block_reduce(ss, false) / (float)a.dim + a.eps);
   if (F8) {
-    top = block_max(top);
+    for (int i = threadIdx.x; i < a.dim; i += kCtaThreads) top = max_nan(top, fabsf(value(i) * inv * a.weight[i]));
+    top = block_reduce(top, true);
     if (!(top == 0.0f)) scale = top / kMax8;
     if (threadIdx.x == 0) a.scale[blockIdx.x] = scale;
   }
-  for (int i = threadIdx.x; i < a.dim; i += kThreads) {
+  for (int i = threadIdx.x; i < a.dim; i += kCtaThreads) {
     const float s = value(i), y = s * inv * a.weight[i];
-    if (F8) static_cast<__nv_fp8_e4m3*>(a.out)[base + i] = __nv_fp8_e4m3(y / scale);
+    if (F8) static_cast<__nv_fp8_storage_t*>(a.out)[base + i] = __nv_cvt_float_to_fp8(y / scale, __NV_SATFINITE, __NV_E4M3);
     else static_cast<T*>(a.out)[base + i] = Act<T>::from_f(y);
     if (a.sum) static_cast<S*>(a.sum)[base + i] = Act<S>::from_f(s);
   }
 }
 
 template <typename T, typename S>
-__global__ void __launch_bounds__(kThreads) add_norm_bwd_kernel(const AddNormBwdArgs a, int parts) {
+__global__ void __launch_bounds__(kCtaThreads) add_norm_bwd_streamed_kernel(const AddNormBwdArgs a, int parts) {
   for (int64_t row = blockIdx.x; row < a.rows; row += parts) {
     const int64_t base = row * a.dim;
     const T* dy = static_cast<const T*>(a.dy) + base;
     const S* s = static_cast<const S*>(a.sum) + base;
     float ss = 0.0f, sd = 0.0f;
-    for (int i = threadIdx.x; i < a.dim; i += kThreads) {
+    for (int i = threadIdx.x; i < a.dim; i += kCtaThreads) {
       const float v = Act<S>::to_f(s[i]);
       ss = fmaf(v, v, ss);
       sd = fmaf(v, a.weight[i] * Act<T>::to_f(dy[i]), sd);
     }
-    const float inv = rsqrtf(block_sum(ss) / (float)a.dim + a.eps);
-    const float c = inv * inv * (block_sum(sd) / (float)a.dim);
-    for (int i = threadIdx.x; i < a.dim; i += kThreads) {
+    const float inv = rsqrtf(block_reduce(ss, false) / (float)a.dim + a.eps);
+    const float c = inv * inv * (block_reduce(sd, false) / (float)a.dim);
+    for (int i = threadIdx.x; i < a.dim; i += kCtaThreads) {
       const float v = Act<S>::to_f(s[i]), g = Act<T>::to_f(dy[i]);
       float d = inv * (a.weight[i] * g - v * c);
       if (a.dsum) d += Act<S>::to_f(static_cast<const S*>(a.dsum)[base + i]);
@@ -93,12 +368,69 @@ __global__ void __launch_bounds__(kThreads) add_norm_bwd_kernel(const AddNormBwd
   }
 }
 
-__global__ void __launch_bounds__(kThreads) column_sum_kernel(float* dst, const float* part, int parts, int dim) {
-  const int i = blockIdx.x * kThreads + threadIdx.x;
-  if (i >= dim) return;
-  float s = 0.0f;
-  for (int p = 0; p < parts; ++p) s += part[(int64_t)p * dim + i];
-  dst[i] = s;
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 152;
+  return sms;
+}
+
+// Threads of a row, and rows of a CTA.
+struct Shape {
+  int nt, rows;
+};
+Shape shape(int64_t rows, int dim, int unit, int held) {
+  const int fewest = 32 * ((dim + 32 * held - 1) / (32 * held));
+  const int most = 32 * ((dim + 32 * unit - 1) / (32 * unit));
+  if (rows <= sm_count()) return {std::max(fewest, std::min(most, kCtaThreads)), 1};
+  return {fewest, std::max(1, kCtaThreads / fewest)};
+}
+int unit_of(int dim) { return dim % 8 == 0 ? 8 : dim % 2 == 0 ? 2 : 1; }
+
+cudaLaunchConfig_t config(int grid, dim3 block, size_t smem, cudaStream_t st, cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3((unsigned)grid);
+  c.blockDim = block;
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr->val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = attr;
+  c.numAttrs = 1;
+  return c;
+}
+
+template <typename T, typename S, bool F8>
+cudaError_t run_norm(const AddNormArgs& a, cudaStream_t st) {
+  const int unit = unit_of(a.dim), held = held_by_thread(unit, sizeof(S), false);
+  if (a.dim > kMaxThreads * held) {
+    add_norm_streamed_kernel<T, S, F8><<<a.rows, kCtaThreads, 0, st>>>(a);
+    return cudaGetLastError();
+  }
+  const Shape s = shape(a.rows, a.dim, unit, held);
+  cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t c = config((a.rows + s.rows - 1) / s.rows, dim3(s.nt, s.rows), 0, st, &attr);
+  if (unit == 8) return cudaLaunchKernelEx(&c, add_norm_kernel<T, S, F8, 8>, a, s.nt);
+  if (unit == 2) return cudaLaunchKernelEx(&c, add_norm_kernel<T, S, F8, 2>, a, s.nt);
+  return cudaLaunchKernelEx(&c, add_norm_kernel<T, S, F8, 1>, a, s.nt);
+}
+
+template <typename T, typename S>
+cudaError_t run_norm_bwd(const AddNormBwdArgs& a, int* used, cudaStream_t st) {
+  const int unit = unit_of(a.dim), held = held_by_thread(unit, sizeof(S), true);
+  const int most = add_rmsnorm_backward_parts(a.rows, a.dim);
+  if (a.dim > kMaxThreads * held) {
+    *used = most;
+    add_norm_bwd_streamed_kernel<T, S><<<most, kCtaThreads, 0, st>>>(a, most);
+    return cudaGetLastError();
+  }
+  const Shape s = shape(a.rows, a.dim, unit, held);
+  const int parts = *used = std::min(most, (a.rows + s.rows - 1) / s.rows);
+  cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t c = config(parts, dim3(s.nt, s.rows), s.rows > 1 ? (size_t)a.dim * 4 : 0, st, &attr);
+  if (unit == 8) return cudaLaunchKernelEx(&c, add_norm_bwd_kernel<T, S, 8>, a, s.nt);
+  if (unit == 2) return cudaLaunchKernelEx(&c, add_norm_bwd_kernel<T, S, 2>, a, s.nt);
+  return cudaLaunchKernelEx(&c, add_norm_bwd_kernel<T, S, 1>, a, s.nt);
 }
 
 }  // namespace
@@ -107,33 +439,28 @@ cudaError_t launch_add_rmsnorm(const AddNormArgs& a, mamba2_dtype act, mamba2_dt
                                cudaStream_t st) {
   using B = __nv_bfloat16;
   const bool f8 = out_type == MAMBA2_E4M3;
-  if (act == MAMBA2_F32) {
-    if (f8) add_norm_kernel<float, float, true><<<a.rows, kThreads, 0, st>>>(a);
-    else add_norm_kernel<float, float, false><<<a.rows, kThreads, 0, st>>>(a);
-  } else if (sum_type == MAMBA2_F32) {
-    if (f8) add_norm_kernel<B, float, true><<<a.rows, kThreads, 0, st>>>(a);
-    else add_norm_kernel<B, float, false><<<a.rows, kThreads, 0, st>>>(a);
-  } else {
-    if (f8) add_norm_kernel<B, B, true><<<a.rows, kThreads, 0, st>>>(a);
-    else add_norm_kernel<B, B, false><<<a.rows, kThreads, 0, st>>>(a);
-  }
-  return cudaGetLastError();
+  if (act == MAMBA2_F32) return f8 ? run_norm<float, float, true>(a, st) : run_norm<float, float, false>(a, st);
+  if (sum_type == MAMBA2_F32) return f8 ? run_norm<B, float, true>(a, st) : run_norm<B, float, false>(a, st);
+  return f8 ? run_norm<B, B, true>(a, st) : run_norm<B, B, false>(a, st);
 }
 
-int add_rmsnorm_backward_parts(int32_t rows, int32_t) { return rows < 304 ? rows : 304; }
+// CTAs of the backward kernel at most (each writes one row of partial sums): two to an SM.
+int add_rmsnorm_backward_parts(int32_t rows, int32_t) { return (int)std::min<int64_t>(rows, 2 * (int64_t)sm_count()); }
 
 cudaError_t launch_add_rmsnorm_backward(const AddNormBwdArgs& a, mamba2_dtype act, mamba2_dtype sum_type,
                                         cudaStream_t st) {
   using B = __nv_bfloat16;
-  const int parts = add_rmsnorm_backward_parts(a.rows, a.dim);
-  if (parts > 0) {
-    if (act == MAMBA2_F32) add_norm_bwd_kernel<float, float><<<parts, kThreads, 0, st>>>(a, parts);
-    else if (sum_type == MAMBA2_F32) add_norm_bwd_kernel<B, float><<<parts, kThreads, 0, st>>>(a, parts);
-    else add_norm_bwd_kernel<B, B><<<parts, kThreads, 0, st>>>(a, parts);
+  int parts = 0;
+  cudaError_t e = cudaSuccess;
+  if (a.rows > 0) {
+    if (act == MAMBA2_F32) e = run_norm_bwd<float, float>(a, &parts, st);
+    else if (sum_type == MAMBA2_F32) e = run_norm_bwd<B, float>(a, &parts, st);
+    else e = run_norm_bwd<B, B>(a, &parts, st);
   }
-  if (a.dweight)
-    column_sum_kernel<<<(a.dim + kThreads - 1) / kThreads, kThreads, 0, st>>>(a.dweight, a.partial, parts, a.dim);
-  return cudaGetLastError();
+  if (e != cudaSuccess || !a.dweight) return e;
+  cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t c = config((a.dim + 31) / 32, dim3(1024), 0, st, &attr);
+  return cudaLaunchKernelEx(&c, column_sum_kernel, a.dweight, (const float*)a.partial, parts, (int)a.dim);
 }
 
 }  // namespace mamba2
