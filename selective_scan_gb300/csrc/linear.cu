@@ -414,6 +414,152 @@ pair_kernel(const __grid_constant__ Product g, const __grid_constant__ CUtensorM
   if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" :: "r"(tmem));
 }
 
+// ------------------------------------------------------------------ few rows
+
+// The product transposed: a tile is 128 rows of w by kN tokens, so a weight of few tokens is read at the
+// rate of memory without 256 rows of output to fill. A cluster of CTAs shares a tile, each over its part of
+// the K axis; they leave their fp32 parts in shared memory, and each then adds up every S-th token's parts in
+// the order of the ranks (over distributed shared memory) and finishes those rows of the output.
+template <int kN>
+struct Few {
+  static constexpr uint32_t kTileW = 128 * kRowBytes, kTileX = kN * kRowBytes, kStage = kTileW + kTileX;
+  // two CTAs to an SM
+  static constexpr int kStages = (int)(110u * 1024u / kStage) > 6 ? 6 : (int)(110u * 1024u / kStage);
+  static constexpr uint32_t kOffBar = kStages * kStage;
+  enum Bar : int { kFull = 0, kEmpty = kStages, kDone = 2 * kStages, kNumBars = 2 * kStages + 1 };
+  static constexpr uint32_t kOffMisc = kOffBar + 8 * kNumBars;
+  static constexpr uint32_t kSmem = kOffMisc + 16 + 1024;
+  static constexpr uint32_t kCols = kN < 32 ? 32 : kN;
+  static_assert(kN * 128 * 4 <= (int)kOffBar, "the parts take the place of the stages");
+};
+constexpr int kFewThreads = 256;
+
+template <bool F8>
+__device__ __forceinline__ void mma_one(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  if constexpr (F8)
+    asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\ntcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
+                 :: "r"(d), "l"(a), "l"(b), "r"(id), "r"(acc));
+  else
+    mma_ss(d, a, b, id, acc);
+}
+
+template <bool F8, int kN, typename TO>
+__global__ void __launch_bounds__(kFewThreads, 2)
+few_rows_kernel(const __grid_constant__ Product g, const __grid_constant__ CUtensorMap tmw,
+                const __grid_constant__ CUtensorMap tmx) {
+  using L = Few<kN>;
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw_base = su32(smem_raw);
+  unsigned char* smem = smem_raw + (((raw_base + 1023u) & ~1023u) - raw_base);
+  const uint32_t sbase = su32(smem);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
+  volatile uint32_t* s_abort = reinterpret_cast<volatile uint32_t*>(smem + L::kOffMisc + 4);
+  auto bar = [&](int id) { return sbase + L::kOffBar + 8u * (uint32_t)id; };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int depth = F8 ? 128 : 64;
+  const int kblocks = (g.K + depth - 1) / depth, S = (int)gridDim.x, rank = (int)blockIdx.x;
+  const int kb0 = (int)((int64_t)kblocks * rank / S), n_kb = (int)((int64_t)kblocks * (rank + 1) / S) - kb0;
+  const int n0 = (int)blockIdx.y * 128, m0 = (int)blockIdx.z * kN;
+
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(su32(s_tmem)), "n"(L::kCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  if (threadIdx.x == 32) {
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(bar(L::kFull + s), 1);
+      mbar_init(bar(L::kEmpty + s), 1);
+    }
+    mbar_init(bar(L::kDone), 1);
+    *s_abort = 0u;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched as a programmatic dependent
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int issued = 0;
+      for (int i = 0; i < n_kb; ++i) {
+        const int s = i % L::kStages;
+        if (i >= L::kStages && !wait_bar(bar(L::kEmpty + s), (uint32_t)((i / L::kStages - 1) & 1), s_abort)) break;
+        const uint32_t dst = sbase + (uint32_t)s * L::kStage;
+        mbar_expect_tx(bar(L::kFull + s), L::kStage);
+        tma_load_2d(dst, &tmw, (kb0 + i) * depth, n0, bar(L::kFull + s));
+        tma_load_2d(dst + L::kTileW, &tmx, (kb0 + i) * depth, m0, bar(L::kFull + s));
+        issued = i + 1;
+      }
+      if (*s_abort)
+        for (int i = max(0, issued - L::kStages); i < issued; ++i)
+          drain_bar(bar(L::kFull + i % L::kStages), (uint32_t)((i / L::kStages) & 1));
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t id = idesc(F8, 128, kN, false, false);
+      for (int i = 0; i < n_kb; ++i) {
+        const int s = i % L::kStages;
+        if (!wait_bar(bar(L::kFull + s), (uint32_t)((i / L::kStages) & 1), s_abort)) break;
+        tc_fence_after();
+        const uint32_t a0 = sbase + (uint32_t)s * L::kStage;
+        const uint64_t ad = operand<false, depth>(a0), bd = operand<false, depth>(a0 + L::kTileW);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_one<F8>(tmem, ad + k_step<false>(k), bd + k_step<false>(k), id, (i > 0 || k > 0) ? 1u : 0u);
+        mma_commit(bar(L::kEmpty + s));
+      }
+      mma_commit(bar(L::kDone));
+    }
+  }
+  __syncwarp();
+  // ---- every product done, every stage read: the parts take the stages' place, [token][128 features]
+  float* part = reinterpret_cast<float*>(smem);
+  const bool done = warp_wait(bar(L::kDone), 0u, s_abort);
+  if (!done) drain_bar(bar(L::kDone), 0u);
+  tc_fence_after();
+  __syncthreads();
+  if (done && warp >= 4) {
+    const int q = warp & 3;
+#pragma unroll
+    for (int c = 0; c < kN; c += 16) {
+      float v[16];
+      tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c, v);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) part[(c + j) * 128 + q * 32 + lane] = v[j];
+    }
+  }
+  tc_fence_before();
+  cluster_sync();
+  {
+    const int col = n0 + 4 * lane;
+    const Columns cc = load_columns(g, col);
+    const int tokens = min(kN, g.M - m0);
+    for (int t = rank + S * warp; t < tokens; t += S * (kFewThreads / 32)) {
+      const int64_t row = m0 + t;
+      const typename Quad<TO>::Raw res = load_residual<TO>(g, row, col);
+      const float sm = g.scale_m ? g.scale_m[row] : 1.0f;
+      float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      const uint32_t at = su32(part + t * 128 + 4 * lane);
+      for (int r = 0; r < S; ++r) {
+        float u[4];
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(u[0]), "=f"(u[1]), "=f"(u[2]), "=f"(u[3]) : "r"(at_rank(at, (uint32_t)r)) : "memory");
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] += u[j];
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] *= sm;
+      finish<TO>(g, row, col, v, cc, res);
+    }
+  }
+  if (threadIdx.x == 0 && *s_abort) atomicAdd(&g_linear_timeouts, 1u);
+  __syncthreads();
+  cluster_sync();  // nobody reads this CTA's parts any more
+  if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "n"(L::kCols));
+}
+
 // ------------------------------------------------------------------ tensor maps
 
 using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -471,6 +617,52 @@ cudaError_t launch_pairs(const Product& g, const void* A, int64_t lda, const voi
   return cudaGetLastError();
 }
 
+// The most rows that the few-rows kernel takes: as long as the pairs' tiles would leave half of the SMs idle.
+int few_rows_most(const Product& g) {
+  const int64_t tiles = (int64_t)((g.M + kBM - 1) / kBM) * ((g.N + kBN - 1) / kBN);
+  return g.M <= 128 || 4 * tiles < sm_count() ? g.M : 0;
+}
+
+template <bool F8, int kN, typename TO>
+cudaError_t launch_few(const Product& g, const void* x, int64_t ldx, const void* w, cudaStream_t st) {
+  using L = Few<kN>;
+  CUtensorMap tmw, tmx;
+  if (!make_map(&tmw, w, g.N, g.K, g.K, 128, F8) || !make_map(&tmx, x, g.M, g.K, ldx, kN, F8)) return cudaErrorInvalidValue;
+  auto kernel = few_rows_kernel<F8, kN, TO>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kSmem);
+  if (e != cudaSuccess) return e;
+  const int tiles_w = (g.N + 127) / 128, tiles_x = (g.M + kN - 1) / kN;
+  const int kblocks = (g.K + (F8 ? 127 : 63)) / (F8 ? 128 : 64);
+  // as many parts of K as fill two CTAs an SM, each of two k-blocks at least
+  const int S = std::max(1, std::min({8, kblocks / 2, (int)(2 * (int64_t)sm_count() / ((int64_t)tiles_w * tiles_x))}));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)S, (unsigned)tiles_w, (unsigned)tiles_x);
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = L::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)S;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, g, tmw, tmx);
+}
+
+// out = x . w^T by the kernel that suits the number of rows.
+template <bool F8, typename TO>
+cudaError_t launch_forward(const Product& g, const void* x, int64_t ldx, const void* w, cudaStream_t st) {
+  if ((g.N + 127) / 128 <= 65535) {
+    if (g.M <= 16) return launch_few<F8, 16, TO>(g, x, ldx, w, st);
+    if (g.M <= 32) return launch_few<F8, 32, TO>(g, x, ldx, w, st);
+    if (g.M <= 64) return launch_few<F8, 64, TO>(g, x, ldx, w, st);
+    if (g.M <= few_rows_most(g)) return launch_few<F8, 128, TO>(g, x, ldx, w, st);
+  }
+  return launch_pairs<F8, false, false, TO>(g, x, ldx, w, g.K, st);
+}
+
 // ------------------------------------------------------------------ backward: dp and the bias
 
 constexpr int kEltThreads = 256;
@@ -520,11 +712,11 @@ cudaError_t launch_linear(const LinearArgs& a, mamba2_dtype in, mamba2_dtype out
                a.x_scale, a.w_scale, a.bias, act, 0};
   g.vec = quad_ok(a.out, a.ld_out, oe) && quad_ok(a.residual, a.ld_res, oe) && quad_ok(a.pre, a.out_f, 2);
   if (in == MAMBA2_BF16) {
-    if (out == MAMBA2_BF16) return launch_pairs<false, false, false, __nv_bfloat16>(g, a.x, a.ld_x, a.w, a.in_f, st);
-    return launch_pairs<false, false, false, float>(g, a.x, a.ld_x, a.w, a.in_f, st);
+    if (out == MAMBA2_BF16) return launch_forward<false, __nv_bfloat16>(g, a.x, a.ld_x, a.w, st);
+    return launch_forward<false, float>(g, a.x, a.ld_x, a.w, st);
   }
-  if (out == MAMBA2_BF16) return launch_pairs<true, false, false, __nv_bfloat16>(g, a.x, a.ld_x, a.w, a.in_f, st);
-  return launch_pairs<true, false, false, float>(g, a.x, a.ld_x, a.w, a.in_f, st);
+  if (out == MAMBA2_BF16) return launch_forward<true, __nv_bfloat16>(g, a.x, a.ld_x, a.w, st);
+  return launch_forward<true, float>(g, a.x, a.ld_x, a.w, st);
 }
 
 int linear_bias_parts(int32_t rows) { return (rows + kRowsPerPart - 1) / kRowsPerPart; }
