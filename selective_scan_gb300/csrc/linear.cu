@@ -35,11 +35,42 @@ namespace {
 
 #include "tc.cuh"
 
+// The flushing forms of the exponential and the reciprocal: what they flush is below 2^-126 (and the others scale
+// around that at several instructions each).
+__device__ __forceinline__ float exp2_ftz(float v) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v));
+  return e;
+}
+__device__ __forceinline__ float recip_ftz(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float sigmoid_ftz(float v) { return recip_ftz(1.0f + exp2_ftz(v * -kLog2e)); }
+
+// The normal distribution's tail 1 - Phi(|v|), and exp(-v^2 / 2), by Abramowitz and Stegun's formula 7.1.26 for
+// erfc (error at most 1.5e-7, and no branch, where erff has one).
+__device__ __forceinline__ void normal_tail(float v, float& tail, float& bell) {
+  const float x = fabsf(v) * 0.70710678118654752f, t = recip_ftz(fmaf(0.3275911f, x, 1.0f));
+  bell = exp2_ftz(x * x * -kLog2e);
+  float p = fmaf(t, 1.061405429f, -1.453152027f);
+  p = fmaf(t, p, 1.421413741f);
+  p = fmaf(t, p, -0.284496736f);
+  p = fmaf(t, p, 0.254829592f);
+  tail = 0.5f * t * p * bell;
+}
+__device__ __forceinline__ float gelu(float v) {
+  float tail, bell;
+  normal_tail(v, tail, bell);
+  return v * (v < 0.0f ? tail : 1.0f - tail);
+}
 __device__ __forceinline__ float activate(float v, int act) {
   switch (act) {
     case MAMBA2_ACT_RELU: return fmaxf(v, 0.0f);
-    case MAMBA2_ACT_SILU: return silu_f(v);
-    case MAMBA2_ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+    case MAMBA2_ACT_SILU: return v * sigmoid_ftz(v);
+    case MAMBA2_ACT_GELU: return gelu(v);
   }
   return v;
 }
@@ -47,11 +78,14 @@ __device__ __forceinline__ float slope(float v, int act) {
   switch (act) {
     case MAMBA2_ACT_RELU: return v > 0.0f ? 1.0f : 0.0f;
     case MAMBA2_ACT_SILU: {
-      const float p = __fdividef(1.0f, 1.0f + __expf(-v));
+      const float p = sigmoid_ftz(v);
       return p * fmaf(v, 1.0f - p, 1.0f);
     }
-    case MAMBA2_ACT_GELU:
-      return fmaf(v * 0.39894228040143268f, __expf(-0.5f * v * v), 0.5f * (1.0f + erff(v * 0.70710678118654752f)));
+    case MAMBA2_ACT_GELU: {
+      float tail, bell;
+      normal_tail(v, tail, bell);
+      return fmaf(v * 0.39894228040143268f, bell, v < 0.0f ? tail : 1.0f - tail);
+    }
   }
   return 1.0f;
 }
@@ -104,6 +138,12 @@ struct Columns {
 };
 __device__ __forceinline__ Columns load_columns(const Product& g, int col) {
   Columns c;
+  if (col + 4 <= g.N) {  // (col is a multiple of four, and both vectors are 16-byte aligned)
+    const float4 one = make_float4(1.0f, 1.0f, 1.0f, 1.0f), none = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const float4 sc = g.scale_n ? __ldg(reinterpret_cast<const float4*>(g.scale_n + col)) : one;
+    const float4 bi = g.bias ? __ldg(reinterpret_cast<const float4*>(g.bias + col)) : none;
+    return {{sc.x, sc.y, sc.z, sc.w}, {bi.x, bi.y, bi.z, bi.w}};
+  }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const bool in = col + j < g.N;
@@ -368,9 +408,28 @@ pair_kernel(const __grid_constant__ Product g, const __grid_constant__ CUtensorM
     const int q = warp & 3, half = (warp - 2) >> 2;
     const uint32_t lane_off = (uint32_t)(q * 32) << 16;
     float* blk = reinterpret_cast<float*>(smem + kOffEpi + (uint32_t)(warp - 2) * kEpiBytes);
+    // what a chunk of 32 columns needs from global memory is fetched a chunk ahead, across tiles: waited for in
+    // its place, it took the epilogue to 15 us a tile (with SiLU and a residual), where 32 k-blocks take 9
+    struct Chunk {
+      typename Quad<TO>::Raw res[8];
+      Columns cols;
+    };
+    auto first_row = [&](int t) { return (int64_t)tile_m0(t) + (int)rank * 128 + q * 32; };
+    auto fetch = [&](int t, int c, Chunk& k) {
+      const int col = tile_n0(t) + half * 128 + c + 4 * (lane & 7);
+      const int64_t row = first_row(t) + (lane >> 3);
+      k.cols = load_columns(g, col);
+      if (!g.residual || !g.vec || col + 4 > g.N) return;
+      const TO* p = static_cast<const TO*>(g.residual) + row * g.ld_res + col;
+#pragma unroll
+      for (int i = 0; i < 8; ++i, p += 4 * g.ld_res)
+        if (row + 4 * i < g.M) k.res[i] = *reinterpret_cast<const typename Quad<TO>::Raw*>(p);
+    };
+    Chunk now;
+    if (my_tiles > 0) fetch(0, 0, now);
     for (int t = 0; t < my_tiles; ++t) {
       const int buf = t & 1;
-      const int64_t row0 = (int64_t)tile_m0(t) + (int)rank * 128 + q * 32;
+      const int64_t row0 = first_row(t);
       const int n0 = tile_n0(t) + half * 128;
       const float sm = g.scale_m && row0 + lane < g.M ? g.scale_m[row0 + lane] : 1.0f;
       if (!warp_wait(bar(kAccFull + buf), (uint32_t)((t >> 1) & 1), s_abort)) break;
@@ -378,26 +437,70 @@ pair_kernel(const __grid_constant__ Product g, const __grid_constant__ CUtensorM
 #pragma unroll 1
       for (int c = 0; c < 128; c += 32) {
         const int col = n0 + c + 4 * (lane & 7);
-        if (n0 + c >= g.N || row0 >= g.M) break;  // the same for the whole warp
-        typename Quad<TO>::Raw res[8];
+        Chunk next;
+        if (c < 96) fetch(t, c + 32, next);
+        else if (t + 1 < my_tiles) fetch(t + 1, 0, next);
+        if (n0 + c < g.N && row0 < g.M) {  // the same for the whole warp
+          uint32_t r[32];
+          tmem_ld32(tmem + lane_off + (uint32_t)(buf * kBN + half * 128 + c), r);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) res[i] = load_residual<TO>(g, row0 + 4 * i + (lane >> 3), col);
-        const Columns cc = load_columns(g, col);
-        uint32_t r[32];
-        tmem_ld32(tmem + lane_off + (uint32_t)(buf * kBN + half * 128 + c), r);
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<float4*>(blk + lane * kEpiLd + 4 * j) =
+                make_float4(__uint_as_float(r[4 * j]) * sm, __uint_as_float(r[4 * j + 1]) * sm,
+                            __uint_as_float(r[4 * j + 2]) * sm, __uint_as_float(r[4 * j + 3]) * sm);
+          __syncwarp();
+          const float* mine = blk + (lane >> 3) * kEpiLd + 4 * (lane & 7);
+          const int64_t row = row0 + (lane >> 3);
+          if (g.vec && n0 + c + 32 <= g.N && row0 + 32 <= g.M) {
+            // the whole block: a step at a time over 32 values, so that the branches are the block's
+            float v[8][4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          *reinterpret_cast<float4*>(blk + lane * kEpiLd + 4 * j) =
-              make_float4(__uint_as_float(r[4 * j]) * sm, __uint_as_float(r[4 * j + 1]) * sm,
-                          __uint_as_float(r[4 * j + 2]) * sm, __uint_as_float(r[4 * j + 3]) * sm);
-        __syncwarp();
+            for (int i = 0; i < 8; ++i) {
+              const float4 f = *reinterpret_cast<const float4*>(mine + 4 * i * kEpiLd);
+              v[i][0] = fmaf(f.x, now.cols.scale[0], now.cols.bias[0]);
+              v[i][1] = fmaf(f.y, now.cols.scale[1], now.cols.bias[1]);
+              v[i][2] = fmaf(f.z, now.cols.scale[2], now.cols.bias[2]);
+              v[i][3] = fmaf(f.w, now.cols.scale[3], now.cols.bias[3]);
+            }
+            if (g.pre) {
+              __nv_bfloat16* p = g.pre + row * g.N + col;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float4 f = *reinterpret_cast<const float4*>(blk + (4 * i + (lane >> 3)) * kEpiLd + 4 * (lane & 7));
-          float v[4] = {f.x, f.y, f.z, f.w};
-          finish<TO>(g, row0 + 4 * i + (lane >> 3), col, v, cc, res[i]);
+              for (int i = 0; i < 8; ++i, p += 4 * (int64_t)g.N) *reinterpret_cast<uint2*>(p) = Quad<__nv_bfloat16>::pack(v[i]);
+            }
+            if (g.act == MAMBA2_ACT_SILU) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i / 4][i % 4] *= sigmoid_ftz(v[i / 4][i % 4]);
+            } else if (g.act == MAMBA2_ACT_GELU) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i / 4][i % 4] = gelu(v[i / 4][i % 4]);
+            } else if (g.act == MAMBA2_ACT_RELU) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i / 4][i % 4] = fmaxf(v[i / 4][i % 4], 0.0f);
+            }
+            if (g.residual) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                float r4[4];
+                Quad<TO>::unpack(now.res[i], r4);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[i][j] += r4[j];
+              }
+            }
+            TO* o = static_cast<TO*>(g.out) + row * g.ld_out + col;
+#pragma unroll
+            for (int i = 0; i < 8; ++i, o += 4 * g.ld_out)
+              *reinterpret_cast<typename Quad<TO>::Raw*>(o) = Quad<TO>::pack(v[i]);
+          } else {
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+              const float4 f = *reinterpret_cast<const float4*>(mine + 4 * i * kEpiLd);
+              float v[4] = {f.x, f.y, f.z, f.w};
+              finish<TO>(g, row + 4 * i, col, v, now.cols, load_residual<TO>(g, row + 4 * i, col));
+            }
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        now = next;
       }
       tc_fence_before();
       __syncwarp();
