@@ -458,9 +458,13 @@ cudaError_t launch_add_rmsnorm_backward(const AddNormBwdArgs& a, mamba2_dtype ac
     else e = run_norm_bwd<B, B>(a, &parts, st);
   }
   if (e != cudaSuccess || !a.dweight) return e;
+  return launch_column_sum(a.dweight, a.partial, parts, a.dim, st);
+}
+
+cudaError_t launch_column_sum(float* dst, const float* part, int parts, int dim, cudaStream_t st) {
   cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t c = config((a.dim + 31) / 32, dim3(1024), 0, st, &attr);
-  return cudaLaunchKernelEx(&c, column_sum_kernel, a.dweight, (const float*)a.partial, parts, (int)a.dim);
+  const cudaLaunchConfig_t c = config((dim + 31) / 32, dim3(1024), 0, st, &attr);
+  return cudaLaunchKernelEx(&c, column_sum_kernel, dst, part, parts, dim);
 }
 
 }  // namespace mamba2

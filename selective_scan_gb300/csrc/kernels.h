@@ -216,6 +216,9 @@ int add_rmsnorm_backward_parts(int32_t rows, int32_t dim);
 cudaError_t launch_add_rmsnorm_backward(const AddNormBwdArgs& a, mamba2_dtype act, mamba2_dtype sum_type,
                                         cudaStream_t st);
 
+// dst[i] = sum over p < parts of part[p][i], in a fixed order.
+cudaError_t launch_column_sum(float* dst, const float* part, int parts, int dim, cudaStream_t st);
+
 struct LinearArgs {
   void* out;
   void* pre;

@@ -284,10 +284,10 @@ __device__ __forceinline__ void commit_pair(uint32_t bar) {  // arrives at this 
 }
 
 // The operand's k-block kb, 128 of its rows (or columns) from r0 on, into dst.
-template <bool F8, bool mn>
-__device__ __forceinline__ void load_half(uint32_t dst, const CUtensorMap* tm, int kb, int r0, uint32_t bar) {
+template <bool F8>
+__device__ __forceinline__ void load_half(bool mn, uint32_t dst, const CUtensorMap* tm, int kb, int r0, uint32_t bar) {
   constexpr int depth = F8 ? 128 : 64;
-  if constexpr (mn) {
+  if (mn) {
     tma_load_pair(dst, tm, r0, kb * depth, bar);
     tma_load_pair(dst + kHalf / 2, tm, r0 + 64, kb * depth, bar);
   } else {
@@ -295,11 +295,31 @@ __device__ __forceinline__ void load_half(uint32_t dst, const CUtensorMap* tm, i
   }
 }
 
-template <bool F8, bool A_MN, bool B_MN, typename TO>
+// Both products of the backward pass in one launch (dw first: its tiles, over all rows, are the longer ones),
+// so that they fill the last round together: pair p takes every npairs-th tile of dw, and the tiles
+// [start[p], start[p + 1]) of dx.
+constexpr int kMaxPairs = 80;
+struct Split {
+  int start[kMaxPairs + 1];
+};
+template <bool kGrad>
+struct Job {
+  Product g[kGrad ? 2 : 1];
+  CUtensorMap a[kGrad ? 2 : 1], b[kGrad ? 2 : 1];
+  Split split;
+};
+template <>
+struct Job<false> {
+  Product g[1];
+  CUtensorMap a[1], b[1];
+};
+
+// kGrad: product 0 is dw (rows of both operands are K), product 1 dx (rows of the second are); else the only
+// product has K along the rows of both.
+template <bool F8, bool kGrad, typename TO>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-pair_kernel(const __grid_constant__ Product g, const __grid_constant__ CUtensorMap tma,
-            const __grid_constant__ CUtensorMap tmb) {
-  static_assert(!F8 || (!A_MN && !B_MN), "8-bit operands have K along the row");
+pair_kernel(const __grid_constant__ Job<kGrad> job) {
+  static_assert(!F8 || !kGrad, "8-bit operands have K along the row");
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw_base = su32(smem_raw);
   unsigned char* smem = smem_raw + (((raw_base + 1023u) & ~1023u) - raw_base);
@@ -312,13 +332,26 @@ pair_kernel(const __grid_constant__ Product g, const __grid_constant__ CUtensorM
   const bool leader = rank == 0;
 
   constexpr int depth = F8 ? 128 : 64;
-  const int tiles_n = (g.N + kBN - 1) / kBN;
-  const int tiles = (g.M + kBM - 1) / kBM * tiles_n;
-  const int kblocks = (g.K + depth - 1) / depth;
   const int pair = (int)blockIdx.x >> 1, npairs = (int)gridDim.x >> 1;
-  const int my_tiles = pair < tiles ? (tiles - 1 - pair) / npairs + 1 : 0;
-  auto tile_m0 = [&](int t) { return ((pair + t * npairs) / tiles_n) * kBM; };
-  auto tile_n0 = [&](int t) { return ((pair + t * npairs) % tiles_n) * kBN; };
+  // this pair's tiles: the first product's pair, + npairs, ..., then the second's range
+  const int tiles0 = (job.g[0].M + kBM - 1) / kBM * ((job.g[0].N + kBN - 1) / kBN);
+  const int mine0 = pair < tiles0 ? (tiles0 - 1 - pair) / npairs + 1 : 0;
+  int mine = mine0;
+  if constexpr (kGrad) mine += job.split.start[pair + 1] - job.split.start[pair];
+  struct Tile {
+    int which, m0, n0;
+  };
+  auto tile = [&](int t) -> Tile {  // N fastest
+    int which = 0, i = pair + t * npairs;
+    if constexpr (kGrad)
+      if (t >= mine0) {
+        which = 1;
+        i = job.split.start[pair] + t - mine0;
+      }
+    const int across = (job.g[which].N + kBN - 1) / kBN;
+    return {which, i / across * kBM, i % across * kBN};
+  };
+  auto kblocks = [&](int which) { return (job.g[which].K + depth - 1) / depth; };
 
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" :: "r"(su32(s_tmem)));
@@ -347,9 +380,10 @@ pair_kernel(const __grid_constant__ Product g, const __grid_constant__ CUtensorM
     // =================== TMA producer
     int it = 0, issued = 0;
     bool ok = true;
-    for (int t = 0; t < my_tiles && ok; ++t) {
-      const int m0 = tile_m0(t) + (int)rank * 128, n0 = tile_n0(t) + (int)rank * 128;
-      for (int kb = 0; kb < kblocks; ++kb, ++it) {
+    for (int t = 0; t < mine && ok; ++t) {
+      const Tile w = tile(t);
+      const int m0 = w.m0 + (int)rank * 128, n0 = w.n0 + (int)rank * 128, nkb = kblocks(w.which);
+      for (int kb = 0; kb < nkb; ++kb, ++it) {
         const int s = it % kStages;
         if (it >= kStages && !warp_wait(bar(kEmpty + s), (uint32_t)(((it / kStages) - 1) & 1), s_abort)) {
           ok = false;
@@ -359,8 +393,8 @@ pair_kernel(const __grid_constant__ Product g, const __grid_constant__ CUtensorM
           const uint32_t dst = sbase + (uint32_t)s * kStage;
           const uint32_t full = at_rank(bar(kFull + s), 0);
           if (leader) mbar_expect_tx(bar(kFull + s), 2 * kStage);
-          load_half<F8, A_MN>(dst, &tma, kb, m0, full);
-          load_half<F8, B_MN>(dst + kHalf, &tmb, kb, n0, full);
+          load_half<F8>(kGrad && w.which == 0, dst, &job.a[w.which], kb, m0, full);
+          load_half<F8>(kGrad, dst + kHalf, &job.b[w.which], kb, n0, full);
         }
         __syncwarp();
         issued = it + 1;
@@ -373,15 +407,18 @@ pair_kernel(const __grid_constant__ Product g, const __grid_constant__ CUtensorM
   } else if (warp == 1) {
     // =================== MMA issuer
     if (leader && lane == 0) {
-      constexpr uint32_t id = idesc(F8, kBM, kBN, A_MN, B_MN);
       int it = 0;
       bool ok = true;
-      for (int t = 0; t < my_tiles && ok; ++t) {
+      for (int t = 0; t < mine && ok; ++t) {
         const int buf = t & 1;
         if (t >= 2 && !wait_bar(bar(kAccEmpty + buf), (uint32_t)(((t >> 1) - 1) & 1), s_abort)) break;
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(buf * kBN);
-        for (int kb = 0; kb < kblocks; ++kb, ++it) {
+        const int which = tile(t).which, nkb = kblocks(which);
+        const bool a_mn = kGrad && which == 0;
+        const uint32_t id = a_mn ? idesc(F8, kBM, kBN, true, kGrad) : idesc(F8, kBM, kBN, false, kGrad);
+        const uint64_t step = a_mn ? k_step<true>(1) : k_step<false>(1);
+        for (int kb = 0; kb < nkb; ++kb, ++it) {
           const int s = it % kStages;
           if (!wait_bar(bar(kFull + s), (uint32_t)((it / kStages) & 1), s_abort)) {
             ok = false;
@@ -389,10 +426,11 @@ pair_kernel(const __grid_constant__ Product g, const __grid_constant__ CUtensorM
           }
           tc_fence_after();
           const uint32_t a0 = sbase + (uint32_t)s * kStage;
-          const uint64_t ad = operand<A_MN, depth>(a0), bd = operand<B_MN, depth>(a0 + kHalf);
+          const uint64_t ad = a_mn ? operand<true, depth>(a0) : operand<false, depth>(a0);
+          const uint64_t bd = operand<kGrad, depth>(a0 + kHalf);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_pair<F8>(d, ad + k_step<A_MN>(k), bd + k_step<B_MN>(k), id, (kb > 0 || k > 0) ? 1u : 0u);
+            mma_pair<F8>(d, ad + (uint64_t)k * step, bd + k_step<kGrad>(k), id, (kb > 0 || k > 0) ? 1u : 0u);
           commit_pair(bar(kEmpty + s));
         }
         if (!ok) break;
@@ -414,10 +452,10 @@ pair_kernel(const __grid_constant__ Product g, const __grid_constant__ CUtensorM
       typename Quad<TO>::Raw res[8];
       Columns cols;
     };
-    auto first_row = [&](int t) { return (int64_t)tile_m0(t) + (int)rank * 128 + q * 32; };
-    auto fetch = [&](int t, int c, Chunk& k) {
-      const int col = tile_n0(t) + half * 128 + c + 4 * (lane & 7);
-      const int64_t row = first_row(t) + (lane >> 3);
+    auto fetch = [&](const Tile& w, int c, Chunk& k) {
+      const Product& g = job.g[w.which];
+      const int col = w.n0 + half * 128 + c + 4 * (lane & 7);
+      const int64_t row = (int64_t)w.m0 + (int)rank * 128 + q * 32 + (lane >> 3);
       k.cols = load_columns(g, col);
       if (!g.residual || !g.vec || col + 4 > g.N) return;
       const TO* p = static_cast<const TO*>(g.residual) + row * g.ld_res + col;
@@ -426,11 +464,14 @@ pair_kernel(const __grid_constant__ Product g, const __grid_constant__ CUtensorM
         if (row + 4 * i < g.M) k.res[i] = *reinterpret_cast<const typename Quad<TO>::Raw*>(p);
     };
     Chunk now;
-    if (my_tiles > 0) fetch(0, 0, now);
-    for (int t = 0; t < my_tiles; ++t) {
+    Tile at = tile(0);
+    if (mine > 0) fetch(at, 0, now);
+    for (int t = 0; t < mine; ++t) {
       const int buf = t & 1;
-      const int64_t row0 = first_row(t);
-      const int n0 = tile_n0(t) + half * 128;
+      const Product& g = job.g[at.which];
+      const int64_t row0 = (int64_t)at.m0 + (int)rank * 128 + q * 32;
+      const int n0 = at.n0 + half * 128;
+      const Tile after = tile(min(t + 1, mine - 1));
       const float sm = g.scale_m && row0 + lane < g.M ? g.scale_m[row0 + lane] : 1.0f;
       if (!warp_wait(bar(kAccFull + buf), (uint32_t)((t >> 1) & 1), s_abort)) break;
       tc_fence_after();
@@ -438,8 +479,8 @@ pair_kernel(const __grid_constant__ Product g, const __grid_constant__ CUtensorM
       for (int c = 0; c < 128; c += 32) {
         const int col = n0 + c + 4 * (lane & 7);
         Chunk next;
-        if (c < 96) fetch(t, c + 32, next);
-        else if (t + 1 < my_tiles) fetch(t + 1, 0, next);
+        if (c < 96) fetch(at, c + 32, next);
+        else fetch(after, 0, next);
         if (n0 + c < g.N && row0 < g.M) {  // the same for the whole warp
           uint32_t r[32];
           tmem_ld32(tmem + lane_off + (uint32_t)(buf * kBN + half * 128 + c), r);
@@ -507,6 +548,7 @@ pair_kernel(const __grid_constant__ Product g, const __grid_constant__ CUtensorM
       if (lane == 0)
         asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
                      :: "r"(at_rank(bar(kAccEmpty + buf), 0)) : "memory");
+      at = after;
     }
   }
 
@@ -703,26 +745,34 @@ int sm_count() {
   return sms;
 }
 
-template <bool F8, bool A_MN, bool B_MN, typename TO>
-cudaError_t launch_pairs(const Product& g, const void* A, int64_t lda, const void* B, int64_t ldb, cudaStream_t st) {
-  CUtensorMap tma, tmb;
-  constexpr int depth = F8 ? 128 : 64;
-  if (!(A_MN ? make_map(&tma, A, g.K, g.M, lda, depth, F8) : make_map(&tma, A, g.M, g.K, lda, 128, F8)) ||
-      !(B_MN ? make_map(&tmb, B, g.K, g.N, ldb, depth, F8) : make_map(&tmb, B, g.N, g.K, ldb, 128, F8)))
-    return cudaErrorInvalidValue;
-  auto kernel = pair_kernel<F8, A_MN, B_MN, TO>;
+int64_t pair_tiles(const Product& g) { return (int64_t)((g.M + kBM - 1) / kBM) * ((g.N + kBN - 1) / kBN); }
+
+template <bool F8, bool kGrad, typename TO>
+cudaError_t start_pairs(const Job<kGrad>& job, int pairs, cudaStream_t st) {
+  auto kernel = pair_kernel<F8, kGrad, TO>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = (int64_t)((g.M + kBM - 1) / kBM) * ((g.N + kBN - 1) / kBN);
-  if (tiles > 0x3fffffff) return cudaErrorInvalidValue;
-  const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, sm_count() / 2));
-  kernel<<<2 * pairs, kThreads, kSmem, st>>>(g, tma, tmb);
+  kernel<<<2 * pairs, kThreads, kSmem, st>>>(job);
   return cudaGetLastError();
+}
+int pair_count(int64_t tiles) {
+  return (int)std::max<int64_t>(1, std::min<int64_t>({tiles, (int64_t)sm_count() / 2, (int64_t)kMaxPairs}));
+}
+
+template <bool F8, typename TO>
+cudaError_t launch_pairs(const Product& g, const void* x, int64_t ldx, const void* w, cudaStream_t st) {
+  Job<false> job = {};
+  job.g[0] = g;
+  if (!make_map(&job.a[0], x, g.M, g.K, ldx, 128, F8) || !make_map(&job.b[0], w, g.N, g.K, g.K, 128, F8))
+    return cudaErrorInvalidValue;
+  const int64_t tiles = pair_tiles(g);
+  if (tiles > 0x3fffffff) return cudaErrorInvalidValue;
+  return start_pairs<F8, false, TO>(job, pair_count(tiles), st);
 }
 
 // The most rows that the few-rows kernel takes: as long as the pairs' tiles would leave half of the SMs idle.
 int few_rows_most(const Product& g) {
-  const int64_t tiles = (int64_t)((g.M + kBM - 1) / kBM) * ((g.N + kBN - 1) / kBN);
+  const int64_t tiles = pair_tiles(g);
   return g.M <= 128 || 4 * tiles < sm_count() ? g.M : 0;
 }
 
@@ -763,38 +813,75 @@ cudaError_t launch_forward(const Product& g, const void* x, int64_t ldx, const v
     if (g.M <= 64) return launch_few<F8, 64, TO>(g, x, ldx, w, st);
     if (g.M <= few_rows_most(g)) return launch_few<F8, 128, TO>(g, x, ldx, w, st);
   }
-  return launch_pairs<F8, false, false, TO>(g, x, ldx, w, g.K, st);
+  return launch_pairs<F8, TO>(g, x, ldx, w, st);
 }
 
 // ------------------------------------------------------------------ backward: dp and the bias
 
-constexpr int kEltThreads = 256;
-constexpr int kRowsPerPart = 64;
+// dp = dy * activation'(pre) rounded to bf16, and the column sums of each kPartRows rows, unrounded. A CTA takes
+// 256 columns of them, a warp every eighth row, a lane 8 columns: adjacent ones where rows are 16-byte aligned,
+// else every 32nd. Bound by HBM: dy and pre in, dp out.
+constexpr int kPartRows = 64;
+constexpr int kPartCols = 256;
 
-// dp = dy * activation'(pre) in bf16, and the column sums of each kRowsPerPart rows
-__global__ void __launch_bounds__(kEltThreads) dp_kernel(const LinearBwdArgs a, int act) {
-  const int n = blockIdx.x * kEltThreads + threadIdx.x;
-  if (n >= a.ld_dp) return;
-  const int m1 = min(a.rows, (int)(blockIdx.y + 1) * kRowsPerPart);
-  float s = 0.0f;
-  for (int m = blockIdx.y * kRowsPerPart; m < m1; ++m) {
-    float v = 0.0f;
-    if (n < a.out_f) {
-      v = __bfloat162float(static_cast<const __nv_bfloat16*>(a.dy)[(int64_t)m * a.out_f + n]);
-      if (act) v *= slope(__bfloat162float(static_cast<const __nv_bfloat16*>(a.pre)[(int64_t)m * a.out_f + n]), act);
+template <bool kVec>
+__global__ void __launch_bounds__(256) dp_kernel(const LinearBwdArgs a, const int act) {
+  __shared__ float sums[8][kPartCols];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c0 = blockIdx.y * kPartCols;
+  const int64_t m0 = (int64_t)blockIdx.x * kPartRows;
+  auto col = [&](int j) { return c0 + (kVec ? 8 * lane + j : lane + 32 * j); };
+  float s[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s[j] = 0.0f;
+  const __nv_bfloat16* dy = static_cast<const __nv_bfloat16*>(a.dy);
+  const __nv_bfloat16* pre = static_cast<const __nv_bfloat16*>(a.pre);
+  if (!kVec || col(0) < a.out_f) {
+#pragma unroll 4
+    for (int i = 0; i < kPartRows / 8; ++i) {
+      const int64_t m = m0 + 8 * i + warp;
+      if (m >= a.rows) break;
+      float v[8], p[8];
+      const int64_t at = m * a.out_f;
+      if constexpr (kVec) {
+        Vec16<__nv_bfloat16>::load_stream(dy + at + col(0), v);
+        if (act) Vec16<__nv_bfloat16>::load_stream(pre + at + col(0), p);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          v[j] = col(j) < a.out_f ? __bfloat162float(dy[at + col(j)]) : 0.0f;
+          p[j] = act && col(j) < a.out_f ? __bfloat162float(pre[at + col(j)]) : 0.0f;
+        }
+      }
+      if (act) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= slope(p[j], act);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] += v[j];
+      if (a.dp) {
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.dp) + m * a.ld_dp;
+        if constexpr (kVec) {
+          Vec16<__nv_bfloat16>::store(o + col(0), v);  // (the products read it next, from L2 as far as it holds)
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (col(j) < a.ld_dp) o[col(j)] = __float2bfloat16_rn(v[j]);
+        }
+      }
     }
-    s += v;
-    static_cast<__nv_bfloat16*>(a.dp)[m * a.ld_dp + n] = __float2bfloat16_rn(v);
   }
-  if (n < a.out_f) a.partial[(int64_t)blockIdx.y * a.out_f + n] = s;
-}
-
-__global__ void __launch_bounds__(kEltThreads) bias_sum_kernel(float* dst, const float* part, int parts, int n) {
-  const int i = blockIdx.x * kEltThreads + threadIdx.x;
-  if (i >= n) return;
-  float s = 0.0f;
-  for (int p = 0; p < parts; ++p) s += part[(int64_t)p * n + i];
-  dst[i] = s;
+  if (!a.dbias) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sums[warp][col(j) - c0] = s[j];
+  __syncthreads();
+  const int c = c0 + (int)threadIdx.x;
+  if (c < a.out_f) {
+    float t = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) t += sums[w][threadIdx.x];
+    a.partial[(int64_t)blockIdx.x * a.out_f + c] = t;
+  }
 }
 
 bool quad_ok(const void* p, int64_t ld, size_t elem) {
@@ -822,38 +909,79 @@ cudaError_t launch_linear(const LinearArgs& a, mamba2_dtype in, mamba2_dtype out
   return launch_forward<true, float>(g, a.x, a.ld_x, a.w, st);
 }
 
-int linear_bias_parts(int32_t rows) { return (rows + kRowsPerPart - 1) / kRowsPerPart; }
+int linear_bias_parts(int32_t rows) { return (rows + kPartRows - 1) / kPartRows; }
 
-cudaError_t launch_linear_backward(const LinearBwdArgs& a, int act, cudaStream_t st) {
+cudaError_t launch_linear_backward(const LinearBwdArgs& args, int act, cudaStream_t st) {
+  LinearBwdArgs a = args;
   if (a.rows == 0) {
     cudaError_t e = a.dw ? cudaMemsetAsync(a.dw, 0, (size_t)a.out_f * a.in_f * 2, st) : cudaSuccess;
     if (e == cudaSuccess && a.dbias) e = cudaMemsetAsync(a.dbias, 0, (size_t)a.out_f * 4, st);
     return e;
   }
   const int parts = linear_bias_parts(a.rows);
-  dp_kernel<<<dim3((unsigned)((a.ld_dp + kEltThreads - 1) / kEltThreads), parts), kEltThreads, 0, st>>>(a, act);
-  cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess && a.dbias) {
-    bias_sum_kernel<<<(a.out_f + kEltThreads - 1) / kEltThreads, kEltThreads, 0, st>>>(a.dbias, a.partial, parts, a.out_f);
-    e = cudaGetLastError();
+  const void* dp = a.dp;
+  if (act == MAMBA2_ACT_NONE && a.out_f % 8 == 0) {  // dy itself, whose rows TMA can take
+    dp = a.dy;
+    a.ld_dp = a.out_f;
+    a.dp = nullptr;
   }
-  Product g = {};
-  g.N = a.in_f;
-  g.ld_out = a.in_f;
-  g.vec = a.in_f % 4 == 0;
-  if (e == cudaSuccess && a.dx) {  // dx[m][k] = sum_n dp[m][n] w[n][k]
-    g.M = a.rows;
-    g.K = a.out_f;
-    g.out = a.dx;
-    e = launch_pairs<false, false, true, __nv_bfloat16>(g, a.dp, a.ld_dp, a.w, a.in_f, st);
+  if (!a.dx && !a.dw) a.dp = nullptr;
+  if (a.dp || a.dbias) {
+    const dim3 grid((unsigned)parts, (unsigned)((a.ld_dp + kPartCols - 1) / kPartCols));
+    if (grid.y > 65535) return cudaErrorInvalidValue;
+    if (a.out_f % 8 == 0) dp_kernel<true><<<grid, 256, 0, st>>>(a, act);
+    else dp_kernel<false><<<grid, 256, 0, st>>>(a, act);
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess && a.dbias) e = launch_column_sum(a.dbias, a.partial, parts, a.out_f, st);
+    if (e != cudaSuccess) return e;
   }
-  if (e == cudaSuccess && a.dw) {  // dw[n][k] = sum_m dp[m][n] x[m][k]
-    g.M = a.out_f;
-    g.K = a.rows;
-    g.out = a.dw;
-    e = launch_pairs<false, true, true, __nv_bfloat16>(g, a.dp, a.ld_dp, a.x, a.ld_x, st);
+  if (!a.dx && !a.dw) return cudaSuccess;
+  Job<true> job = {};
+  for (int i = 0; i < 2; ++i) {
+    Product& g = job.g[i];
+    g.N = a.in_f;
+    g.ld_out = a.in_f;
+    g.vec = 1;  // in_f is a multiple of 8
   }
-  return e;
+  if (a.dw) {  // dw[n][k] = sum_m dp[m][n] x[m][k]
+    job.g[0].M = a.out_f;
+    job.g[0].K = a.rows;
+    job.g[0].out = a.dw;
+    if (!make_map(&job.a[0], dp, a.rows, a.out_f, a.ld_dp, 64, false) ||
+        !make_map(&job.b[0], a.x, a.rows, a.in_f, a.ld_x, 64, false))
+      return cudaErrorInvalidValue;
+  }
+  if (a.dx) {  // dx[m][k] = sum_n dp[m][n] w[n][k]
+    job.g[1].M = a.rows;
+    job.g[1].K = a.out_f;
+    job.g[1].out = a.dx;
+    if (!make_map(&job.a[1], dp, a.rows, a.out_f, a.ld_dp, 128, false) ||
+        !make_map(&job.b[1], a.w, a.out_f, a.in_f, a.in_f, 64, false))
+      return cudaErrorInvalidValue;
+  }
+  const int64_t t0 = pair_tiles(job.g[0]), t1 = pair_tiles(job.g[1]);
+  if (t0 + t1 > 0x3fffffff) return cudaErrorInvalidValue;
+  const int pairs = pair_count(t0 + t1);
+  // dx's tiles go to the pairs with the least of dw, under the lowest load that takes them all
+  const int64_t c0 = (job.g[0].K + 63) / 64 + 1, c1 = (job.g[1].K + 63) / 64 + 1;  // (one for the epilogue's share)
+  auto room = [&](int p, int64_t cap) {
+    const int64_t has = (p < t0 ? (t0 - 1 - p) / pairs + 1 : 0) * c0;
+    return cap > has ? (cap - has) / c1 : 0;
+  };
+  int64_t lo = 0, hi = (t0 / pairs + 1) * c0 + (t1 / pairs + 1) * c1;
+  while (lo < hi) {
+    const int64_t cap = (lo + hi) / 2;
+    int64_t n = 0;
+    for (int p = 0; p < pairs; ++p) n += room(p, cap);
+    if (n >= t1) hi = cap;
+    else lo = cap + 1;
+  }
+  int64_t given = 0;
+  for (int p = 0; p <= pairs; ++p) {
+    job.split.start[p] = (int)given;
+    if (p < pairs) given = std::min(t1, given + room(p, hi));
+  }
+  return start_pairs<false, true, __nv_bfloat16>(job, pairs, st);
 }
 
 }  // namespace mamba2

@@ -934,24 +934,6 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUt
   if (threadIdx.x == 0 && s.abort) atomicAdd(&g_recurrence_timeouts, 1u);
 }
 
-// dlower[ch] = sum of the tiles' parts: 32 channels a CTA, eight threads a channel over every
-// eighth tile, then their sums in order.
-__global__ void __launch_bounds__(256) rec_dlower_kernel(float* dlower, const float* part, int chunks, int dim) {
-  __shared__ float sum[8][32];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
-  float s = 0.0f;
-  if (c < dim)
-    for (int t = w; t < chunks; t += 8) s += part[(int64_t)t * dim + c];
-  sum[w][lane] = s;
-  __syncthreads();
-  if (w == 0 && c < dim) {
-#pragma unroll
-    for (int j = 1; j < 8; ++j) s += sum[j][lane];
-    dlower[c] = s;
-  }
-}
-
 // ------------------------------------------------------------------ single tokens
 
 constexpr int kStepThreads = 128;
@@ -1121,10 +1103,7 @@ cudaError_t launch_recurrence_backward(const RecBwdArgs& a, mamba2_dtype act, vo
   else
     e = vec ? run_bwd<float, true>(a, p.chain, part, p.items, p.groups, st)
             : run_bwd<float, false>(a, p.chain, part, p.items, p.groups, st);
-  if (e == cudaSuccess && a.dlower) {
-    rec_dlower_kernel<<<(a.dim + 31) / 32, 256, 0, st>>>(a.dlower, part, (int)chunks, a.dim);
-    e = cudaGetLastError();
-  }
+  if (e == cudaSuccess && a.dlower) e = launch_column_sum(a.dlower, part, (int)chunks, a.dim, st);
   return e;
 }
 
