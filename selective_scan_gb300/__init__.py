@@ -155,11 +155,14 @@ def _ptr(t) -> Optional[int]:
 
 def _rows(t):
     """(pointer, row stride) of a matrix whose columns are adjacent: a contiguous one or a column range of one."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    (rows, cols), (ld, one) = t.shape, t.stride()
+    if cols > 1 and one != 1:
         raise ValueError("expected a matrix with adjacent columns")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+    if rows <= 1:
+        return t.data_ptr(), cols
+    if ld < cols:
         raise ValueError("rows overlap")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return t.data_ptr(), ld
 
 
 def _type(t) -> int:
@@ -169,7 +172,7 @@ def _type(t) -> int:
 
 def _same(name, t, shape, dtype=None):
     """Raises ValueError unless the tensor (None passes) has this shape, and this type where one is given."""
-    if t is not None and (tuple(t.shape) != tuple(shape) or (dtype is not None and t.dtype != dtype)):
+    if t is not None and (t.shape != shape or (dtype is not None and t.dtype != dtype)):
         raise ValueError(f"{name}: expected shape {tuple(shape)}" + (f" of {dtype}" if dtype is not None else "") +
                          f", got {tuple(t.shape)} of {t.dtype}")
 
@@ -187,10 +190,26 @@ def _workspace(need: int, workspace, device, stream):
     return _ptr(workspace), workspace.numel() * workspace.element_size(), workspace
 
 
+def _current_stream() -> int:
+    """The current device's current stream, without the Stream object that torch.cuda.current_stream makes (most of
+    a small call's host time)."""
+    global _current_stream
+    import torch
+    raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    if raw is None or device is None:
+        def current():
+            return torch.cuda.current_stream().cuda_stream
+    else:
+        def current():
+            return raw(device())
+    torch.cuda.init()
+    _current_stream = current
+    return current()
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -202,15 +221,12 @@ class Batch:
 
     def __init__(self, cu_seqlens: Optional[Sequence[int]], slots: Sequence[int], fresh: Sequence[int]):
         n = len(slots)
-        self.slots = (ctypes.c_int32 * max(n, 1))(*[int(s) for s in slots])
-        self.fresh = (ctypes.c_uint8 * max(n, 1))(*[1 if f else 0 for f in fresh])
+        self.slots = (ctypes.c_int32 * max(n, 1))(*map(int, slots))
+        self.fresh = (ctypes.c_uint8 * max(n, 1))(*map(bool, fresh))
         self.cu = None
         if cu_seqlens is not None:
-            self.cu = (ctypes.c_int32 * (len(cu_seqlens)))(*[int(c) for c in cu_seqlens])
-        self.rb = RecurrentBatch(
-            n, ctypes.cast(self.cu, ctypes.POINTER(ctypes.c_int32)) if self.cu is not None else None,
-            ctypes.cast(self.slots, ctypes.POINTER(ctypes.c_int32)),
-            ctypes.cast(self.fresh, ctypes.POINTER(ctypes.c_uint8)))
+            self.cu = (ctypes.c_int32 * max(1, len(cu_seqlens)))(*map(int, cu_seqlens))
+        self.rb = RecurrentBatch(n, self.cu, self.slots, self.fresh)  # (arrays pass as the pointers)
 
     def ref(self):
         return ctypes.byref(self.rb)

@@ -14,6 +14,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "host.h"
 
 namespace mamba2 {
 namespace {
@@ -368,13 +369,6 @@ __global__ void __launch_bounds__(kCtaThreads) add_norm_bwd_streamed_kernel(cons
   }
 }
 
-int sm_count() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 152;
-  return sms;
-}
-
 // Threads of a row, and rows of a CTA.
 struct Shape {
   int nt, rows;
@@ -382,7 +376,7 @@ struct Shape {
 Shape shape(int64_t rows, int dim, int unit, int held) {
   const int fewest = 32 * ((dim + 32 * held - 1) / (32 * held));
   const int most = 32 * ((dim + 32 * unit - 1) / (32 * unit));
-  if (rows <= sm_count()) return {std::max(fewest, std::min(most, kCtaThreads)), 1};
+  if (rows <= device_sm_count()) return {std::max(fewest, std::min(most, kCtaThreads)), 1};
   return {fewest, std::max(1, kCtaThreads / fewest)};
 }
 int unit_of(int dim) { return dim % 8 == 0 ? 8 : dim % 2 == 0 ? 2 : 1; }
@@ -445,7 +439,7 @@ cudaError_t launch_add_rmsnorm(const AddNormArgs& a, mamba2_dtype act, mamba2_dt
 }
 
 // CTAs of the backward kernel at most (each writes one row of partial sums): two to an SM.
-int add_rmsnorm_backward_parts(int32_t rows, int32_t) { return (int)std::min<int64_t>(rows, 2 * (int64_t)sm_count()); }
+int add_rmsnorm_backward_parts(int32_t rows, int32_t) { return (int)std::min<int64_t>(rows, 2 * (int64_t)device_sm_count()); }
 
 cudaError_t launch_add_rmsnorm_backward(const AddNormBwdArgs& a, mamba2_dtype act, mamba2_dtype sum_type,
                                         cudaStream_t st) {

@@ -131,7 +131,7 @@ mamba2_status mamba2_gated_recurrence_step(void* y, const void* x, const void* g
     for (int i = 0; i <= n; ++i)
       if (rb->cu_seqlens[i] != i) return MAMBA2_ERR_INVALID_ARGUMENT;
   if (n == 0) return MAMBA2_OK;
-  RecStepArgs a = {y, x, gate, lower, state, dim, n, ld_y, ld_x, ld_gate, nullptr, nullptr, nullptr, nullptr, {}};
+  RecStepArgs a = {y, x, gate, lower, state, dim, n, ld_y, ld_x, ld_gate, num_slots, nullptr, nullptr, nullptr, nullptr, {}};
   for (int i = 0; i < n; ++i) a.slot_fresh[i] = (uint32_t)rb->slots[i] | (rb->fresh[i] ? 0x80000000u : 0u);
   return done(launch_recurrence_step(a, act, static_cast<cudaStream_t>(stream)));
 }
@@ -147,12 +147,9 @@ mamba2_status mamba2_gated_recurrence_step_device(void* y, const void* x, const 
     return MAMBA2_ERR_INVALID_ARGUMENT;
   const mamba2_status s = check_step(y, x, gate, lower, state, capacity, dim, ld_y, ld_x, ld_gate, act);
   if (s != MAMBA2_OK) return s;
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  RecStepArgs a = {y, x, gate, lower, state, dim, capacity, ld_y, ld_x, ld_gate, slots_dev, fresh_dev, num_seqs_dev,
-                   status_dev, {}};
-  cudaError_t e = launch_check_device_batch(slots_dev, num_seqs_dev, capacity, num_slots, status_dev, st);
-  if (e == cudaSuccess) e = launch_recurrence_step(a, act, st);
-  return done(e);
+  const RecStepArgs a = {y, x, gate, lower, state, dim, capacity, ld_y, ld_x, ld_gate, num_slots, slots_dev, fresh_dev,
+                         num_seqs_dev, status_dev, {}};
+  return done(launch_recurrence_step(a, act, static_cast<cudaStream_t>(stream)));
 }
 
 mamba2_status mamba2_gated_recurrence_backward(void* dx, void* dgate, float* dlower, float* dstate, const void* dy,

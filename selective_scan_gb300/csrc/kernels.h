@@ -161,12 +161,14 @@ struct RecStepArgs {
   float* state;
   int32_t dim, n;  // n: sequences, or the capacity of a device batch
   int64_t ld_y, ld_x, ld_gate;
+  int32_t num_slots;
   const int32_t* dev_slots;  // device batch (null for a host batch), as in DecodeArgs
   const uint8_t* dev_fresh;
   const int32_t* dev_n;
-  const int32_t* dev_status;
+  int32_t* dev_status;
   uint32_t slot_fresh[MAMBA2_MAX_SEQS];
 };
+// Checks a device batch too (in the kernel, or by launch_check_device_batch).
 cudaError_t launch_recurrence_step(const RecStepArgs& a, mamba2_dtype act, cudaStream_t st);
 
 // Gated recurrence, backward (tab.tile as in RecArgs; slots unused).

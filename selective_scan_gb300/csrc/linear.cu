@@ -26,6 +26,7 @@
 
 #include "../../include/block.h"
 #include "common.cuh"
+#include "host.h"
 
 namespace mamba2 {
 
@@ -738,13 +739,6 @@ bool make_map(CUtensorMap* tm, const void* base, int64_t rows, int64_t cols, int
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int sm_count() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 0;
-  return sms;
-}
-
 int64_t pair_tiles(const Product& g) { return (int64_t)((g.M + kBM - 1) / kBM) * ((g.N + kBN - 1) / kBN); }
 
 template <bool F8, bool kGrad, typename TO>
@@ -756,7 +750,7 @@ cudaError_t start_pairs(const Job<kGrad>& job, int pairs, cudaStream_t st) {
   return cudaGetLastError();
 }
 int pair_count(int64_t tiles) {
-  return (int)std::max<int64_t>(1, std::min<int64_t>({tiles, (int64_t)sm_count() / 2, (int64_t)kMaxPairs}));
+  return (int)std::max<int64_t>(1, std::min<int64_t>({tiles, (int64_t)device_sm_count() / 2, (int64_t)kMaxPairs}));
 }
 
 template <bool F8, typename TO>
@@ -773,7 +767,7 @@ cudaError_t launch_pairs(const Product& g, const void* x, int64_t ldx, const voi
 // The most rows that the few-rows kernel takes: as long as the pairs' tiles would leave half of the SMs idle.
 int few_rows_most(const Product& g) {
   const int64_t tiles = pair_tiles(g);
-  return g.M <= 128 || 4 * tiles < sm_count() ? g.M : 0;
+  return g.M <= 128 || 4 * tiles < device_sm_count() ? g.M : 0;
 }
 
 template <bool F8, int kN, typename TO>
@@ -787,7 +781,7 @@ cudaError_t launch_few(const Product& g, const void* x, int64_t ldx, const void*
   const int tiles_w = (g.N + 127) / 128, tiles_x = (g.M + kN - 1) / kN;
   const int kblocks = (g.K + (F8 ? 127 : 63)) / (F8 ? 128 : 64);
   // as many parts of K as fill two CTAs an SM, each of two k-blocks at least
-  const int S = std::max(1, std::min({8, kblocks / 2, (int)(2 * (int64_t)sm_count() / ((int64_t)tiles_w * tiles_x))}));
+  const int S = std::max(1, std::min({8, kblocks / 2, (int)(2 * (int64_t)device_sm_count() / ((int64_t)tiles_w * tiles_x))}));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)S, (unsigned)tiles_w, (unsigned)tiles_x);
   cfg.blockDim = dim3(kFewThreads);

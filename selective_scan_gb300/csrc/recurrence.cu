@@ -46,6 +46,7 @@
 
 #include "../../include/block.h"
 #include "common.cuh"
+#include "host.h"
 
 namespace mamba2 {
 
@@ -936,37 +937,128 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUt
 
 // ------------------------------------------------------------------ single tokens
 
-constexpr int kStepThreads = 128;
+// One token of each sequence: a CTA takes 1 024 channels of a sequence, a thread four (adjacent ones where rows
+// are aligned for them, else every 256th). At most 8 bytes of state and 3 elements a channel: a full batch is
+// bound by HBM, a small one by the launch, so a device batch of up to kCheckHere sequences is checked by every
+// CTA itself before it touches anything, instead of by a kernel of its own.
+constexpr int kStepThreads = 256;
+constexpr int kCheckHere = 256;
 
-template <typename T>
+// The status of a device batch, as launch_check_device_batch finds it: the count, then the slots' range, then
+// whether two sequences share one. All threads of the CTA call it and get the same answer.
+__device__ __forceinline__ int check_batch(const RecStepArgs& a, int num, int32_t* slots) {
+  __shared__ int worst;  // bit 0: a slot out of range, bit 1: a slot twice
+  if (num < 0 || num > a.n) return MAMBA2_ERR_INVALID_ARGUMENT;
+  if (threadIdx.x == 0) worst = 0;
+  // past the end: a value of its own in each place, which no slot equals
+  for (int i = threadIdx.x; i < kCheckHere; i += kStepThreads) slots[i] = i < num ? a.dev_slots[i] : -1 - i;
+  __syncthreads();
+  int bad = 0;
+  for (int i = threadIdx.x; i < num; i += kStepThreads) {
+    const int mine = slots[i];
+    if (mine < 0 || mine >= a.num_slots) bad |= 1;
+    for (int j = 0; j < i; j += 4) {
+      const int4 v = *reinterpret_cast<const int4*>(slots + j);
+      if (v.x == mine || (v.y == mine && j + 1 < i) || (v.z == mine && j + 2 < i) || (v.w == mine && j + 3 < i)) bad |= 2;
+    }
+  }
+  if (bad) atomicOr(&worst, bad);
+  __syncthreads();
+  return worst & 1 ? MAMBA2_ERR_SLOT_OUT_OF_RANGE : worst & 2 ? MAMBA2_ERR_SLOT_SHARED : MAMBA2_OK;
+}
+
+template <typename T, bool kVec>
 __global__ void __launch_bounds__(kStepThreads) rec_step_kernel(const __grid_constant__ RecStepArgs a) {
-  const int ch = blockIdx.x * kStepThreads + threadIdx.x, i = blockIdx.y;
-  if (ch >= a.dim) return;
+  __shared__ __align__(16) int32_t slots[kCheckHere];
+  const int i = blockIdx.y;
   int slot;
   bool fresh;
   if (a.dev_slots) {
-    if (*a.dev_status != MAMBA2_OK || i >= *a.dev_n) return;
+    const int num = *a.dev_n;
+    if (a.n <= kCheckHere) {
+      const int status = check_batch(a, num, slots);
+      if (blockIdx.x == 0 && i == 0 && threadIdx.x == 0) *a.dev_status = status;
+      if (status != MAMBA2_OK) return;
+    } else if (*a.dev_status != MAMBA2_OK) {
+      return;
+    }
+    if (i >= num) return;
     slot = a.dev_slots[i];
     fresh = a.dev_fresh && a.dev_fresh[i];
   } else {
     slot = (int)(a.slot_fresh[i] & 0x7fffffffu);
     fresh = (a.slot_fresh[i] >> 31) != 0u;
   }
-  const float lo = a.lower ? a.lower[ch] : 0.0f;
-  float* st = a.state + (int64_t)slot * a.dim + ch;
-  float h = fresh ? 0.0f : *st;
-  float up, down;
-  sigmoids(Act<T>::to_f(static_cast<const T*>(a.gate)[i * a.ld_gate + ch]), up, down);
-  h = fmaf(fmaf(1.0f - lo, up, lo), h, (1.0f - lo) * down * Act<T>::to_f(static_cast<const T*>(a.x)[i * a.ld_x + ch]));
-  static_cast<T*>(a.y)[i * a.ld_y + ch] = Act<T>::from_f(h);
-  *st = h;
-}
-
-int sm_count() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 1;
-  return sms;
+  const int c0 = blockIdx.x * 4 * kStepThreads;
+  auto channel = [&](int j) { return c0 + (kVec ? 4 * (int)threadIdx.x + j : (int)threadIdx.x + j * kStepThreads); };
+  float* st = a.state + (int64_t)slot * a.dim;
+  const T* x = static_cast<const T*>(a.x) + i * a.ld_x;
+  const T* gate = static_cast<const T*>(a.gate) + i * a.ld_gate;
+  T* y = static_cast<T*>(a.y) + i * a.ld_y;
+  float xv[4], gv[4], h[4], lo[4];
+  if constexpr (kVec) {
+    if (channel(0) >= a.dim) return;
+    auto four = [](const T* p, float (&v)[4]) {
+      if constexpr (sizeof(T) == 4) {
+        const float4 f = *reinterpret_cast<const float4*>(p);
+        v[0] = f.x;
+        v[1] = f.y;
+        v[2] = f.z;
+        v[3] = f.w;
+      } else {
+        const uint2 w = *reinterpret_cast<const uint2*>(p);
+        v[0] = __uint_as_float(w.x << 16);
+        v[1] = __uint_as_float(w.x & 0xffff0000u);
+        v[2] = __uint_as_float(w.y << 16);
+        v[3] = __uint_as_float(w.y & 0xffff0000u);
+      }
+    };
+    const float4 none = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const float4 hs = fresh ? none : *reinterpret_cast<const float4*>(st + channel(0));
+    const float4 ls = a.lower ? *reinterpret_cast<const float4*>(a.lower + channel(0)) : none;
+    four(x + channel(0), xv);
+    four(gate + channel(0), gv);
+    h[0] = hs.x;
+    h[1] = hs.y;
+    h[2] = hs.z;
+    h[3] = hs.w;
+    lo[0] = ls.x;
+    lo[1] = ls.y;
+    lo[2] = ls.z;
+    lo[3] = ls.w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (channel(j) < a.dim) {
+        xv[j] = Act<T>::to_f(x[channel(j)]);
+        gv[j] = Act<T>::to_f(gate[channel(j)]);
+        h[j] = fresh ? 0.0f : st[channel(j)];
+        lo[j] = a.lower ? a.lower[channel(j)] : 0.0f;
+      }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float up, down;
+    sigmoids(gv[j], up, down);
+    h[j] = fmaf(fmaf(1.0f - lo[j], up, lo[j]), h[j], (1.0f - lo[j]) * down * xv[j]);
+  }
+  if constexpr (kVec) {
+    *reinterpret_cast<float4*>(st + channel(0)) = make_float4(h[0], h[1], h[2], h[3]);
+    if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<float4*>(y + channel(0)) = make_float4(h[0], h[1], h[2], h[3]);
+    } else {
+      const __nv_bfloat162 p = __floats2bfloat162_rn(h[0], h[1]), q = __floats2bfloat162_rn(h[2], h[3]);
+      *reinterpret_cast<uint2*>(y + channel(0)) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (channel(j) < a.dim) {
+        st[channel(j)] = h[j];
+        y[channel(j)] = Act<T>::from_f(h[j]);
+      }
+  }
 }
 
 bool rows16(const void* p, int64_t ld, size_t e) {
@@ -975,7 +1067,7 @@ bool rows16(const void* p, int64_t ld, size_t e) {
 
 // CTAs of a launch: so many to an SM, no more than tiles; empty runs need one.
 int ctas(int64_t items, int per_sm) {
-  return (int)std::max<int64_t>(1, std::min<int64_t>(items, per_sm * (int64_t)sm_count()));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(items, per_sm * (int64_t)device_sm_count()));
 }
 
 using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -1108,9 +1200,21 @@ cudaError_t launch_recurrence_backward(const RecBwdArgs& a, mamba2_dtype act, vo
 }
 
 cudaError_t launch_recurrence_step(const RecStepArgs& a, mamba2_dtype act, cudaStream_t st) {
-  const dim3 grid((a.dim + kStepThreads - 1) / kStepThreads, a.n);
-  if (act == MAMBA2_BF16) rec_step_kernel<__nv_bfloat16><<<grid, kStepThreads, 0, st>>>(a);
-  else rec_step_kernel<float><<<grid, kStepThreads, 0, st>>>(a);
+  if (a.dev_slots && a.n > kCheckHere) {
+    const cudaError_t e = launch_check_device_batch(a.dev_slots, a.dev_n, a.n, a.num_slots, a.dev_status, st);
+    if (e != cudaSuccess) return e;
+  }
+  const dim3 grid((a.dim + 4 * kStepThreads - 1) / (4 * kStepThreads), a.n);
+  const size_t e = act == MAMBA2_BF16 ? 2 : 4;
+  auto fours = [&](const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & (4 * e - 1)) == 0 && ld % 4 == 0; };
+  const bool vec = a.dim % 4 == 0 && fours(a.x, a.ld_x) && fours(a.gate, a.ld_gate) && fours(a.y, a.ld_y);
+  if (act == MAMBA2_BF16) {
+    if (vec) rec_step_kernel<__nv_bfloat16, true><<<grid, kStepThreads, 0, st>>>(a);
+    else rec_step_kernel<__nv_bfloat16, false><<<grid, kStepThreads, 0, st>>>(a);
+  } else {
+    if (vec) rec_step_kernel<float, true><<<grid, kStepThreads, 0, st>>>(a);
+    else rec_step_kernel<float, false><<<grid, kStepThreads, 0, st>>>(a);
+  }
   return cudaGetLastError();
 }
 

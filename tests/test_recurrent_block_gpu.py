@@ -235,6 +235,36 @@ def test_step_fresh_and_bad_device_batches():
         assert (y == 7.0).all() and torch.equal(st.cpu(), pool_)
 
 
+@pytest.mark.parametrize("capacity", [3, 130, 256, 300, 1024])
+@pytest.mark.parametrize("dtype,dim", [(BF16, 64), (F32, 1500), (BF16, 37)])
+def test_step_device_batch_sizes(capacity, dtype, dim):
+    """Batches that the step's own CTAs check and larger ones: the result, and what a bad last slot does."""
+    dev = device()
+    n = capacity - 1
+    x, gate, lo, _, _, _ = rec_inputs(capacity, [capacity], dim, dtype, True)
+    slots = torch.randperm(capacity + 9, generator=torch.Generator().manual_seed(capacity))[:capacity].tolist()
+    fresh = [i % 3 == 0 for i in range(capacity)]
+    pool = randn(7, capacity + 9, dim)
+    ref = R.recurrence(x[:n], gate[:n], lo, pool, cu_of([1] * n), slots[:n], fresh[:n])
+    put = lambda v, t: torch.tensor(v, dtype=t, device=dev)  # noqa: E731
+    for bad, status in ((None, ss.OK), (slots[0], ss.ERR_SLOT_SHARED), (capacity + 9, ss.ERR_SLOT_OUT_OF_RANGE)):
+        st, y, code = pool.to(dev), torch.full((capacity, dim), 7.0, dtype=dtype, device=dev), put([-1], torch.int32)
+        s = list(slots)
+        if bad is not None:
+            s[n - 1] = bad
+        ss.gated_recurrence_step_device(y, x.to(dev), gate.to(dev), lo.to(dev), st, put(s, torch.int32),
+                                        put(fresh, torch.uint8), put([n], torch.int32), code)
+        assert int(code.item()) == status
+        if bad is None:
+            R.check(y[:n], ref["y"], "y")
+            a = torch.tensor(slots[:n])
+            R.check(st[a.to(dev)], tuple(v[a] for v in ref["pool"]), "state")
+            rest = [i for i in range(capacity + 9) if i not in slots[:n]]
+            assert torch.equal(st.cpu()[rest], pool[rest]) and (y[n:] == 7.0).all()
+        else:
+            assert torch.equal(st.cpu(), pool) and (y == 7.0).all()
+
+
 def test_recurrence_past_32_bit_offsets():
     dev = device()
     dim, ld = 64, 1 << 28  # row 9 begins past 2^31 elements
