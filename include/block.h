@@ -46,14 +46,18 @@ extern "C" {
  *   lower [dim] f32, each in [0, 1] (not checked), or NULL
  *   state [num_slots, dim] f32, updated in place at the named slots
  *   checkpoints [mamba2_gated_recurrence_checkpoints(...), dim] f32 or NULL:
- *         the state before each MAMBA2_RECURRENCE_CHUNK tokens of each run, in
- *         order, for the backward pass
+ *         for the backward pass, the state before each
+ *         MAMBA2_RECURRENCE_STEP tokens of each run, in order; a run has rows
+ *         for whole chunks of MAMBA2_RECURRENCE_CHUNK tokens, and those past
+ *         its end are left as they are
  *   workspace 256-byte aligned, of at least the bytes that
  *         mamba2_gated_recurrence_workspace_bytes gives (NULL when 0)
  */
 #define MAMBA2_RECURRENCE_CHUNK 128
+#define MAMBA2_RECURRENCE_STEP 16
 
-/* Rows of `checkpoints`: the sum over runs of ceil(length / chunk). -1 for a
+/* Rows of `checkpoints`: chunk / step times the sum over runs of
+ * ceil(length / chunk). -1 for a
  * cu_seqlens that does not start at 0 or decreases, or a bad num_seqs. */
 int64_t mamba2_gated_recurrence_checkpoints(const int32_t* cu_seqlens, int32_t num_seqs);
 

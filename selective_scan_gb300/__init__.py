@@ -28,7 +28,8 @@ LIB_PATH = _PKG / "libmamba2.so"
 
 F32, BF16, E4M3 = 0, 1, 2
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
-RECURRENCE_CHUNK = 128  # tokens between two checkpoints of the gated recurrence
+# tokens between two checkpoints of the gated recurrence, and of the chunks whose checkpoints a run has whole
+RECURRENCE_STEP, RECURRENCE_CHUNK = 16, 128
 (OK, ERR_INVALID_ARGUMENT, ERR_SLOT_OUT_OF_RANGE, ERR_SLOT_SHARED, ERR_RUNS_DONT_COVER_ROWS,
  ERR_NOT_IMPLEMENTED, ERR_CUDA, ERR_WORKSPACE_TOO_SMALL) = range(8)
 MAX_SEQS = 1024

@@ -58,7 +58,7 @@ extern "C" {
 int64_t mamba2_gated_recurrence_checkpoints(const int32_t* cu_seqlens, int32_t num_seqs) {
   if (!cu_ok(cu_seqlens, num_seqs)) return -1;
   bool chained;
-  return count_chunks(cu_seqlens, num_seqs, &chained);
+  return count_chunks(cu_seqlens, num_seqs, &chained) * (MAMBA2_RECURRENCE_CHUNK / MAMBA2_RECURRENCE_STEP);
 }
 
 size_t mamba2_gated_recurrence_workspace_bytes(const int32_t* cu_seqlens, int32_t num_seqs, int32_t dim,

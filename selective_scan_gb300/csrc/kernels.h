@@ -141,7 +141,7 @@ unsigned int read_gemm_timeouts();
 // MAMBA2_RECURRENCE_CHUNK tokens, ceil(length / chunk) a sequence).
 struct RecArgs {
   void* y;
-  float* ckpt;  // [chunks, dim] or null
+  float* ckpt;  // [chunks * chunk / step, dim] or null
   const void* x;
   const void* gate;
   const float* lower;  // [dim] or null

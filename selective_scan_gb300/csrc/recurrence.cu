@@ -18,7 +18,8 @@
 // predecessors.
 //
 // What precedes chunk l of a run, the same for any timing (so results repeat bit for bit):
-// every chunk publishes its map, and every 16th (0, 16, 32, ...) the state after it too. Chunk l
+// every chunk publishes its map, and every 16th (0, 16, 32, ...) the state after it too (the first
+// the state alone, which it has as early as its map). Chunk l
 // takes the state that lies one such step further back than the nearest, and folds the maps of
 // the 16 to 31 chunks between in order. Maps are published without waiting for anything, and a
 // state is used 16 chunks later at the earliest: later than the tiles that the GPU holds at one
@@ -428,9 +429,9 @@ struct Before {
 };
 // This warp's share: the maps of the chunks kBack warp + 1 .. kBack (warp + 1) before the tile as far as there
 // are k, composed; and the state (warp 0).
-template <typename T, bool kReverse, typename First>
+template <typename T, bool kReverse>
 __device__ __forceinline__ void look_back(const Chain& ch, const Info& f, int first, int groups, int k,
-                                          Before<T>& out, int warp, int lane, First initial) {
+                                          Before<T>& out, int warp, int lane) {
   constexpr int C = kCh<T>;
   const int d0 = kBack * warp + 1, n = min(kBack, max(0, k - d0 + 1));
   const int64_t step = (int64_t)(kReverse ? groups : -groups) * kTileCh<T> * 2;
@@ -439,16 +440,11 @@ __device__ __forceinline__ void look_back(const Chain& ch, const Info& f, int fi
 #pragma unroll
   for (int j = 0; j < kBack; ++j)
     if (j < n) load_record<C>(p + j * step, r[j]);
-  if (warp == 0) {
-    if (f.l == 0) {
-#pragma unroll
-      for (int c = 0; c < C; ++c) h[c] = initial(c);
-    } else {
-      const float* q = state_at<T>(ch, f, first, f.l - 1 - k, groups, lane);
-      load_state<C>(q, h);
+  if (warp == 0 && f.l > 0) {  // (the first chunk's is read where its map is made)
+    const float* q = state_at<T>(ch, f, first, f.l - 1 - k, groups, lane);
+    load_state<C>(q, h);
 #pragma unroll 1
-      for (uint32_t it = 0; !__all_sync(0xffffffffu, is_set(h)) && !gave_up(ch, it, lane); ++it) load_state<C>(q, h);
-    }
+    for (uint32_t it = 0; !__all_sync(0xffffffffu, is_set(h)) && !gave_up(ch, it, lane); ++it) load_state<C>(q, h);
 #pragma unroll
     for (int c = 0; c < C; ++c) out.state[lane * C + c] = h[c];
   }
@@ -503,7 +499,8 @@ template <bool kVec> constexpr int kFwdStage = 2 * kChunkR * kPitch<kVec>;
 template <typename T>
 struct FwdShared {
   Info info[kInfos];
-  float A[kWarps][kTileCh<T>], B[kWarps][kTileCh<T>];      // the warps' maps
+  float A[kWarps][kTileCh<T>], B[kWarps][kTileCh<T>];      // the warps' maps, then of all the warps before each
+  float enter[kTileCh<T>];                                 // the state that enters the tile
   Before<T> before;
   alignas(8) uint64_t full[kFwdStages][kWarps];
   uint32_t abort;
@@ -558,6 +555,11 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ CUtens
     if (threadIdx.x == 0) next = take<kFwdStages>(ch, i + kFwdStages, items);
     const int first = a.tab.tile[f.seq];
     const int before = f.l > 0 ? maps_before(f.l) : 0;
+    float h0[C];  // what the run starts from: asked for early, the run's other tiles wait for it
+    if (warp == kWarps - 1 && f.l == 0)
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        h0[c] = c < left && !seq_fresh(a.tab, f.seq) ? a.state[(int64_t)seq_slot(a.tab, f.seq) * a.dim + ch0 + c] : 0.0f;
     // ---- scan from zero
     unsigned char* st = stages + (i % kFwdStages) * kFwdStage<kVec>;
     const T* tx = static_cast<const T*>(a.x) + f.row * a.ld_x + f.group * kTileCh<T>;
@@ -611,7 +613,7 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ CUtens
     };
     if (nt == kTok) scan(std::true_type{});
     else scan(std::false_type{});
-    float A[C], B[C], ea[C], eb[C];
+    float A[C], B[C];
     P::split(p2, A);
     P::split(h2, B);
 #pragma unroll
@@ -620,51 +622,64 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ CUtens
       s.B[warp][lane * C + c] = B[c];
     }
     __syncthreads();
-    // the map before this warp (ea, eb); the last warp's and its own make the tile's
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      ea[c] = 1.0f;
-      eb[c] = 0.0f;
-    }
-    for (int w = 0; w < warp; ++w)
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const float wa = s.A[w][lane * C + c];
-        eb[c] = fmaf(wa, eb[c], s.B[w][lane * C + c]);
-        ea[c] *= wa;
-      }
     if (warp == kWarps - 1) {
+      // for each warp the map of those before it; after the last, the tile's
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        B[c] = fmaf(A[c], eb[c], B[c]);
-        A[c] *= ea[c];
+        A[c] = 1.0f;
+        B[c] = 0.0f;
       }
-      if (!f.last) publish_map<T>(ch, f, groups, A, B, lane);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w)
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          const float wa = s.A[w][lane * C + c], wb = s.B[w][lane * C + c];
+          s.A[w][lane * C + c] = A[c];
+          s.B[w][lane * C + c] = B[c];
+          B[c] = fmaf(wa, B[c], wb);
+          A[c] *= wa;
+        }
+      if (f.l == 0) {  // nothing to wait for: the state after the first chunk is out as early as the maps
+        float end[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          s.before.state[lane * C + c] = h0[c];
+          end[c] = fmaf(A[c], h0[c], B[c]);
+        }
+        if (!f.last) publish_state<T>(ch, f, first, groups, end, lane);
+      } else if (!f.last) {
+        publish_map<T>(ch, f, groups, A, B, lane);
+      }
     }
-    look_back<T, false>(ch, f, first, groups, before, s.before, warp, lane, [&](int c) {
-      return c < left && !seq_fresh(a.tab, f.seq) ? a.state[(int64_t)seq_slot(a.tab, f.seq) * a.dim + ch0 + c] : 0.0f;
-    });
+    look_back<T, false>(ch, f, first, groups, before, s.before, warp, lane);
     if (threadIdx.x == 0) tile_info<false>(s.info[(i + kFwdStages) % kInfos], a.tab, next, items, groups);
     __syncthreads();
     float in[C];
-    fold_before(s.before, before, in, lane);
     if (warp == kWarps - 1) {
+      fold_before(s.before, before, in, lane);
       float end[C];
 #pragma unroll
       for (int c = 0; c < C; ++c) {
+        s.enter[lane * C + c] = in[c];
         end[c] = fmaf(A[c], in[c], B[c]);
-        if (a.ckpt && c < left) a.ckpt[(int64_t)f.chunk * a.dim + ch0 + c] = in[c];
       }
       if (f.last) {
 #pragma unroll
         for (int c = 0; c < C; ++c)
           if (c < left) a.state[(int64_t)seq_slot(a.tab, f.seq) * a.dim + ch0 + c] = end[c];
-      } else if (f.l % kGroup == 0) {
+      } else if (f.l % kGroup == 0 && f.l > 0) {
         publish_state<T>(ch, f, first, groups, end, lane);
       }
     }
+    __syncthreads();
+    // the state that enters this warp
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      in[c] = fmaf(s.A[warp][lane * C + c], s.enter[lane * C + c], s.B[warp][lane * C + c]);
+      if (a.ckpt && c < left && nt > 0) a.ckpt[((int64_t)f.chunk * kWarps + warp) * a.dim + ch0 + c] = in[c];
+    }
     T* ty = static_cast<T*>(a.y) + (f.row + warp * kTok) * a.ld_y + ch0;
-    const V in2 = P::fma(P::make(ea), P::make(in), P::make(eb));
+    const V in2 = P::make(in);
     auto emit = [&](auto whole) {
 #pragma unroll
       for (int j = 0; j < kTok; ++j)
@@ -699,7 +714,7 @@ template <bool kVec> constexpr int kBwdStage = 3 * kChunkR * kPitch<kVec>;
 template <typename T>
 struct BwdShared {
   Info info[kInfos];
-  float A[kWarps][kTileCh<T>], F[kWarps][kTileCh<T>], R[kWarps][kTileCh<T>];
+  float A[kWarps][kTileCh<T>], R[kWarps][kTileCh<T>];
   Before<T> before;
   float dlo[kWarps][kTileCh<T>];
   alignas(8) uint64_t full[kBwdStages][kWarps];
@@ -766,6 +781,11 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUt
     if (threadIdx.x == 0) next = take<kBwdStages>(ch, i + kBwdStages, items);
     const int first = a.tab.tile[f.seq];
     const int before = f.l > 0 ? maps_before(f.l) : 0;
+    float h0[C];
+    if (warp == 0 && f.l == 0)
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        h0[c] = c < left && a.dstate_end ? a.dstate_end[(int64_t)f.seq * a.dim + ch0 + c] : 0.0f;
     const unsigned char* st = stages + (i % kBwdStages) * kBwdStage<kVec>;
     const T* tx = static_cast<const T*>(a.x) + f.row * a.ld_x + f.group * kTileCh<T>;
     const T* tg = static_cast<const T*>(a.gate) + f.row * a.ld_gate + f.group * kTileCh<T>;
@@ -775,7 +795,7 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUt
     for (int c = 0; c < C; ++c) {
       lo[c] = a.lower && c < left ? a.lower[ch0 + c] : 0.0f;
       un[c] = 1.0f - lo[c];
-      hp[c] = c < left ? a.ckpt[(int64_t)f.chunk * a.dim + ch0 + c] : 0.0f;
+      hp[c] = c < left && warp * kTok < f.n ? a.ckpt[((int64_t)f.chunk * kWarps + warp) * a.dim + ch0 + c] : 0.0f;
     }
     const V lo2 = P::make(lo), un2 = P::make(un);
     const int nt = min(kTok, f.n - warp * kTok);
@@ -788,9 +808,10 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUt
       cp_wait<kBwdStages - 1>();
       __syncwarp();
     }
-    // ---- both scans from zero: h's map (A, F) and R's map (A, R)
+    // ---- the states from the checkpoint on, and R's map (A, R)
     V sg[kTok];  // the smaller sigmoid, signed as the gate
-    V A2 = P::all(1.0f), F2 = P::all(0.0f), R2 = P::all(0.0f);
+    V hs[kTok];  // the state before the token
+    V A2 = P::all(1.0f), R2 = P::all(0.0f), hp2 = P::make(hp);
     auto gates = [&](V v, V& up, V& down, V& ft) {
       float g[C], m[C];
       P::split(v, g);
@@ -816,29 +837,25 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUt
           for (int c = 0; c < C; ++c) m[c] = copysignf(m[c], g[c]);
           sg[j] = P::make(m);
           const V ft = P::fma(un2, up, lo2);
-          F2 = P::fma(ft, F2, P::mul(P::mul(un2, down), P::make(x)));
+          hs[j] = hp2;
+          hp2 = P::fma(ft, hp2, P::mul(P::mul(un2, down), P::make(x)));
           A2 = P::mul(A2, ft);
           R2 = P::fma(A2, P::make(d), R2);
         }
     };
     if (nt == kTok) scan(std::true_type{});
     else scan(std::false_type{});
-    float A[C], F[C], R[C], ea[C], eb[C];
+    float A[C], R[C], ea[C], eb[C];
     P::split(A2, A);
-    P::split(F2, F);
     P::split(R2, R);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       s.A[warp][lane * C + c] = A[c];
-      s.F[warp][lane * C + c] = F[c];
       s.R[warp][lane * C + c] = R[c];
     }
     __syncthreads();
     if (warp == 1 && i > 0 && part) sum_part(i - 1);
-    // the state that enters this warp; the map of R after it; the tile's map of R (warp 0)
-    for (int w = 0; w < warp; ++w)
-#pragma unroll
-      for (int c = 0; c < C; ++c) hp[c] = fmaf(s.A[w][lane * C + c], hp[c], s.F[w][lane * C + c]);
+    // the map of R after this warp, and of the tile (warp 0)
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       ea[c] = 1.0f;
@@ -857,27 +874,19 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUt
         R[c] = fmaf(A[c], eb[c], R[c]);
         A[c] *= ea[c];
       }
-      if (!f.last) publish_map<T>(ch, f, groups, A, R, lane);
-    }
-    // ---- the state before each token
-    V hs[kTok], hp2 = P::make(hp);
-    auto states = [&](auto whole) {
+      if (f.l == 0) {
+        float end[C];
 #pragma unroll
-      for (int j = 0; j < kTok; ++j)
-        if (decltype(whole)::value || j < nt) {
-          float x[C];
-          unpack_word<T>(staged<T, kVec>(st, warp * kTok + j, lane, tx, a.ld_x), x);
-          V up, down, ft;
-          gates(sg[j], up, down, ft);
-          hs[j] = hp2;
-          hp2 = P::fma(ft, hp2, P::mul(P::mul(un2, down), P::make(x)));
+        for (int c = 0; c < C; ++c) {
+          s.before.state[lane * C + c] = h0[c];
+          end[c] = fmaf(A[c], h0[c], R[c]);
         }
-    };
-    if (nt == kTok) states(std::true_type{});
-    else states(std::false_type{});
-    look_back<T, true>(ch, f, first, groups, before, s.before, warp, lane, [&](int c) {
-      return c < left && a.dstate_end ? a.dstate_end[(int64_t)f.seq * a.dim + ch0 + c] : 0.0f;
-    });
+        if (!f.last) publish_state<T>(ch, f, first, groups, end, lane);
+      } else if (!f.last) {
+        publish_map<T>(ch, f, groups, A, R, lane);
+      }
+    }
+    look_back<T, true>(ch, f, first, groups, before, s.before, warp, lane);
     // info[i + 2] takes the place of tile i - 2, whose part of dlower has been summed
     if (threadIdx.x == 0) tile_info<true>(s.info[(i + kBwdStages) % kInfos], a.tab, next, items, groups);
     __syncthreads();
@@ -891,7 +900,7 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUt
 #pragma unroll
         for (int c = 0; c < C; ++c)
           if (a.dstate && c < left) a.dstate[(int64_t)f.seq * a.dim + ch0 + c] = end[c];
-      } else if (f.l % kGroup == 0) {
+      } else if (f.l % kGroup == 0 && f.l > 0) {
         publish_state<T>(ch, f, first, groups, end, lane);
       }
     }

@@ -52,8 +52,8 @@ def test_recurrence_refusals(product_lib):
 
 
 def test_recurrence_checkpoints(product_lib):
-    assert ss.RECURRENCE_CHUNK == 128
-    assert ss.gated_recurrence_checkpoints([0, 0, 1, 129, 257, 386]) == 0 + 1 + 1 + 1 + 2
+    assert (ss.RECURRENCE_STEP, ss.RECURRENCE_CHUNK) == (16, 128)
+    assert ss.gated_recurrence_checkpoints([0, 0, 1, 129, 257, 386]) == 8 * (0 + 1 + 1 + 1 + 2)
     assert ss.gated_recurrence_checkpoints([0]) == 0
     for cu in ([1, 2], [0, 3, 2]):
         with pytest.raises(ss.Mamba2Error):

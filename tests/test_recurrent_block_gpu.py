@@ -80,8 +80,14 @@ def test_recurrence_forward_and_backward(dtype, lengths, dim, off, extra):
     R.check(st[at.to(dev)], tuple(v[at] for v in ref["pool"]), "state")
     others = torch.tensor([s for s in range(n + 3) if s not in slots])
     assert torch.isnan(st.cpu()[others]).all(), "a slot outside the batch was written"
-    firsts = [cu[i] + t for i in range(n) for t in range(0, lengths[i], ss.RECURRENCE_CHUNK)]
-    R.check(kept, (ref["prev"][0][firsts], ref["prev"][2][firsts]), "checkpoints")
+    per = ss.RECURRENCE_CHUNK // ss.RECURRENCE_STEP
+    at_row, row = {}, 0  # checkpoint row -> the token that it stands before
+    for i in range(n):
+        at_row.update({row + k: cu[i] + t for k, t in enumerate(range(0, lengths[i], ss.RECURRENCE_STEP))})
+        row += -(-lengths[i] // ss.RECURRENCE_CHUNK) * per
+    assert row == kept.shape[0]
+    firsts, rows_at = list(at_row.values()), torch.tensor(list(at_row), device=dev)
+    R.check(kept[rows_at], (ref["prev"][0][firsts], ref["prev"][2][firsts]), "checkpoints")
     # backward
     dy, de = randn(seed + 8, rows, dim).to(dtype), randn(seed + 9, n, dim)
     want = R.recurrence_backward(x, gate, lo, ref, cu, dy, de)
@@ -108,7 +114,7 @@ def test_recurrence_optional_outputs_and_repeat():
     for _ in range(2):
         st = pool.to(dev)
         y = torch.empty_like(gx)
-        kept = torch.empty((ss.gated_recurrence_checkpoints(cu), dim), device=dev)
+        kept = torch.zeros((ss.gated_recurrence_checkpoints(cu), dim), device=dev)
         ss.gated_recurrence(y, gx, gg, glo, st, cu, slots, fresh, checkpoints=kept)
         dx, dg, dlo = torch.empty_like(gx), torch.empty_like(gx), torch.empty_like(glo)
         ss.gated_recurrence_backward(dx, dg, dlo, None, dy.to(dev), None, gx, gg, glo, kept, cu)
@@ -279,7 +285,7 @@ def test_recurrence_past_32_bit_offsets():
     ref = R.recurrence(x, gate, lo, torch.zeros((1, dim)), [0, 10], [0], [1])
     R.check(gy, ref["y"], "y")
     R.check(st[slots:], ref["pool"], "state")
-    kept = torch.zeros((1, dim), device=dev)
+    kept = torch.zeros((ss.gated_recurrence_checkpoints([0, 10]), dim), device=dev)
     dy = randn(52, 10, dim).to(BF16)
     gdy, dx, dg = wide[:, 2000:2000 + dim], wide[:, 3000:3000 + dim], wide[:, 4000:4000 + dim]
     gdy.copy_(dy.to(dev))
@@ -494,7 +500,7 @@ def test_side_stream_and_graph_capture():
     w, nw = randn(72, 256, dim, std=0.1).to(BF16).to(dev), randn(73, dim).to(dev)
     dy = randn(74, 1000, 256).to(BF16).to(dev)
     buf = dict(st=torch.empty_like(st0), y=torch.empty_like(gx), n=torch.empty_like(gx), s=torch.empty_like(gx),
-               kept=torch.empty((ss.gated_recurrence_checkpoints(cu), dim), device=dev),
+               kept=torch.zeros((ss.gated_recurrence_checkpoints(cu), dim), device=dev),
                o=torch.empty((1000, 256), dtype=BF16, device=dev), pre=torch.empty((1000, 256), dtype=BF16, device=dev),
                dn=torch.empty_like(gx), dw=torch.empty_like(w), db=torch.empty(256, device=dev), ds=torch.empty_like(gx),
                dnw=torch.empty_like(nw), dx=torch.empty_like(gx), dg=torch.empty_like(gx), dlo=torch.empty_like(glo))
