@@ -144,6 +144,26 @@ def _dt(t) -> int:
     raise TypeError(f"unsupported activation dtype {t.dtype}")
 
 
+def _alike(first, others, f32=()):
+    """Shapes and types of an operator's tensors: ``others`` (name, tensor) are like ``first``; ``f32`` (name, tensor,
+    shape) are fp32 of that shape; None passes. One pass without calls when all is well (it is part of every call)."""
+    shape, dtype = first.shape, first.dtype
+    for name, t in others:
+        if t is not None and (t.shape != shape or t.dtype != dtype):
+            _same(name, t, shape, dtype)
+    for name, t, want in f32:
+        if t is not None and (t.shape != want or t.dtype != _float32()):
+            _same(name, t, want, _float32())
+
+
+def _float32():
+    global _float32
+    import torch
+    f = torch.float32
+    _float32 = lambda: f  # noqa: E731
+    return f
+
+
 def _ptr(t) -> Optional[int]:
     if t is None:
         return None
@@ -481,15 +501,11 @@ def gated_recurrence(y, x, gate, lower, state, cu_seqlens=None, slots=None, fres
     """``mamba2_gated_recurrence``: h_t = f_t h_{t-1} + (1 - f_t) x_t over packed runs, f from ``gate`` and the
     lower bounds; ``state`` updated at the slots. x, gate and y may be column ranges of wider matrices.
     ``checkpoints`` [gated_recurrence_checkpoints(cu_seqlens), dim] f32 is for the backward pass."""
-    import torch
     rows, dim = x.shape
     b = _batch(cu_seqlens, slots, fresh, batch)
-    _same("gate", gate, x.shape, x.dtype)
-    _same("y", y, x.shape, x.dtype)
-    _same("lower", lower, (dim,), torch.float32)
-    _same("state", state, (state.shape[0], dim), torch.float32)
+    _alike(x, (("gate", gate), ("y", y)), (("lower", lower, (dim,)), ("state", state, (state.shape[0], dim))))
     if checkpoints is not None and b.cu is not None:
-        _same("checkpoints", checkpoints, (gated_recurrence_checkpoints(b.cu), dim), torch.float32)
+        _same("checkpoints", checkpoints, (gated_recurrence_checkpoints(b.cu), dim), _float32())
     need = gated_recurrence_workspace_bytes(b.cu, dim) if workspace is None and b.cu is not None else 0
     ws, ws_bytes, _keep = _workspace(need, workspace, x.device, stream)
     (yp, ly), (xp, lx), (gp, lg) = _rows(y), _rows(x), _rows(gate)
@@ -524,18 +540,18 @@ def gated_recurrence_step_device(y, x, gate, lower, state, slots_dev, fresh_dev,
     """``mamba2_gated_recurrence_step_device``: the step with its batch in device memory, as ``decode_step_device``
     takes it (``fresh_dev`` may be None: no sequence is fresh)."""
     import torch
-    cap, dim = int(slots_dev.shape[0]), x.shape[1]
-    _same("x", x, (cap, dim))
-    _same("gate", gate, x.shape, x.dtype)
-    _same("y", y, x.shape, x.dtype)
-    _same("lower", lower, (dim,), torch.float32)
-    _same("state", state, (state.shape[0], dim), torch.float32)
-    _same("slots_dev", slots_dev, (cap,), torch.int32)
-    _same("fresh_dev", fresh_dev, (cap,), torch.uint8)
-    _same("num_seqs_dev", num_seqs_dev, (1,), torch.int32)
-    _same("status_dev", status_dev, (1,), torch.int32)
+    cap, dim, num_slots, i32 = slots_dev.shape[0], x.shape[1], state.shape[0], torch.int32
+    _alike(x, (("gate", gate), ("y", y)), (("lower", lower, (dim,)), ("state", state, (num_slots, dim))))
+    if (x.shape[0] != cap or slots_dev.dtype != i32 or num_seqs_dev.dtype != i32 or status_dev.dtype != i32 or
+            num_seqs_dev.numel() != 1 or status_dev.numel() != 1 or slots_dev.dim() != 1 or
+            (fresh_dev is not None and (fresh_dev.dtype != torch.uint8 or fresh_dev.shape[0] != cap))):
+        _same("x", x, (cap, dim))
+        _same("slots_dev", slots_dev, (cap,), i32)
+        _same("fresh_dev", fresh_dev, (cap,), torch.uint8)
+        _same("num_seqs_dev", num_seqs_dev, (1,), i32)
+        _same("status_dev", status_dev, (1,), i32)
     (yp, ly), (xp, lx), (gp, lg) = _rows(y), _rows(x), _rows(gate)
-    st = _lib().mamba2_gated_recurrence_step_device(yp, xp, gp, _ptr(lower), _ptr(state), state.shape[0], dim, ly, lx,
+    st = _lib().mamba2_gated_recurrence_step_device(yp, xp, gp, _ptr(lower), _ptr(state), num_slots, dim, ly, lx,
                                                     lg, _dt(x), _ptr(slots_dev), _ptr(fresh_dev), _ptr(num_seqs_dev),
                                                     cap, _ptr(status_dev), _stream(stream))
     if check:
@@ -572,15 +588,14 @@ def gated_recurrence_backward(dx, dgate, dlower, dstate, dy, dstate_end, x, gate
 def add_rmsnorm(out, x, weight, eps, residual=None, sum=None, scale=None, stream=None, check=True) -> int:
     """``mamba2_add_rmsnorm``: s = x + residual, out = s / rms(s) * weight; ``sum`` gets s (it may be ``residual``).
     An e4m3 ``out`` takes a ``scale`` per row: out * scale is the normed row."""
-    import torch
     rows, dim = x.shape
     wide = residual if residual is not None else sum
     stype = _dt(wide) if wide is not None else _dt(x)
-    _same("out", out, x.shape)
-    _same("weight", weight, (dim,), torch.float32)
-    _same("residual", residual, x.shape)
-    _same("sum", sum, x.shape, wide.dtype if wide is not None else None)
-    _same("scale", scale, (rows,), torch.float32)
+    if out.shape != x.shape:
+        _same("out", out, x.shape)
+    if wide is not None:
+        _same("sum", wide, x.shape)
+    _alike(wide if wide is not None else x, (("sum", sum),), (("weight", weight, (dim,)), ("scale", scale, (rows,))))
     st = _lib().mamba2_add_rmsnorm(_ptr(out), _ptr(scale), _ptr(sum), _ptr(x), _ptr(residual), _ptr(weight), rows, dim,
                                    float(eps), _dt(x), stype, _type(out), _stream(stream))
     if check:
@@ -616,15 +631,14 @@ def linear(out, x, w, x_scale=None, w_scale=None, bias=None, residual=None, acti
            check=True) -> int:
     """``mamba2_linear``: out = activation(x . w^T * scales + bias) + residual from bf16 or e4m3 operands. x, out and
     residual may be column ranges of wider matrices; ``pre`` gets the pre-activation for the backward pass."""
-    import torch
     (rows, k), n = x.shape, w.shape[0]
-    _same("w", w, (n, k), x.dtype)
-    _same("out", out, (rows, n))
-    _same("x_scale", x_scale, (rows,), torch.float32)
-    _same("w_scale", w_scale, (n,), torch.float32)
-    _same("bias", bias, (n,), torch.float32)
-    _same("residual", residual, (rows, n), out.dtype)
-    _same("pre", pre, (rows, n), torch.bfloat16)
+    if out.shape != (rows, n) or w.shape != (n, k) or w.dtype != x.dtype:
+        _same("w", w, (n, k), x.dtype)
+        _same("out", out, (rows, n))
+    _alike(out, (("residual", residual),), (("x_scale", x_scale, (rows,)), ("w_scale", w_scale, (n,)), ("bias", bias, (n,))))
+    if pre is not None:
+        import torch
+        _same("pre", pre, (rows, n), torch.bfloat16)
     (op, lo), (xp, lx) = _rows(out), _rows(x)
     rp, lr = _rows(residual) if residual is not None else (None, 0)
     st = _lib().mamba2_linear(op, _ptr(pre), xp, _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(bias), rp, rows, k, n, lo,
