@@ -23,6 +23,7 @@
 
 #include <algorithm>
 #include <cstring>
+#include <type_traits>
 
 #include "../../include/block.h"
 #include "common.cuh"
@@ -818,8 +819,8 @@ cudaError_t launch_forward(const Product& g, const void* x, int64_t ldx, const v
 constexpr int kPartRows = 64;
 constexpr int kPartCols = 256;
 
-template <bool kVec>
-__global__ void __launch_bounds__(256) dp_kernel(const LinearBwdArgs a, const int act) {
+template <bool kVec, int act>
+__global__ void __launch_bounds__(256) dp_kernel(const LinearBwdArgs a) {
   __shared__ float sums[8][kPartCols];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c0 = blockIdx.y * kPartCols;
@@ -831,7 +832,7 @@ __global__ void __launch_bounds__(256) dp_kernel(const LinearBwdArgs a, const in
   const __nv_bfloat16* dy = static_cast<const __nv_bfloat16*>(a.dy);
   const __nv_bfloat16* pre = static_cast<const __nv_bfloat16*>(a.pre);
   if (!kVec || col(0) < a.out_f) {
-#pragma unroll 4
+#pragma unroll 2
     for (int i = 0; i < kPartRows / 8; ++i) {
       const int64_t m = m0 + 8 * i + warp;
       if (m >= a.rows) break;
@@ -923,8 +924,17 @@ cudaError_t launch_linear_backward(const LinearBwdArgs& args, int act, cudaStrea
   if (a.dp || a.dbias) {
     const dim3 grid((unsigned)parts, (unsigned)((a.ld_dp + kPartCols - 1) / kPartCols));
     if (grid.y > 65535) return cudaErrorInvalidValue;
-    if (a.out_f % 8 == 0) dp_kernel<true><<<grid, 256, 0, st>>>(a, act);
-    else dp_kernel<false><<<grid, 256, 0, st>>>(a, act);
+    auto run = [&](auto of) {
+      constexpr int kAct = decltype(of)::value;
+      if (a.out_f % 8 == 0) dp_kernel<true, kAct><<<grid, 256, 0, st>>>(a);
+      else dp_kernel<false, kAct><<<grid, 256, 0, st>>>(a);
+    };
+    switch (act) {
+      case MAMBA2_ACT_RELU: run(std::integral_constant<int, MAMBA2_ACT_RELU>{}); break;
+      case MAMBA2_ACT_SILU: run(std::integral_constant<int, MAMBA2_ACT_SILU>{}); break;
+      case MAMBA2_ACT_GELU: run(std::integral_constant<int, MAMBA2_ACT_GELU>{}); break;
+      default: run(std::integral_constant<int, MAMBA2_ACT_NONE>{});
+    }
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess && a.dbias) e = launch_column_sum(a.dbias, a.partial, parts, a.out_f, st);
     if (e != cudaSuccess) return e;
