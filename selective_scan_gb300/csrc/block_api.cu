@@ -281,8 +281,8 @@ mamba2_status mamba2_linear(void* out, void* pre, const void* x, const float* x_
 }
 
 namespace {
-// Rows of dp are padded to a multiple of 16 bytes.
-int64_t ld_dp(int32_t out_features) { return ((int64_t)out_features + 7) / 8 * 8; }
+// Rows of dp are padded to whole blocks of 64 columns.
+int64_t ld_dp(int32_t out_features) { return ((int64_t)out_features + 63) / 64 * 64; }
 size_t dp_bytes(int32_t rows, int32_t out_features) { return align256((size_t)rows * ld_dp(out_features) * 2); }
 }  // namespace
 
