@@ -68,13 +68,19 @@ __device__ __forceinline__ float gelu(float v) {
   normal_tail(v, tail, bell);
   return v * (v < 0.0f ? tail : 1.0f - tail);
 }
-__device__ __forceinline__ float activate(float v, int act) {
-  switch (act) {
-    case MAMBA2_ACT_RELU: return fmaxf(v, 0.0f);
-    case MAMBA2_ACT_SILU: return v * sigmoid_ftz(v);
-    case MAMBA2_ACT_GELU: return gelu(v);
+// (one branch for all of them)
+template <int n>
+__device__ __forceinline__ void activate_all(float (&v)[n], int act) {
+  if (act == MAMBA2_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) v[i] *= sigmoid_ftz(v[i]);
+  } else if (act == MAMBA2_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) v[i] = gelu(v[i]);
+  } else if (act == MAMBA2_ACT_RELU) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) v[i] = fmaxf(v[i], 0.0f);
   }
-  return v;
 }
 __device__ __forceinline__ float slope(float v, int act) {
   switch (act) {
@@ -184,10 +190,7 @@ __device__ __forceinline__ void finish(const Product& g, int64_t row, int col, f
         if (col + j < g.N) p[j] = __float2bfloat16_rn(v[j]);
     }
   }
-  if (g.act != MAMBA2_ACT_NONE) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = activate(v[j], g.act);
-  }
+  activate_all(v, g.act);
   if (g.residual) {
     float r[4];
     Quad<TO>::unpack(res, r);
@@ -550,16 +553,7 @@ pair_kernel(const __grid_constant__ Job<kGrad> job) {
 #pragma unroll
               for (int i = 0; i < 8; ++i, p += 4 * (int64_t)g.N) *reinterpret_cast<uint2*>(p) = Quad<__nv_bfloat16>::pack(v[i]);
             }
-            if (g.act == MAMBA2_ACT_SILU) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i / 4][i % 4] *= sigmoid_ftz(v[i / 4][i % 4]);
-            } else if (g.act == MAMBA2_ACT_GELU) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i / 4][i % 4] = gelu(v[i / 4][i % 4]);
-            } else if (g.act == MAMBA2_ACT_RELU) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i / 4][i % 4] = fmaxf(v[i / 4][i % 4], 0.0f);
-            }
+            activate_all(reinterpret_cast<float(&)[32]>(v), g.act);
             if (g.residual) {
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
@@ -574,11 +568,30 @@ pair_kernel(const __grid_constant__ Job<kGrad> job) {
             for (int i = 0; i < 8; ++i, o += 4 * g.ld_out)
               *reinterpret_cast<typename Quad<TO>::Raw*>(o) = Quad<TO>::pack(v[i]);
           } else {
+            // an edge of the matrix, or rows of any alignment: a row an instruction, a column a lane
+            const int one = n0 + c + lane;
+            const int rows = (int)min((int64_t)32, g.M - row0);
+            if (one < g.N) {
+              const float sc = g.scale_n ? g.scale_n[one] : 1.0f, bi = g.bias ? g.bias[one] : 0.0f;
+              const TO* res = g.residual ? static_cast<const TO*>(g.residual) + row0 * g.ld_res + one : nullptr;
+              TO* o = static_cast<TO*>(g.out) + row0 * g.ld_out + one;
 #pragma unroll 1
-            for (int i = 0; i < 8; ++i) {
-              const float4 f = *reinterpret_cast<const float4*>(mine + 4 * i * kEpiLd);
-              float v[4] = {f.x, f.y, f.z, f.w};
-              finish<TO>(g, row + 4 * i, col, v, now.cols, load_residual<TO>(g, row + 4 * i, col));
+              for (int r0 = 0; r0 < rows; r0 += 8) {
+                float v[8], add[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  add[i] = res && r0 + i < rows ? Act<TO>::to_f(res[(r0 + i) * g.ld_res]) : 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = fmaf(blk[(r0 + i) * kEpiLd + lane], sc, bi);
+                if (g.pre)
+#pragma unroll
+                  for (int i = 0; i < 8; ++i)
+                    if (r0 + i < rows) g.pre[(row0 + r0 + i) * g.N + one] = __float2bfloat16_rn(v[i]);
+                activate_all(v, g.act);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  if (r0 + i < rows) o[(r0 + i) * g.ld_out] = Act<TO>::from_f(v[i] + add[i]);
+              }
             }
           }
           __syncwarp();
