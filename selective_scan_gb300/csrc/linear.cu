@@ -575,22 +575,38 @@ pair_kernel(const __grid_constant__ Job<kGrad> job) {
               const float sc = g.scale_n ? g.scale_n[one] : 1.0f, bi = g.bias ? g.bias[one] : 0.0f;
               const TO* res = g.residual ? static_cast<const TO*>(g.residual) + row0 * g.ld_res + one : nullptr;
               TO* o = static_cast<TO*>(g.out) + row0 * g.ld_out + one;
-#pragma unroll 1
-              for (int r0 = 0; r0 < rows; r0 += 8) {
-                float v[8], add[8];
+              __nv_bfloat16* pre = g.pre ? g.pre + row0 * g.N + one : nullptr;
+              const float* from = blk + lane;
+              constexpr int kSome = 16;
+              auto some = [&](auto all, int left) {  // kSome rows, `left` of them there
+                constexpr bool kAll = decltype(all)::value;
+                float v[kSome], add[kSome];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  add[i] = res && r0 + i < rows ? Act<TO>::to_f(res[(r0 + i) * g.ld_res]) : 0.0f;
+                for (int i = 0; i < kSome; ++i) v[i] = fmaf(from[i * kEpiLd], sc, bi);
+                from += kSome * kEpiLd;
+                if (res) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = fmaf(blk[(r0 + i) * kEpiLd + lane], sc, bi);
-                if (g.pre)
+                  for (int i = 0; i < kSome; ++i, res += g.ld_res)
+                    if (kAll || i < left) add[i] = Act<TO>::to_f(*res);
+                }
+                if (pre) {
 #pragma unroll
-                  for (int i = 0; i < 8; ++i)
-                    if (r0 + i < rows) g.pre[(row0 + r0 + i) * g.N + one] = __float2bfloat16_rn(v[i]);
+                  for (int i = 0; i < kSome; ++i, pre += g.N)
+                    if (kAll || i < left) *pre = __float2bfloat16_rn(v[i]);
+                }
                 activate_all(v, g.act);
+                if (res) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  if (r0 + i < rows) o[(r0 + i) * g.ld_out] = Act<TO>::from_f(v[i] + add[i]);
+                  for (int i = 0; i < kSome; ++i) v[i] += add[i];
+                }
+#pragma unroll
+                for (int i = 0; i < kSome; ++i, o += g.ld_out)
+                  if (kAll || i < left) *o = Act<TO>::from_f(v[i]);
+              };
+#pragma unroll 1
+              for (int left = rows; left > 0; left -= kSome) {
+                if (left >= kSome) some(std::true_type{}, left);
+                else some(std::false_type{}, left);
               }
             }
           }
