@@ -682,7 +682,7 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ CUtens
     const V in2 = P::make(in);
     auto emit = [&](auto whole) {
 #pragma unroll
-      for (int j = 0; j < kTok; ++j)
+      for (int j = 0; j < kTok; ++j, ty += a.ld_y)
         if (decltype(whole)::value || j < nt) {
           float y[C];
           if constexpr (kVec) {
@@ -693,7 +693,7 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ CUtens
           } else {
             P::split(P::fma(ps[j], in2, hs[j]), y);
           }
-          store_row<T, kVec && decltype(whole)::value>(ty + j * a.ld_y, y, left);
+          store_row<T, kVec && decltype(whole)::value>(ty, y, left);
         }
     };
     if (nt == kTok && (f.group + 1) * kTileCh<T> <= a.dim) emit(std::true_type{});
@@ -905,12 +905,12 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUt
       }
     }
     // ---- backwards over the tokens
-    T* ox = static_cast<T*>(a.dx) + (f.row + warp * kTok) * a.ld_dx + ch0;
-    T* og = static_cast<T*>(a.dgate) + (f.row + warp * kTok) * a.ld_dgate + ch0;
+    T* ox = static_cast<T*>(a.dx) + (f.row + warp * kTok + kTok - 1) * a.ld_dx + ch0;
+    T* og = static_cast<T*>(a.dgate) + (f.row + warp * kTok + kTok - 1) * a.ld_dgate + ch0;
     V in2 = P::fma(P::make(ea), P::make(in), P::make(eb)), dlo2 = P::all(0.0f);
     auto emit = [&](auto whole) {
 #pragma unroll
-      for (int j = kTok - 1; j >= 0; --j)
+      for (int j = kTok - 1; j >= 0; --j, ox -= a.ld_dx, og -= a.ld_dgate)
         if (decltype(whole)::value || j < nt) {
           const int r = warp * kTok + j;
           float x[C], d[C], vx[C], vg[C];
@@ -925,8 +925,8 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUt
           P::split(P::mul(P::mul(dd, un2), up), vg);
           dlo2 = P::add(dlo2, dd);
           in2 = P::mul(ft, G);
-          store_row<T, kVec && decltype(whole)::value>(ox + j * a.ld_dx, vx, left);
-          store_row<T, kVec && decltype(whole)::value>(og + j * a.ld_dgate, vg, left);
+          store_row<T, kVec && decltype(whole)::value>(ox, vx, left);
+          store_row<T, kVec && decltype(whole)::value>(og, vg, left);
         }
     };
     if (nt == kTok && (f.group + 1) * kTileCh<T> <= a.dim) emit(std::true_type{});
