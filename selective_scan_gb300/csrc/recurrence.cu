@@ -708,26 +708,31 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ CUtens
 
 // ------------------------------------------------------------------ backward
 
-constexpr int kBwdStages = 2;
+// One stage, so that three CTAs fit an SM (the gates are made twice for that, too: kept, they take the registers of
+// the third): 320 us against 337 for one run of 65 536 tokens by 2 048 channels with two stages and two CTAs, which
+// word by word keeps. (A tile taken further ahead is waited for longer: with the next tile's ticket taken and its
+// rows fetched into L2 meanwhile it was 385.)
+template <bool kVec> constexpr int kBwdStages = kVec ? 1 : 2;
+template <typename T, bool kVec> constexpr int kBwdCtas = kVec ? 3 : 2;
 template <bool kVec> constexpr int kBwdStage = 3 * kChunkR * kPitch<kVec>;
 
-template <typename T>
+template <typename T, bool kVec>
 struct BwdShared {
   Info info[kInfos];
   float A[kWarps][kTileCh<T>], R[kWarps][kTileCh<T>];
   Before<T> before;
   float dlo[kWarps][kTileCh<T>];
-  alignas(8) uint64_t full[kBwdStages][kWarps];
+  alignas(8) uint64_t full[kBwdStages<kVec>][kWarps];
   uint32_t abort;
 };
 
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, kBwdCtas<T, kVec>)
 rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUtensorMap mx,
                const __grid_constant__ CUtensorMap mg, const __grid_constant__ CUtensorMap md,
                const __grid_constant__ Chain ch, float* part, const int items, const int groups) {
   extern __shared__ __align__(128) unsigned char stages[];
-  __shared__ BwdShared<T> s;
+  __shared__ BwdShared<T, kVec> s;
   constexpr int C = kCh<T>;
   using P = Pack<C>;
   using V = typename P::V;
@@ -744,10 +749,10 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUt
                                    {static_cast<const T*>(a.gate), a.ld_gate, &mg},
                                    {static_cast<const T*>(a.dy), a.ld_dy, &md}};
   auto load = [&](int i) {
-    load_tile<T, kVec, 3>(s.info[i % kInfos], in_streams, su32(stages) + (uint32_t)(i % kBwdStages) * kBwdStage<kVec>,
-                          su32(&s.full[i % kBwdStages][warp]), a.dim, warp, lane);
+    load_tile<T, kVec, 3>(s.info[i % kInfos], in_streams, su32(stages) + (uint32_t)(i % kBwdStages<kVec>) * kBwdStage<kVec>,
+                          su32(&s.full[i % kBwdStages<kVec>][warp]), a.dim, warp, lane);
   };
-  if (threadIdx.x < kBwdStages * kWarps) {
+  if (threadIdx.x < kBwdStages<kVec> * kWarps) {
     mbar_init(su32(&s.full[0][0] + threadIdx.x), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     s.abort = 0u;
@@ -765,10 +770,10 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUt
     }
   };
   if (threadIdx.x == 0)
-    for (int i = 0; i < kBwdStages; ++i)
-      tile_info<true>(s.info[i], a.tab, take<kBwdStages>(ch, i, items), items, groups);
+    for (int i = 0; i < kBwdStages<kVec>; ++i)
+      tile_info<true>(s.info[i], a.tab, take<kBwdStages<kVec>>(ch, i, items), items, groups);
   __syncthreads();
-  for (int i = 0; i < kBwdStages; ++i) load(i);
+  for (int i = 0; i < kBwdStages<kVec>; ++i) load(i);
 
   uint32_t phases = 0;
   int i = 0;
@@ -778,7 +783,7 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUt
     const int ch0 = f.group * kTileCh<T> + lane * C;
     const int left = a.dim - ch0;
     int next = 0;
-    if (threadIdx.x == 0) next = take<kBwdStages>(ch, i + kBwdStages, items);
+    if (threadIdx.x == 0) next = take<kBwdStages<kVec>>(ch, i + kBwdStages<kVec>, items);
     const int first = a.tab.tile[f.seq];
     const int before = f.l > 0 ? maps_before(f.l) : 0;
     float h0[C];
@@ -786,7 +791,7 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUt
 #pragma unroll
       for (int c = 0; c < C; ++c)
         h0[c] = c < left && a.dstate_end ? a.dstate_end[(int64_t)f.seq * a.dim + ch0 + c] : 0.0f;
-    const unsigned char* st = stages + (i % kBwdStages) * kBwdStage<kVec>;
+    const unsigned char* st = stages + (i % kBwdStages<kVec>) * kBwdStage<kVec>;
     const T* tx = static_cast<const T*>(a.x) + f.row * a.ld_x + f.group * kTileCh<T>;
     const T* tg = static_cast<const T*>(a.gate) + f.row * a.ld_gate + f.group * kTileCh<T>;
     const T* td = static_cast<const T*>(a.dy) + f.row * a.ld_dy + f.group * kTileCh<T>;
@@ -801,41 +806,27 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUt
     const int nt = min(kTok, f.n - warp * kTok);
     if constexpr (kVec) {
       if (nt > 0) {
-        warp_wait(su32(&s.full[i % kBwdStages][warp]), phases >> (i % kBwdStages) & 1u, &s.abort);
-        phases ^= 1u << (i % kBwdStages);
+        warp_wait(su32(&s.full[i % kBwdStages<kVec>][warp]), phases >> (i % kBwdStages<kVec>) & 1u, &s.abort);
+        phases ^= 1u << (i % kBwdStages<kVec>);
       }
     } else {
-      cp_wait<kBwdStages - 1>();
+      cp_wait<kBwdStages<kVec> - 1>();
       __syncwarp();
     }
     // ---- the states from the checkpoint on, and R's map (A, R)
-    V sg[kTok];  // the smaller sigmoid, signed as the gate
     V hs[kTok];  // the state before the token
     V A2 = P::all(1.0f), R2 = P::all(0.0f), hp2 = P::make(hp);
-    auto gates = [&](V v, V& up, V& down, V& ft) {
-      float g[C], m[C];
-      P::split(v, g);
-#pragma unroll
-      for (int c = 0; c < C; ++c) m[c] = fabsf(g[c]);
-      pick<C>(P::make(m), g, up, down);
-      ft = P::fma(un2, up, lo2);
-    };
     auto scan = [&](auto whole) {
 #pragma unroll
       for (int j = 0; j < kTok; ++j)
         if (decltype(whole)::value || j < nt) {
           const int r = warp * kTok + j;
-          float x[C], g[C], d[C], m[C];
+          float x[C], g[C], d[C];
           unpack_word<T>(staged<T, kVec>(st, r, lane, tx, a.ld_x), x);
           unpack_word<T>(staged<T, kVec>(st + kMat, r, lane, tg, a.ld_gate), g);
           unpack_word<T>(staged<T, kVec>(st + 2 * kMat, r, lane, td, a.ld_dy), d);
-          const V small = small_sigmoid<C>(g);
           V up, down;
-          pick<C>(small, g, up, down);
-          P::split(small, m);
-#pragma unroll
-          for (int c = 0; c < C; ++c) m[c] = copysignf(m[c], g[c]);
-          sg[j] = P::make(m);
+          both_sigmoids<C>(g, up, down);
           const V ft = P::fma(un2, up, lo2);
           hs[j] = hp2;
           hp2 = P::fma(ft, hp2, P::mul(P::mul(un2, down), P::make(x)));
@@ -888,7 +879,7 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUt
     }
     look_back<T, true>(ch, f, first, groups, before, s.before, warp, lane);
     // info[i + 2] takes the place of tile i - 2, whose part of dlower has been summed
-    if (threadIdx.x == 0) tile_info<true>(s.info[(i + kBwdStages) % kInfos], a.tab, next, items, groups);
+    if (threadIdx.x == 0) tile_info<true>(s.info[(i + kBwdStages<kVec>) % kInfos], a.tab, next, items, groups);
     __syncthreads();
     float in[C];
     fold_before(s.before, before, in, lane);
@@ -913,11 +904,13 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUt
       for (int j = kTok - 1; j >= 0; --j, ox -= a.ld_dx, og -= a.ld_dgate)
         if (decltype(whole)::value || j < nt) {
           const int r = warp * kTok + j;
-          float x[C], d[C], vx[C], vg[C];
+          float x[C], g[C], d[C], vx[C], vg[C];
           unpack_word<T>(staged<T, kVec>(st, r, lane, tx, a.ld_x), x);
+          unpack_word<T>(staged<T, kVec>(st + kMat, r, lane, tg, a.ld_gate), g);
           unpack_word<T>(staged<T, kVec>(st + 2 * kMat, r, lane, td, a.ld_dy), d);
-          V up, down, ft;
-          gates(sg[j], up, down, ft);
+          V up, down;
+          both_sigmoids<C>(g, up, down);
+          const V ft = P::fma(un2, up, lo2);
           const V G = P::add(in2, P::make(d));
           // df sigmoid(-g), with df = G (h - x)
           const V dd = P::mul(P::mul(G, P::fma(P::make(x), P::all(-1.0f), hs[j])), down);
@@ -936,7 +929,7 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUt
 #pragma unroll
     for (int c = 0; c < C; ++c) s.dlo[warp][lane * C + c] = dlo[c];
     __syncwarp();  // every lane is done with this stage
-    load(i + kBwdStages);
+    load(i + kBwdStages<kVec>);
   }
   __syncthreads();
   if (warp == 1 && i > 0 && part) sum_part(i - 1);
@@ -1122,7 +1115,7 @@ cudaError_t run_fwd(const RecArgs& a, const Chain& ch, int items, int groups, cu
 }
 template <typename T, bool kVec>
 cudaError_t run_bwd(const RecBwdArgs& a, const Chain& ch, float* part, int items, int groups, cudaStream_t st) {
-  constexpr int smem = kBwdStages * kBwdStage<kVec>;
+  constexpr int smem = kBwdStages<kVec> * kBwdStage<kVec>;
   CUtensorMap mx, mg, md;
   std::memset(&mx, 0, sizeof mx);
   std::memset(&mg, 0, sizeof mg);
@@ -1134,7 +1127,7 @@ cudaError_t run_bwd(const RecBwdArgs& a, const Chain& ch, float* part, int items
     return cudaErrorInvalidValue;
   const cudaError_t e = cudaFuncSetAttribute(rec_bwd_kernel<T, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  rec_bwd_kernel<T, kVec><<<ctas(items, 2), kThreads, smem, st>>>(a, mx, mg, md, ch, part, items, groups);
+  rec_bwd_kernel<T, kVec><<<ctas(items, kBwdCtas<T, kVec>), kThreads, smem, st>>>(a, mx, mg, md, ch, part, items, groups);
   return cudaGetLastError();
 }
 
