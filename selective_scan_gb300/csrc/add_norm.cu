@@ -21,7 +21,7 @@ namespace {
 
 // elements of a row that a thread holds
 constexpr int held_by_thread(int unit, int sum_bytes, bool backward) {
-  return unit == 1 || (backward && sum_bytes == 4) ? 16 : 32;
+  return unit == 1 || backward ? 16 : 32;
 }
 constexpr int kCtaThreads = 256;
 constexpr int kMaxThreads = 512;
@@ -419,12 +419,20 @@ cudaError_t run_norm_bwd(const AddNormBwdArgs& a, int* used, cudaStream_t st) {
     return cudaGetLastError();
   }
   const Shape s = shape(a.rows, a.dim, unit, held);
-  const int parts = *used = std::min(most, (a.rows + s.rows - 1) / s.rows);
-  cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t c = config(parts, dim3(s.nt, s.rows), s.rows > 1 ? (size_t)a.dim * 4 : 0, st, &attr);
-  if (unit == 8) return cudaLaunchKernelEx(&c, add_norm_bwd_kernel<T, S, 8>, a, s.nt);
-  if (unit == 2) return cudaLaunchKernelEx(&c, add_norm_bwd_kernel<T, S, 2>, a, s.nt);
-  return cudaLaunchKernelEx(&c, add_norm_bwd_kernel<T, S, 1>, a, s.nt);
+  const size_t smem = s.rows > 1 ? (size_t)a.dim * 4 : 0;
+  auto run = [&](auto kernel) {  // as many CTAs as the GPU holds: each loads a row while others work on theirs
+    int fit = 0;
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, s.nt * s.rows, smem);
+    if (e != cudaSuccess) return e;
+    *used = (int)std::min<int64_t>({(int64_t)most, ((int64_t)a.rows + s.rows - 1) / s.rows,
+                                    std::max(1, fit) * (int64_t)device_sm_count()});
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t c = config(*used, dim3(s.nt, s.rows), smem, st, &attr);
+    return cudaLaunchKernelEx(&c, kernel, a, s.nt);
+  };
+  if (unit == 8) return run(add_norm_bwd_kernel<T, S, 8>);
+  if (unit == 2) return run(add_norm_bwd_kernel<T, S, 2>);
+  return run(add_norm_bwd_kernel<T, S, 1>);
 }
 
 }  // namespace
@@ -438,8 +446,8 @@ cudaError_t launch_add_rmsnorm(const AddNormArgs& a, mamba2_dtype act, mamba2_dt
   return f8 ? run_norm<B, B, true>(a, st) : run_norm<B, B, false>(a, st);
 }
 
-// CTAs of the backward kernel at most (each writes one row of partial sums): two to an SM.
-int add_rmsnorm_backward_parts(int32_t rows, int32_t) { return (int)std::min<int64_t>(rows, 2 * (int64_t)device_sm_count()); }
+// CTAs of the backward kernel at most (each writes one row of partial sums): eight to an SM.
+int add_rmsnorm_backward_parts(int32_t rows, int32_t) { return (int)std::min<int64_t>(rows, 8 * (int64_t)device_sm_count()); }
 
 cudaError_t launch_add_rmsnorm_backward(const AddNormBwdArgs& a, mamba2_dtype act, mamba2_dtype sum_type,
                                         cudaStream_t st) {
