@@ -944,99 +944,110 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUt
 // bound by HBM, a small one by the launch, so a device batch of up to kCheckHere sequences is checked by every
 // CTA itself before it touches anything, instead of by a kernel of its own.
 constexpr int kStepThreads = 256;
-constexpr int kCheckHere = 256;
+constexpr int kCheckHere = kStepThreads;
+constexpr int kSeenWords = 1024;  // slots that a bitmap in shared memory holds: 32 times as many
 
 // The status of a device batch, as launch_check_device_batch finds it: the count, then the slots' range, then
-// whether two sequences share one. All threads of the CTA call it and get the same answer.
-__device__ __forceinline__ int check_batch(const RecStepArgs& a, int num, int32_t* slots) {
-  __shared__ int worst;  // bit 0: a slot out of range, bit 1: a slot twice
-  if (num < 0 || num > a.n) return MAMBA2_ERR_INVALID_ARGUMENT;
-  if (threadIdx.x == 0) worst = 0;
-  // past the end: a value of its own in each place, which no slot equals
-  for (int i = threadIdx.x; i < kCheckHere; i += kStepThreads) slots[i] = i < num ? a.dev_slots[i] : -1 - i;
-  __syncthreads();
-  int bad = 0;
-  for (int i = threadIdx.x; i < num; i += kStepThreads) {
-    const int mine = slots[i];
-    if (mine < 0 || mine >= a.num_slots) bad |= 1;
-    for (int j = 0; j < i; j += 4) {
-      const int4 v = *reinterpret_cast<const int4*>(slots + j);
-      if (v.x == mine || (v.y == mine && j + 1 < i) || (v.z == mine && j + 2 < i) || (v.w == mine && j + 3 < i)) bad |= 2;
+// whether two sequences share one. mine: the slot of sequence threadIdx.x. All threads of the CTA call it and get
+// the same answer. A pool of more slots than the bitmap holds is compared pair by pair.
+__device__ __forceinline__ int check_batch(int num, int capacity, int num_slots, int mine) {
+  __shared__ uint32_t seen[kSeenWords];
+  if (num < 0 || num > capacity) return MAMBA2_ERR_INVALID_ARGUMENT;
+  const int me = (int)threadIdx.x;
+  const bool in = me < num, small = num_slots <= 32 * kSeenWords;
+  int bad = in && (mine < 0 || mine >= num_slots) ? 1 : 0;
+  if (small) {
+    for (int w = me; w < (num_slots + 31) / 32; w += kStepThreads) seen[w] = 0u;
+    __syncthreads();
+    if (in && !bad) {
+      const uint32_t bit = 1u << (mine & 31);
+      if (atomicOr(&seen[mine >> 5], bit) & bit) bad = 2;
     }
+  } else {
+    seen[me] = (uint32_t)mine;
+    __syncthreads();
+    if (in)
+      for (int j = 0; j < me; ++j)
+        if (seen[j] == (uint32_t)mine) bad |= 2;
   }
-  if (bad) atomicOr(&worst, bad);
-  __syncthreads();
-  return worst & 1 ? MAMBA2_ERR_SLOT_OUT_OF_RANGE : worst & 2 ? MAMBA2_ERR_SLOT_SHARED : MAMBA2_OK;
+  if (__syncthreads_or(bad & 1)) return MAMBA2_ERR_SLOT_OUT_OF_RANGE;
+  return __syncthreads_or(bad) ? MAMBA2_ERR_SLOT_SHARED : MAMBA2_OK;
 }
 
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kStepThreads) rec_step_kernel(const __grid_constant__ RecStepArgs a) {
-  __shared__ __align__(16) int32_t slots[kCheckHere];
   const int i = blockIdx.y;
-  int slot;
+  // everything is asked for before anything is waited for: the batch, the inputs, and, as soon as the slot is known
+  // to be one, its state (a batch that turns out bad is not written)
+  int slot, num = a.n, mine = 0;
   bool fresh;
   if (a.dev_slots) {
-    const int num = *a.dev_n;
-    if (a.n <= kCheckHere) {
-      const int status = check_batch(a, num, slots);
-      if (blockIdx.x == 0 && i == 0 && threadIdx.x == 0) *a.dev_status = status;
-      if (status != MAMBA2_OK) return;
-    } else if (*a.dev_status != MAMBA2_OK) {
-      return;
-    }
-    if (i >= num) return;
+    num = *a.dev_n;
     slot = a.dev_slots[i];
     fresh = a.dev_fresh && a.dev_fresh[i];
+    if (a.n <= kCheckHere && (int)threadIdx.x < a.n) mine = a.dev_slots[threadIdx.x];
   } else {
     slot = (int)(a.slot_fresh[i] & 0x7fffffffu);
     fresh = (a.slot_fresh[i] >> 31) != 0u;
   }
   const int c0 = blockIdx.x * 4 * kStepThreads;
   auto channel = [&](int j) { return c0 + (kVec ? 4 * (int)threadIdx.x + j : (int)threadIdx.x + j * kStepThreads); };
-  float* st = a.state + (int64_t)slot * a.dim;
   const T* x = static_cast<const T*>(a.x) + i * a.ld_x;
   const T* gate = static_cast<const T*>(a.gate) + i * a.ld_gate;
-  T* y = static_cast<T*>(a.y) + i * a.ld_y;
   float xv[4], gv[4], h[4], lo[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) xv[j] = gv[j] = h[j] = lo[j] = 0.0f;
+  auto four = [](const auto* p, float (&v)[4]) {
+    if constexpr (sizeof(*p) == 4) {
+      const float4 f = *reinterpret_cast<const float4*>(p);
+      v[0] = f.x;
+      v[1] = f.y;
+      v[2] = f.z;
+      v[3] = f.w;
+    } else {
+      const uint2 w = *reinterpret_cast<const uint2*>(p);
+      v[0] = __uint_as_float(w.x << 16);
+      v[1] = __uint_as_float(w.x & 0xffff0000u);
+      v[2] = __uint_as_float(w.y << 16);
+      v[3] = __uint_as_float(w.y & 0xffff0000u);
+    }
+  };
+  const bool any = channel(0) < a.dim;  // (kVec: all four or none)
   if constexpr (kVec) {
-    if (channel(0) >= a.dim) return;
-    auto four = [](const T* p, float (&v)[4]) {
-      if constexpr (sizeof(T) == 4) {
-        const float4 f = *reinterpret_cast<const float4*>(p);
-        v[0] = f.x;
-        v[1] = f.y;
-        v[2] = f.z;
-        v[3] = f.w;
-      } else {
-        const uint2 w = *reinterpret_cast<const uint2*>(p);
-        v[0] = __uint_as_float(w.x << 16);
-        v[1] = __uint_as_float(w.x & 0xffff0000u);
-        v[2] = __uint_as_float(w.y << 16);
-        v[3] = __uint_as_float(w.y & 0xffff0000u);
-      }
-    };
-    const float4 none = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const float4 hs = fresh ? none : *reinterpret_cast<const float4*>(st + channel(0));
-    const float4 ls = a.lower ? *reinterpret_cast<const float4*>(a.lower + channel(0)) : none;
-    four(x + channel(0), xv);
-    four(gate + channel(0), gv);
-    h[0] = hs.x;
-    h[1] = hs.y;
-    h[2] = hs.z;
-    h[3] = hs.w;
-    lo[0] = ls.x;
-    lo[1] = ls.y;
-    lo[2] = ls.z;
-    lo[3] = ls.w;
+    if (any) {
+      four(x + channel(0), xv);
+      four(gate + channel(0), gv);
+      if (a.lower) four(a.lower + channel(0), lo);
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (channel(j) < a.dim) {
         xv[j] = Act<T>::to_f(x[channel(j)]);
         gv[j] = Act<T>::to_f(gate[channel(j)]);
-        h[j] = fresh ? 0.0f : st[channel(j)];
-        lo[j] = a.lower ? a.lower[channel(j)] : 0.0f;
+        if (a.lower) lo[j] = a.lower[channel(j)];
       }
+  }
+  const bool is_slot = slot >= 0 && slot < a.num_slots;
+  float* st = a.state + (int64_t)(is_slot ? slot : 0) * a.dim;
+  if (is_slot && !fresh) {
+    if constexpr (kVec) {
+      if (any) four(st + channel(0), h);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (channel(j) < a.dim) h[j] = st[channel(j)];
+    }
+  }
+  if (a.dev_slots) {
+    if (a.n <= kCheckHere) {
+      const int status = check_batch(num, a.n, a.num_slots, mine);
+      if (blockIdx.x == 0 && i == 0 && threadIdx.x == 0) *a.dev_status = status;
+      if (status != MAMBA2_OK) return;
+    } else if (*a.dev_status != MAMBA2_OK) {
+      return;
+    }
+    if (i >= num) return;
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -1044,7 +1055,9 @@ __global__ void __launch_bounds__(kStepThreads) rec_step_kernel(const __grid_con
     sigmoids(gv[j], up, down);
     h[j] = fmaf(fmaf(1.0f - lo[j], up, lo[j]), h[j], (1.0f - lo[j]) * down * xv[j]);
   }
+  T* y = static_cast<T*>(a.y) + i * a.ld_y;
   if constexpr (kVec) {
+    if (!any) return;
     *reinterpret_cast<float4*>(st + channel(0)) = make_float4(h[0], h[1], h[2], h[3]);
     if constexpr (sizeof(T) == 4) {
       *reinterpret_cast<float4*>(y + channel(0)) = make_float4(h[0], h[1], h[2], h[3]);

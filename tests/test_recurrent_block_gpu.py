@@ -271,6 +271,27 @@ def test_step_device_batch_sizes(capacity, dtype, dim):
             assert torch.equal(st.cpu(), pool) and (y == 7.0).all()
 
 
+def test_step_device_batch_of_a_large_pool():
+    """More slots than the check's bitmap holds: the slots are compared pair by pair."""
+    dev = device()
+    n, dim, slots_n = 200, 12, 40000
+    x, gate, _, _, _, _ = rec_inputs(77, [n], dim, F32, False)
+    pool = randn(78, slots_n, dim)
+    slots = torch.randperm(slots_n, generator=torch.Generator().manual_seed(79))[:n].tolist()
+    ref = R.recurrence(x, gate, None, pool, cu_of([1] * n), slots, [0] * n)
+    for twice in (False, True):
+        s = slots[:-1] + [slots[3]] if twice else slots
+        st, y, code = pool.to(dev), torch.full((n, dim), 7.0, device=dev), torch.full((1,), -1, dtype=torch.int32, device=dev)
+        ss.gated_recurrence_step_device(y, x.to(dev), gate.to(dev), None, st, torch.tensor(s, dtype=torch.int32, device=dev),
+                                        None, torch.tensor([n], dtype=torch.int32, device=dev), code)
+        assert int(code.item()) == (ss.ERR_SLOT_SHARED if twice else ss.OK)
+        if twice:
+            assert torch.equal(st.cpu(), pool) and (y == 7.0).all()
+        else:
+            R.check(y, ref["y"], "y")
+            R.check(st[slots], tuple(v[slots] for v in ref["pool"]), "state")
+
+
 def test_recurrence_past_32_bit_offsets():
     dev = device()
     dim, ld = 64, 1 << 28  # row 9 begins past 2^31 elements
