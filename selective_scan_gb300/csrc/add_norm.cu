@@ -1,13 +1,17 @@
 // RMS norm with the residual's addition (block.h), its 8-bit output, and its backward pass.
 // Each reads its inputs from HBM once and writes its outputs once, and that bounds it.
 //
-// A row lives in the registers of `nt` threads, 32 elements each at most (16 where registers would not
-// do: single elements, and fp32 in the backward pass), read and written in units of 16 bytes of bf16 (8
-// elements) where the width allows, else of 2 elements or 1. nt is the fewest whole warps that hold the
-// row, so all of a row's loads are on the way at once; with fewer rows than SMs a row is spread further,
-// up to a thread per unit. Several rows share a CTA up to 256 threads. Sums of squares go warp by warp and
-// then over the warps in order, in fp32. Rows wider than 512 threads hold are read again from L2 instead
-// (the streamed kernels).
+// A row lives in the registers of `nt` threads, 32 elements each at most (16 as single elements and in the
+// backward pass, whose threads also hold their columns' sums), read and written in units of 16 bytes of bf16 (8
+// elements) where the width allows, else of 2 elements or 1. nt is the fewest whole warps that hold the row, so
+// all of a row's loads are on the way at once; with fewer rows than SMs a row is spread further, up to a thread
+// per unit. Several rows share a CTA up to 256 threads. Sums of squares go warp by warp and then over the warps
+// in order, in fp32. Rows wider than 512 threads hold are read again from L2 instead (the streamed kernels).
+//
+// Measured (GB300): 16 384 x 2 560, bf16 with a 32-bit sum, 74 us (6.8 TB/s, the measured copy rate); backward
+// of 16 384 x 2 048, bf16, 51 us (5.3 TB/s; 5 of them the column sums' own kernel), of 16 384 x 2 560 with a
+// 32-bit sum 84 us (6.0 TB/s). A backward CTA loads a row, reduces and stores in turn, so the rate follows the
+// CTAs that an SM holds: with 32 elements a thread and two of them it was 54 and 118 us, with 8 elements 61.
 #include <cuda_fp8.h>
 
 #include <algorithm>
