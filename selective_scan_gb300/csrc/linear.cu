@@ -684,36 +684,44 @@ few_rows_kernel(const __grid_constant__ Product g, const __grid_constant__ CUten
   const int kblocks = (g.K + depth - 1) / depth, S = (int)gridDim.x, rank = (int)blockIdx.x;
   const int kb0 = (int)((int64_t)kblocks * rank / S), n_kb = (int)((int64_t)kblocks * (rank + 1) / S) - kb0;
   const int n0 = (int)blockIdx.y * 128, m0 = (int)blockIdx.z * kN;
+  auto load = [&](int i) {  // the i-th k-block of this CTA's
+    const int s = i % L::kStages;
+    const uint32_t dst = sbase + (uint32_t)s * L::kStage;
+    mbar_expect_tx(bar(L::kFull + s), L::kStage);
+    tma_load_2d(dst, &tmw, (kb0 + i) * depth, n0, bar(L::kFull + s));
+    tma_load_2d(dst + L::kTileW, &tmx, (kb0 + i) * depth, m0, bar(L::kFull + s));
+  };
 
   if (warp == 0) {
+    // the first turn of the stages is under way before anything else is set up
+    if (lane == 0) {
+      for (int s = 0; s < L::kStages; ++s) {
+        mbar_init(bar(L::kFull + s), 1);
+        mbar_init(bar(L::kEmpty + s), 1);
+      }
+      mbar_init(bar(L::kDone), 1);
+      *s_abort = 0u;
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+      asm volatile("griddepcontrol.wait;" ::: "memory");  // launched as a programmatic dependent
+      for (int i = 0; i < min(n_kb, L::kStages); ++i) load(i);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(su32(s_tmem)), "n"(L::kCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  if (threadIdx.x == 32) {
-    for (int s = 0; s < L::kStages; ++s) {
-      mbar_init(bar(L::kFull + s), 1);
-      mbar_init(bar(L::kEmpty + s), 1);
-    }
-    mbar_init(bar(L::kDone), 1);
-    *s_abort = 0u;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched as a programmatic dependent
 
   if (warp == 0) {
     if (lane == 0) {
-      int issued = 0;
-      for (int i = 0; i < n_kb; ++i) {
-        const int s = i % L::kStages;
-        if (i >= L::kStages && !wait_bar(bar(L::kEmpty + s), (uint32_t)((i / L::kStages - 1) & 1), s_abort)) break;
-        const uint32_t dst = sbase + (uint32_t)s * L::kStage;
-        mbar_expect_tx(bar(L::kFull + s), L::kStage);
-        tma_load_2d(dst, &tmw, (kb0 + i) * depth, n0, bar(L::kFull + s));
-        tma_load_2d(dst + L::kTileW, &tmx, (kb0 + i) * depth, m0, bar(L::kFull + s));
+      int issued = min(n_kb, L::kStages);
+      for (int i = L::kStages; i < n_kb; ++i) {
+        if (!wait_bar(bar(L::kEmpty + i % L::kStages), (uint32_t)((i / L::kStages - 1) & 1), s_abort)) break;
+        load(i);
         issued = i + 1;
       }
       if (*s_abort)
@@ -781,7 +789,7 @@ few_rows_kernel(const __grid_constant__ Product g, const __grid_constant__ CUten
   if (threadIdx.x == 0 && *s_abort) atomicAdd(&g_linear_timeouts, 1u);
   __syncthreads();
   cluster_sync();  // nobody reads this CTA's parts any more
-  if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "n"(L::kCols));
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "n"(L::kCols));
 }
 
 // ------------------------------------------------------------------ tensor maps
