@@ -11,7 +11,8 @@
 // Measured (GB300): 16 384 x 2 560, bf16 with a 32-bit sum, 74 us (6.8 TB/s, the measured copy rate); backward
 // of 16 384 x 2 048, bf16, 51 us (5.3 TB/s; 5 of them the column sums' own kernel), of 16 384 x 2 560 with a
 // 32-bit sum 84 us (6.0 TB/s). A backward CTA loads a row, reduces and stores in turn, so the rate follows the
-// CTAs that an SM holds: with 32 elements a thread and two of them it was 54 and 118 us, with 8 elements 61.
+// CTAs that an SM holds: with 32 elements a thread and two of them it was 54 and 118 us, with 8 elements 61; the
+// next row's loads in between the stores made it slower (55 and 94).
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -53,8 +54,31 @@ struct Unit {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) __stcs(reinterpret_cast<Word*>(p) + i, w[i]);
   }
-  __device__ __forceinline__ float get(int j) const { return Act<T>::to_f(reinterpret_cast<const T*>(w)[j]); }
-  __device__ __forceinline__ void set(int j, float v) { reinterpret_cast<T*>(w)[j] = Act<T>::from_f(v); }
+  __device__ __forceinline__ void unpack(float (&v)[W]) const {
+    if constexpr (sizeof(T) == 2 && W > 1) {
+#pragma unroll
+      for (int i = 0; i < W / 2; ++i) {
+        const uint32_t u = reinterpret_cast<const uint32_t*>(w)[i];
+        v[2 * i] = __uint_as_float(u << 16);
+        v[2 * i + 1] = __uint_as_float(u & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) v[i] = Act<T>::to_f(reinterpret_cast<const T*>(w)[i]);
+    }
+  }
+  __device__ __forceinline__ void pack(const float (&v)[W]) {
+    if constexpr (sizeof(T) == 2 && W > 1) {
+#pragma unroll
+      for (int i = 0; i < W / 2; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        reinterpret_cast<uint32_t*>(w)[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) reinterpret_cast<T*>(w)[i] = Act<T>::from_f(v[i]);
+    }
+  }
 };
 // W e4m3 values from fp32, to nearest even
 template <int W>
@@ -146,14 +170,17 @@ add_norm_kernel(const AddNormArgs a, const int nt) {
   for (int u = 0; u < U; ++u) {
     const int c = ((int)threadIdx.x + nt * u) * W;
     if (live && c < a.dim) {
+      xv[u].unpack(s[u]);
+      if (a.residual) {
+        float r1[W];
+        rv[u].unpack(r1);
 #pragma unroll
-      for (int j = 0; j < W; ++j) {
-        s[u][j] = xv[u].get(j) + (a.residual ? rv[u].get(j) : 0.0f);
-        ss[0] = fmaf(s[u][j], s[u][j], ss[0]);
+        for (int j = 0; j < W; ++j) s[u][j] += r1[j];
       }
-      if (a.sum) {
 #pragma unroll
-        for (int j = 0; j < W; ++j) rv[u].set(j, s[u][j]);
+      for (int j = 0; j < W; ++j) ss[0] = fmaf(s[u][j], s[u][j], ss[0]);
+      if (a.sum) {
+        rv[u].pack(s[u]);
         rv[u].store(static_cast<S*>(a.sum) + row * a.dim + c);
       }
     }
@@ -174,8 +201,7 @@ add_norm_kernel(const AddNormArgs a, const int nt) {
       }
       if (!F8) {
         Unit<T, W> o;
-#pragma unroll
-        for (int j = 0; j < W; ++j) o.set(j, s[u][j]);
+        o.pack(s[u]);
         o.store(static_cast<T*>(a.out) + row * a.dim + c);
       }
     }
@@ -201,8 +227,13 @@ add_norm_kernel(const AddNormArgs a, const int nt) {
 
 // CTAs walk the rows; a thread's columns are the same in every row, so it adds up its share of dweight in registers.
 // The CTA's row groups add theirs in order through shared memory, and the CTA writes one row of partial sums.
+// (The registers that keep a row's values packed between its two uses: left alone, the compiler unpacks them once,
+// and half of the CTAs fit.)
 template <typename T, typename S, int W>
-__global__ void __launch_bounds__(kMaxThreads)
+constexpr int kBwdRegs = W < 8 ? 128 : sizeof(S) == 2 ? 64 : sizeof(T) == 2 ? 80 : 112;
+
+template <typename T, typename S, int W>
+__global__ void __maxnreg__((kBwdRegs<T, S, W>))
 add_norm_bwd_kernel(const AddNormBwdArgs a, const int nt) {
   constexpr int U = held_by_thread(W, sizeof(S), true) / W;
   __shared__ float part[2][kMaxThreads / 32][2];
@@ -234,13 +265,14 @@ add_norm_bwd_kernel(const AddNormBwdArgs a, const int nt) {
     for (int u = 0; u < U; ++u) {
       const int c = ((int)threadIdx.x + nt * u) * W;
       if (live && c < a.dim) {
-        float w[W];
+        float w[W], v[W], g[W];
         load_weight<W>(a.weight + c, w);
+        sv[u].unpack(v);
+        gv[u].unpack(g);
 #pragma unroll
         for (int j = 0; j < W; ++j) {
-          const float v = sv[u].get(j);
-          sums[0] = fmaf(v, v, sums[0]);
-          sums[1] = fmaf(v, w[j] * gv[u].get(j), sums[1]);
+          sums[0] = fmaf(v[j], v[j], sums[0]);
+          sums[1] = fmaf(v[j], w[j] * g[j], sums[1]);
         }
       }
     }
@@ -251,23 +283,24 @@ add_norm_bwd_kernel(const AddNormBwdArgs a, const int nt) {
     for (int u = 0; u < U; ++u) {
       const int c = ((int)threadIdx.x + nt * u) * W;
       if (live && c < a.dim) {
-        float w[W], d[W];
+        float w[W], v[W], g[W], d[W];
         load_weight<W>(a.weight + c, w);
+        sv[u].unpack(v);
+        gv[u].unpack(g);
+#pragma unroll
+        for (int j = 0; j < W; ++j) d[j] = 0.0f;
+        if (a.dsum) dv[u].unpack(d);
 #pragma unroll
         for (int j = 0; j < W; ++j) {
-          const float v = sv[u].get(j), g = gv[u].get(j);
-          d[j] = inv * (w[j] * g - v * k);
-          if (a.dsum) d[j] += dv[u].get(j);
-          acc[u][j] = fmaf(g * v, inv, acc[u][j]);
+          d[j] = fmaf(inv, fmaf(w[j], g[j], -v[j] * k), d[j]);
+          acc[u][j] = fmaf(g[j] * v[j], inv, acc[u][j]);
         }
         if (a.dx) {
-#pragma unroll
-          for (int j = 0; j < W; ++j) gv[u].set(j, d[j]);
+          gv[u].pack(d);
           gv[u].store(static_cast<T*>(a.dx) + base + c);
         }
         if (a.dresidual) {
-#pragma unroll
-          for (int j = 0; j < W; ++j) sv[u].set(j, d[j]);
+          sv[u].pack(d);
           sv[u].store(static_cast<S*>(a.dresidual) + base + c);
         }
       }
