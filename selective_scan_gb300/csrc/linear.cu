@@ -319,7 +319,7 @@ __device__ __forceinline__ void load_half(uint32_t dst, const CUtensorMap* tm, i
 }
 
 // Both products of the backward pass in one launch (dw first: its tiles, over all rows, are the longer ones),
-// so that they fill the last round together: pair p takes every npairs-th tile of dw, and the tiles
+// so that they fill the last wave together: pair p takes every npairs-th tile of dw, and the tiles
 // [start[p], start[p + 1]) of dx.
 constexpr int kMaxPairs = 80;
 struct Split {

@@ -12,10 +12,12 @@
 //   2. the tile publishes its map in the workspace, and each warp fetches four of the (at
 //      most 31) maps that precede the tile; folded, they give the state that enters it
 //   3. each warp adds (product of f's) x (its own entering state) to its tokens and stores
-// Inputs stream through a ring in shared memory by TMA (by cp.async where rows are not 16-byte
-// aligned): a warp fetches only the rows that it will read, so a stage is handed over without
-// the other warps, and the next tile's copies are in flight while a tile waits for its
-// predecessors.
+// Inputs stream through a ring in shared memory by TMA, or row by row in bulk copies where they
+// are not 16-byte aligned: a warp fetches only the rows that it will read, so a stage is handed
+// over without the other warps, and the next tile's copies are in flight while a tile waits for
+// its predecessors (with one stage, while the others finish). Unaligned rows are realigned as
+// they are read: for eight runs of 32 768 tokens in all by 2 047 channels of bf16 161 us forwards
+// and 269 backwards (by 2 048: 112 and 177); copied word by word, 192 and 313.
 //
 // What precedes chunk l of a run, the same for any timing (so results repeat bit for bit):
 // every chunk publishes its map, and every 16th (0, 16, 32, ...) the state after it too (the
@@ -75,8 +77,8 @@ constexpr uint32_t kPollLimit = 1u << 21;      // polls before giving up (about 
 template <typename T> constexpr int kCh = 4 / (int)sizeof(T);
 template <typename T> constexpr int kTileCh = 32 * kCh<T>;
 
-// Row of a staged matrix: 32 words, or 33 where rows start between two words.
-template <bool kVec> constexpr int kPitch = kVec ? 128 : 132;
+// Row of a staged matrix: 128 bytes, or with the up to 14 before them that share their first 16.
+template <bool kVec> constexpr int kPitch = kVec ? 128 : 144;
 
 // sigmoid(g) and sigmoid(-g), each with its own digits: with e = exp(-|g|) they are
 // 1 / (1 + e) and e / (1 + e), in the order that g's sign gives; the first is also one minus the
@@ -176,13 +178,6 @@ __device__ __forceinline__ void both_sigmoids(const float (&g)[C], typename Pack
   down = P::make(b);
 }
 
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
-template <int n>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(n) : "memory"); }
-
 // What a CTA knows of a tile. Chunks count from the end that the pass starts at.
 struct Info {
   int item;    // -1: none left
@@ -213,28 +208,6 @@ __device__ __forceinline__ void tile_info(Info& f, const SeqTable& t, int item, 
   f.last = f.l == of - 1;
 }
 
-// Is the first of this row's channels in the upper half of its word? (The word is inside the
-// allocation all the same: allocations begin and end on words.)
-template <typename T>
-__device__ __forceinline__ int odd_start(const T* row) {
-  return sizeof(T) == 2 ? (int)((reinterpret_cast<uintptr_t>(row) >> 1) & 1) : 0;
-}
-
-// This warp's rows [r0, r0 + nt) of the tile at `tile` (row stride ld, m channels from there) into dst, word
-// by word: for rows that TMA does not take (it wants them 16-byte aligned).
-template <typename T>
-__device__ __forceinline__ void load_words(uint32_t dst, const T* tile, int64_t ld, int r0, int nt, int m, int lane) {
-  for (int r = 0; r < nt; ++r) {
-    const T* row = tile + (int64_t)(r0 + r) * ld;
-    const int odd = odd_start(row);
-    const int words = (m * (int)sizeof(T) + 2 * odd + 3) / 4;
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(row - odd);
-    const uint32_t d = dst + (uint32_t)((r0 + r) * 132);
-    if (lane < words) cp_async4(d + 4 * lane, src + lane);
-    if (lane == 0 && words > 32) cp_async4(d + 128, src + 32);
-  }
-}
-
 // A matrix that is streamed through the ring.
 template <typename T>
 struct Stream {
@@ -242,41 +215,81 @@ struct Stream {
   int64_t ld;
   const CUtensorMap* map;  // boxes of 128 bytes x kTok rows
 };
-// This warp's rows of tile f of k matrices, kMat bytes apart, into the stage at st. By TMA the stage's
-// barrier of this warp tells when they are there (rows past the run's end are other runs', or zeros: nothing
-// uses them); word by word, the group of copies that this call commits.
+// This warp's rows of tile f of k matrices, kMat bytes apart, into the stage at st; bar tells when they are there.
+// Where rows are 16-byte aligned, by TMA (rows past the run's end are other runs', or zeros: nothing uses them); else a
+// lane copies a row, from the 16-byte boundary before it to the one after it: what that adds shares its 16 bytes with
+// the row, so it can be read, and nothing uses it.
 template <typename T, bool kVec, int k>
 __device__ __forceinline__ void load_tile(const Info& f, const Stream<T> (&m)[k], uint32_t st, uint32_t bar, int dim,
                                           int warp, int lane) {
   constexpr uint32_t kMat = kChunkR * kPitch<kVec>;
   const int ch0 = f.group * kTileCh<T>, nt = f.item >= 0 ? min(kTok, f.n - warp * kTok) : 0;
+  if (nt <= 0) return;
   if constexpr (kVec) {
-    if (nt > 0 && lane == 0) {
+    if (lane == 0) {
       fence_async_smem();  // what this warp read and wrote there before comes first
       mbar_expect_tx(bar, k * kTok * 128);
 #pragma unroll
       for (int i = 0; i < k; ++i) tma_load_2d(st + i * kMat + warp * kTok * 128, m[i].map, ch0, f.row + warp * kTok, bar);
     }
   } else {
-    if (nt > 0)
+    fence_async_smem();
+    const int valid = min(kTileCh<T>, dim - ch0) * (int)sizeof(T);
+    uint64_t from[k];
+    uint32_t bytes[k], total = 0;
+#pragma unroll
+    for (int i = 0; i < k; ++i) {
+      const uint64_t p = reinterpret_cast<uint64_t>(m[i].p + (int64_t)(f.row + warp * kTok + lane) * m[i].ld + ch0);
+      from[i] = p & ~(uint64_t)15;
+      bytes[i] = lane < nt ? ((uint32_t)(p & 15) + (uint32_t)valid + 15u) & ~15u : 0u;
+      total += bytes[i];
+    }
+    total = __reduce_add_sync(0xffffffffu, total);
+    if (lane == 0) mbar_expect_tx(bar, total);
+    __syncwarp();
+    if (lane < nt)
 #pragma unroll
       for (int i = 0; i < k; ++i)
-        load_words<T>(st + i * kMat, m[i].p + f.row * m[i].ld + ch0, m[i].ld, warp * kTok, nt, min(kTileCh<T>, dim - ch0), lane);
-    cp_commit();
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                     :: "r"(st + i * kMat + (uint32_t)(warp * kTok + lane) * kPitch<kVec>), "l"(from[i]), "r"(bytes[i]),
+                        "r"(bar) : "memory");
+    __syncwarp();
   }
 }
 
-// The lane's word of a staged row.
-template <typename T, bool kVec>
-__device__ __forceinline__ uint32_t staged(const unsigned char* stage, int r, int lane, const T* tile, int64_t ld) {
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(stage + r * kPitch<kVec>) + lane;
-  if constexpr (kVec || sizeof(T) == 4) {
-    return *w;
-  } else {
-    return odd_start(tile + (int64_t)r * ld) ? __funnelshift_r(w[0], w[1], 16) : w[0];
-  }
-}
+// A lane's words of this warp's staged rows of the k matrices.
+template <typename T, bool kVec, int k>
+struct Reader {
+  unsigned char* base;  // the lane's in row 0 of the first matrix
+  uint32_t at = 0, step = 0;  // a byte to a matrix: its first row's address and its stride modulo 16
 
+  __device__ __forceinline__ Reader(unsigned char* st, const Info& f, const Stream<T> (&m)[k], int warp, int lane)
+      : base(st + warp * kTok * kPitch<kVec> + 4 * lane) {
+    static_assert(kTok <= 16, "a row's sum stays inside its byte");
+    if constexpr (!kVec)
+#pragma unroll
+      for (int i = 0; i < k; ++i) {
+        const uint32_t ld = (uint32_t)m[i].ld, row = (uint32_t)(f.row + warp * kTok), e = sizeof(T);
+        at |= (((uint32_t)reinterpret_cast<uintptr_t>(m[i].p) + e * (row * ld + f.group * kTileCh<T>)) & 15u) << (8 * i);
+        step |= (e * ld & 15u) << (8 * i);
+      }
+  }
+  // the (first) word that holds the lane's channels of row j
+  __device__ __forceinline__ unsigned char* slot(int i, int j) const {
+    return base + i * kChunkR * kPitch<kVec> + j * kPitch<kVec> + (kVec ? 0u : (at + j * step) >> (8 * i) & 12u);
+  }
+  __device__ __forceinline__ uint32_t word(int i, int j) const {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(slot(i, j));
+    if constexpr (kVec || sizeof(T) == 4) return w[0];
+    else return __funnelshift_r(w[0], w[1], 8u * ((at + j * step) >> (8 * i) & 2u));  // in the first or across two
+  }
+};
+
+// Does this row start between two words?
+template <typename T>
+__device__ __forceinline__ int odd_start(const T* row) {
+  return sizeof(T) == 2 ? (int)((reinterpret_cast<uintptr_t>(row) >> 1) & 1) : 0;
+}
 // kIn: all of the lane's channels are inside the matrix and p is on a word; else `left` are from p on.
 template <typename T, bool kIn>
 __device__ __forceinline__ void store_row(T* p, const float (&v)[kCh<T>], int left) {
@@ -468,31 +481,30 @@ __device__ __forceinline__ int take(const Chain& ch, int turn, int items) {
 
 // ------------------------------------------------------------------ forward
 
-constexpr int kFwdStages = 2;
+// Three CTAs to an SM, with as many stages as they leave room for.
+template <bool kVec> constexpr int kFwdStages = kVec ? 2 : 1;
 template <bool kVec> constexpr int kFwdStage = 2 * kChunkR * kPitch<kVec>;
+constexpr int kCtas = 3;
 
-template <typename T>
+template <typename T, bool kVec>
 struct FwdShared {
   Info info[kInfos];
   float A[kWarps][kTileCh<T>], B[kWarps][kTileCh<T>];      // the warps' maps, then of all the warps before each
   float enter[kTileCh<T>];                                 // the state that enters the tile
   Before<T> before;
-  alignas(8) uint64_t full[kFwdStages][kWarps];
+  alignas(8) uint64_t full[kFwdStages<kVec>][kWarps];
   uint32_t abort;
 };
 
 // The products of the f's go into shared memory, over the inputs that the lane has consumed (the same 8 bytes
-// a pair of channels), so that three CTAs fit an SM's registers; where a lane's inputs lie across two words
-// they stay in registers, with two CTAs.
-template <typename T, bool kVec> constexpr int kFwdCtas = kVec ? 3 : 2;
-
+// a pair of channels), so that three CTAs fit an SM's registers.
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kThreads, kFwdCtas<T, kVec>)
+__global__ void __launch_bounds__(kThreads, kCtas)
 rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ CUtensorMap mx,
                const __grid_constant__ CUtensorMap mg, const __grid_constant__ Chain ch, const int items,
                const int groups) {
   extern __shared__ __align__(128) unsigned char stages[];
-  __shared__ FwdShared<T> s;
+  __shared__ FwdShared<T, kVec> s;
   constexpr int C = kCh<T>;
   using P = Pack<C>;
   using V = typename P::V;
@@ -506,19 +518,19 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ CUtens
 
   const Stream<T> in_streams[2] = {{static_cast<const T*>(a.x), a.ld_x, &mx}, {static_cast<const T*>(a.gate), a.ld_gate, &mg}};
   auto load = [&](int i) {  // this warp's rows of tile i, if there is one
-    load_tile<T, kVec, 2>(s.info[i % kInfos], in_streams, su32(stages) + (uint32_t)(i % kFwdStages) * kFwdStage<kVec>,
-                          su32(&s.full[i % kFwdStages][warp]), a.dim, warp, lane);
+    load_tile<T, kVec, 2>(s.info[i % kInfos], in_streams, su32(stages) + (uint32_t)(i % kFwdStages<kVec>) * kFwdStage<kVec>,
+                          su32(&s.full[i % kFwdStages<kVec>][warp]), a.dim, warp, lane);
   };
-  if (threadIdx.x < kFwdStages * kWarps) {
+  if (threadIdx.x < kFwdStages<kVec> * kWarps) {
     mbar_init(su32(&s.full[0][0] + threadIdx.x), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     s.abort = 0u;
   }
   if (threadIdx.x == 0)
-    for (int i = 0; i < kFwdStages; ++i)
-      tile_info<false>(s.info[i], a.tab, take<kFwdStages>(ch, i, items), items, groups);
+    for (int i = 0; i < kFwdStages<kVec>; ++i)
+      tile_info<false>(s.info[i], a.tab, take<kFwdStages<kVec>>(ch, i, items), items, groups);
   __syncthreads();
-  for (int i = 0; i < kFwdStages; ++i) load(i);
+  for (int i = 0; i < kFwdStages<kVec>; ++i) load(i);
 
   uint32_t phases = 0;  // bit s: the parity of stage s's next load
   for (int i = 0;; ++i) {
@@ -527,7 +539,7 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ CUtens
     const int ch0 = f.group * kTileCh<T> + lane * C;
     const int left = a.dim - ch0;  // channels of this lane and those after it
     int next = 0;
-    if (threadIdx.x == 0) next = take<kFwdStages>(ch, i + kFwdStages, items);
+    if (threadIdx.x == 0) next = take<kFwdStages<kVec>>(ch, i + kFwdStages<kVec>, items);
     const int first = a.tab.tile[f.seq];
     const int before = f.l > 0 ? maps_before(f.l) : 0;
     float h0[C];  // what the run starts from: asked for early, the run's other tiles wait for it
@@ -536,9 +548,8 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ CUtens
       for (int c = 0; c < C; ++c)
         h0[c] = c < left && !seq_fresh(a.tab, f.seq) ? a.state[(int64_t)seq_slot(a.tab, f.seq) * a.dim + ch0 + c] : 0.0f;
     // ---- scan from zero
-    unsigned char* st = stages + (i % kFwdStages) * kFwdStage<kVec>;
-    const T* tx = static_cast<const T*>(a.x) + f.row * a.ld_x + f.group * kTileCh<T>;
-    const T* tg = static_cast<const T*>(a.gate) + f.row * a.ld_gate + f.group * kTileCh<T>;
+    unsigned char* st = stages + (i % kFwdStages<kVec>) * kFwdStage<kVec>;
+    const Reader<T, kVec, 2> rd(st, f, in_streams, warp, lane);
     float lo[C], un[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -547,28 +558,18 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ CUtens
     }
     const V lo2 = P::make(lo), un2 = P::make(un);
     const int nt = min(kTok, f.n - warp * kTok);
-    // the lane's word of row r of x (and, kMat further, of gate)
-    auto word = [&](int j) {
-      return reinterpret_cast<float*>(st + (warp * kTok + j) * kPitch<kVec>) + lane;
-    };
-    if constexpr (kVec) {
-      if (nt > 0) {
-        warp_wait(su32(&s.full[i % kFwdStages][warp]), phases >> (i % kFwdStages) & 1u, &s.abort);
-        phases ^= 1u << (i % kFwdStages);
-      }
-    } else {
-      cp_wait<kFwdStages - 1>();
-      __syncwarp();
+    if (nt > 0) {
+      warp_wait(su32(&s.full[i % kFwdStages<kVec>][warp]), phases >> (i % kFwdStages<kVec>) & 1u, &s.abort);
+      phases ^= 1u << (i % kFwdStages<kVec>);
     }
-    V hs[kTok], ps[kVec ? 1 : kTok], h2 = P::all(0.0f), p2 = P::all(1.0f);
+    V hs[kTok], h2 = P::all(0.0f), p2 = P::all(1.0f);
     auto scan = [&](auto whole) {  // rows past the run's end count as the identity
 #pragma unroll
       for (int j = 0; j < kTok; ++j) {
         if (decltype(whole)::value || j < nt) {
-          const int r = warp * kTok + j;
           float x[C], g[C];
-          unpack_word<T>(staged<T, kVec>(st, r, lane, tx, a.ld_x), x);
-          unpack_word<T>(staged<T, kVec>(st + kMat, r, lane, tg, a.ld_gate), g);
+          unpack_word<T>(rd.word(0, j), x);
+          unpack_word<T>(rd.word(1, j), g);
           V up, down;
           both_sigmoids<C>(g, up, down);
           const V f2 = P::fma(un2, up, lo2);
@@ -576,14 +577,11 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ CUtens
           p2 = P::mul(p2, f2);
         }
         hs[j] = h2;
-        if constexpr (kVec) {
-          float v[C];
-          P::split(p2, v);
-#pragma unroll
-          for (int c = 0; c < C; ++c) word(j)[c * (kMat / 4)] = v[c];
-        } else {
-          ps[j] = p2;
-        }
+        float v[C];
+        P::split(p2, v);
+        if constexpr (!kVec) __syncwarp();  // (the lane before may share the word)
+        *reinterpret_cast<float*>(rd.slot(0, j)) = v[0];
+        if constexpr (C == 2) *reinterpret_cast<float*>(rd.slot(1, j)) = v[1];
       }
     };
     if (nt == kTok) scan(std::true_type{});
@@ -627,7 +625,7 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ CUtens
       }
     }
     look_back<T, false>(ch, f, first, groups, before, s.before, warp, lane);
-    if (threadIdx.x == 0) tile_info<false>(s.info[(i + kFwdStages) % kInfos], a.tab, next, items, groups);
+    if (threadIdx.x == 0) tile_info<false>(s.info[(i + kFwdStages<kVec>) % kInfos], a.tab, next, items, groups);
     __syncthreads();
     float in[C];
     if (warp == kWarps - 1) {
@@ -659,24 +657,18 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ CUtens
 #pragma unroll
       for (int j = 0; j < kTok; ++j, ty += a.ld_y)
         if (decltype(whole)::value || j < nt) {
-          float y[C];
-          if constexpr (kVec) {
-            float v[C];
-#pragma unroll
-            for (int c = 0; c < C; ++c) v[c] = word(j)[c * (kMat / 4)];
-            P::split(P::fma(P::make(v), in2, hs[j]), y);
-          } else {
-            P::split(P::fma(ps[j], in2, hs[j]), y);
-          }
+          float y[C], v[C];
+          v[0] = *reinterpret_cast<const float*>(rd.slot(0, j));
+          if constexpr (C == 2) v[1] = *reinterpret_cast<const float*>(rd.slot(1, j));
+          P::split(P::fma(P::make(v), in2, hs[j]), y);
           store_row<T, kVec && decltype(whole)::value>(ty, y, left);
         }
     };
     if (nt == kTok && (f.group + 1) * kTileCh<T> <= a.dim) emit(std::true_type{});
     else emit(std::false_type{});
     __syncwarp();  // every lane is done with this stage
-    load(i + kFwdStages);
+    load(i + kFwdStages<kVec>);
   }
-  if constexpr (!kVec) cp_wait<0>();
   __syncthreads();
   if (threadIdx.x == 0 && s.abort) atomicAdd(&g_recurrence_timeouts, 1u);
 }
@@ -684,30 +676,29 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ CUtens
 // ------------------------------------------------------------------ backward
 
 // One stage, so that three CTAs fit an SM (the gates are made twice for that, too: kept, they take the registers of
-// the third): 320 us against 337 for one run of 65 536 tokens by 2 048 channels with two stages and two CTAs, which
-// word by word keeps. (A tile taken further ahead is waited for longer: with the next tile's ticket taken and its
-// rows fetched into L2 meanwhile it was 385.)
-template <bool kVec> constexpr int kBwdStages = kVec ? 1 : 2;
-template <typename T, bool kVec> constexpr int kBwdCtas = kVec ? 3 : 2;
+// the third): 320 us against 337 for one run of 65 536 tokens by 2 048 channels with two stages and two CTAs. (A
+// tile taken further ahead is waited for longer: with the next tile's ticket taken and its rows fetched into L2
+// meanwhile it was 385.)
+constexpr int kBwdStages = 1;
 template <bool kVec> constexpr int kBwdStage = 3 * kChunkR * kPitch<kVec>;
 
-template <typename T, bool kVec>
+template <typename T>
 struct BwdShared {
   Info info[kInfos];
   float A[kWarps][kTileCh<T>], R[kWarps][kTileCh<T>];
   Before<T> before;
   float dlo[kWarps][kTileCh<T>];
-  alignas(8) uint64_t full[kBwdStages<kVec>][kWarps];
+  alignas(8) uint64_t full[kBwdStages][kWarps];
   uint32_t abort;
 };
 
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kThreads, kBwdCtas<T, kVec>)
+__global__ void __launch_bounds__(kThreads, kCtas)
 rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUtensorMap mx,
                const __grid_constant__ CUtensorMap mg, const __grid_constant__ CUtensorMap md,
                const __grid_constant__ Chain ch, float* part, const int items, const int groups) {
   extern __shared__ __align__(128) unsigned char stages[];
-  __shared__ BwdShared<T, kVec> s;
+  __shared__ BwdShared<T> s;
   constexpr int C = kCh<T>;
   using P = Pack<C>;
   using V = typename P::V;
@@ -724,10 +715,10 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUt
                                    {static_cast<const T*>(a.gate), a.ld_gate, &mg},
                                    {static_cast<const T*>(a.dy), a.ld_dy, &md}};
   auto load = [&](int i) {
-    load_tile<T, kVec, 3>(s.info[i % kInfos], in_streams, su32(stages) + (uint32_t)(i % kBwdStages<kVec>) * kBwdStage<kVec>,
-                          su32(&s.full[i % kBwdStages<kVec>][warp]), a.dim, warp, lane);
+    load_tile<T, kVec, 3>(s.info[i % kInfos], in_streams, su32(stages) + (uint32_t)(i % kBwdStages) * kBwdStage<kVec>,
+                          su32(&s.full[i % kBwdStages][warp]), a.dim, warp, lane);
   };
-  if (threadIdx.x < kBwdStages<kVec> * kWarps) {
+  if (threadIdx.x < kBwdStages * kWarps) {
     mbar_init(su32(&s.full[0][0] + threadIdx.x), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     s.abort = 0u;
@@ -745,10 +736,10 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUt
     }
   };
   if (threadIdx.x == 0)
-    for (int i = 0; i < kBwdStages<kVec>; ++i)
-      tile_info<true>(s.info[i], a.tab, take<kBwdStages<kVec>>(ch, i, items), items, groups);
+    for (int i = 0; i < kBwdStages; ++i)
+      tile_info<true>(s.info[i], a.tab, take<kBwdStages>(ch, i, items), items, groups);
   __syncthreads();
-  for (int i = 0; i < kBwdStages<kVec>; ++i) load(i);
+  for (int i = 0; i < kBwdStages; ++i) load(i);
 
   uint32_t phases = 0;
   int i = 0;
@@ -758,7 +749,7 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUt
     const int ch0 = f.group * kTileCh<T> + lane * C;
     const int left = a.dim - ch0;
     int next = 0;
-    if (threadIdx.x == 0) next = take<kBwdStages<kVec>>(ch, i + kBwdStages<kVec>, items);
+    if (threadIdx.x == 0) next = take<kBwdStages>(ch, i + kBwdStages, items);
     const int first = a.tab.tile[f.seq];
     const int before = f.l > 0 ? maps_before(f.l) : 0;
     float h0[C];
@@ -766,10 +757,8 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUt
 #pragma unroll
       for (int c = 0; c < C; ++c)
         h0[c] = c < left && a.dstate_end ? a.dstate_end[(int64_t)f.seq * a.dim + ch0 + c] : 0.0f;
-    const unsigned char* st = stages + (i % kBwdStages<kVec>) * kBwdStage<kVec>;
-    const T* tx = static_cast<const T*>(a.x) + f.row * a.ld_x + f.group * kTileCh<T>;
-    const T* tg = static_cast<const T*>(a.gate) + f.row * a.ld_gate + f.group * kTileCh<T>;
-    const T* td = static_cast<const T*>(a.dy) + f.row * a.ld_dy + f.group * kTileCh<T>;
+    unsigned char* st = stages + (i % kBwdStages) * kBwdStage<kVec>;
+    const Reader<T, kVec, 3> rd(st, f, in_streams, warp, lane);
     float lo[C], un[C], hp[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -779,14 +768,9 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUt
     }
     const V lo2 = P::make(lo), un2 = P::make(un);
     const int nt = min(kTok, f.n - warp * kTok);
-    if constexpr (kVec) {
-      if (nt > 0) {
-        warp_wait(su32(&s.full[i % kBwdStages<kVec>][warp]), phases >> (i % kBwdStages<kVec>) & 1u, &s.abort);
-        phases ^= 1u << (i % kBwdStages<kVec>);
-      }
-    } else {
-      cp_wait<kBwdStages<kVec> - 1>();
-      __syncwarp();
+    if (nt > 0) {
+      warp_wait(su32(&s.full[i % kBwdStages][warp]), phases >> (i % kBwdStages) & 1u, &s.abort);
+      phases ^= 1u << (i % kBwdStages);
     }
     // ---- the states from the checkpoint on, and R's map (A, R)
     V hs[kTok];  // the state before the token
@@ -795,11 +779,10 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUt
 #pragma unroll
       for (int j = 0; j < kTok; ++j)
         if (decltype(whole)::value || j < nt) {
-          const int r = warp * kTok + j;
           float x[C], g[C], d[C];
-          unpack_word<T>(staged<T, kVec>(st, r, lane, tx, a.ld_x), x);
-          unpack_word<T>(staged<T, kVec>(st + kMat, r, lane, tg, a.ld_gate), g);
-          unpack_word<T>(staged<T, kVec>(st + 2 * kMat, r, lane, td, a.ld_dy), d);
+          unpack_word<T>(rd.word(0, j), x);
+          unpack_word<T>(rd.word(1, j), g);
+          unpack_word<T>(rd.word(2, j), d);
           V up, down;
           both_sigmoids<C>(g, up, down);
           const V ft = P::fma(un2, up, lo2);
@@ -854,7 +837,7 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUt
     }
     look_back<T, true>(ch, f, first, groups, before, s.before, warp, lane);
     // info[i + 2] takes the place of tile i - 2, whose part of dlower has been summed
-    if (threadIdx.x == 0) tile_info<true>(s.info[(i + kBwdStages<kVec>) % kInfos], a.tab, next, items, groups);
+    if (threadIdx.x == 0) tile_info<true>(s.info[(i + kBwdStages) % kInfos], a.tab, next, items, groups);
     __syncthreads();
     float in[C];
     fold_before(s.before, before, in, lane);
@@ -878,11 +861,10 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUt
 #pragma unroll
       for (int j = kTok - 1; j >= 0; --j, ox -= a.ld_dx, og -= a.ld_dgate)
         if (decltype(whole)::value || j < nt) {
-          const int r = warp * kTok + j;
           float x[C], g[C], d[C], vx[C], vg[C];
-          unpack_word<T>(staged<T, kVec>(st, r, lane, tx, a.ld_x), x);
-          unpack_word<T>(staged<T, kVec>(st + kMat, r, lane, tg, a.ld_gate), g);
-          unpack_word<T>(staged<T, kVec>(st + 2 * kMat, r, lane, td, a.ld_dy), d);
+          unpack_word<T>(rd.word(0, j), x);
+          unpack_word<T>(rd.word(1, j), g);
+          unpack_word<T>(rd.word(2, j), d);
           V up, down;
           both_sigmoids<C>(g, up, down);
           const V ft = P::fma(un2, up, lo2);
@@ -904,11 +886,10 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUt
 #pragma unroll
     for (int c = 0; c < C; ++c) s.dlo[warp][lane * C + c] = dlo[c];
     __syncwarp();  // every lane is done with this stage
-    load(i + kBwdStages<kVec>);
+    load(i + kBwdStages);
   }
   __syncthreads();
   if (warp == 1 && i > 0 && part) sum_part(i - 1);
-  if constexpr (!kVec) cp_wait<0>();
   if (threadIdx.x == 0 && s.abort) atomicAdd(&g_recurrence_timeouts, 1u);
 }
 
@@ -1089,7 +1070,7 @@ bool make_map(CUtensorMap* tm, const void* base, int64_t rows, int64_t dim, int6
 
 template <typename T, bool kVec>
 cudaError_t run_fwd(const RecArgs& a, const Chain& ch, int items, int groups, cudaStream_t st) {
-  constexpr int smem = kFwdStages * kFwdStage<kVec>;
+  constexpr int smem = kFwdStages<kVec> * kFwdStage<kVec>;
   CUtensorMap mx, mg;
   std::memset(&mx, 0, sizeof mx);
   std::memset(&mg, 0, sizeof mg);
@@ -1098,12 +1079,12 @@ cudaError_t run_fwd(const RecArgs& a, const Chain& ch, int items, int groups, cu
     return cudaErrorInvalidValue;
   const cudaError_t e = cudaFuncSetAttribute(rec_fwd_kernel<T, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  rec_fwd_kernel<T, kVec><<<ctas(items, kFwdCtas<T, kVec>), kThreads, smem, st>>>(a, mx, mg, ch, items, groups);
+  rec_fwd_kernel<T, kVec><<<ctas(items, kCtas), kThreads, smem, st>>>(a, mx, mg, ch, items, groups);
   return cudaGetLastError();
 }
 template <typename T, bool kVec>
 cudaError_t run_bwd(const RecBwdArgs& a, const Chain& ch, float* part, int items, int groups, cudaStream_t st) {
-  constexpr int smem = kBwdStages<kVec> * kBwdStage<kVec>;
+  constexpr int smem = kBwdStages * kBwdStage<kVec>;
   CUtensorMap mx, mg, md;
   std::memset(&mx, 0, sizeof mx);
   std::memset(&mg, 0, sizeof mg);
@@ -1115,7 +1096,7 @@ cudaError_t run_bwd(const RecBwdArgs& a, const Chain& ch, float* part, int items
     return cudaErrorInvalidValue;
   const cudaError_t e = cudaFuncSetAttribute(rec_bwd_kernel<T, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  rec_bwd_kernel<T, kVec><<<ctas(items, kBwdCtas<T, kVec>), kThreads, smem, st>>>(a, mx, mg, md, ch, part, items, groups);
+  rec_bwd_kernel<T, kVec><<<ctas(items, kCtas), kThreads, smem, st>>>(a, mx, mg, md, ch, part, items, groups);
   return cudaGetLastError();
 }
 

@@ -101,6 +101,29 @@ def test_recurrence_forward_and_backward(dtype, lengths, dim, off, extra):
             R.check(got, want[name], name)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dim,at", [(130, ((0, 0), (1, 1), (2, 3), (3, 6), (5, 7))), (67, ((2, 7), (0, 1), (3, 4), (0, 0), (5, 6)))])
+def test_recurrence_matrices_of_different_strides(dtype, dim, at):
+    """x, gate, dy and the outputs each start at an offset and have a stride of their own."""
+    dev = device()
+    lengths = [131, 1, 40]
+    x, gate, lo, pool, slots, fresh = rec_inputs(57, lengths, dim, dtype, True)
+    cu, rows = cu_of(lengths), sum(lengths)
+    ref = R.recurrence(x, gate, lo, pool, cu, slots, fresh)
+    dy = randn(58, rows, dim).to(dtype)
+    want = R.recurrence_backward(x, gate, lo, ref, cu, dy, None)
+    gx, gg, gd = (to_dev(t, dev, *at[i]) for i, t in enumerate((x, gate, dy)))
+    y, dx, dg = (to_dev(torch.zeros_like(x), dev, *at[i]) for i in (3, 4, 0))
+    st, dlo = pool.to(dev), torch.empty(dim, device=dev)
+    kept = torch.empty((ss.gated_recurrence_checkpoints(cu), dim), device=dev)
+    ss.gated_recurrence(y, gx, gg, lo.to(dev), st, cu, slots, fresh, checkpoints=kept)
+    ss.gated_recurrence_backward(dx, dg, dlo, None, gd, None, gx, gg, lo.to(dev), kept, cu)
+    torch.cuda.synchronize()
+    R.check(y, ref["y"], "y")
+    for name, got in (("dx", dx), ("dgate", dg), ("dlower", dlo)):
+        R.check(got, want[name], name)
+
+
 def test_recurrence_optional_outputs_and_repeat():
     """dlower, dstate and dstate_end left out; the same call twice gives the same bits."""
     dev = device()
