@@ -1,12 +1,17 @@
 // RMS norm with the residual's addition (block.h), its 8-bit output, and its backward pass.
 // Each reads its inputs from HBM once and writes its outputs once, and that bounds it.
 //
-// A row lives in the registers of `nt` threads, 32 elements each at most (16 as single elements and in the
-// backward pass, whose threads also hold their columns' sums), read and written in units of 16 bytes of bf16 (8
-// elements) where the width allows, else of 2 elements or 1. nt is the fewest whole warps that hold the row, so
-// all of a row's loads are on the way at once; with fewer rows than SMs a row is spread further, up to a thread
-// per unit. Several rows share a CTA up to 256 threads. Sums of squares go warp by warp and then over the warps
-// in order, in fp32. Rows wider than 512 threads hold are read again from L2 instead (the streamed kernels).
+// A row lives in the registers of `nt` threads, 32 elements each at most (16 in the backward pass, whose threads
+// also hold their columns' sums), read and written in units of 8 elements, 16 bytes of bf16. nt is the fewest whole
+// warps that hold the row, so all of a row's loads are on the way at once; with fewer rows than SMs a row is spread
+// further, up to a thread per unit. Several rows share a CTA up to 256 threads. Sums of squares go warp by warp and
+// then over the warps in order, in fp32. Rows wider than 512 threads hold are read again from L2 instead (the
+// streamed kernels).
+//
+// Where the width is no multiple of 8, units keep the matrix's boundaries instead of the row's (kShift): a row's
+// first and last unit hold other rows' elements too, which are cleared as they arrive and not written. 16 384 x
+// 2 047 of bf16 takes 47 us so, 77 in single elements; its backward 71 against 120 (2 046 in pairs of elements: 66
+// and 74). Units of a row's own are faster where they fit: 2 048 takes 41 and 51, with one warp fewer to a row.
 //
 // Measured (GB300): 16 384 x 2 560, bf16 with a 32-bit sum, 74 us (6.8 TB/s, the measured copy rate); backward
 // of 16 384 x 2 048, bf16, 51 us (5.3 TB/s; 5 of them the column sums' own kernel), of 16 384 x 2 560 with a
@@ -24,10 +29,9 @@
 namespace mamba2 {
 namespace {
 
-// elements of a row that a thread holds
-constexpr int held_by_thread(int unit, int sum_bytes, bool backward) {
-  return unit == 1 || backward ? 16 : 32;
-}
+constexpr int W = 8;          // elements of a unit
+constexpr int kHeld = 32;     // elements of a row that a thread holds
+constexpr int kBwdHeld = 16;  // the same in the backward pass
 constexpr int kCtaThreads = 256;
 constexpr int kMaxThreads = 512;
 constexpr float kMax8 = 448.0f;  // largest e4m3 value
@@ -38,24 +42,54 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// W adjacent elements.
-template <typename T, int W>
+// Where a thread's u-th unit lies in its row. With kShift rows start inside a unit of the matrix (dim is no multiple
+// of 8): units keep the matrix's boundaries, so the first may begin before the row and the last end after it.
+template <bool kShift>
+struct At {
+  int c;  // its first column
+  __device__ __forceinline__ At(int shift, int nt, int u) : c(((int)threadIdx.x + nt * u) * W - (kShift ? shift : 0)) {}
+  __device__ __forceinline__ bool has(int j, int dim) const { return !kShift || (unsigned)(c + j) < (unsigned)dim; }
+  __device__ __forceinline__ bool whole(int dim) const { return !kShift || (c >= 0 && c + W <= dim); }
+};
+
+// How far a row starts behind a boundary.
+__device__ __forceinline__ int shift_of(int64_t row, int dim) { return (int)(row * dim & (W - 1)); }
+
+// A unit's values of one matrix. p: its first column's, which may lie outside the row where whole() is false; the
+// 16 bytes that hold any of the row's elements are read and the rest are zeros, and only the row's are written.
+template <typename T, bool kShift>
 struct Unit {
-  static constexpr int kBytes = W * (int)sizeof(T);
-  using Word = std::conditional_t<kBytes % 16 == 0, uint4,
-                                  std::conditional_t<kBytes == 8, uint2, std::conditional_t<kBytes == 4, uint32_t, uint16_t>>>;
-  static constexpr int kWords = kBytes / (int)sizeof(Word);
-  Word w[kWords];
-  __device__ __forceinline__ void load(const T* p) {
+  static constexpr int kWords = W * (int)sizeof(T) / 16, kEach = 16 / (int)sizeof(T);
+  uint4 w[kWords];
+  __device__ __forceinline__ void load(const T* p, const At<kShift>& at, int dim) {
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) w[i] = __ldcs(reinterpret_cast<const Word*>(p) + i);
+    for (int i = 0; i < kWords; ++i) {
+      const int c = at.c + i * kEach;
+      if (!kShift || kWords == 1 || (c < dim && c + kEach > 0)) w[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+      else w[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
   }
-  __device__ __forceinline__ void store(T* p) const {
+  __device__ __forceinline__ void store(T* p, const At<kShift>& at, int dim) const {
+    if (at.whole(dim)) {
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) __stcs(reinterpret_cast<Word*>(p) + i, w[i]);
+      for (int i = 0; i < kWords; ++i) __stcs(reinterpret_cast<uint4*>(p) + i, w[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < W; ++j)
+        if (at.has(j, dim)) p[j] = reinterpret_cast<const T*>(w)[j];
+    }
+  }
+  // other rows' elements become zeros
+  __device__ __forceinline__ void clear(const At<kShift>& at, int dim) {
+#pragma unroll
+    for (int i = 0; i < W * (int)sizeof(T) / 4; ++i) {
+      uint32_t& v = reinterpret_cast<uint32_t*>(w)[i];
+      if constexpr (sizeof(T) == 2) v &= (at.has(2 * i, dim) ? 0xffffu : 0u) | (at.has(2 * i + 1, dim) ? 0xffff0000u : 0u);
+      else v = at.has(i, dim) ? v : 0u;
+    }
   }
   __device__ __forceinline__ void unpack(float (&v)[W]) const {
-    if constexpr (sizeof(T) == 2 && W > 1) {
+    if constexpr (sizeof(T) == 2) {
 #pragma unroll
       for (int i = 0; i < W / 2; ++i) {
         const uint32_t u = reinterpret_cast<const uint32_t*>(w)[i];
@@ -68,7 +102,7 @@ struct Unit {
     }
   }
   __device__ __forceinline__ void pack(const float (&v)[W]) {
-    if constexpr (sizeof(T) == 2 && W > 1) {
+    if constexpr (sizeof(T) == 2) {
 #pragma unroll
       for (int i = 0; i < W / 2; ++i) {
         const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
@@ -81,40 +115,48 @@ struct Unit {
   }
 };
 // W e4m3 values from fp32, to nearest even
-template <int W>
-__device__ __forceinline__ void store8(__nv_fp8_storage_t* p, const float (&v)[W]) {
-  if constexpr (W == 1) {
-    *p = __nv_cvt_float_to_fp8(v[0], __NV_SATFINITE, __NV_E4M3);
-  } else {
-    uint16_t h[W / 2];
+template <bool kShift>
+__device__ __forceinline__ void store8(__nv_fp8_storage_t* p, const float (&v)[W], const At<kShift>& at, int dim) {
+  uint16_t h[W / 2];
 #pragma unroll
-    for (int i = 0; i < W / 2; ++i)
-      h[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
-    if constexpr (W == 8) *reinterpret_cast<uint2*>(p) = make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
-    else *reinterpret_cast<uint16_t*>(p) = h[0];
+  for (int i = 0; i < W / 2; ++i)
+    h[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+  if (at.whole(dim)) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
+  } else {
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+      if (at.has(j, dim)) p[j] = (__nv_fp8_storage_t)(h[j / 2] >> (8 * (j & 1)));
   }
 }
 
-// The fp32 weights of W columns.
-template <int W>
-__device__ __forceinline__ void load_weight(const float* p, float (&w)[W]) {
-  if constexpr (W == 8) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    w[0] = a.x;
-    w[1] = a.y;
-    w[2] = a.z;
-    w[3] = a.w;
-    w[4] = b.x;
-    w[5] = b.y;
-    w[6] = b.z;
-    w[7] = b.w;
-  } else if constexpr (W == 2) {
-    const float2 a = __ldg(reinterpret_cast<const float2*>(p));
-    w[0] = a.x;
-    w[1] = a.y;
-  } else {
-    w[0] = __ldg(p);
+// The fp32 weights of a unit's columns. Where they start between two 16-byte words, the same for the whole row, the
+// three words that hold them are read and shifted into place.
+template <bool kShift>
+__device__ __forceinline__ void load_weight(const float* weight, const At<kShift>& at, int dim, float (&w)[W]) {
+  constexpr int kRead = kShift ? 12 : 8;
+  float v[kRead];
+  const int first = kShift ? at.c & ~3 : at.c;
+#pragma unroll
+  for (int i = 0; i < kRead / 4; ++i) {
+    const int c = first + 4 * i;
+    const bool in = !kShift || (c >= 0 && c < dim && c < at.c + W);
+    const float4 a = in ? __ldg(reinterpret_cast<const float4*>(weight + c)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    v[4 * i] = a.x;
+    v[4 * i + 1] = a.y;
+    v[4 * i + 2] = a.z;
+    v[4 * i + 3] = a.w;
   }
+  if constexpr (kShift) {
+    if (at.c & 1)
+#pragma unroll
+      for (int j = 0; j < 11; ++j) v[j] = v[j + 1];
+    if (at.c & 2)
+#pragma unroll
+      for (int j = 0; j < W; ++j) v[j] = v[j + 2];
+  }
+#pragma unroll
+  for (int j = 0; j < W; ++j) w[j] = v[j];
 }
 
 // The sums (or NaN-keeping maxima) of n values over the row's nt threads, in a fixed order. part: a place per
@@ -145,31 +187,36 @@ __device__ __forceinline__ void row_reduce(float (&v)[n], int nt, float (*part)[
 // finished; nothing else is.
 __device__ __forceinline__ void wait_for_inputs() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-template <typename T, typename S, bool F8, int W>
+template <typename T, typename S, bool F8, bool kShift>
 __global__ void __launch_bounds__(kMaxThreads)
 add_norm_kernel(const AddNormArgs a, const int nt) {
-  constexpr int U = held_by_thread(W, sizeof(S), false) / W;
+  constexpr int U = kHeld / W;
   __shared__ float part[2][kMaxThreads / 32][1];
   const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   const bool live = row < a.rows;
+  const int shift = shift_of(row, a.dim);
   const T* x = static_cast<const T*>(a.x) + row * a.dim;
   const S* r = static_cast<const S*>(a.residual) + row * a.dim;
   wait_for_inputs();
-  Unit<T, W> xv[U];
-  Unit<S, W> rv[U];
+  Unit<T, kShift> xv[U];
+  Unit<S, kShift> rv[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int c = ((int)threadIdx.x + nt * u) * W;
-    if (live && c < a.dim) {
-      xv[u].load(x + c);
-      if (a.residual) rv[u].load(r + c);
+    const At<kShift> at(shift, nt, u);
+    if (live && at.c < a.dim) {
+      xv[u].load(x + at.c, at, a.dim);
+      if (a.residual) rv[u].load(r + at.c, at, a.dim);
     }
   }
   float s[U][W], ss[1] = {0.0f};
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int c = ((int)threadIdx.x + nt * u) * W;
-    if (live && c < a.dim) {
+    const At<kShift> at(shift, nt, u);
+    if (live && at.c < a.dim) {
+      if (!at.whole(a.dim)) {
+        xv[u].clear(at, a.dim);
+        if (a.residual) rv[u].clear(at, a.dim);
+      }
       xv[u].unpack(s[u]);
       if (a.residual) {
         float r1[W];
@@ -181,7 +228,7 @@ add_norm_kernel(const AddNormArgs a, const int nt) {
       for (int j = 0; j < W; ++j) ss[0] = fmaf(s[u][j], s[u][j], ss[0]);
       if (a.sum) {
         rv[u].pack(s[u]);
-        rv[u].store(static_cast<S*>(a.sum) + row * a.dim + c);
+        rv[u].store(static_cast<S*>(a.sum) + row * a.dim + at.c, at, a.dim);
       }
     }
   }
@@ -190,19 +237,19 @@ add_norm_kernel(const AddNormArgs a, const int nt) {
   float top[1] = {0.0f};
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int c = ((int)threadIdx.x + nt * u) * W;
-    if (live && c < a.dim) {
+    const At<kShift> at(shift, nt, u);
+    if (live && at.c < a.dim) {
       float w[W];
-      load_weight<W>(a.weight + c, w);
+      load_weight(a.weight, at, a.dim, w);
 #pragma unroll
       for (int j = 0; j < W; ++j) {
         s[u][j] = s[u][j] * inv * w[j];
         if (F8) top[0] = max_nan(top[0], fabsf(s[u][j]));
       }
       if (!F8) {
-        Unit<T, W> o;
+        Unit<T, kShift> o;
         o.pack(s[u]);
-        o.store(static_cast<T*>(a.out) + row * a.dim + c);
+        o.store(static_cast<T*>(a.out) + row * a.dim + at.c, at, a.dim);
       }
     }
   }
@@ -213,11 +260,11 @@ add_norm_kernel(const AddNormArgs a, const int nt) {
     if (threadIdx.x == 0) a.scale[row] = scale;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int c = ((int)threadIdx.x + nt * u) * W;
-      if (c < a.dim) {
+      const At<kShift> at(shift, nt, u);
+      if (at.c < a.dim) {
 #pragma unroll
         for (int j = 0; j < W; ++j) s[u][j] *= rs;
-        store8<W>(static_cast<__nv_fp8_storage_t*>(a.out) + row * a.dim + c, s[u]);
+        store8(static_cast<__nv_fp8_storage_t*>(a.out) + row * a.dim + at.c, s[u], at, a.dim);
       }
     }
   }
@@ -228,16 +275,43 @@ add_norm_kernel(const AddNormArgs a, const int nt) {
 // CTAs walk the rows; a thread's columns are the same in every row, so it adds up its share of dweight in registers.
 // The CTA's row groups add theirs in order through shared memory, and the CTA writes one row of partial sums.
 // (The registers that keep a row's values packed between its two uses: left alone, the compiler unpacks them once,
-// and half of the CTAs fit.)
-template <typename T, typename S, int W>
-constexpr int kBwdRegs = W < 8 ? 128 : sizeof(S) == 2 ? 64 : sizeof(T) == 2 ? 80 : 112;
+// and half of the CTAs fit. With kShift what is fastest: 16 bits 71 us with 80, 86 with 64 and 94 with 128, at 16 384
+// x 2 047; 32 bits 52 us with 96 and 54 with 112, at 8 192 x 2 047.)
+// With kShift a thread's columns repeat every eighth row; the grid takes whole multiples of that. Its weights lie in
+// shared memory, shifted once (read with their row's shift from L1 each time: 94 us).
+template <typename T, typename S, bool kShift>
+constexpr int kBwdRegs = sizeof(S) == 2 ? (kShift ? 80 : 64) : sizeof(T) == 2 ? (kShift ? 96 : 80) : (kShift ? 96 : 112);
 
-template <typename T, typename S, int W>
-__global__ void __maxnreg__((kBwdRegs<T, S, W>))
+template <typename T, typename S, bool kShift>
+__global__ void __maxnreg__((kBwdRegs<T, S, kShift>))
 add_norm_bwd_kernel(const AddNormBwdArgs a, const int nt) {
-  constexpr int U = held_by_thread(W, sizeof(S), true) / W;
+  constexpr int U = kBwdHeld / W;
   __shared__ float part[2][kMaxThreads / 32][2];
-  extern __shared__ float columns[];  // [dim], with more than one row to a CTA
+  // With more than one row to a CTA, the sums of dweight [dim]. Before that, with kShift, a row of weights for each of
+  // them, shifted as its units are.
+  extern __shared__ __align__(16) float columns[];
+  const float4* weights = reinterpret_cast<const float4*>(columns + threadIdx.y * nt * U * W) + threadIdx.x * 2;
+  const int shift = shift_of((int64_t)blockIdx.x * blockDim.y + threadIdx.y, a.dim);  // of all of its rows
+  if constexpr (kShift) {
+#pragma unroll
+    for (int k = 0; k < U * W; ++k) {
+      const int i = (int)threadIdx.x + nt * k, c = i - shift;
+      columns[threadIdx.y * nt * U * W + i] = c >= 0 && c < a.dim ? __ldg(a.weight + c) : 0.0f;
+    }
+    __syncthreads();
+  }
+  auto unit_weight = [&](int u, int c, float (&w)[W]) {
+    const float4* p = kShift ? weights + nt * u * 2 : reinterpret_cast<const float4*>(a.weight + c);
+    const float4 lo = kShift ? p[0] : __ldg(p), hi = kShift ? p[1] : __ldg(p + 1);
+    w[0] = lo.x;
+    w[1] = lo.y;
+    w[2] = lo.z;
+    w[3] = lo.w;
+    w[4] = hi.x;
+    w[5] = hi.y;
+    w[6] = hi.z;
+    w[7] = hi.w;
+  };
   wait_for_inputs();
   float acc[U][W];
 #pragma unroll
@@ -249,24 +323,28 @@ add_norm_bwd_kernel(const AddNormBwdArgs a, const int nt) {
   for (int64_t row0 = (int64_t)blockIdx.x * blockDim.y; row0 < a.rows; row0 += step) {
     const int64_t row = row0 + threadIdx.y, base = row * a.dim;
     const bool live = row < a.rows;
-    Unit<S, W> sv[U], dv[U];
-    Unit<T, W> gv[U];
+    Unit<S, kShift> sv[U], dv[U];
+    Unit<T, kShift> gv[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int c = ((int)threadIdx.x + nt * u) * W;
-      if (live && c < a.dim) {
-        sv[u].load(static_cast<const S*>(a.sum) + base + c);
-        gv[u].load(static_cast<const T*>(a.dy) + base + c);
-        if (a.dsum) dv[u].load(static_cast<const S*>(a.dsum) + base + c);
+      const At<kShift> at(shift, nt, u);
+      if (live && at.c < a.dim) {
+        sv[u].load(static_cast<const S*>(a.sum) + base + at.c, at, a.dim);
+        gv[u].load(static_cast<const T*>(a.dy) + base + at.c, at, a.dim);
+        if (a.dsum) dv[u].load(static_cast<const S*>(a.dsum) + base + at.c, at, a.dim);
       }
     }
     float sums[2] = {0.0f, 0.0f};  // of s^2, and of s weight dy
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int c = ((int)threadIdx.x + nt * u) * W;
-      if (live && c < a.dim) {
+      const At<kShift> at(shift, nt, u);
+      if (live && at.c < a.dim) {
+        if (!at.whole(a.dim)) {
+          sv[u].clear(at, a.dim);
+          gv[u].clear(at, a.dim);
+        }
         float w[W], v[W], g[W];
-        load_weight<W>(a.weight + c, w);
+        unit_weight(u, at.c, w);
         sv[u].unpack(v);
         gv[u].unpack(g);
 #pragma unroll
@@ -281,10 +359,10 @@ add_norm_bwd_kernel(const AddNormBwdArgs a, const int nt) {
     const float k = inv * inv * (sums[1] / (float)a.dim);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int c = ((int)threadIdx.x + nt * u) * W;
-      if (live && c < a.dim) {
+      const At<kShift> at(shift, nt, u);
+      if (live && at.c < a.dim) {
         float w[W], v[W], g[W], d[W];
-        load_weight<W>(a.weight + c, w);
+        unit_weight(u, at.c, w);
         sv[u].unpack(v);
         gv[u].unpack(g);
 #pragma unroll
@@ -297,26 +375,27 @@ add_norm_bwd_kernel(const AddNormBwdArgs a, const int nt) {
         }
         if (a.dx) {
           gv[u].pack(d);
-          gv[u].store(static_cast<T*>(a.dx) + base + c);
+          gv[u].store(static_cast<T*>(a.dx) + base + at.c, at, a.dim);
         }
         if (a.dresidual) {
           sv[u].pack(d);
-          sv[u].store(static_cast<S*>(a.dresidual) + base + c);
+          sv[u].store(static_cast<S*>(a.dresidual) + base + at.c, at, a.dim);
         }
       }
     }
   }
   if (!a.dweight) return;
+  if (kShift) __syncthreads();  // done with the weights
   for (int y = 0; y < (int)blockDim.y; ++y) {
     if ((int)threadIdx.y == y) {
       const bool last = y == (int)blockDim.y - 1;
       float* out = last ? a.partial + (int64_t)blockIdx.x * a.dim : columns;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int c = ((int)threadIdx.x + nt * u) * W;
-        if (c < a.dim)
+        const At<kShift> at(shift, nt, u);
 #pragma unroll
-          for (int j = 0; j < W; ++j) out[c + j] = (y > 0 ? columns[c + j] : 0.0f) + acc[u][j];
+        for (int j = 0; j < W; ++j)
+          if (at.c < a.dim && at.has(j, a.dim)) out[at.c + j] = (y > 0 ? columns[at.c + j] : 0.0f) + acc[u][j];
       }
     }
     if (blockDim.y > 1) __syncthreads();
@@ -406,17 +485,18 @@ __global__ void __launch_bounds__(kCtaThreads) add_norm_bwd_streamed_kernel(cons
   }
 }
 
+// Elements that a row's units span at most.
+int span(int dim) { return dim % W == 0 ? dim : dim + W - 1; }
 // Threads of a row, and rows of a CTA.
 struct Shape {
   int nt, rows;
 };
-Shape shape(int64_t rows, int dim, int unit, int held) {
-  const int fewest = 32 * ((dim + 32 * held - 1) / (32 * held));
-  const int most = 32 * ((dim + 32 * unit - 1) / (32 * unit));
+Shape shape(int64_t rows, int dim, int held) {
+  const int fewest = 32 * ((span(dim) + 32 * held - 1) / (32 * held));
+  const int most = 32 * ((span(dim) + 32 * W - 1) / (32 * W));
   if (rows <= device_sm_count()) return {std::max(fewest, std::min(most, kCtaThreads)), 1};
   return {fewest, std::max(1, kCtaThreads / fewest)};
 }
-int unit_of(int dim) { return dim % 8 == 0 ? 8 : dim % 2 == 0 ? 2 : 1; }
 
 cudaLaunchConfig_t config(int grid, dim3 block, size_t smem, cudaStream_t st, cudaLaunchAttribute* attr) {
   cudaLaunchConfig_t c = {};
@@ -433,43 +513,40 @@ cudaLaunchConfig_t config(int grid, dim3 block, size_t smem, cudaStream_t st, cu
 
 template <typename T, typename S, bool F8>
 cudaError_t run_norm(const AddNormArgs& a, cudaStream_t st) {
-  const int unit = unit_of(a.dim), held = held_by_thread(unit, sizeof(S), false);
-  if (a.dim > kMaxThreads * held) {
+  if (span(a.dim) > kMaxThreads * kHeld) {
     add_norm_streamed_kernel<T, S, F8><<<a.rows, kCtaThreads, 0, st>>>(a);
     return cudaGetLastError();
   }
-  const Shape s = shape(a.rows, a.dim, unit, held);
+  const Shape s = shape(a.rows, a.dim, kHeld);
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t c = config((a.rows + s.rows - 1) / s.rows, dim3(s.nt, s.rows), 0, st, &attr);
-  if (unit == 8) return cudaLaunchKernelEx(&c, add_norm_kernel<T, S, F8, 8>, a, s.nt);
-  if (unit == 2) return cudaLaunchKernelEx(&c, add_norm_kernel<T, S, F8, 2>, a, s.nt);
-  return cudaLaunchKernelEx(&c, add_norm_kernel<T, S, F8, 1>, a, s.nt);
+  if (a.dim % W == 0) return cudaLaunchKernelEx(&c, add_norm_kernel<T, S, F8, false>, a, s.nt);
+  return cudaLaunchKernelEx(&c, add_norm_kernel<T, S, F8, true>, a, s.nt);
 }
 
 template <typename T, typename S>
 cudaError_t run_norm_bwd(const AddNormBwdArgs& a, int* used, cudaStream_t st) {
-  const int unit = unit_of(a.dim), held = held_by_thread(unit, sizeof(S), true);
   const int most = add_rmsnorm_backward_parts(a.rows, a.dim);
-  if (a.dim > kMaxThreads * held) {
+  if (span(a.dim) > kMaxThreads * kBwdHeld) {
     *used = most;
     add_norm_bwd_streamed_kernel<T, S><<<most, kCtaThreads, 0, st>>>(a, most);
     return cudaGetLastError();
   }
-  const Shape s = shape(a.rows, a.dim, unit, held);
-  const size_t smem = s.rows > 1 ? (size_t)a.dim * 4 : 0;
+  const Shape s = shape(a.rows, a.dim, kBwdHeld);
+  const size_t smem = a.dim % W ? (size_t)s.rows * s.nt * kBwdHeld * 4 : s.rows > 1 ? (size_t)a.dim * 4 : 0;
   auto run = [&](auto kernel) {  // as many CTAs as the GPU holds: each loads a row while others work on theirs
     int fit = 0;
     const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, s.nt * s.rows, smem);
     if (e != cudaSuccess) return e;
     *used = (int)std::min<int64_t>({(int64_t)most, ((int64_t)a.rows + s.rows - 1) / s.rows,
                                     std::max(1, fit) * (int64_t)device_sm_count()});
+    if ((int64_t)*used * s.rows < a.rows) *used &= ~(W - 1);  // a thread's columns are the same in every W-th row
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t c = config(*used, dim3(s.nt, s.rows), smem, st, &attr);
     return cudaLaunchKernelEx(&c, kernel, a, s.nt);
   };
-  if (unit == 8) return run(add_norm_bwd_kernel<T, S, 8>);
-  if (unit == 2) return run(add_norm_bwd_kernel<T, S, 2>);
-  return run(add_norm_bwd_kernel<T, S, 1>);
+  if (a.dim % W == 0) return run(add_norm_bwd_kernel<T, S, false>);
+  return run(add_norm_bwd_kernel<T, S, true>);
 }
 
 }  // namespace

@@ -407,6 +407,37 @@ def test_add_rmsnorm_many_rows_backward_repeats():
     assert_bits_equal(got[0], got[1], "repeat")
 
 
+@pytest.mark.parametrize("dtype,stype", [(BF16, BF16), (BF16, F32), (F32, F32)])
+@pytest.mark.parametrize("rows,dim", [(6001, 33), (5003, 262), (6007, 1001)])
+def test_add_rmsnorm_rows_that_start_inside_a_unit(dtype, stype, rows, dim):
+    """Rows whose first and last elements share 16 bytes with other rows: those keep to themselves."""
+    dev = device()
+    x, r, w = randn(dim, rows, dim).to(dtype), randn(dim + 1, rows, dim).to(stype), randn(dim + 2, dim)
+    (s64, serr), yref, rel = R.add_rmsnorm(x, r, w, 1e-5)
+    x[100], x[rows - 2] = NAN, NAN
+    ok = torch.ones(rows, dtype=torch.bool)
+    ok[100] = ok[rows - 2] = False
+    gx, total, gw = x.to(dev), r.to(dev), w.to(dev)
+    out, q, scale = torch.empty_like(gx), torch.empty((rows, dim), dtype=E4M3, device=dev), torch.empty(rows, device=dev)
+    ss.add_rmsnorm(q, gx, gw, 1e-5, residual=total, scale=scale)
+    ss.add_rmsnorm(out, gx, gw, 1e-5, residual=total, sum=total)
+    torch.cuda.synchronize()
+    assert torch.isnan(out.cpu()[~ok]).all() and torch.isnan(total.cpu()[~ok].float()).all()
+    R.check(total.cpu()[ok], (s64[ok], serr[ok]), "sum")
+    R.check(out.cpu()[ok], tuple(v[ok] for v in yref), "out")
+    v = (yref[0] / scale.cpu().double()[:, None])[ok]
+    assert ((q.cpu().float().double()[ok] - v).abs() <= torch.maximum(v.abs() * 2.0 ** -4, torch.tensor(2.0 ** -10))
+            + 4 * rel * v.abs() + 2.0 ** -20).all()
+    dy, ds = randn(dim + 3, rows, dim).to(dtype), randn(dim + 4, rows, dim, std=0.5).to(stype)
+    src = s64.to(stype)
+    dref, wref = R.add_rmsnorm_backward(src, w, 1e-5, dy, ds)
+    dx, dr, dw = torch.empty_like(gx), ds.to(dev), torch.full((dim,), NAN, device=dev)
+    ss.add_rmsnorm_backward(dx, dr, dw, dy.to(dev), dr, src.to(dev), gw, 1e-5)
+    R.check(dx, dref, "dx")
+    R.check(dr, dref, "dresidual")
+    R.check(dw, wref, "dweight")
+
+
 def test_add_rmsnorm_rows_of_zeros_and_non_finite():
     dev = device()
     dim = 300
