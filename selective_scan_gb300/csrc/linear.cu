@@ -500,21 +500,42 @@ pair_kernel(const __grid_constant__ Job<kGrad> job) {
     const uint32_t lane_off = (uint32_t)(q * 32) << 16;
     float* blk = reinterpret_cast<float*>(smem + kOffEpi + (uint32_t)(warp - 2) * kEpiBytes);
     // what a chunk of 32 columns needs from global memory is fetched a chunk ahead, across tiles: waited for in
-    // its place, it took the epilogue to 15 us a tile (with SiLU and a residual), where 32 k-blocks take 9
+    // its place, it took the epilogue to 15 us a tile (with SiLU and a residual), where 32 k-blocks take 9.
+    // The residual is 32 words: four columns of eight rows, or at an edge and where rows are not aligned for that
+    // a column of 32 rows (8 192 x 1 024 x 4 095 81 us, 91 when only the first was fetched ahead).
+    using Raw = typename Quad<TO>::Raw;
     struct Chunk {
-      typename Quad<TO>::Raw res[8];
+      uint32_t res[32];
       Columns cols;
+    };
+    constexpr int kRaw = sizeof(Raw) / 4;
+    auto whole = [&](const Product& g, int64_t row0, int col0) {  // the same for the whole warp
+      return g.vec && col0 + 32 <= g.N && row0 + 32 <= g.M;
     };
     auto fetch = [&](const Tile& w, int c, Chunk& k) {
       const Product& g = job.g[w.which];
-      const int col = w.n0 + half * 128 + c + 4 * (lane & 7);
-      const int64_t row = (int64_t)w.m0 + (int)rank * 128 + q * 32 + (lane >> 3);
+      const int col0 = w.n0 + half * 128 + c, col = col0 + 4 * (lane & 7);
+      const int64_t row0 = (int64_t)w.m0 + (int)rank * 128 + q * 32;
       k.cols = load_columns(g, col);
-      if (!g.residual || !g.vec || col + 4 > g.N) return;
-      const TO* p = static_cast<const TO*>(g.residual) + row * g.ld_res + col;
+      if (!g.residual) return;
+      const TO* res = static_cast<const TO*>(g.residual);
+      if (whole(g, row0, col0)) {
+        const TO* p = res + (row0 + (lane >> 3)) * g.ld_res + col;
 #pragma unroll
-      for (int i = 0; i < 8; ++i, p += 4 * g.ld_res)
-        if (row + 4 * i < g.M) k.res[i] = *reinterpret_cast<const typename Quad<TO>::Raw*>(p);
+        for (int i = 0; i < 8; ++i, p += 4 * g.ld_res) {
+          const Raw r = *reinterpret_cast<const Raw*>(p);
+#pragma unroll
+          for (int j = 0; j < kRaw; ++j) k.res[kRaw * i + j] = reinterpret_cast<const uint32_t*>(&r)[j];
+        }
+      } else if (col0 + lane < g.N) {
+        const TO* p = res + row0 * g.ld_res + col0 + lane;
+#pragma unroll
+        for (int i = 0; i < 32; ++i, p += g.ld_res)
+          if (row0 + i < g.M) {
+            if constexpr (sizeof(TO) == 2) k.res[i] = *reinterpret_cast<const uint16_t*>(p);
+            else k.res[i] = *reinterpret_cast<const uint32_t*>(p);
+          }
+      }
     };
     Chunk now;
     Tile at = tile(0);
@@ -545,7 +566,7 @@ pair_kernel(const __grid_constant__ Job<kGrad> job) {
           __syncwarp();
           const float* mine = blk + (lane >> 3) * kEpiLd + 4 * (lane & 7);
           const int64_t row = row0 + (lane >> 3);
-          if (g.vec && n0 + c + 32 <= g.N && row0 + 32 <= g.M) {
+          if (whole(g, row0, n0 + c)) {
             // the whole block: a step at a time over 32 values, so that the branches are the block's
             float v[8][4];
 #pragma unroll
@@ -566,7 +587,10 @@ pair_kernel(const __grid_constant__ Job<kGrad> job) {
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 float r4[4];
-                Quad<TO>::unpack(now.res[i], r4);
+                Raw r;
+#pragma unroll
+                for (int j = 0; j < kRaw; ++j) reinterpret_cast<uint32_t*>(&r)[j] = now.res[kRaw * i + j];
+                Quad<TO>::unpack(r, r4);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) v[i][j] += r4[j];
               }
@@ -581,41 +605,32 @@ pair_kernel(const __grid_constant__ Job<kGrad> job) {
             const int rows = (int)min((int64_t)32, g.M - row0);
             if (one < g.N) {
               const float sc = g.scale_n ? g.scale_n[one] : 1.0f, bi = g.bias ? g.bias[one] : 0.0f;
-              const TO* res = g.residual ? static_cast<const TO*>(g.residual) + row0 * g.ld_res + one : nullptr;
               TO* o = static_cast<TO*>(g.out) + row0 * g.ld_out + one;
               __nv_bfloat16* pre = g.pre ? g.pre + row0 * g.N + one : nullptr;
               const float* from = blk + lane;
               constexpr int kSome = 16;
-              auto some = [&](auto all, int left) {  // kSome rows, `left` of them there
-                constexpr bool kAll = decltype(all)::value;
-                float v[kSome], add[kSome];
+              auto some = [&](auto first) {  // kSome rows, or as many of them as there are
+                constexpr int i0 = decltype(first)::value;
+                float v[kSome];
 #pragma unroll
-                for (int i = 0; i < kSome; ++i) v[i] = fmaf(from[i * kEpiLd], sc, bi);
-                from += kSome * kEpiLd;
-                if (res) {
-#pragma unroll
-                  for (int i = 0; i < kSome; ++i, res += g.ld_res)
-                    if (kAll || i < left) add[i] = Act<TO>::to_f(*res);
-                }
+                for (int i = 0; i < kSome; ++i) v[i] = fmaf(from[(i0 + i) * kEpiLd], sc, bi);
                 if (pre) {
 #pragma unroll
                   for (int i = 0; i < kSome; ++i, pre += g.N)
-                    if (kAll || i < left) *pre = __float2bfloat16_rn(v[i]);
+                    if (i0 + i < rows) *pre = __float2bfloat16_rn(v[i]);
                 }
                 activate_all(v, g.act);
-                if (res) {
+                if (g.residual) {
 #pragma unroll
-                  for (int i = 0; i < kSome; ++i) v[i] += add[i];
+                  for (int i = 0; i < kSome; ++i)
+                    v[i] += __uint_as_float(sizeof(TO) == 2 ? now.res[i0 + i] << 16 : now.res[i0 + i]);
                 }
 #pragma unroll
                 for (int i = 0; i < kSome; ++i, o += g.ld_out)
-                  if (kAll || i < left) *o = Act<TO>::from_f(v[i]);
+                  if (i0 + i < rows) *o = Act<TO>::from_f(v[i]);
               };
-#pragma unroll 1
-              for (int left = rows; left > 0; left -= kSome) {
-                if (left >= kSome) some(std::true_type{}, left);
-                else some(std::false_type{}, left);
-              }
+              some(std::integral_constant<int, 0>{});
+              some(std::integral_constant<int, kSome>{});
             }
           }
           __syncwarp();
