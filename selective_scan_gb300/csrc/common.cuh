@@ -10,15 +10,19 @@
 
 namespace mamba2 {
 
-__device__ __forceinline__ int32_t seq_slot(const SeqTable& t, int i) {
+// (Table: SeqTable, or one of its form for fewer sequences)
+template <typename Table>
+__device__ __forceinline__ int32_t seq_slot(const Table& t, int i) {
   return (int32_t)(t.slot_fresh[i] & 0x7fffffffu);
 }
-__device__ __forceinline__ bool seq_fresh(const SeqTable& t, int i) {
+template <typename Table>
+__device__ __forceinline__ bool seq_fresh(const Table& t, int i) {
   return (t.slot_fresh[i] >> 31) != 0u;
 }
 
 // Largest i in [0, n) with tile[i] <= w (tile is non-decreasing).
-__device__ __forceinline__ int find_tile_seq(const SeqTable& t, int w) {
+template <typename Table>
+__device__ __forceinline__ int find_tile_seq(const Table& t, int w) {
   int lo = 0, hi = t.n - 1;
   while (lo < hi) {
     int mid = (lo + hi + 1) >> 1;

@@ -139,7 +139,7 @@ unsigned int read_gemm_timeouts();
 // ------------------------------------------------------ recurrent block ----
 // Gated recurrence, forward. tab.tile[i] = the sequence's first chunk (chunks of
 // MAMBA2_RECURRENCE_CHUNK tokens, ceil(length / chunk) a sequence).
-struct RecArgs {
+struct RecTensors {
   void* y;
   float* ckpt;  // [chunks * chunk / step, dim] or null
   const void* x;
@@ -148,6 +148,8 @@ struct RecArgs {
   float* state;
   int32_t dim;
   int64_t ld_y, ld_x, ld_gate;
+};
+struct RecArgs : RecTensors {
   SeqTable tab;
 };
 cudaError_t launch_recurrence(const RecArgs& a, mamba2_dtype act, void* ws, cudaStream_t st);
@@ -172,7 +174,7 @@ struct RecStepArgs {
 cudaError_t launch_recurrence_step(const RecStepArgs& a, mamba2_dtype act, cudaStream_t st);
 
 // Gated recurrence, backward (tab.tile as in RecArgs; slots unused).
-struct RecBwdArgs {
+struct RecBwdTensors {
   void* dx;
   void* dgate;
   float* dlower;
@@ -185,6 +187,8 @@ struct RecBwdArgs {
   const float* ckpt;
   int32_t dim;
   int64_t ld_dx, ld_dgate, ld_dy, ld_x, ld_gate;
+};
+struct RecBwdArgs : RecBwdTensors {
   SeqTable tab;
 };
 cudaError_t launch_recurrence_backward(const RecBwdArgs& a, mamba2_dtype act, void* ws, cudaStream_t st);

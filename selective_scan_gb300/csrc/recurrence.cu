@@ -188,23 +188,75 @@ struct Info {
   int l, last; // chunks of the run before this one (in the pass's order), and whether none follows
 };
 
-template <bool kReverse>
-__device__ __forceinline__ void tile_info(Info& f, const SeqTable& t, int item, int items, int groups) {
+// The runs of a call. They are launch parameters, which take time to hand over by the byte, so there is a short form:
+// 300 tokens by 1 536 channels 15.3 us forwards and 21.4 backwards with it, 16.3 and 24.5 with the long one.
+//
+// Also the order in which the chunks of several runs are taken: every run's first, then every run's second, and so
+// on, so that a chunk's predecessors are as long ago as can be and few of them have to be waited for (each run in
+// turn, as the rows lie: 234 us against 184 for 64 runs of 65 536 tokens in all by 2 048 channels, and 212 against
+// 177 for eight).
+template <int kMost>
+struct Runs {
+  int32_t n;
+  int32_t sorted;             // runs that have chunks; 0: chunks in order of rows
+  int32_t cu[kMost + 1];      // first rows
+  int32_t tile[kMost + 1];    // first chunks
+  int32_t before[kMost + 1];  // [c]: chunks that are taken before the c longest runs are alone
+  uint32_t slot_fresh[kMost];
+  uint16_t run[kMost];        // the longest first
+};
+constexpr int kFewRuns = 64;
+template <int kMost>
+void fill_runs(Runs<kMost>& o, const SeqTable& t, bool interleave) {
+  o.n = t.n;
+  o.sorted = 0;
+  std::copy(t.cu, t.cu + t.n + 1, o.cu);
+  std::copy(t.tile, t.tile + t.n + 1, o.tile);
+  std::copy(t.slot_fresh, t.slot_fresh + t.n, o.slot_fresh);
+  if (!interleave) return;
+  auto chunks = [&](int r) { return t.tile[r + 1] - t.tile[r]; };
+  for (int i = 0; i < t.n; ++i)
+    if (chunks(i) > 0) o.run[o.sorted++] = (uint16_t)i;
+  std::stable_sort(o.run, o.run + o.sorted, [&](int a, int b) { return chunks(a) > chunks(b); });
+  int shorter = 0;  // chunks of the runs after the first c
+  o.before[o.sorted] = 0;
+  for (int c = o.sorted - 1; c >= 1; --c) {
+    shorter += chunks(o.run[c]);
+    o.before[c] = shorter + c * chunks(o.run[c]);
+  }
+}
+
+template <bool kReverse, int kMost>
+__device__ __forceinline__ void tile_info(Info& f, const Runs<kMost>& t, int item, int items, int groups) {
   if (item >= items) {
     f.item = -1;
     return;
   }
   f.item = item;
-  const int chunks = t.tile[t.n];
   const int pos = item / groups;
   f.group = item - pos * groups;
-  f.chunk = kReverse ? chunks - 1 - pos : pos;
-  const int s = find_tile_seq(t, f.chunk);
+  int s, of;
+  if (t.sorted > 0) {
+    int c = 1, hi = t.sorted;  // the fewest runs left that pos allows
+    while (c < hi) {
+      const int mid = (c + hi) >> 1;
+      if (t.before[mid] <= pos) hi = mid; else c = mid + 1;
+    }
+    const int in = pos - t.before[c], ended = c < t.sorted ? t.tile[t.run[c] + 1] - t.tile[t.run[c]] : 0;
+    s = t.run[in % c];
+    of = t.tile[s + 1] - t.tile[s];
+    f.l = ended + in / c;
+    f.chunk = t.tile[s] + (kReverse ? of - 1 - f.l : f.l);
+  } else {
+    f.chunk = kReverse ? t.tile[t.n] - 1 - pos : pos;
+    s = find_tile_seq(t, f.chunk);
+    of = t.tile[s + 1] - t.tile[s];
+    f.l = kReverse ? of - 1 - (f.chunk - t.tile[s]) : f.chunk - t.tile[s];
+  }
   f.seq = s;
-  const int c = f.chunk - t.tile[s], of = t.tile[s + 1] - t.tile[s];
+  const int c = f.chunk - t.tile[s];
   f.row = t.cu[s] + c * kChunkR;
   f.n = min(kChunkR, t.cu[s + 1] - f.row);
-  f.l = kReverse ? of - 1 - c : c;
   f.last = f.l == of - 1;
 }
 
@@ -498,9 +550,9 @@ struct FwdShared {
 
 // The products of the f's go into shared memory, over the inputs that the lane has consumed (the same 8 bytes
 // a pair of channels), so that three CTAs fit an SM's registers.
-template <typename T, bool kVec>
+template <typename T, bool kVec, int kMost>
 __global__ void __launch_bounds__(kThreads, kCtas)
-rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ CUtensorMap mx,
+rec_fwd_kernel(const __grid_constant__ RecTensors a, const __grid_constant__ Runs<kMost> t, const __grid_constant__ CUtensorMap mx,
                const __grid_constant__ CUtensorMap mg, const __grid_constant__ Chain ch, const int items,
                const int groups) {
   extern __shared__ __align__(128) unsigned char stages[];
@@ -512,9 +564,9 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ CUtens
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   // runs of no token: a fresh one zeroes its slot
-  for (int i = blockIdx.x; i < a.tab.n; i += gridDim.x)
-    if (a.tab.cu[i] == a.tab.cu[i + 1] && seq_fresh(a.tab, i))
-      for (int c = threadIdx.x; c < a.dim; c += kThreads) a.state[(int64_t)seq_slot(a.tab, i) * a.dim + c] = 0.0f;
+  for (int i = blockIdx.x; i < t.n; i += gridDim.x)
+    if (t.cu[i] == t.cu[i + 1] && seq_fresh(t, i))
+      for (int c = threadIdx.x; c < a.dim; c += kThreads) a.state[(int64_t)seq_slot(t, i) * a.dim + c] = 0.0f;
 
   const Stream<T> in_streams[2] = {{static_cast<const T*>(a.x), a.ld_x, &mx}, {static_cast<const T*>(a.gate), a.ld_gate, &mg}};
   auto load = [&](int i) {  // this warp's rows of tile i, if there is one
@@ -528,7 +580,7 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ CUtens
   }
   if (threadIdx.x == 0)
     for (int i = 0; i < kFwdStages<kVec>; ++i)
-      tile_info<false>(s.info[i], a.tab, take<kFwdStages<kVec>>(ch, i, items), items, groups);
+      tile_info<false>(s.info[i], t, take<kFwdStages<kVec>>(ch, i, items), items, groups);
   __syncthreads();
   for (int i = 0; i < kFwdStages<kVec>; ++i) load(i);
 
@@ -540,13 +592,13 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ CUtens
     const int left = a.dim - ch0;  // channels of this lane and those after it
     int next = 0;
     if (threadIdx.x == 0) next = take<kFwdStages<kVec>>(ch, i + kFwdStages<kVec>, items);
-    const int first = a.tab.tile[f.seq];
+    const int first = t.tile[f.seq];
     const int before = f.l > 0 ? maps_before(f.l) : 0;
     float h0[C];  // what the run starts from: asked for early, the run's other tiles wait for it
     if (warp == kWarps - 1 && f.l == 0)
 #pragma unroll
       for (int c = 0; c < C; ++c)
-        h0[c] = c < left && !seq_fresh(a.tab, f.seq) ? a.state[(int64_t)seq_slot(a.tab, f.seq) * a.dim + ch0 + c] : 0.0f;
+        h0[c] = c < left && !seq_fresh(t, f.seq) ? a.state[(int64_t)seq_slot(t, f.seq) * a.dim + ch0 + c] : 0.0f;
     // ---- scan from zero
     unsigned char* st = stages + (i % kFwdStages<kVec>) * kFwdStage<kVec>;
     const Reader<T, kVec, 2> rd(st, f, in_streams, warp, lane);
@@ -625,7 +677,7 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ CUtens
       }
     }
     look_back<T, false>(ch, f, first, groups, before, s.before, warp, lane);
-    if (threadIdx.x == 0) tile_info<false>(s.info[(i + kFwdStages<kVec>) % kInfos], a.tab, next, items, groups);
+    if (threadIdx.x == 0) tile_info<false>(s.info[(i + kFwdStages<kVec>) % kInfos], t, next, items, groups);
     __syncthreads();
     float in[C];
     if (warp == kWarps - 1) {
@@ -639,7 +691,7 @@ rec_fwd_kernel(const __grid_constant__ RecArgs a, const __grid_constant__ CUtens
       if (f.last) {
 #pragma unroll
         for (int c = 0; c < C; ++c)
-          if (c < left) a.state[(int64_t)seq_slot(a.tab, f.seq) * a.dim + ch0 + c] = end[c];
+          if (c < left) a.state[(int64_t)seq_slot(t, f.seq) * a.dim + ch0 + c] = end[c];
       } else if (f.l % kGroup == 0 && f.l > 0) {
         publish_state<T>(ch, f, first, groups, end, lane);
       }
@@ -692,9 +744,9 @@ struct BwdShared {
   uint32_t abort;
 };
 
-template <typename T, bool kVec>
+template <typename T, bool kVec, int kMost>
 __global__ void __launch_bounds__(kThreads, kCtas)
-rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUtensorMap mx,
+rec_bwd_kernel(const __grid_constant__ RecBwdTensors a, const __grid_constant__ Runs<kMost> t, const __grid_constant__ CUtensorMap mx,
                const __grid_constant__ CUtensorMap mg, const __grid_constant__ CUtensorMap md,
                const __grid_constant__ Chain ch, float* part, const int items, const int groups) {
   extern __shared__ __align__(128) unsigned char stages[];
@@ -706,8 +758,8 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUt
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (a.dstate)  // a run of no token hands its gradient on
-    for (int i = blockIdx.x; i < a.tab.n; i += gridDim.x)
-      if (a.tab.cu[i] == a.tab.cu[i + 1])
+    for (int i = blockIdx.x; i < t.n; i += gridDim.x)
+      if (t.cu[i] == t.cu[i + 1])
         for (int c = threadIdx.x; c < a.dim; c += kThreads)
           a.dstate[(int64_t)i * a.dim + c] = a.dstate_end ? a.dstate_end[(int64_t)i * a.dim + c] : 0.0f;
 
@@ -737,7 +789,7 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUt
   };
   if (threadIdx.x == 0)
     for (int i = 0; i < kBwdStages; ++i)
-      tile_info<true>(s.info[i], a.tab, take<kBwdStages>(ch, i, items), items, groups);
+      tile_info<true>(s.info[i], t, take<kBwdStages>(ch, i, items), items, groups);
   __syncthreads();
   for (int i = 0; i < kBwdStages; ++i) load(i);
 
@@ -750,7 +802,7 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUt
     const int left = a.dim - ch0;
     int next = 0;
     if (threadIdx.x == 0) next = take<kBwdStages>(ch, i + kBwdStages, items);
-    const int first = a.tab.tile[f.seq];
+    const int first = t.tile[f.seq];
     const int before = f.l > 0 ? maps_before(f.l) : 0;
     float h0[C];
     if (warp == 0 && f.l == 0)
@@ -837,7 +889,7 @@ rec_bwd_kernel(const __grid_constant__ RecBwdArgs a, const __grid_constant__ CUt
     }
     look_back<T, true>(ch, f, first, groups, before, s.before, warp, lane);
     // info[i + 2] takes the place of tile i - 2, whose part of dlower has been summed
-    if (threadIdx.x == 0) tile_info<true>(s.info[(i + kBwdStages) % kInfos], a.tab, next, items, groups);
+    if (threadIdx.x == 0) tile_info<true>(s.info[(i + kBwdStages) % kInfos], t, next, items, groups);
     __syncthreads();
     float in[C];
     fold_before(s.before, before, in, lane);
@@ -1068,46 +1120,18 @@ bool make_map(CUtensorMap* tm, const void* base, int64_t rows, int64_t dim, int6
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, bool kVec>
-cudaError_t run_fwd(const RecArgs& a, const Chain& ch, int items, int groups, cudaStream_t st) {
-  constexpr int smem = kFwdStages<kVec> * kFwdStage<kVec>;
-  CUtensorMap mx, mg;
-  std::memset(&mx, 0, sizeof mx);
-  std::memset(&mg, 0, sizeof mg);
-  const int rows = a.tab.cu[a.tab.n];
-  if (kVec && rows > 0 && !(make_map<T>(&mx, a.x, rows, a.dim, a.ld_x) && make_map<T>(&mg, a.gate, rows, a.dim, a.ld_gate)))
-    return cudaErrorInvalidValue;
-  const cudaError_t e = cudaFuncSetAttribute(rec_fwd_kernel<T, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  rec_fwd_kernel<T, kVec><<<ctas(items, kCtas), kThreads, smem, st>>>(a, mx, mg, ch, items, groups);
-  return cudaGetLastError();
-}
-template <typename T, bool kVec>
-cudaError_t run_bwd(const RecBwdArgs& a, const Chain& ch, float* part, int items, int groups, cudaStream_t st) {
-  constexpr int smem = kBwdStages * kBwdStage<kVec>;
-  CUtensorMap mx, mg, md;
-  std::memset(&mx, 0, sizeof mx);
-  std::memset(&mg, 0, sizeof mg);
-  std::memset(&md, 0, sizeof md);
-  const int rows = a.tab.cu[a.tab.n];
-  if (kVec && rows > 0 &&
-      !(make_map<T>(&mx, a.x, rows, a.dim, a.ld_x) && make_map<T>(&mg, a.gate, rows, a.dim, a.ld_gate) &&
-        make_map<T>(&md, a.dy, rows, a.dim, a.ld_dy)))
-    return cudaErrorInvalidValue;
-  const cudaError_t e = cudaFuncSetAttribute(rec_bwd_kernel<T, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  rec_bwd_kernel<T, kVec><<<ctas(items, kCtas), kThreads, smem, st>>>(a, mx, mg, md, ch, part, items, groups);
-  return cudaGetLastError();
-}
-
 // The plan that both passes share: tiles, and the chain (cleared on the stream) when a run has several.
 struct Tiles {
   int groups, items;
   Chain chain;
+  bool interleave;  // several runs, chained
   cudaError_t status;
 };
 Tiles plan(const SeqTable& t, mamba2_dtype act, int32_t dim, void* ws, cudaStream_t st) {
-  Tiles p = {};
+  Tiles p;
+  p.chain = {};
+  p.interleave = false;
+  p.status = cudaSuccess;
   const int width = act == MAMBA2_BF16 ? kTileCh<__nv_bfloat16> : kTileCh<float>;
   p.groups = (dim + width - 1) / width;
   const int64_t chunks = t.tile[t.n], items = chunks * p.groups;
@@ -1119,10 +1143,55 @@ Tiles plan(const SeqTable& t, mamba2_dtype act, int32_t dim, void* ws, cudaStrea
   bool chained = false;
   for (int i = 0; i < t.n; ++i) chained |= t.tile[i + 1] - t.tile[i] > 1;
   if (chained) {
+    p.interleave = t.n > 1;
     p.chain = chain_at(ws, chunks, (int64_t)p.groups * width);
     p.status = cudaMemsetAsync(ws, 0xff, chain_bytes(chunks, t.n, (int64_t)p.groups * width), st);
   }
   return p;
+}
+
+template <typename T, bool kVec>
+cudaError_t run_fwd(const RecArgs& a, const Tiles& p, cudaStream_t st) {
+  constexpr int smem = kFwdStages<kVec> * kFwdStage<kVec>;
+  CUtensorMap mx, mg;
+  std::memset(&mx, 0, sizeof mx);
+  std::memset(&mg, 0, sizeof mg);
+  const int rows = a.tab.cu[a.tab.n];
+  if (kVec && rows > 0 && !(make_map<T>(&mx, a.x, rows, a.dim, a.ld_x) && make_map<T>(&mg, a.gate, rows, a.dim, a.ld_gate)))
+    return cudaErrorInvalidValue;
+  auto run = [&](auto kernel, auto most) {
+    Runs<decltype(most)::value> runs;
+    fill_runs(runs, a.tab, p.interleave);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<ctas(p.items, kCtas), kThreads, smem, st>>>(a, runs, mx, mg, p.chain, p.items, p.groups);
+    return cudaGetLastError();
+  };
+  if (a.tab.n <= kFewRuns) return run(rec_fwd_kernel<T, kVec, kFewRuns>, std::integral_constant<int, kFewRuns>());
+  return run(rec_fwd_kernel<T, kVec, MAMBA2_MAX_SEQS>, std::integral_constant<int, MAMBA2_MAX_SEQS>());
+}
+template <typename T, bool kVec>
+cudaError_t run_bwd(const RecBwdArgs& a, const Tiles& p, float* part, cudaStream_t st) {
+  constexpr int smem = kBwdStages * kBwdStage<kVec>;
+  CUtensorMap mx, mg, md;
+  std::memset(&mx, 0, sizeof mx);
+  std::memset(&mg, 0, sizeof mg);
+  std::memset(&md, 0, sizeof md);
+  const int rows = a.tab.cu[a.tab.n];
+  if (kVec && rows > 0 &&
+      !(make_map<T>(&mx, a.x, rows, a.dim, a.ld_x) && make_map<T>(&mg, a.gate, rows, a.dim, a.ld_gate) &&
+        make_map<T>(&md, a.dy, rows, a.dim, a.ld_dy)))
+    return cudaErrorInvalidValue;
+  auto run = [&](auto kernel, auto most) {
+    Runs<decltype(most)::value> runs;
+    fill_runs(runs, a.tab, p.interleave);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<ctas(p.items, kCtas), kThreads, smem, st>>>(a, runs, mx, mg, md, p.chain, part, p.items, p.groups);
+    return cudaGetLastError();
+  };
+  if (a.tab.n <= kFewRuns) return run(rec_bwd_kernel<T, kVec, kFewRuns>, std::integral_constant<int, kFewRuns>());
+  return run(rec_bwd_kernel<T, kVec, MAMBA2_MAX_SEQS>, std::integral_constant<int, MAMBA2_MAX_SEQS>());
 }
 
 }  // namespace
@@ -1145,10 +1214,10 @@ cudaError_t launch_recurrence(const RecArgs& a, mamba2_dtype act, void* ws, cuda
   const size_t e = act == MAMBA2_BF16 ? 2 : 4;
   const bool vec = rows16(a.x, a.ld_x, e) && rows16(a.gate, a.ld_gate, e) && rows16(a.y, a.ld_y, e);
   if (act == MAMBA2_BF16)
-    return vec ? run_fwd<__nv_bfloat16, true>(a, p.chain, p.items, p.groups, st)
-               : run_fwd<__nv_bfloat16, false>(a, p.chain, p.items, p.groups, st);
-  return vec ? run_fwd<float, true>(a, p.chain, p.items, p.groups, st)
-             : run_fwd<float, false>(a, p.chain, p.items, p.groups, st);
+    return vec ? run_fwd<__nv_bfloat16, true>(a, p, st)
+               : run_fwd<__nv_bfloat16, false>(a, p, st);
+  return vec ? run_fwd<float, true>(a, p, st)
+             : run_fwd<float, false>(a, p, st);
 }
 
 cudaError_t launch_recurrence_backward(const RecBwdArgs& a, mamba2_dtype act, void* ws, cudaStream_t st) {
@@ -1161,11 +1230,11 @@ cudaError_t launch_recurrence_backward(const RecBwdArgs& a, mamba2_dtype act, vo
                    rows16(a.dx, a.ld_dx, es) && rows16(a.dgate, a.ld_dgate, es);
   cudaError_t e;
   if (act == MAMBA2_BF16)
-    e = vec ? run_bwd<__nv_bfloat16, true>(a, p.chain, part, p.items, p.groups, st)
-            : run_bwd<__nv_bfloat16, false>(a, p.chain, part, p.items, p.groups, st);
+    e = vec ? run_bwd<__nv_bfloat16, true>(a, p, part, st)
+            : run_bwd<__nv_bfloat16, false>(a, p, part, st);
   else
-    e = vec ? run_bwd<float, true>(a, p.chain, part, p.items, p.groups, st)
-            : run_bwd<float, false>(a, p.chain, part, p.items, p.groups, st);
+    e = vec ? run_bwd<float, true>(a, p, part, st)
+            : run_bwd<float, false>(a, p, part, st);
   if (e == cudaSuccess && a.dlower) e = launch_column_sum(a.dlower, part, (int)chunks, a.dim, st);
   return e;
 }

@@ -101,6 +101,31 @@ def test_recurrence_forward_and_backward(dtype, lengths, dim, off, extra):
             R.check(got, want[name], name)
 
 
+@pytest.mark.parametrize("runs", [2, 64, 65, 300])
+def test_recurrence_many_runs_of_different_lengths(runs):
+    """Runs whose chunks are taken in turns: longer and shorter ones, some empty, in no order."""
+    dev = device()
+    g = torch.Generator().manual_seed(runs)
+    lengths = [int(v) for v in (torch.rand(runs, generator=g) ** 3 * (3 if runs > 100 else 9) * 128)]
+    lengths[0], lengths[1] = 700, 0
+    dim = 72
+    x, gate, lo, pool, slots, fresh = rec_inputs(runs, lengths, dim, BF16, True)
+    cu, rows = cu_of(lengths), sum(lengths)
+    ref = R.recurrence(x, gate, lo, pool, cu, slots, fresh)
+    gx, gg, glo, st = x.to(dev), gate.to(dev), lo.to(dev), pool.to(dev)
+    y, kept = torch.empty_like(gx), torch.empty((ss.gated_recurrence_checkpoints(cu), dim), device=dev)
+    ss.gated_recurrence(y, gx, gg, glo, st, cu, slots, fresh, checkpoints=kept)
+    dy, de = randn(runs + 8, rows, dim).to(BF16), randn(runs + 9, runs, dim)
+    want = R.recurrence_backward(x, gate, lo, ref, cu, dy, de)
+    dx, dg, dlo, d0 = torch.empty_like(gx), torch.empty_like(gx), torch.empty_like(glo), torch.empty((runs, dim), device=dev)
+    ss.gated_recurrence_backward(dx, dg, dlo, d0, dy.to(dev), de.to(dev), gx, gg, glo, kept, cu)
+    torch.cuda.synchronize()
+    R.check(y, ref["y"], "y")
+    R.check(st, ref["pool"], "state")
+    for name, got in (("dx", dx), ("dgate", dg), ("dstate", d0), ("dlower", dlo)):
+        R.check(got, want[name], name)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("dim,at", [(130, ((0, 0), (1, 1), (2, 3), (3, 6), (5, 7))), (67, ((2, 7), (0, 1), (3, 4), (0, 0), (5, 6)))])
 def test_recurrence_matrices_of_different_strides(dtype, dim, at):
