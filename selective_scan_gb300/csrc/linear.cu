@@ -516,6 +516,7 @@ pair_kernel(const __grid_constant__ Job<kGrad> job) {
       const Product& g = job.g[w.which];
       const int col0 = w.n0 + half * 128 + c, col = col0 + 4 * (lane & 7);
       const int64_t row0 = (int64_t)w.m0 + (int)rank * 128 + q * 32;
+      if (kGrad) return;  // (gradients are the products as they are)
       k.cols = load_columns(g, col);
       if (!g.residual) return;
       const TO* res = static_cast<const TO*>(g.residual);
@@ -546,7 +547,7 @@ pair_kernel(const __grid_constant__ Job<kGrad> job) {
       const int64_t row0 = (int64_t)at.m0 + (int)rank * 128 + q * 32;
       const int n0 = at.n0 + half * 128;
       const Tile after = tile(min(t + 1, mine - 1));
-      const float sm = g.scale_m && row0 + lane < g.M ? g.scale_m[row0 + lane] : 1.0f;
+      const float sm = !kGrad && g.scale_m && row0 + lane < g.M ? g.scale_m[row0 + lane] : 1.0f;
       if (!warp_wait(bar(kAccFull + buf), (uint32_t)((t >> 1) & 1), s_abort)) break;
       tc_fence_after();
 #pragma unroll 1
@@ -572,18 +573,18 @@ pair_kernel(const __grid_constant__ Job<kGrad> job) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const float4 f = *reinterpret_cast<const float4*>(mine + 4 * i * kEpiLd);
-              v[i][0] = fmaf(f.x, now.cols.scale[0], now.cols.bias[0]);
-              v[i][1] = fmaf(f.y, now.cols.scale[1], now.cols.bias[1]);
-              v[i][2] = fmaf(f.z, now.cols.scale[2], now.cols.bias[2]);
-              v[i][3] = fmaf(f.w, now.cols.scale[3], now.cols.bias[3]);
+              v[i][0] = kGrad ? f.x : fmaf(f.x, now.cols.scale[0], now.cols.bias[0]);
+              v[i][1] = kGrad ? f.y : fmaf(f.y, now.cols.scale[1], now.cols.bias[1]);
+              v[i][2] = kGrad ? f.z : fmaf(f.z, now.cols.scale[2], now.cols.bias[2]);
+              v[i][3] = kGrad ? f.w : fmaf(f.w, now.cols.scale[3], now.cols.bias[3]);
             }
-            if (g.pre) {
+            if (!kGrad && g.pre) {
               __nv_bfloat16* p = g.pre + row * g.N + col;
 #pragma unroll
               for (int i = 0; i < 8; ++i, p += 4 * (int64_t)g.N) *reinterpret_cast<uint2*>(p) = Quad<__nv_bfloat16>::pack(v[i]);
             }
-            activate_all(reinterpret_cast<float(&)[32]>(v), g.act);
-            if (g.residual) {
+            if (!kGrad) activate_all(reinterpret_cast<float(&)[32]>(v), g.act);
+            if (!kGrad && g.residual) {
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 float r4[4];
@@ -604,23 +605,24 @@ pair_kernel(const __grid_constant__ Job<kGrad> job) {
             const int one = n0 + c + lane;
             const int rows = (int)min((int64_t)32, g.M - row0);
             if (one < g.N) {
-              const float sc = g.scale_n ? g.scale_n[one] : 1.0f, bi = g.bias ? g.bias[one] : 0.0f;
+              const float sc = !kGrad && g.scale_n ? g.scale_n[one] : 1.0f;
+              const float bi = !kGrad && g.bias ? g.bias[one] : 0.0f;
               TO* o = static_cast<TO*>(g.out) + row0 * g.ld_out + one;
-              __nv_bfloat16* pre = g.pre ? g.pre + row0 * g.N + one : nullptr;
+              __nv_bfloat16* pre = !kGrad && g.pre ? g.pre + row0 * g.N + one : nullptr;
               const float* from = blk + lane;
               constexpr int kSome = 16;
               auto some = [&](auto first) {  // kSome rows, or as many of them as there are
                 constexpr int i0 = decltype(first)::value;
                 float v[kSome];
 #pragma unroll
-                for (int i = 0; i < kSome; ++i) v[i] = fmaf(from[(i0 + i) * kEpiLd], sc, bi);
+                for (int i = 0; i < kSome; ++i) v[i] = kGrad ? from[(i0 + i) * kEpiLd] : fmaf(from[(i0 + i) * kEpiLd], sc, bi);
                 if (pre) {
 #pragma unroll
                   for (int i = 0; i < kSome; ++i, pre += g.N)
                     if (i0 + i < rows) *pre = __float2bfloat16_rn(v[i]);
                 }
-                activate_all(v, g.act);
-                if (g.residual) {
+                if (!kGrad) activate_all(v, g.act);
+                if (!kGrad && g.residual) {
 #pragma unroll
                   for (int i = 0; i < kSome; ++i)
                     v[i] += __uint_as_float(sizeof(TO) == 2 ? now.res[i0 + i] << 16 : now.res[i0 + i]);
@@ -630,7 +632,7 @@ pair_kernel(const __grid_constant__ Job<kGrad> job) {
                   if (i0 + i < rows) *o = Act<TO>::from_f(v[i]);
               };
               some(std::integral_constant<int, 0>{});
-              some(std::integral_constant<int, kSome>{});
+              if (rows > kSome) some(std::integral_constant<int, kSome>{});
             }
           }
           __syncwarp();
