@@ -16,8 +16,8 @@
 // are not 16-byte aligned: a warp fetches only the rows that it will read, so a stage is handed
 // over without the other warps, and the next tile's copies are in flight while a tile waits for
 // its predecessors (with one stage, while the others finish). Unaligned rows are realigned as
-// they are read: for eight runs of 32 768 tokens in all by 2 047 channels of bf16 161 us forwards
-// and 269 backwards (by 2 048: 112 and 177); copied word by word, 192 and 313.
+// they are read: for eight runs of 32 768 tokens in all by 2 047 channels of bf16 154 us forwards
+// and 267 backwards (by 2 048: 97 and 161); copied word by word it was 31 and 44 us more.
 //
 // What precedes chunk l of a run, the same for any timing (so results repeat bit for bit):
 // every chunk publishes its map, and every 16th (0, 16, 32, ...) the state after it too (the
@@ -40,12 +40,12 @@
 // y, and unrounded), and makes dx and dgate in one more sweep over its tokens. dlower is
 // summed per tile and then over the tiles, in order.
 //
-// Measured (GB300, 65 536 tokens x 2 048 channels, bf16, with lower bounds): one run 199 us
-// forward (4.05 TB/s, 60 % of the measured copy rate) and 322 backward (4.2 TB/s); 512 runs,
-// where nothing waits, 171 and 306. fp32 moves 5.7 TB/s either way. What bounds it is issue:
-// 890 instructions a warp and tile forward (26 a token to scan, 7 to store, 150 to look back)
-// at 2.3 an SM and clock, of which 59 us would remain if they were free; then the waits for
-// maps of tiles that run at the same time.
+// Measured (GB300, 65 536 tokens x 2 048 channels, bf16, with lower bounds and, forward, checkpoints): one run
+// 210 us forward (199 without checkpoints: 4.05 TB/s, 60 % of the measured copy rate) and 325 backward (4.2 TB/s);
+// eight runs 177 and 300, 64 runs 182 and 311; 512 runs, where nothing waits, 169 and 306. fp32 moves 5.7 TB/s
+// either way. What bounds it is issue: 890 instructions a warp and tile forward (26 a token to scan, 7 to store, 150
+// to look back) at 2.3 an SM and clock, of which 59 us would remain if they were free; then, for few runs, the waits
+// for maps of tiles that run at the same time.
 #include <cuda.h>
 
 #include <algorithm>
@@ -193,7 +193,7 @@ struct Info {
 //
 // Also the order in which the chunks of several runs are taken: every run's first, then every run's second, and so
 // on, so that a chunk's predecessors are as long ago as can be and few of them have to be waited for (each run in
-// turn, as the rows lie: 234 us against 184 for 64 runs of 65 536 tokens in all by 2 048 channels, and 212 against
+// turn, as the rows lie: 234 us against 182 for 64 runs of 65 536 tokens in all by 2 048 channels, and 212 against
 // 177 for eight).
 template <int kMost>
 struct Runs {
@@ -542,7 +542,6 @@ template <typename T, bool kVec>
 struct FwdShared {
   Info info[kInfos];
   float A[kWarps][kTileCh<T>], B[kWarps][kTileCh<T>];      // the warps' maps, then of all the warps before each
-  float enter[kTileCh<T>];                                 // the state that enters the tile
   Before<T> before;
   alignas(8) uint64_t full[kFwdStages<kVec>][kWarps];
   uint32_t abort;
@@ -680,14 +679,11 @@ rec_fwd_kernel(const __grid_constant__ RecTensors a, const __grid_constant__ Run
     if (threadIdx.x == 0) tile_info<false>(s.info[(i + kFwdStages<kVec>) % kInfos], t, next, items, groups);
     __syncthreads();
     float in[C];
+    fold_before(s.before, before, in, lane);
     if (warp == kWarps - 1) {
-      fold_before(s.before, before, in, lane);
       float end[C];
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        s.enter[lane * C + c] = in[c];
-        end[c] = fmaf(A[c], in[c], B[c]);
-      }
+      for (int c = 0; c < C; ++c) end[c] = fmaf(A[c], in[c], B[c]);
       if (f.last) {
 #pragma unroll
         for (int c = 0; c < C; ++c)
@@ -696,11 +692,10 @@ rec_fwd_kernel(const __grid_constant__ RecTensors a, const __grid_constant__ Run
         publish_state<T>(ch, f, first, groups, end, lane);
       }
     }
-    __syncthreads();
     // the state that enters this warp
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      in[c] = fmaf(s.A[warp][lane * C + c], s.enter[lane * C + c], s.B[warp][lane * C + c]);
+      in[c] = fmaf(s.A[warp][lane * C + c], in[c], s.B[warp][lane * C + c]);
       if (a.ckpt && c < left && nt > 0) a.ckpt[((int64_t)f.chunk * kWarps + warp) * a.dim + ch0 + c] = in[c];
     }
     T* ty = static_cast<T*>(a.y) + (f.row + warp * kTok) * a.ld_y + ch0;
