@@ -68,8 +68,8 @@ constexpr int kChunkR = MAMBA2_RECURRENCE_CHUNK;
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTok = kChunkR / kWarps;         // tokens of a warp
-constexpr int kGroup = 2 * kWarps;             // chunks between two published states
-constexpr int kBack = 2 * kGroup / kWarps;     // maps that a warp looks back at, at most
+constexpr int kMostShift = 4, kLeastShift = 2; // log2 of the chunks between two published states
+constexpr int kBack = (2 << kMostShift) / kWarps;  // maps that a warp looks back at, at most
 constexpr int kInfos = 4;
 constexpr uint32_t kPollLimit = 1u << 21;      // polls before giving up (about a second)
 
@@ -359,7 +359,7 @@ __device__ __forceinline__ void store_row(T* p, const float (&v)[kCh<T>], int le
 }
 
 // ---- workspace: a header, then a record of one (A, B) per channel for each (chunk, channel group), then a
-// record of one state per channel for every kGroup-th chunk of a run (and group).
+// record of one state per channel for every (1 << shift)-th chunk of a run (and group).
 // All of it is set to 0xff bytes first. A record's words are their own flags: every word that a tile
 // publishes is the result of an fp32 operation, which no NaN makes 0xffffffff, so a reader polls the
 // record until that pattern is gone from it, and needs no fence and no second round trip.
@@ -367,17 +367,20 @@ struct Chain {
   uint32_t* head;  // tickets taken, less one; abort when it is no longer 0xffffffff
   float* maps;     // [chunks, groups, tile channels, 2]
   float* states;   // [state_rows, groups, tile channels]
+  int shift;
 };
 constexpr size_t kHead = 256;
 constexpr uint32_t kUnset = 0xffffffffu;
 // Row of the state after chunk l of run i, whose first chunk is t: the runs' rows do not overlap.
-__host__ __device__ constexpr int64_t state_row(int64_t t, int i, int l) { return t / kGroup + i + l / kGroup; }
-size_t chain_bytes(int64_t chunks, int runs, int64_t channels) {
-  return kHead + (size_t)chunks * channels * 8 + (size_t)state_row(chunks, runs, 0) * channels * 4;
+__host__ __device__ constexpr int64_t state_row(int64_t t, int i, int l, int shift) {
+  return (t >> shift) + i + (l >> shift);
 }
-Chain chain_at(void* ws, int64_t chunks, int64_t channels) {
+size_t chain_bytes(int64_t chunks, int runs, int64_t channels, int shift) {
+  return kHead + (size_t)chunks * channels * 8 + (size_t)state_row(chunks, runs, 0, shift) * channels * 4;
+}
+Chain chain_at(void* ws, int64_t chunks, int64_t channels, int shift) {
   float* maps = reinterpret_cast<float*>(static_cast<char*>(ws) + kHead);
-  return {static_cast<uint32_t*>(ws), maps, maps + chunks * channels * 2};
+  return {static_cast<uint32_t*>(ws), maps, maps + chunks * channels * 2, shift};
 }
 
 // A lane's share of a record: (A, B) of each of its channels.
@@ -417,7 +420,7 @@ __device__ __forceinline__ float* map_at(const Chain& ch, int64_t chunk, int gro
 }
 template <typename T>
 __device__ __forceinline__ float* state_at(const Chain& ch, const Info& f, int first, int l, int groups, int lane) {
-  return ch.states + (state_row(first, f.seq, l) * groups + f.group) * kTileCh<T> + lane * kCh<T>;
+  return ch.states + (state_row(first, f.seq, l, ch.shift) * groups + f.group) * kTileCh<T> + lane * kCh<T>;
 }
 template <typename T>
 __device__ __forceinline__ void publish_map(const Chain& ch, const Info& f, int groups, const float (&A)[kCh<T>],
@@ -441,9 +444,9 @@ __device__ __forceinline__ void publish_state(const Chain& ch, const Info& f, in
 }
 
 // Chunks between chunk l > 0 and the published state that it starts from.
-__device__ __forceinline__ int maps_before(int l) {
-  const int g = (l - 1) / kGroup;
-  return l - 1 - (g > 0 ? g - 1 : 0) * kGroup;
+__device__ __forceinline__ int maps_before(int l, int shift) {
+  const int g = (l - 1) >> shift;
+  return l - 1 - ((g > 0 ? g - 1 : 0) << shift);
 }
 
 // Tells a waiting warp to give up: when another one has, or after kPollLimit polls.
@@ -592,7 +595,7 @@ rec_fwd_kernel(const __grid_constant__ RecTensors a, const __grid_constant__ Run
     int next = 0;
     if (threadIdx.x == 0) next = take<kFwdStages<kVec>>(ch, i + kFwdStages<kVec>, items);
     const int first = t.tile[f.seq];
-    const int before = f.l > 0 ? maps_before(f.l) : 0;
+    const int before = f.l > 0 ? maps_before(f.l, ch.shift) : 0;
     float h0[C];  // what the run starts from: asked for early, the run's other tiles wait for it
     if (warp == kWarps - 1 && f.l == 0)
 #pragma unroll
@@ -688,7 +691,7 @@ rec_fwd_kernel(const __grid_constant__ RecTensors a, const __grid_constant__ Run
 #pragma unroll
         for (int c = 0; c < C; ++c)
           if (c < left) a.state[(int64_t)seq_slot(t, f.seq) * a.dim + ch0 + c] = end[c];
-      } else if (f.l % kGroup == 0 && f.l > 0) {
+      } else if (f.l > 0 && (f.l & ((1 << ch.shift) - 1)) == 0) {
         publish_state<T>(ch, f, first, groups, end, lane);
       }
     }
@@ -798,7 +801,7 @@ rec_bwd_kernel(const __grid_constant__ RecBwdTensors a, const __grid_constant__ 
     int next = 0;
     if (threadIdx.x == 0) next = take<kBwdStages>(ch, i + kBwdStages, items);
     const int first = t.tile[f.seq];
-    const int before = f.l > 0 ? maps_before(f.l) : 0;
+    const int before = f.l > 0 ? maps_before(f.l, ch.shift) : 0;
     float h0[C];
     if (warp == 0 && f.l == 0)
 #pragma unroll
@@ -896,7 +899,7 @@ rec_bwd_kernel(const __grid_constant__ RecBwdTensors a, const __grid_constant__ 
 #pragma unroll
         for (int c = 0; c < C; ++c)
           if (a.dstate && c < left) a.dstate[(int64_t)f.seq * a.dim + ch0 + c] = end[c];
-      } else if (f.l % kGroup == 0 && f.l > 0) {
+      } else if (f.l > 0 && (f.l & ((1 << ch.shift) - 1)) == 0) {
         publish_state<T>(ch, f, first, groups, end, lane);
       }
     }
@@ -1115,6 +1118,15 @@ bool make_map(CUtensorMap* tm, const void* base, int64_t rows, int64_t dim, int6
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// log2 of the chunks between two published states: as few as keep a state's readers a round of the GPU behind it (the
+// fewer, the fewer maps to read and fold).
+int state_shift(int64_t chunks, int64_t longest, int64_t groups) {
+  const int64_t at_once = (int64_t)kCtas * device_sm_count(), runs = chunks / longest;  // that are in turn, about
+  int shift = kLeastShift;
+  while (shift < kMostShift && (runs * groups << shift) < at_once) ++shift;
+  return shift;
+}
+
 // The plan that both passes share: tiles, and the chain (cleared on the stream) when a run has several.
 struct Tiles {
   int groups, items;
@@ -1135,12 +1147,13 @@ Tiles plan(const SeqTable& t, mamba2_dtype act, int32_t dim, void* ws, cudaStrea
     return p;
   }
   p.items = (int)items;
-  bool chained = false;
-  for (int i = 0; i < t.n; ++i) chained |= t.tile[i + 1] - t.tile[i] > 1;
-  if (chained) {
+  int longest = 0;
+  for (int i = 0; i < t.n; ++i) longest = std::max(longest, t.tile[i + 1] - t.tile[i]);
+  if (longest > 1) {
     p.interleave = t.n > 1;
-    p.chain = chain_at(ws, chunks, (int64_t)p.groups * width);
-    p.status = cudaMemsetAsync(ws, 0xff, chain_bytes(chunks, t.n, (int64_t)p.groups * width), st);
+    const int shift = state_shift(chunks, longest, p.groups);
+    p.chain = chain_at(ws, chunks, (int64_t)p.groups * width, shift);
+    p.status = cudaMemsetAsync(ws, 0xff, chain_bytes(chunks, t.n, (int64_t)p.groups * width, shift), st);
   }
   return p;
 }
@@ -1194,7 +1207,7 @@ cudaError_t run_bwd(const RecBwdArgs& a, const Tiles& p, float* part, cudaStream
 size_t recurrence_workspace(int64_t chunks, bool chained, int32_t runs, int32_t dim, bool backward) {
   const size_t part = backward ? ((size_t)chunks * dim * 4 + 255) / 256 * 256 : 0;
   // (either type's groups together are at most 63 channels wider than dim)
-  return part + (chained ? (chain_bytes(chunks, runs, (int64_t)dim + 63) + 255) / 256 * 256 : 0);
+  return part + (chained ? (chain_bytes(chunks, runs, (int64_t)dim + 63, kLeastShift) + 255) / 256 * 256 : 0);
 }
 
 unsigned int read_recurrence_timeouts() {
