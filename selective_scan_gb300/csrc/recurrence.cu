@@ -41,8 +41,8 @@
 // summed per tile and then over the tiles, in order.
 //
 // Measured (GB300, 65 536 tokens x 2 048 channels, bf16, with lower bounds and, forward, checkpoints): one run
-// 210 us forward (199 without checkpoints: 4.05 TB/s, 60 % of the measured copy rate) and 325 backward (4.2 TB/s);
-// eight runs 177 and 300, 64 runs 182 and 311; 512 runs, where nothing waits, 169 and 306. fp32 moves 5.7 TB/s
+// 196 us forward (185 without checkpoints: 4.4 TB/s, 64 % of the measured copy rate) and 307 backward (4.4 TB/s); eight runs 164 and 284, 64 runs 166 and 286;
+// 512 runs, where nothing waits, 156 and 285. fp32 moves 5.8 TB/s
 // either way. What bounds it is issue: 890 instructions a warp and tile forward (26 a token to scan, 7 to store, 150
 // to look back) at 2.3 an SM and clock, of which 59 us would remain if they were free; then, for few runs, the waits
 // for maps of tiles that run at the same time.
@@ -191,38 +191,46 @@ struct Info {
 // The runs of a call. They are launch parameters, which take time to hand over by the byte, so there is a short form:
 // 300 tokens by 1 536 channels 15.3 us forwards and 21.4 backwards with it, 16.3 and 24.5 with the long one.
 //
-// Also the order in which the chunks of several runs are taken: every run's first, then every run's second, and so
-// on, so that a chunk's predecessors are as long ago as can be and few of them have to be waited for (each run in
-// turn, as the rows lie: 234 us against 182 for 64 runs of 65 536 tokens in all by 2 048 channels, and 212 against
-// 177 for eight).
+// Also the order in which the chunks of several runs are taken: runs in turns, each one's first chunk, then each
+// one's second, and so on, so that a chunk's predecessors are some time ago and few of them have to be waited for
+// (each run in turn, as the rows lie: 234 us against 166 for 64 runs of 65 536 tokens in all by 2 048 channels, and
+// 212 against 164 for eight). Not more runs at a time than that takes, the longest first: what was published longer
+// ago has left L2.
 template <int kMost>
 struct Runs {
   int32_t n;
   int32_t sorted;             // runs that have chunks; 0: chunks in order of rows
+  int32_t turn;               // so many at a time
   int32_t cu[kMost + 1];      // first rows
   int32_t tile[kMost + 1];    // first chunks
-  int32_t before[kMost + 1];  // [c]: chunks that are taken before the c longest runs are alone
+  int32_t before[kMost];      // [k turn]: chunks before the k-th of those sets; [k turn + c]: of those in it,
+                              // how many are taken before its c longest runs are alone
   uint32_t slot_fresh[kMost];
   uint16_t run[kMost];        // the longest first
 };
 constexpr int kFewRuns = 64;
 template <int kMost>
-void fill_runs(Runs<kMost>& o, const SeqTable& t, bool interleave) {
+void fill_runs(Runs<kMost>& o, const SeqTable& t, int turn) {
   o.n = t.n;
   o.sorted = 0;
+  o.turn = turn;
   std::copy(t.cu, t.cu + t.n + 1, o.cu);
   std::copy(t.tile, t.tile + t.n + 1, o.tile);
   std::copy(t.slot_fresh, t.slot_fresh + t.n, o.slot_fresh);
-  if (!interleave) return;
+  if (turn == 0) return;
   auto chunks = [&](int r) { return t.tile[r + 1] - t.tile[r]; };
   for (int i = 0; i < t.n; ++i)
     if (chunks(i) > 0) o.run[o.sorted++] = (uint16_t)i;
   std::stable_sort(o.run, o.run + o.sorted, [&](int a, int b) { return chunks(a) > chunks(b); });
-  int shorter = 0;  // chunks of the runs after the first c
-  o.before[o.sorted] = 0;
-  for (int c = o.sorted - 1; c >= 1; --c) {
-    shorter += chunks(o.run[c]);
-    o.before[c] = shorter + c * chunks(o.run[c]);
+  int start = 0;
+  for (int k = 0; k < o.sorted; k += turn) {
+    int shorter = 0;  // chunks of the set's runs after the first c
+    for (int c = std::min(turn, o.sorted - k) - 1; c >= 1; --c) {
+      shorter += chunks(o.run[k + c]);
+      o.before[k + c] = shorter + c * chunks(o.run[k + c]);
+    }
+    o.before[k] = start;
+    start += shorter + chunks(o.run[k]);
   }
 }
 
@@ -237,13 +245,21 @@ __device__ __forceinline__ void tile_info(Info& f, const Runs<kMost>& t, int ite
   f.group = item - pos * groups;
   int s, of;
   if (t.sorted > 0) {
-    int c = 1, hi = t.sorted;  // the fewest runs left that pos allows
+    int set = 0, last = (t.sorted - 1) / t.turn;
+    while (set < last) {
+      const int mid = (set + last + 1) >> 1;
+      if (t.before[mid * t.turn] <= pos) set = mid; else last = mid - 1;
+    }
+    set *= t.turn;
+    const int in_set = pos - t.before[set], most = min(t.turn, t.sorted - set);
+    int c = 1, hi = most;  // the fewest runs left that in_set allows
     while (c < hi) {
       const int mid = (c + hi) >> 1;
-      if (t.before[mid] <= pos) hi = mid; else c = mid + 1;
+      if (t.before[set + mid] <= in_set) hi = mid; else c = mid + 1;
     }
-    const int in = pos - t.before[c], ended = c < t.sorted ? t.tile[t.run[c] + 1] - t.tile[t.run[c]] : 0;
-    s = t.run[in % c];
+    const int next = c < most ? t.run[set + c] : 0;
+    const int in = in_set - (c < most ? t.before[set + c] : 0), ended = c < most ? t.tile[next + 1] - t.tile[next] : 0;
+    s = t.run[set + in % c];
     of = t.tile[s + 1] - t.tile[s];
     f.l = ended + in / c;
     f.chunk = t.tile[s] + (kReverse ? of - 1 - f.l : f.l);
@@ -1118,12 +1134,15 @@ bool make_map(CUtensorMap* tm, const void* base, int64_t rows, int64_t dim, int6
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// log2 of the chunks between two published states: as few as keep a state's readers a round of the GPU behind it (the
-// fewer, the fewer maps to read and fold).
-int state_shift(int64_t chunks, int64_t longest, int64_t groups) {
-  const int64_t at_once = (int64_t)kCtas * device_sm_count(), runs = chunks / longest;  // that are in turn, about
+int64_t tiles_at_once() { return (int64_t)kCtas * device_sm_count(); }
+// Runs whose chunks are taken in turns: as many as fill the GPU (64 runs of 65 536 x 2 048: 166 us, 169 with twice and
+// 177 with four times as many).
+int runs_in_turn(int64_t groups) { return (int)((tiles_at_once() + groups - 1) / groups); }
+// log2 of the chunks between two published states: as few as keep a state's readers a wave of tiles behind it (the
+// fewer, the fewer maps to read and fold). runs: those in turn, on average.
+int state_shift(int64_t runs, int64_t groups) {
   int shift = kLeastShift;
-  while (shift < kMostShift && (runs * groups << shift) < at_once) ++shift;
+  while (shift < kMostShift && (runs * groups << shift) < tiles_at_once()) ++shift;
   return shift;
 }
 
@@ -1131,13 +1150,13 @@ int state_shift(int64_t chunks, int64_t longest, int64_t groups) {
 struct Tiles {
   int groups, items;
   Chain chain;
-  bool interleave;  // several runs, chained
+  int turn;  // runs that take turns; 0: none do
   cudaError_t status;
 };
 Tiles plan(const SeqTable& t, mamba2_dtype act, int32_t dim, void* ws, cudaStream_t st) {
   Tiles p;
   p.chain = {};
-  p.interleave = false;
+  p.turn = 0;
   p.status = cudaSuccess;
   const int width = act == MAMBA2_BF16 ? kTileCh<__nv_bfloat16> : kTileCh<float>;
   p.groups = (dim + width - 1) / width;
@@ -1150,8 +1169,8 @@ Tiles plan(const SeqTable& t, mamba2_dtype act, int32_t dim, void* ws, cudaStrea
   int longest = 0;
   for (int i = 0; i < t.n; ++i) longest = std::max(longest, t.tile[i + 1] - t.tile[i]);
   if (longest > 1) {
-    p.interleave = t.n > 1;
-    const int shift = state_shift(chunks, longest, p.groups);
+    if (t.n > 1) p.turn = runs_in_turn(p.groups);
+    const int shift = state_shift(p.turn == 0 ? 1 : std::min<int64_t>(p.turn, chunks / longest), p.groups);
     p.chain = chain_at(ws, chunks, (int64_t)p.groups * width, shift);
     p.status = cudaMemsetAsync(ws, 0xff, chain_bytes(chunks, t.n, (int64_t)p.groups * width, shift), st);
   }
@@ -1169,7 +1188,7 @@ cudaError_t run_fwd(const RecArgs& a, const Tiles& p, cudaStream_t st) {
     return cudaErrorInvalidValue;
   auto run = [&](auto kernel, auto most) {
     Runs<decltype(most)::value> runs;
-    fill_runs(runs, a.tab, p.interleave);
+    fill_runs(runs, a.tab, p.turn);
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     kernel<<<ctas(p.items, kCtas), kThreads, smem, st>>>(a, runs, mx, mg, p.chain, p.items, p.groups);
@@ -1192,7 +1211,7 @@ cudaError_t run_bwd(const RecBwdArgs& a, const Tiles& p, float* part, cudaStream
     return cudaErrorInvalidValue;
   auto run = [&](auto kernel, auto most) {
     Runs<decltype(most)::value> runs;
-    fill_runs(runs, a.tab, p.interleave);
+    fill_runs(runs, a.tab, p.turn);
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     kernel<<<ctas(p.items, kCtas), kThreads, smem, st>>>(a, runs, mx, mg, md, p.chain, part, p.items, p.groups);

@@ -101,14 +101,13 @@ def test_recurrence_forward_and_backward(dtype, lengths, dim, off, extra):
             R.check(got, want[name], name)
 
 
-@pytest.mark.parametrize("runs", [2, 64, 65, 300])
-def test_recurrence_many_runs_of_different_lengths(runs):
+@pytest.mark.parametrize("runs,dim", [(2, 72), (64, 72), (65, 72), (300, 72), (40, 1500)])
+def test_recurrence_many_runs_of_different_lengths(runs, dim):
     """Runs whose chunks are taken in turns: longer and shorter ones, some empty, in no order."""
     dev = device()
     g = torch.Generator().manual_seed(runs)
-    lengths = [int(v) for v in (torch.rand(runs, generator=g) ** 3 * (3 if runs > 100 else 9) * 128)]
+    lengths = [int(v) for v in (torch.rand(runs, generator=g) ** 3 * (3 if runs > 100 or dim > 100 else 9) * 128)]
     lengths[0], lengths[1] = 700, 0
-    dim = 72
     x, gate, lo, pool, slots, fresh = rec_inputs(runs, lengths, dim, BF16, True)
     cu, rows = cu_of(lengths), sum(lengths)
     ref = R.recurrence(x, gate, lo, pool, cu, slots, fresh)
