@@ -517,6 +517,7 @@ __device__ __forceinline__ void look_back(const Chain& ch, const Info& f, int fi
     for (int j = 0; j < kBack; ++j)
       if (j < n) load_record<C>(p + j * step, r[j]);
   }
+  if (n == 0) return;  // (nothing reads its share)
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     float A = 1.0f, B = 0.0f;
