@@ -130,7 +130,7 @@ __device__ __forceinline__ void store8(__nv_fp8_storage_t* p, const float (&v)[W
   }
 }
 
-// The fp32 weights of a unit's columns. Where they start between two 16-byte words, the same for the whole row, the
+// The fp32 weights of a unit's columns; anything for columns outside the row. Where they start between two 16-byte words, the same for the whole row, the
 // three words that hold them are read and shifted into place.
 template <bool kShift>
 __device__ __forceinline__ void load_weight(const float* weight, const At<kShift>& at, int dim, float (&w)[W]) {
@@ -242,9 +242,13 @@ add_norm_kernel(const AddNormArgs a, const int nt) {
       float w[W];
       load_weight(a.weight, at, a.dim, w);
 #pragma unroll
-      for (int j = 0; j < W; ++j) {
-        s[u][j] = s[u][j] * inv * w[j];
-        if (F8) top[0] = max_nan(top[0], fabsf(s[u][j]));
+      for (int j = 0; j < W; ++j) s[u][j] = s[u][j] * inv * w[j];
+      if (F8) {
+        if (!at.whole(a.dim))  // (what lies behind the last weight may be anything)
+#pragma unroll
+          for (int j = 0; j < W; ++j) s[u][j] = at.has(j, a.dim) ? s[u][j] : 0.0f;
+#pragma unroll
+        for (int j = 0; j < W; ++j) top[0] = max_nan(top[0], fabsf(s[u][j]));
       }
       if (!F8) {
         Unit<T, kShift> o;

@@ -462,6 +462,37 @@ def test_add_rmsnorm_rows_that_start_inside_a_unit(dtype, stype, rows, dim):
     R.check(dw, wref, "dweight")
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows,dim", [(1, 1), (3, 7), (5, 77), (300, 1085), (2, 20001)])
+def test_add_rmsnorm_what_lies_behind_the_tensors_is_not_used(dtype, rows, dim):
+    """x, the residual, dy and the weights end inside 16 bytes whose rest is NaN."""
+    dev = device()
+
+    def followed(t):
+        wide = torch.full((t.numel() + 64,), NAN, dtype=t.dtype, device=dev)
+        wide[:t.numel()] = t.to(dev).flatten()
+        return wide[:t.numel()].view(t.shape)
+
+    x, r, w = randn(1, rows, dim).to(dtype), randn(2, rows, dim).to(dtype), randn(3, dim, std=0.3, mean=1.0)
+    (s64, serr), yref, rel = R.add_rmsnorm(x, r, w, 1e-5)
+    gx, gr, gw = followed(x), followed(r), followed(w)
+    out, total = torch.empty_like(gx), torch.empty_like(gx)
+    ss.add_rmsnorm(out, gx, gw, 1e-5, residual=gr, sum=total)
+    R.check(out, yref, "out")
+    R.check(total, (s64, serr), "sum")
+    q, scale = torch.empty((rows, dim), dtype=E4M3, device=dev), torch.full((rows,), NAN, device=dev)
+    ss.add_rmsnorm(q, gx, gw, 1e-5, residual=gr, scale=scale)
+    sref = yref[0].abs().amax(1) / 448
+    R.check(scale, (sref, 2 * rel * sref), "scale")
+    dy = randn(4, rows, dim).to(dtype)
+    src = total.cpu()
+    dref, wref = R.add_rmsnorm_backward(src, w, 1e-5, dy, None)
+    dx, dw = torch.empty_like(gx), torch.empty_like(gw)
+    ss.add_rmsnorm_backward(dx, None, dw, followed(dy), None, followed(src), gw, 1e-5)
+    R.check(dx, dref, "dx")
+    R.check(dw, wref, "dweight")
+
+
 def test_add_rmsnorm_rows_of_zeros_and_non_finite():
     dev = device()
     dim = 300
