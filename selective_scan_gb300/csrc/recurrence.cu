@@ -9,8 +9,8 @@
 // 16 tokens each, a lane 4 bytes of channels. Per tile:
 //   1. each warp scans its tokens from zero, keeping h_t in registers and the product of
 //      the f's in shared memory, and posts its map; the eight maps compose to the tile's
-//   2. the tile publishes its map in the workspace, and each warp fetches four of the (at
-//      most 31) maps that precede the tile; folded, they give the state that enters it
+//   2. the tile publishes its map in the workspace, and each warp fetches up to four of the
+//      maps that precede the tile; folded, they give the state that enters it
 //   3. each warp adds (product of f's) x (its own entering state) to its tokens and stores
 // Inputs stream through a ring in shared memory by TMA, or row by row in bulk copies where they
 // are not 16-byte aligned: a warp fetches only the rows that it will read, so a stage is handed
@@ -21,11 +21,12 @@
 //
 // What precedes chunk l of a run, the same for any timing (so results repeat bit for bit):
 // every chunk publishes its map, and every 16th (0, 16, 32, ...) the state after it too (the
-// first the state alone, which it has as early as its map). Chunk l takes the state that lies
-// one such step further back than the nearest, and folds the maps of the up to 31 chunks
-// between in order. Maps are published without waiting for anything, and a state is used 16
-// chunks later at the earliest: later than the tiles that the GPU holds at one time for wide
-// matrices, so a tile waits for maps alone. (With the nearest state it waited for the maps and
+// first the state alone, which it has as early as its map); every 8th or 4th where many runs or
+// channels are under way at a time. Chunk l takes the state that lies one such step further
+// back than the nearest, and folds the maps of the up to 31 (15, 7) chunks between in order.
+// Maps are published without waiting for anything, and a state is used 16 (8, 4) chunks later
+// at the earliest: later than the tiles that the GPU holds at one time for wide matrices, so a
+// tile waits for maps alone. (With the nearest state it waited for the maps and
 // then for the state made from them: 232 us against 213 for one run of 65 536 tokens by 2 048
 // channels.) Chunk 0 alone reads the pool, so the run's last chunk may overwrite the slot.
 //
@@ -40,12 +41,12 @@
 // y, and unrounded), and makes dx and dgate in one more sweep over its tokens. dlower is
 // summed per tile and then over the tiles, in order.
 //
-// Measured (GB300, 65 536 tokens x 2 048 channels, bf16, with lower bounds and, forward, checkpoints): one run
-// 196 us forward (185 without checkpoints: 4.4 TB/s, 64 % of the measured copy rate) and 307 backward (4.4 TB/s); eight runs 164 and 284, 64 runs 166 and 286;
-// 512 runs, where nothing waits, 156 and 285. fp32 moves 5.8 TB/s
-// either way. What bounds it is issue: 890 instructions a warp and tile forward (26 a token to scan, 7 to store, 150
-// to look back) at 2.3 an SM and clock, of which 59 us would remain if they were free; then, for few runs, the waits
-// for maps of tiles that run at the same time.
+// Measured (GB300, 65 536 tokens x 2 048 channels, bf16, with lower bounds and, forward, checkpoints): one run 197 us
+// forward (186 without checkpoints: 4.3 TB/s, 64 % of the measured copy rate) and 305 backward (4.4 TB/s); eight runs
+// 164 and 281, 64 runs 162 and 281; 512 runs, where nothing waits, 153 and 281. fp32 moves 5.8 TB/s either way. What
+// bounds it is issue: 950 instructions a warp and tile of one run forward (24 a token to scan, 7 to store) at 2.2 an
+// SM and clock, of which 59 us would remain if they were free; then, for few runs, the waits for maps of tiles that
+// run at the same time.
 #include <cuda.h>
 
 #include <algorithm>
@@ -193,8 +194,8 @@ struct Info {
 //
 // Also the order in which the chunks of several runs are taken: runs in turns, each one's first chunk, then each
 // one's second, and so on, so that a chunk's predecessors are some time ago and few of them have to be waited for
-// (each run in turn, as the rows lie: 234 us against 166 for 64 runs of 65 536 tokens in all by 2 048 channels, and
-// 212 against 164 for eight). Not more runs at a time than that takes, the longest first: what was published longer
+// (each run by itself, as the rows lie: 234 us against 184 for 64 runs of 65 536 tokens in all by 2 048 channels,
+// 212 against 177 for eight). Not more runs at a time than that takes, the longest first: what was published longer
 // ago has left L2.
 template <int kMost>
 struct Runs {
