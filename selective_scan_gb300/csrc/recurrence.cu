@@ -343,34 +343,36 @@ struct Reader {
         step |= (e * ld & 15u) << (8 * i);
       }
   }
-  // the (first) word that holds the lane's channels of row j
-  __device__ __forceinline__ unsigned char* slot(int i, int j) const {
-    return base + i * kChunkR * kPitch<kVec> + j * kPitch<kVec> + (kVec ? 0u : (at + j * step) >> (8 * i) & 12u);
-  }
+  // the lane's word of row j, or at the row's offset the one or two that hold its channels, shifted into place
+  // (by their address's low bits: bit 0 is 0, and a shift counts modulo 32)
   __device__ __forceinline__ uint32_t word(int i, int j) const {
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(slot(i, j));
+    const uint32_t off = at_row(j);
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(row(i, j) + (kVec ? 0u : off >> (8 * i) & 12u));
     if constexpr (kVec || sizeof(T) == 4) return w[0];
-    else return __funnelshift_r(w[0], w[1], 8u * ((at + j * step) >> (8 * i) & 2u));  // in the first or across two
+    else return __funnelshift_r(w[0], w[1], i == 0 ? off << 3 : off >> (8 * i - 3));
   }
+  // where row j starts: four bytes there are the lane's once the warp has read the row
+  __device__ __forceinline__ unsigned char* row(int i, int j) const {
+    return base + i * kChunkR * kPitch<kVec> + j * kPitch<kVec>;
+  }
+
+ private:
+  __device__ __forceinline__ uint32_t at_row(int j) const { return (at + j * step) & 0x0f0f0f0fu; }
 };
 
-// Does this row start between two words?
-template <typename T>
-__device__ __forceinline__ int odd_start(const T* row) {
-  return sizeof(T) == 2 ? (int)((reinterpret_cast<uintptr_t>(row) >> 1) & 1) : 0;
-}
-// kIn: all of the lane's channels are inside the matrix and p is on a word; else `left` are from p on.
-template <typename T, bool kIn>
+// A lane's channels to the output. kInside: all of them are inside the matrix, else `left` are from p on; kWords: p is
+// on a word.
+template <typename T, bool kInside, bool kWords>
 __device__ __forceinline__ void store_row(T* p, const float (&v)[kCh<T>], int left) {
   if constexpr (sizeof(T) == 4) {
-    if (kIn || left > 0) *p = v[0];
+    if (kInside || left > 0) *p = v[0];
   } else {
     const __nv_bfloat162 h = __floats2bfloat162_rn(v[0], v[1]);
-    if (kIn || (left >= 2 && !odd_start(p))) {
+    if ((kInside || left > 1) && (kWords || (reinterpret_cast<uintptr_t>(p) & 2) == 0)) {
       *reinterpret_cast<__nv_bfloat162*>(p) = h;
     } else {
-      if (left > 0) p[0] = h.x;
-      if (left > 1) p[1] = h.y;
+      if (kInside || left > 0) p[0] = h.x;
+      if (kInside || left > 1) p[1] = h.y;
     }
   }
 }
@@ -652,9 +654,9 @@ rec_fwd_kernel(const __grid_constant__ RecTensors a, const __grid_constant__ Run
         hs[j] = h2;
         float v[C];
         P::split(p2, v);
-        if constexpr (!kVec) __syncwarp();  // (the lane before may share the word)
-        *reinterpret_cast<float*>(rd.slot(0, j)) = v[0];
-        if constexpr (C == 2) *reinterpret_cast<float*>(rd.slot(1, j)) = v[1];
+        if constexpr (!kVec) __syncwarp();  // (the row is read)
+        *reinterpret_cast<float*>(rd.row(0, j)) = v[0];
+        if constexpr (C == 2) *reinterpret_cast<float*>(rd.row(1, j)) = v[1];
       }
     };
     if (nt == kTok) scan(std::true_type{});
@@ -727,10 +729,10 @@ rec_fwd_kernel(const __grid_constant__ RecTensors a, const __grid_constant__ Run
       for (int j = 0; j < kTok; ++j, ty += a.ld_y)
         if (decltype(whole)::value || j < nt) {
           float y[C], v[C];
-          v[0] = *reinterpret_cast<const float*>(rd.slot(0, j));
-          if constexpr (C == 2) v[1] = *reinterpret_cast<const float*>(rd.slot(1, j));
+          v[0] = *reinterpret_cast<const float*>(rd.row(0, j));
+          if constexpr (C == 2) v[1] = *reinterpret_cast<const float*>(rd.row(1, j));
           P::split(P::fma(P::make(v), in2, hs[j]), y);
-          store_row<T, kVec && decltype(whole)::value>(ty, y, left);
+          store_row<T, decltype(whole)::value, kVec>(ty, y, left);
         }
     };
     if (nt == kTok && (f.group + 1) * kTileCh<T> <= a.dim) emit(std::true_type{});
@@ -944,8 +946,8 @@ rec_bwd_kernel(const __grid_constant__ RecBwdTensors a, const __grid_constant__ 
           P::split(P::mul(P::mul(dd, un2), P::add(up, P::all(-kLeast))), vg);
           dlo2 = P::add(dlo2, dd);
           in2 = P::mul(ft, G);
-          store_row<T, kVec && decltype(whole)::value>(ox, vx, left);
-          store_row<T, kVec && decltype(whole)::value>(og, vg, left);
+          store_row<T, decltype(whole)::value, kVec>(ox, vx, left);
+          store_row<T, decltype(whole)::value, kVec>(og, vg, left);
         }
     };
     if (nt == kTok && (f.group + 1) * kTileCh<T> <= a.dim) emit(std::true_type{});
