@@ -12,12 +12,12 @@
 //   2. the tile publishes its map in the workspace, and each warp fetches up to four of the
 //      maps that precede the tile; folded, they give the state that enters it
 //   3. each warp adds (product of f's) x (its own entering state) to its tokens and stores
-// Inputs stream through a ring in shared memory by TMA, or row by row in bulk copies where they
-// are not 16-byte aligned: a warp fetches only the rows that it will read, so a stage is handed
-// over without the other warps, and the next tile's copies are in flight while a tile waits for
-// its predecessors (with one stage, while the others finish). Unaligned rows are realigned as
-// they are read: for eight runs of 32 768 tokens in all by 2 047 channels of bf16 154 us forwards
-// and 267 backwards (by 2 048: 97 and 161); copied word by word it was 31 and 44 us more.
+// Inputs stream through a ring in shared memory by TMA, or by cp.async where rows are not 16-byte
+// aligned: a warp fetches only the rows that it will read, so a stage is handed over without the
+// other warps, and the next tile's copies are in flight while a tile waits for its predecessors
+// (with one stage, while the others finish). Unaligned rows are shifted into place as they are
+// read, at a third more instructions: eight runs of 32 768 tokens in all by 2 047 channels of
+// bf16 take 132 us forwards and 244 backwards (by 2 048: 91 and 154).
 //
 // What precedes chunk l of a run, the same for any timing (so results repeat bit for bit):
 // every chunk publishes its map, and every 16th (0, 16, 32, ...) the state after it too (the
@@ -284,10 +284,11 @@ struct Stream {
   int64_t ld;
   const CUtensorMap* map;  // boxes of 128 bytes x kTok rows
 };
-// This warp's rows of tile f of k matrices, kMat bytes apart, into the stage at st; bar tells when they are there.
-// Where rows are 16-byte aligned, by TMA (rows past the run's end are other runs', or zeros: nothing uses them); else a
-// lane copies a row, from the 16-byte boundary before it to the one after it: what that adds shares its 16 bytes with
-// the row, so it can be read, and nothing uses it.
+// This warp's rows of tile f of k matrices, kMat bytes apart, into the stage at st (wait_tile waits for them, with bar).
+// Where rows are 16-byte aligned, by TMA: rows past the run's end are other runs', or zeros, and nothing uses them. Else
+// 16 bytes a lane, each row from the 16-byte boundary before it to the one after it: what that adds shares its 16 bytes
+// with the row, so it can be read, and nothing uses it either. (8 runs, 32 768 x 2 046 bf16: 129 us; a bulk copy a row
+// 137 from all lanes and 153 from one; 4 bytes a lane, which can place a row at its word, was slower than those.)
 template <typename T, bool kVec, int k>
 __device__ __forceinline__ void load_tile(const Info& f, const Stream<T> (&m)[k], uint32_t st, uint32_t bar, int dim,
                                           int warp, int lane) {
@@ -302,26 +303,29 @@ __device__ __forceinline__ void load_tile(const Info& f, const Stream<T> (&m)[k]
       for (int i = 0; i < k; ++i) tma_load_2d(st + i * kMat + warp * kTok * 128, m[i].map, ch0, f.row + warp * kTok, bar);
     }
   } else {
-    fence_async_smem();
-    const int valid = min(kTileCh<T>, dim - ch0) * (int)sizeof(T);
-    uint64_t from[k];
-    uint32_t bytes[k], total = 0;
+    constexpr int kUnits = kPitch<false> / 16;  // of a row: where unit u of row r goes is 16 (kUnits r + u) bytes on
+    const uint32_t valid = (uint32_t)min(kTileCh<T>, dim - ch0) * (uint32_t)sizeof(T);
 #pragma unroll
-    for (int i = 0; i < k; ++i) {
-      const uint64_t p = reinterpret_cast<uint64_t>(m[i].p + (int64_t)(f.row + warp * kTok + lane) * m[i].ld + ch0);
-      from[i] = p & ~(uint64_t)15;
-      bytes[i] = lane < nt ? ((uint32_t)(p & 15) + (uint32_t)valid + 15u) & ~15u : 0u;
-      total += bytes[i];
+    for (int c = 0; c < kTok * kUnits; c += 32) {
+      const int r = (c + lane) / kUnits, u = c + lane - r * kUnits;
+#pragma unroll
+      for (int i = 0; i < k; ++i) {
+        const uint64_t p = reinterpret_cast<uint64_t>(m[i].p + (int64_t)(f.row + warp * kTok + r) * m[i].ld + ch0);
+        if (r < nt && 16u * (uint32_t)u < (uint32_t)(p & 15) + valid)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                       :: "r"(st + i * kMat + (uint32_t)(warp * kTok) * kPitch<kVec> + 16u * (uint32_t)(c + lane)),
+                          "l"((p & ~(uint64_t)15) + 16u * (uint32_t)u) : "memory");
+      }
     }
-    total = __reduce_add_sync(0xffffffffu, total);
-    if (lane == 0) mbar_expect_tx(bar, total);
-    __syncwarp();
-    if (lane < nt)
-#pragma unroll
-      for (int i = 0; i < k; ++i)
-        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                     :: "r"(st + i * kMat + (uint32_t)(warp * kTok + lane) * kPitch<kVec>), "l"(from[i]), "r"(bytes[i]),
-                        "r"(bar) : "memory");
+  }
+}
+// Waits for this warp's rows (of its next load).
+template <bool kVec>
+__device__ __forceinline__ void wait_tile(uint32_t bar, uint32_t parity, volatile uint32_t* abort) {
+  if constexpr (kVec) {
+    warp_wait(bar, parity, abort);
+  } else {
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
   }
 }
@@ -634,7 +638,7 @@ rec_fwd_kernel(const __grid_constant__ RecTensors a, const __grid_constant__ Run
     const V un2 = P::make(un), lo2 = P::fma(un2, P::all(-kLeast), P::make(lo));  // (f = up un + lo)
     const int nt = min(kTok, f.n - warp * kTok);
     if (nt > 0) {
-      warp_wait(su32(&s.full[i % kFwdStages<kVec>][warp]), phases >> (i % kFwdStages<kVec>) & 1u, &s.abort);
+      wait_tile<kVec>(su32(&s.full[i % kFwdStages<kVec>][warp]), phases >> (i % kFwdStages<kVec>) & 1u, &s.abort);
       phases ^= 1u << (i % kFwdStages<kVec>);
     }
     V hs[kTok], h2 = P::all(0.0f), p2 = P::all(1.0f);
@@ -840,7 +844,7 @@ rec_bwd_kernel(const __grid_constant__ RecBwdTensors a, const __grid_constant__ 
     const V un2 = P::make(un), lo2 = P::fma(un2, P::all(-kLeast), P::make(lo));  // (f = up un + lo)
     const int nt = min(kTok, f.n - warp * kTok);
     if (nt > 0) {
-      warp_wait(su32(&s.full[i % kBwdStages][warp]), phases >> (i % kBwdStages) & 1u, &s.abort);
+      wait_tile<kVec>(su32(&s.full[i % kBwdStages][warp]), phases >> (i % kBwdStages) & 1u, &s.abort);
       phases ^= 1u << (i % kBwdStages);
     }
     // ---- the states from the checkpoint on, and R's map (A, R)
