@@ -19,6 +19,7 @@ layer view built on them (attention mask in, HF-style cache out).
 """
 from __future__ import annotations
 
+import array
 import ctypes
 from pathlib import Path
 from typing import Optional, Sequence
@@ -236,17 +237,30 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream
 
 
+def _int32s(values):
+    """A ctypes array of these ints (of one 0 if there are none). By way of array.array where it takes them: 64 in a
+    third of the time."""
+    if not isinstance(values, (bytes, bytearray)):
+        try:
+            a = array.array("i", values)
+            return (ctypes.c_int32 * len(a)).from_buffer(a) if a else (ctypes.c_int32 * 1)()
+        except (TypeError, OverflowError):  # floats and the like, and what c_int32 wraps
+            pass
+    return (ctypes.c_int32 * max(1, len(values)))(*map(int, values))
+
+
 class Batch:
     """A RecurrentBatch marshalled once (host arrays kept alive); pass it as
     ``batch=`` to reuse it across calls instead of cu_seqlens/slots/fresh."""
 
     def __init__(self, cu_seqlens: Optional[Sequence[int]], slots: Sequence[int], fresh: Sequence[int]):
         n = len(slots)
-        self.slots = (ctypes.c_int32 * max(n, 1))(*map(int, slots))
-        self.fresh = (ctypes.c_uint8 * max(n, 1))(*map(bool, fresh))
-        self.cu = None
-        if cu_seqlens is not None:
-            self.cu = (ctypes.c_int32 * max(1, len(cu_seqlens)))(*map(int, cu_seqlens))
+        self.slots = _int32s(slots)
+        flags = bytearray(map(bool, fresh)).ljust(max(n, 1), b"\0")
+        if len(flags) > max(n, 1):
+            raise IndexError("fresh: more entries than slots")
+        self.fresh = (ctypes.c_uint8 * len(flags)).from_buffer(flags)
+        self.cu = None if cu_seqlens is None else _int32s(cu_seqlens)
         self.rb = RecurrentBatch(n, self.cu, self.slots, self.fresh)  # (arrays pass as the pointers)
 
     def ref(self):
@@ -478,7 +492,7 @@ def mamba3_siso_varlen_forward(out, final_angle, final_ssm, final_k, final_v, q,
 
 
 def _cu(cu_seqlens):
-    return cu_seqlens if isinstance(cu_seqlens, ctypes.Array) else (ctypes.c_int32 * max(1, len(cu_seqlens)))(*cu_seqlens)
+    return cu_seqlens if isinstance(cu_seqlens, ctypes.Array) else _int32s(cu_seqlens)
 
 
 def gated_recurrence_checkpoints(cu_seqlens) -> int:
