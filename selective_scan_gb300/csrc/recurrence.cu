@@ -72,6 +72,7 @@ constexpr int kTok = kChunkR / kWarps;         // tokens of a warp
 constexpr int kMostShift = 4, kLeastShift = 2; // log2 of the chunks between two published states
 constexpr int kBack = (2 << kMostShift) / kWarps;  // maps that a warp looks back at, at most
 constexpr int kInfos = 4;
+constexpr int kTaker = 32 * 5;                 // the thread that takes the next tile
 constexpr uint32_t kPollLimit = 1u << 21;      // polls before giving up (about a second)
 
 // A lane's channels: 4 bytes of them.
@@ -618,7 +619,7 @@ rec_fwd_kernel(const __grid_constant__ RecTensors a, const __grid_constant__ Run
     const int ch0 = f.group * kTileCh<T> + lane * C;
     const int left = a.dim - ch0;  // channels of this lane and those after it
     int next = 0;
-    if (threadIdx.x == 0) next = take<kFwdStages<kVec>>(ch, i + kFwdStages<kVec>, items);
+    if (threadIdx.x == kTaker) next = take<kFwdStages<kVec>>(ch, i + kFwdStages<kVec>, items);
     const int first = t.tile[f.seq];
     const int before = f.l > 0 ? maps_before(f.l, ch.shift) : 0;
     float h0[C];  // what the run starts from: asked for early, the run's other tiles wait for it
@@ -703,8 +704,8 @@ rec_fwd_kernel(const __grid_constant__ RecTensors a, const __grid_constant__ Run
         publish_map<T>(ch, f, groups, A, B, lane);
       }
     }
+    if (threadIdx.x == kTaker) tile_info<false>(s.info[(i + kFwdStages<kVec>) % kInfos], t, next, items, groups);
     look_back<T, false>(ch, f, first, groups, before, s.before, warp, lane);
-    if (threadIdx.x == 0) tile_info<false>(s.info[(i + kFwdStages<kVec>) % kInfos], t, next, items, groups);
     __syncthreads();
     float in[C];
     fold_before(s.before, before, in, lane);
@@ -824,7 +825,7 @@ rec_bwd_kernel(const __grid_constant__ RecBwdTensors a, const __grid_constant__ 
     const int ch0 = f.group * kTileCh<T> + lane * C;
     const int left = a.dim - ch0;
     int next = 0;
-    if (threadIdx.x == 0) next = take<kBwdStages>(ch, i + kBwdStages, items);
+    if (threadIdx.x == kTaker) next = take<kBwdStages>(ch, i + kBwdStages, items);
     const int first = t.tile[f.seq];
     const int before = f.l > 0 ? maps_before(f.l, ch.shift) : 0;
     float h0[C];
@@ -910,9 +911,9 @@ rec_bwd_kernel(const __grid_constant__ RecBwdTensors a, const __grid_constant__ 
         publish_map<T>(ch, f, groups, A, R, lane);
       }
     }
-    look_back<T, true>(ch, f, first, groups, before, s.before, warp, lane);
     // info[i + 2] takes the place of tile i - 2, whose part of dlower has been summed
-    if (threadIdx.x == 0) tile_info<true>(s.info[(i + kBwdStages) % kInfos], t, next, items, groups);
+    if (threadIdx.x == kTaker) tile_info<true>(s.info[(i + kBwdStages) % kInfos], t, next, items, groups);
+    look_back<T, true>(ch, f, first, groups, before, s.before, warp, lane);
     __syncthreads();
     float in[C];
     fold_before(s.before, before, in, lane);
