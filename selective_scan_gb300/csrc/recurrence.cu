@@ -17,7 +17,7 @@
 // other warps, and the next tile's copies are in flight while a tile waits for its predecessors
 // (with one stage, while the others finish). Unaligned rows are shifted into place as they are
 // read, at a third more instructions: eight runs of 32 768 tokens in all by 2 047 channels of
-// bf16 take 132 us forwards and 244 backwards (by 2 048: 91 and 154).
+// bf16 take 128 us forwards and 212 backwards (by 2 048: 89 and 145).
 //
 // What precedes chunk l of a run, the same for any timing (so results repeat bit for bit):
 // every chunk publishes its map, and every 16th (0, 16, 32, ...) the state after it too (the
@@ -41,10 +41,10 @@
 // y, and unrounded), and makes dx and dgate in one more sweep over its tokens. dlower is
 // summed per tile and then over the tiles, in order.
 //
-// Measured (GB300, 65 536 tokens x 2 048 channels, bf16, with lower bounds and, forward, checkpoints): one run 197 us
-// forward (186 without checkpoints: 4.3 TB/s, 64 % of the measured copy rate) and 305 backward (4.4 TB/s); eight runs
-// 164 and 281, 64 runs 162 and 281; 512 runs, where nothing waits, 153 and 281. fp32 moves 5.8 TB/s either way. What
-// bounds it is issue: 950 instructions a warp and tile of one run forward (24 a token to scan, 7 to store) at 2.2 an
+// Measured (GB300, 65 536 tokens x 2 048 channels, bf16, with lower bounds and, forward, checkpoints): one run 195 us
+// forward (185 without checkpoints: 4.4 TB/s, 64 % of the measured copy rate) and 295 backward (4.6 TB/s); eight runs
+// 159 and 269, 64 runs 160 and 269; 512 runs, where nothing waits, 155 and 275. fp32 moves 5.8 TB/s either way. What
+// bounds it is issue: 954 instructions a warp and tile of one run forward (24 a token to scan, 7 to store) at 2.2 an
 // SM and clock, of which 59 us would remain if they were free; then, for few runs, the waits for maps of tiles that
 // run at the same time.
 #include <cuda.h>
@@ -72,7 +72,9 @@ constexpr int kTok = kChunkR / kWarps;         // tokens of a warp
 constexpr int kMostShift = 4, kLeastShift = 2; // log2 of the chunks between two published states
 constexpr int kBack = (2 << kMostShift) / kWarps;  // maps that a warp looks back at, at most
 constexpr int kInfos = 4;
-constexpr int kTaker = 32 * 5;                 // the thread that takes the next tile
+// The thread that takes the next tile: of a warp that often has no maps to fetch (of the first one, with the nearest
+// maps, eight runs of 65 536 x 2 048 take 164 us instead of 159, backwards 281 instead of 269).
+constexpr int kTaker = 32 * 5;
 constexpr uint32_t kPollLimit = 1u << 21;      // polls before giving up (about a second)
 
 // A lane's channels: 4 bytes of them.
