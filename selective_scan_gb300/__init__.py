@@ -199,16 +199,29 @@ def _same(name, t, shape, dtype=None):
                          f", got {tuple(t.shape)} of {t.dtype}")
 
 
+def _on(stream):
+    """Makes a stream (torch's, a raw handle, or another's by its ``cuda_stream``) torch's current one. Handle 0 is the
+    legacy default stream (of which ExternalStream would make a new stream)."""
+    import torch
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
 def _workspace(need: int, workspace, device, stream):
-    """(pointer, bytes, tensor) of the caller's workspace, or of one made here, whose memory is not given to other
-    work before `stream` has passed the call; keep the tensor until the call returns."""
+    """(pointer, bytes, tensor) of the caller's workspace, or of one made here; keep the tensor until the call returns.
+    Its memory comes from `stream`'s own: what another stream has freed may still be in use there, and what is freed
+    here goes to `stream`'s next work."""
     if workspace is None:
         if need == 0:
             return None, 0, None
         import torch
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        if stream is not None:
-            workspace.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        else:
+            with _on(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=device)
     return _ptr(workspace), workspace.numel() * workspace.element_size(), workspace
 
 

@@ -1,0 +1,111 @@
+"""The recurrent block's operators on a stream that is not torch's current one: where their workspaces come from (on
+the CPU, with a stand-in for torch's streams), and their results while freed memory of the current stream is still in
+use there."""
+import contextlib
+
+import pytest
+import torch
+
+import selective_scan_gb300 as ss
+from tests.gpu_util import device
+from tests.util import assert_bits_equal
+
+
+class _Handle:
+    """A stream of another library: all that it shows is its handle."""
+    cuda_stream = 0x5000
+
+
+@pytest.fixture
+def streams(monkeypatch):
+    """torch.cuda's streams replaced by names; a list of the ones that were current when memory was taken."""
+    now, taken = ["the caller's"], []
+
+    @contextlib.contextmanager
+    def stream(s):
+        before, now[0] = now[0], s
+        yield
+        now[0] = before
+
+    class Memory:
+        def record_stream(self, s):
+            pass
+
+        def is_contiguous(self):
+            return True
+
+        def data_ptr(self):
+            return 0x100
+
+        def numel(self):
+            return 64
+
+        def element_size(self):
+            return 1
+
+    def empty(*_, **__):
+        taken.append(now[0])
+        return Memory()
+
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: ("external", handle))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: "default")
+    monkeypatch.setattr(torch, "empty", empty)
+    return now, taken
+
+
+@pytest.mark.parametrize("stream,where", [(None, "the caller's"), (0x7000, ("external", 0x7000)), (0, "default"),
+                                          (_Handle(), ("external", 0x5000))], ids=["none", "handle", "zero", "object"])
+def test_a_workspace_is_taken_on_the_stream_that_uses_it(streams, stream, where):
+    """Memory that the current stream has freed may still be in use there, so only that stream's order allows its
+    reuse. (0 is the legacy default stream's handle.)"""
+    now, taken = streams
+    assert ss._workspace(64, None, "cuda", stream)[:2] == (0x100, 64)
+    assert taken == [where] and now == ["the caller's"]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("form", ["stream", "handle", "default"])
+def test_operators_beside_a_current_stream_that_is_still_busy(form):
+    """Every operator that takes a workspace of its own, on a stream that is not current, while the current stream
+    still has to write memory that was freed on it: the results are those of the current stream alone."""
+    dev = device()
+    g = torch.Generator().manual_seed(1)
+    draw = lambda *s: torch.randn(s, generator=g)  # noqa: E731
+    lengths, dim, n = [700, 0, 300], 136, 256
+    cu = [0, 700, 700, 1000]
+    x, gate, dy = (draw(1000, dim).bfloat16().to(dev) for _ in range(3))
+    lower, pool, nw = torch.rand(dim, generator=g).to(dev), draw(3, dim).to(dev), draw(dim).to(dev)
+    w, dyl, pre = draw(n, dim).bfloat16().to(dev), draw(1000, n).bfloat16().to(dev), draw(1000, n).bfloat16().to(dev)
+    kept_rows = ss.gated_recurrence_checkpoints(cu)
+
+    def outputs():
+        e = lambda *s, t=torch.bfloat16: torch.zeros(s, dtype=t, device=dev)  # noqa: E731
+        f = torch.float32
+        return dict(st=pool.clone(), y=e(1000, dim), kept=e(kept_rows, dim, t=f), dx=e(1000, dim), dg=e(1000, dim),
+                    dlo=e(dim, t=f), ds=e(1000, dim), dnw=e(dim, t=f), dn=e(1000, dim), dw=e(n, dim), db=e(n, t=f))
+
+    def chain(o, stream):
+        ss.gated_recurrence(o["y"], x, gate, lower, o["st"], cu, [2, 0, 1], [1, 1, 0], checkpoints=o["kept"], stream=stream)
+        ss.gated_recurrence_backward(o["dx"], o["dg"], o["dlo"], None, dy, None, x, gate, lower, o["kept"], cu, stream=stream)
+        ss.add_rmsnorm_backward(o["ds"], None, o["dnw"], dy, None, x, nw, 1e-5, stream=stream)
+        ss.linear_backward(o["dn"], o["dw"], o["db"], dyl, x, w, activation="silu", pre=pre, stream=stream)
+
+    want, got = outputs(), outputs()
+    chain(want, None)
+    torch.cuda.synchronize()
+    sizes = [ss.gated_recurrence_workspace_bytes(cu, dim), ss.gated_recurrence_workspace_bytes(cu, dim, True),
+             ss.library().mamba2_add_rmsnorm_backward_workspace_bytes(1000, dim),
+             ss.library().mamba2_linear_backward_workspace_bytes(1000, dim, n)]
+    side = torch.cuda.Stream()
+    stream = {"stream": side, "handle": side.cuda_stream, "default": 0}[form]
+    busy = torch.cuda.Stream() if form == "default" else torch.cuda.current_stream()
+    busy.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(busy):
+        torch.cuda._sleep(50_000_000)
+        written = [torch.zeros(s, dtype=torch.uint8, device=dev) for s in sizes]
+        del written  # (their blocks are the ones that torch gives out next on this stream)
+        chain(got, stream)
+    torch.cuda.synchronize()
+    for k in want:
+        assert_bits_equal(got[k], want[k], k)
