@@ -20,7 +20,7 @@ from typing import Optional
 
 import torch
 
-from . import (add_rmsnorm, add_rmsnorm_backward, gated_recurrence, gated_recurrence_backward,
+from . import (_on as _on_stream, add_rmsnorm, add_rmsnorm_backward, gated_recurrence, gated_recurrence_backward,
                gated_recurrence_checkpoints, gated_recurrence_step_device, linear, linear_backward)
 
 E4M3 = torch.float8_e4m3fn
@@ -152,6 +152,4 @@ class RecurrentBlock:
 
 
 def _on(stream):
-    if stream is None:
-        return contextlib.nullcontext()
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+    return contextlib.nullcontext() if stream is None else _on_stream(stream)

@@ -24,8 +24,10 @@ def streams(monkeypatch):
     @contextlib.contextmanager
     def stream(s):
         before, now[0] = now[0], s
-        yield
-        now[0] = before
+        try:
+            yield
+        finally:
+            now[0] = before
 
     class Memory:
         def record_stream(self, s):
@@ -62,6 +64,30 @@ def test_a_workspace_is_taken_on_the_stream_that_uses_it(streams, stream, where)
     now, taken = streams
     assert ss._workspace(64, None, "cuda", stream)[:2] == (0x100, 64)
     assert taken == [where] and now == ["the caller's"]
+
+
+@pytest.mark.parametrize("stream,where", [(None, "the caller's"), (0x7000, ("external", 0x7000)), (0, "default")],
+                         ids=["none", "handle", "zero"])
+def test_the_block_runs_on_the_stream_that_it_is_given(streams, monkeypatch, stream, where):
+    """Its operators run on torch's current stream, so that has to be the stream asked for, also for handle 0."""
+    from selective_scan_gb300 import recurrent_block
+    now, _ = streams
+    ran = []
+
+    class Stop(Exception):
+        pass
+
+    def add_rmsnorm(*_, **__):
+        ran.append(now[0])
+        raise Stop
+
+    monkeypatch.setattr(recurrent_block, "add_rmsnorm", add_rmsnorm)
+    w = torch.zeros((8, 16), dtype=torch.bfloat16)
+    block = recurrent_block.RecurrentBlock(recurrent_block.RecurrentBlockWeights(
+        norm_w=None, w_x=w, b_x=None, w_gate=w, b_gate=None, lower=None, w_out=None, b_out=None))
+    with pytest.raises(Stop):
+        block.prefill(w, None, None, [0, 8], [0], [1], stream=stream)
+    assert ran == [where] and now == ["the caller's"]
 
 
 @pytest.mark.gpu
