@@ -183,8 +183,8 @@ __device__ __forceinline__ void row_reduce(float (&v)[n], int nt, float (*part)[
     for (int k = 0; k < n; ++k) v[k] = kMax ? max_nan(v[k], part[row0 + i][k]) : v[k] + part[row0 + i][k];
 }
 
-// Launched as a programmatic dependent: the weights, a parameter, may be read before the kernel in front has
-// finished; nothing else is.
+// Launched as a programmatic dependent: nothing of global memory is read or written before this. (The weights too may
+// come from the kernel in front, an optimizer's step or a cast, or from one before it that it did not wait for.)
 __device__ __forceinline__ void wait_for_inputs() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 template <typename T, typename S, bool F8, bool kShift>
@@ -296,6 +296,7 @@ add_norm_bwd_kernel(const AddNormBwdArgs a, const int nt) {
   extern __shared__ __align__(16) float columns[];
   const float4* weights = reinterpret_cast<const float4*>(columns + threadIdx.y * nt * U * W) + threadIdx.x * 2;
   const int shift = shift_of((int64_t)blockIdx.x * blockDim.y + threadIdx.y, a.dim);  // of all of its rows
+  wait_for_inputs();
   if constexpr (kShift) {
 #pragma unroll
     for (int k = 0; k < U * W; ++k) {
@@ -316,7 +317,6 @@ add_norm_bwd_kernel(const AddNormBwdArgs a, const int nt) {
     w[6] = hi.z;
     w[7] = hi.w;
   };
-  wait_for_inputs();
   float acc[U][W];
 #pragma unroll
   for (int u = 0; u < U; ++u)
