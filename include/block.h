@@ -180,7 +180,7 @@ mamba2_status mamba2_add_rmsnorm_backward(void* dx, void* dresidual, float* dwei
  */
 typedef enum mamba2_activation {
   MAMBA2_ACT_NONE = 0,
-  MAMBA2_ACT_RELU = 1, /* max(p, 0) */
+  MAMBA2_ACT_RELU = 1, /* max(p, 0); NaN for a NaN, as the others */
   MAMBA2_ACT_SILU = 2, /* p sigmoid(p) */
   MAMBA2_ACT_GELU = 3  /* p Phi(p), Phi the normal distribution function */
 } mamba2_activation;
@@ -198,7 +198,7 @@ size_t mamba2_linear_backward_workspace_bytes(int32_t rows, int32_t in_features,
  * Gradients, for bf16 operands: with dp = dy * activation'(pre),
  *   dx = dp . w,  dw = dp^T . x,  dbias = sum over rows of dp (fixed order).
  * The residual's gradient is dy itself. dp is rounded to bf16 where it enters
- * the two products (dbias sums it unrounded); relu'(0) = 0.
+ * the two products (dbias sums it unrounded); relu'(0) = 0, relu'(NaN) = NaN.
  *
  *   dx    [rows, in_features] bf16 or NULL
  *   dw    [out_features, in_features] bf16 or NULL

@@ -76,6 +76,12 @@ __device__ __forceinline__ float gelu(float v) {
   normal_tail(v, tail, bell);
   return v * (v < 0.0f ? tail : 1.0f - tail);
 }
+// max(v, 0); a NaN stays one.
+__device__ __forceinline__ float relu(float v) {
+  float r;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(v));
+  return r;
+}
 // (one branch for all of them)
 template <int n>
 __device__ __forceinline__ void activate_all(float (&v)[n], int act) {
@@ -87,12 +93,12 @@ __device__ __forceinline__ void activate_all(float (&v)[n], int act) {
     for (int i = 0; i < n; ++i) v[i] = gelu(v[i]);
   } else if (act == MAMBA2_ACT_RELU) {
 #pragma unroll
-    for (int i = 0; i < n; ++i) v[i] = fmaxf(v[i], 0.0f);
+    for (int i = 0; i < n; ++i) v[i] = relu(v[i]);
   }
 }
 __device__ __forceinline__ float slope(float v, int act) {
   switch (act) {
-    case MAMBA2_ACT_RELU: return v > 0.0f ? 1.0f : 0.0f;
+    case MAMBA2_ACT_RELU: return v > 0.0f ? 1.0f : v <= 0.0f ? 0.0f : v;  // (a NaN's is NaN)
     case MAMBA2_ACT_SILU: {
       const float p = sigmoid_ftz(v);
       return p * fmaf(v, 1.0f - p, 1.0f);
