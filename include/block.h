@@ -129,8 +129,9 @@ mamba2_status mamba2_gated_recurrence_backward(void* dx, void* dgate, float* dlo
  *            `residual` itself; the norm is of the unrounded sum)
  *   out      [rows, dim] out_type: act or MAMBA2_E4M3
  *   scale    [rows] f32, with MAMBA2_E4M3 only: max |y| / 448 over the row (1
- *            for a row of zeros); out is y / scale in e4m3, to nearest even. A
- *            row holding a NaN or an infinity has a NaN scale and NaN outputs.
+ *            for a row of zeros; rounded up where it is below 2^-126); out is
+ *            y / scale in e4m3, to nearest even. A row holding a NaN or an
+ *            infinity has a NaN scale and NaN outputs.
  *   weight   [dim] f32; eps >= 0
  */
 mamba2_status mamba2_add_rmsnorm(void* out, float* scale, void* sum, const void* x, const void* residual,

@@ -42,6 +42,28 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+// The scale of a row whose largest |y| is top: with it as the divisor, top comes to 448. Below the normal numbers, where
+// a rounding may be of any size, it is rounded up, so that no quotient passes 448 and none is by zero.
+__device__ __forceinline__ float scale_of(float top) {
+  if (top == 0.0f) return 1.0f;
+  const float scale = top / kMax8;
+  return scale < 0x1p-126f ? __fdiv_ru(top, kMax8) : scale;
+}
+// Many quotients by one scale, each as if divided: with r near 1 / d and q = y r, the remainder q d - y is exact in one
+// fma, and q - r (q d - y) is y / d to 2^-47 before its rounding (Markstein's correction). y and d are made 2^100 times as
+// large where the reciprocal or the remainder would leave the normal numbers (a y that is still too small for that is
+// 0 in 8 bits), and an infinite scale makes them 0 (or NaN, for an infinite y). (16 384 x 2 048 of bf16, with the residual and
+// its sum: by division 42 us, by a reciprocal alone, which rounds twice, 38.)
+struct Quotients {
+  float m, d, r;
+  __device__ __forceinline__ explicit Quotients(float scale)
+      : m(scale < 0x1p-60f ? 0x1p100f : isinf(scale) ? 0.0f : 1.0f), d(isinf(scale) ? 1.0f : scale * m), r(1.0f / d) {}
+  __device__ __forceinline__ float operator()(float y) const {
+    const float v = y * m, q = v * r;
+    return fmaf(-fmaf(q, d, -v), r, q);  // (with these signs -0 stays -0)
+  }
+};
+
 // Where a thread's u-th unit lies in its row. With kShift rows start inside a unit of the matrix (dim is no multiple
 // of 8): units keep the matrix's boundaries, so the first may begin before the row and the last end after it.
 template <bool kShift>
@@ -259,7 +281,8 @@ add_norm_kernel(const AddNormArgs a, const int nt) {
   }
   if (F8) {
     row_reduce<true, 1>(top, nt, part[1]);
-    const float scale = top[0] == 0.0f ? 1.0f : top[0] / kMax8, rs = 1.0f / scale;
+    const float scale = scale_of(top[0]);
+    const Quotients by(scale);
     if (!live) return;
     if (threadIdx.x == 0) a.scale[row] = scale;
 #pragma unroll
@@ -267,7 +290,7 @@ add_norm_kernel(const AddNormArgs a, const int nt) {
       const At<kShift> at(shift, nt, u);
       if (at.c < a.dim) {
 #pragma unroll
-        for (int j = 0; j < W; ++j) s[u][j] *= rs;
+        for (int j = 0; j < W; ++j) s[u][j] = by(s[u][j]);
         store8(static_cast<__nv_fp8_storage_t*>(a.out) + row * a.dim + at.c, s[u], at, a.dim);
       }
     }
@@ -444,13 +467,12 @@ __global__ void __launch_bounds__(kCtaThreads) add_norm_streamed_kernel(const Ad
   const T* x = static_cast<const T*>(a.x) + base;
   const S* r = a.residual ? static_cast<const S*>(a.residual) + base : nullptr;
   auto value = [&](int i) { return Act<T>::to_f(x[i]) + (r ? Act<S>::to_f(r[i]) : 0.0f); };
-  float ss = 0.0f, top = 0.0f, scale = 1.0f;
+  float ss = 0.0f, top = 0.0f, scale = 0.0f;
   for (int i = threadIdx.x; i < a.dim; i += kCtaThreads) ss = fmaf(value(i), value(i), ss);
   const float inv = rsqrtf(block_reduce(ss, false) / (float)a.dim + a.eps);
   if (F8) {
     for (int i = threadIdx.x; i < a.dim; i += kCtaThreads) top = max_nan(top, fabsf(value(i) * inv * a.weight[i]));
-    top = block_reduce(top, true);
-    if (!(top == 0.0f)) scale = top / kMax8;
+    scale = scale_of(block_reduce(top, true));
     if (threadIdx.x == 0) a.scale[blockIdx.x] = scale;
   }
   for (int i = threadIdx.x; i < a.dim; i += kCtaThreads) {
