@@ -1,5 +1,7 @@
-"""linear's activations where they go wrong most easily: values that are not finite, by the kernel of few rows, whole
-blocks of pairs' tiles and their edges and unaligned rows."""
+"""linear's activations where they go wrong most easily: values that are not finite, and GELU far below zero, by the
+kernel of few rows, whole blocks of pairs' tiles and their edges and unaligned rows."""
+import math
+
 import pytest
 import torch
 
@@ -72,3 +74,40 @@ def test_a_pre_activation_that_is_nan_reaches_its_gradients(activation, n):
         keep = torch.tensor([i for i in range(got.shape[0]) if i not in hit])
         assert torch.isnan(got[hit]).all(), name
         R.check(got[keep], tuple(v[keep] for v in want[name]), name)
+
+
+def gelu_slack(p):
+    """Relative error of the tail 1 - Phi(|p|) in 32 bits: 2 roundings of p^2 / 2 and one of its factor, which the
+    exponential turns into 3 |p^2 / 2| 2^-24 (2 p^2 is taken, as the exponential rounds its argument too), and 64
+    roundings for the rest (eight terms of a polynomial without cancellation, a reciprocal, an exponential and four
+    products)."""
+    return (64 + 2 * p * p) * R.U
+
+
+@pytest.mark.parametrize("rows,n", SHAPES)
+def test_gelu_keeps_its_digits_below_zero(rows, n):
+    """x = 0, so that the bias is the pre-activation: p Phi(p) to a relative error, however small it is."""
+    dev, k = device(), 16
+    p = torch.linspace(-12.5, 3.0, n)
+    zero = lambda *s: torch.zeros(s, dtype=BF16, device=dev)  # noqa: E731
+    v = p.double()
+    want = 0.5 * v * torch.erfc(-v * math.sqrt(0.5))
+    for t in (F32, BF16):
+        out = torch.empty((rows, n), dtype=t, device=dev)
+        ss.linear(out, zero(rows, k), zero(n, k), bias=p.to(dev), activation="gelu")
+        R.check(out, (want.expand(rows, n), (gelu_slack(v) * want.abs()).expand(rows, n)), "gelu")
+
+
+def test_gelu_slope_keeps_its_digits_below_zero():
+    """One row, so that dbias is dy gelu'(pre) unrounded."""
+    dev, n, k = device(), 400, 16
+    pre = torch.linspace(-12.5, 3.0, n).to(BF16)
+    dy = torch.randn((1, n), generator=torch.Generator().manual_seed(2)).to(BF16)
+    v = pre.double()
+    phi = torch.exp(-v * v / 2) / math.sqrt(2 * math.pi)
+    tail = 0.5 * torch.erfc(-v * math.sqrt(0.5))
+    db = torch.empty(n, device=dev)
+    ss.linear_backward(None, None, db, dy.to(dev), torch.zeros((1, k), dtype=BF16, device=dev),
+                       torch.zeros((n, k), dtype=BF16, device=dev), activation="gelu", pre=pre[None].to(dev))
+    d = dy[0].double()
+    R.check(db, (d * (tail + v * phi), d.abs() * gelu_slack(v) * (tail + v.abs() * phi)), "dbias")
