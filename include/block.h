@@ -20,12 +20,17 @@
  * with a row stride, for which the alignment of their element suffices
  * (16-byte aligned rows are fastest); any other misalignment, a null pointer
  * that is not marked optional, a negative size or a row stride below the width
- * is MAMBA2_ERR_INVALID_ARGUMENT. Outputs must not overlap inputs unless said.
+ * is MAMBA2_ERR_INVALID_ARGUMENT, as are more rows or a greater width than
+ * MAMBA2_MAX_BLOCK_SIZE. Outputs must not overlap inputs unless said.
  */
 #ifndef MAMBA2_BLOCK_H
 #define MAMBA2_BLOCK_H
 
 #include "mamba2.h"
+
+/* Most rows, and columns of a matrix, that a call takes: 2^31 less what rounds
+ * either up to whole tiles. */
+#define MAMBA2_MAX_BLOCK_SIZE 0x7fff0000
 
 #ifdef __cplusplus
 extern "C" {

@@ -34,6 +34,7 @@ RECURRENCE_STEP, RECURRENCE_CHUNK = 16, 128
 (OK, ERR_INVALID_ARGUMENT, ERR_SLOT_OUT_OF_RANGE, ERR_SLOT_SHARED, ERR_RUNS_DONT_COVER_ROWS,
  ERR_NOT_IMPLEMENTED, ERR_CUDA, ERR_WORKSPACE_TOO_SMALL) = range(8)
 MAX_SEQS = 1024
+MAX_BLOCK_SIZE = 0x7fff0000  # most rows and columns of the recurrent block's operators
 
 
 class Mamba2Error(RuntimeError):

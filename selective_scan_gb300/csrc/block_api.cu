@@ -18,6 +18,10 @@ bool strided_ok(const void* p, int64_t ld, int64_t width, size_t elem) {
   return p && aligned_to(p, elem) && ld >= width;
 }
 
+// Rows and columns that the kernels can round up to tiles in 32 bits.
+bool rows_ok(int32_t n) { return n >= 0 && n <= MAMBA2_MAX_BLOCK_SIZE; }
+bool width_ok(int32_t n) { return n > 0 && n <= MAMBA2_MAX_BLOCK_SIZE; }
+
 // cu_seqlens from 0, non-decreasing.
 bool cu_ok(const int32_t* cu, int32_t n) {
   if (n < 0 || n > MAMBA2_MAX_SEQS || (n > 0 && !cu)) return false;
@@ -63,7 +67,7 @@ int64_t mamba2_gated_recurrence_checkpoints(const int32_t* cu_seqlens, int32_t n
 
 size_t mamba2_gated_recurrence_workspace_bytes(const int32_t* cu_seqlens, int32_t num_seqs, int32_t dim,
                                                int32_t backward) {
-  if (dim <= 0 || !cu_ok(cu_seqlens, num_seqs)) return 0;
+  if (!width_ok(dim) || !cu_ok(cu_seqlens, num_seqs)) return 0;
   bool chained;
   const int64_t chunks = count_chunks(cu_seqlens, num_seqs, &chained);
   return recurrence_workspace(chunks, chained, num_seqs, dim, backward != 0);
@@ -74,7 +78,7 @@ mamba2_status mamba2_gated_recurrence(void* y, float* checkpoints, const void* x
                                       int32_t dim, int64_t ld_y, int64_t ld_x, int64_t ld_gate, mamba2_dtype act,
                                       const mamba2_recurrent_batch* rb, void* workspace, size_t workspace_bytes,
                                       void* stream) {
-  if (!act_ok(act) || rows < 0 || dim <= 0 || !rb) return MAMBA2_ERR_INVALID_ARGUMENT;
+  if (!act_ok(act) || !rows_ok(rows) || !width_ok(dim) || !rb) return MAMBA2_ERR_INVALID_ARGUMENT;
   const size_t e = act_size(act);
   if (rows > 0 && (!strided_ok(y, ld_y, dim, e) || !strided_ok(x, ld_x, dim, e) ||
                    !strided_ok(gate, ld_gate, dim, e) || y == x || y == gate))
@@ -108,7 +112,7 @@ mamba2_status mamba2_gated_recurrence(void* y, float* checkpoints, const void* x
 namespace {
 mamba2_status check_step(const void* y, const void* x, const void* gate, const float* lower, const float* state,
                          int32_t n, int32_t dim, int64_t ld_y, int64_t ld_x, int64_t ld_gate, mamba2_dtype act) {
-  if (!act_ok(act) || dim <= 0) return MAMBA2_ERR_INVALID_ARGUMENT;
+  if (!act_ok(act) || !width_ok(dim)) return MAMBA2_ERR_INVALID_ARGUMENT;
   const size_t e = act_size(act);
   if (n > 0 && (!strided_ok(y, ld_y, dim, e) || !strided_ok(x, ld_x, dim, e) ||
                 !strided_ok(gate, ld_gate, dim, e) || y == x || y == gate || !state || !aligned16(state)))
@@ -159,7 +163,7 @@ mamba2_status mamba2_gated_recurrence_backward(void* dx, void* dgate, float* dlo
                                                int64_t ld_x, int64_t ld_gate, mamba2_dtype act,
                                                const int32_t* cu_seqlens, int32_t num_seqs, void* workspace,
                                                size_t workspace_bytes, void* stream) {
-  if (!act_ok(act) || rows < 0 || dim <= 0 || num_seqs < 0 || num_seqs > MAMBA2_MAX_SEQS ||
+  if (!act_ok(act) || !rows_ok(rows) || !width_ok(dim) || num_seqs < 0 || num_seqs > MAMBA2_MAX_SEQS ||
       (num_seqs > 0 && !cu_seqlens) || (dlower && !lower))
     return MAMBA2_ERR_INVALID_ARGUMENT;
   const size_t e = act_size(act);
@@ -213,7 +217,7 @@ mamba2_status mamba2_add_rmsnorm(void* out, float* scale, void* sum, const void*
                                  const float* weight, int32_t rows, int32_t dim, float eps, mamba2_dtype act,
                                  mamba2_dtype sum_type, mamba2_dtype out_type, void* stream) {
   if (!act_ok(act) || (sum_type != act && sum_type != MAMBA2_F32) || (out_type != act && out_type != MAMBA2_E4M3) ||
-      rows < 0 || dim <= 0 || !(eps >= 0.0f) || (out_type == MAMBA2_E4M3 ? (rows > 0 && !scale) : scale != nullptr))
+      !rows_ok(rows) || !width_ok(dim) || !(eps >= 0.0f) || (out_type == MAMBA2_E4M3 ? (rows > 0 && !scale) : scale != nullptr))
     return MAMBA2_ERR_INVALID_ARGUMENT;
   if (rows == 0) return MAMBA2_OK;
   if (!out || !x || !weight || out == x || (residual && out == residual) || (sum && (sum == out || sum == x)))
@@ -226,7 +230,7 @@ mamba2_status mamba2_add_rmsnorm(void* out, float* scale, void* sum, const void*
 }
 
 size_t mamba2_add_rmsnorm_backward_workspace_bytes(int32_t rows, int32_t dim) {
-  if (rows <= 0 || dim <= 0) return 0;
+  if (rows == 0 || !rows_ok(rows) || !width_ok(dim)) return 0;
   return align256((size_t)add_rmsnorm_backward_parts(rows, dim) * dim * 4);
 }
 
@@ -234,7 +238,8 @@ mamba2_status mamba2_add_rmsnorm_backward(void* dx, void* dresidual, float* dwei
                                           const void* dsum, const void* sum, const float* weight, int32_t rows,
                                           int32_t dim, float eps, mamba2_dtype act, mamba2_dtype sum_type,
                                           void* workspace, size_t workspace_bytes, void* stream) {
-  if (!act_ok(act) || (sum_type != act && sum_type != MAMBA2_F32) || rows < 0 || dim <= 0 || !(eps >= 0.0f))
+  if (!act_ok(act) || (sum_type != act && sum_type != MAMBA2_F32) || !rows_ok(rows) || !width_ok(dim) ||
+      !(eps >= 0.0f))
     return MAMBA2_ERR_INVALID_ARGUMENT;
   if (!weight || (rows > 0 && (!dy || !sum))) return MAMBA2_ERR_INVALID_ARGUMENT;
   const void* in[] = {dy, sum, dsum};
@@ -258,7 +263,7 @@ mamba2_status mamba2_linear(void* out, void* pre, const void* x, const float* x_
                             mamba2_activation activation, void* stream) {
   const bool fp8 = in_type == MAMBA2_E4M3;
   if ((!fp8 && !act_ok(in_type)) || !act_ok(out_type) || (int)activation < 0 || activation > MAMBA2_ACT_GELU ||
-      rows < 0 || in_features <= 0 || out_features <= 0)
+      !rows_ok(rows) || !width_ok(in_features) || !width_ok(out_features))
     return MAMBA2_ERR_INVALID_ARGUMENT;
   const int unit = fp8 ? 16 : 8;  // elements of 16 bytes
   if (in_type == MAMBA2_F32 || in_features % unit != 0 || ld_x % unit != 0) return MAMBA2_ERR_NOT_IMPLEMENTED;
@@ -287,7 +292,7 @@ size_t dp_bytes(int32_t rows, int32_t out_features) { return align256((size_t)ro
 }  // namespace
 
 size_t mamba2_linear_backward_workspace_bytes(int32_t rows, int32_t in_features, int32_t out_features) {
-  if (rows <= 0 || in_features <= 0 || out_features <= 0) return 0;
+  if (rows == 0 || !rows_ok(rows) || !width_ok(in_features) || !width_ok(out_features)) return 0;
   return dp_bytes(rows, out_features) + align256((size_t)linear_bias_parts(rows) * out_features * 4);
 }
 
@@ -295,7 +300,8 @@ mamba2_status mamba2_linear_backward(void* dx, void* dw, float* dbias, const voi
                                      const void* x, const void* w, int32_t rows, int32_t in_features,
                                      int32_t out_features, int64_t ld_x, mamba2_activation activation,
                                      void* workspace, size_t workspace_bytes, void* stream) {
-  if ((int)activation < 0 || activation > MAMBA2_ACT_GELU || rows < 0 || in_features <= 0 || out_features <= 0)
+  if ((int)activation < 0 || activation > MAMBA2_ACT_GELU || !rows_ok(rows) || !width_ok(in_features) ||
+      !width_ok(out_features))
     return MAMBA2_ERR_INVALID_ARGUMENT;
   if (in_features % 8 != 0 || ld_x % 8 != 0) return MAMBA2_ERR_NOT_IMPLEMENTED;
   if (rows > 0 && (!dy || (activation != MAMBA2_ACT_NONE && !pre) ||
