@@ -269,6 +269,8 @@ class Batch:
 
     def __init__(self, cu_seqlens: Optional[Sequence[int]], slots: Sequence[int], fresh: Sequence[int]):
         n = len(slots)
+        if cu_seqlens is not None and n > 0 and len(cu_seqlens) <= n:
+            raise ValueError(f"cu_seqlens: {n} runs have {n + 1} boundaries, got {len(cu_seqlens)}")
         self.slots = _int32s(slots)
         flags = bytearray(map(bool, fresh)).ljust(max(n, 1), b"\0")
         if len(flags) > max(n, 1):

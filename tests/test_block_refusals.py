@@ -44,3 +44,14 @@ def test_the_largest_size_is_the_headers(product_lib):
     assert int(re.search(r"#define MAMBA2_MAX_BLOCK_SIZE (0x[0-9a-f]+)", text).group(1), 16) == MOST
     assert product_lib.mamba2_add_rmsnorm_backward_workspace_bytes(MOST, 8) > 0
     assert product_lib.mamba2_linear_backward_workspace_bytes(1, MOST // 8 * 8, 8) > 0
+
+
+def test_a_batch_of_fewer_boundaries_than_runs(product_lib):
+    """The library reads one more boundary than there are slots."""
+    with pytest.raises(ValueError):
+        ss.Batch([0, 4], [0, 1], [1, 1])
+    with pytest.raises(ValueError):
+        ss.Batch([], [0], [1])
+    assert ss.Batch([0, 4, 4], [0, 1], [1, 1]).rb.num_seqs == 2
+    assert ss.Batch(None, [0, 1], [1, 1]).rb.num_seqs == 2 and ss.Batch([0], [], []).rb.num_seqs == 0
+    assert ss.Batch([], [], []).rb.num_seqs == 0
