@@ -41,15 +41,15 @@ gated_rmsnorm_kernel(const NormArgs a, const int w_smem) {
   const int64_t row = rp * kNormRows + r;
   const bool live = row < a.rows;  // the last CTA may hold fewer rows
   const float* wg = a.weight + (int64_t)grp * gs;
+  // launched as a programmatic dependent of the kernel before it, which may be the one
+  // that writes x, z or the weights: everything is read after this wait
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (w_smem) {
     for (int i = threadIdx.x; i < gs / 4; i += kNormThreads * kNormRows)
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"((uint32_t)__cvta_generic_to_shared(wsm + 4 * i)),
                    "l"(wg + 4 * i));
   }
   asm volatile("cp.async.commit_group;\n" ::: "memory");
-  // launched as a programmatic dependent of the kernel before it (the scan that
-  // writes x): the weights above are a parameter; x and z come after this wait
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const float* w = w_smem ? wsm : wg;
   const int64_t base = row * a.dim + (int64_t)grp * gs;
   const T* x = static_cast<const T*>(a.x) + base;
