@@ -67,9 +67,9 @@ decode_step_kernel(const __grid_constant__ DecodeArgs a) {
   const int rows = nh * P;  // state rows owned by this CTA
   const bool dev = a.dev_slots != nullptr;
   // Launched as a programmatic dependent of whatever precedes it on the stream
-  // (the previous step's finish kernel lets it be scheduled early): only the
-  // model's parameters may be read before this wait; the batch, the token's
-  // inputs, both pools and dst come after it.
+  // (the previous step's finish kernel lets it be scheduled early), which may be
+  // what writes anything that this kernel reads, its parameters too.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   float A_h = 0.f, D_h = 0.f, bias_h = 0.f;
   if (threadIdx.x < nh) {
     A_h = a.A_log[h0 + threadIdx.x];
@@ -85,7 +85,6 @@ decode_step_kernel(const __grid_constant__ DecodeArgs a) {
       asm volatile("prefetch.global.L1 [%0];" ::"l"(a.conv_b + c0));
     }
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   // a device batch: nothing is touched unless the batch check (the launch before) passed
   if (dev && (__ldg(a.dev_status) != 0 || s >= __ldg(a.dev_n))) return;
   const bool fresh = dev ? __ldg(a.dev_fresh + s) != 0 : seq_fresh(a.tab, s);
@@ -559,7 +558,7 @@ static cudaError_t launch_decode_tk(const DecodeArgs& a, cudaStream_t st) {
   }
   // programmatic dependent launch: scheduled while the kernel before it (the
   // previous step's finish kernel) runs; it waits (griddepcontrol.wait) before
-  // reading anything but the parameters
+  // reading anything
   cudaLaunchConfig_t scfg = {};
   scfg.gridDim = dim3((unsigned)a.ctas_per_seq, (unsigned)a.tab.n, 1);
   scfg.blockDim = dim3(kDecodeThreads, 1, 1);

@@ -1,9 +1,10 @@
-"""The gated norm's weight when the kernel before the call on its stream has just written it: the norm is launched as
-that kernel's dependent, and may read nothing before it has finished."""
+"""The norm's and the decode step's parameters when the kernel before the call on its stream has just written them:
+both are launched as that kernel's dependents, and may read nothing before it has finished."""
 import pytest
 import torch
 
 import selective_scan_gb300 as ss
+import workloads as W
 from tests.gpu_util import device
 from tests.util import assert_bits_equal
 
@@ -58,3 +59,23 @@ def test_gated_norm(rows, dim, groups):
         return [out]
 
     both(norm, [torch.randn(dim, generator=g)], dev)
+
+
+@pytest.mark.parametrize("n,dims", [(1, W.DIMS_130M), (5, W.DIMS_TINY)])
+def test_decode_step(n, dims):
+    dev = device()
+    wl = W.decode_batch(seed=11, num_seqs=n, steps=1, num_slots=n + 2, dims=dims)
+    p, b = wl.params, wl.batch
+    x, z, dt = (t[0].contiguous().to(dev) for t in (wl.dec_xBC, wl.dec_z, wl.dec_dt))
+    conv0, ssm0 = wl.conv_state.to(dev), wl.ssm_state.to(dev)
+    conv, ssm = torch.empty_like(conv0), torch.empty_like(ssm0)
+
+    def step(q):
+        conv.copy_(conv0)
+        ssm.copy_(ssm0)
+        q[-1].add_(0)
+        out = torch.empty((n, wl.dims.d_inner), dtype=x.dtype, device=dev)
+        ss.decode_step(out, x, z, dt, *q, p.norm_groups, p.eps, conv, ssm, wl.dims, b.slots, b.fresh)
+        return [out, conv, ssm]
+
+    both(step, [p.conv_w, p.conv_b, p.A_log, p.dt_bias, p.D, p.norm_w], dev)
