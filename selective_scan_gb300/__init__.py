@@ -333,16 +333,11 @@ def ssd_scan(dst, xbc, dt, A_log, dt_bias, D, ssm_state, dims, cu_seqlens=None, 
     ``workspace`` is a device tensor of at least ``ssd_scan_workspace_bytes`` bytes
     (allocated here with torch when None and needed).
     """
-    import torch
     rows = xbc.shape[0]
     d = _dims(dims)
     b = _batch(cu_seqlens, slots, fresh, batch)
-    if workspace is None:
-        need = int(_lib().mamba2_ssd_scan_workspace_bytes(ctypes.byref(d), rows, b.ref()))
-        if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=xbc.device)
-    ws_ptr = _ptr(workspace) if workspace is not None else None
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    need = int(_lib().mamba2_ssd_scan_workspace_bytes(ctypes.byref(d), rows, b.ref())) if workspace is None else 0
+    ws_ptr, ws_bytes, _keep = _workspace(need, workspace, xbc.device, stream)
     st = _lib().mamba2_ssd_scan(_ptr(dst), _ptr(xbc), _ptr(dt), _ptr(A_log), _ptr(dt_bias), _ptr(D),
                                 _ptr(ssm_state), ssm_state.shape[0], rows, ctypes.byref(d), _dt(xbc), b.ref(),
                                 ws_ptr, ws_bytes, _stream(stream))
@@ -471,18 +466,17 @@ def prefill_host(out_host, xBC_host, z_host, dt_host, conv_w, conv_b, A_log, dt_
     tensor of at least ``prefill_host_workspace_bytes`` bytes (allocated here with
     torch when None). Asynchronous: synchronise the stream before reading ``out_host``.
     """
-    import torch
     d = _dims(dims)
     b = _batch(cu_seqlens, slots, fresh, batch)
     act = _dt(xBC_host)
+    need = 0
     if workspace is None:
-        need = int(_lib().mamba2_prefill_host_workspace_bytes(ctypes.byref(d), act, b.ref(), int(piece_rows)))
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=ssm_state.device)
+        need = max(1, int(_lib().mamba2_prefill_host_workspace_bytes(ctypes.byref(d), act, b.ref(), int(piece_rows))))
+    ws_ptr, ws_bytes, _keep = _workspace(need, workspace, ssm_state.device, stream)
     st = _lib().mamba2_prefill_host(_ptr(out_host), _ptr(xBC_host), _ptr(z_host), _ptr(dt_host), _ptr(conv_w),
                                     _ptr(conv_b), _ptr(A_log), _ptr(dt_bias), _ptr(D), _ptr(norm_w), int(norm_groups),
                                     float(eps), _ptr(conv_state), _ptr(ssm_state), ssm_state.shape[0], ctypes.byref(d),
-                                    act, b.ref(), int(piece_rows), _ptr(workspace),
-                                    workspace.numel() * workspace.element_size(), _stream(stream))
+                                    act, b.ref(), int(piece_rows), ws_ptr, ws_bytes, _stream(stream))
     if check:
         _check(st, "mamba2_prefill_host")
     return st

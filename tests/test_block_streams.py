@@ -16,6 +16,10 @@ class _Handle:
     cuda_stream = 0x5000
 
 
+class _Stop(Exception):
+    pass
+
+
 @pytest.fixture
 def streams(monkeypatch):
     """torch.cuda's streams replaced by names; a list of the ones that were current when memory was taken."""
@@ -74,20 +78,36 @@ def test_the_block_runs_on_the_stream_that_it_is_given(streams, monkeypatch, str
     now, _ = streams
     ran = []
 
-    class Stop(Exception):
-        pass
-
     def add_rmsnorm(*_, **__):
         ran.append(now[0])
-        raise Stop
+        raise _Stop
 
     monkeypatch.setattr(recurrent_block, "add_rmsnorm", add_rmsnorm)
     w = torch.zeros((8, 16), dtype=torch.bfloat16)
     block = recurrent_block.RecurrentBlock(recurrent_block.RecurrentBlockWeights(
         norm_w=None, w_x=w, b_x=None, w_gate=w, b_gate=None, lower=None, w_out=None, b_out=None))
-    with pytest.raises(Stop):
+    with pytest.raises(_Stop):
         block.prefill(w, None, None, [0, 8], [0], [1], stream=stream)
     assert ran == [where] and now == ["the caller's"]
+
+
+def test_the_scans_workspaces_are_taken_there_too(streams, monkeypatch, product_lib):
+    import workloads as W
+    asked = []
+
+    def workspace(need, given, device, stream):
+        asked.append((need > 0, given, stream))
+        raise _Stop
+
+    monkeypatch.setattr(ss, "_workspace", workspace)
+    d = W.DIMS_130M
+    z, x = torch.zeros((4096, d.d_inner), dtype=torch.bfloat16), torch.zeros((4096, d.conv_dim), dtype=torch.bfloat16)
+    state, batch = torch.zeros(1), ([0, 4096], [0], [1])
+    with pytest.raises(_Stop):
+        ss.ssd_scan(z, x, z, None, None, None, state, d, *batch, stream=0x7000)
+    with pytest.raises(_Stop):
+        ss.prefill_host(z, x, z, z, None, None, None, None, None, None, 1, 1e-5, state, state, d, *batch, stream=0x7000)
+    assert asked == [(True, None, 0x7000)] * 2
 
 
 @pytest.mark.gpu
