@@ -20,6 +20,7 @@ layer view built on them (attention mask in, HF-style cache out).
 from __future__ import annotations
 
 import array
+import contextlib
 import ctypes
 from pathlib import Path
 from typing import Optional, Sequence
@@ -201,8 +202,10 @@ def _same(name, t, shape, dtype=None):
 
 
 def _on(stream):
-    """Makes a stream (torch's, a raw handle, or another's by its ``cuda_stream``) torch's current one. Handle 0 is the
-    legacy default stream (of which ExternalStream would make a new stream)."""
+    """Makes a stream (torch's, a raw handle, or another's by its ``cuda_stream``) torch's current one; None leaves the
+    one that is. Handle 0 is the legacy default stream (of which ExternalStream would make a new stream)."""
+    if stream is None:
+        return contextlib.nullcontext()
     import torch
     if not isinstance(stream, torch.cuda.Stream):
         handle = _stream(stream)
@@ -218,11 +221,8 @@ def _workspace(need: int, workspace, device, stream):
         if need == 0:
             return None, 0, None
         import torch
-        if stream is None:
+        with _on(stream):
             workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        else:
-            with _on(stream):
-                workspace = torch.empty(need, dtype=torch.uint8, device=device)
     return _ptr(workspace), workspace.numel() * workspace.element_size(), workspace
 
 

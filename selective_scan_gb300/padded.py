@@ -13,7 +13,8 @@ packed rows, and the output is scattered back with zeros at padding
 (``mamba2_unpack_rows``). With left padding from an empty cache this is the same as
 zeroing the padded inputs and conv outputs and running every row whole: zero inputs
 keep a zero state at zero. Every step runs in libmamba2's kernels; this module only
-orders the calls and allocates the packed buffers with torch.
+orders the calls and allocates the packed buffers with torch, on the stream that they
+run on (``stream``, else the current one).
 """
 from __future__ import annotations
 
@@ -22,7 +23,7 @@ from typing import Optional
 
 import torch
 
-from . import (causal_conv1d, decode_step, gated_rmsnorm, pack_rows, padded_spans, ssd_scan,
+from . import (_on, causal_conv1d, decode_step, gated_rmsnorm, pack_rows, padded_spans, ssd_scan,
                ssd_scan_workspace_bytes, unpack_rows)
 
 
@@ -85,23 +86,24 @@ def forward(xBC, z, dt, weights: Mamba2Weights, dims, cache: Mamba2Cache,
     rows = cu[-1]
     dev, act = xBC.device, xBC.dtype
     fresh = [0 if cache.has_previous_state else 1] * batch
-    x_p = torch.empty((rows, xBC.shape[2]), dtype=act, device=dev)
-    z_p = torch.empty((rows, z.shape[2]), dtype=act, device=dev)
-    dt_p = torch.empty((rows, dt.shape[2]), dtype=act, device=dev)
-    for dst, src in ((x_p, xBC), (z_p, z), (dt_p, dt)):
-        pack_rows(dst, src.contiguous(), cu, first, stream=stream)
-    w = weights
-    xbc_p = torch.empty_like(x_p)
-    causal_conv1d(xbc_p, x_p, w.conv_w, w.conv_b, cache.conv_pool, cu, cache.slots, fresh, stream=stream)
-    y_p = torch.empty_like(z_p)
-    ws_bytes = ssd_scan_workspace_bytes(dims, rows, cu, cache.slots, fresh)
-    ws = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev) if ws_bytes else None
-    ssd_scan(y_p, xbc_p, dt_p, w.A_log, w.dt_bias, w.D, cache.ssm_pool, dims, cu, cache.slots, fresh,
-             workspace=ws, stream=stream)
-    out_p = torch.empty_like(z_p)
-    gated_rmsnorm(out_p, y_p, z_p, w.norm_w, w.norm_groups, w.eps, stream=stream)
-    out = torch.empty((batch, seqlen, z.shape[2]), dtype=act, device=dev)
-    unpack_rows(out, out_p, cu, first, stream=stream)
+    with _on(stream):
+        x_p = torch.empty((rows, xBC.shape[2]), dtype=act, device=dev)
+        z_p = torch.empty((rows, z.shape[2]), dtype=act, device=dev)
+        dt_p = torch.empty((rows, dt.shape[2]), dtype=act, device=dev)
+        for dst, src in ((x_p, xBC), (z_p, z), (dt_p, dt)):
+            pack_rows(dst, src.contiguous(), cu, first)
+        w = weights
+        xbc_p = torch.empty_like(x_p)
+        causal_conv1d(xbc_p, x_p, w.conv_w, w.conv_b, cache.conv_pool, cu, cache.slots, fresh)
+        y_p = torch.empty_like(z_p)
+        ws_bytes = ssd_scan_workspace_bytes(dims, rows, cu, cache.slots, fresh)
+        ws = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev) if ws_bytes else None
+        ssd_scan(y_p, xbc_p, dt_p, w.A_log, w.dt_bias, w.D, cache.ssm_pool, dims, cu, cache.slots, fresh,
+                 workspace=ws)
+        out_p = torch.empty_like(z_p)
+        gated_rmsnorm(out_p, y_p, z_p, w.norm_w, w.norm_groups, w.eps)
+        out = torch.empty((batch, seqlen, z.shape[2]), dtype=act, device=dev)
+        unpack_rows(out, out_p, cu, first)
     cache.has_previous_state = True
     cache.seqlen_offset = [o + cu[b + 1] - cu[b] for b, o in enumerate(cache.seqlen_offset)]
     return out
@@ -115,10 +117,10 @@ def decode(xBC, z, dt, weights: Mamba2Weights, dims, cache: Mamba2Cache, stream=
     batch = int(xBC.shape[0])
     fresh = [0 if cache.has_previous_state else 1] * batch
     w = weights
-    out = torch.empty((batch, z.shape[1]), dtype=z.dtype, device=z.device)
-    decode_step(out, xBC.contiguous(), z.contiguous(), dt.contiguous(), w.conv_w, w.conv_b, w.A_log, w.dt_bias,
-                w.D, w.norm_w, w.norm_groups, w.eps, cache.conv_pool, cache.ssm_pool, dims, cache.slots, fresh,
-                stream=stream)
+    with _on(stream):
+        out = torch.empty((batch, z.shape[1]), dtype=z.dtype, device=z.device)
+        decode_step(out, xBC.contiguous(), z.contiguous(), dt.contiguous(), w.conv_w, w.conv_b, w.A_log, w.dt_bias,
+                    w.D, w.norm_w, w.norm_groups, w.eps, cache.conv_pool, cache.ssm_pool, dims, cache.slots, fresh)
     cache.has_previous_state = True
     cache.seqlen_offset = [o + 1 for o in cache.seqlen_offset]
     return out

@@ -14,13 +14,12 @@ that their memory goes to no other stream's work.
 """
 from __future__ import annotations
 
-import contextlib
 from dataclasses import dataclass
 from typing import Optional
 
 import torch
 
-from . import (_on as _on_stream, add_rmsnorm, add_rmsnorm_backward, gated_recurrence, gated_recurrence_backward,
+from . import (_on, add_rmsnorm, add_rmsnorm_backward, gated_recurrence, gated_recurrence_backward,
                gated_recurrence_checkpoints, gated_recurrence_step_device, linear, linear_backward)
 
 E4M3 = torch.float8_e4m3fn
@@ -149,7 +148,3 @@ class RecurrentBlock:
             g["hidden"] = torch.empty_like(dout)
             add_rmsnorm_backward(g["hidden"], None, vector("norm_w", w.norm_w), dn, dout, saved.s, w.norm_w, w.eps)
             return g
-
-
-def _on(stream):
-    return contextlib.nullcontext() if stream is None else _on_stream(stream)

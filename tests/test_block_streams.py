@@ -110,6 +110,34 @@ def test_the_scans_workspaces_are_taken_there_too(streams, monkeypatch, product_
     assert asked == [(True, None, 0x7000)] * 2
 
 
+@pytest.mark.parametrize("stream,where", [(None, "the caller's"), (0x7000, ("external", 0x7000)), (0, "default")],
+                         ids=["none", "handle", "zero"])
+def test_the_layer_and_the_padded_batch_run_on_the_stream_that_they_are_given(streams, monkeypatch, product_lib, stream,
+                                                                              where):
+    """Their intermediates, and torch's copies of strided inputs, belong to the stream of the kernels that use them."""
+    import workloads as W
+    from selective_scan_gb300 import layer, padded
+    now, _ = streams
+    d, ran = W.DIMS_TINY, []
+
+    def kernel(*_, **__):
+        ran.append(now[0])
+        raise _Stop
+
+    for module, name in ((layer, "in_proj"), (padded, "pack_rows"), (padded, "decode_step")):
+        monkeypatch.setattr(module, name, kernel)
+    w = padded.Mamba2Weights(*[None] * 6)
+    one = layer.Mamba2Layer(torch.zeros((1, 8)), None, w, d)
+    x, z, dt = torch.zeros((2, 3, d.conv_dim)), torch.zeros((2, 3, d.d_inner)), torch.zeros((2, 3, d.heads))
+    for call in (lambda: one.prefill(x[0], None, None, [0, 3], [0], [1], stream=stream),
+                 lambda: one.decode(x[0], None, None, [0, 1, 2], stream=stream),
+                 lambda: padded.forward(x, z, dt, w, d, padded.Mamba2Cache(None, None, [0, 1]), stream=stream),
+                 lambda: padded.decode(x[:, 0], z[:, 0], dt[:, 0], w, d, padded.Mamba2Cache(None, None, [0, 1]), stream=stream)):
+        with pytest.raises(_Stop):
+            call()
+    assert ran == [where] * 4 and now == ["the caller's"]
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("form", ["stream", "handle", "default"])
 def test_operators_beside_a_current_stream_that_is_still_busy(form):
