@@ -209,7 +209,8 @@ size_t mamba2_linear_backward_workspace_bytes(int32_t rows, int32_t in_features,
  *   dx    [rows, in_features] bf16 or NULL
  *   dw    [out_features, in_features] bf16 or NULL
  *   dbias [out_features] f32 or NULL
- *   dy    [rows, out_features] bf16; pre likewise (NULL with MAMBA2_ACT_NONE)
+ *   dy    [rows, out_features] bf16, contiguous, also for a forward call with
+ *         an f32 out; pre likewise (NULL with MAMBA2_ACT_NONE)
  *   x     [rows, in_features] bf16, row stride ld_x; 16-byte aligned rows
  * in_features and ld_x multiples of 8 (MAMBA2_ERR_NOT_IMPLEMENTED otherwise).
  */

@@ -16,13 +16,15 @@
 // Few rows: the weight takes the instruction's 128 rows and the tokens its N, and a
 // cluster splits the K axis, see few_rows_kernel.
 //
-// Measured (GB300, bf16, in a graph): 16 384 x 2 048 x 4 096 with bias, SiLU and residual
-// 169 us (1 630 TFLOP/s, 86 % of the measured cuBLAS rate), without any of them 159; the
-// products alone, the epilogue's work left out, take 139 (1 980), so what remains is the last
-// tile's epilogue (6 us), the fill and what the epilogue takes from the products beside it.
-// e4m3 16 001 x 4 096 x 4 096 with residual 170 us (3 160 TFLOP/s). 5 x 2 048 x 8 192 8.0 us
-// (4.2 TB/s of weights). Both backward products of 8 192 x 2 048 x 4 096 154 us (1 790
-// TFLOP/s).
+// Measured (GB300, bf16, six calls in a graph on an idle GPU; in brackets without a pause, where
+// the power limit holds the clock down): 16 384 x 2 048 x 4 096 with bias, SiLU and residual
+// 171 us [197] (1 610 TFLOP/s, 84 % of the measured cuBLAS rate in bursts), without any of them
+// 158 [179], with `pre` too 182 [207], GELU 188 [208]; the products alone, the epilogue's work
+// left out, took 139 (1 980), so what remains is the last tile's epilogue (6 us), the fill and
+// what the epilogue takes from the products beside it. e4m3 16 001 x 4 096 x 4 096 with residual
+// 174 us [201] (3 090 TFLOP/s). Both backward products of 8 192 x 2 048 x 4 096 152 us [179]
+// (1 810 TFLOP/s). 5 x 2 048 x 8 192 9.5 us with weights from HBM (3.5 TB/s; 7.5 us with three
+// weights in turn, which L2 holds in good part), in e4m3 7.5 us (2.2 TB/s).
 //
 // Every mbarrier wait is bounded; a timeout stops the CTA's roles, drains what was
 // issued, frees tensor memory and counts the CTA in g_linear_timeouts.
@@ -899,7 +901,7 @@ cudaError_t launch_pairs(const Product& g, const void* x, int64_t ldx, const voi
 }
 
 // The most rows that the few-rows kernel takes: as long as the pairs' tiles would leave half of the SMs idle (K and N
-// of 2 048 and 4 096: 512 rows, 32 tiles, 15.8 us against 18.6 by pairs; 768 rows, 48 tiles, 22.9 against 18.8).
+// of 2 048 and 4 096: 512 rows, 32 tiles, 15.7 us against 17.1 by pairs; 768 rows, 48 tiles, 22.0 against 17.6).
 int few_rows_most(const Product& g) {
   const int64_t tiles = pair_tiles(g);
   return g.M <= 128 || 4 * tiles < device_sm_count() ? g.M : 0;
@@ -915,8 +917,8 @@ cudaError_t launch_few(const Product& g, const void* x, int64_t ldx, const void*
   if (e != cudaSuccess) return e;
   const int tiles_w = (g.N + 127) / 128, tiles_x = (g.M + kN - 1) / kN;
   const int kblocks = (g.K + (F8 ? 127 : 63)) / (F8 ? 128 : 64);
-  // as many parts of K as fill two CTAs an SM, each of two k-blocks at least (5 x 2 048 x 8 192: 4 parts 9.6 us, 2 10.0,
-  // 1 12.9, 7 13.7; 5 x 4 096 x 4 096: 8 parts 10.0, 2 13.2, 1 20.7)
+  // as many parts of K as fill two CTAs an SM, each of two k-blocks at least (weights from HBM, 5 x 2 048 x 8 192: 4 parts
+  // 9.5 us, 2 10.1, 1 13.0; 5 x 4 096 x 4 096: 8 and 4 parts 9.9 to 10.3, 2 13.1, 1 20.6)
   const int S = std::max(1, std::min({8, kblocks / 2, (int)(2 * (int64_t)device_sm_count() / ((int64_t)tiles_w * tiles_x))}));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)S, (unsigned)tiles_w, (unsigned)tiles_x);
@@ -950,7 +952,11 @@ cudaError_t launch_forward(const Product& g, const void* x, int64_t ldx, const v
 
 // dp = dy * activation'(pre) rounded to bf16, and the column sums of each kPartRows rows, unrounded. A CTA takes
 // 256 columns of them, a warp every eighth row, a lane 8 columns: adjacent ones where rows are 16-byte aligned,
-// else every 32nd. Bound by HBM: dy and pre in, dp out.
+// else every 32nd. Bound by HBM: dy and pre in, dp out
+// (with the bias's sums 36 us for 8 192 x 4 096 and GELU).
+// The rounding: the tensor cores take bf16 operands, as dy is, so dp carries one rounding more than its formula; dx and dw
+// are off by 2.35e-3 of their 2-norm instead of the 1.66e-3 of their own rounding alone. The bias's sums, which no product
+// takes, have none.
 constexpr int kPartRows = 64;
 constexpr int kPartCols = 256;
 

@@ -17,7 +17,7 @@
 // other warps, and the next tile's copies are in flight while a tile waits for its predecessors
 // (with one stage, while the others finish). Unaligned rows are shifted into place as they are
 // read, at a third more instructions: eight runs of 32 768 tokens in all by 2 047 channels of
-// bf16 take 128 us forwards and 212 backwards (by 2 048: 89 and 145).
+// bf16 take 121 us forwards and 207 backwards (by 2 048: 81 and 140).
 //
 // What precedes chunk l of a run, the same for any timing (so results repeat bit for bit):
 // every chunk publishes its map, and every 16th (0, 16, 32, ...) the state after it too (the
@@ -27,8 +27,8 @@
 // Maps are published without waiting for anything, and a state is used 16 (8, 4) chunks later
 // at the earliest: later than the tiles that the GPU holds at one time for wide matrices, so a
 // tile waits for maps alone. (With the nearest state it waited for the maps and
-// then for the state made from them: 232 us against 213 for one run of 65 536 tokens by 2 048
-// channels.) Chunk 0 alone reads the pool, so the run's last chunk may overwrite the slot.
+// then for the state made from them: 9 % more time for one run of 65 536 tokens by 2 048 channels
+// when this was chosen.) Chunk 0 alone reads the pool, so the run's last chunk may overwrite the slot.
 //
 // Tiles are taken by ticket in an order in which a tile's predecessors come first, so a
 // waiting tile's predecessors are always held by CTAs that run. Waits are bounded; one that
@@ -41,12 +41,12 @@
 // y, and unrounded), and makes dx and dgate in one more sweep over its tokens. dlower is
 // summed per tile and then over the tiles, in order.
 //
-// Measured (GB300, 65 536 tokens x 2 048 channels, bf16, with lower bounds and, forward, checkpoints): one run 195 us
-// forward (185 without checkpoints: 4.4 TB/s, 64 % of the measured copy rate) and 295 backward (4.6 TB/s); eight runs
-// 159 and 269, 64 runs 160 and 269; 512 runs, where nothing waits, 155 and 275. fp32 moves 5.8 TB/s either way. What
-// bounds it is issue: 954 instructions a warp and tile of one run forward (24 a token to scan, 7 to store) at 2.2 an
-// SM and clock, of which 59 us would remain if they were free; then, for few runs, the waits for maps of tiles that
-// run at the same time.
+// Measured (GB300, 65 536 tokens x 2 048 channels, bf16, with lower bounds and, forward, checkpoints): one run 189 us
+// forward (185 without checkpoints: 4.4 TB/s, 64 % of the measured copy rate) and 289 backward (4.8 TB/s); eight runs
+// 154 and 263, 64 runs 155 and 266; 512 runs, where nothing waits, 156 and 270. fp32, 65 536 x 1 024: 5.3 TB/s forward
+// and 5.6 backward for one run, 6.3 and 6.2 for 512. What bounds bf16 is latency: 54 % of the issue slots and 48 % of
+// HBM are active, and the largest share of a warp's time goes to a tile's two barriers of the whole CTA (3.1 of about 9
+// cycles an instruction for one run, where they cover the look-back; 2.0 where nothing is looked back at).
 #include <cuda.h>
 
 #include <algorithm>
@@ -73,7 +73,7 @@ constexpr int kMostShift = 4, kLeastShift = 2; // log2 of the chunks between two
 constexpr int kBack = (2 << kMostShift) / kWarps;  // maps that a warp looks back at, at most
 constexpr int kInfos = 4;
 // The thread that takes the next tile: of a warp that often has no maps to fetch (of the first one, with the nearest
-// maps, eight runs of 65 536 x 2 048 take 164 us instead of 159, backwards 281 instead of 269).
+// maps, eight runs of 65 536 x 2 048 took 3 % longer, backwards 4 %).
 constexpr int kTaker = 32 * 5;
 constexpr uint32_t kPollLimit = 1u << 21;      // polls before giving up (about a second)
 
@@ -162,7 +162,7 @@ __device__ __forceinline__ void unpack_word(uint32_t w, float (&v)[kCh<T>]) {
 // sigmoid(g) and sigmoid(-g) of each channel, each with its own digits: with a = exp(-g) they are 1 / (1 + a) and
 // a / (1 + a). a is kept at 2^126 at most, whose reciprocal is the least that is not flushed and stands for 0: `up`
 // is too large by that (below 2^-102 it counts), which what uses it takes off. (Of two exponentials and reciprocals a
-// channel instead: 210 us against 199 for one run of 65 536 tokens by 2 048 channels, backwards 332 against 309.)
+// channel instead: 6 % more time for one run of 65 536 tokens by 2 048 channels, backwards 7 %, when this was chosen.)
 constexpr float kLeast = 0x1p-126f;
 template <int C>
 __device__ __forceinline__ void both_sigmoids(const float (&g)[C], typename Pack<C>::V& up, typename Pack<C>::V& down) {
@@ -193,12 +193,12 @@ struct Info {
 };
 
 // The runs of a call. They are launch parameters, which take time to hand over by the byte, so there is a short form:
-// 300 tokens by 1 536 channels 15.3 us forwards and 21.4 backwards with it, 16.3 and 24.5 with the long one.
+// a call for 300 tokens by 1 536 channels took 1 us less forwards with it and 3 backwards (7.1 and 10.4 in a graph).
 //
 // Also the order in which the chunks of several runs are taken: runs in turns, each one's first chunk, then each
 // one's second, and so on, so that a chunk's predecessors are some time ago and few of them have to be waited for
-// (each run by itself, as the rows lie: 234 us against 184 for 64 runs of 65 536 tokens in all by 2 048 channels,
-// 212 against 177 for eight). Not more runs at a time than that takes, the longest first: what was published longer
+// (each run by itself, as the rows lie: 1.27 times the time for 64 runs of 65 536 tokens in all by 2 048 channels,
+// 1.20 times for eight, when this was chosen). Not more runs at a time than that takes, the longest first: what was published longer
 // ago has left L2.
 template <int kMost>
 struct Runs {
@@ -290,8 +290,8 @@ struct Stream {
 // This warp's rows of tile f of k matrices, kMat bytes apart, into the stage at st (wait_tile waits for them, with bar).
 // Where rows are 16-byte aligned, by TMA: rows past the run's end are other runs', or zeros, and nothing uses them. Else
 // 16 bytes a lane, each row from the 16-byte boundary before it to the one after it: what that adds shares its 16 bytes
-// with the row, so it can be read, and nothing uses it either. (8 runs, 32 768 x 2 046 bf16: 129 us; a bulk copy a row
-// 137 from all lanes and 153 from one; 4 bytes a lane, which can place a row at its word, was slower than those.)
+// with the row, so it can be read, and nothing uses it either. (8 runs, 32 768 x 2 046 bf16: 118 us; a bulk copy a row
+// took 6 % longer from all lanes and 19 % from one; 4 bytes a lane, which can place a row at its word, longer still.)
 template <typename T, bool kVec, int k>
 __device__ __forceinline__ void load_tile(const Info& f, const Stream<T> (&m)[k], uint32_t st, uint32_t bar, int dim,
                                           int warp, int lane) {
@@ -498,7 +498,7 @@ struct Before {
 };
 // This warp's share: the maps of the chunks kBack warp + 1 .. kBack (warp + 1) before the tile as far as there
 // are k, composed; and the state: a warp that has no maps where states are frequent, else the first (eight runs
-// of 65 536 tokens by 2 048 channels 164 us against 166 with the first; one run 197 against 203 with the other).
+// of 65 536 tokens by 2 048 channels took 1 % longer with the first, one run 3 % longer with the other).
 template <typename T, bool kReverse>
 __device__ __forceinline__ void look_back(const Chain& ch, const Info& f, int first, int groups, int k,
                                           Before<T>& out, int warp, int lane) {
@@ -754,9 +754,9 @@ rec_fwd_kernel(const __grid_constant__ RecTensors a, const __grid_constant__ Run
 // ------------------------------------------------------------------ backward
 
 // One stage, so that three CTAs fit an SM (the gates are made twice for that, too: kept, they take the registers of
-// the third): 320 us against 337 for one run of 65 536 tokens by 2 048 channels with two stages and two CTAs. (A
-// tile taken further ahead is waited for longer: with the next tile's ticket taken and its rows fetched into L2
-// meanwhile it was 385.)
+// the third). Against two stages and two CTAs, 65 536 tokens by 2 048 channels: one run 289 us and 305, eight 263 and 266,
+// 512 270 and 262. (A tile taken further ahead is waited for longer: with the next tile's ticket taken and its rows fetched
+// into L2 meanwhile one run took a fifth longer.)
 constexpr int kBwdStages = 1;
 template <bool kVec> constexpr int kBwdStage = 3 * kChunkR * kPitch<kVec>;
 
@@ -1147,8 +1147,8 @@ bool make_map(CUtensorMap* tm, const void* base, int64_t rows, int64_t dim, int6
 }
 
 int64_t tiles_at_once() { return (int64_t)kCtas * device_sm_count(); }
-// Runs whose chunks are taken in turns: as many as fill the GPU (64 runs of 65 536 x 2 048: 166 us, 169 with twice and
-// 177 with four times as many).
+// Runs whose chunks are taken in turns: as many as fill the GPU (64 runs of 65 536 x 2 048 took 2 % longer with twice and
+// 7 % with four times as many).
 int runs_in_turn(int64_t groups) { return (int)((tiles_at_once() + groups - 1) / groups); }
 // log2 of the chunks between two published states: as few as keep a state's readers a wave of tiles behind it (the
 // fewer, the fewer maps to read and fold). runs: those in turn, on average.

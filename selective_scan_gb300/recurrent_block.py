@@ -8,9 +8,9 @@ projection that adds the stream back:
 
 ``prefill`` and ``decode`` serve (the latter from a batch in device memory, so that a captured CUDA graph can be
 replayed); ``forward`` and ``backward`` train. With 8-bit input projections the norm writes its rows in e4m3 with a
-scale each, and they take them as they are. Every step runs in libmamba2's kernels; this module orders the calls
-and allocates the intermediates with torch, on the stream that they run on (``stream``, else the current one), so
-that their memory goes to no other stream's work.
+scale each, and they take them as they are. Every step runs in libmamba2's kernels, but for the addition of two
+gradients in ``backward``, which is torch's; this module orders the calls and allocates the intermediates with torch,
+on the stream that they run on (``stream``, else the current one), so that their memory goes to no other stream's work.
 """
 from __future__ import annotations
 
@@ -144,7 +144,7 @@ class RecurrentBlock:
             g["w_x"], g["w_gate"] = torch.empty_like(w.w_x), torch.empty_like(w.w_gate)
             linear_backward(dn, g["w_x"], vector("b_x", w.b_x), dx, saved.n, w.w_x, activation="silu", pre=saved.pre_x)
             linear_backward(dn_gate, g["w_gate"], vector("b_gate", w.b_gate), dgate, saved.n, w.w_gate)
-            dn += dn_gate
+            dn += dn_gate  # (in bf16: each product's gradient is rounded, and their sum)
             g["hidden"] = torch.empty_like(dout)
             add_rmsnorm_backward(g["hidden"], None, vector("norm_w", w.norm_w), dn, dout, saved.s, w.norm_w, w.eps)
             return g
