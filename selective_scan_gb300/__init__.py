@@ -14,7 +14,9 @@ Entry points (same names as the C ABI without the ``mamba2_`` prefix):
 ``mamba3_siso_varlen_forward`` (C name unchanged). The operators of the recurrent block
 (``include/block.h``): ``add_rmsnorm``, ``linear`` and ``gated_recurrence``, each with its
 ``_backward``, and ``gated_recurrence_step`` / ``gated_recurrence_step_device``;
-``selective_scan_gb300.recurrent_block`` runs them together. ``selective_scan_gb300.padded`` holds the padded-batch
+``selective_scan_gb300.recurrent_block`` runs them together. The gated delta rule (``include/delta.h``):
+``gated_delta_rule``, its ``_step``, ``_step_device`` and ``_backward``. Beam search over recurrent states
+(``include/beam.h``): ``beam_select`` and ``reorder_states``. ``selective_scan_gb300.padded`` holds the padded-batch
 layer view built on them (attention mask in, HF-style cache out).
 """
 from __future__ import annotations
@@ -36,6 +38,8 @@ RECURRENCE_STEP, RECURRENCE_CHUNK = 16, 128
  ERR_NOT_IMPLEMENTED, ERR_CUDA, ERR_WORKSPACE_TOO_SMALL) = range(8)
 MAX_SEQS = 1024
 MAX_BLOCK_SIZE = 0x7fff0000  # most rows and columns of the recurrent block's operators
+DELTA_CHUNK = 64  # tokens between two checkpoints of the gated delta rule
+MAX_BEAMS = 32  # beams of a sequence, and candidates that are kept of it
 
 
 class Mamba2Error(RuntimeError):
@@ -117,6 +121,21 @@ def _lib():
         lib.mamba2_linear_backward_workspace_bytes.argtypes = [i32, i32, i32]
         lib.mamba2_linear_backward_workspace_bytes.restype = sz
         lib.mamba2_linear_backward.argtypes = [p] * 7 + [i32, i32, i32, i64, act, p, sz, p]
+        lib.mamba2_gated_delta_rule_checkpoints.argtypes = [p, i32]
+        lib.mamba2_gated_delta_rule_checkpoints.restype = i64
+        lib.mamba2_gated_delta_rule_workspace_bytes.argtypes = [p, i32, dims, act, i32]
+        lib.mamba2_gated_delta_rule_workspace_bytes.restype = sz
+        lib.mamba2_gated_delta_rule.argtypes = [p] * 8 + [i32, i32, i64, i64, i64, i64, dims, f32, f32, act, rb, p, sz, p]
+        lib.mamba2_gated_delta_rule_step.argtypes = [p] * 7 + [i32, i64, i64, i64, i64, dims, f32, f32, act, rb, p]
+        lib.mamba2_gated_delta_rule_step_device.argtypes = [p] * 7 + [i32, i64, i64, i64, i64, dims, f32, f32, act, p, p,
+                                                                      p, i32, p, p]
+        lib.mamba2_beam_select_workspace_bytes.argtypes = [i32, i32, i32, i32]
+        lib.mamba2_beam_select_workspace_bytes.restype = sz
+        lib.mamba2_beam_select.argtypes = [p] * 7 + [i32, i32, i32, i32, i64, i32, act, p, sz, p]
+        lib.mamba2_reorder_states.argtypes = [p, p, i32, i32, p, p, i32, i32, p, p]
+        for name in ("mamba2_gated_delta_rule", "mamba2_gated_delta_rule_step", "mamba2_gated_delta_rule_step_device",
+                     "mamba2_beam_select", "mamba2_reorder_states"):
+            getattr(lib, name).restype = ctypes.c_int
         for name in ("mamba2_gated_recurrence", "mamba2_gated_recurrence_step", "mamba2_gated_recurrence_step_device",
                      "mamba2_gated_recurrence_backward", "mamba2_add_rmsnorm", "mamba2_add_rmsnorm_backward",
                      "mamba2_linear", "mamba2_linear_backward"):
@@ -692,6 +711,171 @@ def linear_backward(dx, dw, dbias, dy, x, w, activation="none", pre=None, worksp
                                        lx, ACTIVATIONS[activation], ws, ws_bytes, _stream(stream))
     if check:
         _check(st, "mamba2_linear_backward")
+    return st
+
+
+def _heads(name, t, heads, width, rows, dtype):
+    """(pointer, row stride) of a [rows, heads, width] tensor whose heads are contiguous: a contiguous one, or a column
+    range of a wider matrix's rows split into heads."""
+    if t.shape != (rows, heads, width) or t.dtype != dtype:
+        _same(name, t, (rows, heads, width), dtype)
+    ld, per, one = t.stride()
+    if (width > 1 and one != 1) or (heads > 1 and per != width):
+        raise ValueError(f"{name}: a row's heads must be contiguous")
+    if rows <= 1:
+        ld = heads * width
+        ld += -ld % 8  # (of one row, whatever the library takes)
+    elif ld < heads * width:
+        raise ValueError(f"{name}: rows overlap")
+    return t.data_ptr(), ld
+
+
+def _delta(y, q, k, v, g, beta, state, scale, l2_eps):
+    """What the gated delta rule's forward calls pass on: pointers, strides, dims, scale and l2_eps."""
+    (rows, heads, headdim), (groups, d_state) = v.shape, q.shape[1:]
+    _alike(v, (), (("g", g, (rows, heads)), ("beta", beta, (rows, heads)),
+                   ("state", state, (state.shape[0], heads, headdim, d_state))))
+    (yp, ly), (vp, lv) = _heads("y", y, heads, headdim, rows, v.dtype), _heads("v", v, heads, headdim, rows, v.dtype)
+    (qp, lq), (kp, lk) = (_heads(n, t, groups, d_state, rows, v.dtype) for n, t in (("q", q), ("k", k)))
+    return ((yp, qp, kp, vp, _ptr(g), _ptr(beta), _ptr(state)), (ly, lq, lk, lv),
+            Dims(heads, headdim, d_state, groups, 1), d_state ** -0.5 if scale is None else float(scale),
+            -1.0 if l2_eps is None else _l2_eps(l2_eps))
+
+
+def _l2_eps(eps):
+    if not eps >= 0:
+        raise ValueError(f"l2_eps: expected a number >= 0 or None, got {eps}")
+    return float(eps)
+
+
+def gated_delta_rule_checkpoints(cu_seqlens) -> int:
+    """``mamba2_gated_delta_rule_checkpoints``: the states that ``checkpoints`` of a batch with these runs holds."""
+    cu = _cu(cu_seqlens)
+    n = int(_lib().mamba2_gated_delta_rule_checkpoints(cu, len(cu) - 1))
+    if n < 0:
+        raise Mamba2Error(ERR_RUNS_DONT_COVER_ROWS, "mamba2_gated_delta_rule_checkpoints")
+    return n
+
+
+def gated_delta_rule_workspace_bytes(cu_seqlens, heads, headdim, d_state, groups, dtype, backward=False) -> int:
+    """``mamba2_gated_delta_rule_workspace_bytes`` of the forward or backward call with tensors of this type."""
+    import torch
+    cu, d = _cu(cu_seqlens), Dims(int(heads), int(headdim), int(d_state), int(groups), 1)
+    act = BF16 if dtype == torch.bfloat16 else F32
+    return int(_lib().mamba2_gated_delta_rule_workspace_bytes(cu, len(cu) - 1, ctypes.byref(d), act, 1 if backward else 0))
+
+
+def gated_delta_rule(y, q, k, v, g, beta, state, cu_seqlens=None, slots=None, fresh=None, scale=None, l2_eps=None,
+                     checkpoints=None, workspace=None, stream=None, check=True, batch=None) -> int:
+    """``mamba2_gated_delta_rule`` over packed runs: S_t = a_t S_{t-1} + u_t k_t^T with a_t = exp(g_t) and
+    u_t = beta_t (v_t - a_t S_{t-1} k_t), y_t = scale S_t q_t; ``state`` [slots, heads, headdim, d_state] f32 updated at
+    the slots. q, k [rows, groups, d_state] and v, y [rows, heads, headdim] may be column ranges of wider matrices; g
+    (log decay) and beta [rows, heads] f32 may be None (no decay, 1). ``scale`` is d_state ** -0.5 unless given;
+    ``l2_eps`` divides every key and query by its length first. ``checkpoints`` [gated_delta_rule_checkpoints(
+    cu_seqlens), heads, headdim, d_state] f32 is for the backward pass."""
+    b = _batch(cu_seqlens, slots, fresh, batch)
+    (yp, qp, kp, vp, gp, bp, sp), strides, d, scale, eps = _delta(y, q, k, v, g, beta, state, scale, l2_eps)
+    if checkpoints is not None and b.cu is not None:
+        _same("checkpoints", checkpoints, (gated_delta_rule_checkpoints(b.cu),) + state.shape[1:], _float32())
+    need = 0
+    if workspace is None and b.cu is not None:
+        need = int(_lib().mamba2_gated_delta_rule_workspace_bytes(b.cu, len(b.cu) - 1, ctypes.byref(d), _dt(v), 0))
+    ws, ws_bytes, _keep = _workspace(need, workspace, v.device, stream)
+    st = _lib().mamba2_gated_delta_rule(yp, _ptr(checkpoints), qp, kp, vp, gp, bp, sp, state.shape[0], v.shape[0],
+                                        *strides, ctypes.byref(d), scale, eps, _dt(v), b.ref(), ws, ws_bytes,
+                                        _stream(stream))
+    if check:
+        _check(st, "mamba2_gated_delta_rule")
+    return st
+
+
+def gated_delta_rule_step(y, q, k, v, g, beta, state, slots=None, fresh=None, cu_seqlens=None, scale=None, l2_eps=None,
+                          stream=None, check=True, batch=None) -> int:
+    """``mamba2_gated_delta_rule_step``: one token per sequence."""
+    b = _batch(cu_seqlens, slots, fresh, batch)
+    _same("v", v, (b.rb.num_seqs,) + v.shape[1:])
+    ptrs, strides, d, scale, eps = _delta(y, q, k, v, g, beta, state, scale, l2_eps)
+    st = _lib().mamba2_gated_delta_rule_step(*ptrs, state.shape[0], *strides, ctypes.byref(d), scale, eps, _dt(v),
+                                             b.ref(), _stream(stream))
+    if check:
+        _check(st, "mamba2_gated_delta_rule_step")
+    return st
+
+
+def gated_delta_rule_step_device(y, q, k, v, g, beta, state, slots_dev, fresh_dev, num_seqs_dev, status_dev, scale=None,
+                                 l2_eps=None, stream=None, check=True) -> int:
+    """``mamba2_gated_delta_rule_step_device``: the step with its batch in device memory, as ``decode_step_device``
+    takes it (``fresh_dev`` may be None: no sequence is fresh)."""
+    import torch
+    cap, i32 = slots_dev.shape[0], torch.int32
+    if (v.shape[0] != cap or slots_dev.dtype != i32 or num_seqs_dev.dtype != i32 or status_dev.dtype != i32 or
+            num_seqs_dev.numel() != 1 or status_dev.numel() != 1 or slots_dev.dim() != 1 or
+            (fresh_dev is not None and (fresh_dev.dtype != torch.uint8 or fresh_dev.shape != (cap,)))):
+        _same("v", v, (cap,) + v.shape[1:])
+        _same("slots_dev", slots_dev, (cap,), i32)
+        _same("fresh_dev", fresh_dev, (cap,), torch.uint8)
+        _same("num_seqs_dev", num_seqs_dev, (1,), i32)
+        _same("status_dev", status_dev, (1,), i32)
+    ptrs, strides, d, scale, eps = _delta(y, q, k, v, g, beta, state, scale, l2_eps)
+    st = _lib().mamba2_gated_delta_rule_step_device(*ptrs, state.shape[0], *strides, ctypes.byref(d), scale, eps, _dt(v),
+                                                    _ptr(slots_dev), _ptr(fresh_dev), _ptr(num_seqs_dev), cap,
+                                                    _ptr(status_dev), _stream(stream))
+    if check:
+        _check(st, "mamba2_gated_delta_rule_step_device")
+    return st
+
+
+def beam_select(scores_out, parents, tokens, logits, scores, finished=None, finished_out=None, eos=None, workspace=None,
+                stream=None, check=True) -> int:
+    """``mamba2_beam_select``: of every sequence's beams x vocabulary the largest ``scores + log_softmax(logits)``, equal
+    ones by beam, then token. ``logits`` [batch * beams, vocab] (rows may be column ranges of a wider matrix), ``scores``
+    [batch, beams] f32; ``scores_out`` f32, ``parents`` and ``tokens`` int32 [batch, out]. With ``eos``, beams that
+    ``finished`` [batch, beams] uint8 names go on as they are, and ``finished_out`` [batch, out] tells which have ended."""
+    import torch
+    (batch, beams), (rows, vocab), out = scores.shape, logits.shape, scores_out.shape[1]
+    if rows != batch * beams:
+        _same("logits", logits, (batch * beams, vocab))
+    for name, t, shape, dtype in (("scores", scores, (batch, beams), torch.float32), ("scores_out", scores_out, (batch, out), torch.float32),
+                                  ("parents", parents, (batch, out), torch.int32), ("tokens", tokens, (batch, out), torch.int32),
+                                  ("finished", finished, (batch, beams), torch.uint8),
+                                  ("finished_out", finished_out, (batch, out), torch.uint8)):
+        if t is not None and (t.shape != shape or t.dtype != dtype):
+            _same(name, t, shape, dtype)
+    if eos is not None and not 0 <= eos < vocab:
+        raise ValueError(f"eos: expected a token below {vocab} or None, got {eos}")
+    (lp, ld), act = _rows(logits), _dt(logits)
+    need = int(_lib().mamba2_beam_select_workspace_bytes(batch, beams, out, vocab)) if workspace is None else 0
+    ws, ws_bytes, _keep = _workspace(need, workspace, logits.device, stream)
+    st = _lib().mamba2_beam_select(_ptr(scores_out), _ptr(parents), _ptr(tokens), _ptr(finished_out), lp, _ptr(scores),
+                                   _ptr(finished), batch, beams, out, vocab, ld, -1 if eos is None else int(eos),
+                                   act, ws, ws_bytes, _stream(stream))
+    if check:
+        _check(st, "mamba2_beam_select")
+    return st
+
+
+def reorder_states(pools, slots, parents, status_dev, stream=None, check=True) -> int:
+    """``mamba2_reorder_states``: in every pool [num_slots, ...] (of any type) at once, the slot of each beam takes the
+    state that its parent's had: pool[slots[b, j]] = pool[slots[b, parents[b, j]]]. ``slots`` and ``parents`` [batch,
+    beams] and ``status_dev`` (one element) are int32 device tensors, checked on the device: ``status_dev`` holds the
+    outcome once the stream has passed the call."""
+    import torch
+    pools = list(pools)
+    batch, beams = slots.shape
+    for name, t in (("slots", slots), ("parents", parents)):
+        _same(name, t, (batch, beams), torch.int32)
+    _same("status_dev", status_dev, (1,), torch.int32)
+    num_slots = int(pools[0].shape[0]) if pools else 0
+    for i, t in enumerate(pools):
+        if t.shape[0] != num_slots:
+            raise ValueError(f"pool {i}: expected {num_slots} slots, got {t.shape[0]}")
+    n = len(pools)
+    ptrs = (ctypes.c_void_p * max(n, 1))(*map(_ptr, pools))
+    sizes = (ctypes.c_int64 * max(n, 1))(*(t.numel() // max(num_slots, 1) * t.element_size() for t in pools))
+    st = _lib().mamba2_reorder_states(ptrs, sizes, n, num_slots, _ptr(slots), _ptr(parents), batch, beams,
+                                      _ptr(status_dev), _stream(stream))
+    if check:
+        _check(st, "mamba2_reorder_states")
     return st
 
 

@@ -258,6 +258,66 @@ cudaError_t launch_linear_backward(const LinearBwdArgs& a, int act, cudaStream_t
 unsigned int read_linear_timeouts();
 unsigned int read_recurrence_timeouts();
 
+// ------------------------------------------------------ gated delta rule ----
+// Packed runs (delta.h). tab.tile[i] = the sequence's first chunk of MAMBA2_DELTA_CHUNK tokens.
+struct DeltaTensors {
+  void* y;
+  float* ckpt;  // [chunks, heads, dv, dk] or null
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* g;     // [rows, heads] or null
+  const float* beta;  // [rows, heads] or null
+  float* state;       // [num_slots, heads, dv, dk]
+  int32_t heads, groups, dv, dk;
+  int64_t ld_y, ld_q, ld_k, ld_v;
+  float scale, l2_eps;
+};
+struct DeltaArgs : DeltaTensors {
+  SeqTable tab;
+};
+cudaError_t launch_delta_serial(const DeltaArgs& a, mamba2_dtype act, cudaStream_t st);
+
+struct DeltaStepArgs : DeltaTensors {  // (ckpt unused)
+  int32_t n;  // sequences, or the capacity of a device batch
+  int32_t num_slots;
+  const int32_t* dev_slots;  // device batch (null for a host batch), as in DecodeArgs
+  const uint8_t* dev_fresh;
+  const int32_t* dev_n;
+  int32_t* dev_status;
+  uint32_t slot_fresh[MAMBA2_MAX_SEQS];
+};
+// Checks a device batch too (in the kernel, or by launch_check_device_batch).
+cudaError_t launch_delta_step(const DeltaStepArgs& a, mamba2_dtype act, cudaStream_t st);
+
+// ------------------------------------------------------------ beams ----
+struct BeamArgs {
+  float* scores_out;
+  int32_t* parents;
+  int32_t* tokens;
+  uint8_t* finished_out;
+  const void* logits;
+  const float* scores;
+  const uint8_t* finished;
+  int32_t batch, beams, out, vocab, eos;
+  int64_t ld;
+  void* ws;
+};
+size_t beam_workspace(int64_t rows, int32_t out, int32_t vocab);
+cudaError_t launch_beam_select(const BeamArgs& a, mamba2_dtype act, cudaStream_t st);
+
+struct ReorderArgs {
+  int32_t num_pools, num_slots, batch, beams;
+  const int32_t* slots;
+  const int32_t* parents;
+  int32_t* status;
+  char* pool[64];
+  int64_t bytes[64];  // of a slot
+  int32_t tile[65];   // first work tile of the pool (kReorderTile bytes of every beam's slot)
+};
+constexpr int kReorderTile = 4096;
+cudaError_t launch_reorder(const ReorderArgs& a, cudaStream_t st);
+
 // ------------------------------------------------------------ mamba3 ----
 // Mamba-3 SISO varlen forward (head width 64, Q/K width 128). Sequence i owns
 // rows [cu[i], cu[i+1]); order[] lists the sequences longest first (the CTAs

@@ -63,6 +63,7 @@ __device__ unsigned int g_recurrence_timeouts = 0;
 
 namespace {
 
+#include "batch_check.cuh"
 #include "tc.cuh"
 
 constexpr int kChunkR = MAMBA2_RECURRENCE_CHUNK;
@@ -979,34 +980,6 @@ rec_bwd_kernel(const __grid_constant__ RecBwdTensors a, const __grid_constant__ 
 // CTA itself before it touches anything, instead of by a kernel of its own.
 constexpr int kStepThreads = 256;
 constexpr int kCheckHere = kStepThreads;
-constexpr int kSeenWords = 1024;  // slots that a bitmap in shared memory holds: 32 times as many
-
-// The status of a device batch, as launch_check_device_batch finds it: the count, then the slots' range, then
-// whether two sequences share one. mine: the slot of sequence threadIdx.x. All threads of the CTA call it and get
-// the same answer. A pool of more slots than the bitmap holds is compared pair by pair.
-__device__ __forceinline__ int check_batch(int num, int capacity, int num_slots, int mine) {
-  __shared__ uint32_t seen[kSeenWords];
-  if (num < 0 || num > capacity) return MAMBA2_ERR_INVALID_ARGUMENT;
-  const int me = (int)threadIdx.x;
-  const bool in = me < num, small = num_slots <= 32 * kSeenWords;
-  int bad = in && (mine < 0 || mine >= num_slots) ? 1 : 0;
-  if (small) {
-    for (int w = me; w < (num_slots + 31) / 32; w += kStepThreads) seen[w] = 0u;
-    __syncthreads();
-    if (in && !bad) {
-      const uint32_t bit = 1u << (mine & 31);
-      if (atomicOr(&seen[mine >> 5], bit) & bit) bad = 2;
-    }
-  } else {
-    seen[me] = (uint32_t)mine;
-    __syncthreads();
-    if (in)
-      for (int j = 0; j < me; ++j)
-        if (seen[j] == (uint32_t)mine) bad |= 2;
-  }
-  if (__syncthreads_or(bad & 1)) return MAMBA2_ERR_SLOT_OUT_OF_RANGE;
-  return __syncthreads_or(bad) ? MAMBA2_ERR_SLOT_SHARED : MAMBA2_OK;
-}
 
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kStepThreads) rec_step_kernel(const __grid_constant__ RecStepArgs a) {
@@ -1075,7 +1048,7 @@ __global__ void __launch_bounds__(kStepThreads) rec_step_kernel(const __grid_con
   }
   if (a.dev_slots) {
     if (a.n <= kCheckHere) {
-      const int status = check_batch(num, a.n, a.num_slots, mine);
+      const int status = check_batch<kStepThreads>(num, a.n, a.num_slots, mine);
       if (blockIdx.x == 0 && i == 0 && threadIdx.x == 0) *a.dev_status = status;
       if (status != MAMBA2_OK) return;
     } else if (*a.dev_status != MAMBA2_OK) {
