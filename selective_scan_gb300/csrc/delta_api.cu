@@ -98,8 +98,10 @@ int64_t mamba2_gated_delta_rule_checkpoints(const int32_t* cu_seqlens, int32_t n
 size_t mamba2_gated_delta_rule_workspace_bytes(const int32_t* cu_seqlens, int32_t num_seqs, const mamba2_dims* dims,
                                                mamba2_dtype act, int32_t backward) {
   (void)backward;
-  if (!act_ok(act) || delta_dims(dims) != MAMBA2_OK || !cu_ok(cu_seqlens, num_seqs)) return 0;
-  return 0;
+  if (!act_ok(act) || delta_dims(dims) != MAMBA2_OK || !cu_ok(cu_seqlens, num_seqs) ||
+      !delta_chunked_supported(act, dims->headdim, dims->d_state))
+    return 0;
+  return (delta_workspace(count_chunks(cu_seqlens, num_seqs), dims->heads) + 255) / 256 * 256;
 }
 
 mamba2_status mamba2_gated_delta_rule(void* y, float* checkpoints, const void* q, const void* k, const void* v,
@@ -126,7 +128,8 @@ mamba2_status mamba2_gated_delta_rule(void* y, float* checkpoints, const void* q
   a.ckpt = checkpoints;
   fill_table(a.tab, rb);
   fill_chunks(a.tab);
-  return done(launch_delta_serial(a, act, static_cast<cudaStream_t>(stream)));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return done(delta_chunked_supported(act, a.dv, a.dk) ? launch_delta_chunked(a, workspace, st) : launch_delta_serial(a, act, st));
 }
 
 namespace {

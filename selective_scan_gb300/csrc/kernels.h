@@ -277,6 +277,10 @@ struct DeltaArgs : DeltaTensors {
   SeqTable tab;
 };
 cudaError_t launch_delta_serial(const DeltaArgs& a, mamba2_dtype act, cudaStream_t st);
+// Whether the chunked kernels take this shape, and their workspace.
+bool delta_chunked_supported(mamba2_dtype act, int dv, int dk);
+size_t delta_workspace(int64_t chunks, int heads);
+cudaError_t launch_delta_chunked(const DeltaArgs& a, void* ws, cudaStream_t st);
 
 struct DeltaStepArgs : DeltaTensors {  // (ckpt unused)
   int32_t n;  // sequences, or the capacity of a device batch
