@@ -89,6 +89,37 @@ mamba2_status mamba2_gated_delta_rule_step_device(void* y, const void* q, const 
                                                   const uint8_t* fresh_dev, const int32_t* num_seqs_dev,
                                                   int32_t capacity, int32_t* status_dev, void* stream);
 
+/*
+ * Gradients of the forward call, from the checkpoints that it wrote. With G_t
+ * the gradient that reaches S_t: G_t = scale dy_t q_t^T + (a_{t+1} G_{t+1} -
+ * a_{t+1} dv_{t+1} k_{t+1}^T), the last one plus dstate_end;
+ *   dv_t = beta_t G_t k_t,  dbeta_t = (G_t k_t) . (v_t - a_t S_{t-1} k_t),
+ *   dq_t = scale dy_t^T S_t,  dk_t = u_t^T G_t - a_t dv_t^T S_{t-1} (both
+ *   summed over the group's heads, and carried through the division by their
+ *   lengths),  dg_t = <G_t - dv_t k_t^T, a_t S_{t-1}>,
+ *   dstate = a_0 (G_0 - dv_0 k_0^T) (dstate_end itself for a run of no rows).
+ * For bf16, with d_state and headdim of at most 128; MAMBA2_ERR_NOT_IMPLEMENTED
+ * otherwise. Operands of the products that end in dq, dk, dg and dbeta are
+ * rounded to bf16; dv and dstate come from operands of twice its digits.
+ *
+ *   dq, dk    [rows, ngroups, d_state] act, row strides ld_dq, ld_dk
+ *   dv        [rows, heads, headdim] act, row stride ld_dv
+ *   dg, dbeta [rows, heads] act, contiguous, or NULL (also of a g or beta that
+ *             is NULL)
+ *   dstate    [num_seqs, heads, headdim, d_state] f32 or NULL: of each run's
+ *             initial state (also written for fresh runs, whose state was zero)
+ *   dy        [rows, heads, headdim] act, row stride ld_dy
+ *   dstate_end  as dstate, or NULL (zero)
+ */
+mamba2_status mamba2_gated_delta_rule_backward(void* dq, void* dk, void* dv, void* dg, void* dbeta, float* dstate,
+                                               const void* dy, const float* dstate_end, const void* q, const void* k,
+                                               const void* v, const float* g, const float* beta,
+                                               const float* checkpoints, int32_t rows, int64_t ld_dq, int64_t ld_dk,
+                                               int64_t ld_dv, int64_t ld_dy, int64_t ld_q, int64_t ld_k, int64_t ld_v,
+                                               const mamba2_dims* dims, float scale, float l2_eps, mamba2_dtype act,
+                                               const int32_t* cu_seqlens, int32_t num_seqs, void* workspace,
+                                               size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

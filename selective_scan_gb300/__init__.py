@@ -129,12 +129,13 @@ def _lib():
         lib.mamba2_gated_delta_rule_step.argtypes = [p] * 7 + [i32, i64, i64, i64, i64, dims, f32, f32, act, rb, p]
         lib.mamba2_gated_delta_rule_step_device.argtypes = [p] * 7 + [i32, i64, i64, i64, i64, dims, f32, f32, act, p, p,
                                                                       p, i32, p, p]
+        lib.mamba2_gated_delta_rule_backward.argtypes = [p] * 14 + [i32] + [i64] * 7 + [dims, f32, f32, act, p, i32, p, sz, p]
         lib.mamba2_beam_select_workspace_bytes.argtypes = [i32, i32, i32, i32]
         lib.mamba2_beam_select_workspace_bytes.restype = sz
         lib.mamba2_beam_select.argtypes = [p] * 7 + [i32, i32, i32, i32, i64, i32, act, p, sz, p]
         lib.mamba2_reorder_states.argtypes = [p, p, i32, i32, p, p, i32, i32, p, p]
         for name in ("mamba2_gated_delta_rule", "mamba2_gated_delta_rule_step", "mamba2_gated_delta_rule_step_device",
-                     "mamba2_beam_select", "mamba2_reorder_states"):
+                     "mamba2_gated_delta_rule_backward", "mamba2_beam_select", "mamba2_reorder_states"):
             getattr(lib, name).restype = ctypes.c_int
         for name in ("mamba2_gated_recurrence", "mamba2_gated_recurrence_step", "mamba2_gated_recurrence_step_device",
                      "mamba2_gated_recurrence_backward", "mamba2_add_rmsnorm", "mamba2_add_rmsnorm_backward",
@@ -822,6 +823,37 @@ def gated_delta_rule_step_device(y, q, k, v, g, beta, state, slots_dev, fresh_de
                                                     _ptr(status_dev), _stream(stream))
     if check:
         _check(st, "mamba2_gated_delta_rule_step_device")
+    return st
+
+
+def gated_delta_rule_backward(dq, dk, dv, dg, dbeta, dstate, dy, dstate_end, q, k, v, g, beta, checkpoints, cu_seqlens,
+                              scale=None, l2_eps=None, workspace=None, stream=None, check=True) -> int:
+    """``mamba2_gated_delta_rule_backward``: gradients of q, k, v, g, beta and the initial states (``dg``, ``dbeta``,
+    ``dstate`` and ``dstate_end`` may be None) from the forward call's checkpoints, for bf16. ``dg`` and ``dbeta``
+    [rows, heads] have the type of v."""
+    (rows, heads, headdim), (groups, d_state), cu = v.shape, q.shape[1:], _cu(cu_seqlens)
+    n, f32 = len(cu) - 1, _float32()
+    ends = (n, heads, headdim, d_state)
+    _alike(v, (), (("g", g, (rows, heads)), ("beta", beta, (rows, heads)), ("dstate", dstate, ends),
+                   ("dstate_end", dstate_end, ends)))
+    for name, t in (("dg", dg), ("dbeta", dbeta)):
+        _same(name, t, (rows, heads), v.dtype)
+    _same("checkpoints", checkpoints, (gated_delta_rule_checkpoints(cu),) + ends[1:], f32)
+    narrow = [_heads(name, t, groups, d_state, rows, v.dtype) for name, t in (("dq", dq), ("dk", dk), ("q", q), ("k", k))]
+    wide = [_heads(name, t, heads, headdim, rows, v.dtype) for name, t in (("dv", dv), ("dy", dy), ("v", v))]
+    ((dqp, ldq), (dkp, ldk), (qp, lq), (kp, lk)), ((dvp, ldv), (dyp, ldy), (vp, lv)) = narrow, wide
+    d = Dims(heads, headdim, d_state, groups, 1)
+    need = 0
+    if workspace is None:
+        need = int(_lib().mamba2_gated_delta_rule_workspace_bytes(cu, n, ctypes.byref(d), _dt(v), 1))
+    ws, ws_bytes, _keep = _workspace(need, workspace, v.device, stream)
+    st = _lib().mamba2_gated_delta_rule_backward(
+        dqp, dkp, dvp, _ptr(dg), _ptr(dbeta), _ptr(dstate), dyp, _ptr(dstate_end), qp, kp, vp, _ptr(g), _ptr(beta),
+        _ptr(checkpoints), rows, ldq, ldk, ldv, ldy, lq, lk, lv, ctypes.byref(d),
+        d_state ** -0.5 if scale is None else float(scale), -1.0 if l2_eps is None else _l2_eps(l2_eps), _dt(v), cu, n, ws,
+        ws_bytes, _stream(stream))
+    if check:
+        _check(st, "mamba2_gated_delta_rule_backward")
     return st
 
 

@@ -20,7 +20,7 @@ CSRC = PKG / "csrc"
 BUILD = PKG / "_build"
 LIB = PKG / "libmamba2.so"
 SOURCES = ["api.cu", "conv1d.cu", "scan.cu", "scan_tc.cu", "norm.cu", "decode.cu", "pack.cu", "gemm_tc.cu", "selftest.cu", "mamba3.cu",
-           "block_api.cu", "recurrence.cu", "add_norm.cu", "linear.cu", "delta_api.cu", "delta.cu", "delta_chunk.cu", "beam.cu"]
+           "block_api.cu", "recurrence.cu", "add_norm.cu", "linear.cu", "delta_api.cu", "delta.cu", "delta_chunk.cu", "delta_bwd.cu", "beam.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-I", str(ROOT / "include")] + ARCH

@@ -97,11 +97,12 @@ int64_t mamba2_gated_delta_rule_checkpoints(const int32_t* cu_seqlens, int32_t n
 
 size_t mamba2_gated_delta_rule_workspace_bytes(const int32_t* cu_seqlens, int32_t num_seqs, const mamba2_dims* dims,
                                                mamba2_dtype act, int32_t backward) {
-  (void)backward;
   if (!act_ok(act) || delta_dims(dims) != MAMBA2_OK || !cu_ok(cu_seqlens, num_seqs) ||
       !delta_chunked_supported(act, dims->headdim, dims->d_state))
     return 0;
-  return (delta_workspace(count_chunks(cu_seqlens, num_seqs), dims->heads) + 255) / 256 * 256;
+  const int64_t chunks = count_chunks(cu_seqlens, num_seqs);
+  if (backward) return delta_backward_workspace(chunks, dims->heads, dims->headdim, dims->d_state);
+  return (delta_records(chunks, dims->heads, false) + 255) / 256 * 256;
 }
 
 mamba2_status mamba2_gated_delta_rule(void* y, float* checkpoints, const void* q, const void* k, const void* v,
@@ -190,6 +191,69 @@ mamba2_status mamba2_gated_delta_rule_step_device(void* y, const void* q, const 
   a.dev_n = num_seqs_dev;
   a.dev_status = status_dev;
   return done(launch_delta_step(a, act, static_cast<cudaStream_t>(stream)));
+}
+
+mamba2_status mamba2_gated_delta_rule_backward(void* dq, void* dk, void* dv, void* dg, void* dbeta, float* dstate,
+                                               const void* dy, const float* dstate_end, const void* q, const void* k,
+                                               const void* v, const float* g, const float* beta,
+                                               const float* checkpoints, int32_t rows, int64_t ld_dq, int64_t ld_dk,
+                                               int64_t ld_dv, int64_t ld_dy, int64_t ld_q, int64_t ld_k, int64_t ld_v,
+                                               const mamba2_dims* dims, float scale, float l2_eps, mamba2_dtype act,
+                                               const int32_t* cu_seqlens, int32_t num_seqs, void* workspace,
+                                               size_t workspace_bytes, void* stream) {
+  if (!act_ok(act) || rows < 0 || rows > MAMBA2_MAX_BLOCK_SIZE || num_seqs < 0 || num_seqs > MAMBA2_MAX_SEQS ||
+      (num_seqs > 0 && !cu_seqlens) || std::isnan(scale) || std::isnan(l2_eps))
+    return MAMBA2_ERR_INVALID_ARGUMENT;
+  mamba2_status s = delta_dims(dims);
+  if (s != MAMBA2_OK) return s;
+  if (!delta_chunked_supported(act, dims->headdim, dims->d_state)) return MAMBA2_ERR_NOT_IMPLEMENTED;
+  const void* plain[] = {dg, dbeta, dstate, dstate_end, checkpoints};
+  for (const void* p : plain)
+    if (!aligned16(p)) return MAMBA2_ERR_INVALID_ARGUMENT;
+  if (rows > 0) {
+    // (dv stands where the forward has y; dq, dk and dy are held to the same)
+    s = delta_tensors(dv, q, k, v, g, beta, nullptr, ld_dv, ld_q, ld_k, ld_v, dims);
+    if (s == MAMBA2_OK) s = delta_tensors(dy, dq, dk, v, nullptr, nullptr, nullptr, ld_dy, ld_dq, ld_dk, ld_v, dims);
+    if (s != MAMBA2_OK) return s;
+    if (!checkpoints) return MAMBA2_ERR_INVALID_ARGUMENT;
+    const void* out[] = {dq, dk, dv, dg, dbeta};
+    const void* in[] = {dy, q, k, v, g, beta, checkpoints, dstate_end};
+    for (int i = 0; i < 5; ++i) {
+      if (!out[i]) continue;
+      for (const void* p : in)
+        if (p == out[i]) return MAMBA2_ERR_INVALID_ARGUMENT;
+      for (int j = 0; j < i; ++j)
+        if (out[j] == out[i]) return MAMBA2_ERR_INVALID_ARGUMENT;
+    }
+  }
+  if (num_seqs == 0) {
+    if (rows != 0) return MAMBA2_ERR_RUNS_DONT_COVER_ROWS;
+    return MAMBA2_OK;
+  }
+  if (!cu_ok(cu_seqlens, num_seqs) || cu_seqlens[num_seqs] != rows) return MAMBA2_ERR_RUNS_DONT_COVER_ROWS;
+  if (dstate && dstate == dstate_end) return MAMBA2_ERR_INVALID_ARGUMENT;
+  const size_t need = mamba2_gated_delta_rule_workspace_bytes(cu_seqlens, num_seqs, dims, act, 1);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return MAMBA2_ERR_WORKSPACE_TOO_SMALL;
+  if (need > 0 && !aligned_to(workspace, 256)) return MAMBA2_ERR_INVALID_ARGUMENT;
+  DeltaBwdArgs a;
+  fill(a, nullptr, q, k, v, g, beta, nullptr, 0, ld_q, ld_k, ld_v, dims, scale, l2_eps);
+  a.ckpt = const_cast<float*>(checkpoints);
+  a.dq = dq;
+  a.dk_out = dk;
+  a.dv_out = dv;
+  a.dg = dg;
+  a.dbeta = dbeta;
+  a.dstate = dstate;
+  a.dy = dy;
+  a.dstate_end = dstate_end;
+  a.ld_dq = ld_dq;
+  a.ld_dk = ld_dk;
+  a.ld_dv = ld_dv;
+  a.ld_dy = ld_dy;
+  a.tab.n = num_seqs;
+  for (int i = 0; i <= num_seqs; ++i) a.tab.cu[i] = cu_seqlens[i];
+  fill_chunks(a.tab);
+  return done(launch_delta_backward(a, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 size_t mamba2_beam_select_workspace_bytes(int32_t batch, int32_t beams, int32_t out, int32_t vocab) {

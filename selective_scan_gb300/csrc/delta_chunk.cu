@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(const __grid_c
       n = rsqrtf(s + a.l2_eps);
     }
     if (r >= c.len) n = 0.0f;
-    (is_q ? qn : kn)[r] = is_q ? n * a.scale : n;
+    (is_q ? qn : kn)[r] = n;
   }
   // K K^T and Q K^T below and on the diagonal blocks: a warp 16 rows
   float kk[8][4], qk[8][4];
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(const __grid_c
         const int j = j0 + e;
         const float d = j <= i ? ex2((ghi[i] - ghi[j]) + (glo[i] - glo[j])) * kn[j] : 0.0f;
         l[e] = j < i ? kk[n][2 * half + e] * d * kn[i] * beta[j] : 0.0f;
-        p[e] = j <= i ? qk[n][2 * half + e] * d * qn[i] : 0.0f;
+        p[e] = j <= i ? qk[n][2 * half + e] * d * (qn[i] * a.scale) : 0.0f;
       }
       *reinterpret_cast<float2*>(A + i * kLdA + j0) = make_float2(l[0], l[1]);
       uint32_t hi, lo;
@@ -168,8 +168,14 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(const __grid_c
       const float up = ex2(ghi[i] + glo[i]), left = ex2((chi - ghi[i]) + (clo - glo[i]));
       f[kUp + i] = up * kn[i];
       f[kLeft + i] = left * kn[i];
-      f[kUpQ + i] = up * qn[i];
+      f[kUpQ + i] = up * (qn[i] * a.scale);
       f[kBeta + i] = beta[i];
+      if (kBackward) {
+        f[kGHi + i] = ghi[i];
+        f[kGLo + i] = glo[i];
+        f[kKn + i] = kn[i];
+        f[kQn + i] = qn[i];
+      }
     }
     if (threadIdx.x == 0) f[kGamma] = ex2(chi + clo);
   }
@@ -483,16 +489,21 @@ cudaError_t run_chain(const DeltaArgs& a, const unsigned char* records, cudaStre
   return cudaGetLastError();
 }
 
+template <int DK, bool kBackward>
+cudaError_t run_prep(const DeltaArgs& a, unsigned char* records, cudaStream_t st) {
+  const int chunks = a.tab.tile[a.tab.n];
+  if (chunks == 0) return cudaSuccess;
+  auto kernel = delta_prep_kernel<DK, kBackward>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PrepSmem::kBytes);
+  if (e != cudaSuccess) return e;
+  kernel<<<dim3(chunks, a.heads), kPrepThreads, PrepSmem::kBytes, st>>>(a, records);
+  return cudaGetLastError();
+}
+
 template <int DK>
 cudaError_t run_forward(const DeltaArgs& a, unsigned char* records, cudaStream_t st) {
-  const int chunks = a.tab.tile[a.tab.n];
-  if (chunks > 0) {
-    auto kernel = delta_prep_kernel<DK, false>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PrepSmem::kBytes);
-    if (e != cudaSuccess) return e;
-    kernel<<<dim3(chunks, a.heads), kPrepThreads, PrepSmem::kBytes, st>>>(a, records);
-    if (const cudaError_t f = cudaGetLastError(); f != cudaSuccess) return f;
-  }
+  const cudaError_t e = run_prep<DK, false>(a, records, st);
+  if (e != cudaSuccess) return e;
   const int64_t chains = (int64_t)a.tab.n * a.heads, sms = device_sm_count();
   if (a.dv > 64 && chains >= sms) return run_chain<DK, 8>(a, records, st);
   if (a.dv > 32 && 2 * chains >= sms) return run_chain<DK, 4>(a, records, st);
@@ -503,7 +514,12 @@ cudaError_t run_forward(const DeltaArgs& a, unsigned char* records, cudaStream_t
 
 bool delta_chunked_supported(mamba2_dtype act, int dv, int dk) { return act == MAMBA2_BF16 && dk <= 128 && dv <= 128; }
 
-size_t delta_workspace(int64_t chunks, int heads) { return (size_t)chunks * heads * record_bytes(false); }
+size_t delta_records(int64_t chunks, int heads, bool backward) { return (size_t)chunks * heads * record_bytes(backward); }
+
+cudaError_t launch_delta_records(const DeltaArgs& a, void* ws, cudaStream_t st) {
+  unsigned char* records = static_cast<unsigned char*>(ws);
+  return a.dk <= 64 ? run_prep<64, true>(a, records, st) : run_prep<128, true>(a, records, st);
+}
 
 cudaError_t launch_delta_chunked(const DeltaArgs& a, void* ws, cudaStream_t st) {
   unsigned char* records = static_cast<unsigned char*>(ws);

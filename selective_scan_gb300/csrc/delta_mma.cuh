@@ -85,9 +85,12 @@ constexpr int kTri = 10 * 512;
 __device__ __forceinline__ constexpr int block_at(int i, int j) { return (i * (i + 1) / 2 + j) * 512; }
 // Inv = (I + L diag(beta))^-1 in two bf16 parts, then the scores P (in two, for the backward pass), then the factors.
 constexpr int kOffInvLo = kTri, kOffP = 2 * kTri, kOffPLo = 3 * kTri;
-enum Factor : int { kUp = 0, kLeft = kC, kUpQ = 2 * kC, kBeta = 3 * kC, kGamma = 4 * kC, kFactors = 4 * kC + 64 };
+// Per token: exp(G) kappa, exp(G_C - G) kappa, scale exp(G) kappa_q, beta; exp(G_C); and for the backward pass G in two
+// parts (in units of log 2), kappa and kappa_q.
+enum Factor : int { kUp = 0, kLeft = kC, kUpQ = 2 * kC, kBeta = 3 * kC, kGamma = 4 * kC, kGHi = 5 * kC, kGLo = 6 * kC,
+                    kKn = 7 * kC, kQn = 8 * kC };
 __host__ __device__ constexpr int off_factors(bool backward) { return (backward ? 4 : 3) * kTri; }
-__host__ __device__ constexpr int record_bytes(bool backward) { return off_factors(backward) + kFactors * 4; }
+__host__ __device__ constexpr int record_bytes(bool backward) { return off_factors(backward) + (backward ? 9 : 5) * kC * 4; }
 
 // Which run, and which of its chunks, the batch's chunk is.
 struct Chunk {

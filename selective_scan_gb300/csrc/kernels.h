@@ -277,10 +277,25 @@ struct DeltaArgs : DeltaTensors {
   SeqTable tab;
 };
 cudaError_t launch_delta_serial(const DeltaArgs& a, mamba2_dtype act, cudaStream_t st);
-// Whether the chunked kernels take this shape, and their workspace.
+// Whether the chunked kernels take this shape; the records of their first pass, which are the forward's workspace.
 bool delta_chunked_supported(mamba2_dtype act, int dv, int dk);
-size_t delta_workspace(int64_t chunks, int heads);
+size_t delta_records(int64_t chunks, int heads, bool backward);
 cudaError_t launch_delta_chunked(const DeltaArgs& a, void* ws, cudaStream_t st);
+cudaError_t launch_delta_records(const DeltaArgs& a, void* ws, cudaStream_t st);  // the backward's
+
+struct DeltaBwdArgs : DeltaArgs {  // (y and state unused, ckpt read; tab's slots unused)
+  void* dq;
+  void* dk_out;
+  void* dv_out;
+  void* dg;
+  void* dbeta;
+  float* dstate;
+  const void* dy;
+  const float* dstate_end;
+  int64_t ld_dq, ld_dk, ld_dv, ld_dy;
+};
+size_t delta_backward_workspace(int64_t chunks, int heads, int dv, int dk);
+cudaError_t launch_delta_backward(const DeltaBwdArgs& a, void* ws, cudaStream_t st);
 
 struct DeltaStepArgs : DeltaTensors {  // (ckpt unused)
   int32_t n;  // sequences, or the capacity of a device batch

@@ -10,6 +10,8 @@ behind another in a chunk: LOCAL16. Operands of products that end in a bf16 outp
 2^-8 at most (half a step)."""
 from __future__ import annotations
 
+import math
+
 import torch
 
 U = 2.0 ** -24
@@ -71,14 +73,15 @@ def forward(q, k, v, g, beta, pool, cu, slots, fresh, scale, eps, local):
 
 
 def backward(keep, cu, dy, dstate_end, scale, groups):
-    """Gradients by name, and for each a bound on its magnitude (the norm of a vector, for q and k)."""
+    """Gradients by name, and for each a bound on its magnitude (the norm of a vector, for q and k); for those of g and
+    beta, which are single sums over a state and may cancel, the 2-norm of their terms too."""
     qh, kh, a, b = keep["qh"], keep["kh"], keep["a"], keep["b"]
     rows, H, P = dy.shape
     n = len(cu) - 1
     dy = dy.double()
     dqh, dkh, dv = torch.zeros_like(qh), torch.zeros_like(kh), torch.zeros_like(dy)
     dg, db = torch.zeros_like(a), torch.zeros_like(b)
-    mq, mk, mg, mb = (torch.zeros_like(a) for _ in range(4))
+    mq, mk, mg, mb, tg, tb = (torch.zeros_like(a) for _ in range(6))
     mv = torch.zeros_like(dy)
     N = qh.shape[2]
     d0, e0 = torch.zeros((n, H, P, N), dtype=torch.float64), torch.zeros((n, H, P), dtype=torch.float64)
@@ -100,6 +103,7 @@ def backward(keep, cu, dy, dstate_end, scale, groups):
             dkh[t] = (u[..., None] * D).sum(1)
             db[t] = (du * r).sum(-1)
             mb[t] = (m * kl * r.abs()).sum(-1)
+            tb[t] = (D * kt[:, None, :] * r[..., None]).norm(dim=(-1, -2))
             dv[t] = bt * du
             mv[t] = bt * m * kl
             dkh[t] -= (dv[t][..., None] * dec).sum(1)
@@ -109,23 +113,24 @@ def backward(keep, cu, dy, dstate_end, scale, groups):
             m = m + mv[t] * kl
             dg[t] = (D * dec).sum((-1, -2))
             mg[t] = (m * at * ms).sum(-1)
+            tg[t] = (D * dec).norm(dim=(-1, -2))
             D, m, e = at[..., None] * D, at * m, at * e
         d0[i], e0[i] = D, e
     per = H // groups
 
     def gather(d, mag, unit_, length, by):
-        d, mag = d.unflatten(1, (groups, per)).sum(2) * by, mag.unflatten(1, (groups, per)).sum(2) * by
+        d, mag = d.unflatten(1, (groups, per)).sum(2) * by, mag.unflatten(1, (groups, per)).sum(2) * abs(by)
         return (d - unit_ * (d * unit_).sum(-1, keepdim=True)) / length[..., None], 2 * mag / length
 
     plain = bool((keep["qn"] == 1).all()) and bool((keep["kn"] == 1).all())
     if plain:
         dq, dk = dqh.unflatten(1, (groups, per)).sum(2) * scale, dkh.unflatten(1, (groups, per)).sum(2)
-        mq, mk = mq.unflatten(1, (groups, per)).sum(2) * scale, mk.unflatten(1, (groups, per)).sum(2)
+        mq, mk = mq.unflatten(1, (groups, per)).sum(2) * abs(scale), mk.unflatten(1, (groups, per)).sum(2)
     else:
         dq, mq = gather(dqh, mq, keep["qu"], keep["qn"], scale)
         dk, mk = gather(dkh, mk, keep["ku"], keep["kn"], 1.0)
     return dict(dq=(dq, mq[..., None]), dk=(dk, mk[..., None]), dv=(dv, mv), dg=(dg, mg), dbeta=(db, mb),
-                dstate=(d0, e0[..., None]))
+                dstate=(d0, e0[..., None]), terms=dict(dg=tg, dbeta=tb))
 
 
 def within(got, value, slack, what):
@@ -143,9 +148,11 @@ def within(got, value, slack, what):
                              f"expected {value[at].item()} within {bound.expand(value.shape)[at].item()}")
 
 
-def near(got, value, most, what):
-    """The 2-norm of the difference, relative."""
+def near(got, value, most, what, terms=None):
+    """The 2-norm of the difference, relative to the values' own (with the terms' of values that are sums)."""
     g, n = got.detach().cpu().double(), float(value.norm())
+    if terms is not None:
+        n = math.hypot(n, float(terms.norm()))
     off = float((g - value).norm())
     assert off <= most * n, f"{what}: off by {off / n if n else off:.3g} of its norm, at most {most:.3g}"
 

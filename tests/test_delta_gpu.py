@@ -244,3 +244,117 @@ def test_prefill_then_steps_is_prefill():
     torch.cuda.synchronize()
     R.near(z, y.cpu().double(), 2e-6, "y")
     R.near(parts, whole.cpu().double(), 2e-6, "state")
+
+
+# ---------------------------------------------------------------- backward
+
+def check_backward(seed, lengths, groups, heads, d_state, headdim, l2, pad=None, g=True, beta=True, ends=True, change=None,
+                   scale=None):
+    dev = device()
+    q, k, v, gv, bv, pool, slots, fresh = inputs(seed, lengths, groups, heads, d_state, headdim, BF16, l2)
+    gv, bv = (gv if g else None), (bv if beta else None)
+    if change:
+        q, k, v, gv, bv = change(q, k, v, gv, bv)
+    cu, rows, n, eps = cu_of(lengths), sum(lengths), len(lengths), EPS if l2 else None
+    by = d_state ** -0.5 if scale is None else scale
+    fwd = R.forward(q, k, v, gv, bv, pool, cu, slots, fresh, by, eps, R.LOCAL16)
+    dy = randn(seed + 8, rows, heads, headdim).to(BF16)
+    de = randn(seed + 9, n, heads, headdim, d_state, std=0.3) if ends else None
+    want = R.backward(fwd["keep"], cu, dy, de, by, groups)
+    gq, gk, gvv, gdy, y, dq, dk, dv = in_rows([q, k, v, dy, torch.zeros_like(v), torch.zeros_like(q), torch.zeros_like(k),
+                                               torch.zeros_like(v)], dev, pad)
+    gg, gb = (t.to(dev) if t is not None else None for t in (gv, bv))
+    st = pool.to(dev)
+    kept = torch.full((ss.gated_delta_rule_checkpoints(cu),) + pool.shape[1:], NAN, device=dev)
+    ss.gated_delta_rule(y, gq, gk, gvv, gg, gb, st, cu, slots, fresh, scale=scale, l2_eps=eps, checkpoints=kept)
+    dg, db = (torch.full((rows, heads), NAN, dtype=BF16, device=dev) for _ in range(2))
+    ds = torch.full((n,) + pool.shape[1:], NAN, device=dev)
+    args = [gdy, de.to(dev) if ends else None, gq, gk, gvv, gg, gb, kept, cu]
+    ss.gated_delta_rule_backward(dq, dk, dv, dg, db, ds, *args, scale=scale, l2_eps=eps)
+    torch.cuda.synchronize()
+    got = dict(dq=dq, dk=dk, dv=dv, dg=dg, dbeta=db, dstate=ds)
+    for name, t in got.items():
+        value, size = want[name]
+        if name == "dstate":
+            R.within(t, value, size, name)
+            R.near(t, value, 1e-5, name)
+            continue
+        # at most eight operands one behind another are rounded to bf16, each by 2^-8 of what its terms add up to at most;
+        # dg is a running sum over a chunk in 32 bits (192 additions at most, of terms that others of its dg are made of)
+        R.within(t, value, 8 * R.HALF16 * size + (192 * R.U * size.amax() if name == "dg" and rows else 0), name)
+        if rows > 1 and not change:  # 1.7e-3 a rounding (rms): eight of them and the output's own
+            R.near(t, value, 5.1e-3, name, want["terms"].get(name))
+    # the same again, without what is optional: the same bits
+    more = [torch.empty_like(t) for t in (q.to(dev), k.to(dev), v.to(dev))]
+    ss.gated_delta_rule_backward(*more, None, None, None, *args, scale=scale, l2_eps=eps)
+    torch.cuda.synchronize()
+    for a, b in zip(more, (dq, dk, dv)):
+        assert_bits_equal(a.cpu(), b.contiguous().cpu(), "the same call again")
+
+
+@pytest.mark.parametrize("lengths", LENGTHS, ids=str)
+@pytest.mark.parametrize("groups,heads,d_state,headdim", SHAPES)
+def test_backward(lengths, groups, heads, d_state, headdim):
+    check_backward(d_state + len(lengths), lengths, groups, heads, d_state, headdim, heads != 3)
+
+
+@pytest.mark.parametrize("pad", [0, 8, 24])
+def test_backward_of_column_ranges(pad):
+    check_backward(11, [70, 1, 200], 2, 4, 72, 40, True, pad=pad)
+
+
+@pytest.mark.parametrize("g,beta,ends", [(False, True, True), (True, False, False), (False, False, False)])
+def test_backward_without_decay_beta_or_end_states(g, beta, ends):
+    check_backward(12, [130, 40], 2, 2, 64, 64, True, g=g, beta=beta, ends=ends)
+
+
+@pytest.mark.parametrize("change", [strong_decay, alike_keys, corner_betas, zero_rows], ids=lambda f: f.__name__)
+def test_backward_of_values_at_the_edge(change):
+    check_backward(13, [200, 3, 64], 1, 2, 128, 64, change is not zero_rows, change=change)
+
+
+def test_backward_scale():
+    check_backward(14, [66], 1, 1, 64, 64, False, scale=-3.0)
+
+
+def test_backward_of_many_heads_and_runs():
+    """Runs and heads enough for every split of a state over warps."""
+    check_backward(15, [3] * 40 + [64, 130], 2, 4, 32, 128, True)
+
+
+@pytest.mark.parametrize("l2", [True, False])
+def test_gradients_against_differences(l2):
+    """The gradients' projection on a direction against central differences of the 64-bit loop."""
+    dev = device()
+    lengths, G, H, N, P = [70, 33], 1, 2, 24, 16
+    q, k, v, g, beta, pool, slots, _ = inputs(31, lengths, G, H, N, P, BF16, l2)
+    fresh, cu, rows, eps = [0, 0], cu_of(lengths), sum(lengths), EPS if l2 else None
+    dy, de = randn(32, rows, H, P).to(BF16), randn(33, 2, H, P, N, std=0.3)
+    at = torch.tensor(slots)
+
+    def loss(q, k, v, g, beta, pool):
+        r = R.forward(q, k, v, g, beta, pool, cu, slots, fresh, N ** -0.5, eps, R.LOCAL16)
+        return float((r["y"] * dy.double()).sum() + (r["pool"][at] * de.double()).sum())
+
+    base = [t.double() for t in (q, k, v, g, beta, pool)]
+    gin = [t.to(dev) for t in (q, k, v, g, beta)]
+    kept = torch.empty((ss.gated_delta_rule_checkpoints(cu),) + pool.shape[1:], device=dev)
+    y, st = torch.empty_like(gin[2]), pool.to(dev)
+    ss.gated_delta_rule(y, *gin, st, cu, slots, fresh, l2_eps=eps, checkpoints=kept)
+    out = [torch.empty_like(gin[0]), torch.empty_like(gin[1]), torch.empty_like(gin[2])] + [torch.empty((rows, H), dtype=BF16, device=dev) for _ in range(2)]
+    ds = torch.empty((2, H, P, N), device=dev)
+    ss.gated_delta_rule_backward(*out, ds, dy.to(dev), de.to(dev), *gin, kept, cu, l2_eps=eps)
+    torch.cuda.synchronize()
+    grads = [t.cpu().double() for t in out] + [ds.cpu().double()]
+    for i, name in enumerate(("q", "k", "v", "g", "beta", "state")):
+        way = randn(40 + i, *base[i].shape).double()
+        if name == "state":
+            way[[s for s in range(pool.shape[0]) if s not in slots]] = 0
+        h = 1e-5
+        up, down = [list(base) for _ in range(2)]
+        up[i], down[i] = base[i] + h * way, base[i] - h * way
+        slope = (loss(*up) - loss(*down)) / (2 * h)
+        got = grads[i] * (way if name != "state" else way[at])
+        # each gradient is off by 5.1e-3 of its norm at most (above), so a projection by that times both norms
+        most = 5.1e-3 * float(grads[i].norm()) * float((way if name != "state" else way[at]).norm()) + 1e-6 * abs(slope)
+        assert abs(float(got.sum()) - slope) <= most, (name, float(got.sum()), slope, most)

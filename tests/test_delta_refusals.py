@@ -210,3 +210,70 @@ def test_reorder_tensors(product_lib):
                                       ([pool[:, ::2]], order, order, status)):
         with pytest.raises(ValueError):
             ss.reorder_states(pools, slots, parents, st, stream=0)
+
+
+def backward(lib, ptrs=None, ld=(256,) * 7, d=None, scale=1.0, eps=-1.0, act=ss.BF16, rows=3, cu=(0, 3), ws=WS):
+    arr = (ctypes.c_int32 * max(1, len(cu)))(*cu)
+    return lib.mamba2_gated_delta_rule_backward(*(ptrs or P[:14]), rows, *ld, d if d is not None else dims(), scale, eps, act, arr,
+                                                len(cu) - 1, *ws, None)
+
+
+# dq, dk, dv, dg, dbeta, dstate, dy, dstate_end, q, k, v, g, beta, checkpoints
+@pytest.mark.parametrize("at", range(14))
+def test_backward_pointers(product_lib, at):
+    for bad in (None, P[at] + 8):
+        if bad is None and at in (3, 4, 5, 7, 11, 12):  # optional
+            continue
+        ptrs = P[:14]
+        ptrs[at] = bad
+        assert backward(product_lib, ptrs) == INV
+    if at < 5:  # an output over an input, or over another
+        for other in list(range(6, 14)) + [i for i in range(5) if i != at]:
+            ptrs = P[:14]
+            ptrs[at] = ptrs[other]
+            assert backward(product_lib, ptrs) == INV
+    if at == 5:
+        ptrs = P[:14]
+        ptrs[5] = ptrs[7]
+        assert backward(product_lib, ptrs) == INV
+
+
+def test_backward_arguments(product_lib):
+    lib = product_lib
+    for change, want in ((dict(heads=0), INV), (dict(heads=3), INV), (dict(headdim=60), NOT), (dict(headdim=136), NOT), (dict(d_state=136), NOT)):
+        assert backward(lib, d=dims(**change), ld=(1 << 20,) * 7) == want
+    for i in range(7):
+        short, odd = [256] * 7, [264] * 7
+        short[i], odd[i] = 248, 260
+        assert backward(lib, ld=short) == INV and backward(lib, ld=odd) == NOT
+    assert backward(lib, act=ss.F32) == NOT and backward(lib, act=ss.E4M3) == INV
+    assert backward(lib, scale=NAN) == INV and backward(lib, eps=NAN) == INV and backward(lib, rows=-1) == INV
+    for cu in ((0, 2), (1, 3), (0, 4, 3), (0,)):
+        assert backward(lib, cu=cu) == ss.ERR_RUNS_DONT_COVER_ROWS
+    assert backward(lib, ws=(None, 1 << 40)) == SMALL and backward(lib, ws=(P[18], 1000)) == SMALL
+    assert backward(lib, ws=(P[18] + 128, 1 << 40)) == INV
+    assert backward(lib, [None] * 14, rows=0, cu=(0,)) == ss.OK
+
+
+def test_chunked_forward_workspace(product_lib):
+    """bf16 heads of at most 128 x 128 go by chunks, which take a workspace; the others do not."""
+    b = ss.Batch([0, 3], [1], [0])
+    for ws, want in (((None, 1 << 40), SMALL), ((P[18], 1000), SMALL), ((P[18] + 128, 1 << 40), INV)):
+        assert product_lib.mamba2_gated_delta_rule(*P[:8], 5, 3, 256, 256, 256, 256, dims(), 1.0, -1.0, ss.BF16, b.ref(), *ws, None) == want
+    assert ss.gated_delta_rule_workspace_bytes([0, 65], 4, 64, 128, 2, torch.bfloat16) > 0
+    assert ss.gated_delta_rule_workspace_bytes([0, 65], 4, 64, 128, 2, torch.float32) == 0
+    assert ss.gated_delta_rule_workspace_bytes([0, 65], 4, 136, 128, 2, torch.bfloat16) == 0
+
+
+@pytest.mark.parametrize("name,bad", [("dq", lambda t: t[:2]), ("dk", lambda t: t.float()), ("dv", lambda t: t[:, :2]), ("dg", lambda t: t.float()),
+                                      ("dbeta", lambda t: t[:, :3]), ("dstate", lambda t: t[:, :, :, :8]), ("dstate_end", lambda t: t.double()),
+                                      ("dy", lambda t: t.float()), ("checkpoints", lambda t: t[:0]), ("q", lambda t: t[:2])], ids=str)
+def test_backward_tensors(product_lib, name, bad):
+    t = delta_tensors()
+    state = t.pop("state")
+    y = t.pop("y")
+    t.update(dq=t["q"].clone(), dk=t["q"].clone(), dv=y.clone(), dg=t["g"].bfloat16(), dbeta=t["g"].bfloat16(), dstate=state[:1].clone(),
+             dy=y.clone(), dstate_end=state[:1].clone(), checkpoints=state[:1].clone())
+    t[name] = bad(t[name])
+    with pytest.raises(ValueError):
+        ss.gated_delta_rule_backward(**t, cu_seqlens=[0, 3], stream=0)
