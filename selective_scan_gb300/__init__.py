@@ -158,13 +158,18 @@ def library():
 # marshalling
 # --------------------------------------------------------------------------
 
+_CODES = {}  # torch's activation types and their codes (filled by the first call: torch is imported then)
+
+
 def _dt(t) -> int:
-    import torch
-    if t.dtype == torch.bfloat16:
-        return BF16
-    if t.dtype == torch.float32:
-        return F32
-    raise TypeError(f"unsupported activation dtype {t.dtype}")
+    code = _CODES.get(t.dtype)
+    if code is None:
+        import torch
+        _CODES.update({torch.bfloat16: BF16, torch.float32: F32})
+        if t.dtype not in _CODES:
+            raise TypeError(f"unsupported activation dtype {t.dtype}")
+        code = _CODES[t.dtype]
+    return code
 
 
 def _alike(first, others, f32=()):
@@ -715,13 +720,14 @@ def linear_backward(dx, dw, dbias, dy, x, w, activation="none", pre=None, worksp
     return st
 
 
-def _heads(name, t, heads, width, rows, dtype):
+def _heads(name, t, shape, dtype):
     """(pointer, row stride) of a [rows, heads, width] tensor whose heads are contiguous: a contiguous one, or a column
     range of a wider matrix's rows split into heads."""
-    if t.shape != (rows, heads, width) or t.dtype != dtype:
-        _same(name, t, (rows, heads, width), dtype)
+    if t.shape != shape or t.dtype != dtype:
+        _same(name, t, shape, dtype)
     ld, per, one = t.stride()
-    if (width > 1 and one != 1) or (heads > 1 and per != width):
+    rows, heads, width = shape
+    if (one != 1 and width > 1) or (per != width and heads > 1):
         raise ValueError(f"{name}: a row's heads must be contiguous")
     if rows <= 1:
         ld = heads * width
@@ -731,15 +737,39 @@ def _heads(name, t, heads, width, rows, dtype):
     return t.data_ptr(), ld
 
 
+_DIMS = {}
+
+
+def _delta_dims(heads, headdim, d_state, groups):
+    """A reference to these dims (made once: a small call's host time counts)."""
+    key = (heads, headdim, d_state, groups)
+    d = _DIMS.get(key)
+    if d is None:
+        if len(_DIMS) > 256:
+            _DIMS.clear()
+        d = _DIMS[key] = ctypes.byref(Dims(heads, headdim, d_state, groups, 1))
+    return d
+
+
 def _delta(y, q, k, v, g, beta, state, scale, l2_eps):
     """What the gated delta rule's forward calls pass on: pointers, strides, dims, scale and l2_eps."""
-    (rows, heads, headdim), (groups, d_state) = v.shape, q.shape[1:]
-    _alike(v, (), (("g", g, (rows, heads)), ("beta", beta, (rows, heads)),
-                   ("state", state, (state.shape[0], heads, headdim, d_state))))
-    (yp, ly), (vp, lv) = _heads("y", y, heads, headdim, rows, v.dtype), _heads("v", v, heads, headdim, rows, v.dtype)
-    (qp, lq), (kp, lk) = (_heads(n, t, groups, d_state, rows, v.dtype) for n, t in (("q", q), ("k", k)))
+    wide, narrow, dtype = v.shape, q.shape, v.dtype
+    rows, heads, headdim = wide
+    _, groups, d_state = narrow
+    if narrow[0] != rows:
+        _same("q", q, (rows, groups, d_state))
+    per_row, f32 = (rows, heads), _float32()
+    for name, t in (("g", g), ("beta", beta)):
+        if t is not None and (t.shape != per_row or t.dtype != f32):
+            _same(name, t, per_row, f32)
+    if state.shape[1:] != (heads, headdim, d_state) or state.dtype != f32:
+        _same("state", state, (state.shape[0], heads, headdim, d_state), f32)
+    yp, ly = _heads("y", y, wide, dtype)
+    vp, lv = _heads("v", v, wide, dtype)
+    qp, lq = _heads("q", q, narrow, dtype)
+    kp, lk = _heads("k", k, narrow, dtype)
     return ((yp, qp, kp, vp, _ptr(g), _ptr(beta), _ptr(state)), (ly, lq, lk, lv),
-            Dims(heads, headdim, d_state, groups, 1), d_state ** -0.5 if scale is None else float(scale),
+            _delta_dims(heads, headdim, d_state, groups), d_state ** -0.5 if scale is None else float(scale),
             -1.0 if l2_eps is None else _l2_eps(l2_eps))
 
 
@@ -780,11 +810,10 @@ def gated_delta_rule(y, q, k, v, g, beta, state, cu_seqlens=None, slots=None, fr
         _same("checkpoints", checkpoints, (gated_delta_rule_checkpoints(b.cu),) + state.shape[1:], _float32())
     need = 0
     if workspace is None and b.cu is not None:
-        need = int(_lib().mamba2_gated_delta_rule_workspace_bytes(b.cu, len(b.cu) - 1, ctypes.byref(d), _dt(v), 0))
+        need = int(_lib().mamba2_gated_delta_rule_workspace_bytes(b.cu, len(b.cu) - 1, d, _dt(v), 0))
     ws, ws_bytes, _keep = _workspace(need, workspace, v.device, stream)
     st = _lib().mamba2_gated_delta_rule(yp, _ptr(checkpoints), qp, kp, vp, gp, bp, sp, state.shape[0], v.shape[0],
-                                        *strides, ctypes.byref(d), scale, eps, _dt(v), b.ref(), ws, ws_bytes,
-                                        _stream(stream))
+                                        *strides, d, scale, eps, _dt(v), b.ref(), ws, ws_bytes, _stream(stream))
     if check:
         _check(st, "mamba2_gated_delta_rule")
     return st
@@ -796,7 +825,7 @@ def gated_delta_rule_step(y, q, k, v, g, beta, state, slots=None, fresh=None, cu
     b = _batch(cu_seqlens, slots, fresh, batch)
     _same("v", v, (b.rb.num_seqs,) + v.shape[1:])
     ptrs, strides, d, scale, eps = _delta(y, q, k, v, g, beta, state, scale, l2_eps)
-    st = _lib().mamba2_gated_delta_rule_step(*ptrs, state.shape[0], *strides, ctypes.byref(d), scale, eps, _dt(v),
+    st = _lib().mamba2_gated_delta_rule_step(*ptrs, state.shape[0], *strides, d, scale, eps, _dt(v),
                                              b.ref(), _stream(stream))
     if check:
         _check(st, "mamba2_gated_delta_rule_step")
@@ -818,7 +847,7 @@ def gated_delta_rule_step_device(y, q, k, v, g, beta, state, slots_dev, fresh_de
         _same("num_seqs_dev", num_seqs_dev, (1,), i32)
         _same("status_dev", status_dev, (1,), i32)
     ptrs, strides, d, scale, eps = _delta(y, q, k, v, g, beta, state, scale, l2_eps)
-    st = _lib().mamba2_gated_delta_rule_step_device(*ptrs, state.shape[0], *strides, ctypes.byref(d), scale, eps, _dt(v),
+    st = _lib().mamba2_gated_delta_rule_step_device(*ptrs, state.shape[0], *strides, d, scale, eps, _dt(v),
                                                     _ptr(slots_dev), _ptr(fresh_dev), _ptr(num_seqs_dev), cap,
                                                     _ptr(status_dev), _stream(stream))
     if check:
@@ -839,17 +868,17 @@ def gated_delta_rule_backward(dq, dk, dv, dg, dbeta, dstate, dy, dstate_end, q, 
     for name, t in (("dg", dg), ("dbeta", dbeta)):
         _same(name, t, (rows, heads), v.dtype)
     _same("checkpoints", checkpoints, (gated_delta_rule_checkpoints(cu),) + ends[1:], f32)
-    narrow = [_heads(name, t, groups, d_state, rows, v.dtype) for name, t in (("dq", dq), ("dk", dk), ("q", q), ("k", k))]
-    wide = [_heads(name, t, heads, headdim, rows, v.dtype) for name, t in (("dv", dv), ("dy", dy), ("v", v))]
+    narrow = [_heads(name, t, (rows, groups, d_state), v.dtype) for name, t in (("dq", dq), ("dk", dk), ("q", q), ("k", k))]
+    wide = [_heads(name, t, v.shape, v.dtype) for name, t in (("dv", dv), ("dy", dy), ("v", v))]
     ((dqp, ldq), (dkp, ldk), (qp, lq), (kp, lk)), ((dvp, ldv), (dyp, ldy), (vp, lv)) = narrow, wide
-    d = Dims(heads, headdim, d_state, groups, 1)
+    d = _delta_dims(heads, headdim, d_state, groups)
     need = 0
     if workspace is None:
-        need = int(_lib().mamba2_gated_delta_rule_workspace_bytes(cu, n, ctypes.byref(d), _dt(v), 1))
+        need = int(_lib().mamba2_gated_delta_rule_workspace_bytes(cu, n, d, _dt(v), 1))
     ws, ws_bytes, _keep = _workspace(need, workspace, v.device, stream)
     st = _lib().mamba2_gated_delta_rule_backward(
         dqp, dkp, dvp, _ptr(dg), _ptr(dbeta), _ptr(dstate), dyp, _ptr(dstate_end), qp, kp, vp, _ptr(g), _ptr(beta),
-        _ptr(checkpoints), rows, ldq, ldk, ldv, ldy, lq, lk, lv, ctypes.byref(d),
+        _ptr(checkpoints), rows, ldq, ldk, ldv, ldy, lq, lk, lv, d,
         d_state ** -0.5 if scale is None else float(scale), -1.0 if l2_eps is None else _l2_eps(l2_eps), _dt(v), cu, n, ws,
         ws_bytes, _stream(stream))
     if check:
@@ -892,18 +921,18 @@ def reorder_states(pools, slots, parents, status_dev, stream=None, check=True) -
     beams] and ``status_dev`` (one element) are int32 device tensors, checked on the device: ``status_dev`` holds the
     outcome once the stream has passed the call."""
     import torch
-    pools = list(pools)
-    batch, beams = slots.shape
-    for name, t in (("slots", slots), ("parents", parents)):
-        _same(name, t, (batch, beams), torch.int32)
-    _same("status_dev", status_dev, (1,), torch.int32)
-    num_slots = int(pools[0].shape[0]) if pools else 0
+    (batch, beams), i32, n = slots.shape, torch.int32, len(pools)
+    if slots.dtype != i32 or parents.shape != slots.shape or parents.dtype != i32 or status_dev.shape != (1,) or status_dev.dtype != i32:
+        _same("slots", slots, (batch, beams), i32)
+        _same("parents", parents, (batch, beams), i32)
+        _same("status_dev", status_dev, (1,), i32)
+    num_slots = pools[0].shape[0] if n else 0
+    sizes = []
     for i, t in enumerate(pools):
         if t.shape[0] != num_slots:
             raise ValueError(f"pool {i}: expected {num_slots} slots, got {t.shape[0]}")
-    n = len(pools)
-    ptrs = (ctypes.c_void_p * max(n, 1))(*map(_ptr, pools))
-    sizes = (ctypes.c_int64 * max(n, 1))(*(t.numel() // max(num_slots, 1) * t.element_size() for t in pools))
+        sizes.append(t.nbytes // (num_slots or 1))
+    ptrs, sizes = (ctypes.c_void_p * (n or 1))(*map(_ptr, pools)), (ctypes.c_int64 * (n or 1))(*sizes)
     st = _lib().mamba2_reorder_states(ptrs, sizes, n, num_slots, _ptr(slots), _ptr(parents), batch, beams,
                                       _ptr(status_dev), _stream(stream))
     if check:

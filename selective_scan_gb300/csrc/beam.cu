@@ -12,13 +12,19 @@ namespace {
 
 // ------------------------------------------------------------------ selection
 //
-// Two kernels. The first reads the logits, once: a CTA takes a part of a row and leaves its maximum, the sum of
-// exp(x - maximum) and its `out` largest logits; a row's order is that of its logits, so the log-sum-exp is not
+// Two kernels. The first reads the logits, once: a CTA takes a part of a row into registers and leaves its maximum, the
+// sum of exp(x - maximum) and its `out` largest logits; a row's order is that of its logits, so the log-sum-exp is not
 // needed to choose among them. The second joins a row's parts, forms the values in fp64 and ranks a sequence's
-// candidates by counting how many come before each. Bound by HBM, and for few rows by the two launches.
+// candidates by counting how many come before each.
+//
+// In a part, the `out`-th largest of a warp's 32 lane maxima has `out` logits at or above it, so the largest such of the
+// eight warps is a bound below which nothing counts: the few logits that reach it are collected and ranked by counting.
+// Where more reach it than are held (many ties), the warps take them one by one instead.
 constexpr int kScanThreads = 256, kScanWarps = kScanThreads / 32;
 constexpr int kMost = MAMBA2_MAX_BEAMS;  // candidates of a list: one to a lane
-constexpr int kPartMin = 2048;           // logits of a part at least: 256 a warp
+constexpr int kHeld = 1024;              // logits that are collected
+// Vectors of a thread: eight where that leaves every SM four CTAs, else two, so that few rows spread over the SMs.
+constexpr int kMany = 8, kFew = 2;
 
 __device__ __forceinline__ float ex2(float v) {
   float e;
@@ -52,36 +58,10 @@ struct Best {
   }
 };
 
-// Maximum and sum of exponentials below it; nothing yet is (-infinity, 0).
-struct Soft {
-  float m, s;
-  // n values in one go (a NaN makes the sum NaN, an infinity too)
-  template <int n>
-  __device__ __forceinline__ void add(const float (&v)[n], float top) {
-    const float to = fmaxf(m, top), base = to == -INFINITY ? 0.0f : to;
-    if (to > m) s = m == -INFINITY ? s : s * ex2((m - base) * kLog2e);
-    m = to;
-    const float off = -base * kLog2e;
-    float t = 0.0f;
-#pragma unroll
-    for (int j = 0; j < n; ++j) t += ex2(fmaf(v[j], kLog2e, off));
-    s += t;
-  }
-  __device__ __forceinline__ void join(float om, float os) {
-    const float to = fmaxf(m, om);
-    if (to == -INFINITY) {
-      s += os;
-      return;
-    }
-    s = (m == -INFINITY ? s : s * ex2((m - to) * kLog2e)) + (om == -INFINITY ? os : os * ex2((om - to) * kLog2e));
-    m = to;
-  }
-};
-
 struct PartOut {  // of one part of one row
   float* m;
   float* s;
-  float* x;  // [out]
+  float* x;  // [out], descending; -infinity behind the last
   int* at;
 };
 __host__ __device__ inline size_t part_words(int out) { return 2 + 2 * (size_t)out; }
@@ -89,135 +69,288 @@ __device__ __forceinline__ PartOut part_at(void* ws, int64_t i, int out) {
   float* p = static_cast<float*>(ws) + i * (int64_t)part_words(out);
   return {p, p + 1, p + 2, reinterpret_cast<int*>(p + 2 + out)};
 }
-
 template <typename T>
-__global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_constant__ BeamArgs a, int part) {
-  constexpr int V = Vec16<T>::n;
-  __shared__ float wm[kScanWarps], wsum[kScanWarps], wx[kScanWarps][kMost];
-  __shared__ int wat[kScanWarps][kMost];
+constexpr int part_logits(int vectors) { return kScanThreads * vectors * Vec16<T>::n; }
+
+// An order-preserving image of a float (-0 as 0), and with it a logit and its index as one number: larger is better.
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);
+  return b ^ ((int32_t)b < 0 ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t k) { return __uint_as_float(k ^ ((int32_t)k < 0 ? 0x80000000u : 0xffffffffu)); }
+__device__ __forceinline__ uint64_t key_of(float v, int index) { return (uint64_t)ordered(v) << 32 | (uint32_t)~index; }
+__device__ __forceinline__ float key_logit(uint64_t k) { return unordered((uint32_t)(k >> 32)); }
+__device__ __forceinline__ int key_index(uint64_t k) { return (int)~(uint32_t)k; }
+
+__device__ __forceinline__ int64_t ordered(double v) {  // (v is a number or an infinity)
+  const int64_t b = __double_as_longlong(v + 0.0);
+  return b ^ (b < 0 ? 0x7fffffffffffffffll : 0);
+}
+__device__ __forceinline__ double unordered(int64_t k) { return __longlong_as_double(k ^ (k < 0 ? 0x7fffffffffffffffll : 0)); }
+
+// A thread's vector of logits and their maximum.
+template <typename T> struct Logits;
+template <> struct Logits<float> {
+  static constexpr int n = 4;
+  float v[4];
+  __device__ __forceinline__ void load(const float* p) {
+    const float4 f = __ldcs(reinterpret_cast<const float4*>(p));
+    v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+  }
+  __device__ __forceinline__ void load_some(const float* p, int64_t left) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = j < left ? p[j] : -INFINITY;
+  }
+  __device__ __forceinline__ float at(int j) const { return v[j]; }
+  __device__ __forceinline__ float top() const { return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])); }  // (passes over a NaN)
+  // sets the bits of vector u's logits that reach `least`: element j's is 4 u + j
+  __device__ __forceinline__ void reach(float least, int u, uint32_t (&bits)[2]) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (v[j] >= least) bits[0] |= 1u << (4 * u + j);
+  }
+  __device__ static __forceinline__ int element(int half, int bit) { return bit; }  // 4 u + j of a bit
+};
+template <> struct Logits<__nv_bfloat16> {
+  static constexpr int n = 8;
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
+    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+  }
+  __device__ __forceinline__ void load_some(const __nv_bfloat16* p, int64_t left) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t lo = 2 * j < left ? *reinterpret_cast<const uint16_t*>(p + 2 * j) : 0xff80u;
+      const uint32_t hi = 2 * j + 1 < left ? *reinterpret_cast<const uint16_t*>(p + 2 * j + 1) : 0xff80u;
+      w[j] = hi << 16 | lo;
+    }
+  }
+  __device__ __forceinline__ float at(int j) const { return __uint_as_float(j & 1 ? w[j >> 1] & 0xffff0000u : w[j >> 1] << 16); }
+  __device__ __forceinline__ float top() const {
+    auto h = [&](int j) { return *reinterpret_cast<const __nv_bfloat162*>(&w[j]); };
+    const __nv_bfloat162 m = __hmax2(__hmax2(h(0), h(1)), __hmax2(h(2), h(3)));
+    return fmaxf(__low2float(m), __high2float(m));
+  }
+  // word 4 u + i, of elements 2 i and 2 i + 1, has bits (4 u + i) % 16 and that + 16 of bits[(4 u + i) / 16]
+  __device__ __forceinline__ void reach(float least, int u, uint32_t (&bits)[2]) const {
+    const __nv_bfloat162 l = __float2bfloat162_rn(least);  // (a logit itself, or the lowest number)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = 4 * u + i;
+      bits[k >> 4] |= __hge2_mask(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), l) & (0x00010001u << (k & 15));
+    }
+  }
+  __device__ static __forceinline__ int element(int half, int bit) { return 2 * (16 * half + (bit & 15)) + (bit >> 4); }
+};
+
+// kVectors: 16-byte vectors of a thread. The part's last vector may pass the row's end, and the row's first logits up to
+// a 16-byte boundary (`head`) are part 0's besides.
+template <typename T, int kVectors>
+__global__ void __launch_bounds__(kScanThreads, kVectors == kMany ? 4 : 6) beam_scan_kernel(const __grid_constant__ BeamArgs a) {
+  constexpr int V = Logits<T>::n;
+  __shared__ __align__(16) uint64_t key[kHeld + 2];
+  __shared__ float wm[kScanWarps], wsum[kScanWarps], wleast[kScanWarps];
+  __shared__ int held;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t row = blockIdx.y;
   if (a.finished && a.finished[row]) return;  // (its logits are not candidates)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const T* p = static_cast<const T*>(a.logits) + row * a.ld;
-  // elements before the row's first 16-byte boundary; parts and warps begin whole vectors behind it
   const int head = min(a.vocab, (int)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / (int)sizeof(T));
-  const int64_t lo = (int64_t)blockIdx.x * part, hi = min((int64_t)a.vocab - head, lo + part);  // behind the head
-  const int each = part / kScanWarps;
-  const int64_t w0 = lo + (int64_t)warp * each, w1 = min(hi, w0 + each);
-  Best best;
-  best.clear();
-  Soft soft = {-INFINITY, 0.0f};
-  auto one = [&](float v, bool in, int index) {  // an element a lane (-infinity where there is none)
-    const float u[1] = {in ? v : -INFINITY};
-    soft.add(u, u[0]);
-    for (uint32_t todo = __ballot_sync(0xffffffffu, u[0] > best.least); todo; todo &= todo - 1) {
-      const int from = __ffs(todo) - 1;
-      const float c = __shfl_sync(0xffffffffu, u[0], from);
-      const int at = __shfl_sync(0xffffffffu, index, from);
-      if (c > best.least) best.add(c, at, a.out, lane);
-    }
-  };
-  if (blockIdx.x == 0 && warp == 0 && head > 0) one(lane < head ? Act<T>::to_f(p[lane]) : 0.0f, lane < head, lane);
-  p += head;
-  int64_t i = w0;
-  constexpr int kAhead = 4;  // vectors of a lane that are on their way
-  auto vector = [&](const float (&v)[V], int64_t from) {
-    float top = v[0];
+  const int rest = a.vocab - head;
+  const int64_t lo = (int64_t)blockIdx.x * part_logits<T>(kVectors);
+  auto first = [&](int u) { return lo + ((int64_t)u * kScanThreads + threadIdx.x) * V; };  // behind the head
+  Logits<T> x[kVectors];
 #pragma unroll
-    for (int j = 1; j < V; ++j) top = fmaxf(top, v[j]);
-    soft.add(v, top);
-    for (uint32_t todo = __ballot_sync(0xffffffffu, top > best.least); todo; todo &= todo - 1) {
-      const int l = __ffs(todo) - 1;
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float c = __shfl_sync(0xffffffffu, v[j], l);
-        if (c > best.least) best.add(c, (int)(head + from + l * V + j), a.out, lane);
-      }
-    }
-  };
-  for (; i + kAhead * 32 * V <= w1; i += kAhead * 32 * V) {
-    float v[kAhead][V];
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) Vec16<T>::load_stream(p + i + (u * 32 + lane) * V, v[u]);
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) vector(v[u], i + u * 32 * V);
+  for (int u = 0; u < kVectors; ++u) {
+    if (first(u) + V <= rest) x[u].load(p + head + first(u));
+    else x[u].load_some(p + head + first(u), rest - first(u));
   }
-  for (; i + 32 * V <= w1; i += 32 * V) {
-    float v[V];
-    Vec16<T>::load_stream(p + i + lane * V, v);
-    vector(v, i);
-  }
-  for (; i < w1; i += 32) one(i + lane < w1 ? Act<T>::to_f(p[i + lane]) : 0.0f, i + lane < w1, (int)(head + i + lane));
+  // a logit of the head (warp 0's lanes)
+  const float extra = blockIdx.x == 0 && (int)threadIdx.x < head ? Act<T>::to_f(p[threadIdx.x]) : -INFINITY;
+  float top = extra;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    soft.join(__shfl_xor_sync(0xffffffffu, soft.m, o), __shfl_xor_sync(0xffffffffu, soft.s, o));
-  wx[warp][lane] = best.x;
-  wat[warp][lane] = best.at;
-  if (lane == 0) {
-    wm[warp] = soft.m;
-    wsum[warp] = soft.s;
+  for (int u = 0; u < kVectors; ++u) top = fmaxf(top, x[u].top());
+  if (!(top > -INFINITY)) top = -INFINITY;  // (nothing but NaNs)
+  {  // the warp's maximum and its `out`-th lane maximum
+    uint32_t k = ordered(top), most = 0;
+    for (int r = 0; r < a.out; ++r) {
+      most = __reduce_max_sync(0xffffffffu, k);
+      if (r == 0 && lane == 0) wm[warp] = unordered(most);
+      if (lane == __ffs(__ballot_sync(0xffffffffu, k == most)) - 1) k = 0;
+    }
+    if (lane == 0) wleast[warp] = unordered(most);
+    if (threadIdx.x == 0) held = 0;
   }
   __syncthreads();
-  if (warp != 0) return;
+  float m = wm[0], least = wleast[0];
+#pragma unroll
   for (int w = 1; w < kScanWarps; ++w) {
-    soft.join(wm[w], wsum[w]);
-    const float x = wx[w][lane];
-    const int at = wat[w][lane];
-    for (int r = 0; r < a.out; ++r) {
-      const float c = __shfl_sync(0xffffffffu, x, r);
-      if (!(c > best.least)) break;
-      best.add(c, __shfl_sync(0xffffffffu, at, r), a.out, lane);
-    }
+    m = fmaxf(m, wm[w]);
+    least = fmaxf(least, wleast[w]);
   }
+  auto collect = [&](float v, int index) {
+    const int to = atomicAdd(&held, 1);
+    if (to < kHeld) key[to] = key_of(v, index);
+  };
+  if (least == -INFINITY) least = sizeof(T) == 4 ? -3.402823466e38f : -3.389531390e38f;  // the type's lowest number
+  if (top >= least) {  // which of this thread's logits they are; they are few, and read again
+    if (extra >= least) collect(extra, (int)threadIdx.x);
+    uint32_t bits[2] = {0, 0};
+#pragma unroll
+    for (int u = 0; u < kVectors; ++u) x[u].reach(least, u, bits);
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half)
+#pragma unroll 1
+      for (uint32_t todo = bits[half]; todo; todo &= todo - 1) {
+        const int e = Logits<T>::element(half, __ffs(todo) - 1), at = (int)(first(e / V) + e % V);
+        collect(Act<T>::to_f(p[head + at]), head + at);
+      }
+  }
+  const float base = m == -INFINITY ? 0.0f : m, off = -base * kLog2e;
+  float sum = ex2(fmaf(extra, kLog2e, off)), part[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int u = 0; u < kVectors; ++u)
+#pragma unroll
+    for (int j = 0; j < V; ++j) part[j & 1] += ex2(fmaf(x[u].at(j), kLog2e, off));
+  sum += part[0] + part[1];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) wsum[warp] = sum;
+  __syncthreads();
   const PartOut o = part_at(a.ws, row * gridDim.x + blockIdx.x, a.out);
-  if (lane == 0) {
-    *o.m = soft.m;
-    *o.s = soft.s;
+  int n = held;
+  if (n > kHeld) {  // warp by warp, in the order of their indices: each its own logits, a vector of all lanes at a time
+    Best best;
+    best.clear();
+    for (uint32_t todo = __ballot_sync(0xffffffffu, extra > best.least); todo; todo &= todo - 1) {
+      const int from = __ffs(todo) - 1;
+      const float c = __shfl_sync(0xffffffffu, extra, from);
+      if (c > best.least) best.add(c, from, a.out, lane);
+    }
+#pragma unroll
+    for (int u = 0; u < kVectors; ++u)
+      for (uint32_t todo = __ballot_sync(0xffffffffu, x[u].top() > best.least); todo; todo &= todo - 1) {
+        const int from = __ffs(todo) - 1;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float c = __shfl_sync(0xffffffffu, x[u].at(j), from);
+          if (c > best.least)
+            best.add(c, (int)(head + lo + ((int64_t)u * kScanThreads + warp * 32 + from) * V + j), a.out, lane);
+        }
+      }
+    __syncthreads();  // everyone has read `held`
+    if (threadIdx.x == 0) held = 0;
+    __syncthreads();
+    if (best.at >= 0) key[atomicAdd(&held, 1)] = key_of(best.x, best.at);
+    __syncthreads();
+    n = held;
   }
-  if (lane < a.out) {
-    o.x[lane] = best.x;
-    o.at[lane] = best.at;
+  if (threadIdx.x == 0) {
+    float total = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kScanWarps; ++w) total += wsum[w];
+    *o.m = m;
+    *o.s = total;
+    key[n] = key[n + 1] = 0;  // (no key is as small)
+  }
+  for (int e = threadIdx.x + n; e < a.out; e += kScanThreads) {  // fewer logits than are asked for
+    o.x[e] = -INFINITY;
+    o.at[e] = -1;
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < n; e += kScanThreads) {
+    const uint64_t mine = key[e];
+    int before = 0;
+#pragma unroll 4
+    for (int c = 0; c < n; c += 2) {
+      const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(key + c);
+      before += (two.x > mine ? 1 : 0) + (two.y > mine ? 1 : 0);
+    }
+    if (before < a.out) {
+      o.x[before] = key_logit(mine);
+      o.at[before] = key_index(mine);
+    }
   }
 }
 
-// A warp a beam, a CTA a sequence.
+// A warp a beam, a CTA a sequence. kNear entries of a part's list are held in shared memory; it is rare that more of one
+// are among the largest of the row.
+constexpr int kNear = 8;
+
 __global__ void __launch_bounds__(32 * kMost) beam_rank_kernel(const __grid_constant__ BeamArgs a, int parts) {
-  __shared__ double value[kMost * kMost];
+  extern __shared__ __align__(16) uint64_t near_keys[];  // [beams][31][kNear]
+  __shared__ int64_t value[kMost * kMost];  // (compared as integers: a warp takes 16 cycles to compare doubles)
   __shared__ int token[kMost * kMost];
+  __shared__ int before[kMost * kMost];
+  __shared__ double lses[kMost];
+  __shared__ float tops[kMost], totals[kMost];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int beam = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t row = (int64_t)blockIdx.x * a.beams + beam;
   const float score = a.scores[row];
   const bool done = a.finished && a.finished[row];
-  Best best;
-  best.clear();
-  double total = 0.0, m = -INFINITY;
+  uint64_t* near = near_keys + beam * (31 * kNear);
+  const int held = min(a.out, kNear);
+  uint64_t list = 0;  // the row's `lane`-th largest logit; 0: none
+  float m = -INFINITY, total = 0.0f;
   if (!done) {
-    for (int p = lane; p < parts; p += 32) m = fmax(m, (double)*part_at(a.ws, row * parts + p, a.out).m);
+    // parts 31 at a time, a lane each, merged with what the row has so far: the largest head is taken `out` times
+    for (int p0 = 0; p0 < parts; p0 += 31) {
+      const int count = min(31, parts - p0);
+      auto entry = [&](int p, int e) {
+        const PartOut q = part_at(a.ws, row * parts + p0 + p, a.out);
+        const int at = q.at[e];
+        const float x = q.x[e];
+        return at >= 0 ? key_of(x, at) : 0;
+      };
+      const bool mine = lane < count;
+      const PartOut q = part_at(a.ws, row * parts + p0 + (mine ? lane : 0), a.out);
+      const float pm = mine ? *q.m : -INFINITY, ps = mine ? *q.s : 0.0f;
+      for (int e = lane; e < count * held; e += 32) near[e / held * kNear + e % held] = entry(e / held, e % held);
+      __syncwarp();
+      float to = pm;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
-    for (int p = lane; p < parts; p += 32) {
-      const PartOut q = part_at(a.ws, row * parts + p, a.out);
-      const float pm = *q.m, ps = *q.s;
-      total += pm == -INFINITY ? (double)ps : (double)ps * exp((double)pm - m);  // (an empty part's sum is 0, or NaN)
-    }
+      for (int o = 16; o > 0; o >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, o));
+      to = fmaxf(to, m);
+      float s = pm == -INFINITY ? ps : ps * ex2((pm - to) * kLog2e);  // (an empty part's sum is 0, or NaN)
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    for (int p = 0; p < parts; ++p) {  // ascending, so ties stay in order
-      const PartOut q = part_at(a.ws, row * parts + p, a.out);
-      const float x = lane < a.out ? q.x[lane] : -INFINITY;
-      const int at = lane < a.out ? q.at[lane] : -1;
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      total = (m == -INFINITY ? total : total * ex2((m - to) * kLog2e)) + s;
+      m = to;
+      // (what the row has so far stands in lane 31)
+      const uint64_t so_far = list;
+      const uint64_t first = __shfl_sync(0xffffffffu, so_far, 0);
+      uint64_t head = mine ? near[lane * kNear] : lane == 31 ? first : 0;
+      int next = 1;
       for (int r = 0; r < a.out; ++r) {
-        const float c = __shfl_sync(0xffffffffu, x, r);
-        if (!(c > best.least)) break;
-        best.add(c, __shfl_sync(0xffffffffu, at, r), a.out, lane);
+        const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(head >> 32));
+        const uint32_t low = __reduce_max_sync(0xffffffffu, (uint32_t)(head >> 32) == hi ? (uint32_t)head : 0u);
+        const uint64_t best = (uint64_t)hi << 32 | low;
+        if (lane == r) list = best;
+        const int from = __ffs(__ballot_sync(0xffffffffu, head == best)) - 1;
+        const uint64_t follow = __shfl_sync(0xffffffffu, so_far, min(__shfl_sync(0xffffffffu, next, 31), 31));
+        if (lane == from && best != 0) {
+          if (lane == 31) head = next < a.out ? follow : 0;
+          else head = next >= a.out ? 0 : next < kNear ? near[lane * kNear + next] : entry(lane, next);
+          ++next;
+        }
       }
+      __syncwarp();
     }
   }
-  const double lse = m + log(total);
+  for (int c = threadIdx.x; c < a.beams * a.out; c += blockDim.x) before[c] = 0;
+  if (lane == 0) {
+    tops[beam] = m;
+    totals[beam] = total;
+  }
+  __syncthreads();
+  if (beam == 0 && lane < a.beams) lses[lane] = (double)tops[lane] + log((double)totals[lane]);
+  __syncthreads();
+  const double lse = lses[beam];
   double v = -INFINITY;
   int at = -1;
   if (done) {
@@ -225,60 +358,65 @@ __global__ void __launch_bounds__(32 * kMost) beam_rank_kernel(const __grid_cons
       v = score;
       at = a.eos;
     }
-  } else if (lane < a.out && best.x > -INFINITY) {
-    v = (double)score + ((double)best.x - lse);
-    at = best.at;
+  } else if (list != 0 && lane < a.out) {
+    v = (double)score + ((double)key_logit(list) - lse);
+    at = key_index(list);
   }
   // what is not a number, or -infinity, is no better than any token: the row goes on with its lowest ones that are not
   // in the list already (a dead row's list counts as empty)
   if (!(v > -INFINITY)) at = -1;
   const int real = __popc(__ballot_sync(0xffffffffu, at >= 0));
-  if (lane >= real) {  // the (lane - real + 1)-th token that is not among the first `real`
-    v = -INFINITY;
-    at = -1;
-  }
+  if (lane >= real) v = -INFINITY;
   int free_at = lane - real;
-  for (int pass = 0; pass < real; ++pass) {  // the number of listed tokens at or below the candidate settles it
+  for (int pass = 0; pass < real && real < a.out; ++pass) {  // the number of listed tokens at or below it settles it
     int below = 0;
     for (int r = 0; r < real; ++r) below += __shfl_sync(0xffffffffu, at, r) <= free_at ? 1 : 0;
     free_at = lane - real + below;
   }
-  if (lane >= real && lane < a.out && free_at < a.vocab) at = free_at;
+  if (lane >= real) at = lane < a.out && free_at < a.vocab ? free_at : -1;
   if (lane < a.out) {
-    value[beam * a.out + lane] = v;
+    value[beam * a.out + lane] = ordered(v);
     token[beam * a.out + lane] = at;
   }
   __syncthreads();
+  // Of each beam's list, which is in order, what comes before a candidate is counted by bisection: a thread a candidate
+  // and a list.
   const int all = a.beams * a.out;
+  for (int i = threadIdx.x; i < all * a.beams; i += blockDim.x) {
+    const int c = i % all, ob = i / all, b = c / a.out;
+    const int64_t mine = value[c];
+    auto ahead = [&](int r) {  // is entry r of that list there, and before this candidate?
+      if (r >= a.out || token[ob * a.out + r] < 0) return false;
+      const int64_t ov = value[ob * a.out + r];
+      return ov > mine || (ov == mine && ob < b);
+    };
+    int n = 0;
+#pragma unroll
+    for (int step = kMost / 2; step > 0; step >>= 1)
+      if (ahead(n + step - 1)) n += step;
+    n += ahead(n) ? 1 : 0;  // (31 is the most that the steps add up to)
+    atomicAdd(&before[c], ob == b ? c - b * a.out : n);
+  }
+  __syncthreads();
   for (int c = threadIdx.x; c < all; c += blockDim.x) {
-    const double mine = value[c];
     const int t = token[c], b = c / a.out;
-    if (t < 0) continue;  // (a vocabulary smaller than `out`)
-    int before = 0;
-    for (int o = 0; o < all; ++o) {
-      const int ot = token[o], ob = o / a.out;
-      const double ov = value[o];
-      before += ot >= 0 && (ov > mine || (ov == mine && (ob < b || (ob == b && ot < t)))) ? 1 : 0;
-    }
-    if (before < a.out) {
-      const int64_t to = (int64_t)blockIdx.x * a.out + before;
-      a.scores_out[to] = (float)mine;
-      a.parents[to] = b;
-      a.tokens[to] = t;
-      if (a.finished_out)
-        a.finished_out[to] = (a.finished && a.finished[(int64_t)blockIdx.x * a.beams + b]) || t == a.eos ? 1 : 0;
-    }
+    if (t < 0 || before[c] >= a.out) continue;  // (no token: a vocabulary smaller than `out`)
+    const int64_t to = (int64_t)blockIdx.x * a.out + before[c];
+    a.scores_out[to] = (float)unordered(value[c]);
+    a.parents[to] = b;
+    a.tokens[to] = t;
+    if (a.finished_out)
+      a.finished_out[to] = (a.finished && a.finished[(int64_t)blockIdx.x * a.beams + b]) || t == a.eos ? 1 : 0;
   }
 }
 
-// Parts of a row: as many as give every SM four CTAs, of kPartMin logits at least.
-int beam_parts(int64_t rows, int vocab) {
-  const int64_t want = std::max<int64_t>(1, 4 * (int64_t)device_sm_count() / std::max<int64_t>(rows, 1));
-  return (int)std::max<int64_t>(1, std::min<int64_t>(want, (vocab + kPartMin - 1) / kPartMin));
+int beam_vectors(int64_t rows, int vocab) {
+  return rows * (vocab / (kScanThreads * 8 * 8)) >= 4 * (int64_t)device_sm_count() ? kMany : kFew;
 }
-int part_size(int parts, int vocab) {  // whole vectors of every warp
-  const int64_t unit = kScanWarps * 32 * 8;
-  return (int)(((int64_t)vocab + parts * unit - 1) / (parts * unit) * unit);
+// Parts of a row; for the workspace those of fp32 logits, which are the more.
+int beam_parts(int64_t rows, int vocab, mamba2_dtype act) {
+  const int64_t part = act == MAMBA2_F32 ? part_logits<float>(beam_vectors(rows, vocab)) : part_logits<__nv_bfloat16>(beam_vectors(rows, vocab));
+  return (int)((vocab + part - 1) / part);
 }
 
 // ------------------------------------------------------------------ reordering
@@ -355,8 +493,13 @@ __global__ void __launch_bounds__(MAMBA2_MAX_SEQS) reorder_check_kernel(const __
                 : off ? MAMBA2_ERR_INVALID_ARGUMENT : MAMBA2_OK;
 }
 
-cudaError_t start(const void* kernel, dim3 grid, int threads, void** args, cudaStream_t st) {
+cudaError_t start(const void* kernel, dim3 grid, int threads, size_t smem, void** args, cudaStream_t st) {
+  if (smem > 36 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
+  cfg.dynamicSmemBytes = smem;
   cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
   cfg.stream = st;
@@ -371,20 +514,26 @@ cudaError_t start(const void* kernel, dim3 grid, int threads, void** args, cudaS
 }  // namespace
 
 size_t beam_workspace(int64_t rows, int32_t out, int32_t vocab) {
-  return (size_t)rows * beam_parts(rows, vocab) * part_words(out) * 4;
+  return (size_t)rows * beam_parts(rows, vocab, MAMBA2_F32) * part_words(out) * 4;
 }
 
 cudaError_t launch_beam_select(const BeamArgs& args, mamba2_dtype act, cudaStream_t st) {
   BeamArgs a = args;
   const int64_t rows = (int64_t)a.batch * a.beams;
-  int parts = beam_parts(rows, a.vocab), part = part_size(parts, a.vocab);
-  const void* scan = act == MAMBA2_BF16 ? reinterpret_cast<const void*>(beam_scan_kernel<__nv_bfloat16>)
-                                        : reinterpret_cast<const void*>(beam_scan_kernel<float>);
-  void* first[] = {&a, &part};
-  cudaError_t e = start(scan, dim3((unsigned)parts, (unsigned)rows), kScanThreads, first, st);
+  int parts = beam_parts(rows, a.vocab, act);
+  const bool many = beam_vectors(rows, a.vocab) == kMany;
+  const void* scan;
+  if (act == MAMBA2_BF16)
+    scan = many ? reinterpret_cast<const void*>(beam_scan_kernel<__nv_bfloat16, kMany>)
+                : reinterpret_cast<const void*>(beam_scan_kernel<__nv_bfloat16, kFew>);
+  else
+    scan = many ? reinterpret_cast<const void*>(beam_scan_kernel<float, kMany>) : reinterpret_cast<const void*>(beam_scan_kernel<float, kFew>);
+  void* first[] = {&a};
+  cudaError_t e = start(scan, dim3((unsigned)parts, (unsigned)rows), kScanThreads, 0, first, st);
   if (e != cudaSuccess) return e;
   void* second[] = {&a, &parts};
-  return start(reinterpret_cast<const void*>(beam_rank_kernel), dim3((unsigned)a.batch), 32 * a.beams, second, st);
+  return start(reinterpret_cast<const void*>(beam_rank_kernel), dim3((unsigned)a.batch), 32 * a.beams,
+               (size_t)a.beams * 31 * kNear * sizeof(uint64_t), second, st);
 }
 
 cudaError_t launch_reorder(const ReorderArgs& a, cudaStream_t st) {
