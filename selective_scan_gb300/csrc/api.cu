@@ -322,7 +322,8 @@ mamba2_status mamba2_selftest_bounded_wait(int32_t* status_dev, void* stream) {
 
 unsigned int mamba2_device_timeouts(void) {
   const unsigned int counts[] = {read_device_timeouts(), read_gemm_timeouts(), read_m3_timeouts(),
-                                 read_linear_timeouts(), read_recurrence_timeouts()};
+                                 read_linear_timeouts(), read_recurrence_timeouts(), read_delta_timeouts(),
+                                 read_delta_back_timeouts()};
   unsigned int sum = 0;
   for (const unsigned int c : counts) {
     if (c == 0xffffffffu) return c;

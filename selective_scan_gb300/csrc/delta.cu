@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kThreads) delta_serial_kernel(const __grid_con
   constexpr int unit = 16 / sizeof(T), kTile = sizeof(T) * DK > 512 ? 8 : 16;
   __shared__ __align__(16) T sk[2][kTile][DK], sq[2][kTile][DK], sv[2][kTile][kRowsCta];
   __shared__ float sg[2][kTile], sb[2][kTile];
-  const int i = blockIdx.z, h = blockIdx.y, grp = h / (a.heads / a.groups);
+  const int i = a.order[blockIdx.z], h = blockIdx.y, grp = h / (a.heads / a.groups);
   const int row0 = blockIdx.x * kRowsCta, lane = threadIdx.x % kLanes;
   const int mine = (int)threadIdx.x / kLanes * kRowsThread, row = row0 + mine;
   const bool live = row < a.dv;  // (dv is even)

@@ -32,9 +32,17 @@ int64_t count_chunks(const int32_t* cu, int32_t n) {
   return total;
 }
 
-void fill_chunks(SeqTable& t) {
+void fill_chunks(DeltaArgs& a) {
+  SeqTable& t = a.tab;
   t.tile[0] = 0;
-  for (int i = 0; i < t.n; ++i) t.tile[i + 1] = t.tile[i] + (int32_t)chunks_of((int64_t)t.cu[i + 1] - t.cu[i]);
+  for (int i = 0; i < t.n; ++i) {
+    t.tile[i + 1] = t.tile[i] + (int32_t)chunks_of((int64_t)t.cu[i + 1] - t.cu[i]);
+    a.order[i] = (uint16_t)i;
+  }
+  std::sort(a.order, a.order + t.n, [&](int x, int y) {
+    const int32_t lx = t.cu[x + 1] - t.cu[x], ly = t.cu[y + 1] - t.cu[y];
+    return lx != ly ? lx > ly : x < y;
+  });
 }
 
 // Sizes that make sense, then those that the kernels take. (Heads are a grid dimension.)
@@ -128,7 +136,7 @@ mamba2_status mamba2_gated_delta_rule(void* y, float* checkpoints, const void* q
   fill(a, y, q, k, v, g, beta, state, ld_y, ld_q, ld_k, ld_v, dims, scale, l2_eps);
   a.ckpt = checkpoints;
   fill_table(a.tab, rb);
-  fill_chunks(a.tab);
+  fill_chunks(a);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   return done(delta_chunked_supported(act, a.dv, a.dk) ? launch_delta_chunked(a, workspace, st) : launch_delta_serial(a, act, st));
 }
@@ -252,7 +260,7 @@ mamba2_status mamba2_gated_delta_rule_backward(void* dq, void* dk, void* dv, voi
   a.ld_dy = ld_dy;
   a.tab.n = num_seqs;
   for (int i = 0; i <= num_seqs; ++i) a.tab.cu[i] = cu_seqlens[i];
-  fill_chunks(a.tab);
+  fill_chunks(a);
   return done(launch_delta_backward(a, workspace, static_cast<cudaStream_t>(stream)));
 }
 

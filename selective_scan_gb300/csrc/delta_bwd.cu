@@ -18,9 +18,13 @@
 
 #include "../../include/delta.h"
 #include "common.cuh"
+#include "delta_tiles.h"
 #include "host.h"
 
 namespace mamba2 {
+
+__device__ unsigned int g_delta_back_timeouts = 0;
+
 namespace {
 
 #include "delta_mma.cuh"
@@ -30,23 +34,30 @@ using bf16 = __nv_bfloat16;
 // ------------------------------------------------------------------ dS through the chunks
 
 template <int DK, int NW>
-struct Back {
-  static constexpr int kTile = kC * DK * 2;
-  static constexpr int kQ = kTile, kRec = 2 * kTile, kDO = kRec + record_bytes(true);
-  static constexpr int kStage = kDO + NW * kC * 32;
-  static constexpr int kSmem = 2 * kStage;
+struct Back : Stages<DK, true, NW> {
+  static constexpr int kOffBar = Stages<DK, true, NW>::kEnd, kSmem = kOffBar + 32;
 };
 
 template <int DK, int NW>
-__global__ void __launch_bounds__(32 * NW) delta_back_kernel(const __grid_constant__ DeltaBwdArgs a, const unsigned char* records, bf16* ds) {
+__global__ void __launch_bounds__(32 * NW) delta_back_kernel(const __grid_constant__ DeltaBwdArgs a, const __grid_constant__ DeltaMaps maps, const unsigned char* records, bf16* ds) {
   using L = Back<DK, NW>;
-  constexpr int kThreads = 32 * NW, KS = DK / 16;
-  extern __shared__ __align__(128) unsigned char smem[];
+  constexpr int KS = DK / 16;
+  extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t base = sm32(smem);
+  if (not_aligned(base, &g_delta_back_timeouts)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int run = blockIdx.z, h = blockIdx.y, grp = h / (a.heads / a.groups);
+  const int run = a.order[blockIdx.z], h = blockIdx.y, grp = h / (a.heads / a.groups);
   const int dv0 = blockIdx.x * 16 * NW, dv = dv0 + 16 * warp;
   const int first = a.tab.cu[run], len = a.tab.cu[run + 1] - first, n = (len + kC - 1) / kC;
+  auto bar = [&](int ch) { return base + L::kOffBar + 8u * (uint32_t)(ch & 1); };
+  volatile uint32_t* gave_up = reinterpret_cast<volatile uint32_t*>(smem + L::kOffBar + 16);
+  if (threadIdx.x == 0) {
+    bar_init(bar(0), 32);
+    bar_init(bar(1), 32);
+    *gave_up = 0u;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
   float s[2 * KS][4];  // dS: rows dv + g and + 8, columns 8 n + 2 t and + 1
   const int64_t at0 = (int64_t)(dv + g) * a.dk + 2 * t, mine = ((int64_t)run * a.heads + h) * a.dv * a.dk;
   auto each = [&](auto f) {
@@ -67,37 +78,21 @@ __global__ void __launch_bounds__(32 * NW) delta_back_kernel(const __grid_consta
       v[0] = f.x;
       v[1] = f.y;
     });
-  auto fetch = [&](int ch) {
-    const uint32_t to = base + (uint32_t)(ch & 1) * L::kStage;
-    const int64_t row0 = first + (int64_t)ch * kC;
-    const int m = min(kC, len - ch * kC);
-    constexpr int units = DK / 8;
-    const bf16* k = static_cast<const bf16*>(a.k) + (int64_t)grp * a.dk;
-    const bf16* q = static_cast<const bf16*>(a.q) + (int64_t)grp * a.dk;
-    for (int e = threadIdx.x; e < kC * units; e += kThreads) {
-      const int r = e / units, u = e % units;
-      const bool in = r < m && 8 * u < a.dk;
-      const int64_t row = row0 + (in ? r : 0);
-      const int col = in ? 8 * u : 0;
-      copy16(to + wide_at<DK>(r, u), k + row * a.ld_k + col, in);
-      copy16(to + L::kQ + wide_at<DK>(r, u), q + row * a.ld_q + col, in);
-    }
-    const unsigned char* rec = records + ((int64_t)(a.tab.tile[run] + ch) * a.heads + h) * record_bytes(true);
-    for (int e = threadIdx.x; e < record_bytes(true) / 16; e += kThreads) copy16(to + L::kRec + 16 * e, rec + 16 * e, true);
-    const bf16* d = static_cast<const bf16*>(a.dy) + (int64_t)h * a.dv + dv0;
-    for (int e = threadIdx.x; e < kC * 2 * NW; e += kThreads) {
-      const int r = e / (2 * NW), u = e % (2 * NW);
-      const bool in = r < m && dv0 + 8 * u < a.dv;
-      copy16(to + L::kDO + (u >> 1) * (kC * 32) + narrow_at(r, u & 1), d + (row0 + (in ? r : 0)) * a.ld_dy + (in ? 8 * u : 0), in);
-    }
-    copies_end();
+  auto fetch = [&](int ch) {  // (warp 0)
+    load_stage<DK, true, NW>(ch, base, bar(ch), a, maps, a.dy, a.ld_dy,
+                             records + ((int64_t)(a.tab.tile[run] + ch) * a.heads + h) * record_bytes(true),
+                             first + (int64_t)ch * kC, min(kC, len - ch * kC), grp, h, dv0, lane);
   };
-  if (n > 0) fetch(n - 1);
+  if (n > 0 && warp == 0) fetch(n - 1);
   for (int ch = n - 1; ch >= 0; --ch) {
-    copies_done();
-    __syncthreads();
-    if (ch > 0) fetch(ch - 1);
-    const uint32_t at = base + (uint32_t)(ch & 1) * L::kStage, rec = at + L::kRec, dt = at + L::kDO + warp * (kC * 32);
+    if (ch < n - 1) {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (dv was written where another chunk's dO comes)
+      __syncthreads();  // every warp is done with the other stage
+    }
+    if (ch > 0 && warp == 0) fetch(ch - 1);
+    bar_wait(bar(ch), (uint32_t)(((n - 1 - ch) >> 1) & 1), gave_up);
+    __syncwarp();
+    const uint32_t at = base + L::k(ch), qt = base + L::q(ch), rec = base + L::rec(ch), dt = base + L::v(ch) + warp * L::kStrip;
     const float* f = reinterpret_cast<const float*>(smem + (rec - base) + off_factors(true));
     {  // dS1, for the gradients that take it as an operand (rounded as such)
       bf16* o = ds + ((int64_t)(a.tab.tile[run] + ch) * a.heads + h) * a.dv * a.dk;
@@ -116,7 +111,7 @@ __global__ void __launch_bounds__(32 * NW) delta_back_kernel(const __grid_consta
       for (int j = 0; j < 4; ++j) split(s[2 * ks + (j >> 1)][2 * (j & 1)], s[2 * ks + (j >> 1)][2 * (j & 1) + 1], sh[j], sl[j]);
 #pragma unroll
       for (int nb = 0; nb < 4; ++nb) {
-        load4(b, at + wide_rows<DK>(16 * nb, 2 * ks, lane));
+        load4(b, at + wide_rows(16 * nb, 2 * ks, lane));
         mma(x[2 * nb], sh, b[0], b[1]);
         mma(x[2 * nb + 1], sh, b[2], b[3]);
         mma(x[2 * nb], sl, b[0], b[1]);
@@ -195,12 +190,12 @@ __global__ void __launch_bounds__(32 * NW) delta_back_kernel(const __grid_consta
 #pragma unroll
       for (int nb = 0; nb < KS; ++nb) {
         uint32_t b[4];
-        load4t(b, at + L::kQ + wide_cols<DK>(16 * jb, 2 * nb, lane));
+        load4t(b, qt + wide_cols(16 * jb, 2 * nb, lane));
         mma(s[2 * nb], oh, b[0], b[1]);
         mma(s[2 * nb + 1], oh, b[2], b[3]);
         mma(s[2 * nb], ol, b[0], b[1]);
         mma(s[2 * nb + 1], ol, b[2], b[3]);
-        load4t(b, at + wide_cols<DK>(16 * jb, 2 * nb, lane));
+        load4t(b, at + wide_cols(16 * jb, 2 * nb, lane));
         mma(s[2 * nb], vh, b[0], b[1]);
         mma(s[2 * nb + 1], vh, b[2], b[3]);
         mma(s[2 * nb], vl, b[0], b[1]);
@@ -224,6 +219,7 @@ __global__ void __launch_bounds__(32 * NW) delta_back_kernel(const __grid_consta
     }
   }
   if (a.dstate) each([&](float* v, int64_t at) { *reinterpret_cast<float2*>(a.dstate + mine + at) = make_float2(v[0], v[1]); });
+  if (lane == 0 && *gave_up) atomicAdd(&g_delta_back_timeouts, 1u);
 }
 
 // ------------------------------------------------------------------ the other gradients
@@ -273,7 +269,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
     for (int e = threadIdx.x; e < kC * units; e += kGradThreads) {
       const int r = e / units, u = e % units;
       const bool in = r < c.len && 8 * u < width;
-      copy16(base + to + wide_at<C>(r, u), p + (int64_t)(c.row + (in ? r : 0)) * ld + (in ? 8 * u : 0), in);
+      copy16(base + to + wide_at(r, u), p + (int64_t)(c.row + (in ? r : 0)) * ld + (in ? 8 * u : 0), in);
     }
   };
   tile(L::kK, a.k, a.ld_k, (int64_t)grp * a.dk, a.dk, std::integral_constant<int, DK>{});
@@ -287,7 +283,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
   // the pair of a [64][C] tile that this thread's sum (column tile i of its half, row g + 8 e) is of
   auto pair_at = [&](uint32_t tile_off, int i, int e, auto cols) -> uint32_t* {
     constexpr int C = decltype(cols)::value;
-    return reinterpret_cast<uint32_t*>(smem + tile_off + wide_at<C>(r0 + g + 8 * e, half * (C / 16) + i) + 4 * t);
+    return reinterpret_cast<uint32_t*>(smem + tile_off + wide_at(r0 + g + 8 * e, half * (C / 16) + i) + 4 * t);
   };
   constexpr std::integral_constant<int, DK> wide_k{};
   constexpr std::integral_constant<int, DV> wide_v{};
@@ -320,8 +316,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
           for (int j = 0; j < 8; ++j) dot = fmaf(v[j], d[j], dot);
           w0 = Vec16<bf16>::pack(v);
         }
-        *reinterpret_cast<uint4*>(smem + L::kS0 + wide_at<DK>(r, u)) = w0;
-        *reinterpret_cast<uint4*>(smem + L::kDS + wide_at<DK>(r, u)) = w1;
+        *reinterpret_cast<uint4*>(smem + L::kS0 + wide_at<DV>(r, u)) = w0;
+        *reinterpret_cast<uint4*>(smem + L::kDS + wide_at<DV>(r, u)) = w1;
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
@@ -337,11 +333,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         uint32_t x[4], b[4];
-        load4(x, base + (half ? L::kK : L::kQ) + wide_cols<DK>(r0, 2 * ks, lane));
+        load4(x, base + (half ? L::kK : L::kQ) + wide_cols(r0, 2 * ks, lane));
 #pragma unroll
         for (int nb = 0; nb < 4; ++nb)
           if (nb <= rb) {
-            load4(b, base + L::kK + wide_rows<DK>(16 * nb, 2 * ks, lane));
+            load4(b, base + L::kK + wide_rows(16 * nb, 2 * ks, lane));
             mma(qk[2 * nb], x, b[0], b[1]);
             mma(qk[2 * nb + 1], x, b[2], b[3]);
           }
@@ -357,10 +353,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         uint32_t k[4], b[4];
-        load4(k, base + L::kK + wide_cols<DK>(r0, 2 * ks, lane));
+        load4(k, base + L::kK + wide_cols(r0, 2 * ks, lane));
 #pragma unroll
         for (int nb = 0; nb < NV / 2; ++nb) {
-          load4(b, base + L::kS0 + wide_rows<DK>(half * (DV / 2) + 16 * nb, 2 * ks, lane));
+          load4(b, base + L::kS0 + wide_rows<DV>(half * (DV / 2) + 16 * nb, 2 * ks, lane));
           mma(x[2 * nb], k, b[0], b[1]);
           mma(x[2 * nb + 1], k, b[2], b[3]);
         }
@@ -387,7 +383,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
         load4(w, base + L::kInv + block_at(rb, jb) + narrow_cols(0, lane));
 #pragma unroll
         for (int nb = 0; nb < NV / 2; ++nb) {
-          load4t(b, base + L::kV + wide_cols<DV>(16 * jb, half * (DV / 16) + 2 * nb, lane));
+          load4t(b, base + L::kV + wide_cols(16 * jb, half * (DV / 16) + 2 * nb, lane));
           mma(x[2 * nb], w, b[0], b[1]);
           mma(x[2 * nb + 1], w, b[2], b[3]);
         }
@@ -407,11 +403,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
 #pragma unroll
       for (int ks = 0; ks < VS; ++ks) {
         uint32_t d[4], b[4];
-        load4(d, base + (half ? L::kDV : L::kDO) + wide_cols<DV>(r0, 2 * ks, lane));
+        load4(d, base + (half ? L::kDV : L::kDO) + wide_cols(r0, 2 * ks, lane));
 #pragma unroll
         for (int nb = 0; nb < 4; ++nb)
           if (nb <= rb) {
-            load4(b, base + L::kR + wide_rows<DV>(16 * nb, 2 * ks, lane));
+            load4(b, base + L::kR + wide_rows(16 * nb, 2 * ks, lane));
             mma(x[2 * nb], d, b[0], b[1]);
             mma(x[2 * nb + 1], d, b[2], b[3]);
           }
@@ -440,7 +436,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
                 vec[L::kDiag + at] = w;
               }
             }
-            *reinterpret_cast<uint32_t*>(smem + (half ? L::kE : L::kF) + wide_at<kC>(at, i) + 4 * t) = pair(out[0], out[1]);
+            *reinterpret_cast<uint32_t*>(smem + (half ? L::kE : L::kF) + wide_at(at, i) + 4 * t) = pair(out[0], out[1]);
           }
         }
 #pragma unroll
@@ -465,10 +461,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
 #pragma unroll
         for (int ks = 0; ks < VS; ++ks) {
           uint32_t d[4], b[4];
-          load4(d, base + left + wide_cols<DV>(r0, 2 * ks, lane));
+          load4(d, base + left + wide_cols(r0, 2 * ks, lane));
 #pragma unroll
           for (int nb = 0; nb < NK / 2; ++nb) {
-            load4t(b, base + right + wide_cols<DK>(16 * ks, half * (DK / 16) + 2 * nb, lane));
+            load4t(b, base + right + wide_cols<DV>(16 * ks, half * (DK / 16) + 2 * nb, lane));
             mma(x[2 * nb], d, b[0], b[1]);
             mma(x[2 * nb + 1], d, b[2], b[3]);
           }
@@ -519,11 +515,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
     // within the chunk
     for (int jb = 0; jb <= rb; ++jb) {
       uint32_t w[4], e[4], b[4];
-      load4(w, base + L::kF + wide_cols<kC>(r0, 2 * jb, lane));
-      load4(e, base + L::kE + wide_cols<kC>(r0, 2 * jb, lane));
+      load4(w, base + L::kF + wide_cols(r0, 2 * jb, lane));
+      load4(e, base + L::kE + wide_cols(r0, 2 * jb, lane));
 #pragma unroll
       for (int nb = 0; nb < NK / 2; ++nb) {
-        load4t(b, base + L::kK + wide_cols<DK>(16 * jb, half * (DK / 16) + 2 * nb, lane));
+        load4t(b, base + L::kK + wide_cols(16 * jb, half * (DK / 16) + 2 * nb, lane));
         mma(dq[2 * nb], w, b[0], b[1]);
         mma(dq[2 * nb + 1], w, b[2], b[3]);
         mma(dk[2 * nb], e, b[0], b[1]);
@@ -532,14 +528,14 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
     }
     for (int ib = rb; ib < 4; ++ib) {
       uint32_t w[4], e[4], b[4];
-      load4t(w, base + L::kF + wide_rows<kC>(16 * ib, 2 * rb, lane));
-      load4t(e, base + L::kE + wide_rows<kC>(16 * ib, 2 * rb, lane));
+      load4t(w, base + L::kF + wide_rows(16 * ib, 2 * rb, lane));
+      load4t(e, base + L::kE + wide_rows(16 * ib, 2 * rb, lane));
 #pragma unroll
       for (int nb = 0; nb < NK / 2; ++nb) {
-        load4t(b, base + L::kQ + wide_cols<DK>(16 * ib, half * (DK / 16) + 2 * nb, lane));
+        load4t(b, base + L::kQ + wide_cols(16 * ib, half * (DK / 16) + 2 * nb, lane));
         mma(dk[2 * nb], w, b[0], b[1]);
         mma(dk[2 * nb + 1], w, b[2], b[3]);
-        load4t(b, base + L::kK + wide_cols<DK>(16 * ib, half * (DK / 16) + 2 * nb, lane));
+        load4t(b, base + L::kK + wide_cols(16 * ib, half * (DK / 16) + 2 * nb, lane));
         mma(dk[2 * nb], e, b[0], b[1]);
         mma(dk[2 * nb + 1], e, b[2], b[3]);
       }
@@ -620,20 +616,20 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
     if (r >= c.len || 8 * u >= a.dk) continue;
     const int64_t col = (int64_t)grp * a.dk + 8 * u;
     *reinterpret_cast<uint4*>(static_cast<bf16*>(a.dq) + (int64_t)(c.row + r) * a.ld_dq + col) =
-        *reinterpret_cast<const uint4*>(smem + L::kQ + wide_at<DK>(r, u));
+        *reinterpret_cast<const uint4*>(smem + L::kQ + wide_at(r, u));
     *reinterpret_cast<uint4*>(static_cast<bf16*>(a.dk_out) + (int64_t)(c.row + r) * a.ld_dk + col) =
-        *reinterpret_cast<const uint4*>(smem + L::kK + wide_at<DK>(r, u));
+        *reinterpret_cast<const uint4*>(smem + L::kK + wide_at(r, u));
   }
 }
 
 template <int DK, int NW>
-cudaError_t run_back(const DeltaBwdArgs& a, const unsigned char* records, bf16* ds, cudaStream_t st) {
+cudaError_t run_back(const DeltaBwdArgs& a, const DeltaMaps& maps, const unsigned char* records, bf16* ds, cudaStream_t st) {
   using L = Back<DK, NW>;
   auto kernel = delta_back_kernel<DK, NW>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   if (e != cudaSuccess) return e;
   const dim3 grid((a.dv + 16 * NW - 1) / (16 * NW), a.heads, a.tab.n);
-  kernel<<<grid, 32 * NW, L::kSmem, st>>>(a, records, ds);
+  kernel<<<grid, 32 * NW, L::kSmem, st>>>(a, maps, records, ds);
   return cudaGetLastError();
 }
 
@@ -651,11 +647,13 @@ cudaError_t run_grad(const DeltaBwdArgs& a, const unsigned char* records, const 
 
 template <int DK>
 cudaError_t run_backward(const DeltaBwdArgs& a, const unsigned char* records, bf16* ds, cudaStream_t st) {
+  DeltaMaps maps;
+  if (a.tab.cu[a.tab.n] > 0 && !delta_maps(&maps, a, a.dy, a.ld_dy)) return cudaErrorInvalidValue;
   const int64_t chains = (int64_t)a.tab.n * a.heads, sms = device_sm_count();
   cudaError_t e;
-  if (a.dv > 64 && chains >= sms) e = run_back<DK, 8>(a, records, ds, st);
-  else if (a.dv > 32 && 2 * chains >= sms) e = run_back<DK, 4>(a, records, ds, st);
-  else e = run_back<DK, 2>(a, records, ds, st);
+  if (a.dv > 64 && chains >= sms) e = run_back<DK, 8>(a, maps, records, ds, st);
+  else if (a.dv > 32 && 2 * chains >= sms) e = run_back<DK, 4>(a, maps, records, ds, st);
+  else e = run_back<DK, 2>(a, maps, records, ds, st);
   if (e != cudaSuccess) return e;
   return a.dv <= 64 ? run_grad<DK, 64>(a, records, ds, st) : run_grad<DK, 128>(a, records, ds, st);
 }
@@ -663,6 +661,12 @@ cudaError_t run_backward(const DeltaBwdArgs& a, const unsigned char* records, bf
 size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 
 }  // namespace
+
+unsigned int read_delta_back_timeouts() {
+  unsigned int v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_delta_back_timeouts, sizeof v) != cudaSuccess) return 0xffffffffu;
+  return v;
+}
 
 size_t delta_backward_workspace(int64_t chunks, int heads, int dv, int dk) {
   return round256(delta_records(chunks, heads, true)) + round256((size_t)chunks * heads * dv * dk * 2);

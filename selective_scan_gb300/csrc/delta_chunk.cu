@@ -18,9 +18,13 @@
 
 #include "../../include/delta.h"
 #include "common.cuh"
+#include "delta_tiles.h"
 #include "host.h"
 
 namespace mamba2 {
+
+__device__ unsigned int g_delta_timeouts = 0;
+
 namespace {
 
 #include "delta_mma.cuh"
@@ -71,8 +75,8 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(const __grid_c
       const int r = e / units, u = e % units;
       const bool in = r < c.len && 8 * u < a.dk;
       const int64_t row = c.row + (in ? r : 0), col = in ? 8 * u : 0;
-      copy16(sk + wide_at<DK>(r, u), k + row * a.ld_k + col, in);
-      copy16(sq + wide_at<DK>(r, u), q + row * a.ld_q + col, in);
+      copy16(sk + wide_at(r, u), k + row * a.ld_k + col, in);
+      copy16(sq + wide_at(r, u), q + row * a.ld_q + col, in);
     }
     copies_end();
   }
@@ -103,7 +107,7 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(const __grid_c
       float s = 0.0f;
       for (int u = 0; u < DK / 8; ++u) {
         float v[8];
-        Vec16<bf16>::unpack(*reinterpret_cast<const uint4*>(smem + (is_q ? kC * DK * 2 : 0) + wide_at<DK>(r, u)), v);
+        Vec16<bf16>::unpack(*reinterpret_cast<const uint4*>(smem + (is_q ? kC * DK * 2 : 0) + wide_at(r, u)), v);
 #pragma unroll
         for (int j = 0; j < 8; ++j) s = fmaf(v[j], v[j], s);
       }
@@ -122,12 +126,12 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(const __grid_c
 #pragma unroll
   for (int ks = 0; ks < DK / 16; ++ks) {
     uint32_t ak[4], aq[4], b[4];
-    load4(ak, sk + wide_cols<DK>(r0, 2 * ks, lane));
-    load4(aq, sq + wide_cols<DK>(r0, 2 * ks, lane));
+    load4(ak, sk + wide_cols(r0, 2 * ks, lane));
+    load4(aq, sq + wide_cols(r0, 2 * ks, lane));
 #pragma unroll
     for (int nb = 0; nb < 4; ++nb)
       if (nb <= warp) {
-        load4(b, sk + wide_rows<DK>(16 * nb, 2 * ks, lane));
+        load4(b, sk + wide_rows(16 * nb, 2 * ks, lane));
         mma(kk[2 * nb], ak, b[0], b[1]);
         mma(kk[2 * nb + 1], ak, b[2], b[3]);
         mma(qk[2 * nb], aq, b[0], b[1]);
@@ -274,25 +278,32 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(const __grid_c
 // ------------------------------------------------------------------ the state through the chunks
 
 template <int DK, int NW>
-struct Chain {
-  static constexpr int kTile = kC * DK * 2;
-  static constexpr int kQ = kTile, kRec = 2 * kTile, kV = kRec + record_bytes(false);
-  static constexpr int kStage = kV + NW * kC * 32;
-  static constexpr int kSmem = 2 * kStage;
+struct Chain : Stages<DK, false, NW> {
+  static constexpr int kOffBar = Stages<DK, false, NW>::kEnd, kSmem = kOffBar + 32;
 };
 
 template <int DK, int NW>
-__global__ void __launch_bounds__(32 * NW) delta_chain_kernel(const __grid_constant__ DeltaArgs a, const unsigned char* records) {
+__global__ void __launch_bounds__(32 * NW) delta_chain_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ DeltaMaps maps, const unsigned char* records) {
   using L = Chain<DK, NW>;
-  constexpr int kThreads = 32 * NW, KS = DK / 16;
-  extern __shared__ __align__(128) unsigned char smem[];
+  constexpr int KS = DK / 16;
+  extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t base = sm32(smem);
+  if (not_aligned(base, &g_delta_timeouts)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int run = blockIdx.z, h = blockIdx.y, grp = h / (a.heads / a.groups);
+  const int run = a.order[blockIdx.z], h = blockIdx.y, grp = h / (a.heads / a.groups);
   const int dv0 = blockIdx.x * 16 * NW, dv = dv0 + 16 * warp;  // this CTA's, this warp's first row
   const int first = a.tab.cu[run], len = a.tab.cu[run + 1] - first, n = (len + kC - 1) / kC;
   const bool fresh = seq_fresh(a.tab, run);
   if (len == 0 && !fresh) return;
+  auto bar = [&](int ch) { return base + L::kOffBar + 8u * (uint32_t)(ch & 1); };
+  volatile uint32_t* gave_up = reinterpret_cast<volatile uint32_t*>(smem + L::kOffBar + 16);
+  if (threadIdx.x == 0) {
+    bar_init(bar(0), 32);
+    bar_init(bar(1), 32);
+    *gave_up = 0u;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
   // the state: rows dv + g and + 8, columns 8 n + 2 t and + 1
   float s[2 * KS][4];
   float* st = a.state + ((int64_t)seq_slot(a.tab, run) * a.heads + h) * a.dv * a.dk;
@@ -315,37 +326,21 @@ __global__ void __launch_bounds__(32 * NW) delta_chain_kernel(const __grid_const
       v[0] = f.x;
       v[1] = f.y;
     });
-  auto fetch = [&](int ch) {
-    const uint32_t to = base + (uint32_t)(ch & 1) * L::kStage;
-    const int64_t row0 = first + (int64_t)ch * kC;
-    const int m = min(kC, len - ch * kC);
-    constexpr int units = DK / 8;
-    const bf16* k = static_cast<const bf16*>(a.k) + (int64_t)grp * a.dk;
-    const bf16* q = static_cast<const bf16*>(a.q) + (int64_t)grp * a.dk;
-    for (int e = threadIdx.x; e < kC * units; e += kThreads) {
-      const int r = e / units, u = e % units;
-      const bool in = r < m && 8 * u < a.dk;
-      const int64_t row = row0 + (in ? r : 0);
-      const int col = in ? 8 * u : 0;
-      copy16(to + wide_at<DK>(r, u), k + row * a.ld_k + col, in);
-      copy16(to + L::kQ + wide_at<DK>(r, u), q + row * a.ld_q + col, in);
-    }
-    const unsigned char* rec = records + ((int64_t)(a.tab.tile[run] + ch) * a.heads + h) * record_bytes(false);
-    for (int e = threadIdx.x; e < record_bytes(false) / 16; e += kThreads) copy16(to + L::kRec + 16 * e, rec + 16 * e, true);
-    const bf16* v = static_cast<const bf16*>(a.v) + (int64_t)h * a.dv + dv0;
-    for (int e = threadIdx.x; e < kC * 2 * NW; e += kThreads) {
-      const int r = e / (2 * NW), u = e % (2 * NW);
-      const bool in = r < m && dv0 + 8 * u < a.dv;
-      copy16(to + L::kV + (u >> 1) * (kC * 32) + narrow_at(r, u & 1), v + (row0 + (in ? r : 0)) * a.ld_v + (in ? 8 * u : 0), in);
-    }
-    copies_end();
+  auto fetch = [&](int ch) {  // (warp 0)
+    load_stage<DK, false, NW>(ch, base, bar(ch), a, maps, a.v, a.ld_v,
+                              records + ((int64_t)(a.tab.tile[run] + ch) * a.heads + h) * record_bytes(false),
+                              first + (int64_t)ch * kC, min(kC, len - ch * kC), grp, h, dv0, lane);
   };
-  if (n > 0) fetch(0);
+  if (n > 0 && warp == 0) fetch(0);
   for (int ch = 0; ch < n; ++ch) {
-    copies_done();
-    __syncthreads();  // this chunk's tiles are there, and every warp is done with the other stage
-    if (ch + 1 < n) fetch(ch + 1);
-    const uint32_t at = base + (uint32_t)(ch & 1) * L::kStage, rec = at + L::kRec, vt = at + L::kV + warp * (kC * 32);
+    if (ch > 0) {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (y was written where the next chunk's v comes)
+      __syncthreads();  // every warp is done with the other stage
+    }
+    if (ch + 1 < n && warp == 0) fetch(ch + 1);
+    bar_wait(bar(ch), (uint32_t)((ch >> 1) & 1), gave_up);
+    __syncwarp();
+    const uint32_t at = base + L::k(ch), qt = base + L::q(ch), rec = base + L::rec(ch), vt = base + L::v(ch) + warp * L::kStrip;
     const float* f = reinterpret_cast<const float*>(smem + (rec - base) + off_factors(false));
     if (a.ckpt) {
       float* o = a.ckpt + ((int64_t)(a.tab.tile[run] + ch) * a.heads + h) * a.dv * a.dk;
@@ -359,19 +354,22 @@ __global__ void __launch_bounds__(32 * NW) delta_chain_kernel(const __grid_const
       for (int j = 0; j < 4; ++j) x[i][j] = y[i][j] = 0.0f;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      uint32_t sh[4], sl[4], b[4];
+      uint32_t sh[4], sl[4], b[4][4], c[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) split(s[2 * ks + (j >> 1)][2 * (j & 1)], s[2 * ks + (j >> 1)][2 * (j & 1) + 1], sh[j], sl[j]);
 #pragma unroll
       for (int nb = 0; nb < 4; ++nb) {
-        load4(b, at + wide_rows<DK>(16 * nb, 2 * ks, lane));
-        mma(x[2 * nb], sh, b[0], b[1]);
-        mma(x[2 * nb + 1], sh, b[2], b[3]);
-        mma(x[2 * nb], sl, b[0], b[1]);
-        mma(x[2 * nb + 1], sl, b[2], b[3]);
-        load4(b, at + L::kQ + wide_rows<DK>(16 * nb, 2 * ks, lane));
-        mma(y[2 * nb], sh, b[0], b[1]);
-        mma(y[2 * nb + 1], sh, b[2], b[3]);
+        load4(b[nb], at + wide_rows(16 * nb, 2 * ks, lane));
+        mma(x[2 * nb], sh, b[nb][0], b[nb][1]);
+        mma(x[2 * nb + 1], sh, b[nb][2], b[nb][3]);
+      }
+#pragma unroll
+      for (int nb = 0; nb < 4; ++nb) {
+        load4(c, qt + wide_rows(16 * nb, 2 * ks, lane));
+        mma(y[2 * nb], sh, c[0], c[1]);
+        mma(y[2 * nb + 1], sh, c[2], c[3]);
+        mma(x[2 * nb], sl, b[nb][0], b[nb][1]);
+        mma(x[2 * nb + 1], sl, b[nb][2], b[nb][3]);
       }
     }
     // R = V - up X, as left operands of 16 tokens each
@@ -396,18 +394,26 @@ __global__ void __launch_bounds__(32 * NW) delta_chain_kernel(const __grid_const
       for (int j = 0; j < 4; ++j) x[i][j] = 0.0f;
 #pragma unroll
     for (int jb = 0; jb < 4; ++jb)
+    {
+      uint32_t b[4][4];
 #pragma unroll
       for (int ib = jb; ib < 4; ++ib) {
-        uint32_t bh[4], bl[4];
-        load4(bh, rec + block_at(ib, jb) + narrow_rows(0, lane));
-        load4(bl, rec + kOffInvLo + block_at(ib, jb) + narrow_rows(0, lane));
-        mma(x[2 * ib], ah[jb], bh[0], bh[1]);
-        mma(x[2 * ib + 1], ah[jb], bh[2], bh[3]);
-        mma(x[2 * ib], al[jb], bh[0], bh[1]);
-        mma(x[2 * ib + 1], al[jb], bh[2], bh[3]);
-        mma(x[2 * ib], ah[jb], bl[0], bl[1]);
-        mma(x[2 * ib + 1], ah[jb], bl[2], bl[3]);
+        load4(b[ib], rec + block_at(ib, jb) + narrow_rows(0, lane));
+        mma(x[2 * ib], ah[jb], b[ib][0], b[ib][1]);
+        mma(x[2 * ib + 1], ah[jb], b[ib][2], b[ib][3]);
       }
+#pragma unroll
+      for (int ib = jb; ib < 4; ++ib) {
+        mma(x[2 * ib], al[jb], b[ib][0], b[ib][1]);
+        mma(x[2 * ib + 1], al[jb], b[ib][2], b[ib][3]);
+      }
+#pragma unroll
+      for (int ib = jb; ib < 4; ++ib) {
+        load4(b[ib], rec + kOffInvLo + block_at(ib, jb) + narrow_rows(0, lane));
+        mma(x[2 * ib], ah[jb], b[ib][0], b[ib][1]);
+        mma(x[2 * ib + 1], ah[jb], b[ib][2], b[ib][3]);
+      }
+    }
     // u = beta r; the scores' product takes it as it is, the state's with what is left of it at the chunk's end
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -424,14 +430,17 @@ __global__ void __launch_bounds__(32 * NW) delta_chain_kernel(const __grid_const
       uint32_t uh[4], ul[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) split(x[2 * jb + (j >> 1)][2 * (j & 1)], x[2 * jb + (j >> 1)][2 * (j & 1) + 1], uh[j], ul[j]);
+      uint32_t b[4][4];
 #pragma unroll
       for (int ib = jb; ib < 4; ++ib) {
-        uint32_t b[4];
-        load4(b, rec + kOffP + block_at(ib, jb) + narrow_rows(0, lane));
-        mma(y[2 * ib], uh, b[0], b[1]);
-        mma(y[2 * ib + 1], uh, b[2], b[3]);
-        mma(y[2 * ib], ul, b[0], b[1]);
-        mma(y[2 * ib + 1], ul, b[2], b[3]);
+        load4(b[ib], rec + kOffP + block_at(ib, jb) + narrow_rows(0, lane));
+        mma(y[2 * ib], uh, b[ib][0], b[ib][1]);
+        mma(y[2 * ib + 1], uh, b[ib][2], b[ib][3]);
+      }
+#pragma unroll
+      for (int ib = jb; ib < 4; ++ib) {
+        mma(y[2 * ib], ul, b[ib][0], b[ib][1]);
+        mma(y[2 * ib + 1], ul, b[ib][2], b[ib][3]);
       }
     }
     // S = gamma S + (left u)^T K
@@ -450,13 +459,19 @@ __global__ void __launch_bounds__(32 * NW) delta_chain_kernel(const __grid_const
         split(x[i][2 * (j & 1)] * w.x, x[i][2 * (j & 1) + 1] * w.y, uh[j], ul[j]);
       }
 #pragma unroll
-      for (int nb = 0; nb < KS; ++nb) {
-        uint32_t b[4];
-        load4t(b, at + wide_cols<DK>(16 * jb, 2 * nb, lane));
-        mma(s[2 * nb], uh, b[0], b[1]);
-        mma(s[2 * nb + 1], uh, b[2], b[3]);
-        mma(s[2 * nb], ul, b[0], b[1]);
-        mma(s[2 * nb + 1], ul, b[2], b[3]);
+      for (int n0 = 0; n0 < KS; n0 += 4) {
+        uint32_t b[4][4];
+#pragma unroll
+        for (int nb = 0; nb < 4; ++nb) {
+          load4t(b[nb], at + wide_cols(16 * jb, 2 * (n0 + nb), lane));
+          mma(s[2 * (n0 + nb)], uh, b[nb][0], b[nb][1]);
+          mma(s[2 * (n0 + nb) + 1], uh, b[nb][2], b[nb][3]);
+        }
+#pragma unroll
+        for (int nb = 0; nb < 4; ++nb) {
+          mma(s[2 * (n0 + nb)], ul, b[nb][0], b[nb][1]);
+          mma(s[2 * (n0 + nb) + 1], ul, b[nb][2], b[nb][3]);
+        }
       }
     }
     // y takes the place of the warp's v and goes out a token's 32 bytes at a time
@@ -476,16 +491,301 @@ __global__ void __launch_bounds__(32 * NW) delta_chain_kernel(const __grid_const
     }
   }
   each([&](float* v, int64_t at) { *reinterpret_cast<float2*>(st + at) = make_float2(v[0], v[1]); });
+  if (lane == 0 && *gave_up) atomicAdd(&g_delta_timeouts, 1u);
+}
+
+// ------------------------------------------------------------------ the same with two warps to 16 rows
+//
+// Where there are few chains, a chunk's time is that of its products one after another. Here two warps share 16 rows of
+// the state: each holds one half of its columns, so each has half of the products with K and Q; they add up their parts
+// of X and Y, each takes half of the tokens through Inv and P, and they exchange the u that come out. The first and last
+// 16 tokens are warp 0's, those between warp 1's: both have five of the ten blocks of a triangle.
+template <int DK, int NP>
+struct Pairs : Stages<DK, false, NP> {
+  static constexpr int kMail = 12 * 512;  // of a warp: 48 registers of every lane
+  static constexpr int kOffMail = Stages<DK, false, NP>::kEnd, kOffBar = kOffMail + 2 * NP * kMail;
+  static constexpr int kSmem = kOffBar + 48;
+  enum Bar : int { kFull = 0, kEmpty = 2 };  // + chunk % 2
+};
+
+__device__ __forceinline__ void pair_sync(int pair) { asm volatile("bar.sync %0, 64;" ::"r"(pair + 1) : "memory"); }
+
+template <int DK, int NP>
+__global__ void __launch_bounds__(64 * NP + 32) delta_pairs_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ DeltaMaps maps, const unsigned char* records) {
+  using L = Pairs<DK, NP>;
+  constexpr int KS = DK / 32;  // k-steps of a half
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const uint32_t base = sm32(smem);
+  if (not_aligned(base, &g_delta_timeouts)) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int pr = warp >> 1, half = warp & 1;
+  const int run = a.order[blockIdx.z], h = blockIdx.y, grp = h / (a.heads / a.groups);
+  const int dv0 = blockIdx.x * 16 * NP, dv = dv0 + 16 * pr;
+  const int first = a.tab.cu[run], len = a.tab.cu[run + 1] - first, n = (len + kC - 1) / kC;
+  const bool fresh = seq_fresh(a.tab, run);
+  if (len == 0 && !fresh) return;
+  auto bar = [&](int id) { return base + L::kOffBar + 8u * (uint32_t)id; };
+  volatile uint32_t* gave_up = reinterpret_cast<volatile uint32_t*>(smem + L::kOffBar + 32);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      bar_init(bar(L::kFull + i), 32);
+      bar_init(bar(L::kEmpty + i), 2 * NP);
+    }
+    *gave_up = 0u;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  if (warp == 2 * NP) {
+    for (int ch = 0; ch < n; ++ch) {
+      if (ch >= 2) bar_wait(bar(L::kEmpty + (ch & 1)), (uint32_t)(((ch >> 1) - 1) & 1), gave_up);
+      load_stage<DK, false, NP>(ch, base, bar(L::kFull + (ch & 1)), a, maps, a.v, a.ld_v,
+                                records + ((int64_t)(a.tab.tile[run] + ch) * a.heads + h) * record_bytes(false),
+                                first + (int64_t)ch * kC, min(kC, len - ch * kC), grp, h, dv0, lane);
+    }
+    copies_end();
+    copies_done();
+    return;
+  }
+  const int own[2] = {half, 3 - half};  // this warp's blocks of 16 tokens
+  float s[2 * KS][4];
+  float* st = a.state + ((int64_t)seq_slot(a.tab, run) * a.heads + h) * a.dv * a.dk;
+  const int col0 = half * (DK / 2);
+  const int64_t at0 = (int64_t)(dv + g) * a.dk + col0 + 2 * t;
+  auto each = [&](auto f) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      if (dv + 8 * r < a.dv)
+#pragma unroll
+        for (int i = 0; i < 2 * KS; ++i)
+          if (col0 + 8 * i < a.dk) f(s[i] + 2 * r, at0 + (int64_t)(8 * r) * a.dk + 8 * i);
+  };
+#pragma unroll
+  for (int i = 0; i < 2 * KS; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[i][j] = 0.0f;
+  if (!fresh)
+    each([&](float* v, int64_t at) {
+      const float2 f = *reinterpret_cast<const float2*>(st + at);
+      v[0] = f.x;
+      v[1] = f.y;
+    });
+  unsigned char* mail = smem + L::kOffMail + warp * L::kMail;          // what the other warp reads
+  const unsigned char* post = smem + L::kOffMail + (warp ^ 1) * L::kMail;  // what it has written
+  auto put = [&](int i, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
+    *reinterpret_cast<uint4*>(mail + i * 512 + lane * 16) = make_uint4(w0, w1, w2, w3);
+  };
+  auto get = [&](const unsigned char* from, int i) { return *reinterpret_cast<const uint4*>(from + i * 512 + lane * 16); };
+  for (int ch = 0; ch < n; ++ch) {
+    bar_wait(bar(L::kFull + (ch & 1)), (uint32_t)((ch >> 1) & 1), gave_up);
+    __syncwarp();
+    const uint32_t at = base + L::k(ch), qt = base + L::q(ch), rec = base + L::rec(ch), vt = base + L::v(ch) + pr * L::kStrip;
+    const float* f = reinterpret_cast<const float*>(smem + (rec - base) + off_factors(false));
+    if (a.ckpt) {
+      float* o = a.ckpt + ((int64_t)(a.tab.tile[run] + ch) * a.heads + h) * a.dv * a.dk;
+      each([&](float* v, int64_t to) { *reinterpret_cast<float2*>(o + to) = make_float2(v[0], v[1]); });
+    }
+    float x[8][4], y[8][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[i][j] = y[i][j] = 0.0f;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      uint32_t sh[4], sl[4], b[4][4], c[4];
+      const int unit = half * (DK / 16) + 2 * ks;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) split(s[2 * ks + (j >> 1)][2 * (j & 1)], s[2 * ks + (j >> 1)][2 * (j & 1) + 1], sh[j], sl[j]);
+#pragma unroll
+      for (int nb = 0; nb < 4; ++nb) {
+        load4(b[nb], at + wide_rows(16 * nb, unit, lane));
+        mma(x[2 * nb], sh, b[nb][0], b[nb][1]);
+        mma(x[2 * nb + 1], sh, b[nb][2], b[nb][3]);
+      }
+#pragma unroll
+      for (int nb = 0; nb < 4; ++nb) {
+        load4(c, qt + wide_rows(16 * nb, unit, lane));
+        mma(y[2 * nb], sh, c[0], c[1]);
+        mma(y[2 * nb + 1], sh, c[2], c[3]);
+        mma(x[2 * nb], sl, b[nb][0], b[nb][1]);
+        mma(x[2 * nb + 1], sl, b[nb][2], b[nb][3]);
+      }
+    }
+    pair_sync(pr);  // the other has read its mail of the last chunk
+    // this half's part of X, and of the other's Y
+    float yo[2][2][4];  // Y of this warp's tokens
+#pragma unroll
+    for (int i = 0; i < 8; ++i) put(i, __float_as_uint(x[i][0]), __float_as_uint(x[i][1]), __float_as_uint(x[i][2]), __float_as_uint(x[i][3]));
+#pragma unroll
+    for (int o = 0; o < 2; ++o)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // (block 3 o of the tokens is warp 0's, block 1 + o warp 1's)
+          yo[o][i][j] = half ? y[2 * (1 + o) + i][j] : y[6 * o + i][j];
+          w[j] = __float_as_uint(half ? y[6 * o + i][j] : y[2 * (1 + o) + i][j]);
+        }
+        put(8 + 2 * o + i, w[0], w[1], w[2], w[3]);
+      }
+    pair_sync(pr);
+    auto plus = [&](float (&d)[4], const uint4& w) {
+      d[0] += __uint_as_float(w.x);
+      d[1] += __uint_as_float(w.y);
+      d[2] += __uint_as_float(w.z);
+      d[3] += __uint_as_float(w.w);
+    };
+#pragma unroll
+    for (int i = 0; i < 8; ++i) plus(x[i], get(post, i));
+#pragma unroll
+    for (int o = 0; o < 2; ++o)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) plus(yo[o][i], get(post, 8 + 2 * o + i));
+    // R = V - up X, as left operands of 16 tokens each
+    uint32_t ah[4][4], al[4][4];
+#pragma unroll
+    for (int jb = 0; jb < 4; ++jb) {
+      uint32_t v[4];
+      load4t(v, vt + narrow_cols(16 * jb, lane));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = 2 * jb + (j >> 1);
+        const float2 up = *reinterpret_cast<const float2*>(f + kUp + 8 * i + 2 * t);
+        const uint32_t w = v[(j >> 1) + 2 * (j & 1)];
+        split(fmaf(-up.x, x[i][2 * (j & 1)], __uint_as_float(w << 16)),
+              fmaf(-up.y, x[i][2 * (j & 1) + 1], __uint_as_float(w & 0xffff0000u)), ah[jb][j], al[jb][j]);
+      }
+    }
+    pair_sync(pr);  // both have read the mail
+    // r of this warp's tokens, and from it u: for the scores as it is, for the state with what is left at the chunk's end
+    float r[2][2][4];
+#pragma unroll
+    for (int o = 0; o < 2; ++o)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r[o][i][j] = 0.0f;
+#pragma unroll
+    for (int jb = 0; jb < 4; ++jb) {
+      uint32_t b[2][4], c[2][4];
+#pragma unroll
+      for (int o = 0; o < 2; ++o)
+        if (jb <= own[o]) {
+          load4(b[o], rec + block_at(own[o], jb) + narrow_rows(0, lane));
+          load4(c[o], rec + kOffInvLo + block_at(own[o], jb) + narrow_rows(0, lane));
+          mma(r[o][0], ah[jb], b[o][0], b[o][1]);
+          mma(r[o][1], ah[jb], b[o][2], b[o][3]);
+          mma(r[o][0], al[jb], b[o][0], b[o][1]);
+          mma(r[o][1], al[jb], b[o][2], b[o][3]);
+          mma(r[o][0], ah[jb], c[o][0], c[o][1]);
+          mma(r[o][1], ah[jb], c[o][2], c[o][3]);
+        }
+    }
+#pragma unroll
+    for (int o = 0; o < 2; ++o) {
+      uint32_t uh[4], ul[4], wh[4], wl[4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int tok = 16 * own[o] + 8 * i + 2 * t;
+        const float2 b = *reinterpret_cast<const float2*>(f + kBeta + tok);
+        const float2 left = *reinterpret_cast<const float2*>(f + kLeft + tok);
+        const float2 up = *reinterpret_cast<const float2*>(f + kUpQ + tok);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float u0 = r[o][i][2 * e] * b.x, u1 = r[o][i][2 * e + 1] * b.y;
+          split(u0, u1, uh[2 * i + e], ul[2 * i + e]);
+          split(u0 * left.x, u1 * left.y, wh[2 * i + e], wl[2 * i + e]);
+          yo[o][i][2 * e] *= up.x;
+          yo[o][i][2 * e + 1] *= up.y;
+        }
+      }
+      put(4 * o, uh[0], uh[1], uh[2], uh[3]);
+      put(4 * o + 1, ul[0], ul[1], ul[2], ul[3]);
+      put(4 * o + 2, wh[0], wh[1], wh[2], wh[3]);
+      put(4 * o + 3, wl[0], wl[1], wl[2], wl[3]);
+    }
+    const float gamma = f[kGamma];
+#pragma unroll
+    for (int i = 0; i < 2 * KS; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[i][j] *= gamma;
+    pair_sync(pr);
+#pragma unroll
+    for (int jb = 0; jb < 4; ++jb) {
+      const bool zero = jb == 0 || jb == 3;  // whose block it is, and which of its two
+      const unsigned char* from = (zero ? half == 0 : half == 1) ? mail : post;
+      const int o = jb >> 1;
+      uint32_t b[KS][4];
+      {  // S = gamma S + (left u)^T K
+        const uint4 h4 = get(from, 4 * o + 2), l4 = get(from, 4 * o + 3);
+        const uint32_t wh[4] = {h4.x, h4.y, h4.z, h4.w}, wl[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+        for (int nb = 0; nb < KS; ++nb) {
+          load4t(b[nb], at + wide_cols(16 * jb, half * (DK / 16) + 2 * nb, lane));
+          mma(s[2 * nb], wh, b[nb][0], b[nb][1]);
+          mma(s[2 * nb + 1], wh, b[nb][2], b[nb][3]);
+        }
+#pragma unroll
+        for (int nb = 0; nb < KS; ++nb) {
+          mma(s[2 * nb], wl, b[nb][0], b[nb][1]);
+          mma(s[2 * nb + 1], wl, b[nb][2], b[nb][3]);
+        }
+      }
+      {  // Y = scale exp(G) S0 q + u^T P^T
+        const uint4 h4 = get(from, 4 * o), l4 = get(from, 4 * o + 1);
+        const uint32_t uh[4] = {h4.x, h4.y, h4.z, h4.w}, ul[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (jb <= own[e]) {
+            uint32_t c[4];
+            load4(c, rec + kOffP + block_at(own[e], jb) + narrow_rows(0, lane));
+            mma(yo[e][0], uh, c[0], c[1]);
+            mma(yo[e][1], uh, c[2], c[3]);
+            mma(yo[e][0], ul, c[0], c[1]);
+            mma(yo[e][1], ul, c[2], c[3]);
+          }
+      }
+    }
+    // y takes the place of its tokens' v (both warps have read it)
+    const int m = min(kC, len - ch * kC), col = dv + 8 * (lane & 1);
+    bf16* out = static_cast<bf16*>(a.y) + (first + (int64_t)ch * kC) * a.ld_y + (int64_t)h * a.dv + col;
+#pragma unroll
+    for (int o = 0; o < 2; ++o)
+      store4t(vt + narrow_cols(16 * own[o], lane), pair(yo[o][0][0], yo[o][0][1]), pair(yo[o][1][0], yo[o][1][1]),
+              pair(yo[o][0][2], yo[o][0][3]), pair(yo[o][1][2], yo[o][1][3]));
+    __syncwarp();
+#pragma unroll
+    for (int o = 0; o < 2; ++o) {
+      const int tok = 16 * own[o] + (lane >> 1);
+      if (tok < m && col < a.dv)
+        *reinterpret_cast<uint4*>(out + tok * a.ld_y) = *reinterpret_cast<const uint4*>(smem + (vt - base) + narrow_at(tok, lane & 1));
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (y was written where a later chunk's v comes)
+    __syncwarp();
+    if (lane == 0) bar_arrive(bar(L::kEmpty + (ch & 1)));
+  }
+  if (lane == 0 && *gave_up) atomicAdd(&g_delta_timeouts, 1u);
+  each([&](float* v, int64_t at) { *reinterpret_cast<float2*>(st + at) = make_float2(v[0], v[1]); });
+}
+
+template <int DK, int NP>
+cudaError_t run_pairs(const DeltaArgs& a, const DeltaMaps& maps, const unsigned char* records, cudaStream_t st) {
+  using L = Pairs<DK, NP>;
+  auto kernel = delta_pairs_kernel<DK, NP>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((a.dv + 16 * NP - 1) / (16 * NP), a.heads, a.tab.n);
+  kernel<<<grid, 64 * NP + 32, L::kSmem, st>>>(a, maps, records);
+  return cudaGetLastError();
 }
 
 template <int DK, int NW>
-cudaError_t run_chain(const DeltaArgs& a, const unsigned char* records, cudaStream_t st) {
+cudaError_t run_chain(const DeltaArgs& a, const DeltaMaps& maps, const unsigned char* records, cudaStream_t st) {
   using L = Chain<DK, NW>;
   auto kernel = delta_chain_kernel<DK, NW>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   if (e != cudaSuccess) return e;
   const dim3 grid((a.dv + 16 * NW - 1) / (16 * NW), a.heads, a.tab.n);
-  kernel<<<grid, 32 * NW, L::kSmem, st>>>(a, records);
+  kernel<<<grid, 32 * NW, L::kSmem, st>>>(a, maps, records);
   return cudaGetLastError();
 }
 
@@ -504,13 +804,22 @@ template <int DK>
 cudaError_t run_forward(const DeltaArgs& a, unsigned char* records, cudaStream_t st) {
   const cudaError_t e = run_prep<DK, false>(a, records, st);
   if (e != cudaSuccess) return e;
-  const int64_t chains = (int64_t)a.tab.n * a.heads, sms = device_sm_count();
-  if (a.dv > 64 && chains >= sms) return run_chain<DK, 8>(a, records, st);
-  if (a.dv > 32 && 2 * chains >= sms) return run_chain<DK, 4>(a, records, st);
-  return run_chain<DK, 2>(a, records, st);
+  DeltaMaps maps;
+  if (a.tab.cu[a.tab.n] > 0 && !delta_maps(&maps, a, a.v, a.ld_v)) return cudaErrorInvalidValue;
+  const int64_t blocks = (int64_t)a.tab.n * a.heads * ((a.dv + 15) / 16), sms = device_sm_count();  // of 16 rows
+  if (blocks <= sms) return run_pairs<DK, 1>(a, maps, records, st);
+  if (blocks <= 2 * sms) return run_pairs<DK, 2>(a, maps, records, st);
+  if (blocks <= 4 * sms) return run_pairs<DK, 4>(a, maps, records, st);
+  return run_chain<DK, 4>(a, maps, records, st);
 }
 
 }  // namespace
+
+unsigned int read_delta_timeouts() {
+  unsigned int v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_delta_timeouts, sizeof v) != cudaSuccess) return 0xffffffffu;
+  return v;
+}
 
 bool delta_chunked_supported(mamba2_dtype act, int dv, int dk) { return act == MAMBA2_BF16 && dk <= 128 && dv <= 128; }
 

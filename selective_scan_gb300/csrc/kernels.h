@@ -275,10 +275,12 @@ struct DeltaTensors {
 };
 struct DeltaArgs : DeltaTensors {
   SeqTable tab;
+  uint16_t order[MAMBA2_MAX_SEQS];  // the runs, longest first: a chain that starts late is a short one
 };
 cudaError_t launch_delta_serial(const DeltaArgs& a, mamba2_dtype act, cudaStream_t st);
 // Whether the chunked kernels take this shape; the records of their first pass, which are the forward's workspace.
 bool delta_chunked_supported(mamba2_dtype act, int dv, int dk);
+unsigned int read_delta_timeouts();
 size_t delta_records(int64_t chunks, int heads, bool backward);
 cudaError_t launch_delta_chunked(const DeltaArgs& a, void* ws, cudaStream_t st);
 cudaError_t launch_delta_records(const DeltaArgs& a, void* ws, cudaStream_t st);  // the backward's
@@ -295,6 +297,7 @@ struct DeltaBwdArgs : DeltaArgs {  // (y and state unused, ckpt read; tab's slot
   int64_t ld_dq, ld_dk, ld_dv, ld_dy;
 };
 size_t delta_backward_workspace(int64_t chunks, int heads, int dv, int dk);
+unsigned int read_delta_back_timeouts();
 cudaError_t launch_delta_backward(const DeltaBwdArgs& a, void* ws, cudaStream_t st);
 
 struct DeltaStepArgs : DeltaTensors {  // (ckpt unused)
