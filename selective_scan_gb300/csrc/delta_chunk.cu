@@ -36,11 +36,13 @@ using bf16 = __nv_bfloat16;
 constexpr int kPrepThreads = 128;
 constexpr int kLdA = kC + 4;  // floats between the rows of an fp32 triangle in shared memory
 
+template <bool kBackward>
 struct PrepSmem {
-  static constexpr int kTiles = 2 * kC * 128 * 2;      // K and Q; then Inv in fp32
-  static constexpr int kA = kTiles;                    // L diag(beta), fp32
-  static constexpr int kVec = kA + kC * kLdA * 4;      // per token: G (two parts), beta, lengths
-  static constexpr int kBytes = kVec + 6 * kC * 4;
+  // K and Q; then A = L diag(beta) and Inv in fp32, and in A's place Inv in two bf16 parts
+  static constexpr int kInv = kC * kLdA * 4, kTiles = 2 * kInv;
+  static_assert(kTiles >= 2 * kC * 128 * 2, "K and Q");
+  static constexpr int kScores = kTiles;  // the rest of the record: P and the factors
+  static constexpr int kToken = kScores + record_bytes(kBackward) - kOffP, kQn = kToken + kC * 16, kBytes = kQn + kC * 4;
 };
 
 // G_i (in units of log 2) as a sum of two floats.
@@ -59,42 +61,53 @@ __device__ __forceinline__ void scan_decays(float g, float& hi, float& lo, int l
 }
 
 template <int DK, bool kBackward>
-__global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(const __grid_constant__ DeltaArgs a, unsigned char* records) {
+__global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(const __grid_constant__ DeltaArgs a, unsigned char* records) {
+  using L = PrepSmem<kBackward>;
   extern __shared__ __align__(128) unsigned char smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int h = blockIdx.y, grp = h / (a.heads / a.groups);
+  // The last 16 rows have four times the first's work, so which warp has which goes round: the warps of a scheduler
+  // then have all kinds.
+  const int rb = (warp + (int)blockIdx.x + h) & 3, r0 = 16 * rb;
   const Chunk c = chunk_of(a.tab, blockIdx.x);
-  float* vec = reinterpret_cast<float*>(smem + PrepSmem::kVec);
-  float *ghi = vec, *glo = vec + kC, *beta = vec + 2 * kC, *kn = vec + 3 * kC, *qn = vec + 4 * kC;
+  float4* token = reinterpret_cast<float4*>(smem + L::kToken);  // G in two parts, kappa, beta
+  float* qn = reinterpret_cast<float*>(smem + L::kQn);
   const uint32_t sk = sm32(smem), sq = sk + kC * DK * 2;
   {
     const bf16* k = static_cast<const bf16*>(a.k) + (int64_t)grp * a.dk;
     const bf16* q = static_cast<const bf16*>(a.q) + (int64_t)grp * a.dk;
     constexpr int units = DK / 8;
+#pragma unroll 4
     for (int e = threadIdx.x; e < kC * units; e += kPrepThreads) {
       const int r = e / units, u = e % units;
       const bool in = r < c.len && 8 * u < a.dk;
-      const int64_t row = c.row + (in ? r : 0), col = in ? 8 * u : 0;
+      const int64_t row = c.row + (in ? r : 0);
+      const int col = in ? 8 * u : 0;
       copy16(sk + wide_at(r, u), k + row * a.ld_k + col, in);
       copy16(sq + wide_at(r, u), q + row * a.ld_q + col, in);
     }
     copies_end();
   }
   if (warp == 0) {
-    float hi[2], lo[2], last[2] = {0.0f, 0.0f};
+    float hi[2], lo[2], last[2] = {0.0f, 0.0f}, gv[2], bv[2];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int i = 32 * half + lane;
       const int64_t at = (int64_t)(c.row + i) * a.heads + h;
-      float gv = i < c.len && a.g ? a.g[at] : 0.0f;
-      if (gv < -10000.0f) gv = -10000.0f;  // (a NaN stays one)
-      scan_decays(gv * kLog2e, hi[half], lo[half], lane);
+      gv[half] = i < c.len && a.g ? a.g[at] : 0.0f;
+      bv[half] = i < c.len ? (a.beta ? a.beta[at] : 1.0f) : 0.0f;
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      if (gv[half] < -10000.0f) gv[half] = -10000.0f;  // (a NaN stays one)
+      scan_decays(gv[half] * kLog2e, hi[half], lo[half], lane);
       const DF s = df_add(DF{hi[half], lo[half]}, DF{last[0], last[1]});
-      ghi[i] = s.hi;
-      glo[i] = s.lo;
+      const int i = 32 * half + lane;
+      token[i].x = s.hi;
+      token[i].y = s.lo;
+      token[i].w = bv[half];
       last[0] = __shfl_sync(0xffffffffu, s.hi, 31);
       last[1] = __shfl_sync(0xffffffffu, s.lo, 31);
-      beta[i] = i < c.len ? (a.beta ? a.beta[at] : 1.0f) : 0.0f;
     }
   }
   copies_done();
@@ -104,17 +117,19 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(const __grid_c
     const bool is_q = threadIdx.x >= kC;
     float n = 1.0f;
     if (a.l2_eps >= 0.0f) {
-      float s = 0.0f;
+      float s[2] = {0.0f, 0.0f};
+#pragma unroll
       for (int u = 0; u < DK / 8; ++u) {
         float v[8];
         Vec16<bf16>::unpack(*reinterpret_cast<const uint4*>(smem + (is_q ? kC * DK * 2 : 0) + wide_at(r, u)), v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s = fmaf(v[j], v[j], s);
+        for (int j = 0; j < 8; ++j) s[j & 1] = fmaf(v[j], v[j], s[j & 1]);
       }
-      n = rsqrtf(s + a.l2_eps);
+      n = rsqrtf(s[0] + s[1] + a.l2_eps);
     }
     if (r >= c.len) n = 0.0f;
-    (is_q ? qn : kn)[r] = n;
+    if (is_q) qn[r] = n;
+    else token[r].z = n;
   }
   // K K^T and Q K^T below and on the diagonal blocks: a warp 16 rows
   float kk[8][4], qk[8][4];
@@ -122,7 +137,6 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(const __grid_c
   for (int n = 0; n < 8; ++n)
 #pragma unroll
     for (int j = 0; j < 4; ++j) kk[n][j] = qk[n][j] = 0.0f;
-  const int r0 = 16 * warp;
 #pragma unroll
   for (int ks = 0; ks < DK / 16; ++ks) {
     uint32_t ak[4], aq[4], b[4];
@@ -130,7 +144,7 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(const __grid_c
     load4(aq, sq + wide_cols(r0, 2 * ks, lane));
 #pragma unroll
     for (int nb = 0; nb < 4; ++nb)
-      if (nb <= warp) {
+      if (nb <= rb) {
         load4(b, sk + wide_rows(16 * nb, 2 * ks, lane));
         mma(kk[2 * nb], ak, b[0], b[1]);
         mma(kk[2 * nb + 1], ak, b[2], b[3]);
@@ -139,13 +153,16 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(const __grid_c
       }
   }
   __syncthreads();  // lengths are there; K and Q have been read
-  float* A = reinterpret_cast<float*>(smem + PrepSmem::kA);
-  float* inv = reinterpret_cast<float*>(smem);
-  unsigned char* rec = records + ((int64_t)blockIdx.x * a.heads + h) * record_bytes(kBackward);
+  float* A = reinterpret_cast<float*>(smem);
+  float* inv = reinterpret_cast<float*>(smem + L::kInv);
+  unsigned char* scores = smem + L::kScores;
+  const float4 row[2] = {token[r0 + g], token[r0 + g + 8]};
+  const float rq[2] = {qn[r0 + g] * a.scale, qn[r0 + g + 8] * a.scale};
 #pragma unroll
   for (int n = 0; n < 8; ++n) {
-    if (n / 2 > warp) continue;
+    if (n / 2 > rb) continue;
     const int j0 = 8 * n + 2 * t;
+    const float4 col[2] = {token[j0], token[j0 + 1]};
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int i = r0 + g + 8 * half;
@@ -153,45 +170,56 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(const __grid_c
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int j = j0 + e;
-        const float d = j <= i ? ex2((ghi[i] - ghi[j]) + (glo[i] - glo[j])) * kn[j] : 0.0f;
-        l[e] = j < i ? kk[n][2 * half + e] * d * kn[i] * beta[j] : 0.0f;
-        p[e] = j <= i ? qk[n][2 * half + e] * d * (qn[i] * a.scale) : 0.0f;
+        const float d = j <= i ? ex2((row[half].x - col[e].x) + (row[half].y - col[e].y)) * col[e].z : 0.0f;
+        l[e] = j < i ? kk[n][2 * half + e] * d * row[half].z * col[e].w : 0.0f;
+        p[e] = qk[n][2 * half + e] * d * rq[half];
+        if (j > i) p[e] = 0.0f;
       }
       *reinterpret_cast<float2*>(A + i * kLdA + j0) = make_float2(l[0], l[1]);
-      uint32_t hi, lo;
-      split(p[0], p[1], hi, lo);
-      const uint32_t at = block_at(warp, n >> 1) + narrow_at(g + 8 * half, n & 1) + 4 * t;
-      *reinterpret_cast<uint32_t*>(rec + kOffP + at) = hi;
-      if (kBackward) *reinterpret_cast<uint32_t*>(rec + kOffPLo + at) = lo;
-    }
-  }
-  {  // the tokens' factors
-    float* f = reinterpret_cast<float*>(rec + off_factors(kBackward));
-    const float chi = ghi[kC - 1], clo = glo[kC - 1];
-    for (int i = threadIdx.x; i < kC; i += kPrepThreads) {
-      const float up = ex2(ghi[i] + glo[i]), left = ex2((chi - ghi[i]) + (clo - glo[i]));
-      f[kUp + i] = up * kn[i];
-      f[kLeft + i] = left * kn[i];
-      f[kUpQ + i] = up * (qn[i] * a.scale);
-      f[kBeta + i] = beta[i];
-      if (kBackward) {
-        f[kGHi + i] = ghi[i];
-        f[kGLo + i] = glo[i];
-        f[kKn + i] = kn[i];
-        f[kQn + i] = qn[i];
+      const uint32_t at = block_at(rb, n >> 1) + narrow_at(g + 8 * half, n & 1) + 4 * t;
+      if constexpr (kBackward) {
+        uint32_t hi, lo;
+        split(p[0], p[1], hi, lo);
+        *reinterpret_cast<uint32_t*>(scores + at) = hi;
+        *reinterpret_cast<uint32_t*>(scores + kTri + at) = lo;
+      } else {
+        *reinterpret_cast<uint32_t*>(scores + at) = pair(p[0], p[1]);
       }
     }
-    if (threadIdx.x == 0) f[kGamma] = ex2(chi + clo);
+  }
+  if (threadIdx.x < kC) {  // the tokens' factors
+    float* f = reinterpret_cast<float*>(scores + off_factors(kBackward) - kOffP);
+    const int i = threadIdx.x;
+    const float4 v = token[i], end = token[kC - 1];
+    const float up = ex2(v.x + v.y), left = ex2((end.x - v.x) + (end.y - v.y));
+    f[kUp + i] = up * v.z;
+    f[kLeft + i] = left * v.z;
+    f[kUpQ + i] = up * (qn[i] * a.scale);
+    f[kBeta + i] = v.w;
+    f[kGamma + i] = ex2(end.x + end.y);
+    if (kBackward) {
+      f[kGHi + i] = v.x;
+      f[kGLo + i] = v.y;
+      f[kKn + i] = v.z;
+      f[kQn + i] = qn[i];
+    }
   }
   __syncwarp();
   // Inv: the diagonal blocks by substitution, a column a lane (a warp's own rows of A are what it wrote)
   if (lane < 16) {
     float x[16];
+    const float* rows = A + r0 * kLdA + r0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float s = i == lane ? 1.0f : 0.0f;
 #pragma unroll
-      for (int l = 0; l < i; ++l) s = fmaf(-A[(r0 + i) * kLdA + r0 + l], x[l], s);
+      for (int l = 0; l < i; l += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(rows + i * kLdA + l);
+        s = fmaf(-v.x, x[l], s);
+        if (l + 1 < i) s = fmaf(-v.y, x[l + 1], s);
+        if (l + 2 < i) s = fmaf(-v.z, x[l + 2], s);
+        if (l + 3 < i) s = fmaf(-v.w, x[l + 3], s);
+      }
       x[i] = s;
       inv[(r0 + i) * kLdA + r0 + lane] = s;
     }
@@ -218,13 +246,13 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(const __grid_c
     auto times = [&](float (&d)[2][4], const uint32_t (&ah)[4], const uint32_t (&al)[4], const uint32_t (&bh)[2][2],
                      const uint32_t (&bl)[2][2]) {
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        mma(d[n], al, bh[n][0], bh[n][1]);
-        mma(d[n], ah, bl[n][0], bl[n][1]);
-        mma(d[n], ah, bh[n][0], bh[n][1]);
-      }
+      for (int n = 0; n < 2; ++n) mma(d[n], al, bh[n][0], bh[n][1]);
+#pragma unroll
+      for (int n = 0; n < 2; ++n) mma(d[n], ah, bl[n][0], bl[n][1]);
+#pragma unroll
+      for (int n = 0; n < 2; ++n) mma(d[n], ah, bh[n][0], bh[n][1]);
     };
-    const int j = warp;
+    const int j = 3 - rb;  // (the first column has the most blocks: for the warp that had the fewest rows)
     uint32_t ih[3][4], il[3][4], bh[2][2], bl[2][2];  // Inv_lj^T of l = j, j + 1, j + 2
     {
       float d[2][4];  // Inv_jj^T: (row g: column g of Inv_jj, its rows 2t, 2t + 1)
@@ -260,7 +288,8 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(const __grid_c
     }
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < 10 * 32; e += kPrepThreads) {  // a 16-byte unit of each part
+#pragma unroll
+  for (int e = threadIdx.x; e < 10 * 32; e += kPrepThreads) {  // a 16-byte unit of each part, where A was
     const int blk = e >> 5, r = (e >> 1) & 15, u = e & 1;
     const int i = blk < 1 ? 0 : blk < 3 ? 1 : blk < 6 ? 2 : 3, j = blk - i * (i + 1) / 2;
     const float* from = inv + (16 * i + r) * kLdA + 16 * j + 8 * u;
@@ -270,8 +299,20 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(const __grid_c
     split(x.z, x.w, hi.y, lo.y);
     split(y.x, y.y, hi.z, lo.z);
     split(y.z, y.w, hi.w, lo.w);
-    *reinterpret_cast<uint4*>(rec + blk * 512 + narrow_at(r, u)) = hi;
-    *reinterpret_cast<uint4*>(rec + kOffInvLo + blk * 512 + narrow_at(r, u)) = lo;
+    *reinterpret_cast<uint4*>(smem + blk * 512 + narrow_at(r, u)) = hi;
+    *reinterpret_cast<uint4*>(smem + kOffInvLo + blk * 512 + narrow_at(r, u)) = lo;
+  }
+  // the record goes out in two copies
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    unsigned char* rec = records + ((int64_t)blockIdx.x * a.heads + h) * record_bytes(kBackward);
+    auto out = [](unsigned char* to, uint32_t from, int bytes) {
+      asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to), "r"(from), "r"(bytes) : "memory");
+    };
+    out(rec, sk, kOffP);
+    out(rec + kOffP, sk + L::kScores, record_bytes(kBackward) - kOffP);
+    asm volatile("cp.async.bulk.commit_group;\ncp.async.bulk.wait_group 0;" ::: "memory");
   }
 }
 
@@ -794,9 +835,9 @@ cudaError_t run_prep(const DeltaArgs& a, unsigned char* records, cudaStream_t st
   const int chunks = a.tab.tile[a.tab.n];
   if (chunks == 0) return cudaSuccess;
   auto kernel = delta_prep_kernel<DK, kBackward>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PrepSmem::kBytes);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PrepSmem<kBackward>::kBytes);
   if (e != cudaSuccess) return e;
-  kernel<<<dim3(chunks, a.heads), kPrepThreads, PrepSmem::kBytes, st>>>(a, records);
+  kernel<<<dim3(chunks, a.heads), kPrepThreads, PrepSmem<kBackward>::kBytes, st>>>(a, records);
   return cudaGetLastError();
 }
 
