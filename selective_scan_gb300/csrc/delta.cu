@@ -79,40 +79,45 @@ __device__ __forceinline__ float dot(const Two (&a)[N], const Two (&b)[N]) {
   return both(s) + both(t);
 }
 
-// What a token's key, query, decay and beta come to; qn has the scale.
+// What a token's key, query, decay and beta come to: a; beta / |k|; a / |k|; scale / |q|.
 struct Token {
-  float a, beta, kn, qn;
+  float a, write, read, qn;
 };
 template <int N>
 __device__ __forceinline__ Token token_of(const Two (&k)[N], const Two (&q)[N], float g, float beta, float scale, float l2_eps) {
-  Token t = {expf(g), beta, 1.0f, scale};
+  float kn = 1.0f, qn = scale;
   if (l2_eps >= 0.0f) {
-    t.kn = rsqrtf(sum8(dot(k, k)) + l2_eps);
-    t.qn = scale * rsqrtf(sum8(dot(q, q)) + l2_eps);
+    kn = rsqrtf(sum8(dot(k, k)) + l2_eps);
+    qn = scale * rsqrtf(sum8(dot(q, q)) + l2_eps);
   }
-  return t;
+  const float a = expf(g);
+  return {a, beta * kn, a * kn, qn};
 }
 
-// One token: the state rows s, the key and query of this lane's elements, the rows' v; gives the rows' y.
+// One token: the state rows s, the key and query of this lane's elements, the rows' v; gives this lane's part of the
+// rows' S q.
 template <int N>
 __device__ __forceinline__ void advance(Two (&s)[kRowsThread][N], const Two (&k)[N], const Two (&q)[N],
                                         const float (&v)[kRowsThread], const Token& t, float (&y)[kRowsThread]) {
   float p[kRowsThread];
+  const Two a = two(t.a, t.a);
 #pragma unroll
   for (int r = 0; r < kRowsThread; ++r) p[r] = dot(s[r], k);
 #pragma unroll
+  for (int r = 0; r < kRowsThread; ++r)
+#pragma unroll
+    for (int e = 0; e < N; ++e) s[r][e] = mul(a, s[r][e]);  // (while the sums go round)
+#pragma unroll
   for (int r = 0; r < kRowsThread; ++r) p[r] = sum8(p[r]);
-  const Two a = two(t.a, t.a);
 #pragma unroll
   for (int r = 0; r < kRowsThread; ++r) {
-    const float u = t.beta * (v[r] - t.a * t.kn * p[r]) * t.kn;
+    const float u = t.write * fmaf(-t.read, p[r], v[r]);
     const Two uu = two(u, u);
 #pragma unroll
-    for (int e = 0; e < N; ++e) s[r][e] = fma(a, s[r][e], mul(uu, k[e]));
-    y[r] = dot(s[r], q);
+    for (int e = 0; e < N; ++e) s[r][e] = fma(uu, k[e], s[r][e]);
   }
 #pragma unroll
-  for (int r = 0; r < kRowsThread; ++r) y[r] = t.qn * sum8(y[r]);
+  for (int r = 0; r < kRowsThread; ++r) y[r] = dot(s[r], q);
 }
 
 // ------------------------------------------------------------------ packed runs
@@ -215,22 +220,45 @@ __global__ void __launch_bounds__(kSerialThreads) delta_serial_kernel(const __gr
       if (lane == 0) tokens[t] = tok;
     }
     __syncthreads();
-    auto one = [&](int t) {
+    auto one = [&](int t, float (&yp)[kRowsThread]) {
       Two kv[N], qv[N];
-      float vv[kRowsThread], yv[kRowsThread];
+      float vv[kRowsThread];
       load(sk[b][t], kv);
       load(sq[b][t], qv);
 #pragma unroll
       for (int r = 0; r < kRowsThread; ++r) vv[r] = Act<T>::to_f(sv[b][t][mine + r]);
-      advance(s, kv, qv, vv, tokens[t], yv);
-      if (live && lane == 0) store_two(y + ((int64_t)first + t0 + t) * a.ld_y, yv[0], yv[1]);
+      advance(s, kv, qv, vv, tokens[t], yp);
     };
-    int t = 0;
-    for (; t + 4 <= n; t += 4) {  // (a token's operands are on their way while the one before it is worked on)
+    int t = row0 + (int)(threadIdx.x & ~31u) / kLanes * kRowsThread < a.dv ? 0 : n;  // (a warp without rows has no work)
+    for (; t + 8 <= n; t += 8) {
+      // eight tokens' parts are summed at once, so that no token waits for another's output: 7 shuffles a row that leave
+      // lane j with token j's
+      float yp[8][kRowsThread];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) one(t + j);
+      for (int j = 0; j < 8; ++j) one(t + j, yp[j]);
+      float out[kRowsThread];
+#pragma unroll
+      for (int r = 0; r < kRowsThread; ++r) {
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (j < o) {
+              const bool up = (lane & o) != 0;
+              const float keep = up ? yp[j + o][r] : yp[j][r], send = up ? yp[j][r] : yp[j + o][r];
+              yp[j][r] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+            }
+        out[r] = tokens[t + lane].qn * yp[0][r];
+      }
+      if (live) store_two(y + ((int64_t)first + t0 + t + lane) * a.ld_y, out[0], out[1]);
     }
-    for (; t < n; ++t) one(t);
+    for (; t < n; ++t) {
+      float yp[kRowsThread];
+      one(t, yp);
+#pragma unroll
+      for (int r = 0; r < kRowsThread; ++r) yp[r] = tokens[t].qn * sum8(yp[r]);
+      if (live && lane == 0) store_two(y + ((int64_t)first + t0 + t) * a.ld_y, yp[0], yp[1]);
+    }
     __syncthreads();  // (the next fetch but one overwrites this buffer)
   }
   each([&](Two* w, int64_t at) { store_four(st + at, w); });
@@ -297,7 +325,10 @@ __global__ void __launch_bounds__(kStepThreads) delta_step_kernel(const __grid_c
     }
     if (i >= num) return;
   }
-  advance(s, k, q, v, token_of(k, q, g, beta, a.scale, a.l2_eps), y);
+  const Token t = token_of(k, q, g, beta, a.scale, a.l2_eps);
+  advance(s, k, q, v, t, y);
+#pragma unroll
+  for (int r = 0; r < kRowsThread; ++r) y[r] = t.qn * sum8(y[r]);
   if (!live) return;
 #pragma unroll
   for (int r = 0; r < kRowsThread; ++r)

@@ -625,49 +625,63 @@ __global__ void __launch_bounds__(64 * NP + 32) delta_pairs_kernel(const __grid_
       float* o = a.ckpt + ((int64_t)(a.tab.tile[run] + ch) * a.heads + h) * a.dv * a.dk;
       each([&](float* v, int64_t to) { *reinterpret_cast<float2*>(o + to) = make_float2(v[0], v[1]); });
     }
-    float x[8][4], y[8][4];
+    float x[8][4];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[i][j] = y[i][j] = 0.0f;
+      for (int j = 0; j < 4; ++j) x[i][j] = 0.0f;
+    uint32_t sh[KS][4];
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      uint32_t sh[4], sl[4], b[4][4], c[4];
+      uint32_t sl[4], b[4][4];
       const int unit = half * (DK / 16) + 2 * ks;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) split(s[2 * ks + (j >> 1)][2 * (j & 1)], s[2 * ks + (j >> 1)][2 * (j & 1) + 1], sh[j], sl[j]);
+      for (int j = 0; j < 4; ++j) split(s[2 * ks + (j >> 1)][2 * (j & 1)], s[2 * ks + (j >> 1)][2 * (j & 1) + 1], sh[ks][j], sl[j]);
 #pragma unroll
       for (int nb = 0; nb < 4; ++nb) {
         load4(b[nb], at + wide_rows(16 * nb, unit, lane));
-        mma(x[2 * nb], sh, b[nb][0], b[nb][1]);
-        mma(x[2 * nb + 1], sh, b[nb][2], b[nb][3]);
+        mma(x[2 * nb], sh[ks], b[nb][0], b[nb][1]);
+        mma(x[2 * nb + 1], sh[ks], b[nb][2], b[nb][3]);
       }
 #pragma unroll
       for (int nb = 0; nb < 4; ++nb) {
-        load4(c, qt + wide_rows(16 * nb, unit, lane));
-        mma(y[2 * nb], sh, c[0], c[1]);
-        mma(y[2 * nb + 1], sh, c[2], c[3]);
         mma(x[2 * nb], sl, b[nb][0], b[nb][1]);
         mma(x[2 * nb + 1], sl, b[nb][2], b[nb][3]);
       }
     }
     pair_sync(pr);  // the other has read its mail of the last chunk
-    // this half's part of X, and of the other's Y
-    float yo[2][2][4];  // Y of this warp's tokens
 #pragma unroll
     for (int i = 0; i < 8; ++i) put(i, __float_as_uint(x[i][0]), __float_as_uint(x[i][1]), __float_as_uint(x[i][2]), __float_as_uint(x[i][3]));
+    // (this half's part of Y, which nothing of the chain waits for, while the mail is on its way)
+    float yo[2][2][4];  // Y of this warp's tokens
+    {
+      float y[8][4];
 #pragma unroll
-    for (int o = 0; o < 2; ++o)
+      for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint32_t w[4];
+        for (int j = 0; j < 4; ++j) y[i][j] = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {  // (block 3 o of the tokens is warp 0's, block 1 + o warp 1's)
-          yo[o][i][j] = half ? y[2 * (1 + o) + i][j] : y[6 * o + i][j];
-          w[j] = __float_as_uint(half ? y[6 * o + i][j] : y[2 * (1 + o) + i][j]);
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int nb = 0; nb < 4; ++nb) {
+          uint32_t c[4];
+          load4(c, qt + wide_rows(16 * nb, half * (DK / 16) + 2 * ks, lane));
+          mma(y[2 * nb], sh[ks], c[0], c[1]);
+          mma(y[2 * nb + 1], sh[ks], c[2], c[3]);
         }
-        put(8 + 2 * o + i, w[0], w[1], w[2], w[3]);
-      }
+#pragma unroll
+      for (int o = 0; o < 2; ++o)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {  // (block 3 o of the tokens is warp 0's, block 1 + o warp 1's)
+            yo[o][i][j] = half ? y[2 * (1 + o) + i][j] : y[6 * o + i][j];
+            w[j] = __float_as_uint(half ? y[6 * o + i][j] : y[2 * (1 + o) + i][j]);
+          }
+          put(8 + 2 * o + i, w[0], w[1], w[2], w[3]);
+        }
+    }
     pair_sync(pr);
     auto plus = [&](float (&d)[4], const uint4& w) {
       d[0] += __uint_as_float(w.x);
@@ -698,13 +712,13 @@ __global__ void __launch_bounds__(64 * NP + 32) delta_pairs_kernel(const __grid_
     }
     pair_sync(pr);  // both have read the mail
     // r of this warp's tokens, and from it u: for the scores as it is, for the state with what is left at the chunk's end
-    float r[2][2][4];
+    float r[2][2][4], rl[2][2][4];  // (two sums, for a shorter chain)
 #pragma unroll
     for (int o = 0; o < 2; ++o)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) r[o][i][j] = 0.0f;
+        for (int j = 0; j < 4; ++j) r[o][i][j] = rl[o][i][j] = 0.0f;
 #pragma unroll
     for (int jb = 0; jb < 4; ++jb) {
       uint32_t b[2][4], c[2][4];
@@ -715,10 +729,10 @@ __global__ void __launch_bounds__(64 * NP + 32) delta_pairs_kernel(const __grid_
           load4(c[o], rec + kOffInvLo + block_at(own[o], jb) + narrow_rows(0, lane));
           mma(r[o][0], ah[jb], b[o][0], b[o][1]);
           mma(r[o][1], ah[jb], b[o][2], b[o][3]);
-          mma(r[o][0], al[jb], b[o][0], b[o][1]);
-          mma(r[o][1], al[jb], b[o][2], b[o][3]);
-          mma(r[o][0], ah[jb], c[o][0], c[o][1]);
-          mma(r[o][1], ah[jb], c[o][2], c[o][3]);
+          mma(rl[o][0], al[jb], b[o][0], b[o][1]);
+          mma(rl[o][1], al[jb], b[o][2], b[o][3]);
+          mma(rl[o][0], ah[jb], c[o][0], c[o][1]);
+          mma(rl[o][1], ah[jb], c[o][2], c[o][3]);
         }
     }
 #pragma unroll
@@ -732,7 +746,7 @@ __global__ void __launch_bounds__(64 * NP + 32) delta_pairs_kernel(const __grid_
         const float2 up = *reinterpret_cast<const float2*>(f + kUpQ + tok);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float u0 = r[o][i][2 * e] * b.x, u1 = r[o][i][2 * e + 1] * b.y;
+          const float u0 = (r[o][i][2 * e] + rl[o][i][2 * e]) * b.x, u1 = (r[o][i][2 * e + 1] + rl[o][i][2 * e + 1]) * b.y;
           split(u0, u1, uh[2 * i + e], ul[2 * i + e]);
           split(u0 * left.x, u1 * left.y, wh[2 * i + e], wl[2 * i + e]);
           yo[o][i][2 * e] *= up.x;
@@ -750,41 +764,42 @@ __global__ void __launch_bounds__(64 * NP + 32) delta_pairs_kernel(const __grid_
 #pragma unroll
       for (int j = 0; j < 4; ++j) s[i][j] *= gamma;
     pair_sync(pr);
+    auto mail_of = [&](int jb) {  // block jb's u: whose it is; it is that one's block jb / 2
+      return ((jb == 0 || jb == 3) == (half == 0)) ? static_cast<const unsigned char*>(mail) : post;
+    };
+    // S = gamma S + (left u)^T K, which the next chunk waits for
 #pragma unroll
     for (int jb = 0; jb < 4; ++jb) {
-      const bool zero = jb == 0 || jb == 3;  // whose block it is, and which of its two
-      const unsigned char* from = (zero ? half == 0 : half == 1) ? mail : post;
-      const int o = jb >> 1;
       uint32_t b[KS][4];
-      {  // S = gamma S + (left u)^T K
-        const uint4 h4 = get(from, 4 * o + 2), l4 = get(from, 4 * o + 3);
-        const uint32_t wh[4] = {h4.x, h4.y, h4.z, h4.w}, wl[4] = {l4.x, l4.y, l4.z, l4.w};
+      const uint4 h4 = get(mail_of(jb), 4 * (jb >> 1) + 2), l4 = get(mail_of(jb), 4 * (jb >> 1) + 3);
+      const uint32_t wh[4] = {h4.x, h4.y, h4.z, h4.w}, wl[4] = {l4.x, l4.y, l4.z, l4.w};
 #pragma unroll
-        for (int nb = 0; nb < KS; ++nb) {
-          load4t(b[nb], at + wide_cols(16 * jb, half * (DK / 16) + 2 * nb, lane));
-          mma(s[2 * nb], wh, b[nb][0], b[nb][1]);
-          mma(s[2 * nb + 1], wh, b[nb][2], b[nb][3]);
-        }
-#pragma unroll
-        for (int nb = 0; nb < KS; ++nb) {
-          mma(s[2 * nb], wl, b[nb][0], b[nb][1]);
-          mma(s[2 * nb + 1], wl, b[nb][2], b[nb][3]);
-        }
+      for (int nb = 0; nb < KS; ++nb) {
+        load4t(b[nb], at + wide_cols(16 * jb, half * (DK / 16) + 2 * nb, lane));
+        mma(s[2 * nb], wh, b[nb][0], b[nb][1]);
+        mma(s[2 * nb + 1], wh, b[nb][2], b[nb][3]);
       }
-      {  // Y = scale exp(G) S0 q + u^T P^T
-        const uint4 h4 = get(from, 4 * o), l4 = get(from, 4 * o + 1);
-        const uint32_t uh[4] = {h4.x, h4.y, h4.z, h4.w}, ul[4] = {l4.x, l4.y, l4.z, l4.w};
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (jb <= own[e]) {
-            uint32_t c[4];
-            load4(c, rec + kOffP + block_at(own[e], jb) + narrow_rows(0, lane));
-            mma(yo[e][0], uh, c[0], c[1]);
-            mma(yo[e][1], uh, c[2], c[3]);
-            mma(yo[e][0], ul, c[0], c[1]);
-            mma(yo[e][1], ul, c[2], c[3]);
-          }
+      for (int nb = 0; nb < KS; ++nb) {
+        mma(s[2 * nb], wl, b[nb][0], b[nb][1]);
+        mma(s[2 * nb + 1], wl, b[nb][2], b[nb][3]);
       }
+    }
+    // Y = scale exp(G) S0 q + u^T P^T
+#pragma unroll
+    for (int jb = 0; jb < 4; ++jb) {
+      const uint4 h4 = get(mail_of(jb), 4 * (jb >> 1)), l4 = get(mail_of(jb), 4 * (jb >> 1) + 1);
+      const uint32_t uh[4] = {h4.x, h4.y, h4.z, h4.w}, ul[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (jb <= own[e]) {
+          uint32_t c[4];
+          load4(c, rec + kOffP + block_at(own[e], jb) + narrow_rows(0, lane));
+          mma(yo[e][0], uh, c[0], c[1]);
+          mma(yo[e][1], uh, c[2], c[3]);
+          mma(yo[e][0], ul, c[0], c[1]);
+          mma(yo[e][1], ul, c[2], c[3]);
+        }
     }
     // y takes the place of its tokens' v (both warps have read it)
     const int m = min(kC, len - ch * kC), col = dv + 8 * (lane & 1);
