@@ -34,8 +34,8 @@ using bf16 = __nv_bfloat16;
 // ------------------------------------------------------------------ dS through the chunks
 
 template <int DK, int NW>
-struct Back : Stages<DK, true, NW> {
-  static constexpr int kOffBar = Stages<DK, true, NW>::kEnd, kSmem = kOffBar + 32;
+struct Back : Stages<DK, true, NW, 2> {
+  static constexpr int kOffBar = Stages<DK, true, NW, 2>::kEnd, kSmem = kOffBar + 32;
 };
 
 template <int DK, int NW>
@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(32 * NW) delta_back_kernel(const __grid_consta
       v[1] = f.y;
     });
   auto fetch = [&](int ch) {  // (warp 0)
-    load_stage<DK, true, NW>(ch, base, bar(ch), a, maps, a.dy, a.ld_dy,
+    load_stage<DK, true, NW, 2>(ch, base, bar(ch), a, maps, a.dy, a.ld_dy,
                              records + ((int64_t)(a.tab.tile[run] + ch) * a.heads + h) * record_bytes(true),
                              first + (int64_t)ch * kC, min(kC, len - ch * kC), grp, h, dv0, lane);
   };
@@ -101,21 +101,20 @@ __global__ void __launch_bounds__(32 * NW) delta_back_kernel(const __grid_consta
     // dU^T = left (dS1^T)^T K^T + dO^T P
     float x[8][4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[i][j] = 0.0f;
-#pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      uint32_t sh[4], sl[4], b[4];
+      uint32_t sh[4], sl[4], b[4][4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) split(s[2 * ks + (j >> 1)][2 * (j & 1)], s[2 * ks + (j >> 1)][2 * (j & 1) + 1], sh[j], sl[j]);
 #pragma unroll
       for (int nb = 0; nb < 4; ++nb) {
-        load4(b, at + wide_rows(16 * nb, 2 * ks, lane));
-        mma(x[2 * nb], sh, b[0], b[1]);
-        mma(x[2 * nb + 1], sh, b[2], b[3]);
-        mma(x[2 * nb], sl, b[0], b[1]);
-        mma(x[2 * nb + 1], sl, b[2], b[3]);
+        load4(b[nb], at + wide_rows(16 * nb, 2 * ks, lane));
+        mma_if(ks == 0, x[2 * nb], sh, b[nb][0], b[nb][1]);
+        mma_if(ks == 0, x[2 * nb + 1], sh, b[nb][2], b[nb][3]);
+      }
+#pragma unroll
+      for (int nb = 0; nb < 4; ++nb) {
+        mma(x[2 * nb], sl, b[nb][0], b[nb][1]);
+        mma(x[2 * nb + 1], sl, b[nb][2], b[nb][3]);
       }
     }
 #pragma unroll

@@ -319,12 +319,12 @@ __global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(const __gri
 // ------------------------------------------------------------------ the state through the chunks
 
 template <int DK, int NW>
-struct Chain : Stages<DK, false, NW> {
-  static constexpr int kOffBar = Stages<DK, false, NW>::kEnd, kSmem = kOffBar + 32;
+struct Chain : Stages<DK, false, NW, 2> {
+  static constexpr int kOffBar = Stages<DK, false, NW, 2>::kEnd, kSmem = kOffBar + 32;
 };
 
 template <int DK, int NW>
-__global__ void __launch_bounds__(32 * NW) delta_chain_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ DeltaMaps maps, const unsigned char* records) {
+__global__ void __launch_bounds__(32 * NW, NW == 8 ? 1 : 2) delta_chain_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ DeltaMaps maps, const unsigned char* records) {
   using L = Chain<DK, NW>;
   constexpr int KS = DK / 16;
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(32 * NW) delta_chain_kernel(const __grid_const
       v[1] = f.y;
     });
   auto fetch = [&](int ch) {  // (warp 0)
-    load_stage<DK, false, NW>(ch, base, bar(ch), a, maps, a.v, a.ld_v,
+    load_stage<DK, false, NW, 2>(ch, base, bar(ch), a, maps, a.v, a.ld_v,
                               records + ((int64_t)(a.tab.tile[run] + ch) * a.heads + h) * record_bytes(false),
                               first + (int64_t)ch * kC, min(kC, len - ch * kC), grp, h, dv0, lane);
   };
@@ -390,10 +390,6 @@ __global__ void __launch_bounds__(32 * NW) delta_chain_kernel(const __grid_const
     // X^T = S0 K^T (the state in two parts) and S0 Q^T (in one: it ends in a bf16 output)
     float x[8][4], y[8][4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[i][j] = y[i][j] = 0.0f;
-#pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       uint32_t sh[4], sl[4], b[4][4], c[4];
 #pragma unroll
@@ -401,14 +397,14 @@ __global__ void __launch_bounds__(32 * NW) delta_chain_kernel(const __grid_const
 #pragma unroll
       for (int nb = 0; nb < 4; ++nb) {
         load4(b[nb], at + wide_rows(16 * nb, 2 * ks, lane));
-        mma(x[2 * nb], sh, b[nb][0], b[nb][1]);
-        mma(x[2 * nb + 1], sh, b[nb][2], b[nb][3]);
+        mma_if(ks == 0, x[2 * nb], sh, b[nb][0], b[nb][1]);
+        mma_if(ks == 0, x[2 * nb + 1], sh, b[nb][2], b[nb][3]);
       }
 #pragma unroll
       for (int nb = 0; nb < 4; ++nb) {
         load4(c, qt + wide_rows(16 * nb, 2 * ks, lane));
-        mma(y[2 * nb], sh, c[0], c[1]);
-        mma(y[2 * nb + 1], sh, c[2], c[3]);
+        mma_if(ks == 0, y[2 * nb], sh, c[0], c[1]);
+        mma_if(ks == 0, y[2 * nb + 1], sh, c[2], c[3]);
         mma(x[2 * nb], sl, b[nb][0], b[nb][1]);
         mma(x[2 * nb + 1], sl, b[nb][2], b[nb][3]);
       }
@@ -430,18 +426,14 @@ __global__ void __launch_bounds__(32 * NW) delta_chain_kernel(const __grid_const
     }
     // r^T = R^T Inv^T
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[i][j] = 0.0f;
-#pragma unroll
     for (int jb = 0; jb < 4; ++jb)
     {
       uint32_t b[4][4];
 #pragma unroll
       for (int ib = jb; ib < 4; ++ib) {
         load4(b[ib], rec + block_at(ib, jb) + narrow_rows(0, lane));
-        mma(x[2 * ib], ah[jb], b[ib][0], b[ib][1]);
-        mma(x[2 * ib + 1], ah[jb], b[ib][2], b[ib][3]);
+        mma_if(jb == 0, x[2 * ib], ah[jb], b[ib][0], b[ib][1]);
+        mma_if(jb == 0, x[2 * ib + 1], ah[jb], b[ib][2], b[ib][3]);
       }
 #pragma unroll
       for (int ib = jb; ib < 4; ++ib) {
@@ -541,18 +533,21 @@ __global__ void __launch_bounds__(32 * NW) delta_chain_kernel(const __grid_const
 // the state: each holds one half of its columns, so each has half of the products with K and Q; they add up their parts
 // of X and Y, each takes half of the tokens through Inv and P, and they exchange the u that come out. The first and last
 // 16 tokens are warp 0's, those between warp 1's: both have five of the ten blocks of a triangle.
+constexpr int kAhead = 3;  // chunks whose tiles are held (with two, 970 of a chunk's 4 300 cycles were waiting for them)
+
 template <int DK, int NP>
-struct Pairs : Stages<DK, false, NP> {
+struct Pairs : Stages<DK, false, NP, kAhead> {
   static constexpr int kMail = 12 * 512;  // of a warp: 48 registers of every lane
-  static constexpr int kOffMail = Stages<DK, false, NP>::kEnd, kOffBar = kOffMail + 2 * NP * kMail;
-  static constexpr int kSmem = kOffBar + 48;
-  enum Bar : int { kFull = 0, kEmpty = 2 };  // + chunk % 2
+  static constexpr int kOffMail = Stages<DK, false, NP, kAhead>::kEnd, kOffBar = kOffMail + 2 * NP * kMail;
+  static constexpr int kOffFlag = kOffBar + 8 * 2 * kAhead, kSmem = kOffFlag + 16;
+  enum Bar : int { kFull = 0, kEmpty = kAhead };  // + chunk % kAhead
+  static_assert(kSmem <= 232448, "shared memory plan exceeds 227 KB");
 };
 
 __device__ __forceinline__ void pair_sync(int pair) { asm volatile("bar.sync %0, 64;" ::"r"(pair + 1) : "memory"); }
 
 template <int DK, int NP>
-__global__ void __launch_bounds__(64 * NP + 32) delta_pairs_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ DeltaMaps maps, const unsigned char* records) {
+__global__ void __launch_bounds__(64 * NP + 32, 1) delta_pairs_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ DeltaMaps maps, const unsigned char* records) {
   using L = Pairs<DK, NP>;
   constexpr int KS = DK / 32;  // k-steps of a half
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -566,9 +561,9 @@ __global__ void __launch_bounds__(64 * NP + 32) delta_pairs_kernel(const __grid_
   const bool fresh = seq_fresh(a.tab, run);
   if (len == 0 && !fresh) return;
   auto bar = [&](int id) { return base + L::kOffBar + 8u * (uint32_t)id; };
-  volatile uint32_t* gave_up = reinterpret_cast<volatile uint32_t*>(smem + L::kOffBar + 32);
+  volatile uint32_t* gave_up = reinterpret_cast<volatile uint32_t*>(smem + L::kOffFlag);
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kAhead; ++i) {
       bar_init(bar(L::kFull + i), 32);
       bar_init(bar(L::kEmpty + i), 2 * NP);
     }
@@ -578,8 +573,8 @@ __global__ void __launch_bounds__(64 * NP + 32) delta_pairs_kernel(const __grid_
   __syncthreads();
   if (warp == 2 * NP) {
     for (int ch = 0; ch < n; ++ch) {
-      if (ch >= 2) bar_wait(bar(L::kEmpty + (ch & 1)), (uint32_t)(((ch >> 1) - 1) & 1), gave_up);
-      load_stage<DK, false, NP>(ch, base, bar(L::kFull + (ch & 1)), a, maps, a.v, a.ld_v,
+      if (ch >= kAhead) bar_wait(bar(L::kEmpty + ch % kAhead), (uint32_t)((ch / kAhead - 1) & 1), gave_up);
+      load_stage<DK, false, NP, kAhead>(ch, base, bar(L::kFull + ch % kAhead), a, maps, a.v, a.ld_v,
                                 records + ((int64_t)(a.tab.tile[run] + ch) * a.heads + h) * record_bytes(false),
                                 first + (int64_t)ch * kC, min(kC, len - ch * kC), grp, h, dv0, lane);
     }
@@ -617,7 +612,7 @@ __global__ void __launch_bounds__(64 * NP + 32) delta_pairs_kernel(const __grid_
   };
   auto get = [&](const unsigned char* from, int i) { return *reinterpret_cast<const uint4*>(from + i * 512 + lane * 16); };
   for (int ch = 0; ch < n; ++ch) {
-    bar_wait(bar(L::kFull + (ch & 1)), (uint32_t)((ch >> 1) & 1), gave_up);
+    bar_wait(bar(L::kFull + ch % kAhead), (uint32_t)((ch / kAhead) & 1), gave_up);
     __syncwarp();
     const uint32_t at = base + L::k(ch), qt = base + L::q(ch), rec = base + L::rec(ch), vt = base + L::v(ch) + pr * L::kStrip;
     const float* f = reinterpret_cast<const float*>(smem + (rec - base) + off_factors(false));
@@ -626,10 +621,6 @@ __global__ void __launch_bounds__(64 * NP + 32) delta_pairs_kernel(const __grid_
       each([&](float* v, int64_t to) { *reinterpret_cast<float2*>(o + to) = make_float2(v[0], v[1]); });
     }
     float x[8][4];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[i][j] = 0.0f;
     uint32_t sh[KS][4];
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
@@ -640,8 +631,8 @@ __global__ void __launch_bounds__(64 * NP + 32) delta_pairs_kernel(const __grid_
 #pragma unroll
       for (int nb = 0; nb < 4; ++nb) {
         load4(b[nb], at + wide_rows(16 * nb, unit, lane));
-        mma(x[2 * nb], sh[ks], b[nb][0], b[nb][1]);
-        mma(x[2 * nb + 1], sh[ks], b[nb][2], b[nb][3]);
+        mma_if(ks == 0, x[2 * nb], sh[ks], b[nb][0], b[nb][1]);
+        mma_if(ks == 0, x[2 * nb + 1], sh[ks], b[nb][2], b[nb][3]);
       }
 #pragma unroll
       for (int nb = 0; nb < 4; ++nb) {
@@ -657,17 +648,13 @@ __global__ void __launch_bounds__(64 * NP + 32) delta_pairs_kernel(const __grid_
     {
       float y[8][4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) y[i][j] = 0.0f;
-#pragma unroll
       for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
         for (int nb = 0; nb < 4; ++nb) {
           uint32_t c[4];
           load4(c, qt + wide_rows(16 * nb, half * (DK / 16) + 2 * ks, lane));
-          mma(y[2 * nb], sh[ks], c[0], c[1]);
-          mma(y[2 * nb + 1], sh[ks], c[2], c[3]);
+          mma_if(ks == 0, y[2 * nb], sh[ks], c[0], c[1]);
+          mma_if(ks == 0, y[2 * nb + 1], sh[ks], c[2], c[3]);
         }
 #pragma unroll
       for (int o = 0; o < 2; ++o)
@@ -714,12 +701,6 @@ __global__ void __launch_bounds__(64 * NP + 32) delta_pairs_kernel(const __grid_
     // r of this warp's tokens, and from it u: for the scores as it is, for the state with what is left at the chunk's end
     float r[2][2][4], rl[2][2][4];  // (two sums, for a shorter chain)
 #pragma unroll
-    for (int o = 0; o < 2; ++o)
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) r[o][i][j] = rl[o][i][j] = 0.0f;
-#pragma unroll
     for (int jb = 0; jb < 4; ++jb) {
       uint32_t b[2][4], c[2][4];
 #pragma unroll
@@ -727,10 +708,10 @@ __global__ void __launch_bounds__(64 * NP + 32) delta_pairs_kernel(const __grid_
         if (jb <= own[o]) {
           load4(b[o], rec + block_at(own[o], jb) + narrow_rows(0, lane));
           load4(c[o], rec + kOffInvLo + block_at(own[o], jb) + narrow_rows(0, lane));
-          mma(r[o][0], ah[jb], b[o][0], b[o][1]);
-          mma(r[o][1], ah[jb], b[o][2], b[o][3]);
-          mma(rl[o][0], al[jb], b[o][0], b[o][1]);
-          mma(rl[o][1], al[jb], b[o][2], b[o][3]);
+          mma_if(jb == 0, r[o][0], ah[jb], b[o][0], b[o][1]);
+          mma_if(jb == 0, r[o][1], ah[jb], b[o][2], b[o][3]);
+          mma_if(jb == 0, rl[o][0], al[jb], b[o][0], b[o][1]);
+          mma_if(jb == 0, rl[o][1], al[jb], b[o][2], b[o][3]);
           mma(rl[o][0], ah[jb], c[o][0], c[o][1]);
           mma(rl[o][1], ah[jb], c[o][2], c[o][3]);
         }
@@ -817,7 +798,7 @@ __global__ void __launch_bounds__(64 * NP + 32) delta_pairs_kernel(const __grid_
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (y was written where a later chunk's v comes)
     __syncwarp();
-    if (lane == 0) bar_arrive(bar(L::kEmpty + (ch & 1)));
+    if (lane == 0) bar_arrive(bar(L::kEmpty + ch % kAhead));
   }
   if (lane == 0 && *gave_up) atomicAdd(&g_delta_timeouts, 1u);
   each([&](float* v, int64_t at) { *reinterpret_cast<float2*>(st + at) = make_float2(v[0], v[1]); });

@@ -33,6 +33,16 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// The first product of a sum.
+__device__ __forceinline__ void mma_new(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},{%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+__device__ __forceinline__ void mma_if(bool first, float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (first) mma_new(d, a, b0, b1);  // (known when compiled)
+  else mma(d, a, b0, b1);
+}
 __device__ __forceinline__ void load4(uint32_t (&r)[4], uint32_t at) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
@@ -143,16 +153,16 @@ __device__ __forceinline__ Chunk chunk_of(const Table& t, int chunk) {
 
 // ---- a chunk's tiles: keys and queries of a group, the record of a head, and 16 columns of values (or gradients of y)
 // for each of kStrips strips of the state's rows
-// (two of each, for the chunk at hand and the next)
-template <int DK, bool kBackward, int kStrips>
+// (kDepth of each, for the chunk at hand and the next)
+template <int DK, bool kBackward, int kStrips, int kDepth>
 struct Stages {
   static constexpr int kTile = kC * DK * 2, kStrip = kC * 32, kRecBytes = copied_bytes(kBackward);
-  static constexpr int kV = 4 * kTile, kRec = kV + 2 * kStrips * kStrip, kEnd = kRec + 2 * kRecBytes;
+  static constexpr int kV = kDepth * 2 * kTile, kRec = kV + kDepth * kStrips * kStrip, kEnd = kRec + kDepth * kRecBytes;
   static constexpr int kCopied = 2 * kTile + kRecBytes + kStrips * kStrip;
-  __device__ static __forceinline__ uint32_t k(int ch) { return (uint32_t)(ch & 1) * (2 * kTile); }
+  __device__ static __forceinline__ uint32_t k(int ch) { return (uint32_t)(ch % kDepth) * (2 * kTile); }
   __device__ static __forceinline__ uint32_t q(int ch) { return k(ch) + kTile; }
-  __device__ static __forceinline__ uint32_t v(int ch) { return kV + (uint32_t)(ch & 1) * (kStrips * kStrip); }
-  __device__ static __forceinline__ uint32_t rec(int ch) { return kRec + (uint32_t)(ch & 1) * kRecBytes; }
+  __device__ static __forceinline__ uint32_t v(int ch) { return kV + (uint32_t)(ch % kDepth) * (kStrips * kStrip); }
+  __device__ static __forceinline__ uint32_t rec(int ch) { return kRec + (uint32_t)(ch % kDepth) * kRecBytes; }
 };
 
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, uint32_t bar) {
@@ -163,11 +173,11 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* tm, int 
 
 // By a whole warp; `bar` counts its 32 lanes. Whole chunks by tensor maps; the rows behind a run's last chunk, which may
 // be another run's, are zeros, so that one comes row by row. v: the head's columns from v0 on, of a.dv in all.
-template <int DK, bool kBackward, int kStrips>
+template <int DK, bool kBackward, int kStrips, int kDepth>
 __device__ __forceinline__ void load_stage(int ch, uint32_t base, uint32_t bar, const DeltaArgs& a, const DeltaMaps& maps, const void* vp,
                                            int64_t ld_v, const unsigned char* rec, int64_t row0, int m, int grp, int h, int v0,
                                            int lane) {
-  using L = Stages<DK, kBackward, kStrips>;
+  using L = Stages<DK, kBackward, kStrips, kDepth>;
   const uint32_t tk = base + L::k(ch), tq = base + L::q(ch), tv = base + L::v(ch), tr = base + L::rec(ch);
   if (m == kC) {
     if (lane == 0) {
