@@ -31,6 +31,11 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 
+// A state as an operand: 64 of its rows to a tile (those behind the last strip of 16 are not written).
+template <int DK>
+constexpr int kStateTile = 64 * DK * 2;
+__host__ __device__ constexpr int state_tiles(int dv) { return (dv + 63) / 64; }
+
 // ------------------------------------------------------------------ dS through the chunks
 
 template <int DK, int NW>
@@ -39,7 +44,7 @@ struct Back : Stages<DK, true, NW, 2> {
 };
 
 template <int DK, int NW>
-__global__ void __launch_bounds__(32 * NW) delta_back_kernel(const __grid_constant__ DeltaBwdArgs a, const __grid_constant__ DeltaMaps maps, const unsigned char* records, bf16* ds) {
+__global__ void __launch_bounds__(32 * NW) delta_back_kernel(const __grid_constant__ DeltaBwdArgs a, const __grid_constant__ DeltaMaps maps, const unsigned char* records, unsigned char* ds) {
   using L = Back<DK, NW>;
   constexpr int KS = DK / 16;
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -94,9 +99,14 @@ __global__ void __launch_bounds__(32 * NW) delta_back_kernel(const __grid_consta
     __syncwarp();
     const uint32_t at = base + L::k(ch), qt = base + L::q(ch), rec = base + L::rec(ch), dt = base + L::v(ch) + warp * L::kStrip;
     const float* f = reinterpret_cast<const float*>(smem + (rec - base) + off_factors(true));
-    {  // dS1, for the gradients that take it as an operand (rounded as such)
-      bf16* o = ds + ((int64_t)(a.tab.tile[run] + ch) * a.heads + h) * a.dv * a.dk;
-      each([&](float* v, int64_t to) { *reinterpret_cast<uint32_t*>(o + to) = pair(v[0], v[1]); });
+    {  // dS1, for the gradients that take it as an operand (rounded as such), as they hold it in shared memory
+      unsigned char* o = ds + ((int64_t)(a.tab.tile[run] + ch) * a.heads + h) * state_tiles(a.dv) * kStateTile<DK> +
+                         (dv >> 6) * kStateTile<DK>;
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int i = 0; i < 2 * KS; ++i)
+          *reinterpret_cast<uint32_t*>(o + wide_at((dv & 63) + g + 8 * half, i) + 4 * t) = pair(s[i][2 * half], s[i][2 * half + 1]);
     }
     // dU^T = left (dS1^T)^T K^T + dO^T P
     float x[8][4];
@@ -223,20 +233,31 @@ __global__ void __launch_bounds__(32 * NW) delta_back_kernel(const __grid_consta
 
 // ------------------------------------------------------------------ the other gradients
 
-// A CTA takes a chunk and one group of keys, its heads one after another, so that what they add to a query or key is
-// summed in registers in their order. Warp w: rows 16 (w % 4) of the chunk, columns of half w / 4.
-constexpr int kGradThreads = 256;
+// An item is a chunk and one group of keys, its heads one after another, so that what they add to a query or key is
+// summed in registers in their order; a head in steps of 64 of its v channels, whose tiles are copied while the step
+// before is worked on. A CTA an SM takes every so-manieth item. Warp w: rows 16 (w % 4) of the chunk, columns of quarter w / 4; of the 64 x 64 products the first
+// two quarters have Pr and the others Er, each two of the four blocks of 16 columns.
+constexpr int kGradWarps = 16, kGradThreads = 32 * kGradWarps;
 
-template <int DK, int DV>
+template <int DK>
 struct Grad {
-  static constexpr int kState = DV * DK * 2, kTileK = kC * DK * 2, kTileV = kC * DV * 2, kSq = kC * kC * 2;
-  static constexpr int kS0 = 0, kDS = kState, kV = 2 * kState, kDO = kV + kTileV, kDV = kDO + kTileV, kR = kDV + kTileV;
-  static constexpr int kK = kR + kTileV, kQ = kK + kTileK, kF = kQ + kTileK, kE = kF + kSq, kInv = kE + kSq;
-  static constexpr int kFac = kInv + kTri, kVec = kFac + 9 * kC * 4;
-  // floats at kVec: sums of W's rows [2 halves], columns [2][4 row blocks], its diagonal, a and the write's rows [2 halves]
-  static constexpr int kRow = 0, kCol = 2 * kC, kDiag = 10 * kC, kA = 11 * kC, kWrite = 13 * kC, kDot = 15 * kC;
-  static constexpr int kSmem = kVec + (15 * kC + 8) * 4;
+  static constexpr int kTileK = kC * DK * 2, kState = kStateTile<DK>, kTile = kC * 64 * 2;
+  static constexpr int kK = 0, kQ = kTileK, kS0 = 4 * kTileK;  // K and Q twice: of the chunk at hand and the next
+  // of each step, twice: dS, V (then R), dO, dV (then F and E, the last step of a head)
+  static constexpr int kStep = kS0 + kState, kDS = 0, kV = kState, kDO = kV + kTile, kDV = kDO + kTile, kStepBytes = kDV + kTile;
+  static constexpr int kF = kDO, kE = kDV;
+  static constexpr int kR = kStep + 2 * kStepBytes, kWide = kR + kTile;  // kWide: S0 in fp32
+  // of each head, twice: Inv and the factors
+  static constexpr int kHead = kWide + 64 * DK * 4, kFac = kTri, kHeadBytes = kTri + 9 * kC * 4;
+  // floats at kVec: sums of W's rows [4 quarters], columns [2][4 row blocks], its diagonal, a and the write's rows
+  // [4 quarters], the inner product [16 warps]
+  static constexpr int kVec = kHead + 2 * kHeadBytes;
+  static constexpr int kRow = 0, kCol = 4 * kC, kDiag = 12 * kC, kA = 13 * kC, kWrite = 17 * kC, kDot = 21 * kC;
+  static constexpr int kBar = kVec + (21 * kC + 16) * 4, kSmem = kBar + 32;  // barriers: the steps' two, S0's; the flag
   static_assert(kSmem <= 232448, "shared memory plan exceeds 227 KB");
+};
+struct GradMaps {
+  CUtensorMap k, q, v, dy, dv;  // 64 rows of 64 columns of a head
 };
 
 __device__ __forceinline__ float sum_quad(float v) {  // over the lanes of a row
@@ -249,347 +270,414 @@ __device__ __forceinline__ float sum_rows(float v) {  // over the lanes of a col
   return v + __shfl_xor_sync(0xffffffffu, v, 16);
 }
 
-template <int DK, int DV>
-__global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __grid_constant__ DeltaBwdArgs a, const unsigned char* records, const bf16* ds) {
-  using L = Grad<DK, DV>;
-  constexpr int KS = DK / 16, VS = DV / 16, NK = DK / 16, NV = DV / 16;  // steps over columns; column tiles of a half
-  extern __shared__ __align__(128) unsigned char smem[];
+template <int DK>
+__global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __grid_constant__ DeltaBwdArgs a, const __grid_constant__ GradMaps maps,
+                                                                     const unsigned char* records, const unsigned char* ds) {
+  using L = Grad<DK>;
+  constexpr int KS = DK / 16, NK = DK / 32;  // steps over columns; column tiles of 8 of a quarter
+  extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t base = sm32(smem);
+  if (not_aligned(base, &g_delta_back_timeouts)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int rb = warp & 3, half = warp >> 2, r0 = 16 * rb;
-  const int grp = blockIdx.y, per = a.heads / a.groups;
-  const Chunk c = chunk_of(a.tab, blockIdx.x);
+  const int rb = warp & 3, quarter = warp >> 2, r0 = 16 * rb;
+  const bool second = quarter >= 2;  // of the 64 x 64 products: Er
+  // this warp's two blocks of their columns (the first and last, or those between: about the same number below the diagonal)
+  const int block[2] = {quarter & 1, 3 - (quarter & 1)};
+  const int per = a.heads / a.groups, halves = state_tiles(a.dv), steps = per * halves;
+  const int64_t items = (int64_t)a.tab.tile[a.tab.n] * a.groups;
   float* vec = reinterpret_cast<float*>(smem + L::kVec);
-  const float* f = reinterpret_cast<const float*>(smem + L::kFac);
+  volatile uint32_t* gave_up = reinterpret_cast<volatile uint32_t*>(smem + L::kBar + 24);
+  auto bar = [&](int i) { return base + L::kBar + 8u * (uint32_t)i; };  // 0, 1: a step's tiles; 2: its S0
 
-  auto tile = [&](uint32_t to, const void* from, int64_t ld, int64_t col, int width, auto cols) {  // 64 rows, zeros past the matrix
-    constexpr int C = decltype(cols)::value, units = C / 8;
-    const bf16* p = static_cast<const bf16*>(from) + col;
-    for (int e = threadIdx.x; e < kC * units; e += kGradThreads) {
-      const int r = e / units, u = e % units;
-      const bool in = r < c.len && 8 * u < width;
-      copy16(base + to + wide_at(r, u), p + (int64_t)(c.row + (in ? r : 0)) * ld + (in ? 8 * u : 0), in);
+  if (threadIdx.x == 0) {
+    bar_init(bar(0), kGradThreads);
+    bar_init(bar(1), kGradThreads);
+    bar_init(bar(2), 1);
+    *gave_up = 0u;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  auto bulk = [](uint32_t to, const void* from, int bytes, uint32_t b) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(to), "l"(from), "r"(bytes), "r"(b) : "memory");
+  };
+  // Of an item (a chunk and a group) and its i-th step the tiles, by every thread: whole chunks by tensor maps, a run's
+  // last rows one by one (zeros behind them). n: steps of this CTA before it, m: items.
+  auto fetch = [&](const Chunk& c, int chunk, int grp, int i, int n, int m) {
+    const int h = grp * per + i / halves, half = i % halves;
+    const uint32_t b = bar(n & 1), to = base + L::kStep + (uint32_t)(n & 1) * L::kStepBytes, kq = base + (uint32_t)(m & 1) * (2 * L::kTileK);
+    if (threadIdx.x == 0) {
+      const int64_t item = (int64_t)chunk * a.heads + h;
+      const bool whole = c.len == kC;
+      uint32_t bytes = L::kState + (whole ? 3 * L::kTile : 0);
+      if (half == 0) bytes += L::kHeadBytes;
+      if (i == 0 && whole) bytes += 2 * L::kTileK;
+      asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(b), "r"(bytes) : "memory");
+      // S0, fp32, into the place that the step before has emptied
+      const int rows = min(64, a.dv - 64 * half);
+      asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar(2)), "r"(rows * a.dk * 4) : "memory");
+      bulk(base + L::kWide, a.ckpt + (item * a.dv + 64 * half) * a.dk, rows * a.dk * 4, bar(2));
+      bulk(to + L::kDS, ds + (item * halves + half) * L::kState, L::kState, b);
+      if (whole) {
+        if (i == 0) {
+#pragma unroll
+          for (int x = 0; x < DK / 64; ++x) {
+            tma_3d(kq + L::kK + x * kC * 128, &maps.k, 64 * x, grp, c.row, b);
+            tma_3d(kq + L::kQ + x * kC * 128, &maps.q, 64 * x, grp, c.row, b);
+          }
+        }
+        tma_3d(to + L::kV, &maps.v, 64 * half, h, c.row, b);
+        tma_3d(to + L::kDO, &maps.dy, 64 * half, h, c.row, b);
+        tma_3d(to + L::kDV, &maps.dv, 64 * half, h, c.row, b);
+      }
+      if (half == 0) {
+        const unsigned char* rec = records + item * record_bytes(true);
+        const uint32_t head = base + L::kHead + (uint32_t)((m * per + i / halves) & 1) * L::kHeadBytes;
+        bulk(head, rec, kTri, b);
+        bulk(head + L::kFac, rec + off_factors(true), 9 * kC * 4, b);
+      }
+    }
+    if (c.len < kC) {
+      auto rows = [&](uint32_t at, const void* from, int64_t ld, int64_t col, int width, int units) {
+        const bf16* p = static_cast<const bf16*>(from) + col;
+        for (int e = threadIdx.x; e < kC * units; e += kGradThreads) {
+          const int r = e / units, u = e % units;
+          const bool in = r < c.len && 8 * u < width;
+          copy16(at + wide_at(r, u), p + (int64_t)(c.row + (in ? r : 0)) * ld + (in ? 8 * u : 0), in);
+        }
+      };
+      if (i == 0) {
+        rows(kq + L::kK, a.k, a.ld_k, (int64_t)grp * a.dk, a.dk, DK / 8);
+        rows(kq + L::kQ, a.q, a.ld_q, (int64_t)grp * a.dk, a.dk, DK / 8);
+      }
+      const int64_t col = (int64_t)h * a.dv + 64 * half;
+      const int width = a.dv - 64 * half;
+      rows(to + L::kV, a.v, a.ld_v, col, width, 8);
+      rows(to + L::kDO, a.dy, a.ld_dy, col, width, 8);
+      rows(to + L::kDV, a.dv_out, a.ld_dv, col, width, 8);
+      bar_arrive_copies(b);  // (the barrier counts every thread)
+    } else {
+      bar_arrive(b);
     }
   };
-  tile(L::kK, a.k, a.ld_k, (int64_t)grp * a.dk, a.dk, std::integral_constant<int, DK>{});
-  tile(L::kQ, a.q, a.ld_q, (int64_t)grp * a.dk, a.dk, std::integral_constant<int, DK>{});
 
-  float dq[NK][4], dk[NK][4], qk[8][4];  // qk: Q K^T in the first half's warps, K K^T in the second's
+  float dq[NK][4], dk[NK][4], qk[2][2][4];  // qk: Q K^T (or K K^T) of this warp's two blocks
+  uint32_t kq0 = 0;  // where the item's K and Q are
+  // the pair of a key or query that this thread's sum (column tile i of its quarter, row g + 8 e) is of
+  auto pair_at = [&](uint32_t tile, int i, int e) -> uint32_t* {
+    return reinterpret_cast<uint32_t*>(smem + kq0 + tile + wide_at(r0 + g + 8 * e, quarter * NK + i) + 4 * t);
+  };
+  float x[2][2][4], at_row[2], write_row[2], dot = 0.0f;  // Pr or Er; rows' parts of a and of the write; <dS1, S0>
+
+  int64_t item = blockIdx.x;  // (no more CTAs than items)
+  Chunk c = chunk_of(a.tab, (int)(item / a.groups));
+  fetch(c, (int)(item / a.groups), (int)(item % a.groups), 0, 0, 0);
+  int n = 0;
+  for (int m = 0; item < items; ++m, item += gridDim.x) {
+  const int grp = (int)(item % a.groups);
+  const int64_t after = item + gridDim.x;
+  const Chunk next = after < items ? chunk_of(a.tab, (int)(after / a.groups)) : c;
+  kq0 = (uint32_t)(m & 1) * (2 * L::kTileK);
+  const uint32_t kq = base + kq0;
 #pragma unroll
   for (int i = 0; i < NK; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) dq[i][j] = dk[i][j] = 0.0f;
-  // the pair of a [64][C] tile that this thread's sum (column tile i of its half, row g + 8 e) is of
-  auto pair_at = [&](uint32_t tile_off, int i, int e, auto cols) -> uint32_t* {
-    constexpr int C = decltype(cols)::value;
-    return reinterpret_cast<uint32_t*>(smem + tile_off + wide_at(r0 + g + 8 * e, half * (C / 16) + i) + 4 * t);
-  };
-  constexpr std::integral_constant<int, DK> wide_k{};
-  constexpr std::integral_constant<int, DV> wide_v{};
-
-  for (int hh = 0; hh < per; ++hh) {
-    const int h = grp * per + hh;
-    if (hh > 0) __syncthreads();  // the last head's tiles have been read
-    tile(L::kV, a.v, a.ld_v, (int64_t)h * a.dv, a.dv, wide_v);
-    tile(L::kDO, a.dy, a.ld_dy, (int64_t)h * a.dv, a.dv, wide_v);
-    tile(L::kDV, a.dv_out, a.ld_dv, (int64_t)h * a.dv, a.dv, wide_v);
-    const int64_t item = (int64_t)blockIdx.x * a.heads + h;
-    const unsigned char* rec = records + item * record_bytes(true);
-    for (int e = threadIdx.x; e < kTri / 16; e += kGradThreads) copy16(base + L::kInv + 16 * e, rec + 16 * e, true);
-    for (int e = threadIdx.x; e < 9 * kC / 4; e += kGradThreads) copy16(base + L::kFac + 16 * e, rec + off_factors(true) + 16 * e, true);
-    copies_end();
-    {  // S0 as bf16, dS1, and their inner product
-      const float* s0 = a.ckpt + item * a.dv * a.dk;
-      const bf16* s1 = ds + item * a.dv * a.dk;
-      float dot = 0.0f;
-      for (int e = threadIdx.x; e < DV * DK / 8; e += kGradThreads) {
-        const int r = e / (DK / 8), u = e % (DK / 8);
-        uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
-        if (r < a.dv && 8 * u < a.dk) {
-          float v[8], d[8];
-          Vec16<float>::load_stream(s0 + (int64_t)r * a.dk + 8 * u, v);
-          Vec16<float>::load_stream(s0 + (int64_t)r * a.dk + 8 * u + 4, v + 4);
-          w1 = __ldcs(reinterpret_cast<const uint4*>(s1 + (int64_t)r * a.dk + 8 * u));
-          Vec16<bf16>::unpack(w1, d);
+  for (int i = 0; i < steps; ++i, ++n) {
+    const int half = i % halves, hh = i / halves, h = grp * per + hh;
+    const uint32_t st = L::kStep + (uint32_t)(n & 1) * L::kStepBytes;
+    const unsigned char* head = smem + L::kHead + ((m * per + hh) & 1) * L::kHeadBytes;
+    const uint32_t inv = sm32(head);
+    const float* f = reinterpret_cast<const float*>(head + L::kFac);
+    const int strips = min(4, (a.dv - 64 * half + 15) / 16), rows = min(64, a.dv - 64 * half);
+    bar_wait(bar(n & 1), (uint32_t)((n >> 1) & 1), gave_up);
+    bar_wait(bar(2), (uint32_t)(n & 1), gave_up);
+    if (half == 0) {
+      dot = at_row[0] = at_row[1] = write_row[0] = write_row[1] = 0.0f;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) dot = fmaf(v[j], d[j], dot);
-          w0 = Vec16<bf16>::pack(v);
-        }
-        *reinterpret_cast<uint4*>(smem + L::kS0 + wide_at<DV>(r, u)) = w0;
-        *reinterpret_cast<uint4*>(smem + L::kDS + wide_at<DV>(r, u)) = w1;
-      }
+      for (int o = 0; o < 2; ++o)
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      if (lane == 0) vec[L::kDot + warp] = dot;
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[o][n][j] = 0.0f;
     }
-    copies_done();
+    for (int e = threadIdx.x; e < 16 * strips * (DK / 8); e += kGradThreads) {  // S0 as an operand, and its product with dS1
+      const int r = e / (DK / 8), u = e % (DK / 8);
+      uint4 w = make_uint4(0, 0, 0, 0);
+      if (r < rows && 8 * u < a.dk) {
+        float v[8], d[8];
+        const float* from = reinterpret_cast<const float*>(smem + L::kWide) + r * a.dk + 8 * u;
+        Vec16<float>::load(from, v);
+        Vec16<float>::load(from + 4, v + 4);
+        Vec16<bf16>::unpack(*reinterpret_cast<const uint4*>(smem + st + L::kDS + wide_at(r, u)), d);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dot = fmaf(v[j], d[j], dot);
+        w = Vec16<bf16>::pack(v);
+      }
+      *reinterpret_cast<uint4*>(smem + L::kS0 + wide_at(r, u)) = w;
+    }
     __syncthreads();
-    if (hh == 0) {
+    if (i + 1 < steps) fetch(c, (int)(item / a.groups), grp, i + 1, n + 1, m);
+    else if (after < items) fetch(next, (int)(after / a.groups), (int)(after % a.groups), 0, n + 1, m + 1);
+    if (i == 0) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int o = 0; o < 2; ++o)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) qk[i][j] = 0.0f;
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) qk[o][n][j] = 0.0f;
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        uint32_t x[4], b[4];
-        load4(x, base + (half ? L::kK : L::kQ) + wide_cols(r0, 2 * ks, lane));
+        uint32_t v[4], b[4];
+        load4(v, kq + (second ? L::kK : L::kQ) + wide_cols(r0, 2 * ks, lane));
 #pragma unroll
-        for (int nb = 0; nb < 4; ++nb)
-          if (nb <= rb) {
-            load4(b, base + L::kK + wide_rows(16 * nb, 2 * ks, lane));
-            mma(qk[2 * nb], x, b[0], b[1]);
-            mma(qk[2 * nb + 1], x, b[2], b[3]);
+        for (int o = 0; o < 2; ++o)
+          if (block[o] <= rb) {
+            load4(b, kq + L::kK + wide_rows(16 * block[o], 2 * ks, lane));
+            mma(qk[o][0], v, b[0], b[1]);
+            mma(qk[o][1], v, b[2], b[3]);
           }
       }
     }
-    // R = V - up K S0^T, in V's place
-    {
-      float x[NV][4];
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[i][j] = 0.0f;
+    // R = V - up K S0^T, in V's place: a strip of 16 channels a quarter
+    if (quarter < strips) {
+      float y[2][4];
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         uint32_t k[4], b[4];
-        load4(k, base + L::kK + wide_cols(r0, 2 * ks, lane));
-#pragma unroll
-        for (int nb = 0; nb < NV / 2; ++nb) {
-          load4(b, base + L::kS0 + wide_rows<DV>(half * (DV / 2) + 16 * nb, 2 * ks, lane));
-          mma(x[2 * nb], k, b[0], b[1]);
-          mma(x[2 * nb + 1], k, b[2], b[3]);
-        }
+        load4(k, kq + L::kK + wide_cols(r0, 2 * ks, lane));
+        load4(b, base + L::kS0 + wide_rows(16 * quarter, 2 * ks, lane));
+        mma_if(ks == 0, y[0], k, b[0], b[1]);
+        mma_if(ks == 0, y[1], k, b[2], b[3]);
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const float up = f[kUp + r0 + g + 8 * e];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          uint32_t* p = pair_at(L::kV, i, e, wide_v);
-          *p = pair(fmaf(-up, x[i][2 * e], __uint_as_float(*p << 16)), fmaf(-up, x[i][2 * e + 1], __uint_as_float(*p & 0xffff0000u)));
+        for (int n = 0; n < 2; ++n) {
+          uint32_t* p = reinterpret_cast<uint32_t*>(smem + st + L::kV + wide_at(r0 + g + 8 * e, 2 * quarter + n) + 4 * t);
+          *p = pair(fmaf(-up, y[n][2 * e], __uint_as_float(*p << 16)), fmaf(-up, y[n][2 * e + 1], __uint_as_float(*p & 0xffff0000u)));
         }
       }
     }
     __syncthreads();
-    {  // r = Inv R
-      float x[NV][4];
+    if (quarter < strips) {  // r = Inv R
+      float y[2][4];
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
+      for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[i][j] = 0.0f;
+        for (int j = 0; j < 4; ++j) y[n][j] = 0.0f;
       for (int jb = 0; jb <= rb; ++jb) {
         uint32_t w[4], b[4];
-        load4(w, base + L::kInv + block_at(rb, jb) + narrow_cols(0, lane));
-#pragma unroll
-        for (int nb = 0; nb < NV / 2; ++nb) {
-          load4t(b, base + L::kV + wide_cols(16 * jb, half * (DV / 16) + 2 * nb, lane));
-          mma(x[2 * nb], w, b[0], b[1]);
-          mma(x[2 * nb + 1], w, b[2], b[3]);
-        }
+        load4(w, inv + block_at(rb, jb) + narrow_cols(0, lane));
+        load4t(b, base + st + L::kV + wide_cols(16 * jb, 2 * quarter, lane));
+        mma(y[0], w, b[0], b[1]);
+        mma(y[1], w, b[2], b[3]);
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int i = 0; i < NV; ++i) *pair_at(L::kR, i, e, wide_v) = pair(x[i][2 * e], x[i][2 * e + 1]);
+        for (int n = 0; n < 2; ++n)
+          *reinterpret_cast<uint32_t*>(smem + L::kR + wide_at(r0 + g + 8 * e, 2 * quarter + n) + 4 * t) = pair(y[n][2 * e], y[n][2 * e + 1]);
     }
     __syncthreads();
-    {  // Pr (first half) or Er, F or -E, and W's sums
-      float x[8][4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+    for (int ks = 0; ks < 4; ++ks)  // Pr or Er
+      if (ks < strips) {
+        uint32_t w[4], b[4];
+        load4(w, base + st + (second ? L::kDV : L::kDO) + wide_cols(r0, 2 * ks, lane));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[i][j] = 0.0f;
-#pragma unroll
-      for (int ks = 0; ks < VS; ++ks) {
-        uint32_t d[4], b[4];
-        load4(d, base + (half ? L::kDV : L::kDO) + wide_cols(r0, 2 * ks, lane));
-#pragma unroll
-        for (int nb = 0; nb < 4; ++nb)
-          if (nb <= rb) {
-            load4(b, base + L::kR + wide_rows(16 * nb, 2 * ks, lane));
-            mma(x[2 * nb], d, b[0], b[1]);
-            mma(x[2 * nb + 1], d, b[2], b[3]);
+        for (int p = 0; p < 2; ++p)
+          if (block[p] <= rb) {
+            load4(b, base + L::kR + wide_rows(16 * block[p], 2 * ks, lane));
+            mma(x[p][0], w, b[0], b[1]);
+            mma(x[p][1], w, b[2], b[3]);
           }
       }
-      float row[2] = {0.0f, 0.0f};
+    // what goes through the states, one product after another (all three at once take more registers than there are)
+    auto through = [&](uint32_t left, uint32_t right, float (&y)[NK][4]) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float col[2] = {0.0f, 0.0f};
-        if (i / 2 <= rb) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int at = r0 + g + 8 * e;
-            const float mine = half ? f[kKn + at] : f[kQn + at] * a.scale;
-            float out[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const int to = 8 * i + 2 * t + j;
-              const bool in = half ? to < at : to <= at;
-              const float d = in ? ex2((f[kGHi + at] - f[kGHi + to]) + (f[kGLo + at] - f[kGLo + to])) * f[kKn + to] * mine : 0.0f;
-              const float p = x[i][2 * e + j] * d, w = p * qk[i][2 * e + j];
-              out[j] = half ? -p * f[kBeta + to] : p * f[kBeta + to];
-              if (to < at) {
-                row[e] = fmaf(f[kBeta + to], w, row[e]);
-                col[j] += w;
-              } else if (to == at && !half) {
-                vec[L::kDiag + at] = w;
-              }
-            }
-            *reinterpret_cast<uint32_t*>(smem + (half ? L::kE : L::kF) + wide_at(at, i) + 4 * t) = pair(out[0], out[1]);
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float total = sum_rows(col[j]);
-          if (g == 0) vec[L::kCol + (4 * half + rb) * kC + 8 * i + 2 * t + j] = total;
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        row[e] = sum_quad(row[e]);
-        if (t == 0) vec[L::kRow + half * kC + r0 + g + 8 * e] = row[e];
-      }
-    }
-    {  // what goes through the states
-      float x[NK][4], at[2] = {0.0f, 0.0f};
-      auto product = [&](uint32_t left, uint32_t right) {
-#pragma unroll
-        for (int i = 0; i < NK; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) x[i][j] = 0.0f;
-#pragma unroll
-        for (int ks = 0; ks < VS; ++ks) {
-          uint32_t d[4], b[4];
-          load4(d, base + left + wide_cols(r0, 2 * ks, lane));
+      for (int ks = 0; ks < 4; ++ks)
+        if (ks < strips) {
+          uint32_t w[4], b[4];
+          load4(w, left + wide_cols(r0, 2 * ks, lane));
 #pragma unroll
           for (int nb = 0; nb < NK / 2; ++nb) {
-            load4t(b, base + right + wide_cols<DV>(16 * ks, half * (DK / 16) + 2 * nb, lane));
-            mma(x[2 * nb], d, b[0], b[1]);
-            mma(x[2 * nb + 1], d, b[2], b[3]);
+            load4t(b, right + wide_cols(16 * ks, quarter * NK + 2 * nb, lane));
+            mma_if(ks == 0, y[2 * nb], w, b[0], b[1]);
+            mma_if(ks == 0, y[2 * nb + 1], w, b[2], b[3]);
           }
         }
-      };
-      // adds w x to a gradient, and gives w x . (query or key) of the row
-      auto add = [&](float (&to)[NK][4], int e, float w, uint32_t with) {
-        float dot = 0.0f;
+    };
+    // adds w y to a gradient; gives y . (query or key) of the row
+    auto add = [&](const float (&y)[NK][4], int e, float w, uint32_t with, float (&to)[NK][4]) {
+      float dots[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < NK; ++i) {
-          const uint32_t p = *pair_at(with, i, e, wide_k);
-          dot = fmaf(x[i][2 * e], __uint_as_float(p << 16), dot);
-          dot = fmaf(x[i][2 * e + 1], __uint_as_float(p & 0xffff0000u), dot);
-          to[i][2 * e] = fmaf(w, x[i][2 * e], to[i][2 * e]);
-          to[i][2 * e + 1] = fmaf(w, x[i][2 * e + 1], to[i][2 * e + 1]);
-        }
-        return dot * w;
-      };
-      product(L::kDO, L::kS0);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) at[e] += add(dq, e, f[kUpQ + r0 + g + 8 * e], L::kQ);
-      product(L::kDV, L::kS0);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) at[e] += add(dk, e, -f[kUp + r0 + g + 8 * e], L::kK);
-      product(L::kR, L::kDS);
+      for (int i = 0; i < NK; ++i) {
+        const uint32_t p = *pair_at(with, i, e);
+        dots[0] = fmaf(y[i][2 * e], __uint_as_float(p << 16), dots[0]);
+        dots[1] = fmaf(y[i][2 * e + 1], __uint_as_float(p & 0xffff0000u), dots[1]);
+        to[i][2 * e] = fmaf(w, y[i][2 * e], to[i][2 * e]);
+        to[i][2 * e + 1] = fmaf(w, y[i][2 * e + 1], to[i][2 * e + 1]);
+      }
+      return dots[0] + dots[1];
+    };
+    {
+      float y[NK][4];
+      through(base + st + L::kDO, base + L::kS0, y);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int i = r0 + g + 8 * e;
-        float dot = 0.0f;  // without beta, which dbeta is without
-        const float left = f[kLeft + i], w = left * f[kBeta + i];
+        const float w = f[kUpQ + r0 + g + 8 * e];
+        at_row[e] = fmaf(w, add(y, e, w, L::kQ, dq), at_row[e]);
+      }
+      through(base + st + L::kDV, base + L::kS0, y);
 #pragma unroll
-        for (int n = 0; n < NK; ++n) {
-          const uint32_t p = *pair_at(L::kK, n, e, wide_k);
-          dot = fmaf(x[n][2 * e], __uint_as_float(p << 16), dot);
-          dot = fmaf(x[n][2 * e + 1], __uint_as_float(p & 0xffff0000u), dot);
-          dk[n][2 * e] = fmaf(w, x[n][2 * e], dk[n][2 * e]);
-          dk[n][2 * e + 1] = fmaf(w, x[n][2 * e + 1], dk[n][2 * e + 1]);
+      for (int e = 0; e < 2; ++e) {
+        const float w = -f[kUp + r0 + g + 8 * e];
+        at_row[e] = fmaf(w, add(y, e, w, L::kK, dk), at_row[e]);
+      }
+      through(base + L::kR, base + st + L::kDS, y);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {  // (the write's product without beta, which dbeta is without)
+        const float w = f[kLeft + r0 + g + 8 * e];
+        write_row[e] = fmaf(w, add(y, e, w * f[kBeta + r0 + g + 8 * e], L::kK, dk), write_row[e]);
+      }
+    }
+    if (half == halves - 1) {
+      __syncthreads();  // dO and dV have been read
+      // F or -E, and W's sums
+      float row[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int o = 0; o < 2; ++o)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const int to0 = 16 * block[o] + 8 * n + 2 * t;
+          float col[2] = {0.0f, 0.0f};
+          if (block[o] <= rb) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int at = r0 + g + 8 * e;
+              const float mine = second ? f[kKn + at] : f[kQn + at] * a.scale;
+              float out[2];
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const int to = to0 + j;
+                const bool in = second ? to < at : to <= at;
+                const float d = in ? ex2((f[kGHi + at] - f[kGHi + to]) + (f[kGLo + at] - f[kGLo + to])) * f[kKn + to] * mine : 0.0f;
+                const float p = x[o][n][2 * e + j] * d, w = p * qk[o][n][2 * e + j];
+                out[j] = second ? -p * f[kBeta + to] : p * f[kBeta + to];
+                if (to < at) {
+                  row[e] = fmaf(f[kBeta + to], w, row[e]);
+                  col[j] += w;
+                } else if (to == at && !second) {
+                  vec[L::kDiag + at] = w;
+                }
+              }
+              *reinterpret_cast<uint32_t*>(smem + st + (second ? L::kE : L::kF) + wide_at(at, 2 * block[o] + n) + 4 * t) = pair(out[0], out[1]);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float total = sum_rows(col[j]);
+            if (g == 0) vec[L::kCol + ((second ? 4 : 0) + rb) * kC + to0 + j] = total;
+          }
         }
-        dot = sum_quad(dot * left);
-        const float av = sum_quad(at[e]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float s = sum_quad(row[e]), av = sum_quad(at_row[e]), wr = sum_quad(write_row[e]);
         if (t == 0) {
-          vec[L::kWrite + half * kC + i] = dot;
-          vec[L::kA + half * kC + i] = av;
+          vec[L::kRow + quarter * kC + r0 + g + 8 * e] = s;
+          vec[L::kA + quarter * kC + r0 + g + 8 * e] = av;
+          vec[L::kWrite + quarter * kC + r0 + g + 8 * e] = wr;
+        }
+      }
+      float d = dot;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+      if (lane == 0) vec[L::kDot + warp] = d;
+      __syncthreads();
+      // within the chunk
+      for (int jb = 0; jb <= rb; ++jb) {
+        uint32_t w[4], e[4], b[4];
+        load4(w, base + st + L::kF + wide_cols(r0, 2 * jb, lane));
+        load4(e, base + st + L::kE + wide_cols(r0, 2 * jb, lane));
+#pragma unroll
+        for (int nb = 0; nb < NK / 2; ++nb) {
+          load4t(b, kq + L::kK + wide_cols(16 * jb, quarter * NK + 2 * nb, lane));
+          mma(dq[2 * nb], w, b[0], b[1]);
+          mma(dq[2 * nb + 1], w, b[2], b[3]);
+          mma(dk[2 * nb], e, b[0], b[1]);
+          mma(dk[2 * nb + 1], e, b[2], b[3]);
+        }
+      }
+      for (int ib = rb; ib < 4; ++ib) {
+        uint32_t w[4], e[4], b[4];
+        load4t(w, base + st + L::kF + wide_rows(16 * ib, 2 * rb, lane));
+        load4t(e, base + st + L::kE + wide_rows(16 * ib, 2 * rb, lane));
+#pragma unroll
+        for (int nb = 0; nb < NK / 2; ++nb) {
+          load4t(b, kq + L::kQ + wide_cols(16 * ib, quarter * NK + 2 * nb, lane));
+          mma(dk[2 * nb], w, b[0], b[1]);
+          mma(dk[2 * nb + 1], w, b[2], b[3]);
+          load4t(b, kq + L::kK + wide_cols(16 * ib, quarter * NK + 2 * nb, lane));
+          mma(dk[2 * nb], e, b[0], b[1]);
+          mma(dk[2 * nb + 1], e, b[2], b[3]);
+        }
+      }
+      if (warp == 0 && (a.dg || a.dbeta)) {  // tokens 2 lane and + 1
+        float inner = 0.0f, step[2], all = 0.0f, db[2];
+#pragma unroll
+        for (int w = 0; w < kGradWarps; ++w) inner += vec[L::kDot + w];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int at = 2 * lane + j;
+          auto four = [&](int from) { return (vec[from + at] + vec[from + kC + at]) + (vec[from + 2 * kC + at] + vec[from + 3 * kC + at]); };
+          const float col = four(L::kCol) - four(L::kCol + 4 * kC), av = four(L::kA), wr = four(L::kWrite);
+          const float row_sum = (vec[L::kRow + at] + vec[L::kRow + kC + at]) - (vec[L::kRow + 2 * kC + at] + vec[L::kRow + 3 * kC + at]);
+          db[j] = wr + vec[L::kDiag + at] + col;
+          step[j] = f[kBeta + at] * (wr + col) - av - row_sum;
+          all += av;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+        float before = step[0] + step[1];  // of the lanes before this one, exclusive
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const float u = __shfl_up_sync(0xffffffffu, before, o);
+          if (lane >= o) before += u;
+        }
+        before -= step[0] + step[1];
+        const float start = fmaf(f[kGamma], inner, all);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int at = 2 * lane + j;
+          if (at >= c.len) break;
+          const int64_t to = (int64_t)(c.row + at) * a.heads + h;
+          if (a.dg) static_cast<bf16*>(a.dg)[to] = __float2bfloat16_rn(start + before + (j ? step[0] : 0.0f));
+          if (a.dbeta) static_cast<bf16*>(a.dbeta)[to] = __float2bfloat16_rn(db[j]);
         }
       }
     }
-    __syncthreads();
-    // within the chunk
-    for (int jb = 0; jb <= rb; ++jb) {
-      uint32_t w[4], e[4], b[4];
-      load4(w, base + L::kF + wide_cols(r0, 2 * jb, lane));
-      load4(e, base + L::kE + wide_cols(r0, 2 * jb, lane));
-#pragma unroll
-      for (int nb = 0; nb < NK / 2; ++nb) {
-        load4t(b, base + L::kK + wide_cols(16 * jb, half * (DK / 16) + 2 * nb, lane));
-        mma(dq[2 * nb], w, b[0], b[1]);
-        mma(dq[2 * nb + 1], w, b[2], b[3]);
-        mma(dk[2 * nb], e, b[0], b[1]);
-        mma(dk[2 * nb + 1], e, b[2], b[3]);
-      }
-    }
-    for (int ib = rb; ib < 4; ++ib) {
-      uint32_t w[4], e[4], b[4];
-      load4t(w, base + L::kF + wide_rows(16 * ib, 2 * rb, lane));
-      load4t(e, base + L::kE + wide_rows(16 * ib, 2 * rb, lane));
-#pragma unroll
-      for (int nb = 0; nb < NK / 2; ++nb) {
-        load4t(b, base + L::kQ + wide_cols(16 * ib, half * (DK / 16) + 2 * nb, lane));
-        mma(dk[2 * nb], w, b[0], b[1]);
-        mma(dk[2 * nb + 1], w, b[2], b[3]);
-        load4t(b, base + L::kK + wide_cols(16 * ib, half * (DK / 16) + 2 * nb, lane));
-        mma(dk[2 * nb], e, b[0], b[1]);
-        mma(dk[2 * nb + 1], e, b[2], b[3]);
-      }
-    }
-    if (warp == 0 && (a.dg || a.dbeta)) {  // tokens 2 lane and + 1
-      float dot = 0.0f, step[2], all = 0.0f, db[2];
-#pragma unroll
-      for (int w = 0; w < kGradThreads / 32; ++w) dot += vec[L::kDot + w];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int i = 2 * lane + j;
-        float col = 0.0f;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) col += vec[L::kCol + r * kC + i] - vec[L::kCol + (4 + r) * kC + i];
-        const float av = vec[L::kA + i] + vec[L::kA + kC + i], wr = vec[L::kWrite + i] + vec[L::kWrite + kC + i];
-        db[j] = wr + vec[L::kDiag + i] + col;
-        step[j] = f[kBeta + i] * (wr + col) - av - (vec[L::kRow + i] - vec[L::kRow + kC + i]);
-        all += av;
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-      float before = step[0] + step[1];  // of the lanes before this one, exclusive
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const float u = __shfl_up_sync(0xffffffffu, before, o);
-        if (lane >= o) before += u;
-      }
-      before -= step[0] + step[1];
-      const float start = fmaf(f[kGamma], dot, all);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int i = 2 * lane + j;
-        if (i >= c.len) break;
-        const int64_t to = (int64_t)(c.row + i) * a.heads + h;
-        if (a.dg) static_cast<bf16*>(a.dg)[to] = __float2bfloat16_rn(start + before + (j ? step[0] : 0.0f));
-        if (a.dbeta) static_cast<bf16*>(a.dbeta)[to] = __float2bfloat16_rn(db[j]);
-      }
-    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (R was written where a later step's v comes)
+    __syncthreads();  // this step's tiles have been read
   }
-  __syncthreads();
+  // (any head's lengths; the copies under way go to the other)
+  const float* f = reinterpret_cast<const float*>(smem + L::kHead + ((m * per + per - 1) & 1) * L::kHeadBytes + L::kFac);
   // a length's own gradient: d - kappa^2 (x . d) x
   if (a.l2_eps >= 0.0f) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       float dots[2] = {0.0f, 0.0f};
 #pragma unroll
-      for (int i = 0; i < NK; ++i) {
-        const uint32_t q = *pair_at(L::kQ, i, e, wide_k), k = *pair_at(L::kK, i, e, wide_k);
-        dots[0] = fmaf(dq[i][2 * e], __uint_as_float(q << 16), fmaf(dq[i][2 * e + 1], __uint_as_float(q & 0xffff0000u), dots[0]));
-        dots[1] = fmaf(dk[i][2 * e], __uint_as_float(k << 16), fmaf(dk[i][2 * e + 1], __uint_as_float(k & 0xffff0000u), dots[1]));
+      for (int n = 0; n < NK; ++n) {
+        const uint32_t q = *pair_at(L::kQ, n, e), k = *pair_at(L::kK, n, e);
+        dots[0] = fmaf(dq[n][2 * e], __uint_as_float(q << 16), fmaf(dq[n][2 * e + 1], __uint_as_float(q & 0xffff0000u), dots[0]));
+        dots[1] = fmaf(dk[n][2 * e], __uint_as_float(k << 16), fmaf(dk[n][2 * e + 1], __uint_as_float(k & 0xffff0000u), dots[1]));
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const float d = sum_quad(dots[j]);
-        if (t == 0) vec[(2 * j + half) * kC + r0 + g + 8 * e] = d;
+        if (t == 0) vec[(4 * j + quarter) * kC + r0 + g + 8 * e] = d;
       }
     }
     __syncthreads();
@@ -599,14 +687,15 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
     const int at = r0 + g + 8 * e;
     float wq = 0.0f, wk = 0.0f;
     if (a.l2_eps >= 0.0f) {
-      wq = f[kQn + at] * f[kQn + at] * (vec[at] + vec[kC + at]);
-      wk = f[kKn + at] * f[kKn + at] * (vec[2 * kC + at] + vec[3 * kC + at]);
+      auto four = [&](int from) { return (vec[from + at] + vec[from + kC + at]) + (vec[from + 2 * kC + at] + vec[from + 3 * kC + at]); };
+      wq = f[kQn + at] * f[kQn + at] * four(0);
+      wk = f[kKn + at] * f[kKn + at] * four(4 * kC);
     }
 #pragma unroll
-    for (int i = 0; i < NK; ++i) {
-      uint32_t *q = pair_at(L::kQ, i, e, wide_k), *k = pair_at(L::kK, i, e, wide_k);
-      *q = pair(fmaf(-wq, __uint_as_float(*q << 16), dq[i][2 * e]), fmaf(-wq, __uint_as_float(*q & 0xffff0000u), dq[i][2 * e + 1]));
-      *k = pair(fmaf(-wk, __uint_as_float(*k << 16), dk[i][2 * e]), fmaf(-wk, __uint_as_float(*k & 0xffff0000u), dk[i][2 * e + 1]));
+    for (int n = 0; n < NK; ++n) {
+      uint32_t *q = pair_at(L::kQ, n, e), *k = pair_at(L::kK, n, e);
+      *q = pair(fmaf(-wq, __uint_as_float(*q << 16), dq[n][2 * e]), fmaf(-wq, __uint_as_float(*q & 0xffff0000u), dq[n][2 * e + 1]));
+      *k = pair(fmaf(-wk, __uint_as_float(*k << 16), dk[n][2 * e]), fmaf(-wk, __uint_as_float(*k & 0xffff0000u), dk[n][2 * e + 1]));
     }
   }
   __syncthreads();
@@ -615,14 +704,19 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
     if (r >= c.len || 8 * u >= a.dk) continue;
     const int64_t col = (int64_t)grp * a.dk + 8 * u;
     *reinterpret_cast<uint4*>(static_cast<bf16*>(a.dq) + (int64_t)(c.row + r) * a.ld_dq + col) =
-        *reinterpret_cast<const uint4*>(smem + L::kQ + wide_at(r, u));
+        *reinterpret_cast<const uint4*>(smem + kq0 + L::kQ + wide_at(r, u));
     *reinterpret_cast<uint4*>(static_cast<bf16*>(a.dk_out) + (int64_t)(c.row + r) * a.ld_dk + col) =
-        *reinterpret_cast<const uint4*>(smem + L::kK + wide_at(r, u));
+        *reinterpret_cast<const uint4*>(smem + kq0 + L::kK + wide_at(r, u));
   }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (the gradients were written where later keys come)
+  __syncthreads();
+  c = next;
+  }
+  if (threadIdx.x == 0 && *gave_up) atomicAdd(&g_delta_back_timeouts, 1u);
 }
 
 template <int DK, int NW>
-cudaError_t run_back(const DeltaBwdArgs& a, const DeltaMaps& maps, const unsigned char* records, bf16* ds, cudaStream_t st) {
+cudaError_t run_back(const DeltaBwdArgs& a, const DeltaMaps& maps, const unsigned char* records, unsigned char* ds, cudaStream_t st) {
   using L = Back<DK, NW>;
   auto kernel = delta_back_kernel<DK, NW>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
@@ -632,20 +726,27 @@ cudaError_t run_back(const DeltaBwdArgs& a, const DeltaMaps& maps, const unsigne
   return cudaGetLastError();
 }
 
-template <int DK, int DV>
-cudaError_t run_grad(const DeltaBwdArgs& a, const unsigned char* records, const bf16* ds, cudaStream_t st) {
-  using L = Grad<DK, DV>;
+template <int DK>
+cudaError_t run_grad(const DeltaBwdArgs& a, const unsigned char* records, const unsigned char* ds, cudaStream_t st) {
+  using L = Grad<DK>;
   const int chunks = a.tab.tile[a.tab.n];
   if (chunks == 0) return cudaSuccess;
-  auto kernel = delta_grad_kernel<DK, DV>;
+  const int64_t rows = a.tab.cu[a.tab.n];
+  GradMaps maps;
+  if (!delta_map(&maps.k, a.k, rows, a.groups, a.dk, a.ld_k, 64) || !delta_map(&maps.q, a.q, rows, a.groups, a.dk, a.ld_q, 64) ||
+      !delta_map(&maps.v, a.v, rows, a.heads, a.dv, a.ld_v, 64) || !delta_map(&maps.dy, a.dy, rows, a.heads, a.dv, a.ld_dy, 64) ||
+      !delta_map(&maps.dv, a.dv_out, rows, a.heads, a.dv, a.ld_dv, 64))
+    return cudaErrorInvalidValue;
+  auto kernel = delta_grad_kernel<DK>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   if (e != cudaSuccess) return e;
-  kernel<<<dim3(chunks, a.groups), kGradThreads, L::kSmem, st>>>(a, records, ds);
+  const int64_t items = (int64_t)chunks * a.groups;
+  kernel<<<(unsigned)std::min<int64_t>(items, device_sm_count()), kGradThreads, L::kSmem, st>>>(a, maps, records, ds);
   return cudaGetLastError();
 }
 
 template <int DK>
-cudaError_t run_backward(const DeltaBwdArgs& a, const unsigned char* records, bf16* ds, cudaStream_t st) {
+cudaError_t run_backward(const DeltaBwdArgs& a, const unsigned char* records, unsigned char* ds, cudaStream_t st) {
   DeltaMaps maps;
   if (a.tab.cu[a.tab.n] > 0 && !delta_maps(&maps, a, a.dy, a.ld_dy)) return cudaErrorInvalidValue;
   const int64_t chains = (int64_t)a.tab.n * a.heads, sms = device_sm_count();
@@ -653,8 +754,7 @@ cudaError_t run_backward(const DeltaBwdArgs& a, const unsigned char* records, bf
   if (a.dv > 64 && chains >= sms) e = run_back<DK, 8>(a, maps, records, ds, st);
   else if (a.dv > 32 && 2 * chains >= sms) e = run_back<DK, 4>(a, maps, records, ds, st);
   else e = run_back<DK, 2>(a, maps, records, ds, st);
-  if (e != cudaSuccess) return e;
-  return a.dv <= 64 ? run_grad<DK, 64>(a, records, ds, st) : run_grad<DK, 128>(a, records, ds, st);
+  return e == cudaSuccess ? run_grad<DK>(a, records, ds, st) : e;
 }
 
 size_t round256(size_t v) { return (v + 255) / 256 * 256; }
@@ -668,12 +768,13 @@ unsigned int read_delta_back_timeouts() {
 }
 
 size_t delta_backward_workspace(int64_t chunks, int heads, int dv, int dk) {
-  return round256(delta_records(chunks, heads, true)) + round256((size_t)chunks * heads * dv * dk * 2);
+  const size_t states = (size_t)chunks * heads * state_tiles(dv) * (dk <= 64 ? kStateTile<64> : kStateTile<128>);
+  return round256(delta_records(chunks, heads, true)) + round256(states);
 }
 
 cudaError_t launch_delta_backward(const DeltaBwdArgs& a, void* ws, cudaStream_t st) {
   unsigned char* records = static_cast<unsigned char*>(ws);
-  bf16* ds = reinterpret_cast<bf16*>(records + round256(delta_records(a.tab.tile[a.tab.n], a.heads, true)));
+  unsigned char* ds = records + round256(delta_records(a.tab.tile[a.tab.n], a.heads, true));
   const cudaError_t e = launch_delta_records(a, ws, st);
   if (e != cudaSuccess) return e;
   return a.dk <= 64 ? run_backward<64>(a, records, ds, st) : run_backward<128>(a, records, ds, st);
