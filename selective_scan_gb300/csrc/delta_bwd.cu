@@ -235,9 +235,9 @@ __global__ void __launch_bounds__(32 * NW) delta_back_kernel(const __grid_consta
 
 // An item is a chunk and one group of keys, its heads one after another, so that what they add to a query or key is
 // summed in registers in their order; a head in steps of 64 of its v channels, whose tiles are copied while the step
-// before is worked on. A CTA an SM takes every so-manieth item. Warp w: rows 16 (w % 4) of the chunk, columns of quarter w / 4; of the 64 x 64 products the first
-// two quarters have Pr and the others Er, each two of the four blocks of 16 columns.
-constexpr int kGradWarps = 16, kGradThreads = 32 * kGradWarps;
+// before is worked on. A CTA an SM takes every so-manieth item. A warp: 16 rows of the chunk, half of the columns; of
+// the 64 x 64 products the first half has Pr and the other Er.
+constexpr int kGradWarps = 8, kGradThreads = 32 * kGradWarps;
 
 template <int DK>
 struct Grad {
@@ -249,11 +249,11 @@ struct Grad {
   static constexpr int kR = kStep + 2 * kStepBytes, kWide = kR + kTile;  // kWide: S0 in fp32
   // of each head, twice: Inv and the factors
   static constexpr int kHead = kWide + 64 * DK * 4, kFac = kTri, kHeadBytes = kTri + 9 * kC * 4;
-  // floats at kVec: sums of W's rows [4 quarters], columns [2][4 row blocks], its diagonal, a and the write's rows
-  // [4 quarters], the inner product [16 warps]
+  // floats at kVec: sums of W's rows [2 halves], columns [2][4 row blocks], its diagonal, a and the write's rows
+  // [2 halves], the inner product [8 warps]
   static constexpr int kVec = kHead + 2 * kHeadBytes;
-  static constexpr int kRow = 0, kCol = 4 * kC, kDiag = 12 * kC, kA = 13 * kC, kWrite = 17 * kC, kDot = 21 * kC;
-  static constexpr int kBar = kVec + (21 * kC + 16) * 4, kSmem = kBar + 32;  // barriers: the steps' two, S0's; the flag
+  static constexpr int kRow = 0, kCol = 2 * kC, kDiag = 10 * kC, kA = 11 * kC, kWrite = 13 * kC, kDot = 15 * kC;
+  static constexpr int kBar = kVec + (15 * kC + 16) * 4, kSmem = kBar + 32;  // barriers: the steps' two, S0's; the flag
   static_assert(kSmem <= 232448, "shared memory plan exceeds 227 KB");
 };
 struct GradMaps {
@@ -274,15 +274,14 @@ template <int DK>
 __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __grid_constant__ DeltaBwdArgs a, const __grid_constant__ GradMaps maps,
                                                                      const unsigned char* records, const unsigned char* ds) {
   using L = Grad<DK>;
-  constexpr int KS = DK / 16, NK = DK / 32;  // steps over columns; column tiles of 8 of a quarter
+  constexpr int KS = DK / 16, NK = DK / 16;  // steps over columns; column tiles of 8 of a half
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t base = sm32(smem);
   if (not_aligned(base, &g_delta_back_timeouts)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int rb = warp & 3, quarter = warp >> 2, r0 = 16 * rb;
-  const bool second = quarter >= 2;  // of the 64 x 64 products: Er
-  // this warp's two blocks of their columns (the first and last, or those between: about the same number below the diagonal)
-  const int block[2] = {quarter & 1, 3 - (quarter & 1)};
+  // (a scheduler's two warps have rows that add up to the same work in the triangles)
+  const int part = warp >> 2, rb = part ? 3 - (warp & 3) : warp & 3, r0 = 16 * rb;
+  const bool second = part == 1;  // of the 64 x 64 products: Er
   const int per = a.heads / a.groups, halves = state_tiles(a.dv), steps = per * halves;
   const int64_t items = (int64_t)a.tab.tile[a.tab.n] * a.groups;
   float* vec = reinterpret_cast<float*>(smem + L::kVec);
@@ -361,13 +360,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
     }
   };
 
-  float dq[NK][4], dk[NK][4], qk[2][2][4];  // qk: Q K^T (or K K^T) of this warp's two blocks
+  float dq[NK][4], dk[NK][4], qk[4][2][4];  // qk: Q K^T (or K K^T), by blocks of 16 columns
   uint32_t kq0 = 0;  // where the item's K and Q are
-  // the pair of a key or query that this thread's sum (column tile i of its quarter, row g + 8 e) is of
+  // the pair of a key or query that this thread's sum (column tile i of its half, row g + 8 e) is of
   auto pair_at = [&](uint32_t tile, int i, int e) -> uint32_t* {
-    return reinterpret_cast<uint32_t*>(smem + kq0 + tile + wide_at(r0 + g + 8 * e, quarter * NK + i) + 4 * t);
+    return reinterpret_cast<uint32_t*>(smem + kq0 + tile + wide_at(r0 + g + 8 * e, part * NK + i) + 4 * t);
   };
-  float x[2][2][4], at_row[2], write_row[2], dot = 0.0f;  // Pr or Er; rows' parts of a and of the write; <dS1, S0>
+  float x[4][2][4], at_row[2], write_row[2], dot = 0.0f;  // Pr or Er; rows' parts of a and of the write; <dS1, S0>
 
   int64_t item = blockIdx.x;  // (no more CTAs than items)
   Chunk c = chunk_of(a.tab, (int)(item / a.groups));
@@ -389,21 +388,23 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
     const unsigned char* head = smem + L::kHead + ((m * per + hh) & 1) * L::kHeadBytes;
     const uint32_t inv = sm32(head);
     const float* f = reinterpret_cast<const float*>(head + L::kFac);
-    const int strips = min(4, (a.dv - 64 * half + 15) / 16), rows = min(64, a.dv - 64 * half);
+    const int rows = min(64, a.dv - 64 * half);
     bar_wait(bar(n & 1), (uint32_t)((n >> 1) & 1), gave_up);
     bar_wait(bar(2), (uint32_t)(n & 1), gave_up);
     if (half == 0) {
       dot = at_row[0] = at_row[1] = write_row[0] = write_row[1] = 0.0f;
 #pragma unroll
-      for (int o = 0; o < 2; ++o)
+      for (int o = 0; o < 4; ++o)
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
           for (int j = 0; j < 4; ++j) x[o][n][j] = 0.0f;
     }
-    for (int e = threadIdx.x; e < 16 * strips * (DK / 8); e += kGradThreads) {  // S0 as an operand, and its product with dS1
+#pragma unroll 2
+    for (int e = threadIdx.x; e < 64 * (DK / 8); e += kGradThreads) {  // S0 as an operand, and its product with dS1
       const int r = e / (DK / 8), u = e % (DK / 8);
       uint4 w = make_uint4(0, 0, 0, 0);
+      if (r >= rows) *reinterpret_cast<uint4*>(smem + st + L::kDS + wide_at(r, u)) = w;  // (rows that the state has not)
       if (r < rows && 8 * u < a.dk) {
         float v[8], d[8];
         const float* from = reinterpret_cast<const float*>(smem + L::kWide) + r * a.dk + 8 * u;
@@ -421,7 +422,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
     else if (after < items) fetch(next, (int)(after / a.groups), (int)(after % a.groups), 0, n + 1, m + 1);
     if (i == 0) {
 #pragma unroll
-      for (int o = 0; o < 2; ++o)
+      for (int o = 0; o < 4; ++o)
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -431,83 +432,85 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
         uint32_t v[4], b[4];
         load4(v, kq + (second ? L::kK : L::kQ) + wide_cols(r0, 2 * ks, lane));
 #pragma unroll
-        for (int o = 0; o < 2; ++o)
-          if (block[o] <= rb) {
-            load4(b, kq + L::kK + wide_rows(16 * block[o], 2 * ks, lane));
+        for (int o = 0; o < 4; ++o)
+          if (o <= rb) {
+            load4(b, kq + L::kK + wide_rows(16 * o, 2 * ks, lane));
             mma(qk[o][0], v, b[0], b[1]);
             mma(qk[o][1], v, b[2], b[3]);
           }
       }
     }
-    // R = V - up K S0^T, in V's place: a strip of 16 channels a quarter
-    if (quarter < strips) {
-      float y[2][4];
+    // R = V - up K S0^T, in V's place: 32 channels a half
+    {
+      float y[4][4];
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         uint32_t k[4], b[4];
         load4(k, kq + L::kK + wide_cols(r0, 2 * ks, lane));
-        load4(b, base + L::kS0 + wide_rows(16 * quarter, 2 * ks, lane));
-        mma_if(ks == 0, y[0], k, b[0], b[1]);
-        mma_if(ks == 0, y[1], k, b[2], b[3]);
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          load4(b, base + L::kS0 + wide_rows(32 * part + 16 * n, 2 * ks, lane));
+          mma_if(ks == 0, y[2 * n], k, b[0], b[1]);
+          mma_if(ks == 0, y[2 * n + 1], k, b[2], b[3]);
+        }
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const float up = f[kUp + r0 + g + 8 * e];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          uint32_t* p = reinterpret_cast<uint32_t*>(smem + st + L::kV + wide_at(r0 + g + 8 * e, 2 * quarter + n) + 4 * t);
+        for (int n = 0; n < 4; ++n) {
+          uint32_t* p = reinterpret_cast<uint32_t*>(smem + st + L::kV + wide_at(r0 + g + 8 * e, 4 * part + n) + 4 * t);
           *p = pair(fmaf(-up, y[n][2 * e], __uint_as_float(*p << 16)), fmaf(-up, y[n][2 * e + 1], __uint_as_float(*p & 0xffff0000u)));
         }
       }
     }
     __syncthreads();
-    if (quarter < strips) {  // r = Inv R
-      float y[2][4];
+    {  // r = Inv R
+      float y[4][4];
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int jb = 0; jb < 4; ++jb)
+        if (jb <= rb) {
+          uint32_t w[4], b[4];
+          load4(w, inv + block_at(rb, jb) + narrow_cols(0, lane));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) y[n][j] = 0.0f;
-      for (int jb = 0; jb <= rb; ++jb) {
-        uint32_t w[4], b[4];
-        load4(w, inv + block_at(rb, jb) + narrow_cols(0, lane));
-        load4t(b, base + st + L::kV + wide_cols(16 * jb, 2 * quarter, lane));
-        mma(y[0], w, b[0], b[1]);
-        mma(y[1], w, b[2], b[3]);
-      }
+          for (int n = 0; n < 2; ++n) {
+            load4t(b, base + st + L::kV + wide_cols(16 * jb, 4 * part + 2 * n, lane));
+            mma_if(jb == 0, y[2 * n], w, b[0], b[1]);
+            mma_if(jb == 0, y[2 * n + 1], w, b[2], b[3]);
+          }
+        }
 #pragma unroll
       for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-          *reinterpret_cast<uint32_t*>(smem + L::kR + wide_at(r0 + g + 8 * e, 2 * quarter + n) + 4 * t) = pair(y[n][2 * e], y[n][2 * e + 1]);
+        for (int n = 0; n < 4; ++n)
+          *reinterpret_cast<uint32_t*>(smem + L::kR + wide_at(r0 + g + 8 * e, 4 * part + n) + 4 * t) = pair(y[n][2 * e], y[n][2 * e + 1]);
     }
     __syncthreads();
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks)  // Pr or Er
-      if (ks < strips) {
-        uint32_t w[4], b[4];
-        load4(w, base + st + (second ? L::kDV : L::kDO) + wide_cols(r0, 2 * ks, lane));
+    for (int ks = 0; ks < 4; ++ks) {  // Pr or Er
+      uint32_t w[4], b[4];
+      load4(w, base + st + (second ? L::kDV : L::kDO) + wide_cols(r0, 2 * ks, lane));
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
-          if (block[p] <= rb) {
-            load4(b, base + L::kR + wide_rows(16 * block[p], 2 * ks, lane));
-            mma(x[p][0], w, b[0], b[1]);
-            mma(x[p][1], w, b[2], b[3]);
-          }
-      }
+      for (int p = 0; p < 4; ++p)
+        if (p <= rb) {
+          load4(b, base + L::kR + wide_rows(16 * p, 2 * ks, lane));
+          mma(x[p][0], w, b[0], b[1]);
+          mma(x[p][1], w, b[2], b[3]);
+        }
+    }
     // what goes through the states, one product after another (all three at once take more registers than there are)
     auto through = [&](uint32_t left, uint32_t right, float (&y)[NK][4]) {
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks)
-        if (ks < strips) {
-          uint32_t w[4], b[4];
-          load4(w, left + wide_cols(r0, 2 * ks, lane));
+      for (int ks = 0; ks < 4; ++ks) {
+        uint32_t w[4], b[4];
+        load4(w, left + wide_cols(r0, 2 * ks, lane));
 #pragma unroll
-          for (int nb = 0; nb < NK / 2; ++nb) {
-            load4t(b, right + wide_cols(16 * ks, quarter * NK + 2 * nb, lane));
-            mma_if(ks == 0, y[2 * nb], w, b[0], b[1]);
-            mma_if(ks == 0, y[2 * nb + 1], w, b[2], b[3]);
-          }
+        for (int nb = 0; nb < NK / 2; ++nb) {
+          load4t(b, right + wide_cols(16 * ks, part * NK + 2 * nb, lane));
+          mma_if(ks == 0, y[2 * nb], w, b[0], b[1]);
+          mma_if(ks == 0, y[2 * nb + 1], w, b[2], b[3]);
         }
+      }
     };
     // adds w y to a gradient; gives y . (query or key) of the row
     auto add = [&](const float (&y)[NK][4], int e, float w, uint32_t with, float (&to)[NK][4]) {
@@ -546,34 +549,42 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
     if (half == halves - 1) {
       __syncthreads();  // dO and dV have been read
       // F or -E, and W's sums
-      float row[2] = {0.0f, 0.0f};
+      float row[2] = {0.0f, 0.0f}, mine[2], mine_hi[2], mine_lo[2];
 #pragma unroll
-      for (int o = 0; o < 2; ++o)
+      for (int e = 0; e < 2; ++e) {
+        const int at = r0 + g + 8 * e;
+        mine[e] = second ? f[kKn + at] : f[kQn + at] * a.scale;
+        mine_hi[e] = f[kGHi + at];
+        mine_lo[e] = f[kGLo + at];
+      }
+#pragma unroll
+      for (int o = 0; o < 4; ++o)
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          const int to0 = 16 * block[o] + 8 * n + 2 * t;
+          const int to0 = 16 * o + 8 * n + 2 * t;
           float col[2] = {0.0f, 0.0f};
-          if (block[o] <= rb) {
+          if (o <= rb) {
+            auto pairs = [&](int from) { return *reinterpret_cast<const float2*>(f + from + to0); };
+            const float2 hi = pairs(kGHi), lo = pairs(kGLo), kn = pairs(kKn), beta = pairs(kBeta);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int at = r0 + g + 8 * e;
-              const float mine = second ? f[kKn + at] : f[kQn + at] * a.scale;
               float out[2];
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
                 const int to = to0 + j;
-                const bool in = second ? to < at : to <= at;
-                const float d = in ? ex2((f[kGHi + at] - f[kGHi + to]) + (f[kGLo + at] - f[kGLo + to])) * f[kKn + to] * mine : 0.0f;
+                const float b = j ? beta.y : beta.x;
+                const float apart = (mine_hi[e] - (j ? hi.y : hi.x)) + (mine_lo[e] - (j ? lo.y : lo.x));
+                const float d = to <= at ? ex2(apart) * ((j ? kn.y : kn.x) * mine[e]) : 0.0f;
                 const float p = x[o][n][2 * e + j] * d, w = p * qk[o][n][2 * e + j];
-                out[j] = second ? -p * f[kBeta + to] : p * f[kBeta + to];
-                if (to < at) {
-                  row[e] = fmaf(f[kBeta + to], w, row[e]);
-                  col[j] += w;
-                } else if (to == at && !second) {
-                  vec[L::kDiag + at] = w;
-                }
+                const bool diagonal = to == at;
+                out[j] = second ? (diagonal ? 0.0f : -p * b) : p * b;
+                if (!second && diagonal) vec[L::kDiag + at] = w;
+                const float below = diagonal ? 0.0f : w;
+                row[e] = fmaf(b, below, row[e]);
+                col[j] += below;
               }
-              *reinterpret_cast<uint32_t*>(smem + st + (second ? L::kE : L::kF) + wide_at(at, 2 * block[o] + n) + 4 * t) = pair(out[0], out[1]);
+              *reinterpret_cast<uint32_t*>(smem + st + (second ? L::kE : L::kF) + wide_at(at, 2 * o + n) + 4 * t) = pair(out[0], out[1]);
             }
           }
 #pragma unroll
@@ -586,9 +597,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
       for (int e = 0; e < 2; ++e) {
         const float s = sum_quad(row[e]), av = sum_quad(at_row[e]), wr = sum_quad(write_row[e]);
         if (t == 0) {
-          vec[L::kRow + quarter * kC + r0 + g + 8 * e] = s;
-          vec[L::kA + quarter * kC + r0 + g + 8 * e] = av;
-          vec[L::kWrite + quarter * kC + r0 + g + 8 * e] = wr;
+          vec[L::kRow + part * kC + r0 + g + 8 * e] = s;
+          vec[L::kA + part * kC + r0 + g + 8 * e] = av;
+          vec[L::kWrite + part * kC + r0 + g + 8 * e] = wr;
         }
       }
       float d = dot;
@@ -603,7 +614,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
         load4(e, base + st + L::kE + wide_cols(r0, 2 * jb, lane));
 #pragma unroll
         for (int nb = 0; nb < NK / 2; ++nb) {
-          load4t(b, kq + L::kK + wide_cols(16 * jb, quarter * NK + 2 * nb, lane));
+          load4t(b, kq + L::kK + wide_cols(16 * jb, part * NK + 2 * nb, lane));
           mma(dq[2 * nb], w, b[0], b[1]);
           mma(dq[2 * nb + 1], w, b[2], b[3]);
           mma(dk[2 * nb], e, b[0], b[1]);
@@ -616,10 +627,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
         load4t(e, base + st + L::kE + wide_rows(16 * ib, 2 * rb, lane));
 #pragma unroll
         for (int nb = 0; nb < NK / 2; ++nb) {
-          load4t(b, kq + L::kQ + wide_cols(16 * ib, quarter * NK + 2 * nb, lane));
+          load4t(b, kq + L::kQ + wide_cols(16 * ib, part * NK + 2 * nb, lane));
           mma(dk[2 * nb], w, b[0], b[1]);
           mma(dk[2 * nb + 1], w, b[2], b[3]);
-          load4t(b, kq + L::kK + wide_cols(16 * ib, quarter * NK + 2 * nb, lane));
+          load4t(b, kq + L::kK + wide_cols(16 * ib, part * NK + 2 * nb, lane));
           mma(dk[2 * nb], e, b[0], b[1]);
           mma(dk[2 * nb + 1], e, b[2], b[3]);
         }
@@ -632,8 +643,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
         for (int j = 0; j < 2; ++j) {
           const int at = 2 * lane + j;
           auto four = [&](int from) { return (vec[from + at] + vec[from + kC + at]) + (vec[from + 2 * kC + at] + vec[from + 3 * kC + at]); };
-          const float col = four(L::kCol) - four(L::kCol + 4 * kC), av = four(L::kA), wr = four(L::kWrite);
-          const float row_sum = (vec[L::kRow + at] + vec[L::kRow + kC + at]) - (vec[L::kRow + 2 * kC + at] + vec[L::kRow + 3 * kC + at]);
+          const float col = four(L::kCol) - four(L::kCol + 4 * kC), row_sum = vec[L::kRow + at] - vec[L::kRow + kC + at];
+          const float av = vec[L::kA + at] + vec[L::kA + kC + at], wr = vec[L::kWrite + at] + vec[L::kWrite + kC + at];
           db[j] = wr + vec[L::kDiag + at] + col;
           step[j] = f[kBeta + at] * (wr + col) - av - row_sum;
           all += av;
@@ -677,7 +688,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const float d = sum_quad(dots[j]);
-        if (t == 0) vec[(4 * j + quarter) * kC + r0 + g + 8 * e] = d;
+        if (t == 0) vec[(2 * j + part) * kC + r0 + g + 8 * e] = d;
       }
     }
     __syncthreads();
@@ -687,9 +698,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
     const int at = r0 + g + 8 * e;
     float wq = 0.0f, wk = 0.0f;
     if (a.l2_eps >= 0.0f) {
-      auto four = [&](int from) { return (vec[from + at] + vec[from + kC + at]) + (vec[from + 2 * kC + at] + vec[from + 3 * kC + at]); };
-      wq = f[kQn + at] * f[kQn + at] * four(0);
-      wk = f[kKn + at] * f[kKn + at] * four(4 * kC);
+      wq = f[kQn + at] * f[kQn + at] * (vec[at] + vec[kC + at]);
+      wk = f[kKn + at] * f[kKn + at] * (vec[2 * kC + at] + vec[3 * kC + at]);
     }
 #pragma unroll
     for (int n = 0; n < NK; ++n) {
