@@ -40,11 +40,12 @@ __host__ __device__ constexpr int state_tiles(int dv) { return (dv + 63) / 64; }
 
 template <int DK, int NW>
 struct Back : Stages<DK, true, NW, 2> {
-  static constexpr int kOffBar = Stages<DK, true, NW, 2>::kEnd, kSmem = kOffBar + 32;
+  // Inv and P, of one chunk: the next one's come while dS is updated (two of them would leave an SM one CTA)
+  static constexpr int kTriangles = Stages<DK, true, NW, 2>::kEnd, kOffBar = kTriangles + 4 * kTri, kSmem = kOffBar + 32;
 };
 
 template <int DK, int NW>
-__global__ void __launch_bounds__(32 * NW) delta_back_kernel(const __grid_constant__ DeltaBwdArgs a, const __grid_constant__ DeltaMaps maps, const unsigned char* records, unsigned char* ds) {
+__global__ void __launch_bounds__(32 * NW, NW == 8 ? 1 : 2) delta_back_kernel(const __grid_constant__ DeltaBwdArgs a, const __grid_constant__ DeltaMaps maps, const unsigned char* records, unsigned char* ds) {
   using L = Back<DK, NW>;
   constexpr int KS = DK / 16;
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -55,10 +56,12 @@ __global__ void __launch_bounds__(32 * NW) delta_back_kernel(const __grid_consta
   const int dv0 = blockIdx.x * 16 * NW, dv = dv0 + 16 * warp;
   const int first = a.tab.cu[run], len = a.tab.cu[run + 1] - first, n = (len + kC - 1) / kC;
   auto bar = [&](int ch) { return base + L::kOffBar + 8u * (uint32_t)(ch & 1); };
-  volatile uint32_t* gave_up = reinterpret_cast<volatile uint32_t*>(smem + L::kOffBar + 16);
+  const uint32_t tri_bar = base + L::kOffBar + 16, rec = base + L::kTriangles;
+  volatile uint32_t* gave_up = reinterpret_cast<volatile uint32_t*>(smem + L::kOffBar + 24);
   if (threadIdx.x == 0) {
     bar_init(bar(0), 32);
     bar_init(bar(1), 32);
+    bar_init(tri_bar, 1);
     *gave_up = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -88,7 +91,16 @@ __global__ void __launch_bounds__(32 * NW) delta_back_kernel(const __grid_consta
                              records + ((int64_t)(a.tab.tile[run] + ch) * a.heads + h) * record_bytes(true),
                              first + (int64_t)ch * kC, min(kC, len - ch * kC), grp, h, dv0, lane);
   };
-  if (n > 0 && warp == 0) fetch(n - 1);
+  auto fetch_triangles = [&](int ch) {  // (a thread)
+    const unsigned char* from = records + ((int64_t)(a.tab.tile[run] + ch) * a.heads + h) * record_bytes(true);
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(tri_bar), "r"((uint32_t)(4 * kTri)) : "memory");
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(rec), "l"(from), "r"((uint32_t)(4 * kTri)), "r"(tri_bar) : "memory");
+  };
+  if (n > 0 && warp == 0) {
+    fetch(n - 1);
+    if (lane == 0) fetch_triangles(n - 1);
+  }
   for (int ch = n - 1; ch >= 0; --ch) {
     if (ch < n - 1) {
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (dv was written where another chunk's dO comes)
@@ -97,8 +109,8 @@ __global__ void __launch_bounds__(32 * NW) delta_back_kernel(const __grid_consta
     if (ch > 0 && warp == 0) fetch(ch - 1);
     bar_wait(bar(ch), (uint32_t)(((n - 1 - ch) >> 1) & 1), gave_up);
     __syncwarp();
-    const uint32_t at = base + L::k(ch), qt = base + L::q(ch), rec = base + L::rec(ch), dt = base + L::v(ch) + warp * L::kStrip;
-    const float* f = reinterpret_cast<const float*>(smem + (rec - base) + off_factors(true));
+    const uint32_t at = base + L::k(ch), qt = base + L::q(ch), dt = base + L::v(ch) + warp * L::kStrip;
+    const float* f = reinterpret_cast<const float*>(smem + L::rec(ch));
     {  // dS1, for the gradients that take it as an operand (rounded as such), as they hold it in shared memory
       unsigned char* o = ds + ((int64_t)(a.tab.tile[run] + ch) * a.heads + h) * state_tiles(a.dv) * kStateTile<DK> +
                          (dv >> 6) * kStateTile<DK>;
@@ -133,6 +145,8 @@ __global__ void __launch_bounds__(32 * NW) delta_back_kernel(const __grid_consta
 #pragma unroll
       for (int j = 0; j < 4; ++j) x[i][j] *= j & 1 ? w.y : w.x;
     }
+    bar_wait(tri_bar, (uint32_t)((n - 1 - ch) & 1), gave_up);
+    __syncwarp();
 #pragma unroll
     for (int ib = 0; ib < 4; ++ib) {
       uint32_t v[4];
@@ -144,6 +158,10 @@ __global__ void __launch_bounds__(32 * NW) delta_back_kernel(const __grid_consta
         load4t(b, rec + kOffP + block_at(ib, jb) + narrow_cols(0, lane));
         mma(x[2 * jb], d, b[0], b[1]);
         mma(x[2 * jb + 1], d, b[2], b[3]);
+      }
+#pragma unroll
+      for (int jb = 0; jb <= ib; ++jb) {
+        uint32_t b[4];
         load4t(b, rec + kOffPLo + block_at(ib, jb) + narrow_cols(0, lane));
         mma(x[2 * jb], d, b[0], b[1]);
         mma(x[2 * jb + 1], d, b[2], b[3]);
@@ -176,6 +194,10 @@ __global__ void __launch_bounds__(32 * NW) delta_back_kernel(const __grid_consta
         mma(y[2 * jb], uh, bl[0], bl[1]);
         mma(y[2 * jb + 1], uh, bl[2], bl[3]);
       }
+    }
+    if (ch > 0) {
+      __syncthreads();  // every warp is done with the triangles
+      if (threadIdx.x == 0) fetch_triangles(ch - 1);
     }
     // dS0 = gamma dS1 + (upq dO)^T Q - (up dV)^T K
     const float gamma = f[kGamma];

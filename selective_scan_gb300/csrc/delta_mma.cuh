@@ -134,7 +134,9 @@ constexpr int kOffInvLo = kTri, kOffP = 2 * kTri, kOffPLo = 3 * kTri;
 enum Factor : int { kUp = 0, kLeft = kC, kUpQ = 2 * kC, kBeta = 3 * kC, kGamma = 4 * kC, kGHi = 5 * kC, kGLo = 6 * kC,
                     kKn = 7 * kC, kQn = 8 * kC };
 __host__ __device__ constexpr int off_factors(bool backward) { return (backward ? 4 : 3) * kTri; }
-__host__ __device__ constexpr int copied_bytes(bool backward) { return off_factors(backward) + 5 * kC * 4; }  // for the chains
+// What the chains copy with a chunk's tiles: all of it, or (backward) the factors alone.
+__host__ __device__ constexpr int copied_from(bool backward) { return backward ? off_factors(true) : 0; }
+__host__ __device__ constexpr int copied_bytes(bool backward) { return (backward ? 0 : off_factors(false)) + 5 * kC * 4; }
 __host__ __device__ constexpr int record_bytes(bool backward) { return off_factors(backward) + (backward ? 9 : 5) * kC * 4; }
 
 // Which run, and which of its chunks, the batch's chunk is.
@@ -185,7 +187,7 @@ __device__ __forceinline__ void load_stage(int ch, uint32_t base, uint32_t bar, 
 #pragma unroll
       for (int b = 0; b < DK / 64; ++b) tma_3d(tk + b * kC * 128, &maps.k, 64 * b, grp, (int)row0, bar);
       asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                   ::"r"(tr), "l"(rec), "r"((uint32_t)L::kRecBytes), "r"(bar) : "memory");
+                   ::"r"(tr), "l"(rec + copied_from(kBackward)), "r"((uint32_t)L::kRecBytes), "r"(bar) : "memory");
 #pragma unroll
       for (int b = 0; b < DK / 64; ++b) tma_3d(tq + b * kC * 128, &maps.q, 64 * b, grp, (int)row0, bar);
 #pragma unroll
@@ -209,7 +211,7 @@ __device__ __forceinline__ void load_stage(int ch, uint32_t base, uint32_t bar, 
     copy16(tq + wide_at(r, u), q + row * a.ld_q + col, in);
   }
 #pragma unroll 4
-  for (int e = lane; e < L::kRecBytes / 16; e += 32) copy16(tr + 16 * e, rec + 16 * e, true);
+  for (int e = lane; e < L::kRecBytes / 16; e += 32) copy16(tr + 16 * e, rec + copied_from(kBackward) + 16 * e, true);
 #pragma unroll 4
   for (int e = lane; e < kC * 2 * kStrips; e += 32) {
     const int r = e / (2 * kStrips), u = e % (2 * kStrips);
