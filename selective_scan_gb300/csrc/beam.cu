@@ -17,14 +17,18 @@ namespace {
 // needed to choose among them. The second joins a row's parts, forms the values in fp64 and ranks a sequence's
 // candidates by counting how many come before each.
 //
-// In a part, the `out`-th largest of a warp's 32 lane maxima has `out` logits at or above it, so the largest such of the
-// eight warps is a bound below which nothing counts: the few logits that reach it are collected and ranked by counting.
-// Where more reach it than are held (many ties), the warps take them one by one instead.
+// In a part, the threads fall into 8, 16 or 32 groups (at least `out` of them) by their lane, and the least of the
+// groups' maxima has `out` logits at or above it: a bound below which nothing counts. The few logits that reach it (22,
+// 54 or 130 of a part in random order) are collected and ranked by counting. Where more reach it than are held (many
+// ties), the warps take them one by one instead.
 constexpr int kScanThreads = 256, kScanWarps = kScanThreads / 32;
 constexpr int kMost = MAMBA2_MAX_BEAMS;  // candidates of a list: one to a lane
 constexpr int kHeld = 1024;              // logits that are collected
-// Vectors of a thread: eight where that leaves every SM four CTAs, else two, so that few rows spread over the SMs.
-constexpr int kMany = 8, kFew = 2;
+// 16-byte vectors of a thread. Half as many doubles the parts that a row's lists are joined from, and is no faster even
+// where the parts are fewer than the SMs (scan and join, us, of 8, 4 and 2 vectors: 4 rows of 131 072 fp32 logits
+// 3.6 + 6.8, 3.5 + 10.1, 3.6 + 14.5; 80 of 32 001 5.2 + 6.7, 6.1 + 7.8, 8.3 + 13.6; 512 of 131 072 bf16 41 + 13, 62 + 16,
+// 87 + 18).
+constexpr int kVectors = 8;
 
 __device__ __forceinline__ float ex2(float v) {
   float e;
@@ -32,6 +36,23 @@ __device__ __forceinline__ float ex2(float v) {
   return e;
 }
 constexpr float kLog2e = 1.4426950408889634f;
+
+struct Two {  // of packed instructions
+  unsigned long long v;
+  __device__ __forceinline__ Two(float x, float y) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y)); }
+  __device__ __forceinline__ float2 get() const {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+  }
+};
+// sum += exp2(x scale + off)
+__device__ __forceinline__ void add_exp(Two& sum, Two x, Two scale, Two off) {
+  asm volatile("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(x.v) : "l"(scale.v), "l"(off.v));
+  const float2 f = x.get();
+  const Two e(ex2(f.x), ex2(f.y));
+  asm volatile("add.rn.f32x2 %0, %0, %1;" : "+l"(sum.v) : "l"(e.v));
+}
 
 // The largest logits that a warp has met, a lane each, descending, equal ones by index: lane r holds the r-th. What it
 // is offered comes with ascending indices, so an equal one always goes behind. -infinity is never taken.
@@ -70,7 +91,7 @@ __device__ __forceinline__ PartOut part_at(void* ws, int64_t i, int out) {
   return {p, p + 1, p + 2, reinterpret_cast<int*>(p + 2 + out)};
 }
 template <typename T>
-constexpr int part_logits(int vectors) { return kScanThreads * vectors * Vec16<T>::n; }
+constexpr int kPartLogits = kScanThreads * kVectors * Vec16<T>::n;
 
 // An order-preserving image of a float (-0 as 0), and with it a logit and its index as one number: larger is better.
 __device__ __forceinline__ uint32_t ordered(float v) {
@@ -144,13 +165,13 @@ template <> struct Logits<__nv_bfloat16> {
   __device__ static __forceinline__ int element(int half, int bit) { return 2 * (16 * half + (bit & 15)) + (bit >> 4); }
 };
 
-// kVectors: 16-byte vectors of a thread. The part's last vector may pass the row's end, and the row's first logits up to
-// a 16-byte boundary (`head`) are part 0's besides.
-template <typename T, int kVectors>
-__global__ void __launch_bounds__(kScanThreads, kVectors == kMany ? 4 : 6) beam_scan_kernel(const __grid_constant__ BeamArgs a) {
+// The part's last vector may pass the row's end, and the row's first logits up to a 16-byte boundary (`head`) are part
+// 0's besides.
+template <typename T>
+__global__ void __launch_bounds__(kScanThreads, 4) beam_scan_kernel(const __grid_constant__ BeamArgs a) {
   constexpr int V = Logits<T>::n;
   __shared__ __align__(16) uint64_t key[kHeld + 2];
-  __shared__ float wm[kScanWarps], wsum[kScanWarps], wleast[kScanWarps];
+  __shared__ float tops[kScanWarps][32], wsum[kScanWarps];
   __shared__ int held;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -160,13 +181,19 @@ __global__ void __launch_bounds__(kScanThreads, kVectors == kMany ? 4 : 6) beam_
   const T* p = static_cast<const T*>(a.logits) + row * a.ld;
   const int head = min(a.vocab, (int)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / (int)sizeof(T));
   const int rest = a.vocab - head;
-  const int64_t lo = (int64_t)blockIdx.x * part_logits<T>(kVectors);
+  const int64_t lo = (int64_t)blockIdx.x * kPartLogits<T>;
   auto first = [&](int u) { return lo + ((int64_t)u * kScanThreads + threadIdx.x) * V; };  // behind the head
   Logits<T> x[kVectors];
+  auto load = [&](Logits<T>& to, int u) {
+    if (first(u) + V <= rest) to.load(p + head + first(u));
+    else to.load_some(p + head + first(u), rest - first(u));
+  };
+  if (lo + kPartLogits<T> <= rest) {
 #pragma unroll
-  for (int u = 0; u < kVectors; ++u) {
-    if (first(u) + V <= rest) x[u].load(p + head + first(u));
-    else x[u].load_some(p + head + first(u), rest - first(u));
+    for (int u = 0; u < kVectors; ++u) x[u].load(p + head + first(u));
+  } else {
+#pragma unroll
+    for (int u = 0; u < kVectors; ++u) load(x[u], u);
   }
   // a logit of the head (warp 0's lanes)
   const float extra = blockIdx.x == 0 && (int)threadIdx.x < head ? Act<T>::to_f(p[threadIdx.x]) : -INFINITY;
@@ -174,23 +201,16 @@ __global__ void __launch_bounds__(kScanThreads, kVectors == kMany ? 4 : 6) beam_
 #pragma unroll
   for (int u = 0; u < kVectors; ++u) top = fmaxf(top, x[u].top());
   if (!(top > -INFINITY)) top = -INFINITY;  // (nothing but NaNs)
-  {  // the warp's maximum and its `out`-th lane maximum
-    uint32_t k = ordered(top), most = 0;
-    for (int r = 0; r < a.out; ++r) {
-      most = __reduce_max_sync(0xffffffffu, k);
-      if (r == 0 && lane == 0) wm[warp] = unordered(most);
-      if (lane == __ffs(__ballot_sync(0xffffffffu, k == most)) - 1) k = 0;
-    }
-    if (lane == 0) wleast[warp] = unordered(most);
-    if (threadIdx.x == 0) held = 0;
-  }
+  tops[warp][lane] = top;
+  if (threadIdx.x == 0) held = 0;
   __syncthreads();
-  float m = wm[0], least = wleast[0];
+  float group = tops[0][lane];
 #pragma unroll
-  for (int w = 1; w < kScanWarps; ++w) {
-    m = fmaxf(m, wm[w]);
-    least = fmaxf(least, wleast[w]);
-  }
+  for (int w = 1; w < kScanWarps; ++w) group = fmaxf(group, tops[w][lane]);
+  if (a.out <= 16) group = fmaxf(group, __shfl_xor_sync(0xffffffffu, group, 16));
+  if (a.out <= 8) group = fmaxf(group, __shfl_xor_sync(0xffffffffu, group, 8));
+  const float m = unordered(__reduce_max_sync(0xffffffffu, ordered(group)));
+  float least = unordered(__reduce_min_sync(0xffffffffu, ordered(group)));
   auto collect = [&](float v, int index) {
     const int to = atomicAdd(&held, 1);
     if (to < kHeld) key[to] = key_of(v, index);
@@ -210,12 +230,12 @@ __global__ void __launch_bounds__(kScanThreads, kVectors == kMany ? 4 : 6) beam_
       }
   }
   const float base = m == -INFINITY ? 0.0f : m, off = -base * kLog2e;
-  float sum = ex2(fmaf(extra, kLog2e, off)), part[2] = {0.0f, 0.0f};
+  Two part(ex2(fmaf(extra, kLog2e, off)), 0.0f);
 #pragma unroll
   for (int u = 0; u < kVectors; ++u)
 #pragma unroll
-    for (int j = 0; j < V; ++j) part[j & 1] += ex2(fmaf(x[u].at(j), kLog2e, off));
-  sum += part[0] + part[1];
+    for (int j = 0; j < V; j += 2) add_exp(part, {x[u].at(j), x[u].at(j + 1)}, {kLog2e, kLog2e}, {off, off});
+  float sum = part.get().x + part.get().y;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) wsum[warp] = sum;
@@ -230,17 +250,20 @@ __global__ void __launch_bounds__(kScanThreads, kVectors == kMany ? 4 : 6) beam_
       const float c = __shfl_sync(0xffffffffu, extra, from);
       if (c > best.least) best.add(c, from, a.out, lane);
     }
-#pragma unroll
-    for (int u = 0; u < kVectors; ++u)
-      for (uint32_t todo = __ballot_sync(0xffffffffu, x[u].top() > best.least); todo; todo &= todo - 1) {
+#pragma unroll 1
+    for (int u = 0; u < kVectors; ++u) {  // (read again, so that they need not be held until here)
+      Logits<T> again;
+      load(again, u);
+      for (uint32_t todo = __ballot_sync(0xffffffffu, again.top() > best.least); todo; todo &= todo - 1) {
         const int from = __ffs(todo) - 1;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          const float c = __shfl_sync(0xffffffffu, x[u].at(j), from);
+          const float c = __shfl_sync(0xffffffffu, again.at(j), from);
           if (c > best.least)
             best.add(c, (int)(head + lo + ((int64_t)u * kScanThreads + warp * 32 + from) * V + j), a.out, lane);
         }
       }
+    }
     __syncthreads();  // everyone has read `held`
     if (threadIdx.x == 0) held = 0;
     __syncthreads();
@@ -410,12 +433,9 @@ __global__ void __launch_bounds__(32 * kMost) beam_rank_kernel(const __grid_cons
   }
 }
 
-int beam_vectors(int64_t rows, int vocab) {
-  return rows * (vocab / (kScanThreads * 8 * 8)) >= 4 * (int64_t)device_sm_count() ? kMany : kFew;
-}
-// Parts of a row; for the workspace those of fp32 logits, which are the more.
-int beam_parts(int64_t rows, int vocab, mamba2_dtype act) {
-  const int64_t part = act == MAMBA2_F32 ? part_logits<float>(beam_vectors(rows, vocab)) : part_logits<__nv_bfloat16>(beam_vectors(rows, vocab));
+// Parts of a row.
+int beam_parts(int vocab, mamba2_dtype act) {
+  const int64_t part = act == MAMBA2_F32 ? kPartLogits<float> : kPartLogits<__nv_bfloat16>;
   return (int)((vocab + part - 1) / part);
 }
 
@@ -513,21 +533,17 @@ cudaError_t start(const void* kernel, dim3 grid, int threads, size_t smem, void*
 
 }  // namespace
 
+// (of fp32 logits, whose parts are the more)
 size_t beam_workspace(int64_t rows, int32_t out, int32_t vocab) {
-  return (size_t)rows * beam_parts(rows, vocab, MAMBA2_F32) * part_words(out) * 4;
+  return (size_t)rows * beam_parts(vocab, MAMBA2_F32) * part_words(out) * 4;
 }
 
 cudaError_t launch_beam_select(const BeamArgs& args, mamba2_dtype act, cudaStream_t st) {
   BeamArgs a = args;
   const int64_t rows = (int64_t)a.batch * a.beams;
-  int parts = beam_parts(rows, a.vocab, act);
-  const bool many = beam_vectors(rows, a.vocab) == kMany;
-  const void* scan;
-  if (act == MAMBA2_BF16)
-    scan = many ? reinterpret_cast<const void*>(beam_scan_kernel<__nv_bfloat16, kMany>)
-                : reinterpret_cast<const void*>(beam_scan_kernel<__nv_bfloat16, kFew>);
-  else
-    scan = many ? reinterpret_cast<const void*>(beam_scan_kernel<float, kMany>) : reinterpret_cast<const void*>(beam_scan_kernel<float, kFew>);
+  int parts = beam_parts(a.vocab, act);
+  const void* scan = act == MAMBA2_BF16 ? reinterpret_cast<const void*>(beam_scan_kernel<__nv_bfloat16>)
+                                        : reinterpret_cast<const void*>(beam_scan_kernel<float>);
   void* first[] = {&a};
   cudaError_t e = start(scan, dim3((unsigned)parts, (unsigned)rows), kScanThreads, 0, first, st);
   if (e != cudaSuccess) return e;

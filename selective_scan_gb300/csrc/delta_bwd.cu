@@ -45,7 +45,7 @@ struct Back : Stages<DK, true, NW, 2> {
 };
 
 template <int DK, int NW>
-__global__ void __launch_bounds__(32 * NW, NW == 8 ? 1 : 2) delta_back_kernel(const __grid_constant__ DeltaBwdArgs a, const __grid_constant__ DeltaMaps maps, const unsigned char* records, unsigned char* ds) {
+__global__ void __launch_bounds__(32 * NW, 2) delta_back_kernel(const __grid_constant__ DeltaBwdArgs a, const __grid_constant__ DeltaMaps maps, const unsigned char* records, unsigned char* ds) {
   using L = Back<DK, NW>;
   constexpr int KS = DK / 16;
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -781,11 +781,12 @@ template <int DK>
 cudaError_t run_backward(const DeltaBwdArgs& a, const unsigned char* records, unsigned char* ds, cudaStream_t st) {
   DeltaMaps maps;
   if (a.tab.cu[a.tab.n] > 0 && !delta_maps(&maps, a, a.dy, a.ld_dy)) return cudaErrorInvalidValue;
-  const int64_t chains = (int64_t)a.tab.n * a.heads, sms = device_sm_count();
-  cudaError_t e;
-  if (a.dv > 64 && chains >= sms) e = run_back<DK, 8>(a, maps, records, ds, st);
-  else if (a.dv > 32 && 2 * chains >= sms) e = run_back<DK, 4>(a, maps, records, ds, st);
-  else e = run_back<DK, 2>(a, maps, records, ds, st);
+  // Four warps share a chunk's tiles where that leaves most SMs a CTA; eight never were faster (us of 8, 4 and 2 warps,
+  // 8 192 tokens, 16 heads of 128 x 128: 8 runs 169, 122, 127; 16 runs 110, 109, 116; 32 runs 119, 105, 126; of 4 runs
+  // 159 and 156 of 4 and 2 warps, of 2 runs 312 and 304).
+  const int64_t blocks = (int64_t)a.tab.n * a.heads * ((a.dv + 15) / 16);  // of 16 rows
+  const cudaError_t e = blocks >= 4 * device_sm_count() ? run_back<DK, 4>(a, maps, records, ds, st)
+                                                        : run_back<DK, 2>(a, maps, records, ds, st);
   return e == cudaSuccess ? run_grad<DK>(a, records, ds, st) : e;
 }
 
