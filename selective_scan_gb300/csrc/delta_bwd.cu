@@ -759,14 +759,15 @@ cudaError_t run_back(const DeltaBwdArgs& a, const DeltaMaps& maps, const unsigne
 }
 
 template <int DK>
-cudaError_t run_grad(const DeltaBwdArgs& a, const unsigned char* records, const unsigned char* ds, cudaStream_t st) {
+cudaError_t run_grad(const DeltaBwdArgs& a, const DeltaMaps& both, const unsigned char* records, const unsigned char* ds, cudaStream_t st) {
   using L = Grad<DK>;
   const int chunks = a.tab.tile[a.tab.n];
   if (chunks == 0) return cudaSuccess;
   const int64_t rows = a.tab.cu[a.tab.n];
   GradMaps maps;
-  if (!delta_map(&maps.k, a.k, rows, a.groups, a.dk, a.ld_k, 64) || !delta_map(&maps.q, a.q, rows, a.groups, a.dk, a.ld_q, 64) ||
-      !delta_map(&maps.v, a.v, rows, a.heads, a.dv, a.ld_v, 64) || !delta_map(&maps.dy, a.dy, rows, a.heads, a.dv, a.ld_dy, 64) ||
+  maps.k = both.k;
+  maps.q = both.q;
+  if (!delta_map(&maps.v, a.v, rows, a.heads, a.dv, a.ld_v, 64) || !delta_map(&maps.dy, a.dy, rows, a.heads, a.dv, a.ld_dy, 64) ||
       !delta_map(&maps.dv, a.dv_out, rows, a.heads, a.dv, a.ld_dv, 64))
     return cudaErrorInvalidValue;
   auto kernel = delta_grad_kernel<DK>;
@@ -778,16 +779,14 @@ cudaError_t run_grad(const DeltaBwdArgs& a, const unsigned char* records, const 
 }
 
 template <int DK>
-cudaError_t run_backward(const DeltaBwdArgs& a, const unsigned char* records, unsigned char* ds, cudaStream_t st) {
-  DeltaMaps maps;
-  if (a.tab.cu[a.tab.n] > 0 && !delta_maps(&maps, a, a.dy, a.ld_dy)) return cudaErrorInvalidValue;
+cudaError_t run_backward(const DeltaBwdArgs& a, const DeltaMaps& maps, const unsigned char* records, unsigned char* ds, cudaStream_t st) {
   // Four warps share a chunk's tiles where that leaves most SMs a CTA; eight never were faster (us of 8, 4 and 2 warps,
   // 8 192 tokens, 16 heads of 128 x 128: 8 runs 169, 122, 127; 16 runs 110, 109, 116; 32 runs 119, 105, 126; of 4 runs
   // 159 and 156 of 4 and 2 warps, of 2 runs 312 and 304).
   const int64_t blocks = (int64_t)a.tab.n * a.heads * ((a.dv + 15) / 16);  // of 16 rows
   const cudaError_t e = blocks >= 4 * device_sm_count() ? run_back<DK, 4>(a, maps, records, ds, st)
                                                         : run_back<DK, 2>(a, maps, records, ds, st);
-  return e == cudaSuccess ? run_grad<DK>(a, records, ds, st) : e;
+  return e == cudaSuccess ? run_grad<DK>(a, maps, records, ds, st) : e;
 }
 
 size_t round256(size_t v) { return (v + 255) / 256 * 256; }
@@ -808,9 +807,11 @@ size_t delta_backward_workspace(int64_t chunks, int heads, int dv, int dk) {
 cudaError_t launch_delta_backward(const DeltaBwdArgs& a, void* ws, cudaStream_t st) {
   unsigned char* records = static_cast<unsigned char*>(ws);
   unsigned char* ds = records + round256(delta_records(a.tab.tile[a.tab.n], a.heads, true));
-  const cudaError_t e = launch_delta_records(a, ws, st);
+  DeltaMaps maps;
+  if (a.tab.cu[a.tab.n] > 0 && !delta_maps(&maps, a, a.dy, a.ld_dy)) return cudaErrorInvalidValue;
+  const cudaError_t e = launch_delta_records(a, maps, ws, st);
   if (e != cudaSuccess) return e;
-  return a.dk <= 64 ? run_backward<64>(a, records, ds, st) : run_backward<128>(a, records, ds, st);
+  return a.dk <= 64 ? run_backward<64>(a, maps, records, ds, st) : run_backward<128>(a, maps, records, ds, st);
 }
 
 }  // namespace mamba2

@@ -42,7 +42,8 @@ struct PrepSmem {
   static constexpr int kInv = kC * kLdA * 4, kTiles = 2 * kInv;
   static_assert(kTiles >= 2 * kC * 128 * 2, "K and Q");
   static constexpr int kScores = kTiles;  // the rest of the record: P and the factors
-  static constexpr int kToken = kScores + record_bytes(kBackward) - kOffP, kQn = kToken + kC * 16, kBytes = kQn + kC * 4;
+  static constexpr int kToken = kScores + record_bytes(kBackward) - kOffP, kQn = kToken + kC * 16, kBar = kQn + kC * 4;
+  static constexpr int kBytes = kBar + 16;  // the tiles' barrier and the flag
 };
 
 // G_i (in units of log 2) as a sum of two floats.
@@ -61,9 +62,11 @@ __device__ __forceinline__ void scan_decays(float g, float& hi, float& lo, int l
 }
 
 template <int DK, bool kBackward>
-__global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(const __grid_constant__ DeltaArgs a, unsigned char* records) {
+__global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ DeltaMaps maps, unsigned char* records) {
   using L = PrepSmem<kBackward>;
-  extern __shared__ __align__(128) unsigned char smem[];
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const uint32_t sk = sm32(smem), sq = sk + kC * DK * 2, bar = sk + L::kBar;
+  if (not_aligned(sk, &g_delta_timeouts)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int h = blockIdx.y, grp = h / (a.heads / a.groups);
   // The last 16 rows have four times the first's work, so which warp has which goes round: the warps of a scheduler
@@ -72,8 +75,20 @@ __global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(const __gri
   const Chunk c = chunk_of(a.tab, blockIdx.x);
   float4* token = reinterpret_cast<float4*>(smem + L::kToken);  // G in two parts, kappa, beta
   float* qn = reinterpret_cast<float*>(smem + L::kQn);
-  const uint32_t sk = sm32(smem), sq = sk + kC * DK * 2;
-  {
+  volatile uint32_t* gave_up = reinterpret_cast<volatile uint32_t*>(smem + L::kBar + 8);
+  if (c.len == kC) {
+    if (threadIdx.x == 0) {
+      bar_init(bar, 1);
+      *gave_up = 0u;
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+      asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(2u * kC * DK * 2) : "memory");
+#pragma unroll
+      for (int b = 0; b < DK / 64; ++b) {
+        tma_3d(sk + b * kC * 128, &maps.k, 64 * b, grp, c.row, bar);
+        tma_3d(sq + b * kC * 128, &maps.q, 64 * b, grp, c.row, bar);
+      }
+    }
+  } else {  // the rows behind the run's last, which may be another run's, are zeros
     const bf16* k = static_cast<const bf16*>(a.k) + (int64_t)grp * a.dk;
     const bf16* q = static_cast<const bf16*>(a.q) + (int64_t)grp * a.dk;
     constexpr int units = DK / 8;
@@ -88,8 +103,8 @@ __global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(const __gri
     }
     copies_end();
   }
-  if (warp == 0) {
-    float hi[2], lo[2], last[2] = {0.0f, 0.0f}, gv[2], bv[2];
+  float gv[2] = {}, bv[2] = {};
+  if (rb == 0) {
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int i = 32 * half + lane;
@@ -97,6 +112,11 @@ __global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(const __gri
       gv[half] = i < c.len && a.g ? a.g[at] : 0.0f;
       bv[half] = i < c.len ? (a.beta ? a.beta[at] : 1.0f) : 0.0f;
     }
+  }
+  copies_done();
+  __syncthreads();
+  if (rb == 0) {  // the warp with the least of the products sums the decays
+    float hi[2], lo[2], last[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       if (gv[half] < -10000.0f) gv[half] = -10000.0f;  // (a NaN stays one)
@@ -110,29 +130,13 @@ __global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(const __gri
       last[1] = __shfl_sync(0xffffffffu, s.lo, 31);
     }
   }
-  copies_done();
-  __syncthreads();
-  {  // reciprocal lengths: a thread a row
-    const int r = threadIdx.x & (kC - 1);
-    const bool is_q = threadIdx.x >= kC;
-    float n = 1.0f;
-    if (a.l2_eps >= 0.0f) {
-      float s[2] = {0.0f, 0.0f};
-#pragma unroll
-      for (int u = 0; u < DK / 8; ++u) {
-        float v[8];
-        Vec16<bf16>::unpack(*reinterpret_cast<const uint4*>(smem + (is_q ? kC * DK * 2 : 0) + wide_at(r, u)), v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[j & 1] = fmaf(v[j], v[j], s[j & 1]);
-      }
-      n = rsqrtf(s[0] + s[1] + a.l2_eps);
-    }
-    if (r >= c.len) n = 0.0f;
-    if (is_q) qn[r] = n;
-    else token[r].z = n;
+  if (c.len == kC) {
+    bar_wait(bar, 0, gave_up);
+    __syncwarp();
   }
-  // K K^T and Q K^T below and on the diagonal blocks: a warp 16 rows
-  float kk[8][4], qk[8][4];
+  // K K^T and Q K^T below and on the diagonal blocks, a warp 16 rows; and of Q Q^T what has the queries' lengths
+  float kk[8][4], qk[8][4], qq[2][4] = {};
+  const bool l2 = a.l2_eps >= 0.0f;
 #pragma unroll
   for (int n = 0; n < 8; ++n)
 #pragma unroll
@@ -151,6 +155,24 @@ __global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(const __gri
         mma(qk[2 * nb], aq, b[0], b[1]);
         mma(qk[2 * nb + 1], aq, b[2], b[3]);
       }
+    if (l2) {
+      load4(b, sq + wide_rows(r0, 2 * ks, lane));
+      mma(qq[0], aq, b[0], b[1]);
+      mma(qq[1], aq, b[2], b[3]);
+    }
+  }
+  if (t == g >> 1) {  // reciprocal lengths, from the diagonals
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      float k2 = 0.0f;
+#pragma unroll
+      for (int nb = 0; nb < 4; ++nb)
+        if (nb == rb) k2 = g & 1 ? kk[2 * nb + half][2 * half + 1] : kk[2 * nb + half][2 * half];
+      const float q2 = g & 1 ? qq[half][2 * half + 1] : qq[half][2 * half];
+      const int r = r0 + g + 8 * half;
+      token[r].z = r >= c.len ? 0.0f : l2 ? rsqrtf(k2 + a.l2_eps) : 1.0f;
+      qn[r] = r >= c.len ? 0.0f : l2 ? rsqrtf(q2 + a.l2_eps) : 1.0f;
+    }
   }
   __syncthreads();  // lengths are there; K and Q have been read
   float* A = reinterpret_cast<float*>(smem);
@@ -313,6 +335,7 @@ __global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(const __gri
     out(rec, sk, kOffP);
     out(rec + kOffP, sk + L::kScores, record_bytes(kBackward) - kOffP);
     asm volatile("cp.async.bulk.commit_group;\ncp.async.bulk.wait_group 0;" ::: "memory");
+    if (c.len == kC && *gave_up) atomicAdd(&g_delta_timeouts, 1u);
   }
 }
 
@@ -827,22 +850,22 @@ cudaError_t run_chain(const DeltaArgs& a, const DeltaMaps& maps, const unsigned 
 }
 
 template <int DK, bool kBackward>
-cudaError_t run_prep(const DeltaArgs& a, unsigned char* records, cudaStream_t st) {
+cudaError_t run_prep(const DeltaArgs& a, const DeltaMaps& maps, unsigned char* records, cudaStream_t st) {
   const int chunks = a.tab.tile[a.tab.n];
   if (chunks == 0) return cudaSuccess;
   auto kernel = delta_prep_kernel<DK, kBackward>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PrepSmem<kBackward>::kBytes);
   if (e != cudaSuccess) return e;
-  kernel<<<dim3(chunks, a.heads), kPrepThreads, PrepSmem<kBackward>::kBytes, st>>>(a, records);
+  kernel<<<dim3(chunks, a.heads), kPrepThreads, PrepSmem<kBackward>::kBytes, st>>>(a, maps, records);
   return cudaGetLastError();
 }
 
 template <int DK>
 cudaError_t run_forward(const DeltaArgs& a, unsigned char* records, cudaStream_t st) {
-  const cudaError_t e = run_prep<DK, false>(a, records, st);
-  if (e != cudaSuccess) return e;
   DeltaMaps maps;
   if (a.tab.cu[a.tab.n] > 0 && !delta_maps(&maps, a, a.v, a.ld_v)) return cudaErrorInvalidValue;
+  const cudaError_t e = run_prep<DK, false>(a, maps, records, st);
+  if (e != cudaSuccess) return e;
   const int64_t blocks = (int64_t)a.tab.n * a.heads * ((a.dv + 15) / 16), sms = device_sm_count();  // of 16 rows
   if (blocks <= sms) return run_pairs<DK, 1>(a, maps, records, st);
   if (blocks <= 2 * sms) return run_pairs<DK, 2>(a, maps, records, st);
@@ -862,9 +885,9 @@ bool delta_chunked_supported(mamba2_dtype act, int dv, int dk) { return act == M
 
 size_t delta_records(int64_t chunks, int heads, bool backward) { return (size_t)chunks * heads * record_bytes(backward); }
 
-cudaError_t launch_delta_records(const DeltaArgs& a, void* ws, cudaStream_t st) {
+cudaError_t launch_delta_records(const DeltaArgs& a, const DeltaMaps& maps, void* ws, cudaStream_t st) {
   unsigned char* records = static_cast<unsigned char*>(ws);
-  return a.dk <= 64 ? run_prep<64, true>(a, records, st) : run_prep<128, true>(a, records, st);
+  return a.dk <= 64 ? run_prep<64, true>(a, maps, records, st) : run_prep<128, true>(a, maps, records, st);
 }
 
 cudaError_t launch_delta_chunked(const DeltaArgs& a, void* ws, cudaStream_t st) {

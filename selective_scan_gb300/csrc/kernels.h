@@ -273,6 +273,7 @@ struct DeltaTensors {
   int64_t ld_y, ld_q, ld_k, ld_v;
   float scale, l2_eps;
 };
+struct DeltaMaps;  // delta_tiles.h
 struct DeltaArgs : DeltaTensors {
   SeqTable tab;
   uint16_t order[MAMBA2_MAX_SEQS];  // the runs, longest first: a chain that starts late is a short one
@@ -283,7 +284,7 @@ bool delta_chunked_supported(mamba2_dtype act, int dv, int dk);
 unsigned int read_delta_timeouts();
 size_t delta_records(int64_t chunks, int heads, bool backward);
 cudaError_t launch_delta_chunked(const DeltaArgs& a, void* ws, cudaStream_t st);
-cudaError_t launch_delta_records(const DeltaArgs& a, void* ws, cudaStream_t st);  // the backward's
+cudaError_t launch_delta_records(const DeltaArgs& a, const DeltaMaps& maps, void* ws, cudaStream_t st);  // the backward's
 
 struct DeltaBwdArgs : DeltaArgs {  // (y and state unused, ckpt read; tab's slots unused)
   void* dq;
