@@ -61,7 +61,8 @@ mamba2_status mamba2_beam_select(float* scores_out, int32_t* parents, int32_t* t
  *   pool[slots[b][j]] = pool[slots[b][parents[b][j]]]   (as it was before)
  *
  *   pools      host array of num_pools device pointers, each a pool of
- *              num_slots slots of slot_bytes[i] bytes; no two overlap
+ *              num_slots slots of slot_bytes[i] bytes; two that overlap are
+ *              refused
  *   slots      [batch, beams] int32, all different
  *   parents    [batch, beams] int32 in [0, beams)
  *   status_dev int32: receives the mamba2_status of what is checked on the

@@ -16,6 +16,9 @@
  * 0 <= beta |k|^2 <= 2 (not checked). A g below -10000 is taken as -10000: the
  * state is forgotten, as exp(-104) already leaves nothing of it in fp32.
  *
+ * Runs do not touch one another, but a value that is not finite may reach the
+ * outputs of its run from the beginning of its MAMBA2_DELTA_CHUNK tokens on.
+ *
  *   q, k   [rows, ngroups, d_state] act, row strides ld_q, ld_k
  *   v, y   [rows, heads, headdim] act, row strides ld_v, ld_y
  *   g      [rows, heads] f32 or NULL (0: nothing decays)

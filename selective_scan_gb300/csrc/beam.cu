@@ -302,6 +302,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) beam_scan_kernel(const __grid
 // A warp a beam, a CTA a sequence. kNear entries of a part's list are held in shared memory; it is rare that more of one
 // are among the largest of the row.
 constexpr int kNear = 8;
+constexpr int kRankSmem = 31 * kNear * (int)sizeof(uint64_t);  // of a beam
 
 __global__ void __launch_bounds__(32 * kMost) beam_rank_kernel(const __grid_constant__ BeamArgs a, int parts) {
   extern __shared__ __align__(16) uint64_t near_keys[];  // [beams][31][kNear]
@@ -514,8 +515,8 @@ __global__ void __launch_bounds__(MAMBA2_MAX_SEQS) reorder_check_kernel(const __
 }
 
 cudaError_t start(const void* kernel, dim3 grid, int threads, size_t smem, void** args, cudaStream_t st) {
-  if (smem > 36 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (smem > 30 * 1024) {  // (one value for every call: another thread's may be between this and its launch)
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRankSmem * kMost);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
@@ -549,7 +550,7 @@ cudaError_t launch_beam_select(const BeamArgs& args, mamba2_dtype act, cudaStrea
   if (e != cudaSuccess) return e;
   void* second[] = {&a, &parts};
   return start(reinterpret_cast<const void*>(beam_rank_kernel), dim3((unsigned)a.batch), 32 * a.beams,
-               (size_t)a.beams * 31 * kNear * sizeof(uint64_t), second, st);
+               (size_t)a.beams * kRankSmem, second, st);
 }
 
 cudaError_t launch_reorder(const ReorderArgs& a, cudaStream_t st) {

@@ -308,6 +308,13 @@ mamba2_status mamba2_reorder_states(void* const* pools, const int64_t* slot_byte
     a.tile[i] = (int32_t)tiles;
     tiles += (slot_bytes[i] + kReorderTile - 1) / kReorderTile;
     if (tiles > MAMBA2_MAX_BLOCK_SIZE) return MAMBA2_ERR_INVALID_ARGUMENT;
+    if (slot_bytes[i] == 0 || num_slots == 0) continue;
+    if (num_slots > (int64_t(1) << 48) / slot_bytes[i]) return MAMBA2_ERR_INVALID_ARGUMENT;  // (no memory is as large)
+    const uintptr_t p = reinterpret_cast<uintptr_t>(pools[i]), end = p + (uint64_t)slot_bytes[i] * num_slots;
+    for (int j = 0; j < i; ++j) {  // what overlaps would be moved twice
+      const uintptr_t q = reinterpret_cast<uintptr_t>(pools[j]);
+      if (slot_bytes[j] > 0 && p < q + (uint64_t)slot_bytes[j] * num_slots && q < end) return MAMBA2_ERR_INVALID_ARGUMENT;
+    }
   }
   for (int i = num_pools; i <= MAMBA2_MAX_POOLS; ++i) a.tile[i] = (int32_t)tiles;
   if (batch == 0) return done(cudaMemsetAsync(status_dev, 0, 4, static_cast<cudaStream_t>(stream)));

@@ -79,6 +79,26 @@ def test_ties(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("out", [3, 8, 9, 16, 17, 32])
+@pytest.mark.parametrize("order", ["falling", "rising", "one lane", "few", "none but one vector's"])
+def test_logits_in_order(dtype, out, order):
+    """A bound that is taken from groups of threads: the largest all in a few of them, or most of them without any."""
+    dev, vocab = device(), 20000
+    base = torch.linspace(4, -4, vocab).to(dtype).float()  # (bf16: hundreds alike)
+    if order == "rising":
+        base = base.flip(0)
+    elif order == "one lane":
+        base[torch.arange(vocab) // 8 % 32 == 5] += 20.0
+    elif order == "few":
+        base[torch.arange(vocab) % 700 != 3] = -INF
+    elif order == "none but one vector's":
+        base[16:] = -INF
+    logits = base.expand(4, vocab).clone()
+    logits[1] = logits[1].roll(4321)
+    check(dev, logits.to(dtype), torch.tensor([[0.0, -1.0], [-0.5, -0.5]]), None, None, out)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_masks_dead_beams_and_values_that_are_no_numbers(dtype):
     dev = device()
     logits, scores = draw(5, 5, 4, 300, dtype, masked=0.3)

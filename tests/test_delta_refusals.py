@@ -203,6 +203,15 @@ def test_reorder_arguments(product_lib, kw):
     assert reorder(product_lib, **kw) == INV
 
 
+def test_pools_that_overlap(product_lib):
+    """One pool twice, or two that share bytes, would be moved twice."""
+    for second in (P[0], P[0] + 64 * 19, P[0] - 64 * 19):
+        assert reorder(product_lib, pools=(P[0], second)) == INV
+    pool, order, status = torch.zeros((9, 4)), torch.zeros((2, 3), dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ss.Mamba2Error):
+        ss.reorder_states([pool, pool], order, order, status, stream=0)
+
+
 def test_reorder_tensors(product_lib):
     pool, order, status = torch.zeros((9, 4)), torch.zeros((2, 3), dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
     for pools, slots, parents, st in (([pool, pool[:8]], order, order, status), ([pool], order.long(), order, status),
