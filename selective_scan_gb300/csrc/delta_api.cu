@@ -219,9 +219,9 @@ mamba2_status mamba2_gated_delta_rule_backward(void* dq, void* dk, void* dv, voi
   for (const void* p : plain)
     if (!aligned16(p)) return MAMBA2_ERR_INVALID_ARGUMENT;
   if (rows > 0) {
-    // (dv stands where the forward has y; dq, dk and dy are held to the same)
+    // (dv stands where the forward has y; dq, dk and dy are held to the same; v may be dy)
     s = delta_tensors(dv, q, k, v, g, beta, nullptr, ld_dv, ld_q, ld_k, ld_v, dims);
-    if (s == MAMBA2_OK) s = delta_tensors(dy, dq, dk, v, nullptr, nullptr, nullptr, ld_dy, ld_dq, ld_dk, ld_v, dims);
+    if (s == MAMBA2_OK) s = delta_tensors(dy, dq, dk, dv, nullptr, nullptr, nullptr, ld_dy, ld_dq, ld_dk, ld_dv, dims);
     if (s != MAMBA2_OK) return s;
     if (!checkpoints) return MAMBA2_ERR_INVALID_ARGUMENT;
     const void* out[] = {dq, dk, dv, dg, dbeta};
