@@ -21,6 +21,9 @@ namespace {
 // groups' maxima has `out` logits at or above it: a bound below which nothing counts. The few logits that reach it (22,
 // 54 or 130 of a part in random order) are collected and ranked by counting. Where more reach it than are held (many
 // ties), the warps take them one by one instead.
+//
+// The first is bound by issue and latency between a part's loads and its end: 512 rows of 131 072 bf16 logits 29 us,
+// 4.6 TB/s. The second waits for its own steps: 64 sequences of 8 beams about 5 us behind the first.
 constexpr int kScanThreads = 256, kScanWarps = kScanThreads / 32;
 constexpr int kMost = MAMBA2_MAX_BEAMS;  // candidates of a list: one to a lane
 constexpr int kHeld = 1024;              // logits that are collected
@@ -444,7 +447,8 @@ int beam_parts(int vocab, mamba2_dtype act) {
 
 // A CTA takes kReorderTile bytes of the slots of one sequence's beams, a thread the same bytes of every beam: it has
 // read what it moves before it writes, so beams may take one another's places in any order. Bound by HBM: each state
-// that moves is read and written once (one that several beams take comes from L1 after the first).
+// that moves is read and written once (one that several beams take comes from L1 after the first): 16 sequences of 4
+// beams, 12 pools of 1 MB a slot, 163 to 171 us, 6.3 to 6.6 TB/s.
 constexpr int kReorderThreads = 256;
 constexpr int kReorderCheck = kReorderThreads;
 

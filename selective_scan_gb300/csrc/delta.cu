@@ -124,7 +124,9 @@ __device__ __forceinline__ void advance(Two (&s)[kRowsThread][N], const Two (&k)
 
 // A CTA takes 32 rows of one head's state over a whole run; the inputs of 16 tokens (8 where they are wide) are copied to
 // shared memory while those before them are worked on, and what depends on a token's key and query alone is made for all
-// 16 at once. Bound by the chain of a token: a product, three shuffles, the update.
+// 16 at once. Bound by the chain of a token, a product, three shuffles and the update, and the issue of its
+// instructions: 13 runs of fp32, 3 109 tokens, 6 heads of 104 x 72, take 108 us, about 230 ns a token of
+// the longest.
 constexpr int kSerialThreads = 128, kSerialRows = kSerialThreads / kLanes * kRowsThread;
 
 __device__ __forceinline__ void copy16(void* dst, const void* src) {
@@ -267,7 +269,7 @@ __global__ void __launch_bounds__(kSerialThreads) delta_serial_kernel(const __gr
 // ------------------------------------------------------------------ single tokens
 
 // One token of each sequence: a CTA takes 64 rows of one head's state. Bound by HBM: the state is read and written once,
-// everything is asked for before anything is waited for.
+// everything is asked for before anything is waited for. 256 sequences of 16 heads of 128 x 128: 92 us, 5.8 TB/s.
 constexpr int kStepThreads = 256, kStepRows = kStepThreads / kLanes * kRowsThread;
 constexpr int kCheckHere = kStepThreads;
 

@@ -13,6 +13,13 @@
 //   dg_t = exp(G_C) <dS1, S0> + sum_{i>=t} a_i + sum_{j<t} b_j + sum_{i>=t>j} W_ij,
 //   W_ij = beta_j (P_ij Pr_ij - L_ij Er_ij),  a_i = upq_i dO_i S0 q_i - up_i dV_i S0 k_i,  b_j = beta_j left_j (r dS1)_j . k_j,
 // a running sum over t of rows and columns of the same W, so that what cancels cancels exactly.
+//
+// What is rounded: dS, dU, dV and the triangles enter products that end in dS or dV as two bf16 numbers each (2^-16 of
+// them); what ends in dq, dk, dg and dbeta, which are bf16, as one (2^-9). dV between the kernels is its output in bf16,
+// a chunk's dS1 a bf16 operand; their sums are fp32.
+//
+// 8 192 tokens, 8 runs, 16 heads of 128 x 128: the records 35 us, dS 122, the other gradients 199 (0.32 GB in and out of
+// the call in all: 0.9 TB/s).
 #include <algorithm>
 #include <type_traits>
 
@@ -37,6 +44,8 @@ constexpr int kStateTile = 64 * DK * 2;
 __host__ __device__ constexpr int state_tiles(int dv) { return (dv + 63) / 64; }
 
 // ------------------------------------------------------------------ dS through the chunks
+
+// As the forward chain: products that wait for one another, in two warps a scheduler.
 
 template <int DK, int NW>
 struct Back : Stages<DK, true, NW, 2> {
@@ -257,7 +266,9 @@ __global__ void __launch_bounds__(32 * NW, 2) delta_back_kernel(const __grid_con
 
 // An item is a chunk and one group of keys, its heads one after another, so that what they add to a query or key is
 // summed in registers in their order; a head in steps of 64 of its v channels, whose tiles are copied while the step
-// before is worked on. A CTA an SM takes every so-manieth item. A warp: 16 rows of the chunk, half of the columns; of
+// before is worked on. A CTA an SM takes every so-manieth item (two an SM of half the width, one step's tiles at a time,
+// took 254 us where this takes 199). Bound by latency and shared memory: a product's operands are read again by every
+// warp that has a part of it. A warp: 16 rows of the chunk, half of the columns; of
 // the 64 x 64 products the first half has Pr and the other Er.
 constexpr int kGradWarps = 8, kGradThreads = 32 * kGradWarps;
 

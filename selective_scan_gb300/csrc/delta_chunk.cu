@@ -6,13 +6,16 @@
 // the corrections r (u = beta r) satisfy (I + L diag(beta)) r = R, R_i = v_i - exp(G_i) kappa_i S0 k_i, so
 //   r = Inv R,   y_i = scale (exp(G_i) S0 q_i + sum_{j<=i} P_ij u_j),   S = exp(G_C) S0 + sum_j exp(G_C - G_j) kappa_j u_j k_j^T.
 //
-// Two kernels. The first takes every chunk and head by itself: Inv, P and the factors of its tokens, into a record. The
+// Two kernels, one after the other. The first takes every chunk and head by itself: Inv, P and the factors of its tokens, into a record. The
 // second carries the state through a run's chunks. A warp owns 16 rows of the state (v channels) in registers, as the
 // sums of its products are laid out, and every product of the chain has the state, R or u as its left operand:
 //   X^T = S0 K^T,  r^T = R^T Inv^T,  Y^T = S0 Q^T + u^T P^T,  S += u^T K
 // which is again the sums' own layout. So nothing that the chain makes leaves the warp, and warps meet once a chunk, for
 // the tiles that they share. A chain's products are small (16 x 64 x 128) and wait for one another, which is why they run
 // on warp products: 21 cycles from one to the next, where a tensor-memory round trip takes several hundred.
+//
+// What is rounded: the state, R, r and u enter products that end in the state as two bf16 numbers each (2^-16 of them),
+// Inv likewise; S0 Q^T and P, which end in a bf16 output, as one.
 #include <algorithm>
 #include <type_traits>
 
@@ -33,6 +36,9 @@ using bf16 = __nv_bfloat16;
 
 // ------------------------------------------------------------------ chunks by themselves
 
+// A warp has 16 of the chunk's 64 rows. Bound by latency and issue (half of the issue slots, a third of the tensor pipe):
+// a CTA's phases wait for one another, and five CTAs an SM fill in for each other. 16 384 chunks and heads of 128
+// channels take 203 us (0.53 GB of records and inputs: 2.6 TB/s), 4 288 take 58 us.
 constexpr int kPrepThreads = 128;
 constexpr int kLdA = kC + 4;  // floats between the rows of an fp32 triangle in shared memory
 
@@ -341,13 +347,18 @@ __global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(const __gri
 
 // ------------------------------------------------------------------ the state through the chunks
 
+// Four warps share a chunk's tiles, two CTAs an SM (of 128 channels: 113 KB, 238 registers). Bound by the tensor pipe,
+// busy 68 % of the time, and by two warps a scheduler that wait for their own products in between: 24 prompts of 16 384
+// tokens in all, 16 heads of 128 x 128, take 142 us (0.25 GB in and out: 1.8 TB/s). Eight warps to a chunk's tiles took
+// 157 us, three CTAs an SM (168 registers, the keys alone held twice) 153 us, so it is instructions that they share, not
+// latency that more warps would fill.
 template <int DK, int NW>
 struct Chain : Stages<DK, false, NW, 2> {
   static constexpr int kOffBar = Stages<DK, false, NW, 2>::kEnd, kSmem = kOffBar + 32;
 };
 
 template <int DK, int NW>
-__global__ void __launch_bounds__(32 * NW, NW == 8 ? 1 : 2) delta_chain_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ DeltaMaps maps, const unsigned char* records) {
+__global__ void __launch_bounds__(32 * NW, 2) delta_chain_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ DeltaMaps maps, const unsigned char* records) {
   using L = Chain<DK, NW>;
   constexpr int KS = DK / 16;
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -555,7 +566,9 @@ __global__ void __launch_bounds__(32 * NW, NW == 8 ? 1 : 2) delta_chain_kernel(c
 // Where there are few chains, a chunk's time is that of its products one after another. Here two warps share 16 rows of
 // the state: each holds one half of its columns, so each has half of the products with K and Q; they add up their parts
 // of X and Y, each takes half of the tokens through Inv and P, and they exchange the u that come out. The first and last
-// 16 tokens are warp 0's, those between warp 1's: both have five of the ten blocks of a triangle.
+// 16 tokens are warp 0's, those between warp 1's: both have five of the ten blocks of a triangle. One more warp copies.
+// Bound by latency: one run of 32 768 tokens, 32 heads of 128 x 128, takes 990 us, 3 800 cycles a chunk (one warp to 16
+// rows: 5 200), of which the tensor pipe works 47 %.
 constexpr int kAhead = 3;  // chunks whose tiles are held (with two, 970 of a chunk's 4 300 cycles were waiting for them)
 
 template <int DK, int NP>
@@ -866,10 +879,13 @@ cudaError_t run_forward(const DeltaArgs& a, unsigned char* records, cudaStream_t
   if (a.tab.cu[a.tab.n] > 0 && !delta_maps(&maps, a, a.v, a.ld_v)) return cudaErrorInvalidValue;
   const cudaError_t e = run_prep<DK, false>(a, maps, records, st);
   if (e != cudaSuccess) return e;
-  const int64_t blocks = (int64_t)a.tab.n * a.heads * ((a.dv + 15) / 16), sms = device_sm_count();  // of 16 rows
+  // Two warps to 16 rows while the SMs have room for them, so that a chunk takes less time; beyond that one warp, which
+  // does no product twice and needs no exchange. Microseconds of (two warps, one block of 16 rows a CTA | two blocks |
+  // one warp, four blocks), 8 192 tokens, 16 heads of 128 x 128: 128 blocks in all 230 | 250 | 348, 256 blocks
+  // 232 | 182 | 253, 384 blocks 235 | 146 | 156, 512 blocks 221 | 137 | 129, 1 024 blocks 214 | 123 | 97.
+  const int64_t blocks = (int64_t)a.tab.n * a.heads * ((a.dv + 15) / 16), sms = device_sm_count();
   if (blocks <= sms) return run_pairs<DK, 1>(a, maps, records, st);
-  if (blocks <= 2 * sms) return run_pairs<DK, 2>(a, maps, records, st);
-  if (blocks <= 4 * sms) return run_pairs<DK, 4>(a, maps, records, st);
+  if (blocks <= 3 * sms) return run_pairs<DK, 2>(a, maps, records, st);
   return run_chain<DK, 4>(a, maps, records, st);
 }
 
