@@ -16,7 +16,8 @@ Entry points (same names as the C ABI without the ``mamba2_`` prefix):
 ``_backward``, and ``gated_recurrence_step`` / ``gated_recurrence_step_device``;
 ``selective_scan_gb300.recurrent_block`` runs them together. The gated delta rule (``include/delta.h``):
 ``gated_delta_rule``, its ``_step``, ``_step_device`` and ``_backward``. Beam search over recurrent states
-(``include/beam.h``): ``beam_select`` and ``reorder_states``. ``selective_scan_gb300.padded`` holds the padded-batch
+(``include/beam.h``): ``beam_select`` and ``reorder_states``. ``selective_scan_gb300.delta_block`` and
+``selective_scan_gb300.beams`` run them together. ``selective_scan_gb300.padded`` holds the padded-batch
 layer view built on them (attention mask in, HF-style cache out).
 """
 from __future__ import annotations
