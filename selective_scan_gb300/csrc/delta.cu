@@ -120,6 +120,53 @@ __device__ __forceinline__ void advance(Two (&s)[kRowsThread][N], const Two (&k)
   for (int r = 0; r < kRowsThread; ++r) y[r] = dot(s[r], q);
 }
 
+// Two tokens at once, from the state S before them, so that all of S's sums go round together and S is scaled once: with
+// a and u of each, and S' the state between,
+//   S' k1 = a0 (S k1) + u0 (k0 . k1),  S'' = a0 a1 S + a1 u0 k0 + u1 k1,
+//   S' q0 = a0 (S q0) + u0 (k0 . q0),  S'' q1 = a0 a1 (S q1) + a1 u0 (k0 . q1) + u1 (k1 . q1)
+struct Products {
+  float kk, kq00, kq01, kq11;
+};
+// Gives this lane's parts of S q0 and S q1, and what u0 and u1 add to them.
+template <int N>
+__device__ __forceinline__ void advance_two(Two (&s)[kRowsThread][N], const Two (&k0)[N], const Two (&k1)[N], const Two (&q0)[N],
+                                            const Two (&q1)[N], const float (&v0)[kRowsThread], const float (&v1)[kRowsThread],
+                                            const Token& t0, const Token& t1, const Products& c, float (&y0)[kRowsThread],
+                                            float (&y1)[kRowsThread], float (&add0)[kRowsThread], float (&add1)[kRowsThread]) {
+  float p0[kRowsThread], p1[kRowsThread];
+#pragma unroll
+  for (int r = 0; r < kRowsThread; ++r) {
+    p0[r] = dot(s[r], k0);
+    p1[r] = dot(s[r], k1);
+  }
+#pragma unroll
+  for (int r = 0; r < kRowsThread; ++r) {
+    p0[r] = sum8(p0[r]);
+    p1[r] = sum8(p1[r]);
+  }
+#pragma unroll
+  for (int r = 0; r < kRowsThread; ++r) {  // (while the sums go round)
+    y0[r] = dot(s[r], q0);
+    y1[r] = dot(s[r], q1);
+  }
+  const Two a = two(t0.a * t1.a, t0.a * t1.a);
+#pragma unroll
+  for (int r = 0; r < kRowsThread; ++r)
+#pragma unroll
+    for (int e = 0; e < N; ++e) s[r][e] = mul(a, s[r][e]);
+#pragma unroll
+  for (int r = 0; r < kRowsThread; ++r) {
+    const float u0 = t0.write * fmaf(-t0.read, p0[r], v0[r]);
+    const float u1 = t1.write * fmaf(-t1.read, fmaf(u0, c.kk, t0.a * p1[r]), v1[r]);
+    const float u = t1.a * u0;
+    add0[r] = u0 * c.kq00;
+    add1[r] = fmaf(u, c.kq01, u1 * c.kq11);
+    const Two w0 = two(u, u), w1 = two(u1, u1);
+#pragma unroll
+    for (int e = 0; e < N; ++e) s[r][e] = fma(w1, k1[e], fma(w0, k0[e], s[r][e]));
+  }
+}
+
 // ------------------------------------------------------------------ packed runs
 
 // A CTA takes 32 rows of one head's state over a whole run; the inputs of 16 tokens (8 where they are wide) are copied to
@@ -143,6 +190,7 @@ __global__ void __launch_bounds__(kSerialThreads) delta_serial_kernel(const __gr
   __shared__ __align__(16) T sk[2][kTile][DK], sq[2][kTile][DK], sv[2][kTile][kSerialRows];
   __shared__ float sg[2][kTile], sb[2][kTile];
   __shared__ __align__(16) Token tokens[kTile];
+  __shared__ __align__(16) Products products[kTile / 2];
   const int i = a.order[blockIdx.z], h = blockIdx.y, grp = h / (a.heads / a.groups);
   const int row0 = blockIdx.x * kSerialRows, lane = threadIdx.x % kLanes;
   const int mine = (int)threadIdx.x / kLanes * kRowsThread, row = row0 + mine;
@@ -220,6 +268,15 @@ __global__ void __launch_bounds__(kSerialThreads) delta_serial_kernel(const __gr
       load(sq[b][t], qv);
       const Token tok = token_of(kv, qv, sg[b][t], sb[b][t], a.scale, a.l2_eps);
       if (lane == 0) tokens[t] = tok;
+      const float own = sum8(dot(kv, qv));
+      load(sk[b][t ^ 1], qv);
+      const float kk = sum8(dot(kv, qv));
+      load(sq[b][t ^ 1], qv);
+      const float across = sum8(dot(kv, qv));
+      if (lane == 0) {  // (an odd token's own product alone)
+        if (t & 1) products[t >> 1].kq11 = own;
+        else products[t >> 1].kk = kk, products[t >> 1].kq00 = own, products[t >> 1].kq01 = across;
+      }
     }
     __syncthreads();
     auto one = [&](int t, float (&yp)[kRowsThread]) {
@@ -235,10 +292,26 @@ __global__ void __launch_bounds__(kSerialThreads) delta_serial_kernel(const __gr
     for (; t + 8 <= n; t += 8) {
       // eight tokens' parts are summed at once, so that no token waits for another's output: 7 shuffles a row that leave
       // lane j with token j's
-      float yp[8][kRowsThread];
+      float yp[8][kRowsThread], add[kRowsThread] = {};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) one(t + j, yp[j]);
+      for (int j = 0; j < 8; j += 2) {
+        Two k0[N], k1[N], q0[N], q1[N];
+        float v0[kRowsThread], v1[kRowsThread], add0[kRowsThread], add1[kRowsThread];
+        load(sk[b][t + j], k0);
+        load(sk[b][t + j + 1], k1);
+        load(sq[b][t + j], q0);
+        load(sq[b][t + j + 1], q1);
+#pragma unroll
+        for (int r = 0; r < kRowsThread; ++r) {
+          v0[r] = Act<T>::to_f(sv[b][t + j][mine + r]);
+          v1[r] = Act<T>::to_f(sv[b][t + j + 1][mine + r]);
+        }
+        advance_two(s, k0, k1, q0, q1, v0, v1, tokens[t + j], tokens[t + j + 1], products[(t + j) >> 1], yp[j], yp[j + 1], add0, add1);
+#pragma unroll
+        for (int r = 0; r < kRowsThread; ++r) add[r] = lane == j ? add0[r] : lane == j + 1 ? add1[r] : add[r];
+      }
       float out[kRowsThread];
+      const float left = lane & 1 ? tokens[t + lane - 1].a * tokens[t + lane].a : tokens[t + lane].a;
 #pragma unroll
       for (int r = 0; r < kRowsThread; ++r) {
 #pragma unroll
@@ -250,7 +323,7 @@ __global__ void __launch_bounds__(kSerialThreads) delta_serial_kernel(const __gr
               const float keep = up ? yp[j + o][r] : yp[j][r], send = up ? yp[j][r] : yp[j + o][r];
               yp[j][r] = keep + __shfl_xor_sync(0xffffffffu, send, o);
             }
-        out[r] = tokens[t + lane].qn * yp[0][r];
+        out[r] = tokens[t + lane].qn * fmaf(left, yp[0][r], add[r]);
       }
       if (live) store_two(y + ((int64_t)first + t0 + t + lane) * a.ld_y, out[0], out[1]);
     }
