@@ -171,9 +171,9 @@ __device__ __forceinline__ void advance_two(Two (&s)[kRowsThread][N], const Two 
 
 // A CTA takes 32 rows of one head's state over a whole run; the inputs of 16 tokens (8 where they are wide) are copied to
 // shared memory while those before them are worked on, and what depends on a token's key and query alone is made for all
-// 16 at once. Bound by the chain of a token, a product, three shuffles and the update, and the issue of its
-// instructions: 13 runs of fp32, 3 109 tokens, 6 heads of 104 x 72, take 108 us, about 230 ns a token of
-// the longest.
+// 16 at once. Bound by the chain of two tokens, a product, three shuffles and the update, and the issue of their
+// instructions: 13 runs of fp32, 3 109 tokens, 6 heads of 104 x 72, take 95 us, about 200 ns a token of the longest (one
+// token at a time 108). A row to eight lanes instead of two takes 119, as every warp reads the keys and queries.
 constexpr int kSerialThreads = 128, kSerialRows = kSerialThreads / kLanes * kRowsThread;
 
 __device__ __forceinline__ void copy16(void* dst, const void* src) {
@@ -221,18 +221,19 @@ __global__ void __launch_bounds__(kSerialThreads) delta_serial_kernel(const __gr
   const T* k = static_cast<const T*>(a.k) + (int64_t)grp * a.dk;
   const T* v = static_cast<const T*>(a.v) + (int64_t)h * a.dv + row0;
   T* y = static_cast<T*>(a.y) + (int64_t)h * a.dv + row;
-  const int wide = a.dk / unit, tall = min(kSerialRows, a.dv - row0) / unit;
-  auto fetch = [&](int t0) {
-    const int b = (t0 / kTile) & 1, n = min(kTile, len - t0);
-    for (int e = threadIdx.x; e < n * wide; e += kSerialThreads) {
-      const int t = e / wide, c = (e - t * wide) * unit;
+  const int tall = min(kSerialRows, a.dv - row0);
+  auto fetch = [&](int t0) {  // (eight threads a token)
+    const int b = (t0 / kTile) & 1, n = min(kTile, len - t0), t = (int)threadIdx.x / kLanes;
+    if (t < n) {
       const int64_t at = (int64_t)first + t0 + t;
-      copy16(&sk[b][t][c], k + at * a.ld_k + c);
-      copy16(&sq[b][t][c], q + at * a.ld_q + c);
-    }
-    for (int e = threadIdx.x; e < n * tall; e += kSerialThreads) {
-      const int t = e / tall, c = (e - t * tall) * unit;
-      copy16(&sv[b][t][c], v + ((int64_t)first + t0 + t) * a.ld_v + c);
+      const T *kt = k + at * a.ld_k, *qt = q + at * a.ld_q, *vt = v + at * a.ld_v;
+#pragma unroll
+      for (int c = lane * unit; c < DK; c += kLanes * unit)
+        if (c < a.dk) {
+          copy16(&sk[b][t][c], kt + c);
+          copy16(&sq[b][t][c], qt + c);
+        }
+      if (lane * unit < tall) copy16(&sv[b][t][lane * unit], vt + lane * unit);
     }
     if ((int)threadIdx.x < n) {
       const int64_t at = ((int64_t)first + t0 + threadIdx.x) * a.heads + h;
