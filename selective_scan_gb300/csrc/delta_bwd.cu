@@ -18,8 +18,8 @@
 // them); what ends in dq, dk, dg and dbeta, which are bf16, as one (2^-9). dV between the kernels is its output in bf16,
 // a chunk's dS1 a bf16 operand; their sums are fp32.
 //
-// 8 192 tokens, 8 runs, 16 heads of 128 x 128: the records 35 us, dS 122, the other gradients 199 (0.32 GB in and out of
-// the call in all: 0.9 TB/s).
+// 8 192 tokens, 8 runs, 16 heads of 128 x 128: the records 35 us, dS 122, the other gradients 177 (0.32 GB in and out of
+// the call in all: 1.0 TB/s).
 #include <algorithm>
 #include <type_traits>
 
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(32 * NW, 2) delta_back_kernel(const __grid_con
 // An item is a chunk and one group of keys, its heads one after another, so that what they add to a query or key is
 // summed in registers in their order; a head in steps of 64 of its v channels, whose tiles are copied while the step
 // before is worked on. A CTA an SM takes every so-manieth item (two an SM of half the width, one step's tiles at a time,
-// took 254 us where this takes 199). Bound by latency and shared memory: a product's operands are read again by every
+// took 254 us where this took 199 then). Bound by latency and shared memory: a product's operands are read again by every
 // warp that has a part of it. A warp: 16 rows of the chunk, half of the columns; of
 // the 64 x 64 products the first half has Pr and the other Er.
 constexpr int kGradWarps = 8, kGradThreads = 32 * kGradWarps;
@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
   const int part = warp >> 2, rb = part ? 3 - (warp & 3) : warp & 3, r0 = 16 * rb;
   const bool second = part == 1;  // of the 64 x 64 products: Er
   const int per = a.heads / a.groups, halves = state_tiles(a.dv), steps = per * halves;
-  const int64_t items = (int64_t)a.tab.tile[a.tab.n] * a.groups;
+  const unsigned items = (unsigned)a.tab.tile[a.tab.n] * (unsigned)a.groups, groups = (unsigned)a.groups;
   float* vec = reinterpret_cast<float*>(smem + L::kVec);
   volatile uint32_t* gave_up = reinterpret_cast<volatile uint32_t*>(smem + L::kBar + 24);
   auto bar = [&](int i) { return base + L::kBar + 8u * (uint32_t)i; };  // 0, 1: a step's tiles; 2: its S0
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
     }
   };
 
-  float dq[NK][4], dk[NK][4], qk[4][2][4];  // qk: Q K^T (or K K^T), by blocks of 16 columns
+  float dq[NK][4], dk[NK][4];
   uint32_t kq0 = 0;  // where the item's K and Q are
   // the pair of a key or query that this thread's sum (column tile i of its half, row g + 8 e) is of
   auto pair_at = [&](uint32_t tile, int i, int e) -> uint32_t* {
@@ -401,14 +401,14 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
   };
   float x[4][2][4], at_row[2], write_row[2], dot = 0.0f;  // Pr or Er; rows' parts of a and of the write; <dS1, S0>
 
-  int64_t item = blockIdx.x;  // (no more CTAs than items)
-  Chunk c = chunk_of(a.tab, (int)(item / a.groups));
-  fetch(c, (int)(item / a.groups), (int)(item % a.groups), 0, 0, 0);
+  unsigned item = blockIdx.x;  // (no more CTAs than items)
+  Chunk c = chunk_of(a.tab, (int)(item / groups));
+  fetch(c, (int)(item / groups), (int)(item % groups), 0, 0, 0);
   int n = 0;
   for (int m = 0; item < items; ++m, item += gridDim.x) {
-  const int grp = (int)(item % a.groups);
-  const int64_t after = item + gridDim.x;
-  const Chunk next = after < items ? chunk_of(a.tab, (int)(after / a.groups)) : c;
+  const int chunk = (int)(item / groups), grp = (int)(item % groups);
+  const unsigned after = item + gridDim.x;
+  const Chunk next = after < items ? chunk_of(a.tab, (int)(after / groups)) : c;
   kq0 = (uint32_t)(m & 1) * (2 * L::kTileK);
   const uint32_t kq = base + kq0;
 #pragma unroll
@@ -451,28 +451,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
       *reinterpret_cast<uint4*>(smem + L::kS0 + wide_at(r, u)) = w;
     }
     __syncthreads();
-    if (i + 1 < steps) fetch(c, (int)(item / a.groups), grp, i + 1, n + 1, m);
-    else if (after < items) fetch(next, (int)(after / a.groups), (int)(after % a.groups), 0, n + 1, m + 1);
-    if (i == 0) {
-#pragma unroll
-      for (int o = 0; o < 4; ++o)
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) qk[o][n][j] = 0.0f;
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        uint32_t v[4], b[4];
-        load4(v, kq + (second ? L::kK : L::kQ) + wide_cols(r0, 2 * ks, lane));
-#pragma unroll
-        for (int o = 0; o < 4; ++o)
-          if (o <= rb) {
-            load4(b, kq + L::kK + wide_rows(16 * o, 2 * ks, lane));
-            mma(qk[o][0], v, b[0], b[1]);
-            mma(qk[o][1], v, b[2], b[3]);
-          }
-      }
-    }
+    if (i + 1 < steps) fetch(c, chunk, grp, i + 1, n + 1, m);
+    else if (after < items) fetch(next, (int)(after / groups), (int)(after % groups), 0, n + 1, m + 1);
     // R = V - up K S0^T, in V's place: 32 channels a half
     {
       float y[4][4];
@@ -580,6 +560,26 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
       }
     }
     if (half == halves - 1) {
+      // Q K^T (or K K^T), by blocks of 16 columns (of every head again: 32 registers held took 197 us for 177, spills)
+      float qk[4][2][4];
+#pragma unroll
+      for (int o = 0; o < 4; ++o)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) qk[o][n][j] = 0.0f;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        uint32_t v[4], b[4];
+        load4(v, kq + (second ? L::kK : L::kQ) + wide_cols(r0, 2 * ks, lane));
+#pragma unroll
+        for (int o = 0; o < 4; ++o)
+          if (o <= rb) {
+            load4(b, kq + L::kK + wide_rows(16 * o, 2 * ks, lane));
+            mma(qk[o][0], v, b[0], b[1]);
+            mma(qk[o][1], v, b[2], b[3]);
+          }
+      }
       __syncthreads();  // dO and dV have been read
       // F or -E, and W's sums
       float row[2] = {0.0f, 0.0f}, mine[2], mine_hi[2], mine_lo[2];
@@ -785,6 +785,7 @@ cudaError_t run_grad(const DeltaBwdArgs& a, const DeltaMaps& both, const unsigne
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   if (e != cudaSuccess) return e;
   const int64_t items = (int64_t)chunks * a.groups;
+  if (items + device_sm_count() > 0xffffffffll) return cudaErrorInvalidValue;  // (queries that no memory holds)
   kernel<<<(unsigned)std::min<int64_t>(items, device_sm_count()), kGradThreads, L::kSmem, st>>>(a, maps, records, ds);
   return cudaGetLastError();
 }
