@@ -37,8 +37,8 @@ using bf16 = __nv_bfloat16;
 // ------------------------------------------------------------------ chunks by themselves
 
 // A warp has 16 of the chunk's 64 rows. Bound by latency and issue (half of the issue slots, a third of the tensor pipe):
-// a CTA's phases wait for one another, and five CTAs an SM fill in for each other. 16 384 chunks and heads of 128
-// channels take 203 us (0.53 GB of records and inputs: 2.6 TB/s), 4 288 take 58 us.
+// a CTA's phases wait for one another, and four CTAs an SM fill in for each other. 16 384 chunks and heads of 128
+// channels, two heads a group, take 176 us (0.54 GB of records and inputs: 3.1 TB/s), 4 240 take 52 us.
 constexpr int kPrepThreads = 128;
 constexpr int kLdA = kC + 4;  // floats between the rows of an fp32 triangle in shared memory
 
@@ -68,16 +68,16 @@ __device__ __forceinline__ void scan_decays(float g, float& hi, float& lo, int l
 }
 
 template <int DK, bool kBackward>
-__global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ DeltaMaps maps, unsigned char* records) {
+__global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ DeltaMaps maps, unsigned char* records, int several) {
   using L = PrepSmem<kBackward>;
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t sk = sm32(smem), sq = sk + kC * DK * 2, bar = sk + L::kBar;
   if (not_aligned(sk, &g_delta_timeouts)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int h = blockIdx.y, grp = h / (a.heads / a.groups);
+  const int h0 = blockIdx.y * several, grp = h0 / (a.heads / a.groups);  // the first of this CTA's heads
   // The last 16 rows have four times the first's work, so which warp has which goes round: the warps of a scheduler
   // then have all kinds.
-  const int rb = (warp + (int)blockIdx.x + h) & 3, r0 = 16 * rb;
+  const int rb = (warp + (int)(blockIdx.x + blockIdx.y)) & 3, r0 = 16 * rb;
   const Chunk c = chunk_of(a.tab, blockIdx.x);
   float4* token = reinterpret_cast<float4*>(smem + L::kToken);  // G in two parts, kappa, beta
   float* qn = reinterpret_cast<float*>(smem + L::kQn);
@@ -109,8 +109,9 @@ __global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(const __gri
     }
     copies_end();
   }
+  // The decays of a head: asked for early, and summed by the warp with the least of the products.
   float gv[2] = {}, bv[2] = {};
-  if (rb == 0) {
+  auto ask = [&](int h) {
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int i = 32 * half + lane;
@@ -118,10 +119,8 @@ __global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(const __gri
       gv[half] = i < c.len && a.g ? a.g[at] : 0.0f;
       bv[half] = i < c.len ? (a.beta ? a.beta[at] : 1.0f) : 0.0f;
     }
-  }
-  copies_done();
-  __syncthreads();
-  if (rb == 0) {  // the warp with the least of the products sums the decays
+  };
+  auto sum_decays = [&]() {
     float hi[2], lo[2], last[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
@@ -135,7 +134,11 @@ __global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(const __gri
       last[0] = __shfl_sync(0xffffffffu, s.hi, 31);
       last[1] = __shfl_sync(0xffffffffu, s.lo, 31);
     }
-  }
+  };
+  if (rb == 0) ask(h0);
+  copies_done();
+  __syncthreads();
+  if (rb == 0) sum_decays();
   if (c.len == kC) {
     bar_wait(bar, 0, gave_up);
     __syncwarp();
@@ -184,6 +187,14 @@ __global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(const __gri
   float* A = reinterpret_cast<float*>(smem);
   float* inv = reinterpret_cast<float*>(smem + L::kInv);
   unsigned char* scores = smem + L::kScores;
+  for (int hh = 0; hh < several; ++hh) {
+  if (hh > 0) {
+    if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncthreads();  // the last record has been copied
+    if (rb == 0) sum_decays();
+    __syncthreads();
+  }
+  if (rb == 0 && hh + 1 < several) ask(h0 + hh + 1);
   const float4 row[2] = {token[r0 + g], token[r0 + g + 8]};
   const float rq[2] = {qn[r0 + g] * a.scale, qn[r0 + g + 8] * a.scale};
 #pragma unroll
@@ -334,13 +345,17 @@ __global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(const __gri
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncthreads();
   if (threadIdx.x == 0) {
-    unsigned char* rec = records + ((int64_t)blockIdx.x * a.heads + h) * record_bytes(kBackward);
+    unsigned char* rec = records + ((int64_t)blockIdx.x * a.heads + h0 + hh) * record_bytes(kBackward);
     auto out = [](unsigned char* to, uint32_t from, int bytes) {
       asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to), "r"(from), "r"(bytes) : "memory");
     };
     out(rec, sk, kOffP);
     out(rec + kOffP, sk + L::kScores, record_bytes(kBackward) - kOffP);
-    asm volatile("cp.async.bulk.commit_group;\ncp.async.bulk.wait_group 0;" ::: "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+  }
+  if (threadIdx.x == 0) {
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     if (c.len == kC && *gave_up) atomicAdd(&g_delta_timeouts, 1u);
   }
 }
@@ -869,7 +884,14 @@ cudaError_t run_prep(const DeltaArgs& a, const DeltaMaps& maps, unsigned char* r
   auto kernel = delta_prep_kernel<DK, kBackward>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PrepSmem<kBackward>::kBytes);
   if (e != cudaSuccess) return e;
-  kernel<<<dim3(chunks, a.heads), kPrepThreads, PrepSmem<kBackward>::kBytes, st>>>(a, maps, records);
+  // Heads of a group that a CTA takes one after another, from one product of keys and queries: as many, up to eight, as
+  // leave three quarters of the SMs' places a CTA (us of 1, 2, 4 and 8 heads, chunks of 128 channels and 16 heads: 512
+  // chunks of one group 108, 89, 84, 83; 128 of two groups 31, 27, 26, 37; 64 of eight groups 18.4 and 16.6 of 1 and 2
+  // heads, 32 of them 10.5 and 11.6).
+  int several = 1;
+  for (int d = 2; d <= 8; ++d)
+    if (a.heads / a.groups % d == 0 && (int64_t)chunks * (a.heads / d) >= 3 * device_sm_count()) several = d;
+  kernel<<<dim3(chunks, a.heads / several), kPrepThreads, PrepSmem<kBackward>::kBytes, st>>>(a, maps, records, several);
   return cudaGetLastError();
 }
 
