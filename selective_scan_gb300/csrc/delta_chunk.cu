@@ -422,6 +422,8 @@ __global__ void __launch_bounds__(32 * NW, 2) delta_chain_kernel(const __grid_co
                               first + (int64_t)ch * kC, min(kC, len - ch * kC), grp, h, dv0, lane);
   };
   if (n > 0 && warp == 0) fetch(0);
+  auto kept = [&](int ch) { return a.ckpt + ((int64_t)(a.tab.tile[run] + ch) * a.heads + h) * a.dv * a.dk; };
+  if (a.ckpt && n > 0) each([&](float* v, int64_t at) { *reinterpret_cast<float2*>(kept(0) + at) = make_float2(v[0], v[1]); });
   for (int ch = 0; ch < n; ++ch) {
     if (ch > 0) {
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (y was written where the next chunk's v comes)
@@ -432,10 +434,6 @@ __global__ void __launch_bounds__(32 * NW, 2) delta_chain_kernel(const __grid_co
     __syncwarp();
     const uint32_t at = base + L::k(ch), qt = base + L::q(ch), rec = base + L::rec(ch), vt = base + L::v(ch) + warp * L::kStrip;
     const float* f = reinterpret_cast<const float*>(smem + (rec - base) + off_factors(false));
-    if (a.ckpt) {
-      float* o = a.ckpt + ((int64_t)(a.tab.tile[run] + ch) * a.heads + h) * a.dv * a.dk;
-      each([&](float* v, int64_t to) { *reinterpret_cast<float2*>(o + to) = make_float2(v[0], v[1]); });
-    }
     // X^T = S0 K^T (the state in two parts) and S0 Q^T (in one: it ends in a bf16 output)
     float x[8][4], y[8][4];
 #pragma unroll
@@ -570,6 +568,30 @@ __global__ void __launch_bounds__(32 * NW, 2) delta_chain_kernel(const __grid_co
       if (tok < m && col < a.dv)
         *reinterpret_cast<uint4*>(out + tok * a.ld_y) =
             *reinterpret_cast<const uint4*>(smem + (vt - base) + narrow_at(tok, lane & 1));
+    }
+    // The next chunk's checkpoint by way of y's place, 32 columns at a time: from the registers a store would touch eight
+    // lines for 256 bytes (8 192 tokens, 16 heads, 8 runs 125 us, with lines whole 122; 16 runs 106 and 101).
+    if (a.ckpt && ch + 1 < n) {
+      unsigned char* turn = smem + (vt - base);
+      auto unit = [](int row, int u) { return row * 128 + ((u ^ (2 * (row & 3))) << 4); };
+#pragma unroll
+      for (int r = 0; r < DK / 32; ++r) {
+        __syncwarp();
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<float2*>(turn + unit(g + 8 * half, 2 * i + (t >> 1)) + 8 * (t & 1)) =
+                make_float2(s[4 * r + i][2 * half], s[4 * r + i][2 * half + 1]);
+        __syncwarp();
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+          const int row = 4 * it + (lane >> 3), c = 32 * r + 4 * (lane & 7);
+          if (dv + row < a.dv && c < a.dk)
+            *reinterpret_cast<float4*>(kept(ch + 1) + (int64_t)(dv + row) * a.dk + c) =
+                *reinterpret_cast<const float4*>(turn + unit(row, lane & 7));
+        }
+      }
     }
   }
   each([&](float* v, int64_t at) { *reinterpret_cast<float2*>(st + at) = make_float2(v[0], v[1]); });
