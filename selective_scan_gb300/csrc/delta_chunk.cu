@@ -36,7 +36,7 @@ using bf16 = __nv_bfloat16;
 
 // ------------------------------------------------------------------ chunks by themselves
 
-// A warp has 16 of the chunk's 64 rows. Bound by latency and issue (half of the issue slots, a third of the tensor pipe):
+// A warp has 16 of the chunk's 64 rows. Bound by latency and issue (42 % of the issue slots, 23 % of the tensor pipe):
 // a CTA's phases wait for one another, and four CTAs an SM fill in for each other. 16 384 chunks and heads of 128
 // channels, two heads a group, take 176 us (0.54 GB of records and inputs: 3.1 TB/s), 4 240 take 52 us.
 constexpr int kPrepThreads = 128;
@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const __gri
 
 // ------------------------------------------------------------------ the state through the chunks
 
-// Four warps share a chunk's tiles, two CTAs an SM (of 128 channels: 113 KB, 238 registers). Bound by the tensor pipe,
+// Four warps share a chunk's tiles, two CTAs an SM (of 128 channels: 113 KB, 243 registers). Bound by the tensor pipe,
 // busy 68 % of the time, and by two warps a scheduler that wait for their own products in between: 24 prompts of 16 384
 // tokens in all, 16 heads of 128 x 128, take 142 us (0.25 GB in and out: 1.8 TB/s). Eight warps to a chunk's tiles took
 // 157 us, three CTAs an SM (168 registers, the keys alone held twice) 153 us, so it is instructions that they share, not
