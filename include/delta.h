@@ -103,7 +103,8 @@ mamba2_status mamba2_gated_delta_rule_step_device(void* y, const void* q, const 
  *   dstate = a_0 (G_0 - dv_0 k_0^T) (dstate_end itself for a run of no rows).
  * For bf16, with d_state and headdim of at most 128; MAMBA2_ERR_NOT_IMPLEMENTED
  * otherwise. Operands of the products that end in dq, dk, dg and dbeta are
- * rounded to bf16; dv and dstate come from operands of twice its digits.
+ * rounded to bf16; dv and dstate, and v_t - a_t S_{t-1} k_t, which may be a small
+ * difference, come from operands of twice its digits.
  *
  *   dq, dk    [rows, ngroups, d_state] act, row strides ld_dq, ld_dk
  *   dv        [rows, heads, headdim] act, row stride ld_dv

@@ -15,8 +15,10 @@
 // a running sum over t of rows and columns of the same W, so that what cancels cancels exactly.
 //
 // What is rounded: dS, dU, dV and the triangles enter products that end in dS or dV as two bf16 numbers each (2^-16 of
-// them); what ends in dq, dk, dg and dbeta, which are bf16, as one (2^-9). dV between the kernels is its output in bf16,
-// a chunk's dS1 a bf16 operand; their sums are fp32.
+// them), and so do S0, R and Inv where they end in r: r is what the state has not predicted of v, a small difference of
+// large numbers once the state has learnt them, and dbeta and a part of dk are proportional to it. r itself, and what
+// else ends in dq, dk, dg and dbeta, which are bf16, enters as one (2^-9). dV between the kernels is its output in bf16, a
+// chunk's dS1 a bf16 operand; their sums are fp32.
 //
 // 8 192 tokens, 8 runs, 16 heads of 128 x 128: the records 32 us, dS 122, the other gradients 177 (0.32 GB in and out of
 // the call in all: 1.0 TB/s).
@@ -279,15 +281,16 @@ struct Grad {
   // of each step, twice: dS, V (then R), dO, dV (then F and E, the last step of a head)
   static constexpr int kStep = kS0 + kState, kDS = 0, kV = kState, kDO = kV + kTile, kDV = kDO + kTile, kStepBytes = kDV + kTile;
   static constexpr int kF = kDO, kE = kDV;
-  static constexpr int kR = kStep + 2 * kStepBytes, kWide = kR + kTile;  // kWide: S0 in fp32
-  // of each head, twice: Inv and the factors
-  static constexpr int kHead = kWide + 64 * DK * 4, kFac = kTri, kHeadBytes = kTri + 9 * kC * 4;
+  // kWide: S0 in fp32, until it is an operand; then what S0 and R leave of themselves as bf16 numbers
+  static constexpr int kR = kStep + 2 * kStepBytes, kWide = kR + kTile, kS0Lo = kWide, kRLo = kWide + kState;
+  // of each head, twice: Inv and the factors; Inv's second part once
+  static constexpr int kHead = kWide + 64 * DK * 4, kFac = kTri, kHeadBytes = kTri + 9 * kC * 4, kInvLo = kHead + 2 * kHeadBytes;
   // floats at kVec: sums of W's rows [2 halves], columns [2][4 row blocks], its diagonal, a and the write's rows
   // [2 halves], the inner product [8 warps]
-  static constexpr int kVec = kHead + 2 * kHeadBytes;
+  static constexpr int kVec = kInvLo + kTri;
   static constexpr int kRow = 0, kCol = 2 * kC, kDiag = 10 * kC, kA = 11 * kC, kWrite = 13 * kC, kDot = 15 * kC;
   static constexpr int kBar = kVec + (15 * kC + 16) * 4, kSmem = kBar + 32;  // barriers: the steps' two, S0's; the flag
-  static_assert(kSmem <= 232448, "shared memory plan exceeds 227 KB");
+  static_assert(kRLo + kTile <= kHead && kSmem <= 232448, "shared memory plan exceeds 227 KB");
 };
 struct GradMaps {
   CUtensorMap k, q, v, dy, dv;  // 64 rows of 64 columns of a head
@@ -345,10 +348,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
       if (half == 0) bytes += L::kHeadBytes;
       if (i == 0 && whole) bytes += 2 * L::kTileK;
       asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(b), "r"(bytes) : "memory");
-      // S0, fp32, into the place that the step before has emptied
-      const int rows = min(64, a.dv - 64 * half);
-      asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar(2)), "r"(rows * a.dk * 4) : "memory");
-      bulk(base + L::kWide, a.ckpt + (item * a.dv + 64 * half) * a.dk, rows * a.dk * 4, bar(2));
       bulk(to + L::kDS, ds + (item * halves + half) * L::kState, L::kState, b);
       if (whole) {
         if (i == 0) {
@@ -393,6 +392,16 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
     }
   };
 
+  // And its S0, in fp32, with the second part of Inv: into the places that the step before has emptied (a thread).
+  auto fetch_state = [&](int chunk, int grp, int i) {
+    const int half = i % halves, rows = min(64, a.dv - 64 * half);
+    const int64_t item = (int64_t)chunk * a.heads + grp * per + i / halves;
+    const uint32_t bytes = (uint32_t)(rows * a.dk * 4 + (half == 0 ? kTri : 0));
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar(2)), "r"(bytes) : "memory");
+    bulk(base + L::kWide, a.ckpt + (item * a.dv + 64 * half) * a.dk, rows * a.dk * 4, bar(2));
+    if (half == 0) bulk(base + L::kInvLo, records + item * record_bytes(true) + kOffInvLo, kTri, bar(2));
+  };
+
   float dq[NK][4], dk[NK][4];
   uint32_t kq0 = 0;  // where the item's K and Q are
   // the pair of a key or query that this thread's sum (column tile i of its half, row g + 8 e) is of
@@ -404,6 +413,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
   unsigned item = blockIdx.x;  // (no more CTAs than items)
   Chunk c = chunk_of(a.tab, (int)(item / groups));
   fetch(c, (int)(item / groups), (int)(item % groups), 0, 0, 0);
+  if (threadIdx.x == 0) fetch_state((int)(item / groups), (int)(item % groups), 0);
   int n = 0;
   for (int m = 0; item < items; ++m, item += gridDim.x) {
   const int chunk = (int)(item / groups), grp = (int)(item % groups);
@@ -433,10 +443,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
 #pragma unroll
           for (int j = 0; j < 4; ++j) x[o][n][j] = 0.0f;
     }
-#pragma unroll 2
-    for (int e = threadIdx.x; e < 64 * (DK / 8); e += kGradThreads) {  // S0 as an operand, and its product with dS1
-      const int r = e / (DK / 8), u = e % (DK / 8);
+    uint4 s0_lo[DK / 32];
+#pragma unroll
+    for (int z = 0; z < DK / 32; ++z) {  // S0 as an operand in two parts, and its product with dS1
+      const int e = threadIdx.x + z * kGradThreads, r = e / (DK / 8), u = e % (DK / 8);
       uint4 w = make_uint4(0, 0, 0, 0);
+      s0_lo[z] = w;
       if (r >= rows) *reinterpret_cast<uint4*>(smem + st + L::kDS + wide_at(r, u)) = w;  // (rows that the state has not)
       if (r < rows && 8 * u < a.dk) {
         float v[8], d[8];
@@ -446,14 +458,23 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
         Vec16<bf16>::unpack(*reinterpret_cast<const uint4*>(smem + st + L::kDS + wide_at(r, u)), d);
 #pragma unroll
         for (int j = 0; j < 8; ++j) dot = fmaf(v[j], d[j], dot);
-        w = Vec16<bf16>::pack(v);
+        split(v[0], v[1], w.x, s0_lo[z].x);
+        split(v[2], v[3], w.y, s0_lo[z].y);
+        split(v[4], v[5], w.z, s0_lo[z].z);
+        split(v[6], v[7], w.w, s0_lo[z].w);
       }
       *reinterpret_cast<uint4*>(smem + L::kS0 + wide_at(r, u)) = w;
+    }
+    __syncthreads();  // S0 has been read
+#pragma unroll
+    for (int z = 0; z < DK / 32; ++z) {
+      const int e = threadIdx.x + z * kGradThreads;
+      *reinterpret_cast<uint4*>(smem + L::kS0Lo + wide_at(e / (DK / 8), e % (DK / 8))) = s0_lo[z];
     }
     __syncthreads();
     if (i + 1 < steps) fetch(c, chunk, grp, i + 1, n + 1, m);
     else if (after < items) fetch(next, (int)(after / groups), (int)(after % groups), 0, n + 1, m + 1);
-    // R = V - up K S0^T, in V's place: 32 channels a half
+    // R = V - up K S0^T, in V's place and kRLo: 32 channels a half
     {
       float y[4][4];
 #pragma unroll
@@ -465,6 +486,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
           load4(b, base + L::kS0 + wide_rows(32 * part + 16 * n, 2 * ks, lane));
           mma_if(ks == 0, y[2 * n], k, b[0], b[1]);
           mma_if(ks == 0, y[2 * n + 1], k, b[2], b[3]);
+          load4(b, base + L::kS0Lo + wide_rows(32 * part + 16 * n, 2 * ks, lane));
+          mma(y[2 * n], k, b[0], b[1]);
+          mma(y[2 * n + 1], k, b[2], b[3]);
         }
       }
 #pragma unroll
@@ -472,8 +496,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
         const float up = f[kUp + r0 + g + 8 * e];
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-          uint32_t* p = reinterpret_cast<uint32_t*>(smem + st + L::kV + wide_at(r0 + g + 8 * e, 4 * part + n) + 4 * t);
-          *p = pair(fmaf(-up, y[n][2 * e], __uint_as_float(*p << 16)), fmaf(-up, y[n][2 * e + 1], __uint_as_float(*p & 0xffff0000u)));
+          const uint32_t at = wide_at(r0 + g + 8 * e, 4 * part + n) + 4 * t;
+          uint32_t* p = reinterpret_cast<uint32_t*>(smem + st + L::kV + at);
+          split(fmaf(-up, y[n][2 * e], __uint_as_float(*p << 16)), fmaf(-up, y[n][2 * e + 1], __uint_as_float(*p & 0xffff0000u)), *p,
+                *reinterpret_cast<uint32_t*>(smem + L::kRLo + at));
         }
       }
     }
@@ -483,13 +509,19 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
 #pragma unroll
       for (int jb = 0; jb < 4; ++jb)
         if (jb <= rb) {
-          uint32_t w[4], b[4];
+          uint32_t w[4], wl[4], b[4];
           load4(w, inv + block_at(rb, jb) + narrow_cols(0, lane));
+          load4(wl, base + L::kInvLo + block_at(rb, jb) + narrow_cols(0, lane));
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
             load4t(b, base + st + L::kV + wide_cols(16 * jb, 4 * part + 2 * n, lane));
             mma_if(jb == 0, y[2 * n], w, b[0], b[1]);
             mma_if(jb == 0, y[2 * n + 1], w, b[2], b[3]);
+            mma(y[2 * n], wl, b[0], b[1]);
+            mma(y[2 * n + 1], wl, b[2], b[3]);
+            load4t(b, base + L::kRLo + wide_cols(16 * jb, 4 * part + 2 * n, lane));
+            mma(y[2 * n], w, b[0], b[1]);
+            mma(y[2 * n + 1], w, b[2], b[3]);
           }
         }
 #pragma unroll
@@ -498,7 +530,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
         for (int n = 0; n < 4; ++n)
           *reinterpret_cast<uint32_t*>(smem + L::kR + wide_at(r0 + g + 8 * e, 4 * part + n) + 4 * t) = pair(y[n][2 * e], y[n][2 * e + 1]);
     }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (the second parts were written where the next S0 comes)
     __syncthreads();
+    if (threadIdx.x == 0) {
+      if (i + 1 < steps) fetch_state(chunk, grp, i + 1);
+      else if (after < items) fetch_state((int)(after / groups), (int)(after % groups), 0);
+    }
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {  // Pr or Er
       uint32_t w[4], b[4];
