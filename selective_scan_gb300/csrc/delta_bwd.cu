@@ -12,7 +12,9 @@
 // and g_t reaches what a state before it gives to a row at or behind it:
 //   dg_t = exp(G_C) <dS1, S0> + sum_{i>=t} a_i + sum_{j<t} b_j + sum_{i>=t>j} W_ij,
 //   W_ij = beta_j (P_ij Pr_ij - L_ij Er_ij),  a_i = upq_i dO_i S0 q_i - up_i dV_i S0 k_i,  b_j = beta_j left_j (r dS1)_j . k_j,
-// a running sum over t of rows and columns of the same W, so that what cancels cancels exactly.
+// summed without differences of its terms: what a token forgets is an exact zero in each, so dg is 0 where nothing is left
+// of the state. For t in the chunk's 16 rows T, the double sum is that of W's column sums over row blocks I > T up to
+// column t, of its rows from t to T's last left of T's columns, and of the same rows within T's own block.
 //
 // What is rounded: dS, dU, dV and the triangles enter products that end in dS or dV as two bf16 numbers each (2^-16 of
 // them), and so do S0, R and Inv where they end in r: r is what the state has not predicted of v, a small difference of
@@ -285,7 +287,8 @@ struct Grad {
   static constexpr int kR = kStep + 2 * kStepBytes, kWide = kR + kTile, kS0Lo = kWide, kRLo = kWide + kState;
   // of each head, twice: Inv and the factors; Inv's second part once
   static constexpr int kHead = kWide + 64 * DK * 4, kFac = kTri, kHeadBytes = kTri + 9 * kC * 4, kInvLo = kHead + 2 * kHeadBytes;
-  // floats at kVec: sums of W's rows [2 halves], columns [2][4 row blocks], its diagonal, a and the write's rows
+  // floats at kVec: W's part of dg from a token's own row block [2 halves], sums of W's columns [2][4 row blocks] (without
+  // beta), its diagonal, a and the write's rows
   // [2 halves], the inner product [8 warps]
   static constexpr int kVec = kInvLo + kTri;
   static constexpr int kRow = 0, kCol = 2 * kC, kDiag = 10 * kC, kA = 11 * kC, kWrite = 13 * kC, kDot = 15 * kC;
@@ -299,6 +302,14 @@ struct GradMaps {
 __device__ __forceinline__ float sum_quad(float v) {  // over the lanes of a row
   v += __shfl_xor_sync(0xffffffffu, v, 1);
   return v + __shfl_xor_sync(0xffffffffu, v, 2);
+}
+__device__ __forceinline__ float sum_behind(float v, int lane) {  // of this row and those behind it (of 8)
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) {
+    const float u = __shfl_down_sync(0xffffffffu, v, o);
+    if (lane + o < 32) v += u;
+  }
+  return v;
 }
 __device__ __forceinline__ float sum_rows(float v) {  // over the lanes of a column
   v += __shfl_xor_sync(0xffffffffu, v, 4);
@@ -619,7 +630,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
       }
       __syncthreads();  // dO and dV have been read
       // F or -E, and W's sums
-      float row[2] = {0.0f, 0.0f}, mine[2], mine_hi[2], mine_lo[2];
+      float row[2] = {0.0f, 0.0f}, own[2][2][2] = {};  // rows left of their own block; that block [n][e][j]
+      float mine[2], mine_hi[2], mine_lo[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int at = r0 + g + 8 * e;
@@ -651,7 +663,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
                 out[j] = second ? (diagonal ? 0.0f : -p * b) : p * b;
                 if (!second && diagonal) vec[L::kDiag + at] = w;
                 const float below = diagonal ? 0.0f : w;
-                row[e] = fmaf(b, below, row[e]);
+                if (o == rb) own[n][e][j] = b * below;
+                else row[e] = fmaf(b, below, row[e]);
                 col[j] += below;
               }
               *reinterpret_cast<uint32_t*>(smem + st + (second ? L::kE : L::kF) + wide_at(at, 2 * o + n) + 4 * t) = pair(out[0], out[1]);
@@ -663,6 +676,16 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
             if (g == 0) vec[L::kCol + ((second ? 4 : 0) + rb) * kC + to0 + j] = total;
           }
         }
+      // rows from each on, and of its own block's columns those before it (rows 0-7 have none of columns 8-15)
+      row[1] = sum_behind(row[1], lane);
+      row[0] = sum_behind(row[0], lane) + __shfl_sync(0xffffffffu, row[1], t);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float left = sum_behind(own[0][1][j], lane), right = sum_behind(own[1][1][j], lane);
+        const float top = sum_behind(own[0][0][j], lane) + __shfl_sync(0xffffffffu, left, t);
+        row[0] += 2 * t + j < g ? top : 0.0f;
+        row[1] += left + (2 * t + j < g ? right : 0.0f);
+      }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const float s = sum_quad(row[e]), av = sum_quad(at_row[e]), wr = sum_quad(write_row[e]);
@@ -706,35 +729,57 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
         }
       }
       if (warp == 0 && (a.dg || a.dbeta)) {  // tokens 2 lane and + 1
-        float inner = 0.0f, step[2], all = 0.0f, db[2];
+        float inner = 0.0f, out[2], db[2], av[2], write[2], col[3][2];  // col: of row blocks 1 to 3, left of them
 #pragma unroll
         for (int w = 0; w < kGradWarps; ++w) inner += vec[L::kDot + w];
+        inner *= f[kGamma];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int at = 2 * lane + j;
-          auto four = [&](int from) { return (vec[from + at] + vec[from + kC + at]) + (vec[from + 2 * kC + at] + vec[from + 3 * kC + at]); };
-          const float col = four(L::kCol) - four(L::kCol + 4 * kC), row_sum = vec[L::kRow + at] - vec[L::kRow + kC + at];
-          const float av = vec[L::kA + at] + vec[L::kA + kC + at], wr = vec[L::kWrite + at] + vec[L::kWrite + kC + at];
-          db[j] = wr + vec[L::kDiag + at] + col;
-          step[j] = f[kBeta + at] * (wr + col) - av - row_sum;
-          all += av;
-        }
+          float sums[4];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-        float before = step[0] + step[1];  // of the lanes before this one, exclusive
+          for (int i = 0; i < 4; ++i) sums[i] = vec[L::kCol + i * kC + at] - vec[L::kCol + (4 + i) * kC + at];
+          const float wr = vec[L::kWrite + at] + vec[L::kWrite + kC + at], beta = f[kBeta + at];
+          av[j] = vec[L::kA + at] + vec[L::kA + kC + at];
+          out[j] = inner + (vec[L::kRow + at] - vec[L::kRow + kC + at]);
+          db[j] = wr + vec[L::kDiag + at] + ((sums[0] + sums[1]) + (sums[2] + sums[3]));
+          write[j] = beta * wr;
+#pragma unroll
+          for (int i = 0; i < 3; ++i) col[i][j] = lane < 8 * (i + 1) ? beta * sums[i + 1] : 0.0f;
+        }
+        auto before = [&](const float (&v)[2], bool take) {  // adds the tokens before each of this lane's
+          float sum = v[0] + v[1];
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const float u = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += u;
+          }
+          sum = __shfl_up_sync(0xffffffffu, sum, 1);
+          if (lane == 0) sum = 0.0f;
+          if (take) {
+            out[0] += sum;
+            out[1] += sum + v[0];
+          }
+        };
+        before(write, true);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) before(col[i], lane < 8 * (i + 1));
+        float behind = av[0] + av[1];  // of this lane's tokens on
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const float u = __shfl_up_sync(0xffffffffu, before, o);
-          if (lane >= o) before += u;
+          const float u = __shfl_down_sync(0xffffffffu, behind, o);
+          if (lane + o < 32) behind += u;
         }
-        before -= step[0] + step[1];
-        const float start = fmaf(f[kGamma], inner, all);
+        behind = __shfl_down_sync(0xffffffffu, behind, 1);
+        if (lane == 31) behind = 0.0f;
+        out[0] += behind + av[1] + av[0];
+        out[1] += behind + av[1];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int at = 2 * lane + j;
           if (at >= c.len) break;
           const int64_t to = (int64_t)(c.row + at) * a.heads + h;
-          if (a.dg) static_cast<bf16*>(a.dg)[to] = __float2bfloat16_rn(start + before + (j ? step[0] : 0.0f));
+          if (a.dg) static_cast<bf16*>(a.dg)[to] = __float2bfloat16_rn(out[j]);
           if (a.dbeta) static_cast<bf16*>(a.dbeta)[to] = __float2bfloat16_rn(db[j]);
         }
       }
