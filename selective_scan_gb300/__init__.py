@@ -41,6 +41,7 @@ MAX_SEQS = 1024
 MAX_BLOCK_SIZE = 0x7fff0000  # most rows and columns of the recurrent block's operators
 DELTA_CHUNK = 64  # tokens between two checkpoints of the gated delta rule
 MAX_BEAMS = 32  # beams of a sequence, and candidates that are kept of it
+MAX_POOLS = 64  # pools that one call of the library reorders
 
 
 class Mamba2Error(RuntimeError):
@@ -916,26 +917,43 @@ def beam_select(scores_out, parents, tokens, logits, scores, finished=None, fini
     return st
 
 
+def _pools(pools):
+    """(pointers, bytes of a slot, slots) of state pools."""
+    num_slots, sizes = (pools[0].shape[0] if len(pools) else 0), []
+    for i, t in enumerate(pools):
+        if t.shape[0] != num_slots:
+            raise ValueError(f"pool {i}: expected {num_slots} slots, got {t.shape[0]}")
+        sizes.append(t.nbytes // (num_slots or 1))
+    return [_ptr(t) for t in pools], sizes, num_slots
+
+
+def _overlap(ptrs, sizes, num_slots) -> bool:
+    """Whether two pools share a byte."""
+    spans = sorted((p, p + s * num_slots) for p, s in zip(ptrs, sizes) if s * num_slots > 0)
+    return any(a[1] > b[0] for a, b in zip(spans, spans[1:]))
+
+
 def reorder_states(pools, slots, parents, status_dev, stream=None, check=True) -> int:
     """``mamba2_reorder_states``: in every pool [num_slots, ...] (of any type) at once, the slot of each beam takes the
-    state that its parent's had: pool[slots[b, j]] = pool[slots[b, parents[b, j]]]. ``slots`` and ``parents`` [batch,
-    beams] and ``status_dev`` (one element) are int32 device tensors, checked on the device: ``status_dev`` holds the
-    outcome once the stream has passed the call."""
+    state that its parent's had: pool[slots[b, j]] = pool[slots[b, parents[b, j]]]. There may be any number of pools (the
+    library is called for ``MAX_POOLS`` at a time), none overlapping another. ``slots`` and ``parents`` [batch, beams] and
+    ``status_dev`` (one element) are int32 device tensors, checked on the device: ``status_dev`` holds the outcome once the
+    stream has passed the call."""
     import torch
     (batch, beams), i32, n = slots.shape, torch.int32, len(pools)
     if slots.dtype != i32 or parents.shape != slots.shape or parents.dtype != i32 or status_dev.shape != (1,) or status_dev.dtype != i32:
         _same("slots", slots, (batch, beams), i32)
         _same("parents", parents, (batch, beams), i32)
         _same("status_dev", status_dev, (1,), i32)
-    num_slots = pools[0].shape[0] if n else 0
-    sizes = []
-    for i, t in enumerate(pools):
-        if t.shape[0] != num_slots:
-            raise ValueError(f"pool {i}: expected {num_slots} slots, got {t.shape[0]}")
-        sizes.append(t.nbytes // (num_slots or 1))
-    ptrs, sizes = (ctypes.c_void_p * (n or 1))(*map(_ptr, pools)), (ctypes.c_int64 * (n or 1))(*sizes)
-    st = _lib().mamba2_reorder_states(ptrs, sizes, n, num_slots, _ptr(slots), _ptr(parents), batch, beams,
-                                      _ptr(status_dev), _stream(stream))
+    ptrs, sizes, num_slots = _pools(pools)
+    # (the library refuses what overlaps in one call of it)
+    st = ERR_INVALID_ARGUMENT if n > MAX_POOLS and _overlap(ptrs, sizes, num_slots) else OK
+    for at in range(0, n or 1, MAX_POOLS):
+        if st != OK:
+            break
+        m = min(MAX_POOLS, n - at)
+        st = _lib().mamba2_reorder_states((ctypes.c_void_p * (m or 1))(*ptrs[at:at + m]), (ctypes.c_int64 * (m or 1))(*sizes[at:at + m]),
+                                          m, num_slots, _ptr(slots), _ptr(parents), batch, beams, _ptr(status_dev), _stream(stream))
     if check:
         _check(st, "mamba2_reorder_states")
     return st

@@ -9,18 +9,25 @@ from __future__ import annotations
 
 import torch
 
-from . import _on, beam_select, reorder_states
+from . import MAX_BEAMS, MAX_SEQS, _on, _overlap, _pools, beam_select, reorder_states
 
 
 class Beams:
-    """``slots`` [batch, beams] int32 on the device: where the beams' states are, all different; ``pools``: every
-    layer's pools, each [num_slots, ...]. At first only beam 0 of a sequence is in being (its prompt's prefill has left
+    """``slots`` [batch, beams] int32 on the device: where the beams' states are, all different, of at most ``MAX_SEQS``
+    beams, ``MAX_BEAMS`` a sequence; ``pools``: every layer's pools, each [num_slots, ...], any number of them, none
+    overlapping another. What no step could take is a ValueError here. At first only beam 0 of a sequence is in being (its prompt's prefill has left
     the state in ``slots[:, 0]``); the others come out of it with the first step. With ``eos``, a beam that has it goes
     on as it is. ``tokens`` [batch, beams] holds each beam's last token, ``scores`` its summed log-probability,
     ``finished`` whether it has ended, ``status`` the outcome of the last reordering once the stream has passed it."""
 
     def __init__(self, slots: torch.Tensor, pools, eos=None):
         self.slots, self.pools, self.eos = slots, list(pools), eos
+        if slots.dtype != torch.int32 or slots.dim() != 2 or not slots.is_contiguous():
+            raise ValueError(f"slots: expected a contiguous [batch, beams] of int32, got {tuple(slots.shape)} of {slots.dtype}")
+        if slots.shape[1] < 1 or slots.shape[1] > MAX_BEAMS or slots.numel() > MAX_SEQS:
+            raise ValueError(f"slots: at most {MAX_BEAMS} beams a sequence and {MAX_SEQS} in all, got {tuple(slots.shape)}")
+        if _overlap(*_pools(self.pools)):
+            raise ValueError("two pools overlap")
         dev, shape = slots.device, slots.shape
         self.scores = torch.full(shape, -float("inf"), dtype=torch.float32, device=dev)
         self.scores[:, 0] = 0.0
