@@ -808,11 +808,14 @@ def gated_delta_rule(y, q, k, v, g, beta, state, cu_seqlens=None, slots=None, fr
     cu_seqlens), heads, headdim, d_state] f32 is for the backward pass."""
     b = _batch(cu_seqlens, slots, fresh, batch)
     (yp, qp, kp, vp, gp, bp, sp), strides, d, scale, eps = _delta(y, q, k, v, g, beta, state, scale, l2_eps)
+    n = b.rb.num_seqs  # (cu_seqlens may have more boundaries than the batch has runs)
     if checkpoints is not None and b.cu is not None:
-        _same("checkpoints", checkpoints, (gated_delta_rule_checkpoints(b.cu),) + state.shape[1:], _float32())
+        chunks = int(_lib().mamba2_gated_delta_rule_checkpoints(b.cu, n))
+        if chunks >= 0:  # (else the call below refuses the batch)
+            _same("checkpoints", checkpoints, (chunks,) + state.shape[1:], _float32())
     need = 0
     if workspace is None and b.cu is not None:
-        need = int(_lib().mamba2_gated_delta_rule_workspace_bytes(b.cu, len(b.cu) - 1, d, _dt(v), 0))
+        need = int(_lib().mamba2_gated_delta_rule_workspace_bytes(b.cu, n, d, _dt(v), 0))
     ws, ws_bytes, _keep = _workspace(need, workspace, v.device, stream)
     st = _lib().mamba2_gated_delta_rule(yp, _ptr(checkpoints), qp, kp, vp, gp, bp, sp, state.shape[0], v.shape[0],
                                         *strides, d, scale, eps, _dt(v), b.ref(), ws, ws_bytes, _stream(stream))
