@@ -16,6 +16,12 @@
  * 0 <= beta |k|^2 <= 2 (not checked). A g below -10000 is taken as -10000: the
  * state is forgotten, as exp(-104) already leaves nothing of it in fp32.
  *
+ * bf16 heads of at most 128 x 128 go by chunks on the tensor cores: operands of
+ * the products that end in y alone are bf16, those of the products that end in
+ * the state have twice its digits (2-norms of y and of end states are then about
+ * 1.4e-3, before y's own rounding, and 2e-6 off). All else is fp32, token by
+ * token.
+ *
  * Runs do not touch one another, but a value that is not finite may reach the
  * outputs of its run from the beginning of its MAMBA2_DELTA_CHUNK tokens on.
  *
@@ -28,7 +34,8 @@
  *   dims   heads a multiple of ngroups; conv_kernel is not used
  *
  * A row's heads are contiguous, rows are 16-byte aligned: d_state, headdim and
- * the row strides are multiples of 8. Other sizes, d_state above
+ * the row strides are multiples of 8, and the tensors' pointers (those of g and
+ * beta too) of 16 bytes. Other sizes, d_state above
  * MAMBA2_MAX_DELTA_STATE and an unaligned stride are
  * MAMBA2_ERR_NOT_IMPLEMENTED.
  */

@@ -12,10 +12,13 @@
 //   X^T = S0 K^T,  r^T = R^T Inv^T,  Y^T = S0 Q^T + u^T P^T,  S += u^T K
 // which is again the sums' own layout. So nothing that the chain makes leaves the warp, and warps meet once a chunk, for
 // the tiles that they share. A chain's products are small (16 x 64 x 128) and wait for one another, which is why they run
-// on warp products: 21 cycles from one to the next, where a tensor-memory round trip takes several hundred.
+// on warp products: 21 cycles from one to the next, where a tensor-memory round trip takes several hundred. (A form in
+// tensor memory, where several chains of an SM would fill in for each other, has not been measured.)
 //
 // What is rounded: the state, R, r and u enter products that end in the state as two bf16 numbers each (2^-16 of them),
-// Inv likewise; S0 Q^T and P, which end in a bf16 output, as one.
+// Inv likewise; S0 Q^T and P, which end in a bf16 output, as one. So y is 2.2e-3 off in the 2-norm where its own rounding
+// is 1.7e-3 (P; S0 adds 1e-4 to 3e-4 of it), and an end state 2e-6, all of it from u: in three parts that is 1.1e-6, and
+// 24 prompts of 16 384 tokens take 212 us for 195, one run of 32 768 1 249 for 1 170.
 #include <algorithm>
 #include <type_traits>
 
